@@ -47,7 +47,11 @@ typedef enum {
   MOE_ERR_DEVICE_FAULT = 6   /* device: invalid data (e.g. expert id >= E) */
 } moe_status_t;
 
-typedef enum { MOE_DTYPE_FP8_E4M3 = 0, MOE_DTYPE_BF16 = 1 } moe_dtype_t;
+typedef enum {
+  MOE_DTYPE_FP8_E4M3 = 0,
+  MOE_DTYPE_BF16 = 1,
+  MOE_DTYPE_F32 = 2          /* moe_verify_draft's probabilities only */
+} moe_dtype_t;
 
 typedef enum {
   MOE_EPI_SCATTER = 0,  /* out f32 [M,N] += route_weight * row   (weighted scatter-add) */
@@ -390,6 +394,137 @@ moe_status_t moe_grouped_gemm_noalloc(const moe_gemm_args* args, void* stream);
  * MOE_ERR_TIMEOUT in the status word instead of hanging.  timeout_ns = 0
  * restores the default limit (2 s); drop_producer = 0 restores normal runs. */
 moe_status_t moe_debug_set_pipeline_fault(int drop_producer, uint64_t timeout_ns);
+
+/* ---------------------------------------------------------------------------
+ * Serving operators: the paged key/value cache, the attention that reads it
+ * and the verification of drafted tokens.  The source pages stop at the expert
+ * layer; these are the other operators of the decoder layer's serving step.
+ * The conventions above hold.  `ws` is a workspace whose first MOE_CTRL_BYTES
+ * bytes are the control block (zeroed once): invalid data found on the device
+ * (a slot, page id, token id or length out of range) is recorded there as
+ * MOE_ERR_DEVICE_FAULT, the access is skipped, and moe_get_error reads it. */
+
+/* A paged cache of one layer's keys and values.  A page holds page_size
+ * consecutive positions of one sequence, head by head: element d of position
+ * i, head h of page p is at ((p*heads + h)*page_size + i)*head_dim + d.
+ *   BF16      k, v: bf16; the scales are ignored.
+ *   FP8_E4M3  k, v: E4M3 codes (u8), one scale for each position and head at
+ *             (p*heads + h)*page_size + i: the framework's 1x128 rule with a
+ *             head's row as its block (amax/448; see moe_quant_gather).
+ * page_size 16, 32, 64, 128 or 256; head_dim 64 or 128; k and v 16-byte,
+ * the scales 4-byte aligned; num_pages*heads*page_size < 2^31. */
+typedef struct {
+  moe_dtype_t dtype;
+  int num_pages, page_size, heads, head_dim;
+  void* k;
+  void* v;
+  float* k_scales;            /* FP8: f32 [num_pages, heads, page_size] */
+  float* v_scales;
+} moe_kv_cache;
+
+/* Writes T new positions into the cache, quantising them on the way (FP8) or
+ * copying them (BF16).  k, v: bf16, element d of token t, head h at
+ * t*stride_t + h*stride_h + d (strides in elements, multiples of 8, so views of
+ * a packed projection can be passed).  slots: s32 [T], token t goes to
+ * position slots[t] % page_size of page slots[t] / page_size; -1 skips the
+ * token, any other value outside the cache records MOE_ERR_DEVICE_FAULT.  Two
+ * tokens must not name the same slot.  FP8, for each row of head_dim elements:
+ * amax = max |x|, s = amax/448, code = E4M3_rne_satfinite(x * (1/s)); a row
+ * whose amax is below 448 * 2^-126 (1/s would overflow) gets s = 0 and codes 0.
+ * A NaN keeps its place as the NaN code; a row with an infinity gets s = inf and
+ * reads back as NaN.  T = 0 is a no-op. */
+moe_status_t moe_kv_write(const moe_kv_cache* cache, const void* k, const void* v, int T,
+                          int64_t k_stride_t, int64_t k_stride_h, int64_t v_stride_t,
+                          int64_t v_stride_h, const int32_t* slots, void* ws, void* stream);
+
+/* Reads cached positions back as contiguous bf16 rows [rows, heads, head_dim].
+ * Sequence b's rows cu_rows[b] .. cu_rows[b+1] (s32 [B+1], ascending, the last
+ * one = rows) are its positions starts[b], starts[b]+1, ... (starts NULL: from
+ * 0); position i is in page block_table[b*table_stride + i / page_size].  FP8: bf16(code * scale), one
+ * rounding.  A page id outside the cache or a position past the table reads
+ * as 0 and records MOE_ERR_DEVICE_FAULT.  rows = 0 is a no-op. */
+moe_status_t moe_kv_read(const moe_kv_cache* cache, const int32_t* block_table, int table_stride,
+                         const int32_t* cu_rows, const int32_t* starts, int B, int rows,
+                         void* k_out, void* v_out, void* ws, void* stream);
+
+/* Arguments of moe_paged_attention. */
+typedef struct {
+  moe_kv_cache cache;
+  int B;                      /* sequences */
+  int T;                      /* rows of q: the new tokens of all sequences */
+  int q_heads;                /* a multiple of cache.heads; query head h reads cache
+                                 head h / (q_heads / cache.heads) */
+  int max_q;                  /* at least the largest number of new tokens of a sequence */
+  int max_kv;                 /* about the longest kv_lens: sizes the split of long caches
+                                 (a hint, results do not depend on it); 0 = the table's width */
+  int table_stride;           /* entries in a row of block_table */
+  const void* q;              /* bf16, 16-byte aligned; strides in elements, multiples of 8 */
+  int64_t q_stride_t, q_stride_h;
+  void* out;                  /* bf16, as q */
+  int64_t out_stride_t, out_stride_h;
+  float* lse;                 /* f32 [T, q_heads], or NULL */
+  const int32_t* cu_q;        /* [B+1] first row of each sequence's new tokens; cu_q[B] = T */
+  const int32_t* kv_lens;     /* [B] cached positions of each sequence, its new tokens included */
+  const int32_t* block_table; /* [B, table_stride] page ids */
+  float scale;                /* of the scores; 0 = 1/sqrt(head_dim) */
+  float softcap;              /* c > 0: scores become c * tanh(score / c); 0 = off */
+  int window;                 /* w > 0: a token sees its last w positions, itself included
+                                 (causal only); 0 = off */
+  int causal;                 /* 1: new token i of n sees positions <= kv_len - n + i; 0: all
+                                 kv_len positions (e.g. cross attention to an encoder's states) */
+} moe_attention_args;
+
+/* Workspace of moe_paged_attention: the control block and the counters (the
+ * first MOE_ATTENTION_CTRL_BYTES, all zeroed before the first use; the calls
+ * leave them zero), then room for the partial results of a split cache.  With
+ * MOE_ATTENTION_WS_BYTES every call splits as far as it gains; a smaller one (at
+ * least MOE_ATTENTION_CTRL_BYTES) splits less.  Not to be shared with other
+ * entry points or with a call on another stream that may run at the same time. */
+#define MOE_ATTENTION_CTRL_BYTES (MOE_CTRL_BYTES + 65536)
+#define MOE_ATTENTION_WS_BYTES (64 << 20)
+
+/* Attention of new tokens over a paged cache that already holds their keys
+ * and values (moe_kv_write).  For new token i of sequence b and query head h:
+ *   s_j = cap(scale * q . k_j),  out = sum_j softmax(s)_j v_j over the positions
+ *   j that the mask leaves,  lse = ln sum_j exp s_j.
+ * A row whose mask leaves nothing gets out = 0 and lse = -inf.  Scores, softmax
+ * statistics and sums are binary32; the weights are rounded once for the
+ * second product and out once to bf16.  One sequence's new tokens may be
+ * any number from 0 (chunks of a prompt, drafted runs, single tokens: the form
+ * is chosen by their number).  What lies past kv_lens in a page is never used;
+ * a NaN or infinity in a value row reaches every row of a tile that has a row
+ * seeing it.  Lengths out of range record MOE_ERR_DEVICE_FAULT. */
+moe_status_t moe_paged_attention(const moe_attention_args* args, void* ws, size_t ws_bytes,
+                                 void* stream);
+
+/* Arguments of moe_verify_draft. */
+typedef struct {
+  moe_dtype_t dtype;          /* of p and q: F32 or BF16 */
+  int B, n, V;                /* sequences, drafted tokens at most (1..32), vocabulary (< 2^24) */
+  const void* p;              /* target probabilities: [B, n+1, V], rows contiguous */
+  int64_t p_stride_b, p_stride_i;
+  const void* q;              /* draft probabilities: [B, n, V] */
+  int64_t q_stride_b, q_stride_i;
+  const int32_t* draft;       /* [B, n] drafted tokens */
+  const int32_t* draft_lens;  /* [B] how many were drafted (0..n), or NULL: n each */
+  const float* u_accept;      /* [B, n] random numbers in [0, 1) */
+  const float* u_sample;      /* [B] */
+  int32_t* accepted;          /* [B] */
+  int32_t* tokens;            /* [B, n+1] */
+} moe_verify_args;
+
+/* Verifies drafted tokens against the target's probabilities from given random
+ * numbers.  Sequence b accepts its drafts i = 0, 1, ... while
+ * u_accept[i] * q_i(x_i) < p_i(x_i) (binary32); accepted[b] = r is how many.
+ * One more token is drawn from the weights max(p_r - q_r, 0), or from p_r where
+ * all were accepted (or where those weights are all zero): the smallest token
+ * whose running sum exceeds floor(u24 * total / 2^24), u24 = floor(u_sample *
+ * 2^24).  The weights (clamped to [0, 1], a NaN counts as 0) are summed as integers in units of
+ * 2^-38, so the draw does not depend on the order of the sums.  tokens: the r
+ * accepted drafts, the drawn token, then -1; the drawn token is -1 where p_r
+ * has no weight at all.  A drafted token outside [0, V) is refused and records
+ * MOE_ERR_DEVICE_FAULT.  ws: workspace of at least MOE_CTRL_BYTES. */
+moe_status_t moe_verify_draft(const moe_verify_args* args, void* ws, void* stream);
 
 #ifdef __cplusplus
 }

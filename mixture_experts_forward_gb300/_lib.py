@@ -15,16 +15,19 @@ LIB_PATH = os.path.join(_PKG, "libmoe.so")
 
 MOE_OK, MOE_ERR_INVALID_ARG, MOE_ERR_UNSUPPORTED, MOE_ERR_WORKSPACE = 0, 1, 2, 3
 MOE_ERR_CUDA, MOE_ERR_TIMEOUT, MOE_ERR_DEVICE_FAULT = 4, 5, 6
-DTYPE_FP8, DTYPE_BF16 = 0, 1
+DTYPE_FP8, DTYPE_BF16, DTYPE_F32 = 0, 1, 2
 EPI_SCATTER, EPI_STORE, EPI_SWIGLU, EPI_STORE_BF16 = 0, 1, 2, 3
 SCHED_QUEUE, SCHED_STATIC = 0, 1
 CTRL_BYTES = 256
+ATTENTION_CTRL_BYTES = CTRL_BYTES + 65536   # MOE_ATTENTION_CTRL_BYTES
+ATTENTION_WS_BYTES = 64 << 20               # MOE_ATTENTION_WS_BYTES
 
 EXPORTS = ["moe_status_string", "moe_num_sms", "moe_route", "moe_layout", "moe_quant_gather",
            "moe_grouped_gemm", "moe_scatter", "moe_workspace_size", "moe_forward",
            "moe_forward_host", "moe_get_error", "moe_debug_set_pipeline_fault", "moe_forward_plan",
            "moe_last_cuda_error", "moe_grouped_gemm_noalloc", "moe_swiglu_quant",
-           "moe_forward_workspace_map", "moe_gemm_cta_pairs"]
+           "moe_forward_workspace_map", "moe_gemm_cta_pairs", "moe_kv_write", "moe_kv_read",
+           "moe_paged_attention", "moe_verify_draft"]
 WS_NONE = (1 << 64) - 1   # MOE_WS_NONE
 
 
@@ -69,6 +72,35 @@ class WorkspaceMap(ctypes.Structure):
                [("a_rows", ctypes.c_int), ("block_m", ctypes.c_int)]
 
 
+class KvCache(ctypes.Structure):
+    _fields_ = [("dtype", ctypes.c_int), ("num_pages", ctypes.c_int),
+                ("page_size", ctypes.c_int), ("heads", ctypes.c_int), ("head_dim", ctypes.c_int),
+                ("k", ctypes.c_void_p), ("v", ctypes.c_void_p), ("k_scales", ctypes.c_void_p),
+                ("v_scales", ctypes.c_void_p)]
+
+
+class AttentionArgs(ctypes.Structure):
+    _fields_ = [("cache", KvCache), ("B", ctypes.c_int), ("T", ctypes.c_int),
+                ("q_heads", ctypes.c_int), ("max_q", ctypes.c_int), ("max_kv", ctypes.c_int),
+                ("table_stride", ctypes.c_int), ("q", ctypes.c_void_p),
+                ("q_stride_t", ctypes.c_int64), ("q_stride_h", ctypes.c_int64),
+                ("out", ctypes.c_void_p), ("out_stride_t", ctypes.c_int64),
+                ("out_stride_h", ctypes.c_int64), ("lse", ctypes.c_void_p),
+                ("cu_q", ctypes.c_void_p), ("kv_lens", ctypes.c_void_p),
+                ("block_table", ctypes.c_void_p), ("scale", ctypes.c_float),
+                ("softcap", ctypes.c_float), ("window", ctypes.c_int), ("causal", ctypes.c_int)]
+
+
+class VerifyArgs(ctypes.Structure):
+    _fields_ = [("dtype", ctypes.c_int), ("B", ctypes.c_int), ("n", ctypes.c_int),
+                ("V", ctypes.c_int), ("p", ctypes.c_void_p), ("p_stride_b", ctypes.c_int64),
+                ("p_stride_i", ctypes.c_int64), ("q", ctypes.c_void_p),
+                ("q_stride_b", ctypes.c_int64), ("q_stride_i", ctypes.c_int64),
+                ("draft", ctypes.c_void_p), ("draft_lens", ctypes.c_void_p),
+                ("u_accept", ctypes.c_void_p), ("u_sample", ctypes.c_void_p),
+                ("accepted", ctypes.c_void_p), ("tokens", ctypes.c_void_p)]
+
+
 _lib = None
 
 
@@ -103,6 +135,11 @@ def lib():
                                                 ctypes.POINTER(WorkspaceMap)]
         L.moe_get_error.argtypes = [P, ctypes.POINTER(ctypes.c_int), P]
         L.moe_debug_set_pipeline_fault.argtypes = [I, ctypes.c_uint64]
+        Z = ctypes.c_int64
+        L.moe_kv_write.argtypes = [ctypes.POINTER(KvCache), P, P, I, Z, Z, Z, Z, P, P, P]
+        L.moe_kv_read.argtypes = [ctypes.POINTER(KvCache), P, I, P, P, I, I, P, P, P, P]
+        L.moe_paged_attention.argtypes = [ctypes.POINTER(AttentionArgs), P, ctypes.c_size_t, P]
+        L.moe_verify_draft.argtypes = [ctypes.POINTER(VerifyArgs), P, P]
         for name in EXPORTS:
             if name not in ("moe_status_string", "moe_num_sms", "moe_workspace_size",
                             "moe_last_cuda_error", "moe_gemm_cta_pairs"):
@@ -243,6 +280,155 @@ def swiglu_quant(gu: torch.Tensor, stream=None):
     _check(lib().moe_swiglu_quant(_ptr(gu), R, I, _ptr(h_q), _ptr(h_s), _stream(stream)),
            "moe_swiglu_quant")
     return h_q, h_s
+
+
+# ------------------------------------------------------------------ serving
+def _need(ok: bool, what: str, why: str):
+    if not ok:
+        raise MoeError(MOE_ERR_INVALID_ARG, f"{what}: {why}")
+
+
+def _dense(t, dtype) -> bool:
+    return t.dtype is dtype and t.is_contiguous()
+
+
+def new_kv_cache(dtype, num_pages, page_size, heads, head_dim, device="cuda"):
+    """(k, v, k_scales, v_scales) of a zeroed paged cache; the scales are None
+    for DTYPE_BF16."""
+    shape = (num_pages, heads, page_size, head_dim)
+    fp8 = dtype == DTYPE_FP8
+    kv = [torch.zeros(shape, dtype=torch.uint8 if fp8 else torch.bfloat16, device=device)
+          for _ in range(2)]
+    sc = [torch.zeros(shape[:3], dtype=torch.float32, device=device) if fp8 else None
+          for _ in range(2)]
+    return (*kv, *sc)
+
+
+def _cache(what, k, v, k_scales, v_scales) -> KvCache:
+    """The cache of these page tensors: u8 codes [P, H, page, D] with f32 scales
+    [P, H, page], or bf16 pages without scales."""
+    P, H, page, D = k.shape
+    _need(v.shape == k.shape and k.is_contiguous() and v.is_contiguous() and v.dtype is k.dtype,
+          what, "k and v pages must be contiguous, of one shape and type")
+    if k.dtype is torch.uint8:
+        _need(k_scales is not None and v_scales is not None and
+              _dense(k_scales, torch.float32) and _dense(v_scales, torch.float32) and
+              k_scales.shape == k.shape[:3] and v_scales.shape == k.shape[:3],
+              what, "an FP8 cache needs f32 scales [pages, heads, page_size]")
+        return KvCache(DTYPE_FP8, P, page, H, D, k.data_ptr(), v.data_ptr(), k_scales.data_ptr(),
+                       v_scales.data_ptr())
+    _need(k.dtype is torch.bfloat16, what, "pages are uint8 (E4M3 codes) or bfloat16")
+    return KvCache(DTYPE_BF16, P, page, H, D, k.data_ptr(), v.data_ptr(), None, None)
+
+
+def _keep(stream, *tensors):
+    """Results allocated on the current stream and written on another one."""
+    if stream is not None:
+        for t in tensors:
+            if t is not None:
+                t.record_stream(stream)
+
+
+def kv_write(k: torch.Tensor, v: torch.Tensor, slots: torch.Tensor, k_cache: torch.Tensor,
+             v_cache: torch.Tensor, ws: torch.Tensor, k_scales=None, v_scales=None, stream=None):
+    """moe_kv_write: k, v bf16 [T, heads, head_dim] (strided views allowed, the
+    last dimension contiguous) into the slots s32 [T] of a paged cache."""
+    what = "moe_kv_write"
+    c = _cache(what, k_cache, v_cache, k_scales, v_scales)
+    T = k.shape[0]
+    _need(k.shape == (T, c.heads, c.head_dim) and v.shape == k.shape and
+          k.dtype is torch.bfloat16 and v.dtype is torch.bfloat16 and k.stride(2) == 1 and
+          v.stride(2) == 1, what, "k and v are bf16 [T, heads, head_dim] with contiguous rows")
+    _need(_dense(slots, torch.int32) and slots.numel() == T, what, "slots is int32 [T]")
+    _check(lib().moe_kv_write(c, k.data_ptr(), v.data_ptr(), T, k.stride(0), k.stride(1),
+                              v.stride(0), v.stride(1), slots.data_ptr(), ws.data_ptr(),
+                              _stream(stream)), what)
+
+
+def kv_read(k_cache: torch.Tensor, v_cache: torch.Tensor, block_table: torch.Tensor,
+            cu_rows: torch.Tensor, rows: int, ws: torch.Tensor, k_scales=None, v_scales=None,
+            starts=None, stream=None):
+    """moe_kv_read: (k, v) bf16 [rows, heads, head_dim]; rows = cu_rows[-1]."""
+    what = "moe_kv_read"
+    c = _cache(what, k_cache, v_cache, k_scales, v_scales)
+    B = cu_rows.numel() - 1
+    _need(_dense(block_table, torch.int32) and block_table.dim() == 2 and
+          block_table.shape[0] == B and _dense(cu_rows, torch.int32), what,
+          "block_table is int32 [B, entries], cu_rows int32 [B+1]")
+    _need(starts is None or (_dense(starts, torch.int32) and starts.numel() == B), what,
+          "starts is int32 [B]")
+    k = torch.empty(rows, c.heads, c.head_dim, dtype=torch.bfloat16, device=k_cache.device)
+    v = torch.empty_like(k)
+    _check(lib().moe_kv_read(c, block_table.data_ptr(), block_table.shape[1], cu_rows.data_ptr(),
+                             None if starts is None else starts.data_ptr(), B, rows, k.data_ptr(),
+                             v.data_ptr(), ws.data_ptr(), _stream(stream)), what)
+    _keep(stream, k, v)
+    return k, v
+
+
+def paged_attention(q: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.Tensor,
+                    block_table: torch.Tensor, cu_q: torch.Tensor, kv_lens: torch.Tensor,
+                    ws: torch.Tensor, max_q: int, max_kv: int = 0, k_scales=None, v_scales=None,
+                    scale: float = 0.0, softcap: float = 0.0, window: int = 0, causal=True,
+                    out=None, lse: bool = False, stream=None):
+    """moe_paged_attention: (out bf16 [T, q_heads, head_dim], lse f32 [T, q_heads]
+    or None) of q bf16 [T, q_heads, head_dim].  ws: new_workspace(
+    ATTENTION_WS_BYTES), kept by the caller for its attention calls."""
+    what = "moe_paged_attention"
+    c = _cache(what, k_cache, v_cache, k_scales, v_scales)
+    T, Hq, D = q.shape
+    B = kv_lens.numel()
+    _need(q.dtype is torch.bfloat16 and D == c.head_dim and q.stride(2) == 1, what,
+          "q is bf16 [T, q_heads, head_dim] with contiguous rows")
+    _need(_dense(block_table, torch.int32) and block_table.dim() == 2 and
+          block_table.shape[0] == B and _dense(cu_q, torch.int32) and cu_q.numel() == B + 1 and
+          _dense(kv_lens, torch.int32), what,
+          "block_table is int32 [B, entries], cu_q int32 [B+1], kv_lens int32 [B]")
+    if out is None:
+        out = torch.empty(T, Hq, D, dtype=torch.bfloat16, device=q.device)
+        _keep(stream, out)
+    else:
+        _need(out.dtype is torch.bfloat16 and out.shape == q.shape and out.stride(2) == 1, what,
+              "out is bf16, shaped like q, with contiguous rows")
+    sums = None
+    if lse:
+        sums = torch.empty(T, Hq, dtype=torch.float32, device=q.device)
+        _keep(stream, sums)
+    a = AttentionArgs(c, B, T, Hq, max_q, max_kv, block_table.shape[1], q.data_ptr(), q.stride(0),
+                      q.stride(1), out.data_ptr(), out.stride(0), out.stride(1),
+                      None if sums is None else sums.data_ptr(), cu_q.data_ptr(),
+                      kv_lens.data_ptr(), block_table.data_ptr(), scale, softcap, window,
+                      1 if causal else 0)
+    _check(lib().moe_paged_attention(a, ws.data_ptr(), ws.numel(), _stream(stream)), what)
+    return out, sums
+
+
+def verify_draft(p: torch.Tensor, q: torch.Tensor, draft: torch.Tensor, u_accept: torch.Tensor,
+                 u_sample: torch.Tensor, ws: torch.Tensor, draft_lens=None, stream=None):
+    """moe_verify_draft: (accepted s32 [B], tokens s32 [B, n+1]) of target
+    probabilities p [B, n+1, V] and draft probabilities q [B, n, V] (f32 or bf16)."""
+    what = "moe_verify_draft"
+    B, n, V = q.shape
+    _need(p.shape == (B, n + 1, V) and p.dtype is q.dtype and
+          (p.dtype is torch.float32 or p.dtype is torch.bfloat16) and
+          (V == 1 or (p.stride(2) == 1 and q.stride(2) == 1)), what,
+          "p is [B, n+1, V] and q [B, n, V], f32 or bf16, with contiguous rows")
+    _need(_dense(draft, torch.int32) and draft.shape == (B, n) and
+          _dense(u_accept, torch.float32) and u_accept.shape == (B, n) and
+          _dense(u_sample, torch.float32) and u_sample.numel() == B, what,
+          "draft is int32 [B, n], u_accept f32 [B, n], u_sample f32 [B]")
+    _need(draft_lens is None or (_dense(draft_lens, torch.int32) and draft_lens.numel() == B),
+          what, "draft_lens is int32 [B]")
+    accepted = torch.empty(B, dtype=torch.int32, device=p.device)
+    tokens = torch.empty(B, n + 1, dtype=torch.int32, device=p.device)
+    a = VerifyArgs(DTYPE_F32 if p.dtype is torch.float32 else DTYPE_BF16, B, n, V, p.data_ptr(),
+                   p.stride(0), p.stride(1), q.data_ptr(), q.stride(0), q.stride(1),
+                   draft.data_ptr(), None if draft_lens is None else draft_lens.data_ptr(),
+                   u_accept.data_ptr(), u_sample.data_ptr(), accepted.data_ptr(),
+                   tokens.data_ptr())
+    _check(lib().moe_verify_draft(a, ws.data_ptr(), _stream(stream)), what)
+    _keep(stream, accepted, tokens)
+    return accepted, tokens
 
 
 # ------------------------------------------------------------------ forward

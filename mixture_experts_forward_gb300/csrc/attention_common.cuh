@@ -1,0 +1,186 @@
+// What the two attention kernels share: where a tile's rows stand, the range
+// of keys they see, and the joining of a split tile's parts.
+//
+// A tile is a run of rows of one (sequence, cache head); row r is new token
+// r / group with query head r % group of the head's group, so every head
+// layout, from one query head per cache head to all of them, fills tiles alike.
+#pragma once
+
+#include "ieee_math.cuh"
+#include "serve_internal.cuh"
+
+namespace moe {
+
+constexpr float kLog2e = 1.44269504088896340736f;
+constexpr float kLn2 = 0.69314718055994530942f;
+
+__device__ __forceinline__ float exp2_approx(float x) {
+  float y;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
+__device__ __forceinline__ float rcp_approx(float x) {
+  float y;
+  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
+
+// c * tanh(x / c), by tanh(t) = 1 - 2 / (e^(2t) + 1): absolute error about
+// 2^-23 * c (k = 2 log2(e) / c; e^(2t) overflows to inf and underflows to 0 at
+// the right ends).
+__device__ __forceinline__ float soft_capped(float x, float k, float c) {
+  const float e = exp2_approx(x * k);
+  return c - 2.0f * c * rcp_approx(e + 1.0f);
+}
+
+// One tile's place in its sequence.
+struct TileView {
+  int b, h, first_row;     // sequence, cache head, first row of the tile
+  int rows;                // rows of the tile that exist (0: nothing to do)
+  int q0;                  // row of q of the sequence's first new token
+  int q_len, kv_len;
+  int lo, hi;              // keys that any row of the tile sees (hi <= lo: none)
+};
+
+// The keys row r (of the sequence) sees: [row_lo, row_hi).
+__device__ __forceinline__ int row_hi(const AttnParams& p, const TileView& t, int tok) {
+  return p.causal ? min(t.kv_len, t.kv_len - t.q_len + tok + 1) : t.kv_len;
+}
+__device__ __forceinline__ int row_lo(const AttnParams& p, const TileView& t, int tok) {
+  return p.window > 0 ? max(0, t.kv_len - t.q_len + tok + 1 - p.window) : 0;
+}
+
+__device__ __forceinline__ TileView tile_view(const AttnParams& p, int b, int h, int tile,
+                                              int tile_rows, bool report) {
+  TileView t;
+  t.b = b;
+  t.h = h;
+  t.first_row = tile * tile_rows;
+  t.q0 = __ldg(p.cu_q + b);
+  t.q_len = __ldg(p.cu_q + b + 1) - t.q0;
+  t.kv_len = __ldg(p.kv_lens + b);
+  if (t.q0 < 0 || t.q_len < 0 || t.q_len > p.max_q || t.q0 > p.T - t.q_len) {
+    if (report) set_error(p.ctrl, MOE_ERR_DEVICE_FAULT, 20);
+    t.q_len = 0;
+    t.rows = 0;
+    t.lo = t.hi = 0;
+    return t;
+  }
+  const int64_t room = static_cast<int64_t>(p.table_stride) << p.c.page_log2;
+  if (t.kv_len < 0 || t.kv_len > room) {
+    if (report) set_error(p.ctrl, MOE_ERR_DEVICE_FAULT, 21);
+    t.kv_len = t.kv_len < 0 ? 0 : static_cast<int>(room);
+  }
+  t.rows = min(tile_rows, t.q_len * p.group - t.first_row);
+  if (t.rows <= 0) {
+    t.rows = 0;
+    t.lo = t.hi = 0;
+    return t;
+  }
+  t.lo = row_lo(p, t, t.first_row / p.group);
+  t.hi = max(0, row_hi(p, t, (t.first_row + t.rows - 1) / p.group));
+  return t;
+}
+
+// A tile's keys are cut into parts of p.chunk from `base` (t.lo rounded down
+// to `align`), the last part taking what is left.
+struct Parts {
+  int base, count;         // count <= p.splits; 0: the tile sees no key
+};
+__device__ __forceinline__ Parts tile_parts(const AttnParams& p, const TileView& t, int align) {
+  Parts s;
+  s.base = t.lo / align * align;
+  s.count = t.hi > t.lo ? min(p.splits, (t.hi - s.base + p.chunk - 1) / p.chunk) : 0;
+  return s;
+}
+
+// Row r's place in out and lse.
+__device__ __forceinline__ __nv_bfloat16* out_row(const AttnParams& p, const TileView& t, int r) {
+  const int rr = t.first_row + r, tok = rr / p.group;
+  return p.out + static_cast<int64_t>(t.q0 + tok) * p.o_st +
+         static_cast<int64_t>(t.h * p.group + rr - tok * p.group) * p.o_sh;
+}
+__device__ __forceinline__ float* lse_at(const AttnParams& p, const TileView& t, int r) {
+  const int rr = t.first_row + r, tok = rr / p.group;
+  return p.lse + static_cast<int64_t>(t.q0 + tok) * p.q_heads + t.h * p.group + rr -
+         tok * p.group;
+}
+
+__device__ __forceinline__ float lse_of(float m, float l) {
+  return l == 0.0f ? __int_as_float(0xff800000) : (m + log2f(l)) * kLn2;
+}
+
+// A part's result: rows x D sums, then rows maxima, then rows sums of weights
+// (the maximum m in log2 units; sums relative to 2^m).
+template <int D>
+__host__ __device__ __forceinline__ int64_t partial_floats(int rows) {
+  return static_cast<int64_t>(rows) * (D + 2);
+}
+
+// Called by every thread of the CTA (`threads` of them) after the CTA's part
+// has been written to p.partial: the last CTA of the tile to arrive joins the
+// parts, in their order, and writes out and lse.  `tile` numbers the tiles
+// of the launch, kRows the rows that a part has room for.
+template <int D>
+__device__ __forceinline__ void join_parts(const AttnParams& p, const TileView& t, int64_t tile,
+                                           int part_rows, int count, int tid, int threads,
+                                           int* s_flag) {
+  __threadfence();
+  __syncthreads();
+  if (tid == 0) {
+    const unsigned prev = atomicAdd(p.counters + tile, 1u);
+    const int last = prev == static_cast<unsigned>(count - 1);
+    if (last) p.counters[tile] = 0u;   // every part has arrived
+    *s_flag = last;
+  }
+  __syncthreads();
+  if (!*s_flag) return;
+  __threadfence();
+  const int64_t stride = partial_floats<D>(part_rows);
+  const float* parts = p.partial + tile * p.splits * stride;
+  const float* ml = parts + static_cast<int64_t>(part_rows) * D;
+  for (int i = tid; i < t.rows * (D / 4); i += threads) {
+    const int r = i / (D / 4), d = (i % (D / 4)) * 4;
+    float m = __int_as_float(0xff800000);
+    for (int s = 0; s < count; ++s) m = fmaxf(m, __ldcg(ml + s * stride + r));
+    const float ref = m == __int_as_float(0xff800000) ? 0.0f : m;
+    float l = 0.0f;
+    float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll 4
+    for (int s = 0; s < count; ++s) {
+      const float w = exp2_approx(__ldcg(ml + s * stride + r) - ref);
+      const float4 x = __ldcg(reinterpret_cast<const float4*>(parts + s * stride + r * D + d));
+      l = fmaf(w, __ldcg(ml + s * stride + part_rows + r), l);
+      o.x = fmaf(w, x.x, o.x);
+      o.y = fmaf(w, x.y, o.y);
+      o.z = fmaf(w, x.z, o.z);
+      o.w = fmaf(w, x.w, o.w);
+    }
+    const float inv = l == 0.0f ? 0.0f : 1.0f / l;
+    __nv_bfloat162 a = __floats2bfloat162_rn(o.x * inv, o.y * inv);
+    __nv_bfloat162 b = __floats2bfloat162_rn(o.z * inv, o.w * inv);
+    uint2 u;
+    u.x = *reinterpret_cast<uint32_t*>(&a);
+    u.y = *reinterpret_cast<uint32_t*>(&b);
+    *reinterpret_cast<uint2*>(out_row(p, t, r) + d) = u;
+    if (d == 0 && p.lse != nullptr) *lse_at(p, t, r) = lse_of(m, l);
+  }
+}
+
+// Quantised values: the weight of key j in the second product is
+// 2^(s_j - m) * vs_j for the value scale vs_j, and m is the maximum of
+// s_j + log2 vs_j, so the product stays at or below 1 whatever the scales are
+// and fits binary16; the softmax's own sum divides vs_j out again in binary32.
+// Scales below 2^-100 (values below 448 * 2^-100 = 3.5e-28) count as 2^-100.
+__device__ __forceinline__ float value_scale(float vs) { return fmaxf(vs, 7.8886090522101181e-31f); }
+
+// The binary16 form of a query row: scaled by a power of two that brings its
+// largest element near 2^8, so that only elements 2^-22 below that one lose bits.
+__device__ __forceinline__ void row_pow2(float amax, float& mul, float& inv) {
+  int ex = static_cast<int>((__float_as_uint(amax) >> 23) & 255u);
+  ex = max(ex, 9);
+  mul = __uint_as_float(static_cast<uint32_t>(262 - ex) << 23);
+  inv = __uint_as_float(static_cast<uint32_t>(ex - 8) << 23);
+}
+
+}  // namespace moe

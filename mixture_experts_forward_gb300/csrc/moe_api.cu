@@ -23,8 +23,15 @@ namespace {
 constexpr unsigned long long kDefaultTimeoutNs = 2000000000ull;  // 2 s
 int g_drop_producer = 0;
 unsigned long long g_timeout_ns = kDefaultTimeoutNs;
+thread_local char g_last_error[256] = "";
 
-bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
+}  // namespace
+
+// Shared with the serving operators' entry points (moe_internal.cuh).
+namespace moe {
+
+unsigned long long wait_limit_ns() { return g_timeout_ns; }
+bool loads_dropped() { return g_drop_producer != 0; }
 
 int device_sms() {
   static int cached[64] = {0};
@@ -52,6 +59,17 @@ PFN_cuTensorMapEncodeTiled_v12000 encode_fn() {
   });
   return fn;
 }
+
+moe_status_t cuda_status(cudaError_t e) {
+  if (e == cudaSuccess) return MOE_OK;
+  std::snprintf(g_last_error, sizeof(g_last_error), "%s: %s", cudaGetErrorName(e),
+                cudaGetErrorString(e));
+  return MOE_ERR_CUDA;
+}
+
+}  // namespace moe
+
+namespace {
 
 // 2-D K-major tensor map: rows of `inner` elements, `outer` rows, 128-byte
 // swizzle, box = 128 bytes x box_rows; out-of-range rows read as zero.
@@ -92,15 +110,6 @@ bool make_tmap_rows(CUtensorMap* m, const void* base, bool fp8, uint64_t inner, 
                   CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
                   CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
   return r == CUDA_SUCCESS;
-}
-
-thread_local char g_last_error[256] = "";
-
-moe_status_t cuda_status(cudaError_t e) {
-  if (e == cudaSuccess) return MOE_OK;
-  std::snprintf(g_last_error, sizeof(g_last_error), "%s: %s", cudaGetErrorName(e),
-                cudaGetErrorString(e));
-  return MOE_ERR_CUDA;
 }
 
 int auto_block_m(bool fp8, long long R, int E) {

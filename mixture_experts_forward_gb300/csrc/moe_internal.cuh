@@ -1,9 +1,19 @@
 // Host-side declarations shared by the C-ABI layer and the kernel files.
 #pragma once
 
+#include <cudaTypedefs.h>
+
 #include "moe_common.cuh"
 
 namespace moe {
+
+// Host helpers of the C-ABI layer (moe_api.cu).
+inline bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
+int device_sms();                                // 0 on error; cached per device
+PFN_cuTensorMapEncodeTiled_v12000 encode_fn();   // nullptr if the driver has none
+moe_status_t cuda_status(cudaError_t e);         // records the text of an error
+unsigned long long wait_limit_ns();              // limit of the pipelines' waits
+bool loads_dropped();                            // moe_debug_set_pipeline_fault
 
 // Small kernels that run next to (or just before) the grouped GEMM ask for
 // the largest shared-memory carveout: an SM still holding one of their CTAs
