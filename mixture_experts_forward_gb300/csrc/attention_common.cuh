@@ -120,20 +120,21 @@ __host__ __device__ __forceinline__ int64_t partial_floats(int rows) {
 // Called by every thread of the CTA (`threads` of them) after the CTA's part
 // has been written to p.partial: the last CTA of the tile to arrive joins the
 // parts, in their order, and writes out and lse.  `tile` numbers the tiles
-// of the launch, kRows the rows that a part has room for.
+// of the launch, part_rows the rows that a part has room for; named barrier
+// `bar` joins the threads.
 template <int D>
 __device__ __forceinline__ void join_parts(const AttnParams& p, const TileView& t, int64_t tile,
                                            int part_rows, int count, int tid, int threads,
-                                           int* s_flag) {
+                                           int bar, int* s_flag) {
   __threadfence();
-  __syncthreads();
+  named_bar_sync(bar, threads);
   if (tid == 0) {
     const unsigned prev = atomicAdd(p.counters + tile, 1u);
     const int last = prev == static_cast<unsigned>(count - 1);
     if (last) p.counters[tile] = 0u;   // every part has arrived
     *s_flag = last;
   }
-  __syncthreads();
+  named_bar_sync(bar, threads);
   if (!*s_flag) return;
   __threadfence();
   const int64_t stride = partial_floats<D>(part_rows);

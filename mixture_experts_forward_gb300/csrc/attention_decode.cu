@@ -529,7 +529,8 @@ __global__ void __launch_bounds__(kThreads, 2) decode_kernel(const AttnParams p)
       }
     }
   }
-  if (!whole_tile) join_parts<D>(p, t, tile, kDecodeRows, parts.count, tid, kThreads, &s_flag);
+  if (!whole_tile) join_parts<D>(p, t, tile, kDecodeRows, parts.count, tid, kThreads, 0,
+                                     &s_flag);
 }
 
 template <int D, bool kFP8>

@@ -1,0 +1,929 @@
+// Attention of many rows over the paged cache: chunks of prompts, whole
+// prompts and drafted runs.
+//
+// A CTA takes up to 256 rows (new tokens x query heads of one cache head) as
+// two tiles of 128, and walks the keys they see in tiles of 128.  Both products
+// run on tcgen05 with their results in tensor memory: S = Q K^T (both operands
+// in shared memory) and O += P V with P read from tensor memory, where the
+// softmax threads leave it in place of S, and V as it lies in the cache
+// (keys x channels, the MN-major form of the B operand).  Per pair of row tiles
+// and key tile the tensor core works 4 * 128 * 128 * D * 2 operations, about
+// 2 * 1024 cycles at D = 128, and the exponentials take as long (16 per cycle), so
+// the two row tiles alternate: while one's softmax runs, the tensor core works for the
+// other.  Roles:
+//   warps 0-3, 4-7   softmax of row tile 0, 1: a thread owns a row (a lane of
+//                    tensor memory), so maxima and sums need no shuffles;
+//   warp 8           (BF16) TMA loads of K and V pages into a ring of tiles;
+//   warp 9           issues the MMAs;
+//   warps 12-15      (FP8) copy codes by cp.async into a ring of their own and turn
+//                    them into binary16 tiles: K's codes exactly (their
+//                    scale multiplies the score in binary32), V's times vs * 2^-e, 2^e
+//                    the tile's largest value scale, which keeps them in range
+//                    with 2^-11 of relative rounding; 2^e goes into the softmax.
+// O is rescaled only when a row's maximum grew by more than 2^8 since its
+// reference (the weights then stay below 2^8, far inside their types), which
+// leaves the rescale to a few tiles per row; the softmax threads do it themselves
+// between their S and their P, when no product of theirs is running.
+// With at most 128 rows both softmax groups work on the same rows, on key tiles
+// of even and odd number, each with its own O; they are joined at the end.
+//
+// What lies past the last key must not meet a zero weight (0 * NaN): the second
+// product runs over the 16-key steps that hold keys, and the rest of a last step is
+// zeroed in shared memory before it.
+#include <cstring>
+
+#include "attention_common.cuh"
+
+namespace moe {
+namespace {
+
+constexpr int kKeys = 128;          // keys per tile
+constexpr int kRows = 128;          // rows per row tile
+constexpr uint32_t kHalfBytes = kKeys * 128;   // 64 channels of 128 rows
+
+template <int D, bool kFP8>
+struct TileShape {
+  static constexpr int kTileBytes = kKeys * D * 2;          // Q, K or V tile
+  static constexpr int kSlots = kFP8 ? (D == 128 ? 3 : 6) : (D == 128 ? 5 : 8);
+  static constexpr int kRaw = kFP8 ? 3 : 0;                 // tiles of codes in flight
+  static constexpr int kRawBytes = kKeys * D;
+  static constexpr int kScaleSlots = 3;
+  static constexpr int kThreads = kFP8 ? 512 : 384;
+  // offsets in shared memory
+  static constexpr int oQ = 0;
+  static constexpr int oSlots = 2 * kTileBytes;
+  static constexpr int oRaw = oSlots + kSlots * kTileBytes;
+  static constexpr int oRawScale = oRaw + kRaw * kRawBytes;            // [raw][2][128] f32
+  static constexpr int oScale = oRawScale + (kFP8 ? kRaw * 1024 : 0);  // [slot][ks 128 | vs 128]
+  static constexpr int oRowf = oScale + (kFP8 ? kScaleSlots * 1024 : 0);
+  static constexpr int oEnd = oRowf + (kFP8 ? 1024 : 0);
+  static constexpr int kSmem = oEnd;
+  // setmaxnreg shares: softmax, the rest (BF16: 384 x 168 registers at launch, 2 x 128 x 208 +
+  // 128 x 80 = 63488 of 64512; FP8: 512 x 128, 2 x 128 x 192 + 2 x 128 x 64 = 65536)
+  static constexpr int kRegsSoftmax = kFP8 ? 192 : 208;
+  static constexpr int kRegsOther = kFP8 ? 64 : 80;
+  static_assert(kSlots * kTileBytes >= kRows * D * 4, "the join of two groups fits the ring");
+};
+
+__device__ __forceinline__ void tmem_ld32(uint32_t taddr, float* v) {
+  uint32_t r[32];
+  asm volatile(
+      "tcgen05.ld.sync.aligned.32x32b.x32.b32 "
+      "{%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,"
+      "%16,%17,%18,%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31}, [%32];"
+      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]),
+        "=r"(r[7]), "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]),
+        "=r"(r[14]), "=r"(r[15]), "=r"(r[16]), "=r"(r[17]), "=r"(r[18]), "=r"(r[19]),
+        "=r"(r[20]), "=r"(r[21]), "=r"(r[22]), "=r"(r[23]), "=r"(r[24]), "=r"(r[25]),
+        "=r"(r[26]), "=r"(r[27]), "=r"(r[28]), "=r"(r[29]), "=r"(r[30]), "=r"(r[31])
+      : "r"(taddr));
+#pragma unroll
+  for (int i = 0; i < 32; ++i) v[i] = __uint_as_float(r[i]);
+}
+
+// tcgen05.wait::ld with the 32 registers of an earlier load passed through it,
+// so that their first use stays below the wait
+__device__ __forceinline__ void tmem_ld_wait32(float* v) {
+  asm volatile("tcgen05.wait::ld.sync.aligned;"
+               : "+f"(v[0]), "+f"(v[1]), "+f"(v[2]), "+f"(v[3]), "+f"(v[4]), "+f"(v[5]),
+                 "+f"(v[6]), "+f"(v[7]), "+f"(v[8]), "+f"(v[9]), "+f"(v[10]), "+f"(v[11]),
+                 "+f"(v[12]), "+f"(v[13]), "+f"(v[14]), "+f"(v[15]), "+f"(v[16]), "+f"(v[17]),
+                 "+f"(v[18]), "+f"(v[19]), "+f"(v[20]), "+f"(v[21]), "+f"(v[22]), "+f"(v[23]),
+                 "+f"(v[24]), "+f"(v[25]), "+f"(v[26]), "+f"(v[27]), "+f"(v[28])
+               :
+               : "memory");
+  asm volatile("" : "+f"(v[29]), "+f"(v[30]), "+f"(v[31])::"memory");
+}
+
+__device__ __forceinline__ void tmem_st16(uint32_t taddr, const uint32_t* r) {
+  asm volatile(
+      "tcgen05.st.sync.aligned.32x32b.x16.b32 [%0], "
+      "{%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16};" ::"r"(taddr),
+      "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]),
+      "r"(r[8]), "r"(r[9]), "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15])
+      : "memory");
+}
+__device__ __forceinline__ void tmem_st_wait() {
+  asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory");
+}
+
+// D[tmem] (+)= A[tmem] * B[smem]: A is K-major in tensor memory (two 16-bit
+// elements per column), B MN-major: 128-byte rows of 64 elements (128-byte swizzle), 8-row
+// groups along K 1024 bytes apart, the groups of 64 along N kHalfBytes apart (the leading
+// offset, bits 16..29 of the low word).
+__device__ __forceinline__ void umma_ts(uint32_t d_tmem, uint32_t a_tmem, uint32_t b_lo,
+                                        uint32_t idesc, uint32_t accumulate) {
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t.reg .b64 bd;\n\tsetp.ne.b32 p, %4, 0;\n\t"
+      "mov.b64 bd, {%2, %5};\n\t"
+      "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], bd, %3, p;\n\t}" ::"r"(d_tmem),
+      "r"(a_tmem), "r"(b_lo), "r"(idesc), "r"(accumulate), "r"(kDescHi)
+      : "memory");
+}
+__device__ __forceinline__ uint32_t mn_desc_lo(uint32_t saddr) {
+  return ((saddr & 0x3FFFF) >> 4) | ((kHalfBytes >> 4) << 16);
+}
+
+// (a0, a1) * (b, b) + (c, c)
+__device__ __forceinline__ void fma2_bc(float& d0, float& d1, float a0, float a1, float b, float c) {
+  asm("{\n\t.reg .b64 pa, pb, pc;\n\t"
+      "mov.b64 pa, {%2, %3};\n\tmov.b64 pb, {%4, %4};\n\tmov.b64 pc, {%5, %5};\n\t"
+      "fma.rn.f32x2 pa, pa, pb, pc;\n\tmov.b64 {%0, %1}, pa;\n\t}"
+      : "=f"(d0), "=f"(d1)
+      : "f"(a0), "f"(a1), "f"(b), "f"(c));
+}
+__device__ __forceinline__ void add2(float& d0, float& d1, float a0, float a1) {
+  asm("{\n\t.reg .b64 pa, pd;\n\tmov.b64 pd, {%0, %1};\n\tmov.b64 pa, {%2, %3};\n\t"
+      "add.rn.f32x2 pd, pd, pa;\n\tmov.b64 {%0, %1}, pd;\n\t}"
+      : "+f"(d0), "+f"(d1)
+      : "f"(a0), "f"(a1));
+}
+
+template <int N>
+__device__ __forceinline__ void regs_inc() {
+  asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(N));
+}
+template <int N>
+__device__ __forceinline__ void regs_dec() {
+  asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(N));
+}
+// Named barrier among `count` threads that tells them whether any had `x` set.
+__device__ __forceinline__ bool named_bar_any(int id, int count, bool x) {
+  uint32_t r;
+  asm volatile(
+      "{\n\t.reg .pred a, b;\n\tsetp.ne.u32 a, %3, 0;\n\t"
+      "barrier.cta.red.or.pred b, %1, %2, a;\n\tselp.u32 %0, 1, 0, b;\n\t}"
+      : "=r"(r)
+      : "r"(id), "r"(count), "r"(x ? 1u : 0u)
+      : "memory");
+  return r != 0;
+}
+__device__ __forceinline__ void fence_async_smem() {
+  asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+}
+
+// The order in which key and value tiles are taken: K of the first `lead`
+// tiles, then V of tile i and K of tile i + lead in turn (lead 1: two row tiles share
+// every key tile; lead 2: they take the even and the odd ones).
+struct Item {
+  bool v;
+  int i;
+};
+__device__ __forceinline__ Item item_at(int f, int n, int lead) {
+  const int first = min(lead, n);
+  Item it;
+  if (f < first) {
+    it.v = false;
+    it.i = f;
+    return it;
+  }
+  f -= first;
+  const int pairs = n - first;
+  if (f < 2 * pairs) {
+    it.v = (f & 1) == 0;
+    it.i = it.v ? (f >> 1) : (f >> 1) + lead;
+  } else {
+    it.v = true;
+    it.i = f - pairs;
+  }
+  return it;
+}
+
+struct Bars {
+  uint64_t full[8], empty[8];     // the ring of tiles
+  uint64_t q_full;
+  uint64_t s_full[2], p_full[2], o_done[2];
+  uint64_t sc_full[3], sc_empty[3];
+  uint64_t drain;
+  uint32_t tmem;
+  int abort;
+  int flag;
+  int e[3];                       // FP8: exponent of each tile's value scales
+  float red[2][4];
+};
+
+template <int D, bool kFP8>
+__global__ void __launch_bounds__(TileShape<D, kFP8>::kThreads, 1)
+    tiles_kernel(const __grid_constant__ CUtensorMap map_k,
+                 const __grid_constant__ CUtensorMap map_v, const AttnParams p) {
+  using S = TileShape<D, kFP8>;
+  extern __shared__ __align__(1024) uint8_t smem[];
+  __shared__ Bars bars;
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+
+  // ---- what this CTA has to do (late row tiles see most keys: they start first)
+  const int tiles_bh = p.B * p.c.heads;
+  const int rt = p.row_tiles - 1 - static_cast<int>(blockIdx.x / tiles_bh);
+  const int bh = static_cast<int>(blockIdx.x % tiles_bh);
+  const int b = bh / p.c.heads, h = bh - b * p.c.heads;
+  const int part = blockIdx.y;
+  const TileView t = tile_view(p, b, h, rt, 2 * kRows, part == 0 && rt == 0 && tid == 0);
+  if (t.rows == 0) return;
+  const Parts parts = tile_parts(p, t, kKeys);
+  if (part >= max(1, parts.count)) return;
+  const int k0 = parts.base + part * p.chunk;
+  const int k1 = parts.count == 0 ? k0 : (part + 1 >= parts.count ? t.hi : k0 + p.chunk);
+  const int n = (k1 - k0 + kKeys - 1) / kKeys;                   // key tiles
+  const bool alt = t.rows <= kRows;
+  const int lead = alt ? 2 : 1;
+  int n_of[2];                                                    // key tiles of each group
+  if (alt) {
+    n_of[0] = (n + 1) / 2;
+    n_of[1] = n / 2;
+  } else {
+    const int hi0 = min(k1, row_hi(p, t, (t.first_row + kRows - 1) / p.group));
+    n_of[0] = max(0, min(n, (hi0 - k0 + kKeys - 1) / kKeys));
+    n_of[1] = n;
+  }
+
+  auto bar = [&](const uint64_t& x) { return smem_u32(&x); };
+  if (tid == 0) {
+    for (int i = 0; i < S::kSlots; ++i) {
+      mbar_init(bar(bars.full[i]), kFP8 ? 128 : 1);
+      mbar_init(bar(bars.empty[i]), 1);
+    }
+    mbar_init(bar(bars.q_full), 256);
+    for (int w = 0; w < 2; ++w) {
+      mbar_init(bar(bars.s_full[w]), 1);
+      mbar_init(bar(bars.p_full[w]), 128);
+      mbar_init(bar(bars.o_done[w]), 1);
+    }
+    for (int i = 0; i < S::kScaleSlots; ++i) {
+      mbar_init(bar(bars.sc_full[i]), 128);
+      // (row tile 0 may skip the last two key tiles at most: no later tile waits for their slots)
+      mbar_init(bar(bars.sc_empty[i]), alt ? 4 : 8);
+    }
+    mbar_init(bar(bars.drain), 1);
+    bars.abort = 0;
+    mbar_fence_init();
+  }
+  if (warp == 9) {
+    tmem_alloc(smem_u32(&bars.tmem), 512);
+    tmem_relinquish();
+  }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = bars.tmem;
+  volatile int* abort_flag = &bars.abort;
+  const uint32_t sbase = smem_u32(smem);
+
+  // A bounded wait of a whole warp, whose lanes agree on the result; the first
+  // to give up records it and stops the others.
+  auto wait = [&](uint32_t at, uint32_t parity) -> bool {
+    const bool ok = mbar_wait(at, parity, abort_flag, p.timeout_ns);
+    if (!ok && !*abort_flag) {
+      *abort_flag = 1;
+      set_error(p.ctrl, MOE_ERR_TIMEOUT, 23);
+    }
+    return __all_sync(0xffffffffu, ok);
+  };
+
+  const int32_t* table = p.table + static_cast<int64_t>(b) * p.table_stride;
+
+  if (warp < 8) {
+    // =================================================================== softmax
+    regs_inc<S::kRegsSoftmax>();
+    const int w = warp >> 2;
+    const int row = tid & 127;                       // lane of tensor memory
+    const int my = alt ? row : w * kRows + row;      // row of the CTA's rows
+    const bool real = my < t.rows;
+    const uint32_t lanes = static_cast<uint32_t>(warp & 3) << 21;   // this warp's lanes (<< 16)
+    // ---- the query tiles, in the layout of a K-major operand
+    {
+      constexpr int kPieces = D / 8;                 // 16-byte pieces of a row
+      constexpr int kPerPass = 128 / kPieces;        // rows per pass of the group
+      const int c = row % kPieces;
+      const int rows_here = alt ? 64 : 128;
+      const uint32_t flip = p.scale < 0.0f ? 0x80008000u : 0u;   // the scores' factor is positive
+      for (int r = row / kPieces; r < rows_here; r += kPerPass) {
+        const int tr = alt ? w * 64 + r : r;         // row within its tile
+        const int cr = alt ? tr : w * kRows + r;     // row of the CTA's rows
+        uint4 x = make_uint4(0u, 0u, 0u, 0u);
+        if (cr < t.rows) {
+          const int rr = t.first_row + cr, tok = rr / p.group;
+          x = __ldg(reinterpret_cast<const uint4*>(
+                        p.q + static_cast<int64_t>(t.q0 + tok) * p.q_st +
+                        static_cast<int64_t>(h * p.group + rr - tok * p.group) * p.q_sh) + c);
+          x.x ^= flip;
+          x.y ^= flip;
+          x.z ^= flip;
+          x.w ^= flip;
+        }
+        if constexpr (kFP8) {
+          uint32_t* xw = reinterpret_cast<uint32_t*>(&x);
+          float a = 0.0f;
+#pragma unroll
+          for (int i = 0; i < 4; ++i)
+            a = fmaxf(a, fmaxf(fabsf(__uint_as_float(xw[i] << 16)),
+                               fabsf(__uint_as_float(xw[i] & 0xffff0000u))));
+#pragma unroll
+          for (int o = 1; o < kPieces; o <<= 1) a = fmaxf(a, __shfl_xor_sync(0xffffffffu, a, o));
+          float mul, inv;
+          row_pow2(a, mul, inv);
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            __half2 hh = __floats2half2_rn(__uint_as_float(xw[i] << 16) * mul,
+                                           __uint_as_float(xw[i] & 0xffff0000u) * mul);
+            xw[i] = *reinterpret_cast<uint32_t*>(&hh);
+          }
+          if (c == 0) reinterpret_cast<float*>(smem + S::oRowf)[cr] = inv;
+        }
+        uint8_t* at = smem + S::oQ + (alt ? 0 : w) * S::kTileBytes + (c >> 3) * kHalfBytes +
+                      tr * 128 + (((c & 7) ^ (tr & 7)) << 4);
+        *reinterpret_cast<uint4*>(at) = x;
+      }
+      fence_async_smem();
+      mbar_arrive(bar(bars.q_full));
+    }
+    int r_lo = t.lo, r_hi = t.hi;
+    if (real) {
+      const int tok = (t.first_row + my) / p.group;
+      r_lo = row_lo(p, t, tok);
+      r_hi = row_hi(p, t, tok);
+    }
+    r_lo = max(r_lo, k0);
+    r_hi = min(r_hi, k1);
+    const bool idle = (alt ? (warp & 3) * 32 : w * kRows + (warp & 3) * 32) >= t.rows;
+    const int my_n = n_of[w];
+    const float cap = p.softcap, cap_k = cap > 0.0f ? 2.0f * kLog2e / cap : 0.0f;
+    float sc = fabsf(p.scale) * (cap > 0.0f ? 1.0f : kLog2e);
+    if constexpr (kFP8) {
+      if (my_n > 0) {
+        if (!wait(bar(bars.q_full), 0)) {}           // the other group wrote some of the factors
+        sc *= reinterpret_cast<const float*>(smem + S::oRowf)[my];
+      }
+    }
+    const float ninf = __int_as_float(0xff800000);
+    float m = ninf, ref = 0.0f, l = 0.0f;
+    int E = 0;                                       // FP8: O is in units of 2^E
+    const uint32_t s_tm = tmem + lanes + w * kKeys;
+    const uint32_t o_tm = tmem + lanes + 256 + w * D;
+    bool ok = true;
+    for (int c = 0; c < my_n; ++c) {
+      const int i = alt ? 2 * c + w : c;
+      const int kb = k0 + i * kKeys;
+      ok = wait(bar(bars.s_full[w]), c & 1);
+      if (!ok) break;
+      const int sslot = i % S::kScaleSlots;
+      if constexpr (kFP8) {
+        ok = wait(bar(bars.sc_full[sslot]), (i / S::kScaleSlots) & 1);
+        if (!ok) break;
+      }
+      tc_fence_after();
+      if (!idle) {
+        float s[kKeys];
+#pragma unroll
+        for (int j = 0; j < 4; ++j) tmem_ld32(s_tm + 32 * j, s + 32 * j);
+#pragma unroll
+        for (int j = 0; j < 4; ++j) tmem_ld_wait32(s + 32 * j);
+        int e = 0;
+        if constexpr (kFP8) {
+          const float4* ks = reinterpret_cast<const float4*>(smem + S::oScale + sslot * 1024);
+#pragma unroll
+          for (int j = 0; j < kKeys / 4; ++j) {
+            const float4 k4 = ks[j];
+            mul2(s[4 * j], s[4 * j + 1], s[4 * j], s[4 * j + 1], k4.x, k4.y);
+            mul2(s[4 * j + 2], s[4 * j + 3], s[4 * j + 2], s[4 * j + 3], k4.z, k4.w);
+          }
+          e = bars.e[sslot];
+        }
+        float f = sc;
+        if (cap > 0.0f) {
+#pragma unroll
+          for (int j = 0; j < kKeys; ++j) s[j] = soft_capped(s[j] * sc, cap_k, cap) * kLog2e;
+          f = 1.0f;
+        }
+        if (kb + kKeys > r_hi || kb < r_lo) {
+          const int lo = r_lo - kb, hi = r_hi - kb;
+#pragma unroll
+          for (int j = 0; j < kKeys; ++j) s[j] = (j < lo || j >= hi) ? ninf : s[j];
+        }
+        float x[4] = {s[0], s[1], s[2], s[3]};
+#pragma unroll
+        for (int j = 4; j < kKeys; ++j) x[j & 3] = fmaxf(x[j & 3], s[j]);
+        const float mx = fmaxf(fmaxf(x[0], x[1]), fmaxf(x[2], x[3])) * f;
+        m = fmaxf(m, mx == mx ? mx : ninf);
+        const float want = m == ninf ? 0.0f : m;
+        int E2 = E;
+        if constexpr (kFP8) E2 = c == 0 ? e : max(E, e);
+        if (c == 0) {
+          ref = want;
+          E = E2;
+        } else if (__any_sync(0xffffffffu, want > ref + 8.0f || E2 != E)) {
+          const float keep = ref == want ? 1.0f : exp2_approx(ref - want);
+          l *= keep;
+          const float g = kFP8 ? keep * exp2_approx(static_cast<float>(E - E2)) : keep;
+          ref = want;
+          E = E2;
+          // S of this tile is complete, so every earlier product of this group is too
+#pragma unroll 1
+          for (int d = 0; d < D; d += 16) {
+            float o[16];
+            tmem_ld16(o_tm + d, o);
+            tmem_ld_wait(o);
+            uint32_t r[16];
+#pragma unroll
+            for (int j = 0; j < 16; ++j) r[j] = __float_as_uint(o[j] * g);
+            tmem_st16(o_tm + d, r);
+          }
+        }
+        float shift = -ref;
+        if constexpr (kFP8) shift += static_cast<float>(e - E);
+        float sum0 = 0.0f, sum1 = 0.0f, sum2 = 0.0f, sum3 = 0.0f;
+#pragma unroll
+        for (int q = 0; q < 4; ++q) {
+          uint32_t r[16];
+#pragma unroll
+          for (int j = 0; j < 16; ++j) {
+            float a = s[32 * q + 2 * j], bb = s[32 * q + 2 * j + 1];
+            fma2_bc(a, bb, a, bb, f, shift);
+            a = exp2_approx(a);
+            bb = exp2_approx(bb);
+            if (j & 1) add2(sum2, sum3, a, bb); else add2(sum0, sum1, a, bb);
+            if constexpr (kFP8) {
+              __half2 hh = __floats2half2_rn(a, bb);
+              r[j] = *reinterpret_cast<uint32_t*>(&hh);
+            } else {
+              __nv_bfloat162 hh = __floats2bfloat162_rn(a, bb);
+              r[j] = *reinterpret_cast<uint32_t*>(&hh);
+            }
+          }
+          tmem_st16(s_tm + 16 * q, r);
+        }
+        float sum = (sum0 + sum1) + (sum2 + sum3);
+        if constexpr (kFP8) sum *= exp2_approx(static_cast<float>(E - e));
+        l += sum;
+        tmem_st_wait();
+      }
+      tc_fence_before();
+      if constexpr (kFP8) {
+        __syncwarp();
+        if (lane == 0) mbar_arrive(bar(bars.sc_empty[sslot]));
+      }
+      mbar_arrive(bar(bars.p_full[w]));
+    }
+    if (ok && my_n > 0) ok = wait(bar(bars.o_done[w]), 0);
+    // (group 1 hands over through the ring's memory: group 0's products read it too)
+    if (ok && alt && w == 1 && n_of[0] > 0) ok = wait(bar(bars.o_done[0]), 0);
+    tc_fence_after();
+
+    // ---- results.  Two groups on the same rows: group 1 hands its own over.
+    const bool have = ok && my_n > 0 && !idle;
+    const float unit = kFP8 ? exp2_approx(static_cast<float>(E)) : 1.0f;
+    if (!have) {
+      m = ninf;
+      l = 0.0f;
+    }
+    if (m == ninf) ref = ninf;                       // the row saw no key
+    float* other = reinterpret_cast<float*>(smem + S::oSlots);     // [128][D], pieces swizzled
+    float* other_ml = reinterpret_cast<float*>(smem + S::oQ);      // [2][128]
+    constexpr int kOutPieces = D / 4;
+    auto other_at = [&](int d4) { return other + row * D + ((d4 ^ (row & (kOutPieces - 1))) << 2); };
+    if (alt) {
+      if (w == 1) {
+        if (have) {
+#pragma unroll 1
+          for (int d = 0; d < D; d += 16) {
+            float o[16];
+            tmem_ld16(o_tm + d, o);
+            tmem_ld_wait(o);
+#pragma unroll
+            for (int j = 0; j < 4; ++j)
+              *reinterpret_cast<float4*>(other_at(d / 4 + j)) =
+                  make_float4(o[4 * j] * unit, o[4 * j + 1] * unit, o[4 * j + 2] * unit,
+                              o[4 * j + 3] * unit);
+          }
+        }
+        other_ml[row] = ref;
+        other_ml[128 + row] = l;
+      }
+      named_bar_sync(1, 256);
+    }
+    const bool writes = real && (!alt || w == 0);
+    float g0 = unit, g1 = 0.0f;
+    bool have1 = false;
+    if (alt && w == 0) {
+      const float ref1 = other_ml[row], l1 = other_ml[128 + row];
+      have1 = ref1 != ninf;
+      if (have1) {
+        const float top = fmaxf(ref, ref1);
+        const float a0 = ref == ninf ? 0.0f : exp2_approx(ref - top);
+        g1 = exp2_approx(ref1 - top);
+        l = l * a0 + l1 * g1;
+        g0 = unit * a0;
+        ref = top;
+      }
+    }
+    const bool split = parts.count > 1;
+    float* dst = p.partial + (static_cast<int64_t>(blockIdx.x) * p.splits + part) *
+                                 partial_floats<D>(p.part_rows);
+    const float inv = l == 0.0f ? 0.0f : 1.0f / l;
+    __nv_bfloat16* orow = writes && !split ? out_row(p, t, my) : nullptr;
+    if (!idle && (!alt || w == 0)) {
+#pragma unroll 1
+      for (int d = 0; d < D; d += 16) {
+        float o[16];
+#pragma unroll
+        for (int j = 0; j < 16; ++j) o[j] = 0.0f;
+        if (have) {                       // (the same for all lanes of the warp)
+          tmem_ld16(o_tm + d, o);
+          tmem_ld_wait(o);
+#pragma unroll
+          for (int j = 0; j < 16; ++j) o[j] *= g0;
+        }
+        if (have1) {
+#pragma unroll
+          for (int j = 0; j < 4; ++j) {
+            const float4 y = *reinterpret_cast<const float4*>(other_at(d / 4 + j));
+            o[4 * j] = fmaf(g1, y.x, o[4 * j]);
+            o[4 * j + 1] = fmaf(g1, y.y, o[4 * j + 1]);
+            o[4 * j + 2] = fmaf(g1, y.z, o[4 * j + 2]);
+            o[4 * j + 3] = fmaf(g1, y.w, o[4 * j + 3]);
+          }
+        }
+        if (!writes) continue;
+        if (split) {
+#pragma unroll
+          for (int j = 0; j < 4; ++j)
+            reinterpret_cast<float4*>(dst + static_cast<int64_t>(my) * D + d)[j] =
+                make_float4(o[4 * j], o[4 * j + 1], o[4 * j + 2], o[4 * j + 3]);
+        } else {
+          uint32_t u[8];
+#pragma unroll
+          for (int j = 0; j < 8; ++j) {
+            __nv_bfloat162 hh = __floats2bfloat162_rn(o[2 * j] * inv, o[2 * j + 1] * inv);
+            u[j] = *reinterpret_cast<uint32_t*>(&hh);
+          }
+          reinterpret_cast<uint4*>(orow + d)[0] = make_uint4(u[0], u[1], u[2], u[3]);
+          reinterpret_cast<uint4*>(orow + d)[1] = make_uint4(u[4], u[5], u[6], u[7]);
+        }
+      }
+    }
+    if (writes) {
+      if (split) {
+        dst[static_cast<int64_t>(p.part_rows) * D + my] = ref;
+        dst[static_cast<int64_t>(p.part_rows) * (D + 1) + my] = l;
+      } else if (p.lse != nullptr) {
+        *lse_at(p, t, my) = lse_of(ref, l);
+      }
+    }
+    if (split)
+      join_parts<D>(p, t, blockIdx.x, p.part_rows, parts.count, tid, 256, 1,
+                    &bars.flag);
+  } else if (warp < 12) {
+    regs_dec<S::kRegsOther>();
+    if (warp == 9 && n > 0) {
+      // ================================================================= MMA
+      const uint32_t idesc_s = make_idesc(kFP8 ? 0u : 1u, kRows, kKeys);
+      const uint32_t idesc_o = make_idesc(kFP8 ? 0u : 1u, kRows, D) | (1u << 16);
+      auto slot_at = [&](int f) { return sbase + S::oSlots + (f % S::kSlots) * S::kTileBytes; };
+      auto wait_full = [&](int f) {
+        const bool r = wait(bar(bars.full[f % S::kSlots]), (f / S::kSlots) & 1);
+        tc_fence_after();
+        return r;
+      };
+      auto release = [&](int f) {
+        if (lane == 0) umma_commit(bar(bars.empty[f % S::kSlots]));
+      };
+      auto scores = [&](int w, int f) {
+        if (lane == 0) {
+          const uint32_t a = smem_desc_lo(sbase + S::oQ + (alt ? 0 : w) * S::kTileBytes);
+          const uint32_t k = smem_desc_lo(slot_at(f));
+#pragma unroll
+          for (int s = 0; s < D / 16; ++s) {
+            const uint32_t off = ((s >> 2) * kHalfBytes + (s & 3) * 32) >> 4;
+            umma_lo<false>(tmem + w * kKeys, a + off, k + off, idesc_s, s > 0);
+          }
+          umma_commit(bar(bars.s_full[w]));
+        }
+        __syncwarp();
+      };
+      // the 16-key steps of tile i that hold keys
+      const int first_key = max(t.lo, k0);
+      auto values = [&](int w, int i, int f, bool first) {
+        if (lane == 0) {
+          const int kb = k0 + i * kKeys;
+          const int s0 = max(0, first_key - kb) / 16, s1 = min(8, (k1 - kb + 15) / 16);
+          const uint32_t v = mn_desc_lo(slot_at(f));
+          for (int s = s0; s < s1; ++s)
+            umma_ts(tmem + 256 + w * D, tmem + w * kKeys + s * 8, v + ((s * 2048u) >> 4), idesc_o,
+                    !(first && s == s0));
+        }
+        __syncwarp();
+      };
+      // (BF16) rows of V in those steps that no row sees
+      auto clean = [&](int i, int f) {
+        if constexpr (!kFP8) {
+          const int kb = k0 + i * kKeys;
+          const int lo = max(0, first_key - kb), hi = k1 - kb;
+          if ((lo & 15) != 0 || (hi < kKeys && (hi & 15) != 0)) {
+            auto zero = [&](int r0, int r1) {
+              for (int x = lane; x < (r1 - r0) * (D / 8); x += 32) {
+                const int r = r0 + x / (D / 8), c = x % (D / 8);
+                const uint32_t at = slot_at(f) + (c >> 3) * kHalfBytes + r * 128 + (c & 7) * 16;
+                asm volatile("st.shared.v4.u32 [%0], {%1, %1, %1, %1};" ::"r"(at), "r"(0)
+                             : "memory");
+              }
+            };
+            zero(lo & ~15, lo);
+            if (hi < kKeys) zero(hi, (hi + 15) & ~15);
+            fence_async_smem();
+            __syncwarp();
+          }
+        }
+      };
+      bool ok = wait(bar(bars.q_full), 0);
+      int f = 0, used[2] = {0, 0};         // tiles taken, weights taken of each group
+      if (ok) {
+        if (alt) {
+          for (int w = 0; w < 2 && w < n && ok; ++w) {
+            ok = wait_full(f);
+            if (!ok) break;
+            scores(w, f);
+            release(f++);
+          }
+        } else {
+          ok = wait_full(f);
+          if (ok) {
+            if (n_of[0] > 0) scores(0, f);
+            scores(1, f);
+            release(f++);
+          }
+        }
+      }
+      for (int i = 0; i < n && ok; ++i) {
+        const int fv = f++;
+        const bool more = i + lead < n;
+        const int fk = more ? f++ : -1;
+        bool have_v = false, have_k = false;
+        for (int w = alt ? (i & 1) : 0; w < 2; ++w) {
+          const int c = alt ? (i >> 1) : i;          // this group's tile
+          if (c < n_of[w]) {
+            ok = wait(bar(bars.p_full[w]), used[w] & 1);
+            if (!ok) break;
+            ++used[w];
+            if (!have_v) {
+              ok = wait_full(fv);
+              if (!ok) break;
+              clean(i, fv);
+              have_v = true;
+            }
+            tc_fence_after();
+            values(w, i, fv, c == 0);
+            if (alt || w == 1) release(fv);
+            if (c + 1 < n_of[w]) {
+              if (!have_k) {
+                ok = wait_full(fk);
+                if (!ok) break;
+                have_k = true;
+              }
+              scores(w, fk);
+            } else if (lane == 0) {
+              umma_commit(bar(bars.o_done[w]));
+            }
+            __syncwarp();
+          }
+          if (alt) break;
+        }
+        if (ok && more) release(fk);
+      }
+      if (!ok) {                           // products in flight end before the memory goes
+        if (lane == 0) umma_commit(bar(bars.drain));
+        __syncwarp();
+        mbar_wait_drain(bar(bars.drain), 0, p.timeout_ns);
+      }
+    } else if (!kFP8 && warp == 8 && n > 0) {
+      // ================================================================= TMA loads
+      if constexpr (!kFP8) {
+        const int box = min(1 << p.c.page_log2, kKeys);
+        const int segs = kKeys / box;
+        const uint64_t policy = p.row_tiles > 1 ? policy_evict_last() : policy_evict_first();
+        int f = 0;
+        bool ok = p.drop_producer == 0;
+        if (lane == 0) {
+          tma_prefetch_desc(&map_k);
+          tma_prefetch_desc(&map_v);
+        }
+        for (; f < 2 * n && ok; ++f) {
+          const Item it = item_at(f, n, lead);
+          const int kb = k0 + it.i * kKeys;
+          const int key = kb + lane * box;
+          const bool mine = lane < segs && key < k1;
+          int page = mine ? __ldg(table + (key >> p.c.page_log2)) : 0;
+          if (page < 0 || page >= p.c.num_pages) {
+            set_error(p.ctrl, MOE_ERR_DEVICE_FAULT, 22);
+            page = 0;                      // (a place that exists)
+          }
+          const int slot = f % S::kSlots;
+          ok = wait(bar(bars.empty[slot]), ((f / S::kSlots) & 1) ^ 1);
+          if (!ok) break;
+          const uint32_t full = bar(bars.full[slot]);
+          if (lane == 0) {
+            const int loaded = min(segs, (k1 - kb + box - 1) / box);
+            mbar_arrive_expect_tx(full, loaded * box * D * 2);
+          }
+          __syncwarp();
+          if (mine) {
+            const int row = ((page * p.c.heads + h) << p.c.page_log2) +
+                            (key & ((1 << p.c.page_log2) - 1));
+            const uint32_t dst = sbase + S::oSlots + slot * S::kTileBytes + lane * box * 128;
+#pragma unroll
+            for (int x = 0; x < D / 64; ++x)
+              tma_load_2d(dst + x * kHalfBytes, it.v ? &map_v : &map_k, full, x * 64, row, policy);
+          }
+          __syncwarp();
+        }
+        if (!ok) {                         // copies in flight land before the memory goes
+          for (int g = max(0, f - S::kSlots); g < f; ++g)
+            mbar_wait_drain(bar(bars.full[g % S::kSlots]), (g / S::kSlots) & 1, p.timeout_ns);
+        }
+      }
+    }
+  } else {
+    // =================================================================== FP8: codes to binary16
+    regs_dec<S::kRegsOther>();
+    if constexpr (kFP8) {
+      const int ct = tid - 384;
+      constexpr int kPieces = D / 16;            // 16-code pieces of a row
+      constexpr int kPer = kKeys * kPieces / 128; // pieces per thread
+      constexpr int kRowsPer = 128 / kPieces;    // rows per step of the group
+      const int c = ct % kPieces, r0 = ct / kPieces;
+      const uint32_t raw = sbase + S::oRaw, raw_sc = sbase + S::oRawScale;
+      const int page_mask = (1 << p.c.page_log2) - 1;
+      const int first_key = max(t.lo, k0);
+      // starts the copies of item f into this thread's own places of the raw ring
+      auto start = [&](int f) {
+        if (f < 2 * n) {
+          const Item it = item_at(f, n, lead);
+          const int kb = k0 + it.i * kKeys;
+          // lanes 0..7 hold the page of each 16 keys
+          const int pk = kb + (lane & 7) * 16;
+          int page = pk < k1 ? __ldg(table + (pk >> p.c.page_log2)) : 0;
+          if (page < 0 || page >= p.c.num_pages) {
+            set_error(p.ctrl, MOE_ERR_DEVICE_FAULT, 22);
+            page = 0;
+          }
+          const int slot = f % S::kRaw;
+          const uint8_t* src = it.v ? p.c.v : p.c.k;
+#pragma unroll
+          for (int i = 0; i < kPer; ++i) {
+            const int r = i * kRowsPer + r0;
+            const int pg = __shfl_sync(0xffffffffu, page, r >> 4);
+            const int key = kb + r;
+            const bool valid = key >= first_key && key < k1;
+            const int64_t at = (((static_cast<int64_t>(pg) * p.c.heads + h) << p.c.page_log2) +
+                                (valid ? key & page_mask : 0)) * D + c * 16;
+            const int bytes = valid ? 16 : 0;
+            asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(
+                             raw + slot * S::kRawBytes + (i * 128 + ct) * 16),
+                         "l"(src + at), "r"(bytes)
+                         : "memory");
+          }
+          if (!it.v) {
+            const int pg = __shfl_sync(0xffffffffu, page, ct >> 4);
+            const int key = kb + ct;
+            const bool valid = key >= first_key && key < k1;
+            const int64_t at = ((static_cast<int64_t>(pg) * p.c.heads + h) << p.c.page_log2) +
+                               (valid ? key & page_mask : 0);
+            const int bytes = valid ? 4 : 0;
+            const uint32_t d = raw_sc + slot * 1024 + ct * 4;
+            asm volatile("cp.async.ca.shared.global [%0], [%1], 4, %2;" ::"r"(d),
+                         "l"(p.c.k_scales + at), "r"(bytes)
+                         : "memory");
+            asm volatile("cp.async.ca.shared.global [%0], [%1], 4, %2;" ::"r"(d + 512),
+                         "l"(p.c.v_scales + at), "r"(bytes)
+                         : "memory");
+          }
+        }
+        asm volatile("cp.async.commit_group;" ::: "memory");
+      };
+      bool ok = p.drop_producer == 0;
+      if (ok) {
+        start(0);
+        start(1);
+      }
+      for (int f = 0; f < 2 * n && ok; ++f) {
+        start(f + 2);
+        asm volatile("cp.async.wait_group 2;" ::: "memory");
+        const Item it = item_at(f, n, lead);
+        const int rslot = f % S::kRaw, slot = f % S::kSlots, sslot = it.i % S::kScaleSlots;
+        float* sc = reinterpret_cast<float*>(smem + S::oScale + sslot * 1024);
+        if (!it.v) {
+          ok = wait(bar(bars.sc_empty[sslot]), ((it.i / S::kScaleSlots) & 1) ^ 1);
+          const float* rs = reinterpret_cast<const float*>(smem + S::oRawScale + rslot * 1024);
+          const float ks = rs[ct], vs = rs[128 + ct];
+          float top = vs;
+#pragma unroll
+          for (int o = 16; o > 0; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
+          if (lane == 0) bars.red[it.i & 1][warp & 3] = top;
+          if (ok) {
+            sc[ct] = ks;
+            sc[128 + ct] = vs;
+          }
+          named_bar_sync(2, 128);
+          top = fmaxf(fmaxf(bars.red[it.i & 1][0], bars.red[it.i & 1][1]),
+                      fmaxf(bars.red[it.i & 1][2], bars.red[it.i & 1][3]));
+          const int ex = min(max(static_cast<int>((__float_as_uint(top) >> 23) & 255u), 1), 253);
+          if (ct == 0 && ok) bars.e[sslot] = ex - 127;
+          if (ok) mbar_arrive(bar(bars.sc_full[sslot]));
+        }
+        if (ok) ok = wait(bar(bars.empty[slot]), ((f / S::kSlots) & 1) ^ 1);
+        if (ok) {
+          const uint32_t dst = sbase + S::oSlots + slot * S::kTileBytes;
+          const float mul =
+              it.v ? __uint_as_float(static_cast<uint32_t>(127 - bars.e[sslot]) << 23) : 0.0f;
+#pragma unroll
+          for (int i = 0; i < kPer; ++i) {
+            const int r = i * kRowsPer + r0;
+            uint4 x;
+            asm volatile("ld.shared.v4.u32 {%0, %1, %2, %3}, [%4];"
+                         : "=r"(x.x), "=r"(x.y), "=r"(x.z), "=r"(x.w)
+                         : "r"(raw + rslot * S::kRawBytes + (i * 128 + ct) * 16));
+            const uint32_t xw[4] = {x.x, x.y, x.z, x.w};
+            uint32_t o[8];
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+              o[2 * j] = e4m3x2_to_f16x2(static_cast<uint16_t>(xw[j]));
+              o[2 * j + 1] = e4m3x2_to_f16x2(static_cast<uint16_t>(xw[j] >> 16));
+            }
+            if (it.v) {
+              const __half2 g = __float2half2_rn(sc[128 + r] * mul);
+#pragma unroll
+              for (int j = 0; j < 8; ++j) {
+                __half2 y = __hmul2(*reinterpret_cast<__half2*>(&o[j]), g);
+                o[j] = *reinterpret_cast<uint32_t*>(&y);
+              }
+            }
+            // pieces 2c and 2c + 1 of the row's 16-byte pieces
+            const int p0 = 2 * c;
+            const uint32_t at = dst + (p0 >> 3) * kHalfBytes + r * 128;
+            const uint32_t a0 = at + (((p0 & 7) ^ (r & 7)) << 4);
+            const uint32_t a1 = at + ((((p0 & 7) + 1) ^ (r & 7)) << 4);
+            asm volatile("st.shared.v4.u32 [%0], {%1, %2, %3, %4};" ::"r"(a0), "r"(o[0]),
+                         "r"(o[1]), "r"(o[2]), "r"(o[3])
+                         : "memory");
+            asm volatile("st.shared.v4.u32 [%0], {%1, %2, %3, %4};" ::"r"(a1), "r"(o[4]),
+                         "r"(o[5]), "r"(o[6]), "r"(o[7])
+                         : "memory");
+          }
+          fence_async_smem();
+          mbar_arrive(bar(bars.full[slot]));
+        }
+        // the four warps agree, so that none is left waiting for the others
+        ok = !named_bar_any(2, 128, !ok);
+      }
+      asm volatile("cp.async.wait_all;" ::: "memory");
+    }
+  }
+  tc_fence_before();
+  __syncthreads();
+  if (warp == 9) tmem_dealloc(tmem, 512);
+}
+
+template <int D, bool kFP8>
+cudaError_t launch_t(const AttnParams& p, const CUtensorMap& mk, const CUtensorMap& mv,
+                     cudaStream_t stream) {
+  using S = TileShape<D, kFP8>;
+  cudaError_t e = cudaFuncSetAttribute(tiles_kernel<D, kFP8>,
+                                       cudaFuncAttributeMaxDynamicSharedMemorySize, S::kSmem);
+  if (e != cudaSuccess) return e;
+  const dim3 grid(static_cast<unsigned>(p.B) * p.c.heads * p.row_tiles, p.splits);
+  tiles_kernel<D, kFP8><<<grid, S::kThreads, S::kSmem, stream>>>(mk, mv, p);
+  return cudaGetLastError();
+}
+
+// The cache rows [rows, D] of bf16, in boxes of 64 channels x up to 128 positions.
+bool cache_map(CUtensorMap* m, const void* base, int D, uint64_t rows, uint32_t box_rows) {
+  auto fn = encode_fn();
+  if (fn == nullptr) return false;
+  cuuint64_t dims[2] = {static_cast<cuuint64_t>(D), rows};
+  cuuint64_t strides[1] = {static_cast<cuuint64_t>(D) * 2};
+  cuuint32_t box[2] = {64u, box_rows};
+  cuuint32_t estr[2] = {1, 1};
+  return fn(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, const_cast<void*>(base), dims, strides, box,
+            estr, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
+            CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+            CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+}  // namespace
+
+cudaError_t launch_attention_tiles(const AttnParams& p, int head_dim, bool fp8,
+                                   cudaStream_t stream) {
+  CUtensorMap mk, mv;
+  std::memset(&mk, 0, sizeof(mk));
+  std::memset(&mv, 0, sizeof(mv));
+  if (!fp8) {
+    const uint64_t rows = (static_cast<uint64_t>(p.c.num_pages) * p.c.heads) << p.c.page_log2;
+    const uint32_t box = 1u << p.c.page_log2 < 128u ? 1u << p.c.page_log2 : 128u;
+    if (!cache_map(&mk, p.c.k, head_dim, rows, box) || !cache_map(&mv, p.c.v, head_dim, rows, box))
+      return cudaErrorInvalidValue;
+    return head_dim == 128 ? launch_t<128, false>(p, mk, mv, stream)
+                           : launch_t<64, false>(p, mk, mv, stream);
+  }
+  return head_dim == 128 ? launch_t<128, true>(p, mk, mv, stream)
+                         : launch_t<64, true>(p, mk, mv, stream);
+}
+
+}  // namespace moe

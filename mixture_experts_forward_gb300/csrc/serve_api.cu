@@ -155,30 +155,38 @@ moe_status_t moe_paged_attention(const moe_attention_args* a, void* ws, size_t w
   p.timeout_ns = wait_limit_ns();
   p.drop_producer = loads_dropped() ? 1 : 0;
 
-  const int tile_rows = kDecodeRows;
+  // Few rows per cache head: 16-row tiles, bound by HBM.  More: 256-row tiles on
+  // the tensor cores.
+  const bool few = rows <= kDecodeRows;
+  const int tile_rows = few ? kDecodeRows : kTileRows;
   p.row_tiles = static_cast<int>((rows + tile_rows - 1) / tile_rows);
   const long long tiles = static_cast<long long>(a->B) * p.c.heads * p.row_tiles;
   if (tiles > 0x7fffffffll) return MOE_ERR_UNSUPPORTED;
+  p.part_rows = rows < tile_rows ? static_cast<int>((rows + 15) / 16 * 16) : tile_rows;
   // The keys a tile may see, by the caller's hint
   long long span = a->max_kv > 0 && a->max_kv < room ? a->max_kv : room;
-  if (a->window > 0 && a->window + rows / group + 32 < span) span = a->window + rows / group + 32;
+  if (a->window > 0 && a->window + tile_rows / group + 128 < span)
+    span = a->window + tile_rows / group + 128;
   // Parts of at least kMinChunk keys, until there are about kWaves of them for
   // every place an SM has for a CTA.
-  constexpr long long kMinChunk = 256, kWaves = 4;
-  long long chunk = span * tiles / (kWaves * 2 * sms);
-  if (chunk < kMinChunk) chunk = kMinChunk;
-  chunk = (chunk + 63) / 64 * 64;
+  const long long min_chunk = 256, waves = few ? 4 : 1, places = few ? 2 : 1;
+  long long chunk = span * tiles / (waves * places * sms);
+  if (chunk < min_chunk) chunk = min_chunk;
+  chunk = (chunk + 127) / 128 * 128;
   long long splits = (span + chunk - 1) / chunk;
-  const long long part_bytes = static_cast<long long>(tile_rows) * (D + 2) * 4;
-  const long long fit = static_cast<long long>((ws_bytes - MOE_ATTENTION_CTRL_BYTES) / part_bytes) / tiles;
+  const long long part_bytes = static_cast<long long>(p.part_rows) * (D + 2) * 4;
+  const long long fit =
+      static_cast<long long>((ws_bytes - MOE_ATTENTION_CTRL_BYTES) / part_bytes) / tiles;
   if (splits > fit) splits = fit;
   if (splits > 65535) splits = 65535;
   if (tiles > kMaxTiles || splits < 2) splits = 1;
   // (the last part takes whatever lies past splits * chunk)
-  if (splits > 1) chunk = ((span + splits - 1) / splits + 63) / 64 * 64;
+  if (splits > 1) chunk = ((span + splits - 1) / splits + 127) / 128 * 128;
   p.splits = static_cast<int>(splits);
   p.chunk = static_cast<int>(splits > 1 ? chunk : 0x40000000);
-  return cuda_status(launch_attention_decode(p, D, fp8, static_cast<cudaStream_t>(stream)));
+  const cudaStream_t st = static_cast<cudaStream_t>(stream);
+  return cuda_status(few ? launch_attention_decode(p, D, fp8, st)
+                         : launch_attention_tiles(p, D, fp8, st));
 }
 
 moe_status_t moe_verify_draft(const moe_verify_args* a, void* ws, void* stream) {

@@ -46,6 +46,7 @@ struct AttnParams {
   int window, causal;
   int row_tiles;                 // row tiles per (sequence, head)
   int splits, chunk;             // parts of the keys, keys per part
+  int part_rows;                 // rows that a part's result has room for
   unsigned* counters;            // one per (sequence, head, row tile); zero between calls
   float* partial;                // per (tile, part): rows x (head_dim sums, maximum, sum)
   Ctrl* ctrl;
@@ -63,6 +64,11 @@ cudaError_t launch_kv_read(const KvCacheView& c, int head_dim, bool fp8, const i
 constexpr int kDecodeRows = 16;
 cudaError_t launch_attention_decode(const AttnParams& p, int head_dim, bool fp8,
                                     cudaStream_t stream);
+// Up to 256 rows per tile, tcgen05.
+constexpr int kTileRows = 256;
+constexpr int kTileKeys = 128;
+cudaError_t launch_attention_tiles(const AttnParams& p, int head_dim, bool fp8,
+                                   cudaStream_t stream);
 cudaError_t launch_verify(const moe_verify_args& a, Ctrl* ctrl, int num_sms, cudaStream_t stream);
 
 }  // namespace moe
