@@ -283,13 +283,24 @@ def swiglu_quant(gu: torch.Tensor, stream=None):
 
 
 # ------------------------------------------------------------------ serving
-def _need(ok: bool, what: str, why: str):
-    if not ok:
-        raise MoeError(MOE_ERR_INVALID_ARG, f"{what}: {why}")
+# These calls sit in a serving loop where single tokens cost a few microseconds
+# on the device, so the binding itself is kept to plain attribute reads: no
+# stream object, no tuple comparisons, one structure per call.
+_U8, _BF16, _F32, _I32 = torch.uint8, torch.bfloat16, torch.float32, torch.int32
+_raw_stream_of = getattr(torch._C, "_cuda_getCurrentRawStream", None)
 
 
-def _dense(t, dtype) -> bool:
-    return t.dtype is dtype and t.is_contiguous()
+def _bad(what: str, why: str):
+    raise MoeError(MOE_ERR_INVALID_ARG, f"{what}: {why}")
+
+
+def _raw_stream(stream, t) -> int:
+    """The cudaStream_t of `stream`, or of the current stream of t's device."""
+    if stream is not None:
+        return stream.cuda_stream
+    if _raw_stream_of is not None and t.is_cuda:
+        return _raw_stream_of(t.get_device())
+    return torch.cuda.current_stream(t.device).cuda_stream
 
 
 def new_kv_cache(dtype, num_pages, page_size, heads, head_dim, device="cuda"):
@@ -308,25 +319,31 @@ def _cache(what, k, v, k_scales, v_scales) -> KvCache:
     """The cache of these page tensors: u8 codes [P, H, page, D] with f32 scales
     [P, H, page], or bf16 pages without scales."""
     P, H, page, D = k.shape
-    _need(v.shape == k.shape and k.is_contiguous() and v.is_contiguous() and v.dtype is k.dtype,
-          what, "k and v pages must be contiguous, of one shape and type")
-    if k.dtype is torch.uint8:
-        _need(k_scales is not None and v_scales is not None and
-              _dense(k_scales, torch.float32) and _dense(v_scales, torch.float32) and
-              k_scales.shape == k.shape[:3] and v_scales.shape == k.shape[:3],
-              what, "an FP8 cache needs f32 scales [pages, heads, page_size]")
-        return KvCache(DTYPE_FP8, P, page, H, D, k.data_ptr(), v.data_ptr(), k_scales.data_ptr(),
-                       v_scales.data_ptr())
-    _need(k.dtype is torch.bfloat16, what, "pages are uint8 (E4M3 codes) or bfloat16")
-    return KvCache(DTYPE_BF16, P, page, H, D, k.data_ptr(), v.data_ptr(), None, None)
+    if not (v.shape == k.shape and v.dtype is k.dtype and k.is_contiguous() and
+            v.is_contiguous()):
+        _bad(what, "k and v pages must be contiguous, of one shape and type")
+    if k.dtype is _BF16:
+        return KvCache(DTYPE_BF16, P, page, H, D, k.data_ptr(), v.data_ptr(), None, None)
+    if k.dtype is not _U8:
+        _bad(what, "pages are uint8 (E4M3 codes) or bfloat16")
+    rows = P * H * page
+    if (k_scales is None or v_scales is None or k_scales.dtype is not _F32 or
+            v_scales.dtype is not _F32 or k_scales.numel() != rows or v_scales.numel() != rows or
+            not k_scales.is_contiguous() or not v_scales.is_contiguous()):
+        _bad(what, "an FP8 cache needs f32 scales [pages, heads, page_size]")
+    return KvCache(DTYPE_FP8, P, page, H, D, k.data_ptr(), v.data_ptr(), k_scales.data_ptr(),
+                   v_scales.data_ptr())
+
+
+def _ints(t, n) -> bool:
+    return t.dtype is _I32 and t.numel() == n and t.is_contiguous()
 
 
 def _keep(stream, *tensors):
     """Results allocated on the current stream and written on another one."""
-    if stream is not None:
-        for t in tensors:
-            if t is not None:
-                t.record_stream(stream)
+    for t in tensors:
+        if t is not None:
+            t.record_stream(stream)
 
 
 def kv_write(k: torch.Tensor, v: torch.Tensor, slots: torch.Tensor, k_cache: torch.Tensor,
@@ -335,14 +352,18 @@ def kv_write(k: torch.Tensor, v: torch.Tensor, slots: torch.Tensor, k_cache: tor
     last dimension contiguous) into the slots s32 [T] of a paged cache."""
     what = "moe_kv_write"
     c = _cache(what, k_cache, v_cache, k_scales, v_scales)
-    T = k.shape[0]
-    _need(k.shape == (T, c.heads, c.head_dim) and v.shape == k.shape and
-          k.dtype is torch.bfloat16 and v.dtype is torch.bfloat16 and k.stride(2) == 1 and
-          v.stride(2) == 1, what, "k and v are bf16 [T, heads, head_dim] with contiguous rows")
-    _need(_dense(slots, torch.int32) and slots.numel() == T, what, "slots is int32 [T]")
-    _check(lib().moe_kv_write(c, k.data_ptr(), v.data_ptr(), T, k.stride(0), k.stride(1),
-                              v.stride(0), v.stride(1), slots.data_ptr(), ws.data_ptr(),
-                              _stream(stream)), what)
+    T, H, D = k.shape
+    kt, kh, kd = k.stride()
+    vt, vh, vd = v.stride()
+    if not (H == c.heads and D == c.head_dim and v.shape == k.shape and k.dtype is _BF16 and
+            v.dtype is _BF16 and kd == 1 and vd == 1):
+        _bad(what, "k and v are bf16 [T, heads, head_dim] with contiguous rows")
+    if not _ints(slots, T):
+        _bad(what, "slots is int32 [T]")
+    code = lib().moe_kv_write(c, k.data_ptr(), v.data_ptr(), T, kt, kh, vt, vh, slots.data_ptr(),
+                              ws.data_ptr(), _raw_stream(stream, k))
+    if code:
+        _check(code, what)
 
 
 def kv_read(k_cache: torch.Tensor, v_cache: torch.Tensor, block_table: torch.Tensor,
@@ -351,18 +372,21 @@ def kv_read(k_cache: torch.Tensor, v_cache: torch.Tensor, block_table: torch.Ten
     """moe_kv_read: (k, v) bf16 [rows, heads, head_dim]; rows = cu_rows[-1]."""
     what = "moe_kv_read"
     c = _cache(what, k_cache, v_cache, k_scales, v_scales)
-    B = cu_rows.numel() - 1
-    _need(_dense(block_table, torch.int32) and block_table.dim() == 2 and
-          block_table.shape[0] == B and _dense(cu_rows, torch.int32), what,
-          "block_table is int32 [B, entries], cu_rows int32 [B+1]")
-    _need(starts is None or (_dense(starts, torch.int32) and starts.numel() == B), what,
-          "starts is int32 [B]")
-    k = torch.empty(rows, c.heads, c.head_dim, dtype=torch.bfloat16, device=k_cache.device)
-    v = torch.empty_like(k)
-    _check(lib().moe_kv_read(c, block_table.data_ptr(), block_table.shape[1], cu_rows.data_ptr(),
+    B, entries = block_table.shape
+    if not (_ints(block_table, B * entries) and _ints(cu_rows, B + 1)):
+        _bad(what, "block_table is int32 [B, entries], cu_rows int32 [B+1]")
+    if not (starts is None or _ints(starts, B)):
+        _bad(what, "starts is int32 [B]")
+    shape = (rows, c.heads, c.head_dim)
+    k = torch.empty(shape, dtype=_BF16, device=k_cache.device)
+    v = torch.empty(shape, dtype=_BF16, device=k_cache.device)
+    code = lib().moe_kv_read(c, block_table.data_ptr(), entries, cu_rows.data_ptr(),
                              None if starts is None else starts.data_ptr(), B, rows, k.data_ptr(),
-                             v.data_ptr(), ws.data_ptr(), _stream(stream)), what)
-    _keep(stream, k, v)
+                             v.data_ptr(), ws.data_ptr(), _raw_stream(stream, k_cache))
+    if code:
+        _check(code, what)
+    if stream is not None:
+        _keep(stream, k, v)
     return k, v
 
 
@@ -377,29 +401,31 @@ def paged_attention(q: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.Tenso
     what = "moe_paged_attention"
     c = _cache(what, k_cache, v_cache, k_scales, v_scales)
     T, Hq, D = q.shape
-    B = kv_lens.numel()
-    _need(q.dtype is torch.bfloat16 and D == c.head_dim and q.stride(2) == 1, what,
-          "q is bf16 [T, q_heads, head_dim] with contiguous rows")
-    _need(_dense(block_table, torch.int32) and block_table.dim() == 2 and
-          block_table.shape[0] == B and _dense(cu_q, torch.int32) and cu_q.numel() == B + 1 and
-          _dense(kv_lens, torch.int32), what,
-          "block_table is int32 [B, entries], cu_q int32 [B+1], kv_lens int32 [B]")
+    qt, qh, qd = q.stride()
+    B, entries = block_table.shape
+    if not (q.dtype is _BF16 and D == c.head_dim and qd == 1):
+        _bad(what, "q is bf16 [T, q_heads, head_dim] with contiguous rows")
+    if not (_ints(block_table, B * entries) and _ints(cu_q, B + 1) and _ints(kv_lens, B)):
+        _bad(what, "block_table is int32 [B, entries], cu_q int32 [B+1], kv_lens int32 [B]")
+    sums = torch.empty((T, Hq), dtype=_F32, device=q.device) if lse else None
     if out is None:
-        out = torch.empty(T, Hq, D, dtype=torch.bfloat16, device=q.device)
-        _keep(stream, out)
+        out = torch.empty((T, Hq, D), dtype=_BF16, device=q.device)
+        ot, oh = Hq * D, D
+        if stream is not None:
+            _keep(stream, out)
     else:
-        _need(out.dtype is torch.bfloat16 and out.shape == q.shape and out.stride(2) == 1, what,
-              "out is bf16, shaped like q, with contiguous rows")
-    sums = None
-    if lse:
-        sums = torch.empty(T, Hq, dtype=torch.float32, device=q.device)
-        _keep(stream, sums)
-    a = AttentionArgs(c, B, T, Hq, max_q, max_kv, block_table.shape[1], q.data_ptr(), q.stride(0),
-                      q.stride(1), out.data_ptr(), out.stride(0), out.stride(1),
-                      None if sums is None else sums.data_ptr(), cu_q.data_ptr(),
+        ot, oh, od = out.stride()
+        if not (out.dtype is _BF16 and out.shape == q.shape and od == 1):
+            _bad(what, "out is bf16, shaped like q, with contiguous rows")
+    a = AttentionArgs(c, B, T, Hq, max_q, max_kv, entries, q.data_ptr(), qt, qh, out.data_ptr(),
+                      ot, oh, sums.data_ptr() if lse else None, cu_q.data_ptr(),
                       kv_lens.data_ptr(), block_table.data_ptr(), scale, softcap, window,
                       1 if causal else 0)
-    _check(lib().moe_paged_attention(a, ws.data_ptr(), ws.numel(), _stream(stream)), what)
+    code = lib().moe_paged_attention(a, ws.data_ptr(), ws.numel(), _raw_stream(stream, q))
+    if code:
+        _check(code, what)
+    if stream is not None:
+        _keep(stream, sums)
     return out, sums
 
 
@@ -409,25 +435,29 @@ def verify_draft(p: torch.Tensor, q: torch.Tensor, draft: torch.Tensor, u_accept
     probabilities p [B, n+1, V] and draft probabilities q [B, n, V] (f32 or bf16)."""
     what = "moe_verify_draft"
     B, n, V = q.shape
-    _need(p.shape == (B, n + 1, V) and p.dtype is q.dtype and
-          (p.dtype is torch.float32 or p.dtype is torch.bfloat16) and
-          (V == 1 or (p.stride(2) == 1 and q.stride(2) == 1)), what,
-          "p is [B, n+1, V] and q [B, n, V], f32 or bf16, with contiguous rows")
-    _need(_dense(draft, torch.int32) and draft.shape == (B, n) and
-          _dense(u_accept, torch.float32) and u_accept.shape == (B, n) and
-          _dense(u_sample, torch.float32) and u_sample.numel() == B, what,
-          "draft is int32 [B, n], u_accept f32 [B, n], u_sample f32 [B]")
-    _need(draft_lens is None or (_dense(draft_lens, torch.int32) and draft_lens.numel() == B),
-          what, "draft_lens is int32 [B]")
-    accepted = torch.empty(B, dtype=torch.int32, device=p.device)
-    tokens = torch.empty(B, n + 1, dtype=torch.int32, device=p.device)
-    a = VerifyArgs(DTYPE_F32 if p.dtype is torch.float32 else DTYPE_BF16, B, n, V, p.data_ptr(),
-                   p.stride(0), p.stride(1), q.data_ptr(), q.stride(0), q.stride(1),
-                   draft.data_ptr(), None if draft_lens is None else draft_lens.data_ptr(),
+    pb, pi, pv = p.stride()
+    qb, qi, qv = q.stride()
+    f32 = q.dtype is _F32
+    if not (p.shape == (B, n + 1, V) and p.dtype is q.dtype and (f32 or q.dtype is _BF16) and
+            (V == 1 or (pv == 1 and qv == 1))):
+        _bad(what, "p is [B, n+1, V] and q [B, n, V], f32 or bf16, with contiguous rows")
+    if not (_ints(draft, B * n) and u_accept.dtype is _F32 and u_accept.numel() == B * n and
+            u_accept.is_contiguous() and u_sample.dtype is _F32 and u_sample.numel() == B and
+            u_sample.is_contiguous()):
+        _bad(what, "draft is int32 [B, n], u_accept f32 [B, n], u_sample f32 [B]")
+    if not (draft_lens is None or _ints(draft_lens, B)):
+        _bad(what, "draft_lens is int32 [B]")
+    accepted = torch.empty(B, dtype=_I32, device=p.device)
+    tokens = torch.empty((B, n + 1), dtype=_I32, device=p.device)
+    a = VerifyArgs(DTYPE_F32 if f32 else DTYPE_BF16, B, n, V, p.data_ptr(), pb, pi, q.data_ptr(),
+                   qb, qi, draft.data_ptr(), None if draft_lens is None else draft_lens.data_ptr(),
                    u_accept.data_ptr(), u_sample.data_ptr(), accepted.data_ptr(),
                    tokens.data_ptr())
-    _check(lib().moe_verify_draft(a, ws.data_ptr(), _stream(stream)), what)
-    _keep(stream, accepted, tokens)
+    code = lib().moe_verify_draft(a, ws.data_ptr(), _raw_stream(stream, p))
+    if code:
+        _check(code, what)
+    if stream is not None:
+        _keep(stream, accepted, tokens)
     return accepted, tokens
 
 

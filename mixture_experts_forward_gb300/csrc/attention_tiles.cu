@@ -158,6 +158,14 @@ __device__ __forceinline__ bool named_bar_any(int id, int count, bool x) {
       : "memory");
   return r != 0;
 }
+// One lane of a converged warp, the same one each time.
+__device__ __forceinline__ bool elect_one() {
+  uint32_t r;
+  asm volatile(
+      "{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\tselp.u32 %0, 1, 0, p;\n\t}"
+      : "=r"(r));
+  return r != 0;
+}
 __device__ __forceinline__ void fence_async_smem() {
   asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
 }
@@ -200,6 +208,7 @@ struct Bars {
   int flag;
   int e[3];                       // FP8: exponent of each tile's value scales
   float red[2][4];
+  float other[2][kRows];          // group 1's references and sums, when it hands over
 };
 
 template <int D, bool kFP8>
@@ -296,7 +305,9 @@ __global__ void __launch_bounds__(TileShape<D, kFP8>::kThreads, 1)
       const int c = row % kPieces;
       const int rows_here = alt ? 64 : 128;
       const uint32_t flip = p.scale < 0.0f ? 0x80008000u : 0u;   // the scores' factor is positive
-      for (int r = row / kPieces; r < rows_here; r += kPerPass) {
+#pragma unroll 4
+      for (int pass = 0; pass < rows_here / kPerPass; ++pass) {
+        const int r = row / kPieces + pass * kPerPass;
         const int tr = alt ? w * 64 + r : r;         // row within its tile
         const int cr = alt ? tr : w * kRows + r;     // row of the CTA's rows
         uint4 x = make_uint4(0u, 0u, 0u, 0u);
@@ -477,7 +488,6 @@ __global__ void __launch_bounds__(TileShape<D, kFP8>::kThreads, 1)
     }
     if (m == ninf) ref = ninf;                       // the row saw no key
     float* other = reinterpret_cast<float*>(smem + S::oSlots);     // [128][D], pieces swizzled
-    float* other_ml = reinterpret_cast<float*>(smem + S::oQ);      // [2][128]
     constexpr int kOutPieces = D / 4;
     auto other_at = [&](int d4) { return other + row * D + ((d4 ^ (row & (kOutPieces - 1))) << 2); };
     if (alt) {
@@ -495,8 +505,8 @@ __global__ void __launch_bounds__(TileShape<D, kFP8>::kThreads, 1)
                               o[4 * j + 3] * unit);
           }
         }
-        other_ml[row] = ref;
-        other_ml[128 + row] = l;
+        bars.other[0][row] = ref;
+        bars.other[1][row] = l;
       }
       named_bar_sync(1, 256);
     }
@@ -504,7 +514,7 @@ __global__ void __launch_bounds__(TileShape<D, kFP8>::kThreads, 1)
     float g0 = unit, g1 = 0.0f;
     bool have1 = false;
     if (alt && w == 0) {
-      const float ref1 = other_ml[row], l1 = other_ml[128 + row];
+      const float ref1 = bars.other[0][row], l1 = bars.other[1][row];
       have1 = ref1 != ninf;
       if (have1) {
         const float top = fmaxf(ref, ref1);
@@ -575,53 +585,84 @@ __global__ void __launch_bounds__(TileShape<D, kFP8>::kThreads, 1)
     regs_dec<S::kRegsOther>();
     if (warp == 9 && n > 0) {
       // ================================================================= MMA
+      // Everything that an MMA takes is uniform over the warp and says so
+      // (shuffles, elect.sync): an issue is then a few instructions, where
+      // per-lane registers cost about a hundred cycles each.
       const uint32_t idesc_s = make_idesc(kFP8 ? 0u : 1u, kRows, kKeys);
       const uint32_t idesc_o = make_idesc(kFP8 ? 0u : 1u, kRows, D) | (1u << 16);
-      auto slot_at = [&](int f) { return sbase + S::oSlots + (f % S::kSlots) * S::kTileBytes; };
-      auto wait_full = [&](int f) {
-        const bool r = wait(bar(bars.full[f % S::kSlots]), (f / S::kSlots) & 1);
+      const uint32_t tm = __shfl_sync(0xffffffffu, tmem, 0);
+      const int tiles = __shfl_sync(0xffffffffu, n, 0);
+      const int tiles0 = __shfl_sync(0xffffffffu, n_of[0], 0);
+      const bool two = __shfl_sync(0xffffffffu, alt ? 1 : 0, 0) != 0;
+      const uint32_t q_lo = smem_desc_lo(sbase + S::oQ);
+      const uint32_t k_lo = smem_desc_lo(sbase + S::oSlots);
+      const uint32_t v_lo = mn_desc_lo(sbase + S::oSlots);
+      constexpr uint32_t kSlotStep = S::kTileBytes >> 4;
+      const int first_key = max(t.lo, k0);
+      const int first_step = max(0, first_key - k0) / 16;     // of the first tile
+      const int last_steps = (k1 - (k0 + (n - 1) * kKeys) + 15) / 16;   // of the last tile
+      struct Place {           // an item's slot and the parity of its waits
+        int slot;
+        uint32_t parity;
+      };
+      Place at_f = {0, 0};
+      auto next = [&]() {
+        const Place x = at_f;
+        if (++at_f.slot == S::kSlots) {
+          at_f.slot = 0;
+          at_f.parity ^= 1;
+        }
+        return x;
+      };
+      auto wait_full = [&](const Place& x) {
+        return wait(bar(bars.full[0]) + 8 * x.slot, x.parity);
+      };
+      auto release = [&](const Place& x) {
+        if (elect_one()) umma_commit(bar(bars.empty[0]) + 8 * x.slot);
+      };
+      // S = Q K^T of group w and the key tile in slot x
+      auto scores = [&](int w, const Place& x) {
+        const uint32_t q = q_lo + (two ? 0 : w) * kSlotStep;
+        const uint32_t k = k_lo + x.slot * kSlotStep;
         tc_fence_after();
-        return r;
-      };
-      auto release = [&](int f) {
-        if (lane == 0) umma_commit(bar(bars.empty[f % S::kSlots]));
-      };
-      auto scores = [&](int w, int f) {
-        if (lane == 0) {
-          const uint32_t a = smem_desc_lo(sbase + S::oQ + (alt ? 0 : w) * S::kTileBytes);
-          const uint32_t k = smem_desc_lo(slot_at(f));
+        if (elect_one()) {
 #pragma unroll
           for (int s = 0; s < D / 16; ++s) {
             const uint32_t off = ((s >> 2) * kHalfBytes + (s & 3) * 32) >> 4;
-            umma_lo<false>(tmem + w * kKeys, a + off, k + off, idesc_s, s > 0);
+            umma_lo<false>(tm + w * kKeys, q + off, k + off, idesc_s, s > 0);
           }
-          umma_commit(bar(bars.s_full[w]));
+          umma_commit(bar(bars.s_full[0]) + 8 * w);
         }
-        __syncwarp();
       };
-      // the 16-key steps of tile i that hold keys
-      const int first_key = max(t.lo, k0);
-      auto values = [&](int w, int i, int f, bool first) {
-        if (lane == 0) {
-          const int kb = k0 + i * kKeys;
-          const int s0 = max(0, first_key - kb) / 16, s1 = min(8, (k1 - kb + 15) / 16);
-          const uint32_t v = mn_desc_lo(slot_at(f));
+      // O += P V over the 16-key steps of tile i that hold keys
+      auto values = [&](int w, int i, const Place& x, bool first) {
+        const uint32_t v = v_lo + x.slot * kSlotStep;
+        const uint32_t d = tm + 256 + w * D, pw = tm + w * kKeys;
+        tc_fence_after();
+        if ((i > 0 || first_step == 0) && (i + 1 < tiles || last_steps == 8)) {
+          if (elect_one()) {
+#pragma unroll
+            for (int s = 0; s < 8; ++s)
+              umma_ts(d, pw + s * 8, v + s * (2048u >> 4), idesc_o, s > 0 ? 1u : (first ? 0u : 1u));
+          }
+        } else if (elect_one()) {
+          const int s0 = i == 0 ? first_step : 0, s1 = i + 1 == tiles ? last_steps : 8;
           for (int s = s0; s < s1; ++s)
-            umma_ts(tmem + 256 + w * D, tmem + w * kKeys + s * 8, v + ((s * 2048u) >> 4), idesc_o,
-                    !(first && s == s0));
+            umma_ts(d, pw + s * 8, v + s * (2048u >> 4), idesc_o, (first && s == s0) ? 0u : 1u);
         }
-        __syncwarp();
       };
       // (BF16) rows of V in those steps that no row sees
-      auto clean = [&](int i, int f) {
+      auto clean = [&](int i, const Place& x) {
         if constexpr (!kFP8) {
+          if (i > 0 && i + 1 < tiles) return;
           const int kb = k0 + i * kKeys;
           const int lo = max(0, first_key - kb), hi = k1 - kb;
           if ((lo & 15) != 0 || (hi < kKeys && (hi & 15) != 0)) {
+            const uint32_t base = sbase + S::oSlots + x.slot * S::kTileBytes;
             auto zero = [&](int r0, int r1) {
-              for (int x = lane; x < (r1 - r0) * (D / 8); x += 32) {
-                const int r = r0 + x / (D / 8), c = x % (D / 8);
-                const uint32_t at = slot_at(f) + (c >> 3) * kHalfBytes + r * 128 + (c & 7) * 16;
+              for (int y = lane; y < (r1 - r0) * (D / 8); y += 32) {
+                const int r = r0 + y / (D / 8), c = y % (D / 8);
+                const uint32_t at = base + (c >> 3) * kHalfBytes + r * 128 + (c & 7) * 16;
                 asm volatile("st.shared.v4.u32 [%0], {%1, %1, %1, %1};" ::"r"(at), "r"(0)
                              : "memory");
               }
@@ -634,62 +675,81 @@ __global__ void __launch_bounds__(TileShape<D, kFP8>::kThreads, 1)
         }
       };
       bool ok = wait(bar(bars.q_full), 0);
-      int f = 0, used[2] = {0, 0};         // tiles taken, weights taken of each group
-      if (ok) {
-        if (alt) {
-          for (int w = 0; w < 2 && w < n && ok; ++w) {
-            ok = wait_full(f);
+      uint32_t used0 = 0, used1 = 0;       // parity of each group's weights
+      if (two) {
+        for (int w = 0; w < 2 && w < tiles && ok; ++w) {
+          const Place x = next();
+          ok = wait_full(x);
+          if (!ok) break;
+          scores(w, x);
+          release(x);
+        }
+        for (int i = 0; i < tiles && ok; ++i) {
+          const int w = i & 1;
+          const Place v = next();
+          ok = wait_full(v) && wait(bar(bars.p_full[0]) + 8 * w, (i >> 1) & 1);
+          if (!ok) break;
+          clean(i, v);
+          values(w, i, v, i < 2);
+          release(v);
+          if (i + 2 < tiles) {
+            const Place k = next();
+            ok = wait_full(k);
             if (!ok) break;
-            scores(w, f);
-            release(f++);
-          }
-        } else {
-          ok = wait_full(f);
-          if (ok) {
-            if (n_of[0] > 0) scores(0, f);
-            scores(1, f);
-            release(f++);
+            scores(w, k);
+            release(k);
+          } else if (elect_one()) {
+            umma_commit(bar(bars.o_done[0]) + 8 * w);
           }
         }
-      }
-      for (int i = 0; i < n && ok; ++i) {
-        const int fv = f++;
-        const bool more = i + lead < n;
-        const int fk = more ? f++ : -1;
-        bool have_v = false, have_k = false;
-        for (int w = alt ? (i & 1) : 0; w < 2; ++w) {
-          const int c = alt ? (i >> 1) : i;          // this group's tile
-          if (c < n_of[w]) {
-            ok = wait(bar(bars.p_full[w]), used[w] & 1);
+      } else if (ok) {
+        const Place x = next();
+        ok = wait_full(x);
+        if (ok) {
+          if (tiles0 > 0) scores(0, x);
+          scores(1, x);
+          release(x);
+        }
+        for (int i = 0; i < tiles && ok; ++i) {
+          const Place v = next();
+          ok = wait_full(v);
+          if (!ok) break;
+          clean(i, v);
+          const bool more = i + 1 < tiles;
+          Place k = {0, 0};
+          if (more) k = next();
+          bool have_k = false;
+          if (i < tiles0) {
+            ok = wait(bar(bars.p_full[0]), used0);
             if (!ok) break;
-            ++used[w];
-            if (!have_v) {
-              ok = wait_full(fv);
+            used0 ^= 1;
+            values(0, i, v, i == 0);
+            if (i + 1 < tiles0) {
+              ok = wait_full(k);
               if (!ok) break;
-              clean(i, fv);
-              have_v = true;
+              have_k = true;
+              scores(0, k);
+            } else if (elect_one()) {
+              umma_commit(bar(bars.o_done[0]));
             }
-            tc_fence_after();
-            values(w, i, fv, c == 0);
-            if (alt || w == 1) release(fv);
-            if (c + 1 < n_of[w]) {
-              if (!have_k) {
-                ok = wait_full(fk);
-                if (!ok) break;
-                have_k = true;
-              }
-              scores(w, fk);
-            } else if (lane == 0) {
-              umma_commit(bar(bars.o_done[w]));
-            }
-            __syncwarp();
           }
-          if (alt) break;
+          ok = wait(bar(bars.p_full[1]), used1);
+          if (!ok) break;
+          used1 ^= 1;
+          values(1, i, v, i == 0);
+          release(v);
+          if (more) {
+            ok = have_k || wait_full(k);
+            if (!ok) break;
+            scores(1, k);
+            release(k);
+          } else if (elect_one()) {
+            umma_commit(bar(bars.o_done[1]));
+          }
         }
-        if (ok && more) release(fk);
       }
       if (!ok) {                           // products in flight end before the memory goes
-        if (lane == 0) umma_commit(bar(bars.drain));
+        if (elect_one()) umma_commit(bar(bars.drain));
         __syncwarp();
         mbar_wait_drain(bar(bars.drain), 0, p.timeout_ns);
       }

@@ -167,13 +167,11 @@ moe_status_t moe_paged_attention(const moe_attention_args* a, void* ws, size_t w
   long long span = a->max_kv > 0 && a->max_kv < room ? a->max_kv : room;
   if (a->window > 0 && a->window + tile_rows / group + 128 < span)
     span = a->window + tile_rows / group + 128;
-  // Parts of at least kMinChunk keys, until there are about kWaves of them for
-  // every place an SM has for a CTA.
-  const long long min_chunk = 256, waves = few ? 4 : 1, places = few ? 2 : 1;
-  long long chunk = span * tiles / (waves * places * sms);
-  if (chunk < min_chunk) chunk = min_chunk;
-  chunk = (chunk + 127) / 128 * 128;
-  long long splits = (span + chunk - 1) / chunk;
+  // Parts of at least 256 keys.  Few rows: until there are about four for every
+  // place that an SM has for a CTA.  Many rows: as many as fit the SMs at once.
+  const long long most = (span + 255) / 256;
+  long long splits = few ? 8ll * sms / tiles : sms / tiles;
+  if (splits > most) splits = most;
   const long long part_bytes = static_cast<long long>(p.part_rows) * (D + 2) * 4;
   const long long fit =
       static_cast<long long>((ws_bytes - MOE_ATTENTION_CTRL_BYTES) / part_bytes) / tiles;
@@ -181,9 +179,9 @@ moe_status_t moe_paged_attention(const moe_attention_args* a, void* ws, size_t w
   if (splits > 65535) splits = 65535;
   if (tiles > kMaxTiles || splits < 2) splits = 1;
   // (the last part takes whatever lies past splits * chunk)
-  if (splits > 1) chunk = ((span + splits - 1) / splits + 127) / 128 * 128;
   p.splits = static_cast<int>(splits);
-  p.chunk = static_cast<int>(splits > 1 ? chunk : 0x40000000);
+  p.chunk = splits > 1 ? static_cast<int>(((span + splits - 1) / splits + 127) / 128 * 128)
+                       : 0x40000000;
   const cudaStream_t st = static_cast<cudaStream_t>(stream);
   return cuda_status(few ? launch_attention_decode(p, D, fp8, st)
                          : launch_attention_tiles(p, D, fp8, st));
