@@ -13,13 +13,19 @@
 // other.  Roles:
 //   warps 0-3, 4-7   softmax of row tile 0, 1: a thread owns a row (a lane of
 //                    tensor memory), so maxima and sums need no shuffles;
-//   warp 8           (BF16) TMA loads of K and V pages into a ring of tiles;
+//   warp 8           TMA loads of K and V pages into rings of tiles;
 //   warp 9           issues the MMAs;
-//   warps 12-15      (FP8) copy codes by cp.async into a ring of their own and turn
-//                    them into binary16 tiles: K's codes exactly (their
-//                    scale multiplies the score in binary32), V's times vs * 2^-e, 2^e
-//                    the tile's largest value scale, which keeps them in range
-//                    with 2^-11 of relative rounding; 2^e goes into the softmax.
+//   warps 12-15      (FP8) turn V's codes into binary16 tiles.
+// E4M3 caches: K's codes go to the tensor core as they are (kind::f8f6f4), against
+// the query as the sum of two E4M3 terms (hi = E4M3(q), lo = E4M3(q - hi), after a
+// power of two per row: exact for elements within 2^-10 of the row's largest, to
+// 2^-18 of it below), so a score costs what a 16-bit one does and K is never
+// rewritten; its scale multiplies the score in binary32.  V's codes become
+// code * (vs * 2^-e) in binary16, 2^e the tile's largest value scale, which
+// keeps them in range with 2^-11 of relative rounding; 2^e goes into the
+// softmax.  (Splitting the weights in two E4M3 terms instead would spare V's
+// conversion, but takes four more conversions per pair of weights, and those run
+// at 32 lanes a cycle: 983 cycles per row tile against 230 for V's codes.)
 // O is rescaled only when a row's maximum grew by more than 2^8 since its
 // reference (the weights then stay below 2^8, far inside their types), which
 // leaves the rescale to a few tiles per row; the softmax threads do it themselves
@@ -33,6 +39,7 @@
 #include <cstring>
 
 #include "attention_common.cuh"
+#include "quant_common.cuh"
 
 namespace moe {
 namespace {
@@ -43,27 +50,40 @@ constexpr uint32_t kHalfBytes = kKeys * 128;   // 64 channels of 128 rows
 
 template <int D, bool kFP8>
 struct TileShape {
-  static constexpr int kTileBytes = kKeys * D * 2;          // Q, K or V tile
-  static constexpr int kSlots = kFP8 ? (D == 128 ? 3 : 6) : (D == 128 ? 5 : 8);
-  static constexpr int kRaw = kFP8 ? 3 : 0;                 // tiles of codes in flight
-  static constexpr int kRawBytes = kKeys * D;
+  static constexpr int kTileBytes = kKeys * D * 2;          // a tile of 16-bit elements
+  static constexpr int kCodeBytes = kKeys * D;              // a tile of codes
+  // BF16: one ring of K and V tiles.  FP8: a ring of V tiles in binary16, one of K's
+  // codes, one of V's codes.
+  static constexpr int kSlots = kFP8 ? (D == 128 ? 2 : 3) : (D == 128 ? 5 : 8);
+  static constexpr int kKSlots = kFP8 ? (D == 128 ? 3 : 4) : 0;
+  static constexpr int kRawSlots = kFP8 ? (D == 128 ? 2 : 4) : 0;
   static constexpr int kScaleSlots = 3;
   static constexpr int kThreads = kFP8 ? 512 : 384;
-  // offsets in shared memory
+  // offsets in shared memory.  Q: two row tiles (FP8: each as two tiles of codes)
   static constexpr int oQ = 0;
   static constexpr int oSlots = 2 * kTileBytes;
-  static constexpr int oRaw = oSlots + kSlots * kTileBytes;
-  static constexpr int oRawScale = oRaw + kRaw * kRawBytes;            // [raw][2][128] f32
-  static constexpr int oScale = oRawScale + (kFP8 ? kRaw * 1024 : 0);  // [slot][ks 128 | vs 128]
+  static constexpr int oK = oSlots + kSlots * kTileBytes;
+  static constexpr int oRaw = oK + kKSlots * kCodeBytes;
+  static constexpr int oScale = oRaw + kRawSlots * kCodeBytes;         // [slot][ks 128 | vs 128]
   static constexpr int oRowf = oScale + (kFP8 ? kScaleSlots * 1024 : 0);
-  static constexpr int oEnd = oRowf + (kFP8 ? 1024 : 0);
-  static constexpr int kSmem = oEnd;
+  static constexpr int kSmem = oRowf + (kFP8 ? 1024 : 0);
   // setmaxnreg shares: softmax, the rest (BF16: 384 x 168 registers at launch, 2 x 128 x 208 +
   // 128 x 80 = 63488 of 64512; FP8: 512 x 128, 2 x 128 x 192 + 2 x 128 x 64 = 65536)
   static constexpr int kRegsSoftmax = kFP8 ? 192 : 208;
   static constexpr int kRegsOther = kFP8 ? 64 : 80;
   static_assert(kSlots * kTileBytes >= kRows * D * 4, "the join of two groups fits the ring");
 };
+
+// The 16-byte piece c of row r of a tile of codes (rows of D bytes, the
+// swizzle of that width).
+template <int D>
+__device__ __forceinline__ uint32_t code_piece(int r, int c) {
+  return r * D + ((c ^ (D == 128 ? (r & 7) : ((r >> 1) & 3))) << 4);
+}
+// High descriptor word of a K-major tile of codes: 8-row groups of 8 * D bytes,
+// 128- or 64-byte swizzle.
+template <int D>
+constexpr uint32_t kCodeDescHi = ((8u * D) >> 4) | (1u << 14) | ((D == 128 ? 2u : 4u) << 29);
 
 __device__ __forceinline__ void tmem_ld32(uint32_t taddr, float* v) {
   uint32_t r[32];
@@ -139,6 +159,18 @@ __device__ __forceinline__ void add2(float& d0, float& d1, float a0, float a1) {
       : "f"(a0), "f"(a1));
 }
 
+// D[tmem] (+)= A[smem] * B[smem]^T over 32 E4M3 elements, K-major tiles of codes.
+template <int D>
+__device__ __forceinline__ void umma_codes(uint32_t d_tmem, uint32_t a_lo, uint32_t b_lo,
+                                           uint32_t idesc, uint32_t accumulate) {
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t.reg .b64 ad, bd;\n\tsetp.ne.b32 p, %4, 0;\n\t"
+      "mov.b64 ad, {%1, %5};\n\tmov.b64 bd, {%2, %5};\n\t"
+      "tcgen05.mma.cta_group::1.kind::f8f6f4 [%0], ad, bd, %3, p;\n\t}" ::"r"(d_tmem),
+      "r"(a_lo), "r"(b_lo), "r"(idesc), "r"(accumulate), "r"(kCodeDescHi<D>)
+      : "memory");
+}
+
 template <int N>
 __device__ __forceinline__ void regs_inc() {
   asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(N));
@@ -198,7 +230,9 @@ __device__ __forceinline__ Item item_at(int f, int n, int lead) {
 }
 
 struct Bars {
-  uint64_t full[8], empty[8];     // the ring of tiles
+  uint64_t full[8], empty[8];     // the ring of tiles (FP8: of V)
+  uint64_t k_full[4], k_empty[4]; // FP8: K's codes
+  uint64_t raw_full[4], raw_empty[4];   // FP8: V's codes
   uint64_t q_full;
   uint64_t s_full[2], p_full[2], o_done[2];
   uint64_t sc_full[3], sc_empty[3];
@@ -250,6 +284,14 @@ __global__ void __launch_bounds__(TileShape<D, kFP8>::kThreads, 1)
     for (int i = 0; i < S::kSlots; ++i) {
       mbar_init(bar(bars.full[i]), kFP8 ? 128 : 1);
       mbar_init(bar(bars.empty[i]), 1);
+    }
+    for (int i = 0; i < S::kKSlots; ++i) {
+      mbar_init(bar(bars.k_full[i]), 1);
+      mbar_init(bar(bars.k_empty[i]), 1);
+    }
+    for (int i = 0; i < S::kRawSlots; ++i) {
+      mbar_init(bar(bars.raw_full[i]), 1);
+      mbar_init(bar(bars.raw_empty[i]), 128);
     }
     mbar_init(bar(bars.q_full), 256);
     for (int w = 0; w < 2; ++w) {
@@ -332,17 +374,34 @@ __global__ void __launch_bounds__(TileShape<D, kFP8>::kThreads, 1)
           for (int o = 1; o < kPieces; o <<= 1) a = fmaxf(a, __shfl_xor_sync(0xffffffffu, a, o));
           float mul, inv;
           row_pow2(a, mul, inv);
+          mul *= 0.5f;                   // below 2^8: an E4M3 ends at 448
+          if (c == 0) reinterpret_cast<float*>(smem + S::oRowf)[cr] = 2.0f * inv;
+          uint32_t hi[2], lo[2];
 #pragma unroll
-          for (int i = 0; i < 4; ++i) {
-            __half2 hh = __floats2half2_rn(__uint_as_float(xw[i] << 16) * mul,
-                                           __uint_as_float(xw[i] & 0xffff0000u) * mul);
-            xw[i] = *reinterpret_cast<uint32_t*>(&hh);
+          for (int i = 0; i < 2; ++i) {
+            uint32_t hw = 0, lw = 0;
+#pragma unroll
+            for (int j = 0; j < 2; ++j) {
+              const float x0 = __uint_as_float(xw[2 * i + j] << 16) * mul;
+              const float x1 = __uint_as_float(xw[2 * i + j] & 0xffff0000u) * mul;
+              const uint16_t hc = cvt_e4m3x2(x0, x1);
+              const float2 f = e4m3x2_to_f32(hc);
+              const uint16_t lc = cvt_e4m3x2(x0 - f.x, x1 - f.y);
+              hw |= static_cast<uint32_t>(hc) << (16 * j);
+              lw |= static_cast<uint32_t>(lc) << (16 * j);
+            }
+            hi[i] = hw;
+            lo[i] = lw;
           }
-          if (c == 0) reinterpret_cast<float*>(smem + S::oRowf)[cr] = inv;
+          uint8_t* at = smem + S::oQ + (alt ? 0 : w) * S::kTileBytes +
+                        code_piece<D>(tr, c >> 1) + (c & 1) * 8;
+          *reinterpret_cast<uint2*>(at) = make_uint2(hi[0], hi[1]);
+          *reinterpret_cast<uint2*>(at + S::kCodeBytes) = make_uint2(lo[0], lo[1]);
+        } else {
+          uint8_t* at = smem + S::oQ + (alt ? 0 : w) * S::kTileBytes + (c >> 3) * kHalfBytes +
+                        tr * 128 + (((c & 7) ^ (tr & 7)) << 4);
+          *reinterpret_cast<uint4*>(at) = x;
         }
-        uint8_t* at = smem + S::oQ + (alt ? 0 : w) * S::kTileBytes + (c >> 3) * kHalfBytes +
-                      tr * 128 + (((c & 7) ^ (tr & 7)) << 4);
-        *reinterpret_cast<uint4*>(at) = x;
       }
       fence_async_smem();
       mbar_arrive(bar(bars.q_full));
@@ -588,6 +647,7 @@ __global__ void __launch_bounds__(TileShape<D, kFP8>::kThreads, 1)
       // Everything that an MMA takes is uniform over the warp and says so
       // (shuffles, elect.sync): an issue is then a few instructions, where
       // per-lane registers cost about a hundred cycles each.
+      // (formats: E4M3 and binary16 are 0, bf16 is 1)
       const uint32_t idesc_s = make_idesc(kFP8 ? 0u : 1u, kRows, kKeys);
       const uint32_t idesc_o = make_idesc(kFP8 ? 0u : 1u, kRows, D) | (1u << 16);
       const uint32_t tm = __shfl_sync(0xffffffffu, tmem, 0);
@@ -595,48 +655,63 @@ __global__ void __launch_bounds__(TileShape<D, kFP8>::kThreads, 1)
       const int tiles0 = __shfl_sync(0xffffffffu, n_of[0], 0);
       const bool two = __shfl_sync(0xffffffffu, alt ? 1 : 0, 0) != 0;
       const uint32_t q_lo = smem_desc_lo(sbase + S::oQ);
-      const uint32_t k_lo = smem_desc_lo(sbase + S::oSlots);
+      const uint32_t k_lo = smem_desc_lo(sbase + (kFP8 ? S::oK : S::oSlots));
       const uint32_t v_lo = mn_desc_lo(sbase + S::oSlots);
-      constexpr uint32_t kSlotStep = S::kTileBytes >> 4;
       const int first_key = max(t.lo, k0);
       const int first_step = max(0, first_key - k0) / 16;     // of the first tile
       const int last_steps = (k1 - (k0 + (n - 1) * kKeys) + 15) / 16;   // of the last tile
-      struct Place {           // an item's slot and the parity of its waits
+      struct Place {           // a tile's slot and the parity of its waits
         int slot;
         uint32_t parity;
       };
-      Place at_f = {0, 0};
-      auto next = [&]() {
-        const Place x = at_f;
-        if (++at_f.slot == S::kSlots) {
-          at_f.slot = 0;
-          at_f.parity ^= 1;
+      Place at_v = {0, 0}, at_k = {0, 0};
+      auto step = [](Place& at, int slots) {
+        const Place x = at;
+        if (++at.slot == slots) {
+          at.slot = 0;
+          at.parity ^= 1;
         }
         return x;
       };
-      auto wait_full = [&](const Place& x) {
-        return wait(bar(bars.full[0]) + 8 * x.slot, x.parity);
+      auto next_v = [&]() { return step(at_v, S::kSlots); };
+      auto next_k = [&]() { return kFP8 ? step(at_k, S::kKSlots) : step(at_v, S::kSlots); };
+      auto wait_v = [&](const Place& x) { return wait(bar(bars.full[0]) + 8 * x.slot, x.parity); };
+      auto wait_k = [&](const Place& x) {
+        return wait((kFP8 ? bar(bars.k_full[0]) : bar(bars.full[0])) + 8 * x.slot, x.parity);
       };
-      auto release = [&](const Place& x) {
+      auto release_v = [&](const Place& x) {
         if (elect_one()) umma_commit(bar(bars.empty[0]) + 8 * x.slot);
+      };
+      auto release_k = [&](const Place& x) {
+        if (elect_one())
+          umma_commit((kFP8 ? bar(bars.k_empty[0]) : bar(bars.empty[0])) + 8 * x.slot);
       };
       // S = Q K^T of group w and the key tile in slot x
       auto scores = [&](int w, const Place& x) {
-        const uint32_t q = q_lo + (two ? 0 : w) * kSlotStep;
-        const uint32_t k = k_lo + x.slot * kSlotStep;
+        const uint32_t q = q_lo + (two ? 0 : w) * (S::kTileBytes >> 4);
+        const uint32_t k = k_lo + x.slot * ((kFP8 ? S::kCodeBytes : S::kTileBytes) >> 4);
         tc_fence_after();
         if (elect_one()) {
+          if constexpr (kFP8) {
 #pragma unroll
-          for (int s = 0; s < D / 16; ++s) {
-            const uint32_t off = ((s >> 2) * kHalfBytes + (s & 3) * 32) >> 4;
-            umma_lo<false>(tm + w * kKeys, q + off, k + off, idesc_s, s > 0);
+            for (int s = 0; s < 2 * (D / 32); ++s) {     // hi, then lo
+              const uint32_t off = ((s % (D / 32)) * 32) >> 4;
+              umma_codes<D>(tm + w * kKeys, q + (s / (D / 32)) * (S::kCodeBytes >> 4) + off,
+                            k + off, idesc_s, s > 0);
+            }
+          } else {
+#pragma unroll
+            for (int s = 0; s < D / 16; ++s) {
+              const uint32_t off = ((s >> 2) * kHalfBytes + (s & 3) * 32) >> 4;
+              umma_lo<false>(tm + w * kKeys, q + off, k + off, idesc_s, s > 0);
+            }
           }
           umma_commit(bar(bars.s_full[0]) + 8 * w);
         }
       };
       // O += P V over the 16-key steps of tile i that hold keys
       auto values = [&](int w, int i, const Place& x, bool first) {
-        const uint32_t v = v_lo + x.slot * kSlotStep;
+        const uint32_t v = v_lo + x.slot * (S::kTileBytes >> 4);
         const uint32_t d = tm + 256 + w * D, pw = tm + w * kKeys;
         tc_fence_after();
         if ((i > 0 || first_step == 0) && (i + 1 < tiles || last_steps == 8)) {
@@ -678,46 +753,46 @@ __global__ void __launch_bounds__(TileShape<D, kFP8>::kThreads, 1)
       uint32_t used0 = 0, used1 = 0;       // parity of each group's weights
       if (two) {
         for (int w = 0; w < 2 && w < tiles && ok; ++w) {
-          const Place x = next();
-          ok = wait_full(x);
+          const Place x = next_k();
+          ok = wait_k(x);
           if (!ok) break;
           scores(w, x);
-          release(x);
+          release_k(x);
         }
         for (int i = 0; i < tiles && ok; ++i) {
           const int w = i & 1;
-          const Place v = next();
-          ok = wait_full(v) && wait(bar(bars.p_full[0]) + 8 * w, (i >> 1) & 1);
+          const Place v = next_v();
+          ok = wait_v(v) && wait(bar(bars.p_full[0]) + 8 * w, (i >> 1) & 1);
           if (!ok) break;
           clean(i, v);
           values(w, i, v, i < 2);
-          release(v);
+          release_v(v);
           if (i + 2 < tiles) {
-            const Place k = next();
-            ok = wait_full(k);
+            const Place k = next_k();
+            ok = wait_k(k);
             if (!ok) break;
             scores(w, k);
-            release(k);
+            release_k(k);
           } else if (elect_one()) {
             umma_commit(bar(bars.o_done[0]) + 8 * w);
           }
         }
       } else if (ok) {
-        const Place x = next();
-        ok = wait_full(x);
+        const Place x = next_k();
+        ok = wait_k(x);
         if (ok) {
           if (tiles0 > 0) scores(0, x);
           scores(1, x);
-          release(x);
+          release_k(x);
         }
         for (int i = 0; i < tiles && ok; ++i) {
-          const Place v = next();
-          ok = wait_full(v);
+          const Place v = next_v();
+          ok = wait_v(v);
           if (!ok) break;
           clean(i, v);
           const bool more = i + 1 < tiles;
           Place k = {0, 0};
-          if (more) k = next();
+          if (more) k = next_k();
           bool have_k = false;
           if (i < tiles0) {
             ok = wait(bar(bars.p_full[0]), used0);
@@ -725,7 +800,7 @@ __global__ void __launch_bounds__(TileShape<D, kFP8>::kThreads, 1)
             used0 ^= 1;
             values(0, i, v, i == 0);
             if (i + 1 < tiles0) {
-              ok = wait_full(k);
+              ok = wait_k(k);
               if (!ok) break;
               have_k = true;
               scores(0, k);
@@ -737,12 +812,12 @@ __global__ void __launch_bounds__(TileShape<D, kFP8>::kThreads, 1)
           if (!ok) break;
           used1 ^= 1;
           values(1, i, v, i == 0);
-          release(v);
+          release_v(v);
           if (more) {
-            ok = have_k || wait_full(k);
+            ok = have_k || wait_k(k);
             if (!ok) break;
             scores(1, k);
-            release(k);
+            release_k(k);
           } else if (elect_one()) {
             umma_commit(bar(bars.o_done[1]));
           }
@@ -753,187 +828,196 @@ __global__ void __launch_bounds__(TileShape<D, kFP8>::kThreads, 1)
         __syncwarp();
         mbar_wait_drain(bar(bars.drain), 0, p.timeout_ns);
       }
-    } else if (!kFP8 && warp == 8 && n > 0) {
+    } else if (warp == 8 && n > 0) {
       // ================================================================= TMA loads
-      if constexpr (!kFP8) {
-        const int box = min(1 << p.c.page_log2, kKeys);
-        const int segs = kKeys / box;
-        const uint64_t policy = p.row_tiles > 1 ? policy_evict_last() : policy_evict_first();
-        int f = 0;
-        bool ok = p.drop_producer == 0;
-        if (lane == 0) {
-          tma_prefetch_desc(&map_k);
-          tma_prefetch_desc(&map_v);
+      const int box = min(1 << p.c.page_log2, kKeys);
+      const int segs = kKeys / box;
+      const uint64_t policy = p.row_tiles > 1 ? policy_evict_last() : policy_evict_first();
+      constexpr int kRowBytes = kFP8 ? D : 2 * D;
+      bool ok = p.drop_producer == 0;
+      if (lane == 0) {
+        tma_prefetch_desc(&map_k);
+        tma_prefetch_desc(&map_v);
+      }
+      // a ring: its slots, its barriers, how many tiles it was given
+      struct Ring {
+        uint32_t full, empty, base;
+        int slots, bytes, f;
+      };
+      Ring rv, rk;
+      if constexpr (kFP8) {
+        rv = {bar(bars.raw_full[0]), bar(bars.raw_empty[0]), sbase + S::oRaw, S::kRawSlots,
+              S::kCodeBytes, 0};
+        rk = {bar(bars.k_full[0]), bar(bars.k_empty[0]), sbase + S::oK, S::kKSlots,
+              S::kCodeBytes, 0};
+      } else {
+        rv = {bar(bars.full[0]), bar(bars.empty[0]), sbase + S::oSlots, S::kSlots, S::kTileBytes,
+              0};
+        rk = rv;
+      }
+      auto load = [&](Ring& r, bool v, int i) {
+        const int kb = k0 + i * kKeys;
+        const int key = kb + lane * box;
+        const bool mine = lane < segs && key < k1;
+        int page = mine ? __ldg(table + (key >> p.c.page_log2)) : 0;
+        if (page < 0 || page >= p.c.num_pages) {
+          set_error(p.ctrl, MOE_ERR_DEVICE_FAULT, 22);
+          page = 0;                        // (a place that exists)
         }
-        for (; f < 2 * n && ok; ++f) {
-          const Item it = item_at(f, n, lead);
-          const int kb = k0 + it.i * kKeys;
-          const int key = kb + lane * box;
-          const bool mine = lane < segs && key < k1;
-          int page = mine ? __ldg(table + (key >> p.c.page_log2)) : 0;
-          if (page < 0 || page >= p.c.num_pages) {
-            set_error(p.ctrl, MOE_ERR_DEVICE_FAULT, 22);
-            page = 0;                      // (a place that exists)
-          }
-          const int slot = f % S::kSlots;
-          ok = wait(bar(bars.empty[slot]), ((f / S::kSlots) & 1) ^ 1);
-          if (!ok) break;
-          const uint32_t full = bar(bars.full[slot]);
-          if (lane == 0) {
-            const int loaded = min(segs, (k1 - kb + box - 1) / box);
-            mbar_arrive_expect_tx(full, loaded * box * D * 2);
-          }
-          __syncwarp();
-          if (mine) {
-            const int row = ((page * p.c.heads + h) << p.c.page_log2) +
-                            (key & ((1 << p.c.page_log2) - 1));
-            const uint32_t dst = sbase + S::oSlots + slot * S::kTileBytes + lane * box * 128;
+        const int slot = r.f % r.slots;
+        if (!wait(r.empty + 8 * slot, ((r.f / r.slots) & 1) ^ 1)) return false;
+        const uint32_t full = r.full + 8 * slot;
+        if (lane == 0) {
+          const int loaded = min(segs, (k1 - kb + box - 1) / box);
+          mbar_arrive_expect_tx(full, loaded * box * kRowBytes);
+        }
+        __syncwarp();
+        if (mine) {
+          const int row = ((page * p.c.heads + h) << p.c.page_log2) +
+                          (key & ((1 << p.c.page_log2) - 1));
+          const CUtensorMap* map = v ? &map_v : &map_k;
+          const uint32_t dst = r.base + slot * r.bytes;
+          if constexpr (kFP8) {
+            tma_load_2d(dst + lane * box * D, map, full, 0, row, policy);
+          } else {
 #pragma unroll
             for (int x = 0; x < D / 64; ++x)
-              tma_load_2d(dst + x * kHalfBytes, it.v ? &map_v : &map_k, full, x * 64, row, policy);
+              tma_load_2d(dst + x * kHalfBytes + lane * box * 128, map, full, x * 64, row, policy);
           }
-          __syncwarp();
         }
-        if (!ok) {                         // copies in flight land before the memory goes
-          for (int g = max(0, f - S::kSlots); g < f; ++g)
-            mbar_wait_drain(bar(bars.full[g % S::kSlots]), (g / S::kSlots) & 1, p.timeout_ns);
-        }
+        __syncwarp();
+        ++r.f;
+        return true;
+      };
+      for (int f = 0; f < 2 * n && ok; ++f) {
+        const Item it = item_at(f, n, lead);
+        ok = load(kFP8 && !it.v ? rk : rv, it.v, it.i);
+      }
+      if (!ok) {                           // copies in flight land before the memory goes
+        for (int g = max(0, rv.f - rv.slots); g < rv.f; ++g)
+          mbar_wait_drain(rv.full + 8 * (g % rv.slots), (g / rv.slots) & 1, p.timeout_ns);
+        if (kFP8)
+          for (int g = max(0, rk.f - rk.slots); g < rk.f; ++g)
+            mbar_wait_drain(rk.full + 8 * (g % rk.slots), (g / rk.slots) & 1, p.timeout_ns);
       }
     }
   } else {
-    // =================================================================== FP8: codes to binary16
+    // =================================================================== FP8: V's codes to binary16
     regs_dec<S::kRegsOther>();
     if constexpr (kFP8) {
       const int ct = tid - 384;
-      constexpr int kPieces = D / 16;            // 16-code pieces of a row
+      constexpr int kPieces = D / 16;             // 16-code pieces of a row
       constexpr int kPer = kKeys * kPieces / 128; // pieces per thread
-      constexpr int kRowsPer = 128 / kPieces;    // rows per step of the group
+      constexpr int kRowsPer = 128 / kPieces;     // rows per step of the group
       const int c = ct % kPieces, r0 = ct / kPieces;
-      const uint32_t raw = sbase + S::oRaw, raw_sc = sbase + S::oRawScale;
       const int page_mask = (1 << p.c.page_log2) - 1;
       const int first_key = max(t.lo, k0);
-      // starts the copies of item f into this thread's own places of the raw ring
-      auto start = [&](int f) {
-        if (f < 2 * n) {
-          const Item it = item_at(f, n, lead);
-          const int kb = k0 + it.i * kKeys;
-          // lanes 0..7 hold the page of each 16 keys
-          const int pk = kb + (lane & 7) * 16;
-          int page = pk < k1 ? __ldg(table + (pk >> p.c.page_log2)) : 0;
-          if (page < 0 || page >= p.c.num_pages) {
-            set_error(p.ctrl, MOE_ERR_DEVICE_FAULT, 22);
-            page = 0;
-          }
-          const int slot = f % S::kRaw;
-          const uint8_t* src = it.v ? p.c.v : p.c.k;
-#pragma unroll
-          for (int i = 0; i < kPer; ++i) {
-            const int r = i * kRowsPer + r0;
-            const int pg = __shfl_sync(0xffffffffu, page, r >> 4);
-            const int key = kb + r;
-            const bool valid = key >= first_key && key < k1;
-            const int64_t at = (((static_cast<int64_t>(pg) * p.c.heads + h) << p.c.page_log2) +
-                                (valid ? key & page_mask : 0)) * D + c * 16;
-            const int bytes = valid ? 16 : 0;
-            asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(
-                             raw + slot * S::kRawBytes + (i * 128 + ct) * 16),
-                         "l"(src + at), "r"(bytes)
-                         : "memory");
-          }
-          if (!it.v) {
-            const int pg = __shfl_sync(0xffffffffu, page, ct >> 4);
-            const int key = kb + ct;
-            const bool valid = key >= first_key && key < k1;
-            const int64_t at = ((static_cast<int64_t>(pg) * p.c.heads + h) << p.c.page_log2) +
-                               (valid ? key & page_mask : 0);
-            const int bytes = valid ? 4 : 0;
-            const uint32_t d = raw_sc + slot * 1024 + ct * 4;
-            asm volatile("cp.async.ca.shared.global [%0], [%1], 4, %2;" ::"r"(d),
-                         "l"(p.c.k_scales + at), "r"(bytes)
-                         : "memory");
-            asm volatile("cp.async.ca.shared.global [%0], [%1], 4, %2;" ::"r"(d + 512),
-                         "l"(p.c.v_scales + at), "r"(bytes)
-                         : "memory");
-          }
+      // this thread's key of each tile: its page two tiles ahead, its scales one ahead
+      auto page_of = [&](int i) {
+        const int key = k0 + i * kKeys + ct;
+        return key < k1 ? __ldg(table + (key >> p.c.page_log2)) : -1;
+      };
+      float ks = 0.0f, vs = 0.0f;
+      auto fetch_scales = [&](int i, int page) {
+        const int key = k0 + i * kKeys + ct;
+        ks = vs = 0.0f;
+        if (key < k1 && page >= 0 && page < p.c.num_pages) {
+          const int64_t at = ((static_cast<int64_t>(page) * p.c.heads + h) << p.c.page_log2) +
+                             (key & page_mask);
+          ks = __ldg(p.c.k_scales + at);
+          vs = __ldg(p.c.v_scales + at);
         }
-        asm volatile("cp.async.commit_group;" ::: "memory");
+      };
+      int page_next = page_of(1);
+      fetch_scales(0, page_of(0));
+      int e0 = 0, e1 = 0, e2 = 0;                 // exponents of the last tiles published
+      // hands tile i's scales to the softmax and keeps V's for the conversion
+      auto publish = [&](int i) -> bool {
+        const int slot = i % S::kScaleSlots;
+        const bool ok = wait(bar(bars.sc_empty[slot]), ((i / S::kScaleSlots) & 1) ^ 1);
+        float* sc = reinterpret_cast<float*>(smem + S::oScale + slot * 1024);
+        float top = vs;
+#pragma unroll
+        for (int o = 16; o > 0; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
+        if (ok) {
+          if (lane == 0) bars.red[i & 1][warp & 3] = top;
+          sc[ct] = ks;
+          sc[128 + ct] = vs;
+        }
+        fetch_scales(i + 1, page_next);
+        page_next = page_of(i + 2);
+        // (the four warps agree, so that none is left waiting for the others)
+        if (named_bar_any(2, 128, !ok)) return false;
+        top = fmaxf(fmaxf(bars.red[i & 1][0], bars.red[i & 1][1]),
+                    fmaxf(bars.red[i & 1][2], bars.red[i & 1][3]));
+        const int ex = min(max(static_cast<int>((__float_as_uint(top) >> 23) & 255u), 1), 253);
+        if (ct == 0) bars.e[slot] = ex - 127;
+        e2 = e1;
+        e1 = e0;
+        e0 = ex - 127;
+        mbar_arrive(bar(bars.sc_full[slot]));
+        return true;
       };
       bool ok = p.drop_producer == 0;
-      if (ok) {
-        start(0);
-        start(1);
-      }
-      for (int f = 0; f < 2 * n && ok; ++f) {
-        start(f + 2);
-        asm volatile("cp.async.wait_group 2;" ::: "memory");
-        const Item it = item_at(f, n, lead);
-        const int rslot = f % S::kRaw, slot = f % S::kSlots, sslot = it.i % S::kScaleSlots;
-        float* sc = reinterpret_cast<float*>(smem + S::oScale + sslot * 1024);
-        if (!it.v) {
-          ok = wait(bar(bars.sc_empty[sslot]), ((it.i / S::kScaleSlots) & 1) ^ 1);
-          const float* rs = reinterpret_cast<const float*>(smem + S::oRawScale + rslot * 1024);
-          const float ks = rs[ct], vs = rs[128 + ct];
-          float top = vs;
-#pragma unroll
-          for (int o = 16; o > 0; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
-          if (lane == 0) bars.red[it.i & 1][warp & 3] = top;
-          if (ok) {
-            sc[ct] = ks;
-            sc[128 + ct] = vs;
-          }
-          named_bar_sync(2, 128);
-          top = fmaxf(fmaxf(bars.red[it.i & 1][0], bars.red[it.i & 1][1]),
-                      fmaxf(bars.red[it.i & 1][2], bars.red[it.i & 1][3]));
-          const int ex = min(max(static_cast<int>((__float_as_uint(top) >> 23) & 255u), 1), 253);
-          if (ct == 0 && ok) bars.e[sslot] = ex - 127;
-          if (ok) mbar_arrive(bar(bars.sc_full[sslot]));
-        }
-        if (ok) ok = wait(bar(bars.empty[slot]), ((f / S::kSlots) & 1) ^ 1);
-        if (ok) {
+      for (int i = 0; i < min(lead, n) && ok; ++i) ok = publish(i);
+      for (int i = 0; i < n && ok; ++i) {
+        if (i + lead < n) ok = publish(i + lead);
+        const int rslot = i % S::kRawSlots, slot = i % S::kSlots, sslot = i % S::kScaleSlots;
+        bool here = ok && wait(bar(bars.raw_full[rslot]), (i / S::kRawSlots) & 1);
+        here = here && wait(bar(bars.empty[slot]), ((i / S::kSlots) & 1) ^ 1);
+        if (here) {
+          const int kb = k0 + i * kKeys;
+          const uint32_t src = sbase + S::oRaw + rslot * S::kCodeBytes;
           const uint32_t dst = sbase + S::oSlots + slot * S::kTileBytes;
-          const float mul =
-              it.v ? __uint_as_float(static_cast<uint32_t>(127 - bars.e[sslot]) << 23) : 0.0f;
-#pragma unroll
-          for (int i = 0; i < kPer; ++i) {
-            const int r = i * kRowsPer + r0;
+          const float* sc = reinterpret_cast<const float*>(smem + S::oScale + sslot * 1024) + 128;
+          const int ago = min(i + lead, n - 1) - i;   // tiles published since this one
+          const int e = ago == 0 ? e0 : (ago == 1 ? e1 : e2);
+          const float mul = __uint_as_float(static_cast<uint32_t>(127 - e) << 23);
+          const bool edge = kb < first_key || kb + kKeys > k1;
+#pragma unroll 4
+          for (int j = 0; j < kPer; ++j) {
+            const int r = j * kRowsPer + r0;
             uint4 x;
             asm volatile("ld.shared.v4.u32 {%0, %1, %2, %3}, [%4];"
                          : "=r"(x.x), "=r"(x.y), "=r"(x.z), "=r"(x.w)
-                         : "r"(raw + rslot * S::kRawBytes + (i * 128 + ct) * 16));
+                         : "r"(src + code_piece<D>(r, c)));
+            const __half2 g = __float2half2_rn(sc[r] * mul);
             const uint32_t xw[4] = {x.x, x.y, x.z, x.w};
             uint32_t o[8];
 #pragma unroll
-            for (int j = 0; j < 4; ++j) {
-              o[2 * j] = e4m3x2_to_f16x2(static_cast<uint16_t>(xw[j]));
-              o[2 * j + 1] = e4m3x2_to_f16x2(static_cast<uint16_t>(xw[j] >> 16));
+            for (int q = 0; q < 8; ++q) {
+              uint32_t y = e4m3x2_to_f16x2(static_cast<uint16_t>(xw[q >> 1] >> (16 * (q & 1))));
+              __half2 z = __hmul2(*reinterpret_cast<__half2*>(&y), g);
+              o[q] = *reinterpret_cast<uint32_t*>(&z);
             }
-            if (it.v) {
-              const __half2 g = __float2half2_rn(sc[128 + r] * mul);
+            if (edge && (kb + r < first_key || kb + r >= k1)) {   // a row that nobody sees
 #pragma unroll
-              for (int j = 0; j < 8; ++j) {
-                __half2 y = __hmul2(*reinterpret_cast<__half2*>(&o[j]), g);
-                o[j] = *reinterpret_cast<uint32_t*>(&y);
-              }
+              for (int q = 0; q < 8; ++q) o[q] = 0u;
             }
-            // pieces 2c and 2c + 1 of the row's 16-byte pieces
-            const int p0 = 2 * c;
-            const uint32_t at = dst + (p0 >> 3) * kHalfBytes + r * 128;
-            const uint32_t a0 = at + (((p0 & 7) ^ (r & 7)) << 4);
-            const uint32_t a1 = at + ((((p0 & 7) + 1) ^ (r & 7)) << 4);
-            asm volatile("st.shared.v4.u32 [%0], {%1, %2, %3, %4};" ::"r"(a0), "r"(o[0]),
-                         "r"(o[1]), "r"(o[2]), "r"(o[3])
+            // pieces 2c and 2c + 1 of the row's 16-byte pieces; lanes of the second 64
+            // channels store theirs the other way round, so that 8 lanes hit 8 bank groups
+            const uint32_t at = dst + (c >> 2) * kHalfBytes + r * 128;
+            const int p0 = (2 * c) & 7, swap = (c >> 2) & 1;
+            const uint32_t a0 = at + (((p0 + swap) ^ (r & 7)) << 4);
+            const uint32_t a1 = at + (((p0 + 1 - swap) ^ (r & 7)) << 4);
+            asm volatile("st.shared.v4.u32 [%0], {%1, %2, %3, %4};" ::"r"(a0),
+                         "r"(swap ? o[4] : o[0]), "r"(swap ? o[5] : o[1]),
+                         "r"(swap ? o[6] : o[2]), "r"(swap ? o[7] : o[3])
                          : "memory");
-            asm volatile("st.shared.v4.u32 [%0], {%1, %2, %3, %4};" ::"r"(a1), "r"(o[4]),
-                         "r"(o[5]), "r"(o[6]), "r"(o[7])
+            asm volatile("st.shared.v4.u32 [%0], {%1, %2, %3, %4};" ::"r"(a1),
+                         "r"(swap ? o[0] : o[4]), "r"(swap ? o[1] : o[5]),
+                         "r"(swap ? o[2] : o[6]), "r"(swap ? o[3] : o[7])
                          : "memory");
           }
           fence_async_smem();
           mbar_arrive(bar(bars.full[slot]));
+          mbar_arrive(bar(bars.raw_empty[rslot]));
         }
-        // the four warps agree, so that none is left waiting for the others
-        ok = !named_bar_any(2, 128, !ok);
+        if (i + lead >= n)                   // (no publish agrees for the last tiles)
+          ok = !named_bar_any(2, 128, !here);
+        else if (!here)
+          ok = !named_bar_any(2, 128, true);
       }
-      asm volatile("cp.async.wait_all;" ::: "memory");
     }
   }
   tc_fence_before();
@@ -953,16 +1037,19 @@ cudaError_t launch_t(const AttnParams& p, const CUtensorMap& mk, const CUtensorM
   return cudaGetLastError();
 }
 
-// The cache rows [rows, D] of bf16, in boxes of 64 channels x up to 128 positions.
-bool cache_map(CUtensorMap* m, const void* base, int D, uint64_t rows, uint32_t box_rows) {
+// The cache rows [rows, D] in boxes of up to 128 positions: bf16 in boxes of 64
+// channels (128 bytes), codes in whole rows (D bytes).
+bool cache_map(CUtensorMap* m, const void* base, int D, bool fp8, uint64_t rows,
+               uint32_t box_rows) {
   auto fn = encode_fn();
   if (fn == nullptr) return false;
   cuuint64_t dims[2] = {static_cast<cuuint64_t>(D), rows};
-  cuuint64_t strides[1] = {static_cast<cuuint64_t>(D) * 2};
-  cuuint32_t box[2] = {64u, box_rows};
+  cuuint64_t strides[1] = {static_cast<cuuint64_t>(D) * (fp8 ? 1 : 2)};
+  cuuint32_t box[2] = {fp8 ? static_cast<cuuint32_t>(D) : 64u, box_rows};
   cuuint32_t estr[2] = {1, 1};
-  return fn(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, const_cast<void*>(base), dims, strides, box,
-            estr, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
+  return fn(m, fp8 ? CU_TENSOR_MAP_DATA_TYPE_UINT8 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2,
+            const_cast<void*>(base), dims, strides, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE,
+            fp8 && D == 64 ? CU_TENSOR_MAP_SWIZZLE_64B : CU_TENSOR_MAP_SWIZZLE_128B,
             CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
             CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
@@ -974,16 +1061,16 @@ cudaError_t launch_attention_tiles(const AttnParams& p, int head_dim, bool fp8,
   CUtensorMap mk, mv;
   std::memset(&mk, 0, sizeof(mk));
   std::memset(&mv, 0, sizeof(mv));
-  if (!fp8) {
-    const uint64_t rows = (static_cast<uint64_t>(p.c.num_pages) * p.c.heads) << p.c.page_log2;
-    const uint32_t box = 1u << p.c.page_log2 < 128u ? 1u << p.c.page_log2 : 128u;
-    if (!cache_map(&mk, p.c.k, head_dim, rows, box) || !cache_map(&mv, p.c.v, head_dim, rows, box))
-      return cudaErrorInvalidValue;
-    return head_dim == 128 ? launch_t<128, false>(p, mk, mv, stream)
-                           : launch_t<64, false>(p, mk, mv, stream);
-  }
-  return head_dim == 128 ? launch_t<128, true>(p, mk, mv, stream)
-                         : launch_t<64, true>(p, mk, mv, stream);
+  const uint64_t rows = (static_cast<uint64_t>(p.c.num_pages) * p.c.heads) << p.c.page_log2;
+  const uint32_t box = 1u << p.c.page_log2 < 128u ? 1u << p.c.page_log2 : 128u;
+  if (!cache_map(&mk, p.c.k, head_dim, fp8, rows, box) ||
+      !cache_map(&mv, p.c.v, head_dim, fp8, rows, box))
+    return cudaErrorInvalidValue;
+  if (fp8)
+    return head_dim == 128 ? launch_t<128, true>(p, mk, mv, stream)
+                           : launch_t<64, true>(p, mk, mv, stream);
+  return head_dim == 128 ? launch_t<128, false>(p, mk, mv, stream)
+                         : launch_t<64, false>(p, mk, mv, stream);
 }
 
 }  // namespace moe
