@@ -15,6 +15,7 @@
 //                    tensor memory), so maxima and sums need no shuffles;
 //   warp 8           TMA loads of K and V pages into rings of tiles;
 //   warp 9           issues the MMAs;
+//   warp 10          (FP8) the tiles' scales;
 //   warps 12-15      (FP8) turn V's codes into binary16 tiles.
 // E4M3 caches: K's codes go to the tensor core as they are (kind::f8f6f4), against
 // the query as the sum of two E4M3 terms (hi = E4M3(q), lo = E4M3(q - hi), after a
@@ -26,10 +27,12 @@
 // softmax.  (Splitting the weights in two E4M3 terms instead would spare V's
 // conversion, but takes four more conversions per pair of weights, and those run
 // at 32 lanes a cycle: 983 cycles per row tile against 230 for V's codes.)
-// O is rescaled only when a row's maximum grew by more than 2^8 since its
-// reference (the weights then stay below 2^8, far inside their types), which
-// leaves the rescale to a few tiles per row; the softmax threads do it themselves
-// between their S and their P, when no product of theirs is running.
+// The softmax takes a maximum only for a row's first keys: later weights are
+// taken against that reference, and their sum tells whether one of them came near the end
+// of its type (16-bit floats and binary32 sums lose nothing short of that); only
+// then do a second pass and a rescale of O follow, which the softmax threads do
+// themselves between their S and their P, when no product of theirs is running.
+// (With a running maximum in every tile: 2800 cycles per pair of row tiles, 1.48 us.)
 // With at most 128 rows both softmax groups work on the same rows, on key tiles
 // of even and odd number, each with its own O; they are joined at the end.
 //
@@ -64,7 +67,7 @@ struct TileShape {
   static constexpr int oSlots = 2 * kTileBytes;
   static constexpr int oK = oSlots + kSlots * kTileBytes;
   static constexpr int oRaw = oK + kKSlots * kCodeBytes;
-  static constexpr int oScale = oRaw + kRawSlots * kCodeBytes;         // [slot][ks 128 | vs 128]
+  static constexpr int oScale = oRaw + kRawSlots * kCodeBytes;         // [slot][ks f32 | vs * 2^-e f16x2]
   static constexpr int oRowf = oScale + (kFP8 ? kScaleSlots * 1024 : 0);
   static constexpr int kSmem = oRowf + (kFP8 ? 1024 : 0);
   // setmaxnreg shares: softmax, the rest (BF16: 384 x 168 registers at launch, 2 x 128 x 208 +
@@ -179,17 +182,6 @@ template <int N>
 __device__ __forceinline__ void regs_dec() {
   asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(N));
 }
-// Named barrier among `count` threads that tells them whether any had `x` set.
-__device__ __forceinline__ bool named_bar_any(int id, int count, bool x) {
-  uint32_t r;
-  asm volatile(
-      "{\n\t.reg .pred a, b;\n\tsetp.ne.u32 a, %3, 0;\n\t"
-      "barrier.cta.red.or.pred b, %1, %2, a;\n\tselp.u32 %0, 1, 0, b;\n\t}"
-      : "=r"(r)
-      : "r"(id), "r"(count), "r"(x ? 1u : 0u)
-      : "memory");
-  return r != 0;
-}
 // One lane of a converged warp, the same one each time.
 __device__ __forceinline__ bool elect_one() {
   uint32_t r;
@@ -241,7 +233,6 @@ struct Bars {
   int abort;
   int flag;
   int e[3];                       // FP8: exponent of each tile's value scales
-  float red[2][4];
   float other[2][kRows];          // group 1's references and sums, when it hands over
 };
 
@@ -300,9 +291,10 @@ __global__ void __launch_bounds__(TileShape<D, kFP8>::kThreads, 1)
       mbar_init(bar(bars.o_done[w]), 1);
     }
     for (int i = 0; i < S::kScaleSlots; ++i) {
-      mbar_init(bar(bars.sc_full[i]), 128);
-      // (row tile 0 may skip the last two key tiles at most: no later tile waits for their slots)
-      mbar_init(bar(bars.sc_empty[i]), alt ? 4 : 8);
+      mbar_init(bar(bars.sc_full[i]), 1);
+      // a group's warps and the converting ones (row tile 0 may skip the last two key tiles at
+      // most: no later tile waits for their slots)
+      mbar_init(bar(bars.sc_empty[i]), (alt ? 4 : 8) + 4);
     }
     mbar_init(bar(bars.drain), 1);
     bars.abort = 0;
@@ -425,7 +417,10 @@ __global__ void __launch_bounds__(TileShape<D, kFP8>::kThreads, 1)
       }
     }
     const float ninf = __int_as_float(0xff800000);
-    float m = ninf, ref = 0.0f, l = 0.0f;
+    const float f = cap > 0.0f ? 1.0f : sc;          // from s (or capped scores) to log2 units
+    constexpr float kFar = kFP8 ? 16384.0f : 1.0e18f;
+    float ref = 0.0f, l = 0.0f;
+    bool started = false;                            // the row has seen a key
     int E = 0;                                       // FP8: O is in units of 2^E
     const uint32_t s_tm = tmem + lanes + w * kKeys;
     const uint32_t o_tm = tmem + lanes + 256 + w * D;
@@ -458,70 +453,84 @@ __global__ void __launch_bounds__(TileShape<D, kFP8>::kThreads, 1)
           }
           e = bars.e[sslot];
         }
-        float f = sc;
         if (cap > 0.0f) {
 #pragma unroll
           for (int j = 0; j < kKeys; ++j) s[j] = soft_capped(s[j] * sc, cap_k, cap) * kLog2e;
-          f = 1.0f;
         }
         if (kb + kKeys > r_hi || kb < r_lo) {
           const int lo = r_lo - kb, hi = r_hi - kb;
 #pragma unroll
           for (int j = 0; j < kKeys; ++j) s[j] = (j < lo || j >= hi) ? ninf : s[j];
         }
-        float x[4] = {s[0], s[1], s[2], s[3]};
+        auto row_max = [&]() {
+          float x[4] = {s[0], s[1], s[2], s[3]};
 #pragma unroll
-        for (int j = 4; j < kKeys; ++j) x[j & 3] = fmaxf(x[j & 3], s[j]);
-        const float mx = fmaxf(fmaxf(x[0], x[1]), fmaxf(x[2], x[3])) * f;
-        m = fmaxf(m, mx == mx ? mx : ninf);
-        const float want = m == ninf ? 0.0f : m;
-        int E2 = E;
-        if constexpr (kFP8) E2 = c == 0 ? e : max(E, e);
-        if (c == 0) {
-          ref = want;
-          E = E2;
-        } else if (__any_sync(0xffffffffu, want > ref + 8.0f || E2 != E)) {
-          const float keep = ref == want ? 1.0f : exp2_approx(ref - want);
-          l *= keep;
-          const float g = kFP8 ? keep * exp2_approx(static_cast<float>(E - E2)) : keep;
-          ref = want;
-          E = E2;
-          // S of this tile is complete, so every earlier product of this group is too
-#pragma unroll 1
-          for (int d = 0; d < D; d += 16) {
-            float o[16];
-            tmem_ld16(o_tm + d, o);
-            tmem_ld_wait(o);
+          for (int j = 4; j < kKeys; ++j) x[j & 3] = fmaxf(x[j & 3], s[j]);
+          const float y = fmaxf(fmaxf(x[0], x[1]), fmaxf(x[2], x[3])) * f;
+          return y > ninf ? y : 0.0f;
+        };
+        // a row's first keys set its reference
+        const bool first = !started && kb < r_hi && kb + kKeys > r_lo;
+        if (__any_sync(0xffffffffu, first)) {
+          const float top = row_max();
+          if (first) {
+            ref = top;
+            E = e;
+            started = true;
+          }
+        }
+        // weights, into the place of the scores, and their sum
+        auto weigh = [&]() {
+          float shift = -ref;
+          if constexpr (kFP8) shift += static_cast<float>(e - E);
+          float sum0 = 0.0f, sum1 = 0.0f, sum2 = 0.0f, sum3 = 0.0f;
+#pragma unroll
+          for (int q = 0; q < 4; ++q) {
             uint32_t r[16];
 #pragma unroll
-            for (int j = 0; j < 16; ++j) r[j] = __float_as_uint(o[j] * g);
-            tmem_st16(o_tm + d, r);
+            for (int j = 0; j < 16; ++j) {
+              float a, bb;
+              fma2_bc(a, bb, s[32 * q + 2 * j], s[32 * q + 2 * j + 1], f, shift);
+              a = exp2_approx(a);
+              bb = exp2_approx(bb);
+              if (j & 1) add2(sum2, sum3, a, bb); else add2(sum0, sum1, a, bb);
+              if constexpr (kFP8) {
+                __half2 hh = __floats2half2_rn(a, bb);
+                r[j] = *reinterpret_cast<uint32_t*>(&hh);
+              } else {
+                __nv_bfloat162 hh = __floats2bfloat162_rn(a, bb);
+                r[j] = *reinterpret_cast<uint32_t*>(&hh);
+              }
+            }
+            tmem_st16(s_tm + 16 * q, r);
           }
-        }
-        float shift = -ref;
-        if constexpr (kFP8) shift += static_cast<float>(e - E);
-        float sum0 = 0.0f, sum1 = 0.0f, sum2 = 0.0f, sum3 = 0.0f;
+          return (sum0 + sum1) + (sum2 + sum3);
+        };
+        float sum = weigh();
+        if (__any_sync(0xffffffffu, sum > kFar)) {
+          const bool hot = sum > kFar;
+          const float want = hot ? row_max() : ref;
+          const int E2 = hot ? e : E;
+          const float keep = exp2_approx(ref - want);
+          const float g = kFP8 ? keep * exp2_approx(static_cast<float>(E - E2)) : keep;
+          l *= keep;
+          ref = want;
+          E = E2;
+          if (c > 0) {
+            // S of this tile is complete, so every earlier product of this group is too
+#pragma unroll 1
+            for (int d = 0; d < D; d += 16) {
+              float o[16];
+              tmem_ld16(o_tm + d, o);
+              tmem_ld_wait(o);
+              uint32_t r[16];
 #pragma unroll
-        for (int q = 0; q < 4; ++q) {
-          uint32_t r[16];
-#pragma unroll
-          for (int j = 0; j < 16; ++j) {
-            float a = s[32 * q + 2 * j], bb = s[32 * q + 2 * j + 1];
-            fma2_bc(a, bb, a, bb, f, shift);
-            a = exp2_approx(a);
-            bb = exp2_approx(bb);
-            if (j & 1) add2(sum2, sum3, a, bb); else add2(sum0, sum1, a, bb);
-            if constexpr (kFP8) {
-              __half2 hh = __floats2half2_rn(a, bb);
-              r[j] = *reinterpret_cast<uint32_t*>(&hh);
-            } else {
-              __nv_bfloat162 hh = __floats2bfloat162_rn(a, bb);
-              r[j] = *reinterpret_cast<uint32_t*>(&hh);
+              for (int j = 0; j < 16; ++j) r[j] = __float_as_uint(o[j] * g);
+              tmem_st16(o_tm + d, r);
             }
           }
-          tmem_st16(s_tm + 16 * q, r);
+          sum = weigh();
         }
-        float sum = (sum0 + sum1) + (sum2 + sum3);
         if constexpr (kFP8) sum *= exp2_approx(static_cast<float>(E - e));
         l += sum;
         tmem_st_wait();
@@ -542,10 +551,10 @@ __global__ void __launch_bounds__(TileShape<D, kFP8>::kThreads, 1)
     const bool have = ok && my_n > 0 && !idle;
     const float unit = kFP8 ? exp2_approx(static_cast<float>(E)) : 1.0f;
     if (!have) {
-      m = ninf;
+      started = false;
       l = 0.0f;
     }
-    if (m == ninf) ref = ninf;                       // the row saw no key
+    if (!started) ref = ninf;
     float* other = reinterpret_cast<float*>(smem + S::oSlots);     // [128][D], pieces swizzled
     constexpr int kOutPieces = D / 4;
     auto other_at = [&](int d4) { return other + row * D + ((d4 ^ (row & (kOutPieces - 1))) << 2); };
@@ -900,6 +909,54 @@ __global__ void __launch_bounds__(TileShape<D, kFP8>::kThreads, 1)
           for (int g = max(0, rk.f - rk.slots); g < rk.f; ++g)
             mbar_wait_drain(rk.full + 8 * (g % rk.slots), (g / rk.slots) & 1, p.timeout_ns);
       }
+    } else if (kFP8 && warp == 10) {
+      // ================================================================= FP8: scales
+      // Four keys per lane; pages two tiles ahead, scales one.
+      const int page_mask = (1 << p.c.page_log2) - 1;
+      auto page_of = [&](int i) {
+        const int key = k0 + i * kKeys + 4 * lane;
+        return key < k1 ? __ldg(table + (key >> p.c.page_log2)) : -1;
+      };
+      float ks[4], vs[4];
+      auto fetch = [&](int i, int page) {
+        const int key = k0 + i * kKeys + 4 * lane;
+        const bool have = page >= 0 && page < p.c.num_pages;
+        const int64_t at = ((static_cast<int64_t>(have ? page : 0) * p.c.heads + h)
+                            << p.c.page_log2) + (key & page_mask);
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+          const bool x = have && key + j < k1;
+          ks[j] = x ? __ldg(p.c.k_scales + at + j) : 0.0f;
+          vs[j] = x ? __ldg(p.c.v_scales + at + j) : 0.0f;
+        }
+      };
+      bool ok = p.drop_producer == 0;
+      int page_next = page_of(1);
+      fetch(0, page_of(0));
+      for (int i = 0; i < n && ok; ++i) {
+        const int slot = i % S::kScaleSlots;
+        ok = wait(bar(bars.sc_empty[slot]), ((i / S::kScaleSlots) & 1) ^ 1);
+        if (!ok) break;
+        // the tile's largest value scale (scales are not negative: their bits are ordered)
+        const uint32_t top = __reduce_max_sync(
+            0xffffffffu, __float_as_uint(fmaxf(fmaxf(vs[0], vs[1]), fmaxf(vs[2], vs[3]))));
+        const int ex = min(max(static_cast<int>((top >> 23) & 255u), 1), 253);
+        const float mul = __uint_as_float(static_cast<uint32_t>(254 - ex) << 23);   // 2^-e
+        uint32_t g[4];
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+          __half2 x = __float2half2_rn(vs[j] * mul);
+          g[j] = *reinterpret_cast<uint32_t*>(&x);
+        }
+        uint8_t* sc = smem + S::oScale + slot * 1024 + lane * 16;
+        *reinterpret_cast<float4*>(sc) = make_float4(ks[0], ks[1], ks[2], ks[3]);
+        *reinterpret_cast<uint4*>(sc + 512) = make_uint4(g[0], g[1], g[2], g[3]);
+        if (lane == 0) bars.e[slot] = ex - 127;
+        __syncwarp();
+        if (lane == 0) mbar_arrive(bar(bars.sc_full[slot]));
+        fetch(i + 1, page_next);
+        page_next = page_of(i + 2);
+      }
     }
   } else {
     // =================================================================== FP8: V's codes to binary16
@@ -908,115 +965,62 @@ __global__ void __launch_bounds__(TileShape<D, kFP8>::kThreads, 1)
       const int ct = tid - 384;
       constexpr int kPieces = D / 16;             // 16-code pieces of a row
       constexpr int kPer = kKeys * kPieces / 128; // pieces per thread
-      constexpr int kRowsPer = 128 / kPieces;     // rows per step of the group
-      const int c = ct % kPieces, r0 = ct / kPieces;
-      const int page_mask = (1 << p.c.page_log2) - 1;
+      // 8 lanes of a phase take one piece number of 8 rows: different bank groups in the
+      // codes' swizzle and in the values'
+      const int c = (ct >> 3) % kPieces, r0 = (ct & 7) + 8 * ((ct >> 3) / kPieces);
       const int first_key = max(t.lo, k0);
-      // this thread's key of each tile: its page two tiles ahead, its scales one ahead
-      auto page_of = [&](int i) {
-        const int key = k0 + i * kKeys + ct;
-        return key < k1 ? __ldg(table + (key >> p.c.page_log2)) : -1;
-      };
-      float ks = 0.0f, vs = 0.0f;
-      auto fetch_scales = [&](int i, int page) {
-        const int key = k0 + i * kKeys + ct;
-        ks = vs = 0.0f;
-        if (key < k1 && page >= 0 && page < p.c.num_pages) {
-          const int64_t at = ((static_cast<int64_t>(page) * p.c.heads + h) << p.c.page_log2) +
-                             (key & page_mask);
-          ks = __ldg(p.c.k_scales + at);
-          vs = __ldg(p.c.v_scales + at);
-        }
-      };
-      int page_next = page_of(1);
-      fetch_scales(0, page_of(0));
-      int e0 = 0, e1 = 0, e2 = 0;                 // exponents of the last tiles published
-      // hands tile i's scales to the softmax and keeps V's for the conversion
-      auto publish = [&](int i) -> bool {
-        const int slot = i % S::kScaleSlots;
-        const bool ok = wait(bar(bars.sc_empty[slot]), ((i / S::kScaleSlots) & 1) ^ 1);
-        float* sc = reinterpret_cast<float*>(smem + S::oScale + slot * 1024);
-        float top = vs;
-#pragma unroll
-        for (int o = 16; o > 0; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
-        if (ok) {
-          if (lane == 0) bars.red[i & 1][warp & 3] = top;
-          sc[ct] = ks;
-          sc[128 + ct] = vs;
-        }
-        fetch_scales(i + 1, page_next);
-        page_next = page_of(i + 2);
-        // (the four warps agree, so that none is left waiting for the others)
-        if (named_bar_any(2, 128, !ok)) return false;
-        top = fmaxf(fmaxf(bars.red[i & 1][0], bars.red[i & 1][1]),
-                    fmaxf(bars.red[i & 1][2], bars.red[i & 1][3]));
-        const int ex = min(max(static_cast<int>((__float_as_uint(top) >> 23) & 255u), 1), 253);
-        if (ct == 0) bars.e[slot] = ex - 127;
-        e2 = e1;
-        e1 = e0;
-        e0 = ex - 127;
-        mbar_arrive(bar(bars.sc_full[slot]));
-        return true;
-      };
+      const uint32_t half = (c >> 2) * kHalfBytes;
+      const int p0 = (2 * c) & 7;
       bool ok = p.drop_producer == 0;
-      for (int i = 0; i < min(lead, n) && ok; ++i) ok = publish(i);
+      int rslot = 0, slot = 0, sslot = 0;
+      uint32_t rpar = 0, par = 1, spar = 0;
       for (int i = 0; i < n && ok; ++i) {
-        if (i + lead < n) ok = publish(i + lead);
-        const int rslot = i % S::kRawSlots, slot = i % S::kSlots, sslot = i % S::kScaleSlots;
-        bool here = ok && wait(bar(bars.raw_full[rslot]), (i / S::kRawSlots) & 1);
-        here = here && wait(bar(bars.empty[slot]), ((i / S::kSlots) & 1) ^ 1);
-        if (here) {
-          const int kb = k0 + i * kKeys;
-          const uint32_t src = sbase + S::oRaw + rslot * S::kCodeBytes;
-          const uint32_t dst = sbase + S::oSlots + slot * S::kTileBytes;
-          const float* sc = reinterpret_cast<const float*>(smem + S::oScale + sslot * 1024) + 128;
-          const int ago = min(i + lead, n - 1) - i;   // tiles published since this one
-          const int e = ago == 0 ? e0 : (ago == 1 ? e1 : e2);
-          const float mul = __uint_as_float(static_cast<uint32_t>(127 - e) << 23);
-          const bool edge = kb < first_key || kb + kKeys > k1;
-#pragma unroll 4
-          for (int j = 0; j < kPer; ++j) {
-            const int r = j * kRowsPer + r0;
-            uint4 x;
-            asm volatile("ld.shared.v4.u32 {%0, %1, %2, %3}, [%4];"
-                         : "=r"(x.x), "=r"(x.y), "=r"(x.z), "=r"(x.w)
-                         : "r"(src + code_piece<D>(r, c)));
-            const __half2 g = __float2half2_rn(sc[r] * mul);
-            const uint32_t xw[4] = {x.x, x.y, x.z, x.w};
-            uint32_t o[8];
+        ok = wait(bar(bars.sc_full[0]) + 8 * sslot, spar) &&
+             wait(bar(bars.raw_full[0]) + 8 * rslot, rpar) &&
+             wait(bar(bars.empty[0]) + 8 * slot, par);
+        if (!ok) break;
+        const int kb = k0 + i * kKeys;
+        const uint32_t src = sbase + S::oRaw + rslot * S::kCodeBytes + code_piece<D>(r0, c);
+        const uint32_t dst = sbase + S::oSlots + slot * S::kTileBytes + half + r0 * 128;
+        const uint32_t a0 = dst + ((p0 ^ (r0 & 7)) << 4), a1 = dst + (((p0 + 1) ^ (r0 & 7)) << 4);
+        const __half2* g = reinterpret_cast<const __half2*>(smem + S::oScale + sslot * 1024 + 512);
+        const bool edge = kb < first_key || kb + kKeys > k1;
+        constexpr int kStep = 128 / kPieces;      // rows between a thread's pieces
 #pragma unroll
-            for (int q = 0; q < 8; ++q) {
-              uint32_t y = e4m3x2_to_f16x2(static_cast<uint16_t>(xw[q >> 1] >> (16 * (q & 1))));
-              __half2 z = __hmul2(*reinterpret_cast<__half2*>(&y), g);
-              o[q] = *reinterpret_cast<uint32_t*>(&z);
-            }
-            if (edge && (kb + r < first_key || kb + r >= k1)) {   // a row that nobody sees
+        for (int j = 0; j < kPer; ++j) {
+          const int r = r0 + j * kStep;
+          uint4 x;
+          asm volatile("ld.shared.v4.u32 {%0, %1, %2, %3}, [%4];"
+                       : "=r"(x.x), "=r"(x.y), "=r"(x.z), "=r"(x.w)
+                       : "r"(src + j * kStep * D));
+          const __half2 m2 = g[r];
+          const uint32_t xw[4] = {x.x, x.y, x.z, x.w};
+          uint32_t o[8];
 #pragma unroll
-              for (int q = 0; q < 8; ++q) o[q] = 0u;
-            }
-            // pieces 2c and 2c + 1 of the row's 16-byte pieces; lanes of the second 64
-            // channels store theirs the other way round, so that 8 lanes hit 8 bank groups
-            const uint32_t at = dst + (c >> 2) * kHalfBytes + r * 128;
-            const int p0 = (2 * c) & 7, swap = (c >> 2) & 1;
-            const uint32_t a0 = at + (((p0 + swap) ^ (r & 7)) << 4);
-            const uint32_t a1 = at + (((p0 + 1 - swap) ^ (r & 7)) << 4);
-            asm volatile("st.shared.v4.u32 [%0], {%1, %2, %3, %4};" ::"r"(a0),
-                         "r"(swap ? o[4] : o[0]), "r"(swap ? o[5] : o[1]),
-                         "r"(swap ? o[6] : o[2]), "r"(swap ? o[7] : o[3])
-                         : "memory");
-            asm volatile("st.shared.v4.u32 [%0], {%1, %2, %3, %4};" ::"r"(a1),
-                         "r"(swap ? o[0] : o[4]), "r"(swap ? o[1] : o[5]),
-                         "r"(swap ? o[2] : o[6]), "r"(swap ? o[3] : o[7])
-                         : "memory");
+          for (int q = 0; q < 8; ++q) {
+            uint32_t y = e4m3x2_to_f16x2(static_cast<uint16_t>(xw[q >> 1] >> (16 * (q & 1))));
+            __half2 z = __hmul2(*reinterpret_cast<__half2*>(&y), m2);
+            o[q] = *reinterpret_cast<uint32_t*>(&z);
           }
-          fence_async_smem();
-          mbar_arrive(bar(bars.full[slot]));
-          mbar_arrive(bar(bars.raw_empty[rslot]));
+          if (edge && (kb + r < first_key || kb + r >= k1)) {   // a row that nobody sees
+#pragma unroll
+            for (int q = 0; q < 8; ++q) o[q] = 0u;
+          }
+          asm volatile("st.shared.v4.u32 [%0], {%1, %2, %3, %4};" ::"r"(a0 + j * kStep * 128),
+                       "r"(o[0]), "r"(o[1]), "r"(o[2]), "r"(o[3])
+                       : "memory");
+          asm volatile("st.shared.v4.u32 [%0], {%1, %2, %3, %4};" ::"r"(a1 + j * kStep * 128),
+                       "r"(o[4]), "r"(o[5]), "r"(o[6]), "r"(o[7])
+                       : "memory");
         }
-        if (i + lead >= n)                   // (no publish agrees for the last tiles)
-          ok = !named_bar_any(2, 128, !here);
-        else if (!here)
-          ok = !named_bar_any(2, 128, true);
+        fence_async_smem();
+        mbar_arrive(bar(bars.full[0]) + 8 * slot);
+        mbar_arrive(bar(bars.raw_empty[0]) + 8 * rslot);
+        __syncwarp();
+        if (lane == 0) mbar_arrive(bar(bars.sc_empty[0]) + 8 * sslot);
+        if (++rslot == S::kRawSlots) { rslot = 0; rpar ^= 1; }
+        if (++slot == S::kSlots) { slot = 0; par ^= 1; }
+        if (++sslot == S::kScaleSlots) { sslot = 0; spar ^= 1; }
       }
     }
   }

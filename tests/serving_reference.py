@@ -82,7 +82,7 @@ def attention(q, cache: Paged, q_lens, kv_lens, *, scale=0.0, softcap=0.0, windo
     """(out, lse, tol_out, tol_lse) in float64 of q bf16 [T, Hq, D].
 
     The tolerances bound a binary32 computation: delta, the error of a score, is
-    at most (D + 8) * 2^-23 * scale * sum |q k| (each product exact, every partial
+    at most (D + 8) * 2^-23 * |scale| * sum |q k| (each product exact, every partial
     sum rounded or truncated once), plus c * 2^-20 through a softcap; a weight is
     then off by delta, and once more by its rounding to 8 bits (2^-8, the
     coarsest kernel's); so is the sum, without the rounding; the output is
@@ -113,7 +113,7 @@ def attention(q, cache: Paged, q_lens, kv_lens, *, scale=0.0, softcap=0.0, windo
                 continue
             x = qh @ kh.T * scale
             # scores that nobody sees do not count towards the tolerance
-            delta = ((qh.abs() @ kh.abs().T) * scale * (D + 8) * 2.0 ** -23)
+            delta = ((qh.abs() @ kh.abs().T) * abs(scale) * (D + 8) * 2.0 ** -23)
             delta = delta.masked_fill(~seen, 0.0).amax(1, keepdim=True)
             if softcap:
                 x = softcap * torch.tanh(x / softcap)

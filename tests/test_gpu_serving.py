@@ -242,6 +242,33 @@ def test_sharp_scores(D, fp8, q_lens):
 
 
 @pytest.mark.parametrize("D,fp8", FORMS)
+@pytest.mark.parametrize("sign", [1.0, -1.0])
+@pytest.mark.parametrize("q_len,window", [(1, 0), (150, 0), (300, 70), (300, 1)])
+def test_scores_far_from_zero(D, fp8, sign, q_len, window):
+    """Every score near +-230 (log2 units): nothing may lean on a reference of 0,
+    in rows whose first keys come late neither."""
+    n = 400
+    base = rand_bf16(1, 1, D, seed=3).abs() + 0.5
+    q = base.expand(q_len, 4, D).contiguous().cuda() + rand_bf16(q_len, 4, D, seed=4, scale=0.02).cuda()
+    k = (base * sign).expand(n, 2, D) + rand_bf16(n, 2, D, seed=5, scale=0.05)
+    v = rand_bf16(n, 2, D, seed=6)
+    c = R.Paged([k.to(torch.bfloat16)], [v], 16, fp8)
+    ws = attention_ws()
+    scale = 160.0 / float((base.double() ** 2).sum())
+    got, lse = L.paged_attention(q, c.k, c.v, c.table, cu([q_len]), i32([n]), ws, max_q=q_len,
+                                 k_scales=c.ks, v_scales=c.vs, scale=scale, window=window, lse=True)
+    assert L.get_error(ws) == L.MOE_OK
+    want, want_l, tol, tol_l = R.attention(q, c, [q_len], [n], scale=scale, window=window)
+    assert bool(((got.double() - want).abs() <= tol).all())
+    assert bool(((lse.double() - want_l).abs() <= tol_l).all())
+
+
+@pytest.mark.parametrize("D,fp8", FORMS)
+def test_negative_scale(D, fp8):
+    check_attention([3, 200], [300, 333], 4, 2, D, 32, fp8, scale=-0.11)
+
+
+@pytest.mark.parametrize("D,fp8", FORMS)
 def test_long_caches_are_split(D, fp8):
     check_attention([1], [40000], 8, 1, D, 64, fp8)
     check_attention([2, 1, 20], [20000, 13, 9000], 8, 2, D, 64, fp8)
