@@ -33,13 +33,15 @@
 // then do a second pass and a rescale of O follow, which the softmax threads do
 // themselves between their S and their P, when no product of theirs is running.
 // (With a running maximum in every tile: 2800 cycles per pair of row tiles, 1.48 us.)
-// With at most 128 rows both softmax groups work on the same rows, on key tiles
-// of even and odd number, each with its own O; they are joined at the end.
+// With at most 128 rows there is one row tile, and each softmax group takes half of
+// the columns of every key tile's scores, whose two buffers then alternate: scores of
+// the next tile are ready when a tile's weights are done.
 //
 // What lies past the last key must not meet a zero weight (0 * NaN): the second
 // product runs over the 16-key steps that hold keys, and the rest of a last step is
 // zeroed in shared memory before it.
 #include <cstring>
+#include <type_traits>
 
 #include "attention_common.cuh"
 #include "quant_common.cuh"
@@ -74,7 +76,6 @@ struct TileShape {
   // 128 x 80 = 63488 of 64512; FP8: 512 x 128, 2 x 128 x 192 + 2 x 128 x 64 = 65536)
   static constexpr int kRegsSoftmax = kFP8 ? 192 : 208;
   static constexpr int kRegsOther = kFP8 ? 64 : 80;
-  static_assert(kSlots * kTileBytes >= kRows * D * 4, "the join of two groups fits the ring");
 };
 
 // The 16-byte piece c of row r of a tile of codes (rows of D bytes, the
@@ -182,6 +183,17 @@ template <int N>
 __device__ __forceinline__ void regs_dec() {
   asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(N));
 }
+// Named barrier among `count` threads that tells them whether any had `x` set.
+__device__ __forceinline__ bool named_bar_any(int id, int count, bool x) {
+  uint32_t r;
+  asm volatile(
+      "{\n\t.reg .pred a, b;\n\tsetp.ne.u32 a, %3, 0;\n\t"
+      "barrier.cta.red.or.pred b, %1, %2, a;\n\tselp.u32 %0, 1, 0, b;\n\t}"
+      : "=r"(r)
+      : "r"(id), "r"(count), "r"(x ? 1u : 0u)
+      : "memory");
+  return r != 0;
+}
 // One lane of a converged warp, the same one each time.
 __device__ __forceinline__ bool elect_one() {
   uint32_t r;
@@ -195,8 +207,8 @@ __device__ __forceinline__ void fence_async_smem() {
 }
 
 // The order in which key and value tiles are taken: K of the first `lead`
-// tiles, then V of tile i and K of tile i + lead in turn (lead 1: two row tiles share
-// every key tile; lead 2: they take the even and the odd ones).
+// tiles, then V of tile i and K of tile i + lead in turn (lead 1: a score buffer per row
+// tile; lead 2: two for the one row tile).
 struct Item {
   bool v;
   int i;
@@ -233,7 +245,7 @@ struct Bars {
   int abort;
   int flag;
   int e[3];                       // FP8: exponent of each tile's value scales
-  float other[2][kRows];          // group 1's references and sums, when it hands over
+  float other[2][kRows];          // two groups on the same rows: what one tells the other
 };
 
 template <int D, bool kFP8>
@@ -260,14 +272,10 @@ __global__ void __launch_bounds__(TileShape<D, kFP8>::kThreads, 1)
   const int n = (k1 - k0 + kKeys - 1) / kKeys;                   // key tiles
   const bool alt = t.rows <= kRows;
   const int lead = alt ? 2 : 1;
-  int n_of[2];                                                    // key tiles of each group
-  if (alt) {
-    n_of[0] = (n + 1) / 2;
-    n_of[1] = n / 2;
-  } else {
+  int n_of[2] = {n, n};                                           // key tiles of each group
+  if (!alt) {
     const int hi0 = min(k1, row_hi(p, t, (t.first_row + kRows - 1) / p.group));
     n_of[0] = max(0, min(n, (hi0 - k0 + kKeys - 1) / kKeys));
-    n_of[1] = n;
   }
 
   auto bar = [&](const uint64_t& x) { return smem_u32(&x); };
@@ -287,14 +295,14 @@ __global__ void __launch_bounds__(TileShape<D, kFP8>::kThreads, 1)
     mbar_init(bar(bars.q_full), 256);
     for (int w = 0; w < 2; ++w) {
       mbar_init(bar(bars.s_full[w]), 1);
-      mbar_init(bar(bars.p_full[w]), 128);
+      mbar_init(bar(bars.p_full[w]), alt ? 256 : 128);
       mbar_init(bar(bars.o_done[w]), 1);
     }
     for (int i = 0; i < S::kScaleSlots; ++i) {
       mbar_init(bar(bars.sc_full[i]), 1);
-      // a group's warps and the converting ones (row tile 0 may skip the last two key tiles at
-      // most: no later tile waits for their slots)
-      mbar_init(bar(bars.sc_empty[i]), (alt ? 4 : 8) + 4);
+      // the softmax's warps and the converting ones (row tile 0 may skip the last two key
+      // tiles at most: no later tile waits for their slots)
+      mbar_init(bar(bars.sc_empty[i]), 12);
     }
     mbar_init(bar(bars.drain), 1);
     bars.abort = 0;
@@ -410,9 +418,10 @@ __global__ void __launch_bounds__(TileShape<D, kFP8>::kThreads, 1)
     const int my_n = n_of[w];
     const float cap = p.softcap, cap_k = cap > 0.0f ? 2.0f * kLog2e / cap : 0.0f;
     float sc = fabsf(p.scale) * (cap > 0.0f ? 1.0f : kLog2e);
+    bool ok = true;
     if constexpr (kFP8) {
       if (my_n > 0) {
-        if (!wait(bar(bars.q_full), 0)) {}           // the other group wrote some of the factors
+        ok = wait(bar(bars.q_full), 0);              // the other group wrote some of the factors
         sc *= reinterpret_cast<const float*>(smem + S::oRowf)[my];
       }
     }
@@ -422,185 +431,183 @@ __global__ void __launch_bounds__(TileShape<D, kFP8>::kThreads, 1)
     float ref = 0.0f, l = 0.0f;
     bool started = false;                            // the row has seen a key
     int E = 0;                                       // FP8: O is in units of 2^E
-    const uint32_t s_tm = tmem + lanes + w * kKeys;
-    const uint32_t o_tm = tmem + lanes + 256 + w * D;
-    bool ok = true;
-    for (int c = 0; c < my_n; ++c) {
-      const int i = alt ? 2 * c + w : c;
-      const int kb = k0 + i * kKeys;
-      ok = wait(bar(bars.s_full[w]), c & 1);
-      if (!ok) break;
-      const int sslot = i % S::kScaleSlots;
+    const uint32_t o_tm = tmem + lanes + 256 + (alt ? 0 : w * D);
+
+    // One key tile: kCols scores of this thread's row, from tensor memory at
+    // s_tm, of the keys from kb on, to weights in their place.  kBoth: the other group's
+    // warp of the same rows has the tile's other columns, and the two agree on the
+    // reference (over a barrier of their own).
+    auto tile = [&](auto cols, auto both, int i, int kb, uint32_t s_tm, int sslot) {
+      constexpr int kCols = decltype(cols)::value;
+      constexpr bool kBoth = decltype(both)::value;
+      const int pair_bar = 2 + (warp & 3);
+      float s[kCols];
+#pragma unroll
+      for (int j = 0; j < kCols / 32; ++j) tmem_ld32(s_tm + 32 * j, s + 32 * j);
+#pragma unroll
+      for (int j = 0; j < kCols / 32; ++j) tmem_ld_wait32(s + 32 * j);
+      int e = 0;
       if constexpr (kFP8) {
-        ok = wait(bar(bars.sc_full[sslot]), (i / S::kScaleSlots) & 1);
-        if (!ok) break;
+        const float4* ks = reinterpret_cast<const float4*>(smem + S::oScale + sslot * 1024) +
+                           (kBoth ? w * (kCols / 4) : 0);
+#pragma unroll
+        for (int j = 0; j < kCols / 4; ++j) {
+          const float4 k4 = ks[j];
+          mul2(s[4 * j], s[4 * j + 1], s[4 * j], s[4 * j + 1], k4.x, k4.y);
+          mul2(s[4 * j + 2], s[4 * j + 3], s[4 * j + 2], s[4 * j + 3], k4.z, k4.w);
+        }
+        e = bars.e[sslot];
       }
-      tc_fence_after();
-      if (!idle) {
-        float s[kKeys];
+      if (cap > 0.0f) {
 #pragma unroll
-        for (int j = 0; j < 4; ++j) tmem_ld32(s_tm + 32 * j, s + 32 * j);
+        for (int j = 0; j < kCols; ++j) s[j] = soft_capped(s[j] * sc, cap_k, cap) * kLog2e;
+      }
+      if (kb + kCols > r_hi || kb < r_lo) {
+        const int lo = r_lo - kb, hi = r_hi - kb;
 #pragma unroll
-        for (int j = 0; j < 4; ++j) tmem_ld_wait32(s + 32 * j);
-        int e = 0;
-        if constexpr (kFP8) {
-          const float4* ks = reinterpret_cast<const float4*>(smem + S::oScale + sslot * 1024);
+        for (int j = 0; j < kCols; ++j) s[j] = (j < lo || j >= hi) ? ninf : s[j];
+      }
+      auto row_max = [&]() {
+        float x[4] = {s[0], s[1], s[2], s[3]};
 #pragma unroll
-          for (int j = 0; j < kKeys / 4; ++j) {
-            const float4 k4 = ks[j];
-            mul2(s[4 * j], s[4 * j + 1], s[4 * j], s[4 * j + 1], k4.x, k4.y);
-            mul2(s[4 * j + 2], s[4 * j + 3], s[4 * j + 2], s[4 * j + 3], k4.z, k4.w);
+        for (int j = 4; j < kCols; ++j) x[j & 3] = fmaxf(x[j & 3], s[j]);
+        float y = fmaxf(fmaxf(x[0], x[1]), fmaxf(x[2], x[3])) * f;
+        if constexpr (kBoth) {
+          bars.other[w][row] = y;
+          named_bar_sync(pair_bar, 64);
+          y = fmaxf(y, bars.other[1 - w][row]);
+          named_bar_sync(pair_bar, 64);
+        }
+        return y;
+      };
+      // a row's first keys set its reference
+      const int tile_key = k0 + i * kKeys;
+      const bool first = !started && tile_key < r_hi && tile_key + kKeys > r_lo;
+      if (__any_sync(0xffffffffu, first)) {
+        const float top = row_max();
+        if (first) {
+          ref = top > ninf ? top : 0.0f;
+          E = e;
+          started = true;
+        }
+      }
+      // weights, into the place of the scores, and their sum
+      auto weigh = [&]() {
+        float shift = -ref;
+        if constexpr (kFP8) shift += static_cast<float>(e - E);
+        float sum0 = 0.0f, sum1 = 0.0f, sum2 = 0.0f, sum3 = 0.0f;
+#pragma unroll
+        for (int q = 0; q < kCols / 32; ++q) {
+          uint32_t r[16];
+#pragma unroll
+          for (int j = 0; j < 16; ++j) {
+            float a, bb;
+            fma2_bc(a, bb, s[32 * q + 2 * j], s[32 * q + 2 * j + 1], f, shift);
+            a = exp2_approx(a);
+            bb = exp2_approx(bb);
+            if (j & 1) add2(sum2, sum3, a, bb); else add2(sum0, sum1, a, bb);
+            if constexpr (kFP8) {
+              __half2 hh = __floats2half2_rn(a, bb);
+              r[j] = *reinterpret_cast<uint32_t*>(&hh);
+            } else {
+              __nv_bfloat162 hh = __floats2bfloat162_rn(a, bb);
+              r[j] = *reinterpret_cast<uint32_t*>(&hh);
+            }
           }
-          e = bars.e[sslot];
+          tmem_st16(s_tm + 16 * q, r);
         }
-        if (cap > 0.0f) {
-#pragma unroll
-          for (int j = 0; j < kKeys; ++j) s[j] = soft_capped(s[j] * sc, cap_k, cap) * kLog2e;
-        }
-        if (kb + kKeys > r_hi || kb < r_lo) {
-          const int lo = r_lo - kb, hi = r_hi - kb;
-#pragma unroll
-          for (int j = 0; j < kKeys; ++j) s[j] = (j < lo || j >= hi) ? ninf : s[j];
-        }
-        auto row_max = [&]() {
-          float x[4] = {s[0], s[1], s[2], s[3]};
-#pragma unroll
-          for (int j = 4; j < kKeys; ++j) x[j & 3] = fmaxf(x[j & 3], s[j]);
-          const float y = fmaxf(fmaxf(x[0], x[1]), fmaxf(x[2], x[3])) * f;
-          return y > ninf ? y : 0.0f;
-        };
-        // a row's first keys set its reference
-        const bool first = !started && kb < r_hi && kb + kKeys > r_lo;
-        if (__any_sync(0xffffffffu, first)) {
-          const float top = row_max();
-          if (first) {
-            ref = top;
-            E = e;
-            started = true;
+        return (sum0 + sum1) + (sum2 + sum3);
+      };
+      float sum = weigh();
+      bool far = __any_sync(0xffffffffu, sum > kFar);
+      if constexpr (kBoth) far = named_bar_any(pair_bar, 64, far);
+      if (far) {
+        // (every row of the warp moves to its largest score so far)
+        const float top = row_max();
+        const float want = started ? fmaxf(ref, top) : ref;
+        const float keep = exp2_approx(ref - want);
+        const float g = kFP8 ? keep * exp2_approx(static_cast<float>(E - e)) : keep;
+        l *= keep;
+        ref = want;
+        E = e;
+        if (i > 0) {
+          // the products so far are complete: with one group per row tile the scores'
+          // barrier says so, else the last product's own
+          if constexpr (kBoth) {
+            if (ok) ok = wait(bar(bars.o_done[0]), (i - 1) & 1);
+            tc_fence_after();
           }
-        }
-        // weights, into the place of the scores, and their sum
-        auto weigh = [&]() {
-          float shift = -ref;
-          if constexpr (kFP8) shift += static_cast<float>(e - E);
-          float sum0 = 0.0f, sum1 = 0.0f, sum2 = 0.0f, sum3 = 0.0f;
-#pragma unroll
-          for (int q = 0; q < 4; ++q) {
+          const int d0 = kBoth ? w * (D / 2) : 0, d1 = kBoth ? d0 + D / 2 : D;
+#pragma unroll 1
+          for (int d = d0; d < d1; d += 16) {
+            float o[16];
+            tmem_ld16(o_tm + d, o);
+            tmem_ld_wait(o);
             uint32_t r[16];
 #pragma unroll
-            for (int j = 0; j < 16; ++j) {
-              float a, bb;
-              fma2_bc(a, bb, s[32 * q + 2 * j], s[32 * q + 2 * j + 1], f, shift);
-              a = exp2_approx(a);
-              bb = exp2_approx(bb);
-              if (j & 1) add2(sum2, sum3, a, bb); else add2(sum0, sum1, a, bb);
-              if constexpr (kFP8) {
-                __half2 hh = __floats2half2_rn(a, bb);
-                r[j] = *reinterpret_cast<uint32_t*>(&hh);
-              } else {
-                __nv_bfloat162 hh = __floats2bfloat162_rn(a, bb);
-                r[j] = *reinterpret_cast<uint32_t*>(&hh);
-              }
-            }
-            tmem_st16(s_tm + 16 * q, r);
+            for (int j = 0; j < 16; ++j) r[j] = __float_as_uint(o[j] * g);
+            tmem_st16(o_tm + d, r);
           }
-          return (sum0 + sum1) + (sum2 + sum3);
-        };
-        float sum = weigh();
-        if (__any_sync(0xffffffffu, sum > kFar)) {
-          const bool hot = sum > kFar;
-          const float want = hot ? row_max() : ref;
-          const int E2 = hot ? e : E;
-          const float keep = exp2_approx(ref - want);
-          const float g = kFP8 ? keep * exp2_approx(static_cast<float>(E - E2)) : keep;
-          l *= keep;
-          ref = want;
-          E = E2;
-          if (c > 0) {
-            // S of this tile is complete, so every earlier product of this group is too
-#pragma unroll 1
-            for (int d = 0; d < D; d += 16) {
-              float o[16];
-              tmem_ld16(o_tm + d, o);
-              tmem_ld_wait(o);
-              uint32_t r[16];
-#pragma unroll
-              for (int j = 0; j < 16; ++j) r[j] = __float_as_uint(o[j] * g);
-              tmem_st16(o_tm + d, r);
-            }
-          }
-          sum = weigh();
         }
-        if constexpr (kFP8) sum *= exp2_approx(static_cast<float>(E - e));
-        l += sum;
-        tmem_st_wait();
+        sum = weigh();
+      }
+      if constexpr (kFP8) sum *= exp2_approx(static_cast<float>(E - e));
+      l += sum;
+      tmem_st_wait();
+    };
+
+    // (A wait that gave up ends the waiting, not the loop: the warps of a row then still meet
+    // at the same barriers, and what they compute is dropped.)
+    for (int i = 0; i < my_n; ++i) {
+      // one group per row tile: its own scores; else the two buffers in turn
+      const int buf = alt ? (i & 1) : w;
+      if (ok) ok = wait(bar(bars.s_full[buf]), (alt ? i >> 1 : i) & 1);
+      const int sslot = i % S::kScaleSlots;
+      if constexpr (kFP8) {
+        if (ok) ok = wait(bar(bars.sc_full[sslot]), (i / S::kScaleSlots) & 1);
+      }
+      tc_fence_after();
+      const uint32_t s_tm = tmem + lanes + buf * kKeys;
+      const int kb = k0 + i * kKeys;
+      if (!idle) {
+        if (alt)
+          tile(std::integral_constant<int, 64>(), std::true_type(), i, kb + w * 64, s_tm + w * 64,
+               sslot);
+        else
+          tile(std::integral_constant<int, 128>(), std::false_type(), i, kb, s_tm, sslot);
       }
       tc_fence_before();
       if constexpr (kFP8) {
         __syncwarp();
         if (lane == 0) mbar_arrive(bar(bars.sc_empty[sslot]));
       }
-      mbar_arrive(bar(bars.p_full[w]));
+      mbar_arrive(bar(bars.p_full[buf]));
     }
-    if (ok && my_n > 0) ok = wait(bar(bars.o_done[w]), 0);
-    // (group 1 hands over through the ring's memory: group 0's products read it too)
-    if (ok && alt && w == 1 && n_of[0] > 0) ok = wait(bar(bars.o_done[0]), 0);
+    if (ok && my_n > 0) ok = wait(bar(bars.o_done[alt ? 1 : w]), 0);
     tc_fence_after();
 
-    // ---- results.  Two groups on the same rows: group 1 hands its own over.
+    // ---- results: this thread's row, all its channels or (two groups) half of them
     const bool have = ok && my_n > 0 && !idle;
-    const float unit = kFP8 ? exp2_approx(static_cast<float>(E)) : 1.0f;
     if (!have) {
       started = false;
       l = 0.0f;
     }
     if (!started) ref = ninf;
-    float* other = reinterpret_cast<float*>(smem + S::oSlots);     // [128][D], pieces swizzled
-    constexpr int kOutPieces = D / 4;
-    auto other_at = [&](int d4) { return other + row * D + ((d4 ^ (row & (kOutPieces - 1))) << 2); };
     if (alt) {
-      if (w == 1) {
-        if (have) {
-#pragma unroll 1
-          for (int d = 0; d < D; d += 16) {
-            float o[16];
-            tmem_ld16(o_tm + d, o);
-            tmem_ld_wait(o);
-#pragma unroll
-            for (int j = 0; j < 4; ++j)
-              *reinterpret_cast<float4*>(other_at(d / 4 + j)) =
-                  make_float4(o[4 * j] * unit, o[4 * j + 1] * unit, o[4 * j + 2] * unit,
-                              o[4 * j + 3] * unit);
-          }
-        }
-        bars.other[0][row] = ref;
-        bars.other[1][row] = l;
-      }
-      named_bar_sync(1, 256);
-    }
-    const bool writes = real && (!alt || w == 0);
-    float g0 = unit, g1 = 0.0f;
-    bool have1 = false;
-    if (alt && w == 0) {
-      const float ref1 = bars.other[0][row], l1 = bars.other[1][row];
-      have1 = ref1 != ninf;
-      if (have1) {
-        const float top = fmaxf(ref, ref1);
-        const float a0 = ref == ninf ? 0.0f : exp2_approx(ref - top);
-        g1 = exp2_approx(ref1 - top);
-        l = l * a0 + l1 * g1;
-        g0 = unit * a0;
-        ref = top;
-      }
+      bars.other[w][row] = l;
+      named_bar_sync(2 + (warp & 3), 64);
+      l += bars.other[1 - w][row];
     }
     const bool split = parts.count > 1;
+    const float inv = l == 0.0f ? 0.0f : 1.0f / l;
+    const float g = (kFP8 ? exp2_approx(static_cast<float>(E)) : 1.0f) * (split ? 1.0f : inv);
     float* dst = p.partial + (static_cast<int64_t>(blockIdx.x) * p.splits + part) *
                                  partial_floats<D>(p.part_rows);
-    const float inv = l == 0.0f ? 0.0f : 1.0f / l;
-    __nv_bfloat16* orow = writes && !split ? out_row(p, t, my) : nullptr;
-    if (!idle && (!alt || w == 0)) {
+    __nv_bfloat16* orow = real && !split ? out_row(p, t, my) : nullptr;
+    const int d0 = alt ? w * (D / 2) : 0, d1 = alt ? d0 + D / 2 : D;
+    if (!idle) {
 #pragma unroll 1
-      for (int d = 0; d < D; d += 16) {
+      for (int d = d0; d < d1; d += 16) {
         float o[16];
 #pragma unroll
         for (int j = 0; j < 16; ++j) o[j] = 0.0f;
@@ -608,19 +615,9 @@ __global__ void __launch_bounds__(TileShape<D, kFP8>::kThreads, 1)
           tmem_ld16(o_tm + d, o);
           tmem_ld_wait(o);
 #pragma unroll
-          for (int j = 0; j < 16; ++j) o[j] *= g0;
+          for (int j = 0; j < 16; ++j) o[j] *= g;
         }
-        if (have1) {
-#pragma unroll
-          for (int j = 0; j < 4; ++j) {
-            const float4 y = *reinterpret_cast<const float4*>(other_at(d / 4 + j));
-            o[4 * j] = fmaf(g1, y.x, o[4 * j]);
-            o[4 * j + 1] = fmaf(g1, y.y, o[4 * j + 1]);
-            o[4 * j + 2] = fmaf(g1, y.z, o[4 * j + 2]);
-            o[4 * j + 3] = fmaf(g1, y.w, o[4 * j + 3]);
-          }
-        }
-        if (!writes) continue;
+        if (!real) continue;
         if (split) {
 #pragma unroll
           for (int j = 0; j < 4; ++j)
@@ -630,7 +627,7 @@ __global__ void __launch_bounds__(TileShape<D, kFP8>::kThreads, 1)
           uint32_t u[8];
 #pragma unroll
           for (int j = 0; j < 8; ++j) {
-            __nv_bfloat162 hh = __floats2bfloat162_rn(o[2 * j] * inv, o[2 * j + 1] * inv);
+            __nv_bfloat162 hh = __floats2bfloat162_rn(o[2 * j], o[2 * j + 1]);
             u[j] = *reinterpret_cast<uint32_t*>(&hh);
           }
           reinterpret_cast<uint4*>(orow + d)[0] = make_uint4(u[0], u[1], u[2], u[3]);
@@ -638,7 +635,7 @@ __global__ void __launch_bounds__(TileShape<D, kFP8>::kThreads, 1)
         }
       }
     }
-    if (writes) {
+    if (real && (!alt || w == 0)) {
       if (split) {
         dst[static_cast<int64_t>(p.part_rows) * D + my] = ref;
         dst[static_cast<int64_t>(p.part_rows) * (D + 1) + my] = l;
@@ -647,8 +644,7 @@ __global__ void __launch_bounds__(TileShape<D, kFP8>::kThreads, 1)
       }
     }
     if (split)
-      join_parts<D>(p, t, blockIdx.x, p.part_rows, parts.count, tid, 256, 1,
-                    &bars.flag);
+      join_parts<D>(p, t, blockIdx.x, p.part_rows, parts.count, tid, 256, 1, &bars.flag);
   } else if (warp < 12) {
     regs_dec<S::kRegsOther>();
     if (warp == 9 && n > 0) {
@@ -718,21 +714,25 @@ __global__ void __launch_bounds__(TileShape<D, kFP8>::kThreads, 1)
           umma_commit(bar(bars.s_full[0]) + 8 * w);
         }
       };
-      // O += P V over the 16-key steps of tile i that hold keys
+      // O += P V over the 16-key steps of tile i that hold keys.  P of steps 4..7 lies 32
+      // columns further where two groups wrote it (each in the place of its scores).
+      const uint32_t p_gap = two ? 32 : 0;
       auto values = [&](int w, int i, const Place& x, bool first) {
         const uint32_t v = v_lo + x.slot * (S::kTileBytes >> 4);
-        const uint32_t d = tm + 256 + w * D, pw = tm + w * kKeys;
+        const uint32_t d = tm + 256 + (two ? 0 : w) * D, pw = tm + w * kKeys;
         tc_fence_after();
         if ((i > 0 || first_step == 0) && (i + 1 < tiles || last_steps == 8)) {
           if (elect_one()) {
 #pragma unroll
             for (int s = 0; s < 8; ++s)
-              umma_ts(d, pw + s * 8, v + s * (2048u >> 4), idesc_o, s > 0 ? 1u : (first ? 0u : 1u));
+              umma_ts(d, pw + s * 8 + (s < 4 ? 0 : p_gap), v + s * (2048u >> 4), idesc_o,
+                      s > 0 ? 1u : (first ? 0u : 1u));
           }
         } else if (elect_one()) {
           const int s0 = i == 0 ? first_step : 0, s1 = i + 1 == tiles ? last_steps : 8;
           for (int s = s0; s < s1; ++s)
-            umma_ts(d, pw + s * 8, v + s * (2048u >> 4), idesc_o, (first && s == s0) ? 0u : 1u);
+            umma_ts(d, pw + s * 8 + (s < 4 ? 0 : p_gap), v + s * (2048u >> 4), idesc_o,
+                    (first && s == s0) ? 0u : 1u);
         }
       };
       // (BF16) rows of V in those steps that no row sees
@@ -759,7 +759,7 @@ __global__ void __launch_bounds__(TileShape<D, kFP8>::kThreads, 1)
         }
       };
       bool ok = wait(bar(bars.q_full), 0);
-      uint32_t used0 = 0, used1 = 0;       // parity of each group's weights
+      uint32_t used0 = 0, used1 = 0;       // parity of each row tile's weights
       if (two) {
         for (int w = 0; w < 2 && w < tiles && ok; ++w) {
           const Place x = next_k();
@@ -774,16 +774,18 @@ __global__ void __launch_bounds__(TileShape<D, kFP8>::kThreads, 1)
           ok = wait_v(v) && wait(bar(bars.p_full[0]) + 8 * w, (i >> 1) & 1);
           if (!ok) break;
           clean(i, v);
-          values(w, i, v, i < 2);
+          values(w, i, v, i == 0);
           release_v(v);
+          // o_done[0]: a phase for every product (a rescale at tile i waits for that of tile i - 1,
+          // when that of i - 2 is complete); o_done[1]: the last one
+          if (elect_one()) umma_commit(bar(bars.o_done[0]));
+          if (i + 1 == tiles && elect_one()) umma_commit(bar(bars.o_done[1]));
           if (i + 2 < tiles) {
             const Place k = next_k();
             ok = wait_k(k);
             if (!ok) break;
             scores(w, k);
             release_k(k);
-          } else if (elect_one()) {
-            umma_commit(bar(bars.o_done[0]) + 8 * w);
           }
         }
       } else if (ok) {
@@ -986,15 +988,17 @@ __global__ void __launch_bounds__(TileShape<D, kFP8>::kThreads, 1)
         const __half2* g = reinterpret_cast<const __half2*>(smem + S::oScale + sslot * 1024 + 512);
         const bool edge = kb < first_key || kb + kKeys > k1;
         constexpr int kStep = 128 / kPieces;      // rows between a thread's pieces
+        uint4 x[kPer];                            // all of them first: one latency
+#pragma unroll
+        for (int j = 0; j < kPer; ++j)
+          asm volatile("ld.shared.v4.u32 {%0, %1, %2, %3}, [%4];"
+                       : "=r"(x[j].x), "=r"(x[j].y), "=r"(x[j].z), "=r"(x[j].w)
+                       : "r"(src + j * kStep * D));
 #pragma unroll
         for (int j = 0; j < kPer; ++j) {
           const int r = r0 + j * kStep;
-          uint4 x;
-          asm volatile("ld.shared.v4.u32 {%0, %1, %2, %3}, [%4];"
-                       : "=r"(x.x), "=r"(x.y), "=r"(x.z), "=r"(x.w)
-                       : "r"(src + j * kStep * D));
           const __half2 m2 = g[r];
-          const uint32_t xw[4] = {x.x, x.y, x.z, x.w};
+          const uint32_t xw[4] = {x[j].x, x[j].y, x[j].z, x[j].w};
           uint32_t o[8];
 #pragma unroll
           for (int q = 0; q < 8; ++q) {
