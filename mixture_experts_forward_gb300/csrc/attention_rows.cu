@@ -1,0 +1,759 @@
+// Attention of few rows over the paged cache: single tokens (decode) and
+// short drafted runs, up to 64 rows (new tokens x query heads of one cache head)
+// per tile.  Bound by HBM: every cached byte is read once, by TMA, and meets few rows.
+//
+// The products are turned round, so that a key is a lane and a row a column:
+//   S^T[keys x rows] = K Q^T          (A = the key tile as it lies in the cache)
+//   O^T[channels x rows] += V^T P^T   (A = the value tile, MN-major)
+// With 128 rows of the tensor core filled by keys and channels, 8 or 40 query rows
+// cost no padding to 128; a softmax thread owns a key, so a quantised cache's two
+// scales are one register each, and the maxima and sums over keys cross lanes only at
+// the first tile and at the end: the reference of a row is the maximum of its first
+// keys' scores, and later weights are only checked for the end of their type (then
+// a second pass and a rescale of O follow).
+//
+// E4M3 caches go to the tensor core as they are, in both products: the query is the
+// sum of two E4M3 terms (exact for elements within 2^-10 of the row's largest, to 2^-18 of
+// it below), and so is each weight, hi = E4M3(x), lo = E4M3(16 (x - hi)), with
+// sums of their own: 8 to 9 significant bits over 2^-13 .. 448, the first tile's
+// largest weight at 16 .. 32.  x carries the value scale (relative to 2^E, the first tile's
+// largest), so V is never rewritten.  BF16 caches split the weights in two bf16 terms.
+// Nothing but the output is then rounded to fewer bits than the cache has.
+//
+// Warps 0-3 and 4-7 are two softmax groups, each with half of the rows of every
+// key tile (a thread per key); warp 8 loads, warp 9 issues the MMAs.  Scores are
+// double-buffered in tensor memory.  Up to 32 rows two CTAs share an SM.
+#include <cstring>
+
+#include "attention_tc.cuh"
+
+namespace moe {
+namespace {
+
+template <int D, bool kFP8, int N>
+struct RowsShape {
+  static constexpr int kThreads = 320;
+  static constexpr int kTileBytes = kKeys * D * (kFP8 ? 1 : 2);
+  static constexpr int kQTerm = N * D * (kFP8 ? 1 : 2);  // bytes of the query (of each term)
+  static constexpr int kChunkRows = kFP8 ? 16 : 8;       // rows in 16 bytes of weights
+  static constexpr int kPTerm = N / kChunkRows * kKeys * 16;
+  static constexpr int oSlotsMin = ((kFP8 ? 2 : 1) * kQTerm + 2 * kPTerm + 1023) / 1024 * 1024;
+  // two CTAs per SM where each still has three tiles in shared memory (and 100 registers
+  // hold the rows of a thread)
+  static constexpr int kHalf = 112 * 1024, kWhole = 224 * 1024;
+  static constexpr int kCtas = N <= 32 && (kHalf - oSlotsMin) / kTileBytes >= 3 ? 2 : 1;
+  static constexpr int kFit = ((kCtas == 2 ? kHalf : kWhole) - oSlotsMin) / kTileBytes;
+  static constexpr int kSlots = kFit > 8 ? 8 : kFit;
+  // offsets in shared memory: weights (hi, lo), query (FP8: hi, lo), the ring
+  static constexpr int oP = 0;
+  static constexpr int oQ = 2 * kPTerm;
+  static constexpr int oSlots = oSlotsMin;
+  static constexpr int kSmem = oSlots + kSlots * kTileBytes;
+  static constexpr int kTmem = 4 * N;                    // S twice, O (FP8: hi and lo)
+  static_assert(kSlots >= 3, "two tiles of keys and one of values");
+  static_assert(oQ % 1024 == 0, "swizzled tiles start on 1024 bytes");
+};
+
+template <int N>
+struct RowsBars {
+  uint64_t full[8], empty[8];
+  uint64_t q_full, s_full[2], p_full, o_step, o_last, drain;
+  uint32_t tmem;
+  int abort, flag;
+  int lo[N], hi[N];               // keys that each row sees, in this part
+  alignas(16) float factor[N];    // FP8: of the row's scores
+  int64_t out[N];                 // the row's place in out
+  float part[2][4][N / 2];        // per group and warp: maxima or sums of its rows
+  uint32_t scale[2][4];           // per group and warp: largest value scale (bits)
+};
+
+// D[tmem] (+)= A[smem] * B[smem], any layouts (both descriptors' words given).
+template <bool kFP8>
+__device__ __forceinline__ void umma_ss(uint32_t d, uint32_t a_lo, uint32_t a_hi, uint32_t b_lo,
+                                        uint32_t b_hi, uint32_t idesc, uint32_t accumulate) {
+  if constexpr (kFP8)
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t.reg .b64 ad, bd;\n\tsetp.ne.b32 p, %6, 0;\n\t"
+        "mov.b64 ad, {%1, %2};\n\tmov.b64 bd, {%3, %4};\n\t"
+        "tcgen05.mma.cta_group::1.kind::f8f6f4 [%0], ad, bd, %5, p;\n\t}" ::"r"(d),
+        "r"(a_lo), "r"(a_hi), "r"(b_lo), "r"(b_hi), "r"(idesc), "r"(accumulate)
+        : "memory");
+  else
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t.reg .b64 ad, bd;\n\tsetp.ne.b32 p, %6, 0;\n\t"
+        "mov.b64 ad, {%1, %2};\n\tmov.b64 bd, {%3, %4};\n\t"
+        "tcgen05.mma.cta_group::1.kind::f16 [%0], ad, bd, %5, p;\n\t}" ::"r"(d),
+        "r"(a_lo), "r"(a_hi), "r"(b_lo), "r"(b_hi), "r"(idesc), "r"(accumulate)
+        : "memory");
+}
+
+template <int kCols>
+__device__ __forceinline__ void tmem_ld_cols(uint32_t at, float* v) {
+  if constexpr (kCols == 32) {
+    tmem_ld32(at, v);
+    tmem_ld_wait32(v);
+  } else if constexpr (kCols == 16) {
+    float(&x)[16] = *reinterpret_cast<float(*)[16]>(v);
+    tmem_ld16(at, x);
+    tmem_ld_wait(x);
+  } else {
+    float(&x)[8] = *reinterpret_cast<float(*)[8]>(v);
+    tmem_ld8(at, x);
+    tmem_ld_wait(x);
+  }
+}
+template <int kCols>
+__device__ __forceinline__ void tmem_st_cols(uint32_t at, const uint32_t* r) {
+  if constexpr (kCols >= 16) {
+#pragma unroll
+    for (int i = 0; i < kCols / 16; ++i) tmem_st16(at + 16 * i, r + 16 * i);
+  } else {
+    asm volatile("tcgen05.st.sync.aligned.32x32b.x8.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8};" ::"r"(at),
+                 "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]),
+                 "r"(r[7])
+                 : "memory");
+  }
+}
+
+// A binary32 value as an integer of the same order, and back.
+__device__ __forceinline__ int ordered(float x) {
+  const int b = __float_as_int(x);
+  return b < 0 ? b ^ 0x7fffffff : b;
+}
+__device__ __forceinline__ float unordered(int b) {
+  return __int_as_float(b < 0 ? b ^ 0x7fffffff : b);
+}
+
+template <int D, bool kFP8, int N>
+__global__ void __launch_bounds__(320, RowsShape<D, kFP8, N>::kCtas)
+    rows_kernel(const __grid_constant__ CUtensorMap map_k,
+                const __grid_constant__ CUtensorMap map_v, const AttnParams p) {
+  using S = RowsShape<D, kFP8, N>;
+  constexpr int NH = N / 2;                       // rows of a group
+  extern __shared__ __align__(1024) uint8_t smem[];
+  __shared__ RowsBars<N> bars;
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+
+  const int rt = static_cast<int>(blockIdx.x % p.row_tiles);
+  const int bh = static_cast<int>(blockIdx.x / p.row_tiles);
+  const int b = bh / p.c.heads, h = bh - b * p.c.heads;
+  const int part = blockIdx.y;
+  const TileView t = tile_view(p, b, h, rt, N, part == 0 && rt == 0 && tid == 0);
+  if (t.rows == 0) return;
+  const Parts parts = tile_parts(p, t, kKeys);
+  if (part >= max(1, parts.count)) return;
+  const int k0 = parts.base + part * p.chunk;
+  const int k1 = parts.count == 0 ? k0 : (part + 1 >= parts.count ? t.hi : k0 + p.chunk);
+  const int n = (k1 - k0 + kKeys - 1) / kKeys;    // key tiles
+
+  auto bar = [&](const uint64_t& x) { return smem_u32(&x); };
+  if (tid == 0) {
+    for (int i = 0; i < S::kSlots; ++i) {
+      mbar_init(bar(bars.full[i]), 1);
+      mbar_init(bar(bars.empty[i]), 1);
+    }
+    mbar_init(bar(bars.q_full), 256);
+    mbar_init(bar(bars.s_full[0]), 1);
+    mbar_init(bar(bars.s_full[1]), 1);
+    mbar_init(bar(bars.p_full), 256);
+    mbar_init(bar(bars.o_step), 1);
+    mbar_init(bar(bars.o_last), 1);
+    mbar_init(bar(bars.drain), 1);
+    bars.abort = 0;
+    mbar_fence_init();
+  }
+  if (warp == 9) {
+    tmem_alloc(smem_u32(&bars.tmem), S::kTmem);
+    tmem_relinquish();
+  }
+  if (tid < N) {                                  // the rows' places and keys
+    int lo = 0, hi = 0;
+    int64_t at = 0;
+    if (tid < t.rows) {
+      const int rr = t.first_row + tid, tok = rr / p.group;
+      lo = max(k0, row_lo(p, t, tok));
+      hi = min(k1, row_hi(p, t, tok));
+      at = static_cast<int64_t>(t.q0 + tok) * p.o_st +
+           static_cast<int64_t>(h * p.group + rr - tok * p.group) * p.o_sh;
+    }
+    bars.lo[tid] = lo;
+    bars.hi[tid] = hi;
+    bars.out[tid] = at;
+  }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = bars.tmem;
+  volatile int* abort_flag = &bars.abort;
+  const uint32_t sbase = smem_u32(smem);
+  auto wait = [&](uint32_t at, uint32_t parity) -> bool {
+    const bool ok = mbar_wait(at, parity, abort_flag, p.timeout_ns);
+    if (!ok && !*abort_flag) {
+      *abort_flag = 1;
+      set_error(p.ctrl, MOE_ERR_TIMEOUT, 24);
+    }
+    return __all_sync(0xffffffffu, ok);
+  };
+  const int32_t* table = p.table + static_cast<int64_t>(b) * p.table_stride;
+
+  if (warp < 8) {
+    // =================================================================== softmax
+    const int w = warp >> 2;
+    const int key_lane = (warp & 3) * 32 + lane;         // key of a tile; channel of O
+    const uint32_t lanes = static_cast<uint32_t>(warp & 3) << 21;
+    const int page_mask = (1 << p.c.page_log2) - 1;
+    // this thread's key: its page two tiles ahead, its scales one
+    auto page_of = [&](int i) {
+      const int key = k0 + i * kKeys + key_lane;
+      return kFP8 && key < k1 ? __ldg(table + (key >> p.c.page_log2)) : -1;
+    };
+    float ks_next = 0.0f, vs_next = 0.0f;
+    auto fetch = [&](int i, int page) {
+      if constexpr (kFP8) {
+        const int key = k0 + i * kKeys + key_lane;
+        ks_next = vs_next = 0.0f;
+        if (key < k1 && page >= 0 && page < p.c.num_pages) {
+          const int64_t at = ((static_cast<int64_t>(page) * p.c.heads + h) << p.c.page_log2) +
+                             (key & page_mask);
+          ks_next = __ldg(p.c.k_scales + at);
+          vs_next = __ldg(p.c.v_scales + at);
+        }
+      }
+    };
+    int page_next = page_of(0);
+    // ---- the query, as the B operand of the first product
+    {
+      constexpr int kPieces = D / 8;                     // 16-byte pieces of a row
+      const uint32_t flip = p.scale < 0.0f ? 0x80008000u : 0u;   // the scores' factor is positive
+#pragma unroll 4
+      for (int x0 = 0; x0 < N * kPieces; x0 += 256) {
+        const int x = x0 + tid;
+        if (x0 + (tid & ~31) < N * kPieces) {            // (whole warps)
+          const int r = x / kPieces, c = x % kPieces;
+          uint4 q = make_uint4(0u, 0u, 0u, 0u);
+          if (r < t.rows) {
+            const int rr = t.first_row + r, tok = rr / p.group;
+            q = __ldg(reinterpret_cast<const uint4*>(
+                          p.q + static_cast<int64_t>(t.q0 + tok) * p.q_st +
+                          static_cast<int64_t>(h * p.group + rr - tok * p.group) * p.q_sh) + c);
+            q.x ^= flip;
+            q.y ^= flip;
+            q.z ^= flip;
+            q.w ^= flip;
+          }
+          if constexpr (kFP8) {
+            const uint32_t xw[4] = {q.x, q.y, q.z, q.w};
+            float a = 0.0f;
+#pragma unroll
+            for (int i = 0; i < 4; ++i)
+              a = fmaxf(a, fmaxf(fabsf(__uint_as_float(xw[i] << 16)),
+                                 fabsf(__uint_as_float(xw[i] & 0xffff0000u))));
+#pragma unroll
+            for (int o = 1; o < kPieces; o <<= 1) a = fmaxf(a, __shfl_xor_sync(0xffffffffu, a, o));
+            float mul, inv;
+            row_pow2(a, mul, inv);
+            mul *= 0.5f;                                 // below 2^8: an E4M3 ends at 448
+            if (c == 0)
+              bars.factor[r] = 2.0f * inv * fabsf(p.scale) * (p.softcap > 0.0f ? 1.0f : kLog2e);
+            uint32_t hi[2], lo[2];
+            two_terms(xw, mul, hi, lo);
+            uint8_t* at = smem + S::oQ + code_piece<D>(r, c >> 1) + (c & 1) * 8;
+            *reinterpret_cast<uint2*>(at) = make_uint2(hi[0], hi[1]);
+            *reinterpret_cast<uint2*>(at + S::kQTerm) = make_uint2(lo[0], lo[1]);
+          } else {
+            uint8_t* at = smem + S::oQ + (c >> 3) * (N * 128) + r * 128 + (((c & 7) ^ (r & 7)) << 4);
+            *reinterpret_cast<uint4*>(at) = q;
+          }
+        }
+      }
+      fence_async_smem();
+      mbar_arrive(bar(bars.q_full));
+    }
+    fetch(0, page_next);
+    page_next = page_of(1);
+    bool ok = wait(bar(bars.q_full), 0);                 // (and the other threads' factors)
+    const float ninf = __int_as_float(0xff800000);
+    const float cap = p.softcap, cap_k = cap > 0.0f ? 2.0f * kLog2e / cap : 0.0f;
+    const float sc = fabsf(p.scale) * (cap > 0.0f ? 1.0f : kLog2e);
+    float ref[NH], l[NH];
+    uint32_t pending = 0;                                // rows that have not seen their first key
+    int lo_max = k0, hi_min = k1;
+#pragma unroll
+    for (int r = 0; r < NH; ++r) {
+      ref[r] = 0.0f;
+      l[r] = 0.0f;
+      const int lo = bars.lo[w * NH + r], hi = bars.hi[w * NH + r];
+      if (lo < hi) {
+        pending |= 1u << r;
+        lo_max = max(lo_max, lo);
+      }
+      if (w * NH + r < t.rows) hi_min = min(hi_min, hi);
+    }
+    const uint32_t seeing = pending;
+    const bool idle = w * NH >= t.rows;
+    const int group_bar = 2 + w;
+    int E = 0;                                           // FP8: weights carry vs * 2^(4 - E)
+    const uint32_t o_tm = tmem + lanes + 2 * N + w * NH;
+    constexpr float kFar = kFP8 ? 448.0f : 1.0e18f;
+    // per row over the tile's keys: each thread's x[r] to the maximum over the group
+    auto group_max = [&](float (&x)[NH]) {
+#pragma unroll
+      for (int r = 0; r < NH; ++r) {
+        const int m = __reduce_max_sync(0xffffffffu, ordered(x[r] == x[r] ? x[r] : ninf));
+        if (lane == 0) bars.part[w][warp & 3][r] = unordered(m);
+      }
+      named_bar_sync(group_bar, 128);
+#pragma unroll
+      for (int r = 0; r < NH; ++r)
+        x[r] = fmaxf(fmaxf(bars.part[w][0][r], bars.part[w][1][r]),
+                     fmaxf(bars.part[w][2][r], bars.part[w][3][r]));
+      named_bar_sync(group_bar, 128);
+    };
+    // the exponent of the tile's largest value scale
+    auto group_exponent = [&](float vs) {
+      const uint32_t m = __reduce_max_sync(0xffffffffu, __float_as_uint(vs));
+      if (lane == 0) bars.scale[w][warp & 3] = m;
+      named_bar_sync(group_bar, 128);
+      const uint32_t top = max(max(bars.scale[w][0], bars.scale[w][1]),
+                               max(bars.scale[w][2], bars.scale[w][3]));
+      named_bar_sync(group_bar, 128);
+      return min(max(static_cast<int>((top >> 23) & 255u), 5), 250) - 127;
+    };
+
+    // (A wait that gave up ends the waiting, not the loop: a group's warps still meet at
+    // their barriers, and what they compute is dropped.)
+    for (int i = 0; i < n; ++i) {
+      const int kb = k0 + i * kKeys, key = kb + key_lane;
+      const float ks = ks_next, vs = vs_next;
+      fetch(i + 1, page_next);
+      page_next = page_of(i + 2);
+      if (ok) ok = wait(bar(bars.s_full[i & 1]), (i >> 1) & 1);
+      tc_fence_after();
+      float x[NH];
+      if (!idle) {
+        tmem_ld_cols<NH>(tmem + lanes + (i & 1) * N + w * NH, x);
+#pragma unroll
+        for (int r = 0; r < NH; r += 4) {
+          float4 f = make_float4(sc, sc, sc, sc);
+          if constexpr (kFP8) {
+            f = *reinterpret_cast<const float4*>(&bars.factor[w * NH + r]);
+            mul2(f.x, f.y, f.x, f.y, ks, ks);
+            mul2(f.z, f.w, f.z, f.w, ks, ks);
+          }
+          mul2(x[r], x[r + 1], x[r], x[r + 1], f.x, f.y);
+          mul2(x[r + 2], x[r + 3], x[r + 2], x[r + 3], f.z, f.w);
+        }
+        if (cap > 0.0f) {
+#pragma unroll
+          for (int r = 0; r < NH; ++r) x[r] = soft_capped(x[r], cap_k, cap) * kLog2e;
+        }
+        if (kb < lo_max || kb + kKeys > hi_min) {
+#pragma unroll
+          for (int r = 0; r < NH; ++r)
+            if (key < bars.lo[w * NH + r] || key >= bars.hi[w * NH + r]) x[r] = ninf;
+        }
+        if (pending != 0u) {
+          // rows whose first keys are in this tile take its maximum as their reference
+          uint32_t now = 0;
+#pragma unroll
+          for (int r = 0; r < NH; ++r)
+            if (bars.lo[w * NH + r] < kb + kKeys) now |= 1u << r;
+          now &= pending;
+          if (now != 0u) {
+            float top[NH];
+#pragma unroll
+            for (int r = 0; r < NH; ++r) top[r] = x[r];
+            group_max(top);
+#pragma unroll
+            for (int r = 0; r < NH; ++r)
+              if (now >> r & 1u) ref[r] = top[r] > ninf ? top[r] : 0.0f;
+            // (the first tile has the first keys of some row, or no row of the group sees any)
+            if (kFP8 && pending == seeing) E = group_exponent(vs);
+            pending &= ~now;
+          }
+        }
+        float vw = kFP8 ? vs * exp2_approx(static_cast<float>(4 - E)) : 1.0f;
+        float e[NH];
+        float most = 0.0f;
+#pragma unroll
+        for (int r = 0; r < NH; ++r) {
+          e[r] = exp2_approx(x[r] - ref[r]);
+          most = fmaxf(most, e[r]);
+        }
+        if (named_bar_any(group_bar, 128, most * vw > kFar)) {
+          float top[NH];
+#pragma unroll
+          for (int r = 0; r < NH; ++r) top[r] = x[r];
+          group_max(top);
+          const int E2 = kFP8 ? group_exponent(vs) : 0;
+          if (ok && i > 0) ok = wait(bar(bars.o_step), (i - 1) & 1);
+          tc_fence_after();
+          const float unit = kFP8 ? exp2_approx(static_cast<float>(E - E2)) : 1.0f;
+          float g[NH];
+#pragma unroll
+          for (int r = 0; r < NH; ++r) {
+            const float want = fmaxf(ref[r], top[r]);
+            g[r] = (seeing & ~pending) >> r & 1u ? exp2_approx(ref[r] - want) : 1.0f;
+            if ((seeing & ~pending) >> r & 1u) ref[r] = want;
+            l[r] *= g[r];
+            g[r] *= unit;
+          }
+          E = E2;
+          vw = kFP8 ? vs * exp2_approx(static_cast<float>(4 - E)) : 1.0f;
+          if (i > 0) {
+#pragma unroll
+            for (int term = 0; term < (kFP8 ? 2 : 1); ++term) {
+              float o[NH];
+              tmem_ld_cols<NH>(o_tm + term * N, o);
+              uint32_t u[NH];
+#pragma unroll
+              for (int r = 0; r < NH; ++r) u[r] = __float_as_uint(o[r] * g[r]);
+              tmem_st_cols<NH>(o_tm + term * N, u);
+            }
+            tmem_st_wait();
+          }
+#pragma unroll
+          for (int r = 0; r < NH; ++r) e[r] = exp2_approx(x[r] - ref[r]);
+        }
+#pragma unroll
+        for (int r = 0; r < NH; ++r) {
+          l[r] += e[r];
+          if constexpr (kFP8) e[r] *= vw;
+        }
+#pragma unroll
+        for (int r = 0; r < NH; ++r) x[r] = e[r];
+      }
+      // the last product has read the weights before (that of the tile before it is complete: it
+      // came before these scores)
+      if (ok && i > 0) ok = wait(bar(bars.o_step), (i - 1) & 1);
+      if (!idle) {
+        uint32_t hi[kFP8 ? NH / 4 : NH / 2], lo[kFP8 ? NH / 4 : NH / 2];
+        if constexpr (kFP8) {
+#pragma unroll
+          for (int j = 0; j < NH / 4; ++j) {
+            uint32_t hw = 0, lw = 0;
+#pragma unroll
+            for (int k = 0; k < 2; ++k) {
+              const float a = x[4 * j + 2 * k], c = x[4 * j + 2 * k + 1];
+              const uint16_t hc = cvt_e4m3x2(a, c);
+              uint32_t back = e4m3x2_to_f16x2(hc);
+              __half2 d = __hsub2(__floats2half2_rn(a, c), *reinterpret_cast<__half2*>(&back));
+              d = __hmul2(d, __float2half2_rn(16.0f));
+              uint16_t lc;
+              asm("cvt.rn.satfinite.e4m3x2.f16x2 %0, %1;"
+                  : "=h"(lc)
+                  : "r"(*reinterpret_cast<uint32_t*>(&d)));
+              hw |= static_cast<uint32_t>(hc) << (16 * k);
+              lw |= static_cast<uint32_t>(lc) << (16 * k);
+            }
+            hi[j] = hw;
+            lo[j] = lw;
+          }
+        } else {
+#pragma unroll
+          for (int j = 0; j < NH / 2; ++j) {
+            __nv_bfloat162 hh = __floats2bfloat162_rn(x[2 * j], x[2 * j + 1]);
+            const float2 back = __bfloat1622float2(hh);
+            __nv_bfloat162 ll = __floats2bfloat162_rn(x[2 * j] - back.x, x[2 * j + 1] - back.y);
+            hi[j] = *reinterpret_cast<uint32_t*>(&hh);
+            lo[j] = *reinterpret_cast<uint32_t*>(&ll);
+          }
+        }
+        // [term][chunk of rows][key][16 bytes]
+        constexpr int kWords = (kFP8 ? NH / 4 : NH / 2);           // of this thread, per term
+        const uint32_t at = sbase + S::oP + w * (kWords * 4 / 16) * (kKeys * 16) + key_lane * 16 +
+                            (kWords < 4 ? w * kWords * 4 : 0);
+#pragma unroll
+        for (int term = 0; term < 2; ++term) {
+          const uint32_t* v = term == 0 ? hi : lo;
+          if constexpr (kWords < 4) {
+            asm volatile("st.shared.v2.u32 [%0], {%1, %2};" ::"r"(at + term * S::kPTerm), "r"(v[0]),
+                         "r"(v[1])
+                         : "memory");
+          } else {
+#pragma unroll
+            for (int q = 0; q < kWords / 4; ++q)
+              asm volatile("st.shared.v4.u32 [%0], {%1, %2, %3, %4};" ::"r"(
+                               at + term * S::kPTerm + q * (kKeys * 16)),
+                           "r"(v[4 * q]), "r"(v[4 * q + 1]), "r"(v[4 * q + 2]), "r"(v[4 * q + 3])
+                           : "memory");
+          }
+        }
+        fence_async_smem();
+      }
+      tc_fence_before();
+      mbar_arrive(bar(bars.p_full));
+    }
+    if (ok && n > 0) ok = wait(bar(bars.o_last), 0);
+    tc_fence_after();
+
+    // ---- results: the sums over the keys, then a channel per lane
+    if (!idle) {
+#pragma unroll
+      for (int r = 0; r < NH; ++r) {
+#pragma unroll
+        for (int o = 16; o > 0; o >>= 1) l[r] += __shfl_xor_sync(0xffffffffu, l[r], o);
+        if (lane == 0) bars.part[w][warp & 3][r] = l[r];
+      }
+      named_bar_sync(group_bar, 128);
+      float o[NH];
+#pragma unroll
+      for (int r = 0; r < NH; ++r) o[r] = 0.0f;
+      if (n > 0 && ok) {
+        tmem_ld_cols<NH>(o_tm, o);
+        if constexpr (kFP8) {
+          float o2[NH];
+          tmem_ld_cols<NH>(o_tm + N, o2);
+          const float unit = exp2_approx(static_cast<float>(E - 4));
+#pragma unroll
+          for (int r = 0; r < NH; ++r) o[r] = fmaf(o2[r], 0.0625f, o[r]) * unit;
+        }
+      }
+      const bool split = parts.count > 1;
+      float* dst = p.partial + (static_cast<int64_t>(blockIdx.x) * p.splits + part) *
+                                   partial_floats<D>(p.part_rows);
+#pragma unroll
+      for (int r = 0; r < NH; ++r) {
+        const int row = w * NH + r;
+        if (row >= t.rows) continue;
+        const bool saw = ok && (seeing >> r & 1u);
+        const float sum = saw ? (bars.part[w][0][r] + bars.part[w][1][r]) +
+                                    (bars.part[w][2][r] + bars.part[w][3][r])
+                              : 0.0f;
+        const float rf = saw ? ref[r] : ninf;
+        const float y = saw ? o[r] : 0.0f;
+        if (split) {
+          if (key_lane < D) dst[static_cast<int64_t>(row) * D + key_lane] = y;
+          if (key_lane == 0) {
+            dst[static_cast<int64_t>(p.part_rows) * D + row] = rf;
+            dst[static_cast<int64_t>(p.part_rows) * (D + 1) + row] = sum;
+          }
+        } else {
+          if (key_lane < D)
+            p.out[bars.out[row] + key_lane] =
+                __float2bfloat16_rn(sum == 0.0f ? 0.0f : y * (1.0f / sum));
+          if (key_lane == 0 && p.lse != nullptr) *lse_at(p, t, row) = lse_of(rf, sum);
+        }
+      }
+    }
+    if (parts.count > 1)
+      join_parts<D>(p, t, blockIdx.x, p.part_rows, parts.count, tid, 256, 1, &bars.flag);
+  } else if (warp == 9) {
+    // =================================================================== MMA
+    if (n > 0) {
+      // (everything uniform over the warp: see the 256-row kernel)
+      constexpr uint32_t kFmt = kFP8 ? 0u : 1u;
+      const uint32_t idesc_s = make_idesc(kFmt, 128, N);
+      const uint32_t idesc_o = make_idesc(kFmt, 128, N) | (1u << 15) | (1u << 16);
+      const uint32_t tm = __shfl_sync(0xffffffffu, tmem, 0);
+      const int tiles = __shfl_sync(0xffffffffu, n, 0);
+      // descriptors.  K and Q are K-major; V is MN-major with its channels in groups of one
+      // swizzled row (where D = 64 fills half of the 128, a group stride of 0 repeats them);
+      // the weights are MN-major without swizzle, [chunk of rows][8 keys][16 bytes].
+      constexpr uint32_t kTileHi = kFP8 ? kCodeDescHi<D> : kDescHi;
+      constexpr uint32_t kPHi = ((kKeys * 16) >> 4) | (1u << 14);
+      const uint32_t k_lo = smem_desc_lo(sbase + S::oSlots);
+      const uint32_t v_lo = ((sbase + S::oSlots) >> 4) |
+                            ((D == 128 && !kFP8 ? (kHalfBytes >> 4) : 0u) << 16);
+      const uint32_t q_lo = smem_desc_lo(sbase + S::oQ);
+      const uint32_t p_lo = ((sbase + S::oP) >> 4) | ((128u >> 4) << 16);
+      constexpr int kStepKeys = kFP8 ? 32 : 16;          // keys per MMA of the second product
+      constexpr int kSteps = kKeys / kStepKeys;
+      constexpr uint32_t kVStep = (kStepKeys * (kFP8 ? D : 128)) >> 4;
+      constexpr uint32_t kPStep = (kStepKeys * 16) >> 4;
+      const int first_key = max(t.lo, k0);
+      const int first_step = max(0, first_key - k0) / kStepKeys;
+      const int last_steps = (k1 - (k0 + (n - 1) * kKeys) + kStepKeys - 1) / kStepKeys;
+      int slot = 0;
+      uint32_t parity = 0;
+      auto release = [&]() {
+        if (elect_one()) umma_commit(bar(bars.empty[0]) + 8 * slot);
+        if (++slot == S::kSlots) {
+          slot = 0;
+          parity ^= 1;
+        }
+      };
+      auto wait_tile = [&]() { return wait(bar(bars.full[0]) + 8 * slot, parity); };
+      auto scores = [&](int buf) {
+        const uint32_t a = k_lo + slot * (S::kTileBytes >> 4);
+        tc_fence_after();
+        if (elect_one()) {
+          if constexpr (kFP8) {
+#pragma unroll
+            for (int s = 0; s < 2 * (D / 32); ++s) {     // the query's hi, then lo
+              const uint32_t off = ((s % (D / 32)) * 32) >> 4;
+              umma_ss<true>(tm + buf * N, a + off, kTileHi,
+                            q_lo + (s / (D / 32)) * (S::kQTerm >> 4) + off, kTileHi, idesc_s,
+                            s > 0);
+            }
+          } else {
+#pragma unroll
+            for (int s = 0; s < D / 16; ++s) {
+              const uint32_t in = ((s & 3) * 32) >> 4;
+              umma_ss<false>(tm + buf * N, a + (((s >> 2) * kHalfBytes) >> 4) + in, kTileHi,
+                             q_lo + (((s >> 2) * N * 128) >> 4) + in, kTileHi, idesc_s, s > 0);
+            }
+          }
+          umma_commit(bar(bars.s_full[0]) + 8 * buf);
+        }
+        release();
+      };
+      auto values = [&](int i) {
+        const uint32_t a = v_lo + slot * (S::kTileBytes >> 4);
+        const bool first = i == 0;
+        const int s0 = first ? first_step : 0, s1 = i + 1 == tiles ? last_steps : kSteps;
+        tc_fence_after();
+        if (elect_one()) {
+          if (s0 == 0 && s1 == kSteps) {
+#pragma unroll
+            for (int x = 0; x < 2 * kSteps; ++x) {       // the weights' hi, then lo
+              const int s = x % kSteps, term = x / kSteps;
+              umma_ss<kFP8>(tm + 2 * N + (kFP8 ? term * N : 0), a + s * kVStep, kTileHi,
+                            p_lo + term * (S::kPTerm >> 4) + s * kPStep, kPHi, idesc_o,
+                            (kFP8 ? s > 0 : x > 0) ? 1u : (first ? 0u : 1u));
+            }
+          } else {
+            for (int term = 0; term < 2; ++term)
+              for (int s = s0; s < s1; ++s)
+                umma_ss<kFP8>(tm + 2 * N + (kFP8 ? term * N : 0), a + s * kVStep, kTileHi,
+                              p_lo + term * (S::kPTerm >> 4) + s * kPStep, kPHi, idesc_o,
+                              (s > s0 || (!kFP8 && term > 0)) ? 1u : (first ? 0u : 1u));
+          }
+        }
+        release();
+      };
+      // rows of V in those steps that no row sees
+      auto clean = [&](int i) {
+        if (i > 0 && i + 1 < tiles) return;
+        const int kb = k0 + i * kKeys;
+        const int lo = max(0, first_key - kb), hi = k1 - kb;
+        if (lo % kStepKeys != 0 || (hi < kKeys && hi % kStepKeys != 0)) {
+          const uint32_t base = sbase + S::oSlots + slot * S::kTileBytes;
+          auto zero = [&](int r0, int r1) {
+            constexpr int kRowPieces = S::kTileBytes / kKeys / 16;
+            for (int y = lane; y < (r1 - r0) * kRowPieces; y += 32) {
+              const int r = r0 + y / kRowPieces, c = y % kRowPieces;
+              const uint32_t at = base + (kFP8 ? r * D + c * 16
+                                               : (c >> 3) * kHalfBytes + r * 128 + (c & 7) * 16);
+              asm volatile("st.shared.v4.u32 [%0], {%1, %1, %1, %1};" ::"r"(at), "r"(0) : "memory");
+            }
+          };
+          zero(lo / kStepKeys * kStepKeys, lo);
+          if (hi < kKeys) zero(hi, min(kKeys, (hi + kStepKeys - 1) / kStepKeys * kStepKeys));
+          fence_async_smem();
+          __syncwarp();
+        }
+      };
+      bool ok = wait(bar(bars.q_full), 0);
+      for (int i = 0; i < 2 && i < tiles && ok; ++i) {
+        ok = wait_tile();
+        if (ok) scores(i);
+      }
+      for (int i = 0; i < tiles && ok; ++i) {
+        ok = wait_tile() && wait(bar(bars.p_full), i & 1);
+        if (!ok) break;
+        clean(i);
+        values(i);
+        // o_step: a phase for every product; o_last: the last one
+        if (elect_one()) umma_commit(bar(bars.o_step));
+        if (i + 1 == tiles && elect_one()) umma_commit(bar(bars.o_last));
+        if (i + 2 < tiles) {
+          ok = wait_tile();
+          if (ok) scores(i & 1);
+        }
+      }
+      if (!ok) {                           // products in flight end before the memory goes
+        if (elect_one()) umma_commit(bar(bars.drain));
+        __syncwarp();
+        mbar_wait_drain(bar(bars.drain), 0, p.timeout_ns);
+      }
+    }
+  } else {
+    // =================================================================== TMA loads
+    const int box = min(1 << p.c.page_log2, kKeys);
+    const int segs = kKeys / box;
+    const uint64_t policy = p.row_tiles > 1 ? policy_evict_last() : policy_evict_first();
+    constexpr int kRowBytes = kFP8 ? D : 2 * D;
+    bool ok = p.drop_producer == 0;
+    if (lane == 0) {
+      tma_prefetch_desc(&map_k);
+      tma_prefetch_desc(&map_v);
+    }
+    int f = 0;
+    for (; f < 2 * n && ok; ++f) {
+      const Item it = item_at(f, n, 2);
+      const int kb = k0 + it.i * kKeys;
+      const int key = kb + lane * box;
+      const bool mine = lane < segs && key < k1;
+      int page = mine ? __ldg(table + (key >> p.c.page_log2)) : 0;
+      if (page < 0 || page >= p.c.num_pages) {
+        set_error(p.ctrl, MOE_ERR_DEVICE_FAULT, 22);
+        page = 0;                          // (a place that exists)
+      }
+      const int slot = f % S::kSlots;
+      ok = wait(bar(bars.empty[slot]), ((f / S::kSlots) & 1) ^ 1);
+      if (!ok) break;
+      const uint32_t full = bar(bars.full[slot]);
+      if (lane == 0) {
+        const int loaded = min(segs, (k1 - kb + box - 1) / box);
+        mbar_arrive_expect_tx(full, loaded * box * kRowBytes);
+      }
+      __syncwarp();
+      if (mine) {
+        const int row = ((page * p.c.heads + h) << p.c.page_log2) +
+                        (key & ((1 << p.c.page_log2) - 1));
+        const CUtensorMap* map = it.v ? &map_v : &map_k;
+        const uint32_t dst = sbase + S::oSlots + slot * S::kTileBytes;
+        if constexpr (kFP8) {
+          tma_load_2d(dst + lane * box * D, map, full, 0, row, policy);
+        } else {
+#pragma unroll
+          for (int x = 0; x < D / 64; ++x)
+            tma_load_2d(dst + x * kHalfBytes + lane * box * 128, map, full, x * 64, row, policy);
+        }
+      }
+      __syncwarp();
+    }
+    if (!ok)                               // copies in flight land before the memory goes
+      for (int g = max(0, f - S::kSlots); g < f; ++g)
+        mbar_wait_drain(bar(bars.full[g % S::kSlots]), (g / S::kSlots) & 1, p.timeout_ns);
+  }
+  tc_fence_before();
+  __syncthreads();
+  if (warp == 9) tmem_dealloc(tmem, S::kTmem);
+}
+
+template <int D, bool kFP8, int N>
+cudaError_t launch_n(const AttnParams& p, const CUtensorMap& mk, const CUtensorMap& mv,
+                     cudaStream_t stream) {
+  using S = RowsShape<D, kFP8, N>;
+  cudaError_t e = cudaFuncSetAttribute(rows_kernel<D, kFP8, N>,
+                                       cudaFuncAttributeMaxDynamicSharedMemorySize, S::kSmem);
+  if (e != cudaSuccess) return e;
+  const dim3 grid(static_cast<unsigned>(p.B) * p.c.heads * p.row_tiles, p.splits);
+  rows_kernel<D, kFP8, N><<<grid, S::kThreads, S::kSmem, stream>>>(mk, mv, p);
+  return cudaGetLastError();
+}
+
+template <int D, bool kFP8>
+cudaError_t launch_d(const AttnParams& p, int tile_rows, const CUtensorMap& mk,
+                     const CUtensorMap& mv, cudaStream_t stream) {
+  if (tile_rows == 16) return launch_n<D, kFP8, 16>(p, mk, mv, stream);
+  if (tile_rows == 32) return launch_n<D, kFP8, 32>(p, mk, mv, stream);
+  return launch_n<D, kFP8, 64>(p, mk, mv, stream);
+}
+
+}  // namespace
+
+cudaError_t launch_attention_rows(const AttnParams& p, int tile_rows, int head_dim, bool fp8,
+                                  cudaStream_t stream) {
+  CUtensorMap mk, mv;
+  if (!cache_maps(p, head_dim, fp8, &mk, &mv)) return cudaErrorInvalidValue;
+  if (fp8)
+    return head_dim == 128 ? launch_d<128, true>(p, tile_rows, mk, mv, stream)
+                           : launch_d<64, true>(p, tile_rows, mk, mv, stream);
+  return head_dim == 128 ? launch_d<128, false>(p, tile_rows, mk, mv, stream)
+                         : launch_d<64, false>(p, tile_rows, mk, mv, stream);
+}
+
+}  // namespace moe

@@ -155,10 +155,8 @@ moe_status_t moe_paged_attention(const moe_attention_args* a, void* ws, size_t w
   p.timeout_ns = wait_limit_ns();
   p.drop_producer = loads_dropped() ? 1 : 0;
 
-  // Few rows per cache head: 16-row tiles, bound by HBM.  More: 256-row tiles on
-  // the tensor cores.
-  const bool few = rows <= kDecodeRows;
-  const int tile_rows = few ? kDecodeRows : kTileRows;
+  const bool few = rows <= 128;
+  const int tile_rows = !few ? kTileRows : rows <= 16 ? 16 : rows <= 32 ? 32 : 64;
   p.row_tiles = static_cast<int>((rows + tile_rows - 1) / tile_rows);
   const long long tiles = static_cast<long long>(a->B) * p.c.heads * p.row_tiles;
   if (tiles > 0x7fffffffll) return MOE_ERR_UNSUPPORTED;
@@ -170,7 +168,7 @@ moe_status_t moe_paged_attention(const moe_attention_args* a, void* ws, size_t w
   // Parts of at least 256 keys.  Few rows: until there are about four for every
   // place that an SM has for a CTA.  Many rows: as many as fit the SMs at once.
   const long long most = (span + 255) / 256;
-  long long splits = few ? 8ll * sms / tiles : sms / tiles;
+  long long splits = few ? 4ll * sms / tiles : sms / tiles;
   if (splits > most) splits = most;
   const long long part_bytes = static_cast<long long>(p.part_rows) * (D + 2) * 4;
   const long long fit =
@@ -183,7 +181,7 @@ moe_status_t moe_paged_attention(const moe_attention_args* a, void* ws, size_t w
   p.chunk = splits > 1 ? static_cast<int>(((span + splits - 1) / splits + 127) / 128 * 128)
                        : 0x40000000;
   const cudaStream_t st = static_cast<cudaStream_t>(stream);
-  return cuda_status(few ? launch_attention_decode(p, D, fp8, st)
+  return cuda_status(few ? launch_attention_rows(p, tile_rows, D, fp8, st)
                          : launch_attention_tiles(p, D, fp8, st));
 }
 

@@ -64,6 +64,9 @@ cudaError_t launch_kv_read(const KvCacheView& c, int head_dim, bool fp8, const i
 constexpr int kDecodeRows = 16;
 cudaError_t launch_attention_decode(const AttnParams& p, int head_dim, bool fp8,
                                     cudaStream_t stream);
+// Up to 16, 32 or 64 rows per tile (tile_rows), tcgen05 with keys and channels as the rows.
+cudaError_t launch_attention_rows(const AttnParams& p, int tile_rows, int head_dim, bool fp8,
+                                  cudaStream_t stream);
 // Up to 256 rows per tile, tcgen05.
 constexpr int kTileRows = 256;
 constexpr int kTileKeys = 128;
