@@ -20,9 +20,9 @@
 // largest), so V is never rewritten.  BF16 caches split the weights in two bf16 terms.
 // Nothing but the output is then rounded to fewer bits than the cache has.
 //
-// Warps 0-3 and 4-7 are two softmax groups, each with half of the rows of every
-// key tile (a thread per key); warp 8 loads, warp 9 issues the MMAs.  Scores are
-// double-buffered in tensor memory.  Up to 32 rows two CTAs share an SM.
+// Groups of four warps share the rows of every key tile (a thread per key, 8 or 16 rows
+// each); then one warp loads and one issues the MMAs.  Scores are double-buffered in
+// tensor memory.  Up to 32 rows two CTAs share an SM.
 #include <cstring>
 
 #include "attention_tc.cuh"
@@ -32,29 +32,29 @@ namespace {
 
 template <int D, bool kFP8, int N>
 struct RowsShape {
-  static constexpr int kThreads = 320;
+  static constexpr int kGroups = N == 16 ? 2 : N / 16;   // of softmax warps
+  static constexpr int kSoftmax = kGroups * 128;
+  static constexpr int kThreads = kSoftmax + 64;
   static constexpr int kTileBytes = kKeys * D * (kFP8 ? 1 : 2);
   static constexpr int kQTerm = N * D * (kFP8 ? 1 : 2);  // bytes of the query (of each term)
   static constexpr int kChunkRows = kFP8 ? 16 : 8;       // rows in 16 bytes of weights
   static constexpr int kPTerm = N / kChunkRows * kKeys * 16;
-  static constexpr int oSlotsMin = ((kFP8 ? 2 : 1) * kQTerm + 2 * kPTerm + 1023) / 1024 * 1024;
-  // two CTAs per SM where each still has three tiles in shared memory (and 100 registers
-  // hold the rows of a thread)
-  static constexpr int kHalf = 112 * 1024, kWhole = 224 * 1024;
-  static constexpr int kCtas = N <= 32 && (kHalf - oSlotsMin) / kTileBytes >= 3 ? 2 : 1;
-  static constexpr int kFit = ((kCtas == 2 ? kHalf : kWhole) - oSlotsMin) / kTileBytes;
-  static constexpr int kSlots = kFit > 8 ? 8 : kFit;
   // offsets in shared memory: weights (hi, lo), query (FP8: hi, lo), the ring
   static constexpr int oP = 0;
   static constexpr int oQ = 2 * kPTerm;
-  static constexpr int oSlots = oSlotsMin;
+  static constexpr int oSlots = (oQ + (kFP8 ? 2 : 1) * kQTerm + 1023) / 1024 * 1024;
+  // two CTAs per SM where each still has three tiles in shared memory
+  static constexpr int kHalf = 111 * 1024, kWhole = 222 * 1024;
+  static constexpr int kCtas = N <= 32 && (kHalf - oSlots) / kTileBytes >= 3 ? 2 : 1;
+  static constexpr int kFit = ((kCtas == 2 ? kHalf : kWhole) - oSlots) / kTileBytes;
+  static constexpr int kSlots = kFit > 8 ? 8 : kFit;
   static constexpr int kSmem = oSlots + kSlots * kTileBytes;
-  static constexpr int kTmem = 4 * N;                    // S twice, O (FP8: hi and lo)
+  static constexpr int kTmem = N == 48 ? 256 : 4 * N;    // S twice, O (FP8: hi and lo)
   static_assert(kSlots >= 3, "two tiles of keys and one of values");
   static_assert(oQ % 1024 == 0, "swizzled tiles start on 1024 bytes");
 };
 
-template <int N>
+template <int N, int kGroups>
 struct RowsBars {
   uint64_t full[8], empty[8];
   uint64_t q_full, s_full[2], p_full, o_step, o_last, drain;
@@ -62,9 +62,10 @@ struct RowsBars {
   int abort, flag;
   int lo[N], hi[N];               // keys that each row sees, in this part
   alignas(16) float factor[N];    // FP8: of the row's scores
-  int64_t out[N];                 // the row's place in out
-  float part[2][4][N / 2];        // per group and warp: maxima or sums of its rows
-  uint32_t scale[2][4];           // per group and warp: largest value scale (bits)
+  int64_t q[N], out[N];           // the row's place in q and out
+  alignas(16) float part[kGroups][4][N / kGroups];   // per group and warp: maxima or sums
+  alignas(16) float scale[N];     // of the row's sums at the end
+  uint32_t vs[kGroups][4];        // per group and warp: largest value scale (bits)
 };
 
 // D[tmem] (+)= A[smem] * B[smem], any layouts (both descriptors' words given).
@@ -115,70 +116,97 @@ __device__ __forceinline__ void tmem_st_cols(uint32_t at, const uint32_t* r) {
   }
 }
 
-// A binary32 value as an integer of the same order, and back.
-__device__ __forceinline__ int ordered(float x) {
-  const int b = __float_as_int(x);
-  return b < 0 ? b ^ 0x7fffffff : b;
-}
-__device__ __forceinline__ float unordered(int b) {
-  return __int_as_float(b < 0 ? b ^ 0x7fffffff : b);
+// Reduces NH values per lane over the 32 lanes, halving the values with the
+// lanes: lane i returns the result of value i / (32 / NH).  x is overwritten.
+template <int NH, typename F>
+__device__ __forceinline__ float transposed(float (&x)[NH], F op) {
+  const int lane = threadIdx.x & 31;
+  int o = 16;
+#pragma unroll
+  for (int n = NH; n > 1; n /= 2, o /= 2) {
+    const bool up = (lane & o) != 0;
+#pragma unroll
+    for (int k = 0; k < n / 2; ++k) {
+      const float give = up ? x[k] : x[k + n / 2], keep = up ? x[k + n / 2] : x[k];
+      x[k] = op(keep, __shfl_xor_sync(0xffffffffu, give, o));
+    }
+  }
+#pragma unroll
+  for (; o > 0; o /= 2) x[0] = op(x[0], __shfl_xor_sync(0xffffffffu, x[0], o));
+  return x[0];
 }
 
 template <int D, bool kFP8, int N>
-__global__ void __launch_bounds__(320, RowsShape<D, kFP8, N>::kCtas)
+__global__ void
+    __launch_bounds__(RowsShape<D, kFP8, N>::kThreads, RowsShape<D, kFP8, N>::kCtas)
     rows_kernel(const __grid_constant__ CUtensorMap map_k,
                 const __grid_constant__ CUtensorMap map_v, const AttnParams p) {
   using S = RowsShape<D, kFP8, N>;
-  constexpr int NH = N / 2;                       // rows of a group
+  constexpr int NH = N / S::kGroups;              // rows of a group
+  constexpr int kLoadWarp = S::kSoftmax / 32, kMmaWarp = kLoadWarp + 1;
   extern __shared__ __align__(1024) uint8_t smem[];
-  __shared__ RowsBars<N> bars;
+  __shared__ RowsBars<N, S::kGroups> bars;
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
 
-  const int rt = static_cast<int>(blockIdx.x % p.row_tiles);
-  const int bh = static_cast<int>(blockIdx.x / p.row_tiles);
-  const int b = bh / p.c.heads, h = bh - b * p.c.heads;
-  const int part = blockIdx.y;
-  const TileView t = tile_view(p, b, h, rt, N, part == 0 && rt == 0 && tid == 0);
-  if (t.rows == 0) return;
-  const Parts parts = tile_parts(p, t, kKeys);
-  if (part >= max(1, parts.count)) return;
-  const int k0 = parts.base + part * p.chunk;
-  const int k1 = parts.count == 0 ? k0 : (part + 1 >= parts.count ? t.hi : k0 + p.chunk);
-  const int n = (k1 - k0 + kKeys - 1) / kKeys;    // key tiles
-
+  // ---- what needs no input: barriers, tensor memory
   auto bar = [&](const uint64_t& x) { return smem_u32(&x); };
   if (tid == 0) {
     for (int i = 0; i < S::kSlots; ++i) {
       mbar_init(bar(bars.full[i]), 1);
       mbar_init(bar(bars.empty[i]), 1);
     }
-    mbar_init(bar(bars.q_full), 256);
+    mbar_init(bar(bars.q_full), S::kSoftmax);
     mbar_init(bar(bars.s_full[0]), 1);
     mbar_init(bar(bars.s_full[1]), 1);
-    mbar_init(bar(bars.p_full), 256);
+    mbar_init(bar(bars.p_full), S::kSoftmax);
     mbar_init(bar(bars.o_step), 1);
     mbar_init(bar(bars.o_last), 1);
     mbar_init(bar(bars.drain), 1);
     bars.abort = 0;
     mbar_fence_init();
   }
-  if (warp == 9) {
+  if (warp == kMmaWarp) {
     tmem_alloc(smem_u32(&bars.tmem), S::kTmem);
     tmem_relinquish();
   }
+  if (tid == kLoadWarp * 32) {
+    tma_prefetch_desc(&map_k);
+    tma_prefetch_desc(&map_v);
+  }
+  pdl_wait();
+  pdl_launch_dependents();
+
+  const int rt = static_cast<int>(blockIdx.x % p.row_tiles);
+  const int bh = static_cast<int>(blockIdx.x / p.row_tiles);
+  const int b = bh / p.c.heads, h = bh - b * p.c.heads;
+  const int part = blockIdx.y;
+  const TileView t = tile_view(p, b, h, rt, N, part == 0 && rt == 0 && tid == 0);
+  const Parts parts = tile_parts(p, t, kKeys);
+  if (t.rows == 0 || part >= max(1, parts.count)) {      // nothing to do here
+    if (warp == kMmaWarp) {
+      const uint32_t at = *reinterpret_cast<volatile uint32_t*>(&bars.tmem);
+      tmem_dealloc(at, S::kTmem);
+    }
+    return;
+  }
+  const int k0 = parts.base + part * p.chunk;
+  const int k1 = parts.count == 0 ? k0 : (part + 1 >= parts.count ? t.hi : k0 + p.chunk);
+  const int n = (k1 - k0 + kKeys - 1) / kKeys;    // key tiles
   if (tid < N) {                                  // the rows' places and keys
     int lo = 0, hi = 0;
-    int64_t at = 0;
+    int64_t in = -1, out = 0;
     if (tid < t.rows) {
       const int rr = t.first_row + tid, tok = rr / p.group;
+      const int64_t head = h * p.group + rr - tok * p.group;
       lo = max(k0, row_lo(p, t, tok));
       hi = min(k1, row_hi(p, t, tok));
-      at = static_cast<int64_t>(t.q0 + tok) * p.o_st +
-           static_cast<int64_t>(h * p.group + rr - tok * p.group) * p.o_sh;
+      in = static_cast<int64_t>(t.q0 + tok) * p.q_st + head * p.q_sh;
+      out = static_cast<int64_t>(t.q0 + tok) * p.o_st + head * p.o_sh;
     }
     bars.lo[tid] = lo;
     bars.hi[tid] = hi;
-    bars.out[tid] = at;
+    bars.q[tid] = in;
+    bars.out[tid] = out;
   }
   tc_fence_before();
   __syncthreads();
@@ -196,7 +224,7 @@ __global__ void __launch_bounds__(320, RowsShape<D, kFP8, N>::kCtas)
   };
   const int32_t* table = p.table + static_cast<int64_t>(b) * p.table_stride;
 
-  if (warp < 8) {
+  if (warp < kLoadWarp) {
     // =================================================================== softmax
     const int w = warp >> 2;
     const int key_lane = (warp & 3) * 32 + lane;         // key of a tile; channel of O
@@ -225,17 +253,14 @@ __global__ void __launch_bounds__(320, RowsShape<D, kFP8, N>::kCtas)
     {
       constexpr int kPieces = D / 8;                     // 16-byte pieces of a row
       const uint32_t flip = p.scale < 0.0f ? 0x80008000u : 0u;   // the scores' factor is positive
-#pragma unroll 4
-      for (int x0 = 0; x0 < N * kPieces; x0 += 256) {
+#pragma unroll
+      for (int x0 = 0; x0 < N * kPieces; x0 += S::kSoftmax) {
         const int x = x0 + tid;
         if (x0 + (tid & ~31) < N * kPieces) {            // (whole warps)
           const int r = x / kPieces, c = x % kPieces;
           uint4 q = make_uint4(0u, 0u, 0u, 0u);
-          if (r < t.rows) {
-            const int rr = t.first_row + r, tok = rr / p.group;
-            q = __ldg(reinterpret_cast<const uint4*>(
-                          p.q + static_cast<int64_t>(t.q0 + tok) * p.q_st +
-                          static_cast<int64_t>(h * p.group + rr - tok * p.group) * p.q_sh) + c);
+          if (bars.q[r] >= 0) {
+            q = __ldg(reinterpret_cast<const uint4*>(p.q + bars.q[r]) + c);
             q.x ^= flip;
             q.y ^= flip;
             q.z ^= flip;
@@ -295,13 +320,11 @@ __global__ void __launch_bounds__(320, RowsShape<D, kFP8, N>::kCtas)
     int E = 0;                                           // FP8: weights carry vs * 2^(4 - E)
     const uint32_t o_tm = tmem + lanes + 2 * N + w * NH;
     constexpr float kFar = kFP8 ? 448.0f : 1.0e18f;
-    // per row over the tile's keys: each thread's x[r] to the maximum over the group
+    // Per row over the tile's keys: each thread's x[r] to the maximum over the group.  (A NaN
+    // is no maximum: fmaxf passes over it.)
     auto group_max = [&](float (&x)[NH]) {
-#pragma unroll
-      for (int r = 0; r < NH; ++r) {
-        const int m = __reduce_max_sync(0xffffffffu, ordered(x[r] == x[r] ? x[r] : ninf));
-        if (lane == 0) bars.part[w][warp & 3][r] = unordered(m);
-      }
+      const float m = transposed<NH>(x, [](float a, float c) { return fmaxf(a, c); });
+      if ((lane & (32 / NH - 1)) == 0) bars.part[w][warp & 3][lane / (32 / NH)] = m;
       named_bar_sync(group_bar, 128);
 #pragma unroll
       for (int r = 0; r < NH; ++r)
@@ -312,10 +335,9 @@ __global__ void __launch_bounds__(320, RowsShape<D, kFP8, N>::kCtas)
     // the exponent of the tile's largest value scale
     auto group_exponent = [&](float vs) {
       const uint32_t m = __reduce_max_sync(0xffffffffu, __float_as_uint(vs));
-      if (lane == 0) bars.scale[w][warp & 3] = m;
+      if (lane == 0) bars.vs[w][warp & 3] = m;
       named_bar_sync(group_bar, 128);
-      const uint32_t top = max(max(bars.scale[w][0], bars.scale[w][1]),
-                               max(bars.scale[w][2], bars.scale[w][3]));
+      const uint32_t top = max(max(bars.vs[w][0], bars.vs[w][1]), max(bars.vs[w][2], bars.vs[w][3]));
       named_bar_sync(group_bar, 128);
       return min(max(static_cast<int>((top >> 23) & 255u), 5), 250) - 127;
     };
@@ -461,7 +483,7 @@ __global__ void __launch_bounds__(320, RowsShape<D, kFP8, N>::kCtas)
         }
         // [term][chunk of rows][key][16 bytes]
         constexpr int kWords = (kFP8 ? NH / 4 : NH / 2);           // of this thread, per term
-        const uint32_t at = sbase + S::oP + w * (kWords * 4 / 16) * (kKeys * 16) + key_lane * 16 +
+        const uint32_t at = sbase + S::oP + w * NH / S::kChunkRows * (kKeys * 16) + key_lane * 16 +
                             (kWords < 4 ? w * kWords * 4 : 0);
 #pragma unroll
         for (int term = 0; term < 2; ++term) {
@@ -488,57 +510,64 @@ __global__ void __launch_bounds__(320, RowsShape<D, kFP8, N>::kCtas)
     tc_fence_after();
 
     // ---- results: the sums over the keys, then a channel per lane
+    const bool split = parts.count > 1;
+    float* dst = p.partial + (static_cast<int64_t>(blockIdx.x) * p.splits + part) *
+                                 partial_floats<D>(p.part_rows);
     if (!idle) {
-#pragma unroll
-      for (int r = 0; r < NH; ++r) {
-#pragma unroll
-        for (int o = 16; o > 0; o >>= 1) l[r] += __shfl_xor_sync(0xffffffffu, l[r], o);
-        if (lane == 0) bars.part[w][warp & 3][r] = l[r];
-      }
-      named_bar_sync(group_bar, 128);
       float o[NH];
 #pragma unroll
       for (int r = 0; r < NH; ++r) o[r] = 0.0f;
+      float unit = 1.0f;
       if (n > 0 && ok) {
         tmem_ld_cols<NH>(o_tm, o);
         if constexpr (kFP8) {
           float o2[NH];
           tmem_ld_cols<NH>(o_tm + N, o2);
-          const float unit = exp2_approx(static_cast<float>(E - 4));
+          unit = exp2_approx(static_cast<float>(E - 4));
 #pragma unroll
-          for (int r = 0; r < NH; ++r) o[r] = fmaf(o2[r], 0.0625f, o[r]) * unit;
+          for (int r = 0; r < NH; ++r) o[r] = fmaf(o2[r], 0.0625f, o[r]);
         }
       }
-      const bool split = parts.count > 1;
-      float* dst = p.partial + (static_cast<int64_t>(blockIdx.x) * p.splits + part) *
-                                   partial_floats<D>(p.part_rows);
+      const float sum = transposed<NH>(l, [](float a, float c) { return a + c; });
+      if ((lane & (32 / NH - 1)) == 0) bars.part[w][warp & 3][lane / (32 / NH)] = sum;
+      float mine = 0.0f;                                 // the reference of row key_lane
 #pragma unroll
-      for (int r = 0; r < NH; ++r) {
-        const int row = w * NH + r;
-        if (row >= t.rows) continue;
-        const bool saw = ok && (seeing >> r & 1u);
-        const float sum = saw ? (bars.part[w][0][r] + bars.part[w][1][r]) +
-                                    (bars.part[w][2][r] + bars.part[w][3][r])
+      for (int r = 0; r < NH; ++r) mine = key_lane == r ? ref[r] : mine;
+      named_bar_sync(group_bar, 128);
+      if (key_lane < NH) {
+        const int row = w * NH + key_lane;
+        const bool saw = ok && (seeing >> key_lane & 1u);
+        const float all = saw ? (bars.part[w][0][key_lane] + bars.part[w][1][key_lane]) +
+                                    (bars.part[w][2][key_lane] + bars.part[w][3][key_lane])
                               : 0.0f;
-        const float rf = saw ? ref[r] : ninf;
-        const float y = saw ? o[r] : 0.0f;
-        if (split) {
-          if (key_lane < D) dst[static_cast<int64_t>(row) * D + key_lane] = y;
-          if (key_lane == 0) {
+        const float rf = saw ? mine : ninf;
+        bars.scale[row] = !saw ? 0.0f : split ? unit : all == 0.0f ? 0.0f : unit / all;
+        if (row < t.rows) {
+          if (split) {
             dst[static_cast<int64_t>(p.part_rows) * D + row] = rf;
-            dst[static_cast<int64_t>(p.part_rows) * (D + 1) + row] = sum;
+            dst[static_cast<int64_t>(p.part_rows) * (D + 1) + row] = all;
+          } else if (p.lse != nullptr) {
+            *lse_at(p, t, row) = lse_of(rf, all);
           }
-        } else {
-          if (key_lane < D)
-            p.out[bars.out[row] + key_lane] =
-                __float2bfloat16_rn(sum == 0.0f ? 0.0f : y * (1.0f / sum));
-          if (key_lane == 0 && p.lse != nullptr) *lse_at(p, t, row) = lse_of(rf, sum);
+        }
+      }
+      named_bar_sync(group_bar, 128);
+      if (key_lane < D) {
+#pragma unroll
+        for (int r = 0; r < NH; ++r) {
+          const int row = w * NH + r;
+          if (row < t.rows) {
+            const float g = bars.scale[row];
+            const float y = g == 0.0f ? 0.0f : o[r] * g;
+            if (split) dst[static_cast<int64_t>(row) * D + key_lane] = y;
+            else p.out[bars.out[row] + key_lane] = __float2bfloat16_rn(y);
+          }
         }
       }
     }
-    if (parts.count > 1)
-      join_parts<D>(p, t, blockIdx.x, p.part_rows, parts.count, tid, 256, 1, &bars.flag);
-  } else if (warp == 9) {
+    if (split)
+      join_parts<D>(p, t, blockIdx.x, p.part_rows, parts.count, tid, S::kSoftmax, 1, &bars.flag);
+  } else if (warp == kMmaWarp) {
     // =================================================================== MMA
     if (n > 0) {
       // (everything uniform over the warp: see the 256-row kernel)
@@ -675,10 +704,6 @@ __global__ void __launch_bounds__(320, RowsShape<D, kFP8, N>::kCtas)
     const uint64_t policy = p.row_tiles > 1 ? policy_evict_last() : policy_evict_first();
     constexpr int kRowBytes = kFP8 ? D : 2 * D;
     bool ok = p.drop_producer == 0;
-    if (lane == 0) {
-      tma_prefetch_desc(&map_k);
-      tma_prefetch_desc(&map_v);
-    }
     int f = 0;
     for (; f < 2 * n && ok; ++f) {
       const Item it = item_at(f, n, 2);
@@ -720,7 +745,7 @@ __global__ void __launch_bounds__(320, RowsShape<D, kFP8, N>::kCtas)
   }
   tc_fence_before();
   __syncthreads();
-  if (warp == 9) tmem_dealloc(tmem, S::kTmem);
+  if (warp == kMmaWarp) tmem_dealloc(tmem, S::kTmem);
 }
 
 template <int D, bool kFP8, int N>
@@ -730,9 +755,12 @@ cudaError_t launch_n(const AttnParams& p, const CUtensorMap& mk, const CUtensorM
   cudaError_t e = cudaFuncSetAttribute(rows_kernel<D, kFP8, N>,
                                        cudaFuncAttributeMaxDynamicSharedMemorySize, S::kSmem);
   if (e != cudaSuccess) return e;
-  const dim3 grid(static_cast<unsigned>(p.B) * p.c.heads * p.row_tiles, p.splits);
-  rows_kernel<D, kFP8, N><<<grid, S::kThreads, S::kSmem, stream>>>(mk, mv, p);
-  return cudaGetLastError();
+  cudaLaunchAttribute attr[1];
+  cudaLaunchConfig_t cfg =
+      make_cfg(dim3(static_cast<unsigned>(p.B) * p.c.heads * p.row_tiles, p.splits),
+               dim3(S::kThreads), stream, true, attr);
+  cfg.dynamicSmemBytes = S::kSmem;
+  return cudaLaunchKernelEx(&cfg, rows_kernel<D, kFP8, N>, mk, mv, p);
 }
 
 template <int D, bool kFP8>
@@ -740,6 +768,7 @@ cudaError_t launch_d(const AttnParams& p, int tile_rows, const CUtensorMap& mk,
                      const CUtensorMap& mv, cudaStream_t stream) {
   if (tile_rows == 16) return launch_n<D, kFP8, 16>(p, mk, mv, stream);
   if (tile_rows == 32) return launch_n<D, kFP8, 32>(p, mk, mv, stream);
+  if (tile_rows == 48) return launch_n<D, kFP8, 48>(p, mk, mv, stream);
   return launch_n<D, kFP8, 64>(p, mk, mv, stream);
 }
 

@@ -61,6 +61,8 @@ __global__ void __launch_bounds__(kThreads)
     kv_write_kernel(const __nv_bfloat16* __restrict__ k, const __nv_bfloat16* __restrict__ v,
                     int64_t ks_t, int64_t ks_h, int64_t vs_t, int64_t vs_h,
                     const int32_t* __restrict__ slots, KvCacheView c, int64_t rows, Ctrl* ctrl) {
+  pdl_wait();
+  pdl_launch_dependents();
   constexpr int kTpr = D / 16;             // threads per row
   const int64_t idx = static_cast<int64_t>(blockIdx.x) * kThreads + threadIdx.x;
   const int64_t row = idx / kTpr;
@@ -136,6 +138,8 @@ __global__ void __launch_bounds__(kThreads)
                    int rows, uint4* __restrict__ k_out, uint4* __restrict__ v_out, Ctrl* ctrl) {
   constexpr int kTpr = D / 16;
   __shared__ int64_t s_src[kReadTokens];   // row of the cache at head 0, or -1
+  pdl_wait();
+  pdl_launch_dependents();
   const int r0 = blockIdx.x * kReadTokens;
   if (threadIdx.x < kReadTokens) {
     const int r = r0 + threadIdx.x;
@@ -205,16 +209,18 @@ cudaError_t launch_kv_write(const KvCacheView& c, int head_dim, bool fp8, const 
   const dim3 grid(static_cast<unsigned>((threads + kThreads - 1) / kThreads));
   const __nv_bfloat16* kb = static_cast<const __nv_bfloat16*>(k);
   const __nv_bfloat16* vb = static_cast<const __nv_bfloat16*>(v);
-#define MOE_KVW(DD, F)                                                                           \
-  kv_write_kernel<DD, F><<<grid, kThreads, 0, stream>>>(kb, vb, ks_t, ks_h, vs_t, vs_h, slots, c, \
-                                                        rows, ctrl)
+  cudaLaunchAttribute attr[1];
+  const cudaLaunchConfig_t cfg = make_cfg(grid, dim3(kThreads), stream, true, attr);
+#define MOE_KVW(DD, F)                                                                          \
+  return cudaLaunchKernelEx(&cfg, kv_write_kernel<DD, F>, kb, vb, ks_t, ks_h, vs_t, vs_h, slots, \
+                            c, rows, ctrl)
   if (head_dim == 128) {
-    if (fp8) MOE_KVW(128, true); else MOE_KVW(128, false);
-  } else {
-    if (fp8) MOE_KVW(64, true); else MOE_KVW(64, false);
+    if (fp8) MOE_KVW(128, true);
+    MOE_KVW(128, false);
   }
+  if (fp8) MOE_KVW(64, true);
+  MOE_KVW(64, false);
 #undef MOE_KVW
-  return cudaGetLastError();
 }
 
 cudaError_t launch_kv_read(const KvCacheView& c, int head_dim, bool fp8, const int32_t* table,
@@ -223,16 +229,18 @@ cudaError_t launch_kv_read(const KvCacheView& c, int head_dim, bool fp8, const i
   const dim3 grid((rows + kReadTokens - 1) / kReadTokens);
   uint4* ko = static_cast<uint4*>(k_out);
   uint4* vo = static_cast<uint4*>(v_out);
-#define MOE_KVR(DD, F)                                                                          \
-  kv_read_kernel<DD, F><<<grid, kThreads, 0, stream>>>(c, table, table_stride, cu, starts, B,   \
-                                                       rows, ko, vo, ctrl)
+  cudaLaunchAttribute attr[1];
+  const cudaLaunchConfig_t cfg = make_cfg(grid, dim3(kThreads), stream, true, attr);
+#define MOE_KVR(DD, F)                                                                         \
+  return cudaLaunchKernelEx(&cfg, kv_read_kernel<DD, F>, c, table, table_stride, cu, starts, B, \
+                            rows, ko, vo, ctrl)
   if (head_dim == 128) {
-    if (fp8) MOE_KVR(128, true); else MOE_KVR(128, false);
-  } else {
-    if (fp8) MOE_KVR(64, true); else MOE_KVR(64, false);
+    if (fp8) MOE_KVR(128, true);
+    MOE_KVR(128, false);
   }
+  if (fp8) MOE_KVR(64, true);
+  MOE_KVR(64, false);
 #undef MOE_KVR
-  return cudaGetLastError();
 }
 
 }  // namespace moe

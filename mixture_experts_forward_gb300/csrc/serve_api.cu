@@ -156,7 +156,7 @@ moe_status_t moe_paged_attention(const moe_attention_args* a, void* ws, size_t w
   p.drop_producer = loads_dropped() ? 1 : 0;
 
   const bool few = rows <= 128;
-  const int tile_rows = !few ? kTileRows : rows <= 16 ? 16 : rows <= 32 ? 32 : 64;
+  const int tile_rows = !few ? kTileRows : rows <= 16 ? 16 : rows <= 32 ? 32 : rows <= 48 ? 48 : 64;
   p.row_tiles = static_cast<int>((rows + tile_rows - 1) / tile_rows);
   const long long tiles = static_cast<long long>(a->B) * p.c.heads * p.row_tiles;
   if (tiles > 0x7fffffffll) return MOE_ERR_UNSUPPORTED;
@@ -168,7 +168,7 @@ moe_status_t moe_paged_attention(const moe_attention_args* a, void* ws, size_t w
   // Parts of at least 256 keys.  Few rows: until there are about four for every
   // place that an SM has for a CTA.  Many rows: as many as fit the SMs at once.
   const long long most = (span + 255) / 256;
-  long long splits = few ? 4ll * sms / tiles : sms / tiles;
+  long long splits = few ? 2ll * sms / tiles : sms / tiles;
   if (splits > most) splits = most;
   const long long part_bytes = static_cast<long long>(p.part_rows) * (D + 2) * 4;
   const long long fit =

@@ -6,12 +6,15 @@
 // one pass over a row of p and a row of q: each warp sums its own contiguous
 // run of the vocabulary in fixed point (w = trunc(max(p - q, 0) * 2^38), exact
 // in any order; a row sums to about 2^38, so 2^24 tokens of full weight still
-// fit 64 bits), the CTAs' sums meet over distributed shared memory, and the one
-// warp whose run holds the threshold walks that run again, 32 tokens at a time.
+// fit 64 bits), and the CTAs' sums meet over distributed shared memory.  The CTA
+// whose part holds the threshold splits the one warp's run that holds it over all
+// its warps, and one of those walks the last few hundred tokens, 32 at a time.
 // Rows start at any multiple of the element size (odd vocabularies), so loads
 // are one element per lane, kUnroll of each row in flight per thread; 128-byte
-// requests keep up with HBM.  Bound by HBM for batches, by the latency of the
-// dependent steps (drafts, row, sums, run) for single sequences.
+// requests keep up with HBM.  The weights' conversion is shifts of the float's own
+// bits: a conversion instruction to 64 bits runs at 2 lanes per cycle and was 60 of 85 us
+// for 96 rows of 131071.  Bound by HBM for batches, by the latency of the dependent
+// steps (drafts, row, sums, run) for single sequences.
 #include "serve_internal.cuh"
 
 namespace moe {
@@ -20,7 +23,6 @@ namespace {
 constexpr int kVThreads = 512;
 constexpr int kVWarps = kVThreads / 32;
 constexpr int kVUnroll = 8;
-constexpr float kFix = 274877906944.0f;  // 2^38
 
 __device__ __forceinline__ float load_prob(const float* p) { return __ldg(p); }
 __device__ __forceinline__ float load_prob(const __nv_bfloat16* p) {
@@ -30,7 +32,13 @@ __device__ __forceinline__ float load_prob(const __nv_bfloat16* p) {
 // clamp to [0, 1]; NaN -> 0
 __device__ __forceinline__ float unit(float x) { return fminf(fmaxf(x, 0.0f), 1.0f); }
 
-__device__ __forceinline__ uint64_t fixed(float w) { return static_cast<uint64_t>(w * kFix); }
+// trunc(w * 2^38) of w in [0, 1]: the 24-bit significand shifted by the exponent
+// (2^-23 is one unit of it at exponent 127: 38 - 23 = 15 places left, less 127 - exponent).
+__device__ __forceinline__ uint64_t fixed(float w) {
+  const uint32_t u = __float_as_uint(w);
+  const uint64_t m = static_cast<uint64_t>((u & 0x7fffffu) | 0x800000u) << 15;
+  return m >> min(127u - (u >> 23), 63u);      // (zero and subnormals: shifted out)
+}
 
 __device__ __forceinline__ uint64_t warp_sum(uint64_t v) {
 #pragma unroll
@@ -61,9 +69,11 @@ __device__ __forceinline__ uint64_t ld_cluster_u64(uint32_t addr) {
 
 template <typename T>
 __global__ void __launch_bounds__(kVThreads) verify_kernel(VerifyArgs<T> a, int ctas) {
-  __shared__ uint64_t s_warp[2][kVWarps];  // sums of this CTA's warps: rest, p alone
-  __shared__ uint64_t s_cta[2];
+  __shared__ uint64_t s_warp[kVWarps];     // sums of this CTA's warps
+  __shared__ uint64_t s_cta;
   __shared__ int s_r;
+  pdl_wait();
+  pdl_launch_dependents();
   const int b = blockIdx.x / ctas;
   const int rank = blockIdx.x - b * ctas;
   const int tid = threadIdx.x, lane = tid & 31, w = tid >> 5;
@@ -98,62 +108,63 @@ __global__ void __launch_bounds__(kVThreads) verify_kernel(VerifyArgs<T> a, int 
   const T* p = a.p + b * a.p_sb + r * a.p_si;
   const T* q = a.q + b * a.q_sb + (has_q ? r : 0) * a.q_si;
 
+  // a token's weight: what is left of p after q, or (from_p) p itself
+  auto weight = [&](int v, bool from_p) -> uint64_t {
+    const float x = unit(load_prob(p + v));
+    return fixed(from_p || !has_q ? x : unit(__fsub_rn(x, load_prob(q + v))));
+  };
+  // the sum over this warp's lanes of the weights of [from, to)
+  auto run_sum = [&](int from, int to, bool from_p) -> uint64_t {
+    const bool both = has_q && !from_p;
+    uint64_t sum = 0;
+    int v = from + lane;
+    for (; v + 32 * (kVUnroll - 1) < to; v += 32 * kVUnroll) {
+      float x[kVUnroll], y[kVUnroll];
+#pragma unroll
+      for (int i = 0; i < kVUnroll; ++i) x[i] = load_prob(p + v + 32 * i);
+#pragma unroll
+      for (int i = 0; i < kVUnroll; ++i) y[i] = both ? load_prob(q + v + 32 * i) : 0.0f;
+#pragma unroll
+      for (int i = 0; i < kVUnroll; ++i) {
+        const float w = unit(x[i]);
+        sum += fixed(both ? unit(__fsub_rn(w, y[i])) : w);
+      }
+    }
+    for (; v < to; v += 32) sum += weight(v, from_p);
+    return warp_sum(sum);
+  };
   // this warp's run of the vocabulary: a multiple of 32 tokens per warp
   const int warps = ctas * kVWarps;
   const int per = ((V + warps - 1) / warps + 31) & ~31;
-  const int64_t first = static_cast<int64_t>(rank * kVWarps + w) * per;
-  const int v0 = static_cast<int>(first < V ? first : V);
-  const int v1 = min(V, v0 + per);
-  uint64_t rest = 0, alone = 0;
-  int v = v0 + lane;
-  for (; v + 32 * (kVUnroll - 1) < v1; v += 32 * kVUnroll) {
-    float x[kVUnroll], y[kVUnroll];
-#pragma unroll
-    for (int i = 0; i < kVUnroll; ++i) x[i] = unit(load_prob(p + v + 32 * i));
-#pragma unroll
-    for (int i = 0; i < kVUnroll; ++i) y[i] = has_q ? load_prob(q + v + 32 * i) : 0.0f;
-#pragma unroll
-    for (int i = 0; i < kVUnroll; ++i) {
-      alone += fixed(x[i]);
-      rest += fixed(unit(__fsub_rn(x[i], y[i])));
+  auto run_start = [&](int warp_of_cta) -> int {
+    const int64_t first = static_cast<int64_t>(rank * kVWarps + warp_of_cta) * per;
+    return static_cast<int>(first < V ? first : V);
+  };
+  const int v0 = run_start(w), v1 = min(V, v0 + per);
+  uint64_t total = 0, before = 0;
+  bool from_p = false;
+  for (int attempt = 0; attempt < 2; ++attempt) {
+    // no residual weight anywhere: draw from p itself
+    from_p = attempt == 1;
+    const uint64_t mine = run_sum(v0, v1, from_p);
+    if (lane == 0) s_warp[w] = mine;
+    __syncthreads();
+    if (w == 0) {
+      const uint64_t c = warp_sum(lane < kVWarps ? s_warp[lane] : 0ull);
+      if (lane == 0) s_cta = c;
     }
-  }
-  for (; v < v1; v += 32) {
-    const float x = unit(load_prob(p + v));
-    alone += fixed(x);
-    rest += fixed(unit(__fsub_rn(x, has_q ? load_prob(q + v) : 0.0f)));
-  }
-  rest = warp_sum(rest);
-  alone = warp_sum(alone);
-  if (lane == 0) {
-    s_warp[0][w] = rest;
-    s_warp[1][w] = alone;
-  }
-  __syncthreads();
-  if (w == 0) {
-    const uint64_t c0 = warp_sum(lane < kVWarps ? s_warp[0][lane] : 0ull);
-    const uint64_t c1 = warp_sum(lane < kVWarps ? s_warp[1][lane] : 0ull);
-    if (lane == 0) {
-      s_cta[0] = c0;
-      s_cta[1] = c1;
+    cluster_sync();
+    total = before = 0;
+    for (int c = 0; c < ctas; ++c) {
+      const uint64_t x = ld_cluster_u64(mapa_shared(smem_u32(&s_cta), c));
+      total += x;
+      if (c < rank) before += x;
     }
+    cluster_sync();                        // every CTA has read the others' sums
+    if (total > 0 || !has_q) break;
   }
-  cluster_sync();
-  uint64_t total0 = 0, total1 = 0, before0 = 0, before1 = 0;
-  for (int c = 0; c < ctas; ++c) {
-    const uint32_t at = mapa_shared(smem_u32(s_cta), c);
-    const uint64_t x = ld_cluster_u64(at), y = ld_cluster_u64(at + 8);
-    total0 += x;
-    total1 += y;
-    if (c < rank) {
-      before0 += x;
-      before1 += y;
-    }
-  }
-  cluster_sync();  // every CTA has read the others' sums: they may exit
-  const bool from_p = total0 == 0;         // no residual weight: draw from p itself
-  const uint64_t total = from_p ? total1 : total0;
-  uint64_t u24 = static_cast<uint64_t>(unit(__ldg(a.u_sample + b)) * 16777216.0f);
+  uint64_t u24 = static_cast<uint64_t>(
+      __float2uint_rz(unit(__ldg(a.u_sample + b)) * 16777216.0f));
   if (u24 > 16777215u) u24 = 16777215u;    // 1 is outside [0, 1): the last token
   // floor(u24 * total / 2^24) in 88 bits
   const uint64_t t = (__umul64hi(total, u24) << 40) | ((total * u24) >> 24);
@@ -165,19 +176,29 @@ __global__ void __launch_bounds__(kVThreads) verify_kernel(VerifyArgs<T> a, int 
     }
     if (lane == 0) a.accepted[b] = r;
   }
-  const uint64_t* sums = s_warp[from_p ? 1 : 0];
-  uint64_t acc = from_p ? before1 : before0;
-  for (int i = 0; i < w; ++i) acc += sums[i];
-  if (t < acc || t >= acc + sums[w]) return;
-  // the threshold lies in this warp's run
-  for (int base = v0; base < v1; base += 32) {
-    const int j = base + lane;
-    uint64_t wt = 0;
-    if (j < v1) {
-      const float x = unit(load_prob(p + j));
-      wt = fixed(from_p ? x : unit(__fsub_rn(x, has_q ? load_prob(q + j) : 0.0f)));
+  // the warp's run that holds the threshold, if it is this CTA's: the same for all its threads
+  int owner = -1;
+  uint64_t acc = before;
+  for (int i = 0; i < kVWarps; ++i) {
+    const uint64_t x = s_warp[i];
+    if (owner < 0) {
+      if (t >= acc && t < acc + x) owner = i;
+      else acc += x;
     }
-    uint64_t inc = wt;
+  }
+  if (owner < 0) return;
+  __syncthreads();                         // (s_warp is written again)
+  const int o0 = run_start(owner), o1 = min(V, o0 + per);
+  const int sub = ((o1 - o0 + kVWarps - 1) / kVWarps + 31) & ~31;
+  const int q0 = min(o1, o0 + w * sub), q1 = min(o1, q0 + sub);
+  const uint64_t mine = run_sum(q0, q1, from_p);
+  if (lane == 0) s_warp[w] = mine;
+  __syncthreads();
+  for (int i = 0; i < w; ++i) acc += s_warp[i];
+  if (t < acc || t >= acc + mine) return;
+  for (int base = q0; base < q1; base += 32) {
+    const int j = base + lane;
+    uint64_t inc = j < q1 ? weight(j, from_p) : 0ull;
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) {
       const uint64_t up = __shfl_up_sync(0xffffffffu, inc, o);
@@ -220,13 +241,15 @@ cudaError_t launch_t(const moe_verify_args& a, Ctrl* ctrl, int num_sms, cudaStre
   cfg.gridDim = dim3(static_cast<unsigned>(a.B) * ctas);
   cfg.blockDim = dim3(kVThreads);
   cfg.stream = stream;
-  cudaLaunchAttribute attr[1];
+  cudaLaunchAttribute attr[2];
   attr[0].id = cudaLaunchAttributeClusterDimension;
   attr[0].val.clusterDim.x = ctas;
   attr[0].val.clusterDim.y = 1;
   attr[0].val.clusterDim.z = 1;
+  attr[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[1].val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = attr;
-  cfg.numAttrs = 1;
+  cfg.numAttrs = 2;
   return cudaLaunchKernelEx(&cfg, verify_kernel<T>, k, ctas);
 }
 
