@@ -117,15 +117,17 @@ __host__ __device__ __forceinline__ int64_t partial_floats(int rows) {
   return static_cast<int64_t>(rows) * (D + 2);
 }
 
-// Called by every thread of the CTA (`threads` of them) after the CTA's part
-// has been written to p.partial: the last CTA of the tile to arrive joins the
-// parts, in their order, and writes out and lse.  `tile` numbers the tiles
-// of the launch, part_rows the rows that a part has room for; named barrier
-// `bar` joins the threads.
+// Called by `threads` threads of the CTA after its part has been written to
+// p.partial: the last CTA of the tile to arrive joins the parts, in their order, and writes
+// out and lse.  `tile` numbers the tiles that are split, part_rows the rows that a part has
+// room for; named barrier `bar` joins the threads; `weights` is shared memory for
+// count * part_rows floats.  First a thread per row turns the parts' maxima and sums into
+// weights, then all threads stream the parts, kAhead 16-byte loads in flight each.
 template <int D>
 __device__ __forceinline__ void join_parts(const AttnParams& p, const TileView& t, int64_t tile,
                                            int part_rows, int count, int tid, int threads,
-                                           int bar, int* s_flag) {
+                                           int bar, float* weights, int* s_flag) {
+  constexpr int kAhead = 8;
   __threadfence();
   named_bar_sync(bar, threads);
   if (tid == 0) {
@@ -140,43 +142,53 @@ __device__ __forceinline__ void join_parts(const AttnParams& p, const TileView& 
   const int64_t stride = partial_floats<D>(part_rows);
   const float* parts = p.partial + tile * p.splits * stride;
   const float* ml = parts + static_cast<int64_t>(part_rows) * D;
-  for (int i = tid; i < t.rows * (D / 4); i += threads) {
-    const int r = i / (D / 4), d = (i % (D / 4)) * 4;
-    float m = __int_as_float(0xff800000);
+  const float ninf = __int_as_float(0xff800000);
+  for (int r = tid; r < t.rows; r += threads) {
+    float m = ninf, l = 0.0f;
+#pragma unroll 8
     for (int s = 0; s < count; ++s) m = fmaxf(m, __ldcg(ml + s * stride + r));
-    const float ref = m == __int_as_float(0xff800000) ? 0.0f : m;
-    float l = 0.0f;
-    float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
-#pragma unroll 4
+    const float ref = m == ninf ? 0.0f : m;
+#pragma unroll 8
     for (int s = 0; s < count; ++s) {
       const float w = exp2_approx(__ldcg(ml + s * stride + r) - ref);
-      const float4 x = __ldcg(reinterpret_cast<const float4*>(parts + s * stride + r * D + d));
+      weights[s * part_rows + r] = w;
       l = fmaf(w, __ldcg(ml + s * stride + part_rows + r), l);
-      o.x = fmaf(w, x.x, o.x);
-      o.y = fmaf(w, x.y, o.y);
-      o.z = fmaf(w, x.z, o.z);
-      o.w = fmaf(w, x.w, o.w);
     }
     const float inv = l == 0.0f ? 0.0f : 1.0f / l;
-    __nv_bfloat162 a = __floats2bfloat162_rn(o.x * inv, o.y * inv);
-    __nv_bfloat162 b = __floats2bfloat162_rn(o.z * inv, o.w * inv);
+    for (int s = 0; s < count; ++s) weights[s * part_rows + r] *= inv;
+    if (p.lse != nullptr) *lse_at(p, t, r) = lse_of(m, l);
+  }
+  named_bar_sync(bar, threads);
+  for (int i = tid; i < t.rows * (D / 4); i += threads) {
+    const int r = i / (D / 4), d = (i % (D / 4)) * 4;
+    const float* src = parts + static_cast<int64_t>(r) * D + d;
+    float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
+    for (int s0 = 0; s0 < count; s0 += kAhead) {
+      float4 x[kAhead];
+#pragma unroll
+      for (int j = 0; j < kAhead; ++j)
+        if (s0 + j < count) x[j] = __ldcg(reinterpret_cast<const float4*>(src + (s0 + j) * stride));
+#pragma unroll
+      for (int j = 0; j < kAhead; ++j)
+        if (s0 + j < count) {
+          const float w = weights[(s0 + j) * part_rows + r];
+          o.x = fmaf(w, x[j].x, o.x);
+          o.y = fmaf(w, x[j].y, o.y);
+          o.z = fmaf(w, x[j].z, o.z);
+          o.w = fmaf(w, x[j].w, o.w);
+        }
+    }
+    __nv_bfloat162 a = __floats2bfloat162_rn(o.x, o.y);
+    __nv_bfloat162 b = __floats2bfloat162_rn(o.z, o.w);
     uint2 u;
     u.x = *reinterpret_cast<uint32_t*>(&a);
     u.y = *reinterpret_cast<uint32_t*>(&b);
     *reinterpret_cast<uint2*>(out_row(p, t, r) + d) = u;
-    if (d == 0 && p.lse != nullptr) *lse_at(p, t, r) = lse_of(m, l);
   }
 }
 
-// Quantised values: the weight of key j in the second product is
-// 2^(s_j - m) * vs_j for the value scale vs_j, and m is the maximum of
-// s_j + log2 vs_j, so the product stays at or below 1 whatever the scales are
-// and fits binary16; the softmax's own sum divides vs_j out again in binary32.
-// Scales below 2^-100 (values below 448 * 2^-100 = 3.5e-28) count as 2^-100.
-__device__ __forceinline__ float value_scale(float vs) { return fmaxf(vs, 7.8886090522101181e-31f); }
-
-// The binary16 form of a query row: scaled by a power of two that brings its
-// largest element near 2^8, so that only elements 2^-22 below that one lose bits.
+// The power of two that brings a row's largest element into [2^8, 2^9), and its
+// reciprocal.
 __device__ __forceinline__ void row_pow2(float amax, float& mul, float& inv) {
   int ex = static_cast<int>((__float_as_uint(amax) >> 23) & 255u);
   ex = max(ex, 9);

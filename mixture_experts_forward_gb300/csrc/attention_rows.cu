@@ -51,6 +51,7 @@ struct RowsShape {
   static constexpr int kSmem = oSlots + kSlots * kTileBytes;
   static constexpr int kTmem = N == 48 ? 256 : 4 * N;    // S twice, O (FP8: hi and lo)
   static_assert(kSlots >= 3, "two tiles of keys and one of values");
+  static_assert(kSlots * kTileBytes >= kMaxParts * N * 4, "the joining weights fit the ring");
   static_assert(oQ % 1024 == 0, "swizzled tiles start on 1024 bytes");
 };
 
@@ -566,7 +567,8 @@ __global__ void
       }
     }
     if (split)
-      join_parts<D>(p, t, blockIdx.x, p.part_rows, parts.count, tid, S::kSoftmax, 1, &bars.flag);
+      join_parts<D>(p, t, blockIdx.x, p.part_rows, parts.count, tid, S::kSoftmax, 1,
+                    reinterpret_cast<float*>(smem + S::oSlots), &bars.flag);
   } else if (warp == kMmaWarp) {
     // =================================================================== MMA
     if (n > 0) {

@@ -33,10 +33,6 @@
 // then do a second pass and a rescale of O follow, which the softmax threads do
 // themselves between their S and their P, when no product of theirs is running.
 // (With a running maximum in every tile: 2800 cycles per pair of row tiles, 1.48 us.)
-// With at most 128 rows there is one row tile, and each softmax group takes half of
-// the columns of every key tile's scores, whose two buffers then alternate: scores of
-// the next tile are ready when a tile's weights are done.
-//
 // What lies past the last key must not meet a zero weight (0 * NaN): the second
 // product runs over the 16-key steps that hold keys, and the rest of a last step is
 // zeroed in shared memory before it.
@@ -87,7 +83,6 @@ struct Bars {
   int abort;
   int flag;
   int e[3];                       // FP8: exponent of each tile's value scales
-  float other[2][kRows];          // two groups on the same rows: what one tells the other
 };
 
 template <int D, bool kFP8>
@@ -99,27 +94,7 @@ __global__ void __launch_bounds__(TileShape<D, kFP8>::kThreads, 1)
   __shared__ Bars bars;
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
 
-  // ---- what this CTA has to do (late row tiles see most keys: they start first)
-  const int tiles_bh = p.B * p.c.heads;
-  const int rt = p.row_tiles - 1 - static_cast<int>(blockIdx.x / tiles_bh);
-  const int bh = static_cast<int>(blockIdx.x % tiles_bh);
-  const int b = bh / p.c.heads, h = bh - b * p.c.heads;
-  const int part = blockIdx.y;
-  const TileView t = tile_view(p, b, h, rt, 2 * kRows, part == 0 && rt == 0 && tid == 0);
-  if (t.rows == 0) return;
-  const Parts parts = tile_parts(p, t, kKeys);
-  if (part >= max(1, parts.count)) return;
-  const int k0 = parts.base + part * p.chunk;
-  const int k1 = parts.count == 0 ? k0 : (part + 1 >= parts.count ? t.hi : k0 + p.chunk);
-  const int n = (k1 - k0 + kKeys - 1) / kKeys;                   // key tiles
-  const bool alt = t.rows <= kRows;
-  const int lead = alt ? 2 : 1;
-  int n_of[2] = {n, n};                                           // key tiles of each group
-  if (!alt) {
-    const int hi0 = min(k1, row_hi(p, t, (t.first_row + kRows - 1) / p.group));
-    n_of[0] = max(0, min(n, (hi0 - k0 + kKeys - 1) / kKeys));
-  }
-
+  // ---- what needs no input: barriers, tensor memory
   auto bar = [&](const uint64_t& x) { return smem_u32(&x); };
   if (tid == 0) {
     for (int i = 0; i < S::kSlots; ++i) {
@@ -137,13 +112,12 @@ __global__ void __launch_bounds__(TileShape<D, kFP8>::kThreads, 1)
     mbar_init(bar(bars.q_full), 256);
     for (int w = 0; w < 2; ++w) {
       mbar_init(bar(bars.s_full[w]), 1);
-      mbar_init(bar(bars.p_full[w]), alt ? 256 : 128);
+      mbar_init(bar(bars.p_full[w]), 128);
       mbar_init(bar(bars.o_done[w]), 1);
     }
     for (int i = 0; i < S::kScaleSlots; ++i) {
       mbar_init(bar(bars.sc_full[i]), 1);
-      // the softmax's warps and the converting ones (row tile 0 may skip the last two key
-      // tiles at most: no later tile waits for their slots)
+      // the softmax's warps and the converting ones
       mbar_init(bar(bars.sc_empty[i]), 12);
     }
     mbar_init(bar(bars.drain), 1);
@@ -154,6 +128,46 @@ __global__ void __launch_bounds__(TileShape<D, kFP8>::kThreads, 1)
     tmem_alloc(smem_u32(&bars.tmem), 512);
     tmem_relinquish();
   }
+  if (tid == 256) {
+    tma_prefetch_desc(&map_k);
+    tma_prefetch_desc(&map_v);
+  }
+  pdl_wait();
+  pdl_launch_dependents();
+
+  // ---- what this CTA has to do: first the tiles that are not split, late row tiles (which
+  // see most keys) before early ones, then the parts of the last tiles
+  const int tiles_bh = p.B * p.c.heads;
+  int tile_no = blockIdx.x, part = 0, splits = 1;
+  if (tile_no >= p.whole) {
+    const int last = tiles_bh * p.row_tiles - p.whole;
+    part = (tile_no - p.whole) / last;
+    tile_no = p.whole + (tile_no - p.whole) % last;
+    splits = p.splits;
+  }
+  const int rt = p.row_tiles - 1 - tile_no / tiles_bh;
+  const int bh = tile_no % tiles_bh;
+  const int b = bh / p.c.heads, h = bh - b * p.c.heads;
+  const TileView t = tile_view(p, b, h, rt, 2 * kRows, part == 0 && rt == 0 && tid == 0);
+  // its keys, cut evenly into whole key tiles
+  const int base = t.lo / kKeys * kKeys;
+  const int all = t.hi > t.lo ? (t.hi - base + kKeys - 1) / kKeys : 0;
+  const int each = max(1, (all + splits - 1) / splits), count = (all + each - 1) / each;
+  if (t.rows == 0 || part >= max(1, count)) {                    // nothing to do here
+    if (warp == 9) {
+      const uint32_t at = *reinterpret_cast<volatile uint32_t*>(&bars.tmem);
+      tmem_dealloc(at, 512);
+    }
+    return;
+  }
+  const int k0 = base + part * each * kKeys;
+  const int k1 = all == 0 ? k0 : min(t.hi, k0 + each * kKeys);
+  const int n = (k1 - k0 + kKeys - 1) / kKeys;                   // key tiles
+  // key tiles of each group: row tile 0 may end earlier, row tile 1 may not exist
+  const int hi0 = min(k1, row_hi(p, t, (t.first_row + min(t.rows, kRows) - 1) / p.group));
+  const int n0 = max(0, min(n, (hi0 - k0 + kKeys - 1) / kKeys));
+  const int n1 = t.rows > kRows ? n : 0;
+
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
@@ -179,7 +193,7 @@ __global__ void __launch_bounds__(TileShape<D, kFP8>::kThreads, 1)
     regs_inc<S::kRegsSoftmax>();
     const int w = warp >> 2;
     const int row = tid & 127;                       // lane of tensor memory
-    const int my = alt ? row : w * kRows + row;      // row of the CTA's rows
+    const int my = w * kRows + row;                  // row of the CTA's rows
     const bool real = my < t.rows;
     const uint32_t lanes = static_cast<uint32_t>(warp & 3) << 21;   // this warp's lanes (<< 16)
     // ---- the query tiles, in the layout of a K-major operand
@@ -187,13 +201,11 @@ __global__ void __launch_bounds__(TileShape<D, kFP8>::kThreads, 1)
       constexpr int kPieces = D / 8;                 // 16-byte pieces of a row
       constexpr int kPerPass = 128 / kPieces;        // rows per pass of the group
       const int c = row % kPieces;
-      const int rows_here = alt ? 64 : 128;
       const uint32_t flip = p.scale < 0.0f ? 0x80008000u : 0u;   // the scores' factor is positive
 #pragma unroll 4
-      for (int pass = 0; pass < rows_here / kPerPass; ++pass) {
-        const int r = row / kPieces + pass * kPerPass;
-        const int tr = alt ? w * 64 + r : r;         // row within its tile
-        const int cr = alt ? tr : w * kRows + r;     // row of the CTA's rows
+      for (int pass = 0; pass < kRows / kPerPass; ++pass) {
+        const int tr = row / kPieces + pass * kPerPass;   // row within its tile
+        const int cr = w * kRows + tr;                    // row of the CTA's rows
         uint4 x = make_uint4(0u, 0u, 0u, 0u);
         if (cr < t.rows) {
           const int rr = t.first_row + cr, tok = rr / p.group;
@@ -220,12 +232,12 @@ __global__ void __launch_bounds__(TileShape<D, kFP8>::kThreads, 1)
           if (c == 0) reinterpret_cast<float*>(smem + S::oRowf)[cr] = 2.0f * inv;
           uint32_t hi[2], lo[2];
           two_terms({xw[0], xw[1], xw[2], xw[3]}, mul, hi, lo);
-          uint8_t* at = smem + S::oQ + (alt ? 0 : w) * S::kTileBytes +
+          uint8_t* at = smem + S::oQ + w * S::kTileBytes +
                         code_piece<D>(tr, c >> 1) + (c & 1) * 8;
           *reinterpret_cast<uint2*>(at) = make_uint2(hi[0], hi[1]);
           *reinterpret_cast<uint2*>(at + S::kCodeBytes) = make_uint2(lo[0], lo[1]);
         } else {
-          uint8_t* at = smem + S::oQ + (alt ? 0 : w) * S::kTileBytes + (c >> 3) * kHalfBytes +
+          uint8_t* at = smem + S::oQ + w * S::kTileBytes + (c >> 3) * kHalfBytes +
                         tr * 128 + (((c & 7) ^ (tr & 7)) << 4);
           *reinterpret_cast<uint4*>(at) = x;
         }
@@ -241,14 +253,14 @@ __global__ void __launch_bounds__(TileShape<D, kFP8>::kThreads, 1)
     }
     r_lo = max(r_lo, k0);
     r_hi = min(r_hi, k1);
-    const bool idle = (alt ? (warp & 3) * 32 : w * kRows + (warp & 3) * 32) >= t.rows;
-    const int my_n = n_of[w];
+    const bool idle = w * kRows + (warp & 3) * 32 >= t.rows;
+    const int my_n = w == 0 ? n0 : n1;
     const float cap = p.softcap, cap_k = cap > 0.0f ? 2.0f * kLog2e / cap : 0.0f;
     float sc = fabsf(p.scale) * (cap > 0.0f ? 1.0f : kLog2e);
     bool ok = true;
     if constexpr (kFP8) {
       if (my_n > 0) {
-        ok = wait(bar(bars.q_full), 0);              // the other group wrote some of the factors
+        ok = wait(bar(bars.q_full), 0);              // (other threads wrote the factors)
         sc *= reinterpret_cast<const float*>(smem + S::oRowf)[my];
       }
     }
@@ -258,16 +270,12 @@ __global__ void __launch_bounds__(TileShape<D, kFP8>::kThreads, 1)
     float ref = 0.0f, l = 0.0f;
     bool started = false;                            // the row has seen a key
     int E = 0;                                       // FP8: O is in units of 2^E
-    const uint32_t o_tm = tmem + lanes + 256 + (alt ? 0 : w * D);
+    const uint32_t s_tm = tmem + lanes + w * kKeys, o_tm = tmem + lanes + 256 + w * D;
 
-    // One key tile: kCols scores of this thread's row, from tensor memory at
-    // s_tm, of the keys from kb on, to weights in their place.  kBoth: the other group's
-    // warp of the same rows has the tile's other columns, and the two agree on the
-    // reference (over a barrier of their own).
-    auto tile = [&](auto cols, auto both, int i, int kb, uint32_t s_tm, int sslot) {
-      constexpr int kCols = decltype(cols)::value;
-      constexpr bool kBoth = decltype(both)::value;
-      const int pair_bar = 2 + (warp & 3);
+    // One key tile: the scores of this thread's row, of the keys from kb on, to weights
+    // in their place.
+    auto tile = [&](int i, int kb, int sslot) {
+      constexpr int kCols = kKeys;
       float s[kCols];
 #pragma unroll
       for (int j = 0; j < kCols / 32; ++j) tmem_ld32(s_tm + 32 * j, s + 32 * j);
@@ -275,8 +283,7 @@ __global__ void __launch_bounds__(TileShape<D, kFP8>::kThreads, 1)
       for (int j = 0; j < kCols / 32; ++j) tmem_ld_wait32(s + 32 * j);
       int e = 0;
       if constexpr (kFP8) {
-        const float4* ks = reinterpret_cast<const float4*>(smem + S::oScale + sslot * 1024) +
-                           (kBoth ? w * (kCols / 4) : 0);
+        const float4* ks = reinterpret_cast<const float4*>(smem + S::oScale + sslot * 1024);
 #pragma unroll
         for (int j = 0; j < kCols / 4; ++j) {
           const float4 k4 = ks[j];
@@ -298,18 +305,10 @@ __global__ void __launch_bounds__(TileShape<D, kFP8>::kThreads, 1)
         float x[4] = {s[0], s[1], s[2], s[3]};
 #pragma unroll
         for (int j = 4; j < kCols; ++j) x[j & 3] = fmaxf(x[j & 3], s[j]);
-        float y = fmaxf(fmaxf(x[0], x[1]), fmaxf(x[2], x[3])) * f;
-        if constexpr (kBoth) {
-          bars.other[w][row] = y;
-          named_bar_sync(pair_bar, 64);
-          y = fmaxf(y, bars.other[1 - w][row]);
-          named_bar_sync(pair_bar, 64);
-        }
-        return y;
+        return fmaxf(fmaxf(x[0], x[1]), fmaxf(x[2], x[3])) * f;
       };
       // a row's first keys set its reference
-      const int tile_key = k0 + i * kKeys;
-      const bool first = !started && tile_key < r_hi && tile_key + kKeys > r_lo;
+      const bool first = !started && kb < r_hi && kb + kKeys > r_lo;
       if (__any_sync(0xffffffffu, first)) {
         const float top = row_max();
         if (first) {
@@ -346,9 +345,7 @@ __global__ void __launch_bounds__(TileShape<D, kFP8>::kThreads, 1)
         return (sum0 + sum1) + (sum2 + sum3);
       };
       float sum = weigh();
-      bool far = __any_sync(0xffffffffu, sum > kFar);
-      if constexpr (kBoth) far = named_bar_any(pair_bar, 64, far);
-      if (far) {
+      if (__any_sync(0xffffffffu, sum > kFar)) {
         // (every row of the warp moves to its largest score so far)
         const float top = row_max();
         const float want = started ? fmaxf(ref, top) : ref;
@@ -358,15 +355,9 @@ __global__ void __launch_bounds__(TileShape<D, kFP8>::kThreads, 1)
         ref = want;
         E = e;
         if (i > 0) {
-          // the products so far are complete: with one group per row tile the scores'
-          // barrier says so, else the last product's own
-          if constexpr (kBoth) {
-            if (ok) ok = wait(bar(bars.o_done[0]), (i - 1) & 1);
-            tc_fence_after();
-          }
-          const int d0 = kBoth ? w * (D / 2) : 0, d1 = kBoth ? d0 + D / 2 : D;
+          // (these scores are complete, so every earlier product of this group is too)
 #pragma unroll 1
-          for (int d = d0; d < d1; d += 16) {
+          for (int d = 0; d < D; d += 16) {
             float o[16];
             tmem_ld16(o_tm + d, o);
             tmem_ld_wait(o);
@@ -383,58 +374,47 @@ __global__ void __launch_bounds__(TileShape<D, kFP8>::kThreads, 1)
       tmem_st_wait();
     };
 
-    // (A wait that gave up ends the waiting, not the loop: the warps of a row then still meet
-    // at the same barriers, and what they compute is dropped.)
-    for (int i = 0; i < my_n; ++i) {
-      // one group per row tile: its own scores; else the two buffers in turn
-      const int buf = alt ? (i & 1) : w;
-      if (ok) ok = wait(bar(bars.s_full[buf]), (alt ? i >> 1 : i) & 1);
+    for (int i = 0; i < my_n && ok; ++i) {
+      ok = wait(bar(bars.s_full[w]), i & 1);
       const int sslot = i % S::kScaleSlots;
-      if constexpr (kFP8) {
-        if (ok) ok = wait(bar(bars.sc_full[sslot]), (i / S::kScaleSlots) & 1);
-      }
+      if constexpr (kFP8) ok = ok && wait(bar(bars.sc_full[sslot]), (i / S::kScaleSlots) & 1);
+      if (!ok) break;
       tc_fence_after();
-      const uint32_t s_tm = tmem + lanes + buf * kKeys;
-      const int kb = k0 + i * kKeys;
-      if (!idle) {
-        if (alt)
-          tile(std::integral_constant<int, 64>(), std::true_type(), i, kb + w * 64, s_tm + w * 64,
-               sslot);
-        else
-          tile(std::integral_constant<int, 128>(), std::false_type(), i, kb, s_tm, sslot);
-      }
+      if (!idle) tile(i, k0 + i * kKeys, sslot);
       tc_fence_before();
       if constexpr (kFP8) {
         __syncwarp();
         if (lane == 0) mbar_arrive(bar(bars.sc_empty[sslot]));
       }
-      mbar_arrive(bar(bars.p_full[buf]));
+      mbar_arrive(bar(bars.p_full[w]));
     }
-    if (ok && my_n > 0) ok = wait(bar(bars.o_done[alt ? 1 : w]), 0);
+    if constexpr (kFP8) {
+      // the key tiles that this group does not see: their scales are done with
+      for (int i = my_n; i < n && ok; ++i) {
+        const int sslot = i % S::kScaleSlots;
+        ok = wait(bar(bars.sc_full[sslot]), (i / S::kScaleSlots) & 1);
+        if (lane == 0) mbar_arrive(bar(bars.sc_empty[sslot]));
+      }
+    }
+    if (ok && my_n > 0) ok = wait(bar(bars.o_done[w]), 0);
     tc_fence_after();
 
-    // ---- results: this thread's row, all its channels or (two groups) half of them
+    // ---- results
     const bool have = ok && my_n > 0 && !idle;
     if (!have) {
       started = false;
       l = 0.0f;
     }
     if (!started) ref = ninf;
-    if (alt) {
-      bars.other[w][row] = l;
-      named_bar_sync(2 + (warp & 3), 64);
-      l += bars.other[1 - w][row];
-    }
-    const bool split = parts.count > 1;
+    const bool split = count > 1;
     const float inv = l == 0.0f ? 0.0f : 1.0f / l;
     const float g = (kFP8 ? exp2_approx(static_cast<float>(E)) : 1.0f) * (split ? 1.0f : inv);
-    float* dst = p.partial + (static_cast<int64_t>(blockIdx.x) * p.splits + part) *
+    float* dst = p.partial + (static_cast<int64_t>(tile_no - p.whole) * p.splits + part) *
                                  partial_floats<D>(p.part_rows);
     __nv_bfloat16* orow = real && !split ? out_row(p, t, my) : nullptr;
-    const int d0 = alt ? w * (D / 2) : 0, d1 = alt ? d0 + D / 2 : D;
     if (!idle) {
 #pragma unroll 1
-      for (int d = d0; d < d1; d += 16) {
+      for (int d = 0; d < D; d += 16) {
         float o[16];
 #pragma unroll
         for (int j = 0; j < 16; ++j) o[j] = 0.0f;
@@ -462,7 +442,7 @@ __global__ void __launch_bounds__(TileShape<D, kFP8>::kThreads, 1)
         }
       }
     }
-    if (real && (!alt || w == 0)) {
+    if (real) {
       if (split) {
         dst[static_cast<int64_t>(p.part_rows) * D + my] = ref;
         dst[static_cast<int64_t>(p.part_rows) * (D + 1) + my] = l;
@@ -471,7 +451,8 @@ __global__ void __launch_bounds__(TileShape<D, kFP8>::kThreads, 1)
       }
     }
     if (split)
-      join_parts<D>(p, t, blockIdx.x, p.part_rows, parts.count, tid, 256, 1, &bars.flag);
+      join_parts<D>(p, t, tile_no - p.whole, p.part_rows, count, tid, 256, 1,
+                    reinterpret_cast<float*>(smem + S::oSlots), &bars.flag);
   } else if (warp < 12) {
     regs_dec<S::kRegsOther>();
     if (warp == 9 && n > 0) {
@@ -484,8 +465,8 @@ __global__ void __launch_bounds__(TileShape<D, kFP8>::kThreads, 1)
       const uint32_t idesc_o = make_idesc(kFP8 ? 0u : 1u, kRows, D) | (1u << 16);
       const uint32_t tm = __shfl_sync(0xffffffffu, tmem, 0);
       const int tiles = __shfl_sync(0xffffffffu, n, 0);
-      const int tiles0 = __shfl_sync(0xffffffffu, n_of[0], 0);
-      const bool two = __shfl_sync(0xffffffffu, alt ? 1 : 0, 0) != 0;
+      const int tiles0 = __shfl_sync(0xffffffffu, n0, 0);
+      const int tiles1 = __shfl_sync(0xffffffffu, n1, 0);
       const uint32_t q_lo = smem_desc_lo(sbase + S::oQ);
       const uint32_t k_lo = smem_desc_lo(sbase + (kFP8 ? S::oK : S::oSlots));
       const uint32_t v_lo = mn_desc_lo(sbase + S::oSlots);
@@ -520,7 +501,7 @@ __global__ void __launch_bounds__(TileShape<D, kFP8>::kThreads, 1)
       };
       // S = Q K^T of group w and the key tile in slot x
       auto scores = [&](int w, const Place& x) {
-        const uint32_t q = q_lo + (two ? 0 : w) * (S::kTileBytes >> 4);
+        const uint32_t q = q_lo + w * (S::kTileBytes >> 4);
         const uint32_t k = k_lo + x.slot * ((kFP8 ? S::kCodeBytes : S::kTileBytes) >> 4);
         tc_fence_after();
         if (elect_one()) {
@@ -541,24 +522,22 @@ __global__ void __launch_bounds__(TileShape<D, kFP8>::kThreads, 1)
           umma_commit(bar(bars.s_full[0]) + 8 * w);
         }
       };
-      // O += P V over the 16-key steps of tile i that hold keys.  P of steps 4..7 lies 32
-      // columns further where two groups wrote it (each in the place of its scores).
-      const uint32_t p_gap = two ? 32 : 0;
+      // O += P V over the 16-key steps of tile i that hold keys
       auto values = [&](int w, int i, const Place& x, bool first) {
         const uint32_t v = v_lo + x.slot * (S::kTileBytes >> 4);
-        const uint32_t d = tm + 256 + (two ? 0 : w) * D, pw = tm + w * kKeys;
+        const uint32_t d = tm + 256 + w * D, pw = tm + w * kKeys;
         tc_fence_after();
         if ((i > 0 || first_step == 0) && (i + 1 < tiles || last_steps == 8)) {
           if (elect_one()) {
 #pragma unroll
             for (int s = 0; s < 8; ++s)
-              umma_ts(d, pw + s * 8 + (s < 4 ? 0 : p_gap), v + s * (2048u >> 4), idesc_o,
+              umma_ts(d, pw + s * 8, v + s * (2048u >> 4), idesc_o,
                       s > 0 ? 1u : (first ? 0u : 1u));
           }
         } else if (elect_one()) {
           const int s0 = i == 0 ? first_step : 0, s1 = i + 1 == tiles ? last_steps : 8;
           for (int s = s0; s < s1; ++s)
-            umma_ts(d, pw + s * 8 + (s < 4 ? 0 : p_gap), v + s * (2048u >> 4), idesc_o,
+            umma_ts(d, pw + s * 8, v + s * (2048u >> 4), idesc_o,
                     (first && s == s0) ? 0u : 1u);
         }
       };
@@ -587,79 +566,43 @@ __global__ void __launch_bounds__(TileShape<D, kFP8>::kThreads, 1)
       };
       bool ok = wait(bar(bars.q_full), 0);
       uint32_t used0 = 0, used1 = 0;       // parity of each row tile's weights
-      if (two) {
-        for (int w = 0; w < 2 && w < tiles && ok; ++w) {
-          const Place x = next_k();
-          ok = wait_k(x);
-          if (!ok) break;
-          scores(w, x);
-          release_k(x);
-        }
-        for (int i = 0; i < tiles && ok; ++i) {
-          const int w = i & 1;
-          const Place v = next_v();
-          ok = wait_v(v) && wait(bar(bars.p_full[0]) + 8 * w, (i >> 1) & 1);
-          if (!ok) break;
-          clean(i, v);
-          values(w, i, v, i == 0);
-          release_v(v);
-          // o_done[0]: a phase for every product (a rescale at tile i waits for that of tile i - 1,
-          // when that of i - 2 is complete); o_done[1]: the last one
-          if (elect_one()) umma_commit(bar(bars.o_done[0]));
-          if (i + 1 == tiles && elect_one()) umma_commit(bar(bars.o_done[1]));
-          if (i + 2 < tiles) {
-            const Place k = next_k();
-            ok = wait_k(k);
-            if (!ok) break;
-            scores(w, k);
-            release_k(k);
-          }
-        }
-      } else if (ok) {
+      if (ok) {
         const Place x = next_k();
         ok = wait_k(x);
         if (ok) {
           if (tiles0 > 0) scores(0, x);
-          scores(1, x);
+          if (tiles1 > 0) scores(1, x);
           release_k(x);
         }
-        for (int i = 0; i < tiles && ok; ++i) {
-          const Place v = next_v();
-          ok = wait_v(v);
-          if (!ok) break;
-          clean(i, v);
-          const bool more = i + 1 < tiles;
-          Place k = {0, 0};
-          if (more) k = next_k();
-          bool have_k = false;
-          if (i < tiles0) {
-            ok = wait(bar(bars.p_full[0]), used0);
-            if (!ok) break;
-            used0 ^= 1;
-            values(0, i, v, i == 0);
-            if (i + 1 < tiles0) {
-              ok = wait_k(k);
-              if (!ok) break;
-              have_k = true;
-              scores(0, k);
-            } else if (elect_one()) {
-              umma_commit(bar(bars.o_done[0]));
-            }
-          }
-          ok = wait(bar(bars.p_full[1]), used1);
-          if (!ok) break;
-          used1 ^= 1;
-          values(1, i, v, i == 0);
-          release_v(v);
-          if (more) {
-            ok = have_k || wait_k(k);
-            if (!ok) break;
-            scores(1, k);
-            release_k(k);
+      }
+      for (int i = 0; i < tiles && ok; ++i) {
+        const Place v = next_v();
+        ok = wait_v(v);
+        if (!ok) break;
+        clean(i, v);
+        const bool more = i + 1 < tiles;
+        Place k = {0, 0};
+        bool have_k = false;
+        if (more) k = next_k();
+        // a row tile's product, then its next scores
+        auto turn = [&](int w, int count, uint32_t& used) -> bool {
+          if (i >= count) return true;
+          if (!wait(bar(bars.p_full[0]) + 8 * w, used)) return false;
+          used ^= 1;
+          values(w, i, v, i == 0);
+          if (i + 1 < count) {
+            if (!have_k && !wait_k(k)) return false;
+            have_k = true;
+            scores(w, k);
           } else if (elect_one()) {
-            umma_commit(bar(bars.o_done[1]));
+            umma_commit(bar(bars.o_done[0]) + 8 * w);
           }
-        }
+          return true;
+        };
+        ok = turn(0, tiles0, used0) && turn(1, tiles1, used1);
+        if (!ok) break;
+        release_v(v);
+        if (more) release_k(k);
       }
       if (!ok) {                           // products in flight end before the memory goes
         if (elect_one()) umma_commit(bar(bars.drain));
@@ -673,10 +616,6 @@ __global__ void __launch_bounds__(TileShape<D, kFP8>::kThreads, 1)
       const uint64_t policy = p.row_tiles > 1 ? policy_evict_last() : policy_evict_first();
       constexpr int kRowBytes = kFP8 ? D : 2 * D;
       bool ok = p.drop_producer == 0;
-      if (lane == 0) {
-        tma_prefetch_desc(&map_k);
-        tma_prefetch_desc(&map_v);
-      }
       // a ring: its slots, its barriers, how many tiles it was given
       struct Ring {
         uint32_t full, empty, base;
@@ -728,7 +667,7 @@ __global__ void __launch_bounds__(TileShape<D, kFP8>::kThreads, 1)
         return true;
       };
       for (int f = 0; f < 2 * n && ok; ++f) {
-        const Item it = item_at(f, n, lead);
+        const Item it = item_at(f, n, 1);
         ok = load(kFP8 && !it.v ? rk : rv, it.v, it.i);
       }
       if (!ok) {                           // copies in flight land before the memory goes
@@ -867,9 +806,12 @@ cudaError_t launch_t(const AttnParams& p, const CUtensorMap& mk, const CUtensorM
   cudaError_t e = cudaFuncSetAttribute(tiles_kernel<D, kFP8>,
                                        cudaFuncAttributeMaxDynamicSharedMemorySize, S::kSmem);
   if (e != cudaSuccess) return e;
-  const dim3 grid(static_cast<unsigned>(p.B) * p.c.heads * p.row_tiles, p.splits);
-  tiles_kernel<D, kFP8><<<grid, S::kThreads, S::kSmem, stream>>>(mk, mv, p);
-  return cudaGetLastError();
+  const unsigned tiles = static_cast<unsigned>(p.B) * p.c.heads * p.row_tiles;
+  cudaLaunchAttribute attr[1];
+  cudaLaunchConfig_t cfg = make_cfg(dim3(p.whole + (tiles - p.whole) * p.splits),
+                                    dim3(S::kThreads), stream, true, attr);
+  cfg.dynamicSmemBytes = S::kSmem;
+  return cudaLaunchKernelEx(&cfg, tiles_kernel<D, kFP8>, mk, mv, p);
 }
 
 }  // namespace

@@ -159,30 +159,56 @@ moe_status_t moe_paged_attention(const moe_attention_args* a, void* ws, size_t w
   const int tile_rows = !few ? kTileRows : rows <= 16 ? 16 : rows <= 32 ? 32 : rows <= 48 ? 48 : 64;
   p.row_tiles = static_cast<int>((rows + tile_rows - 1) / tile_rows);
   const long long tiles = static_cast<long long>(a->B) * p.c.heads * p.row_tiles;
-  if (tiles > 0x7fffffffll) return MOE_ERR_UNSUPPORTED;
+  if (tiles > 0x7fffffffll / 2) return MOE_ERR_UNSUPPORTED;
   p.part_rows = rows < tile_rows ? static_cast<int>((rows + 15) / 16 * 16) : tile_rows;
+  const long long part_bytes = static_cast<long long>(p.part_rows) * (D + 2) * 4;
+  const long long room_parts =
+      static_cast<long long>((ws_bytes - MOE_ATTENTION_CTRL_BYTES) / part_bytes);
   // The keys a tile may see, by the caller's hint
   long long span = a->max_kv > 0 && a->max_kv < room ? a->max_kv : room;
   if (a->window > 0 && a->window + tile_rows / group + 128 < span)
     span = a->window + tile_rows / group + 128;
-  // Parts of at least 256 keys.  Few rows: until there are about four for every
-  // place that an SM has for a CTA.  Many rows: as many as fit the SMs at once.
-  const long long most = (span + 255) / 256;
-  long long splits = few ? 2ll * sms / tiles : sms / tiles;
-  if (splits > most) splits = most;
-  const long long part_bytes = static_cast<long long>(p.part_rows) * (D + 2) * 4;
-  const long long fit =
-      static_cast<long long>((ws_bytes - MOE_ATTENTION_CTRL_BYTES) / part_bytes) / tiles;
-  if (splits > fit) splits = fit;
-  if (splits > 65535) splits = 65535;
-  if (tiles > kMaxTiles || splits < 2) splits = 1;
-  // (the last part takes whatever lies past splits * chunk)
-  p.splits = static_cast<int>(splits);
-  p.chunk = splits > 1 ? static_cast<int>(((span + splits - 1) / splits + 127) / 128 * 128)
-                       : 0x40000000;
+  const long long most = (span + 255) / 256;      // parts of at least 256 keys
   const cudaStream_t st = static_cast<cudaStream_t>(stream);
-  return cuda_status(few ? launch_attention_rows(p, tile_rows, D, fp8, st)
-                         : launch_attention_tiles(p, D, fp8, st));
+  if (few) {
+    // Parts of the same length (ragged sequences then give even work), about two for
+    // every SM.
+    long long splits = 2ll * sms / tiles;
+    if (splits > most) splits = most;
+    if (splits > room_parts / tiles) splits = room_parts / tiles;
+    if (splits > kMaxParts) splits = kMaxParts;
+    if (tiles > kMaxTiles || splits < 2) splits = 1;
+    // (the last part takes whatever lies past splits * chunk)
+    p.splits = static_cast<int>(splits);
+    p.chunk = splits > 1 ? static_cast<int>(((span + splits - 1) / splits + 127) / 128 * 128)
+                         : 0x40000000;
+    return cuda_status(launch_attention_rows(p, tile_rows, D, fp8, st));
+  }
+  // One tile per SM at a time.  The tiles past the last full round, which are the early rows,
+  // are cut into the number of parts that takes the least time by this estimate: about 1.5 us
+  // for 128 keys, and 20 us more for a part (its 133 KB written and read again; 2 x 16
+  // heads of 8192 rows and keys: 565 us whole, 623 us with the last 112 tiles in 4 parts;
+  // a 4096-row chunk at 16384 keys: 711 us whole, 688 us with its last 56 in 2).
+  const long long rest = tiles % sms;
+  long long seen = span;
+  if (a->causal != 0) {
+    const long long late = p.row_tiles - 1 - rest / (static_cast<long long>(a->B) * p.c.heads);
+    seen -= late * tile_rows / group;
+    if (seen < 0) seen = 0;
+  }
+  const double tile_us = 1.5 * static_cast<double>(seen) / 128.0;
+  long long splits = 1;
+  double best = tile_us;
+  for (long long s = 2; s <= 16 && s <= most && rest * s <= room_parts; ++s) {
+    const double us = static_cast<double>((rest * s + sms - 1) / sms) * (tile_us / s + 20.0);
+    if (us < best) {
+      best = us;
+      splits = s;
+    }
+  }
+  p.splits = static_cast<int>(splits);
+  p.whole = static_cast<int>(splits > 1 ? tiles - rest : tiles);
+  return cuda_status(launch_attention_tiles(p, D, fp8, st));
 }
 
 moe_status_t moe_verify_draft(const moe_verify_args* a, void* ws, void* stream) {
