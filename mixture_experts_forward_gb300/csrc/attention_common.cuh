@@ -145,17 +145,31 @@ __device__ __forceinline__ void join_parts(const AttnParams& p, const TileView& 
   const float ninf = __int_as_float(0xff800000);
   for (int r = tid; r < t.rows; r += threads) {
     float m = ninf, l = 0.0f;
-#pragma unroll 8
-    for (int s = 0; s < count; ++s) m = fmaxf(m, __ldcg(ml + s * stride + r));
-    const float ref = m == ninf ? 0.0f : m;
-#pragma unroll 8
-    for (int s = 0; s < count; ++s) {
-      const float w = exp2_approx(__ldcg(ml + s * stride + r) - ref);
-      weights[s * part_rows + r] = w;
-      l = fmaf(w, __ldcg(ml + s * stride + part_rows + r), l);
+    for (int s0 = 0; s0 < count; s0 += kAhead) {
+      float pm[kAhead], pl[kAhead];
+#pragma unroll
+      for (int j = 0; j < kAhead; ++j) {
+        const bool x = s0 + j < count;
+        pm[j] = x ? __ldcg(ml + (s0 + j) * stride + r) : ninf;
+        pl[j] = x ? __ldcg(ml + (s0 + j) * stride + part_rows + r) : 0.0f;
+      }
+      float top = m;
+#pragma unroll
+      for (int j = 0; j < kAhead; ++j) top = fmaxf(top, pm[j]);
+      const float ref = top == ninf ? 0.0f : top;
+      l *= exp2_approx(m - ref);
+#pragma unroll
+      for (int j = 0; j < kAhead; ++j)
+        if (s0 + j < count) {
+          l = fmaf(exp2_approx(pm[j] - ref), pl[j], l);
+          weights[(s0 + j) * part_rows + r] = pm[j];
+        }
+      m = top;
     }
+    const float ref = m == ninf ? 0.0f : m;
     const float inv = l == 0.0f ? 0.0f : 1.0f / l;
-    for (int s = 0; s < count; ++s) weights[s * part_rows + r] *= inv;
+    for (int s = 0; s < count; ++s)
+      weights[s * part_rows + r] = exp2_approx(weights[s * part_rows + r] - ref) * inv;
     if (p.lse != nullptr) *lse_at(p, t, r) = lse_of(m, l);
   }
   named_bar_sync(bar, threads);

@@ -39,9 +39,12 @@ struct RowsShape {
   static constexpr int kQTerm = N * D * (kFP8 ? 1 : 2);  // bytes of the query (of each term)
   static constexpr int kChunkRows = kFP8 ? 16 : 8;       // rows in 16 bytes of weights
   static constexpr int kPTerm = N / kChunkRows * kKeys * 16;
+  // FP8 is bound by the softmax warps as well as by HBM: two buffers of weights spare them
+  // the wait for the product before (BF16: 98 % of the copy bandwidth with one)
+  static constexpr int kPBufs = kFP8 ? 2 : 1;
   // offsets in shared memory: weights (hi, lo), query (FP8: hi, lo), the ring
   static constexpr int oP = 0;
-  static constexpr int oQ = 2 * kPTerm;
+  static constexpr int oQ = kPBufs * 2 * kPTerm;
   static constexpr int oSlots = (oQ + (kFP8 ? 2 : 1) * kQTerm + 1023) / 1024 * 1024;
   // two CTAs per SM where each still has three tiles in shared memory
   static constexpr int kHalf = 111 * 1024, kWhole = 222 * 1024;
@@ -58,7 +61,7 @@ struct RowsShape {
 template <int N, int kGroups>
 struct RowsBars {
   uint64_t full[8], empty[8];
-  uint64_t q_full, s_full[2], p_full, o_step, o_last, drain;
+  uint64_t q_full, s_full[2], p_full[2], o_step, o_last, drain;
   uint32_t tmem;
   int abort, flag;
   int lo[N], hi[N];               // keys that each row sees, in this part
@@ -159,7 +162,8 @@ __global__ void
     mbar_init(bar(bars.q_full), S::kSoftmax);
     mbar_init(bar(bars.s_full[0]), 1);
     mbar_init(bar(bars.s_full[1]), 1);
-    mbar_init(bar(bars.p_full), S::kSoftmax);
+    mbar_init(bar(bars.p_full[0]), S::kSoftmax);
+    mbar_init(bar(bars.p_full[1]), S::kSoftmax);
     mbar_init(bar(bars.o_step), 1);
     mbar_init(bar(bars.o_last), 1);
     mbar_init(bar(bars.drain), 1);
@@ -231,7 +235,7 @@ __global__ void
     const int key_lane = (warp & 3) * 32 + lane;         // key of a tile; channel of O
     const uint32_t lanes = static_cast<uint32_t>(warp & 3) << 21;
     const int page_mask = (1 << p.c.page_log2) - 1;
-    // this thread's key: its page two tiles ahead, its scales one
+    // (FP8) this thread's key: its page two tiles ahead, its scales one
     auto page_of = [&](int i) {
       const int key = k0 + i * kKeys + key_lane;
       return kFP8 && key < k1 ? __ldg(table + (key >> p.c.page_log2)) : -1;
@@ -239,11 +243,10 @@ __global__ void
     float ks_next = 0.0f, vs_next = 0.0f;
     auto fetch = [&](int i, int page) {
       if constexpr (kFP8) {
-        const int key = k0 + i * kKeys + key_lane;
         ks_next = vs_next = 0.0f;
-        if (key < k1 && page >= 0 && page < p.c.num_pages) {
-          const int64_t at = ((static_cast<int64_t>(page) * p.c.heads + h) << p.c.page_log2) +
-                             (key & page_mask);
+        if (static_cast<unsigned>(page) < static_cast<unsigned>(p.c.num_pages)) {
+          const int at = ((page * p.c.heads + h) << p.c.page_log2) +
+                         ((k0 + i * kKeys + key_lane) & page_mask);
           ks_next = __ldg(p.c.k_scales + at);
           vs_next = __ldg(p.c.v_scales + at);
         }
@@ -301,12 +304,12 @@ __global__ void
     const float ninf = __int_as_float(0xff800000);
     const float cap = p.softcap, cap_k = cap > 0.0f ? 2.0f * kLog2e / cap : 0.0f;
     const float sc = fabsf(p.scale) * (cap > 0.0f ? 1.0f : kLog2e);
-    float ref[NH], l[NH];
+    float nref[NH], l[NH];                               // minus the rows' references; sums
     uint32_t pending = 0;                                // rows that have not seen their first key
     int lo_max = k0, hi_min = k1;
 #pragma unroll
     for (int r = 0; r < NH; ++r) {
-      ref[r] = 0.0f;
+      nref[r] = 0.0f;
       l[r] = 0.0f;
       const int lo = bars.lo[w * NH + r], hi = bars.hi[w * NH + r];
       if (lo < hi) {
@@ -320,7 +323,6 @@ __global__ void
     const int group_bar = 2 + w;
     int E = 0;                                           // FP8: weights carry vs * 2^(4 - E)
     const uint32_t o_tm = tmem + lanes + 2 * N + w * NH;
-    constexpr float kFar = kFP8 ? 448.0f : 1.0e18f;
     // Per row over the tile's keys: each thread's x[r] to the maximum over the group.  (A NaN
     // is no maximum: fmaxf passes over it.)
     auto group_max = [&](float (&x)[NH]) {
@@ -352,29 +354,41 @@ __global__ void
       page_next = page_of(i + 2);
       if (ok) ok = wait(bar(bars.s_full[i & 1]), (i >> 1) & 1);
       tc_fence_after();
-      float x[NH];
+      constexpr int kWords = kFP8 ? NH / 4 : NH / 2;     // of this thread's weights, per term
+      uint32_t hi[kWords], lo[kWords];
       if (!idle) {
-        tmem_ld_cols<NH>(tmem + lanes + (i & 1) * N + w * NH, x);
+        float s[NH], x[NH];
+        tmem_ld_cols<NH>(tmem + lanes + (i & 1) * N + w * NH, s);
+        // x = s * factor * ks + add, masked
+        const bool edge = kb < lo_max || kb + kKeys > hi_min;
+        auto scaled = [&](bool shifted) {
 #pragma unroll
-        for (int r = 0; r < NH; r += 4) {
-          float4 f = make_float4(sc, sc, sc, sc);
-          if constexpr (kFP8) {
-            f = *reinterpret_cast<const float4*>(&bars.factor[w * NH + r]);
-            mul2(f.x, f.y, f.x, f.y, ks, ks);
-            mul2(f.z, f.w, f.z, f.w, ks, ks);
+          for (int r = 0; r < NH; r += 4) {
+            float4 f = make_float4(sc, sc, sc, sc);
+            if constexpr (kFP8) {
+              f = *reinterpret_cast<const float4*>(&bars.factor[w * NH + r]);
+              mul2(f.x, f.y, f.x, f.y, ks, ks);
+              mul2(f.z, f.w, f.z, f.w, ks, ks);
+            }
+            if (cap > 0.0f) {
+              const float g[4] = {f.x, f.y, f.z, f.w};
+#pragma unroll
+              for (int j = 0; j < 4; ++j)
+                x[r + j] = soft_capped(s[r + j] * g[j], cap_k, cap) * kLog2e +
+                           (shifted ? nref[r + j] : 0.0f);
+            } else {
+#pragma unroll
+              for (int j = 0; j < 4; ++j) x[r + j] = shifted ? nref[r + j] : 0.0f;
+              fma2(x[r], x[r + 1], s[r], s[r + 1], f.x, f.y);
+              fma2(x[r + 2], x[r + 3], s[r + 2], s[r + 3], f.z, f.w);
+            }
           }
-          mul2(x[r], x[r + 1], x[r], x[r + 1], f.x, f.y);
-          mul2(x[r + 2], x[r + 3], x[r + 2], x[r + 3], f.z, f.w);
-        }
-        if (cap > 0.0f) {
+          if (edge) {
 #pragma unroll
-          for (int r = 0; r < NH; ++r) x[r] = soft_capped(x[r], cap_k, cap) * kLog2e;
-        }
-        if (kb < lo_max || kb + kKeys > hi_min) {
-#pragma unroll
-          for (int r = 0; r < NH; ++r)
-            if (key < bars.lo[w * NH + r] || key >= bars.hi[w * NH + r]) x[r] = ninf;
-        }
+            for (int r = 0; r < NH; ++r)
+              if (key < bars.lo[w * NH + r] || key >= bars.hi[w * NH + r]) x[r] = ninf;
+          }
+        };
         if (pending != 0u) {
           // rows whose first keys are in this tile take its maximum as their reference
           uint32_t now = 0;
@@ -383,46 +397,81 @@ __global__ void
             if (bars.lo[w * NH + r] < kb + kKeys) now |= 1u << r;
           now &= pending;
           if (now != 0u) {
-            float top[NH];
-#pragma unroll
-            for (int r = 0; r < NH; ++r) top[r] = x[r];
-            group_max(top);
+            scaled(false);
+            group_max(x);
 #pragma unroll
             for (int r = 0; r < NH; ++r)
-              if (now >> r & 1u) ref[r] = top[r] > ninf ? top[r] : 0.0f;
+              if (now >> r & 1u) nref[r] = x[r] > ninf ? -x[r] : 0.0f;
             // (the first tile has the first keys of some row, or no row of the group sees any)
             if (kFP8 && pending == seeing) E = group_exponent(vs);
             pending &= ~now;
           }
         }
-        float vw = kFP8 ? vs * exp2_approx(static_cast<float>(4 - E)) : 1.0f;
-        float e[NH];
-        float most = 0.0f;
+        // the weights x (FP8: with the value scale), their two terms, and whether one is
+        // beyond its type
+        auto weigh = [&]() -> bool {
+          scaled(true);
 #pragma unroll
-        for (int r = 0; r < NH; ++r) {
-          e[r] = exp2_approx(x[r] - ref[r]);
-          most = fmaxf(most, e[r]);
-        }
-        if (named_bar_any(group_bar, 128, most * vw > kFar)) {
-          float top[NH];
+          for (int r = 0; r < NH; ++r) x[r] = exp2_approx(x[r]);
+          if constexpr (kFP8) {
+            const float vw = vs * exp2_approx(static_cast<float>(4 - E));
+            __half2 most = __float2half2_rn(0.0f);
 #pragma unroll
-          for (int r = 0; r < NH; ++r) top[r] = x[r];
-          group_max(top);
+            for (int j = 0; j < NH / 4; ++j) {
+              uint32_t hw = 0, lw = 0;
+#pragma unroll
+              for (int k = 0; k < 2; ++k) {
+                float a, c;
+                mul2(a, c, x[4 * j + 2 * k], x[4 * j + 2 * k + 1], vw, vw);
+                const uint16_t hc = cvt_e4m3x2(a, c);
+                const uint32_t back = e4m3x2_to_f16x2(hc);
+                const __half2 full = __floats2half2_rn(a, c);
+                most = __hmax2(most, full);
+                __half2 d = __hsub2(full, *reinterpret_cast<const __half2*>(&back));
+                d = __hmul2(d, __float2half2_rn(16.0f));
+                uint16_t lc;
+                asm("cvt.rn.satfinite.e4m3x2.f16x2 %0, %1;"
+                    : "=h"(lc)
+                    : "r"(*reinterpret_cast<uint32_t*>(&d)));
+                hw |= static_cast<uint32_t>(hc) << (16 * k);
+                lw |= static_cast<uint32_t>(lc) << (16 * k);
+              }
+              hi[j] = hw;
+              lo[j] = lw;
+            }
+            return fmaxf(__low2float(most), __high2float(most)) > 448.0f;
+          } else {
+            float most = 0.0f;
+#pragma unroll
+            for (int j = 0; j < NH / 2; ++j) {
+              most = fmaxf(most, fmaxf(x[2 * j], x[2 * j + 1]));
+              __nv_bfloat162 hh = __floats2bfloat162_rn(x[2 * j], x[2 * j + 1]);
+              const float2 back = __bfloat1622float2(hh);
+              __nv_bfloat162 ll = __floats2bfloat162_rn(x[2 * j] - back.x, x[2 * j + 1] - back.y);
+              hi[j] = *reinterpret_cast<uint32_t*>(&hh);
+              lo[j] = *reinterpret_cast<uint32_t*>(&ll);
+            }
+            return most > 1.0e18f;
+          }
+        };
+        bool far = weigh();
+        if (named_bar_any(group_bar, 128, far)) {
+          scaled(false);
+          group_max(x);
           const int E2 = kFP8 ? group_exponent(vs) : 0;
           if (ok && i > 0) ok = wait(bar(bars.o_step), (i - 1) & 1);
           tc_fence_after();
           const float unit = kFP8 ? exp2_approx(static_cast<float>(E - E2)) : 1.0f;
-          float g[NH];
+          const uint32_t started = seeing & ~pending;
 #pragma unroll
           for (int r = 0; r < NH; ++r) {
-            const float want = fmaxf(ref[r], top[r]);
-            g[r] = (seeing & ~pending) >> r & 1u ? exp2_approx(ref[r] - want) : 1.0f;
-            if ((seeing & ~pending) >> r & 1u) ref[r] = want;
-            l[r] *= g[r];
-            g[r] *= unit;
+            const float want = fminf(nref[r], -x[r]);
+            const bool moves = started >> r & 1u;
+            x[r] = moves ? exp2_approx(want - nref[r]) : 1.0f;       // the row's sums shrink
+            if (moves) nref[r] = want;
+            l[r] *= x[r];
           }
           E = E2;
-          vw = kFP8 ? vs * exp2_approx(static_cast<float>(4 - E)) : 1.0f;
           if (i > 0) {
 #pragma unroll
             for (int term = 0; term < (kFP8 ? 2 : 1); ++term) {
@@ -430,61 +479,23 @@ __global__ void
               tmem_ld_cols<NH>(o_tm + term * N, o);
               uint32_t u[NH];
 #pragma unroll
-              for (int r = 0; r < NH; ++r) u[r] = __float_as_uint(o[r] * g[r]);
+              for (int r = 0; r < NH; ++r) u[r] = __float_as_uint(o[r] * x[r] * unit);
               tmem_st_cols<NH>(o_tm + term * N, u);
             }
             tmem_st_wait();
           }
-#pragma unroll
-          for (int r = 0; r < NH; ++r) e[r] = exp2_approx(x[r] - ref[r]);
+          weigh();
         }
 #pragma unroll
-        for (int r = 0; r < NH; ++r) {
-          l[r] += e[r];
-          if constexpr (kFP8) e[r] *= vw;
-        }
-#pragma unroll
-        for (int r = 0; r < NH; ++r) x[r] = e[r];
+        for (int r = 0; r < NH; r += 2) add2(l[r], l[r + 1], x[r], x[r + 1]);
       }
-      // the last product has read the weights before (that of the tile before it is complete: it
-      // came before these scores)
-      if (ok && i > 0) ok = wait(bar(bars.o_step), (i - 1) & 1);
+      // one buffer of weights: the last product has read those before (that of the tile before it
+      // is complete: it came before these scores)
+      if (S::kPBufs == 1 && ok && i > 0) ok = wait(bar(bars.o_step), (i - 1) & 1);
       if (!idle) {
-        uint32_t hi[kFP8 ? NH / 4 : NH / 2], lo[kFP8 ? NH / 4 : NH / 2];
-        if constexpr (kFP8) {
-#pragma unroll
-          for (int j = 0; j < NH / 4; ++j) {
-            uint32_t hw = 0, lw = 0;
-#pragma unroll
-            for (int k = 0; k < 2; ++k) {
-              const float a = x[4 * j + 2 * k], c = x[4 * j + 2 * k + 1];
-              const uint16_t hc = cvt_e4m3x2(a, c);
-              uint32_t back = e4m3x2_to_f16x2(hc);
-              __half2 d = __hsub2(__floats2half2_rn(a, c), *reinterpret_cast<__half2*>(&back));
-              d = __hmul2(d, __float2half2_rn(16.0f));
-              uint16_t lc;
-              asm("cvt.rn.satfinite.e4m3x2.f16x2 %0, %1;"
-                  : "=h"(lc)
-                  : "r"(*reinterpret_cast<uint32_t*>(&d)));
-              hw |= static_cast<uint32_t>(hc) << (16 * k);
-              lw |= static_cast<uint32_t>(lc) << (16 * k);
-            }
-            hi[j] = hw;
-            lo[j] = lw;
-          }
-        } else {
-#pragma unroll
-          for (int j = 0; j < NH / 2; ++j) {
-            __nv_bfloat162 hh = __floats2bfloat162_rn(x[2 * j], x[2 * j + 1]);
-            const float2 back = __bfloat1622float2(hh);
-            __nv_bfloat162 ll = __floats2bfloat162_rn(x[2 * j] - back.x, x[2 * j + 1] - back.y);
-            hi[j] = *reinterpret_cast<uint32_t*>(&hh);
-            lo[j] = *reinterpret_cast<uint32_t*>(&ll);
-          }
-        }
-        // [term][chunk of rows][key][16 bytes]
-        constexpr int kWords = (kFP8 ? NH / 4 : NH / 2);           // of this thread, per term
-        const uint32_t at = sbase + S::oP + w * NH / S::kChunkRows * (kKeys * 16) + key_lane * 16 +
+        // [buffer][term][chunk of rows][key][16 bytes]
+        const uint32_t at = sbase + S::oP + (S::kPBufs == 2 ? (i & 1) * 2 * S::kPTerm : 0) +
+                            w * NH / S::kChunkRows * (kKeys * 16) + key_lane * 16 +
                             (kWords < 4 ? w * kWords * 4 : 0);
 #pragma unroll
         for (int term = 0; term < 2; ++term) {
@@ -505,7 +516,7 @@ __global__ void
         fence_async_smem();
       }
       tc_fence_before();
-      mbar_arrive(bar(bars.p_full));
+      mbar_arrive(bar(bars.p_full[i & 1]));
     }
     if (ok && n > 0) ok = wait(bar(bars.o_last), 0);
     tc_fence_after();
@@ -533,7 +544,7 @@ __global__ void
       if ((lane & (32 / NH - 1)) == 0) bars.part[w][warp & 3][lane / (32 / NH)] = sum;
       float mine = 0.0f;                                 // the reference of row key_lane
 #pragma unroll
-      for (int r = 0; r < NH; ++r) mine = key_lane == r ? ref[r] : mine;
+      for (int r = 0; r < NH; ++r) mine = key_lane == r ? -nref[r] : mine;
       named_bar_sync(group_bar, 128);
       if (key_lane < NH) {
         const int row = w * NH + key_lane;
@@ -632,6 +643,7 @@ __global__ void
       auto values = [&](int i) {
         const uint32_t a = v_lo + slot * (S::kTileBytes >> 4);
         const bool first = i == 0;
+        const uint32_t pb = p_lo + (S::kPBufs == 2 ? (i & 1) * (2 * S::kPTerm >> 4) : 0);
         const int s0 = first ? first_step : 0, s1 = i + 1 == tiles ? last_steps : kSteps;
         tc_fence_after();
         if (elect_one()) {
@@ -640,14 +652,14 @@ __global__ void
             for (int x = 0; x < 2 * kSteps; ++x) {       // the weights' hi, then lo
               const int s = x % kSteps, term = x / kSteps;
               umma_ss<kFP8>(tm + 2 * N + (kFP8 ? term * N : 0), a + s * kVStep, kTileHi,
-                            p_lo + term * (S::kPTerm >> 4) + s * kPStep, kPHi, idesc_o,
+                            pb + term * (S::kPTerm >> 4) + s * kPStep, kPHi, idesc_o,
                             (kFP8 ? s > 0 : x > 0) ? 1u : (first ? 0u : 1u));
             }
           } else {
             for (int term = 0; term < 2; ++term)
               for (int s = s0; s < s1; ++s)
                 umma_ss<kFP8>(tm + 2 * N + (kFP8 ? term * N : 0), a + s * kVStep, kTileHi,
-                              p_lo + term * (S::kPTerm >> 4) + s * kPStep, kPHi, idesc_o,
+                              pb + term * (S::kPTerm >> 4) + s * kPStep, kPHi, idesc_o,
                               (s > s0 || (!kFP8 && term > 0)) ? 1u : (first ? 0u : 1u));
           }
         }
@@ -681,7 +693,7 @@ __global__ void
         if (ok) scores(i);
       }
       for (int i = 0; i < tiles && ok; ++i) {
-        ok = wait_tile() && wait(bar(bars.p_full), i & 1);
+        ok = wait_tile() && wait(bar(bars.p_full[0]) + 8 * (i & 1), (i >> 1) & 1);
         if (!ok) break;
         clean(i);
         values(i);
@@ -775,6 +787,15 @@ cudaError_t launch_d(const AttnParams& p, int tile_rows, const CUtensorMap& mk,
 }
 
 }  // namespace
+
+int attention_rows_places(int tile_rows, int head_dim, bool fp8) {
+  if (tile_rows > 32) return 1;
+  if (tile_rows == 16)
+    return head_dim == 128 ? (fp8 ? RowsShape<128, true, 16>::kCtas : RowsShape<128, false, 16>::kCtas)
+                           : (fp8 ? RowsShape<64, true, 16>::kCtas : RowsShape<64, false, 16>::kCtas);
+  return head_dim == 128 ? (fp8 ? RowsShape<128, true, 32>::kCtas : RowsShape<128, false, 32>::kCtas)
+                         : (fp8 ? RowsShape<64, true, 32>::kCtas : RowsShape<64, false, 32>::kCtas);
+}
 
 cudaError_t launch_attention_rows(const AttnParams& p, int tile_rows, int head_dim, bool fp8,
                                   cudaStream_t stream) {

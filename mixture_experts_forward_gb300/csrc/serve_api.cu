@@ -171,9 +171,9 @@ moe_status_t moe_paged_attention(const moe_attention_args* a, void* ws, size_t w
   const long long most = (span + 255) / 256;      // parts of at least 256 keys
   const cudaStream_t st = static_cast<cudaStream_t>(stream);
   if (few) {
-    // Parts of the same length (ragged sequences then give even work), about two for
-    // every SM.
-    long long splits = 2ll * sms / tiles;
+    // Parts of the same length (ragged sequences then give even work), as many as the SMs
+    // have places for CTAs.
+    long long splits = static_cast<long long>(attention_rows_places(tile_rows, D, fp8)) * sms / tiles;
     if (splits > most) splits = most;
     if (splits > room_parts / tiles) splits = room_parts / tiles;
     if (splits > kMaxParts) splits = kMaxParts;

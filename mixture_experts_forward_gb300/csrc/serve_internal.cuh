@@ -64,6 +64,7 @@ cudaError_t launch_kv_read(const KvCacheView& c, int head_dim, bool fp8, const i
 // Parts of a tile at most.
 constexpr int kMaxParts = 192;
 // Up to 16, 32, 48 or 64 rows per tile (tile_rows), tcgen05 with keys and channels as the rows.
+int attention_rows_places(int tile_rows, int head_dim, bool fp8);   // CTAs per SM
 cudaError_t launch_attention_rows(const AttnParams& p, int tile_rows, int head_dim, bool fp8,
                                   cudaStream_t stream);
 // Up to 256 rows per tile, tcgen05.
