@@ -85,7 +85,8 @@ struct Bars {
   int e[3];                       // FP8: exponent of each tile's value scales
 };
 
-template <int D, bool kFP8>
+// kCap: scores are capped (a form of its own: its registers are not the common one's).
+template <int D, bool kFP8, bool kCap>
 __global__ void __launch_bounds__(TileShape<D, kFP8>::kThreads, 1)
     tiles_kernel(const __grid_constant__ CUtensorMap map_k,
                  const __grid_constant__ CUtensorMap map_v, const AttnParams p) {
@@ -255,8 +256,8 @@ __global__ void __launch_bounds__(TileShape<D, kFP8>::kThreads, 1)
     r_hi = min(r_hi, k1);
     const bool idle = w * kRows + (warp & 3) * 32 >= t.rows;
     const int my_n = w == 0 ? n0 : n1;
-    const float cap = p.softcap, cap_k = cap > 0.0f ? 2.0f * kLog2e / cap : 0.0f;
-    float sc = fabsf(p.scale) * (cap > 0.0f ? 1.0f : kLog2e);
+    const float cap = p.softcap;
+    float sc = fabsf(p.scale);                       // of the scores
     bool ok = true;
     if constexpr (kFP8) {
       if (my_n > 0) {
@@ -265,7 +266,8 @@ __global__ void __launch_bounds__(TileShape<D, kFP8>::kThreads, 1)
       }
     }
     const float ninf = __int_as_float(0xff800000);
-    const float f = cap > 0.0f ? 1.0f : sc;          // from s (or capped scores) to log2 units
+    const float cap_k = kCap ? sc / cap : 0.0f;
+    const float f = (kCap ? cap : sc) * kLog2e;   // from s (or tanh) to log2 units
     constexpr float kFar = kFP8 ? 16384.0f : 1.0e18f;
     float ref = 0.0f, l = 0.0f;
     bool started = false;                            // the row has seen a key
@@ -292,9 +294,21 @@ __global__ void __launch_bounds__(TileShape<D, kFP8>::kThreads, 1)
         }
         e = bars.e[sslot];
       }
-      if (cap > 0.0f) {
+      if constexpr (kCap) {
+        // s becomes tanh(score / cap).  Where every score of the warp's rows is below 0.8 cap,
+        // by a polynomial in packed arithmetic: the two special functions per score of the
+        // general form take 8 cycles of their unit, twice an exponential's.
+        float most = 0.0f;
 #pragma unroll
-        for (int j = 0; j < kCols; ++j) s[j] = soft_capped(s[j] * sc, cap_k, cap) * kLog2e;
+        for (int j = 0; j < kCols; ++j) most = fmaxf(most, fabsf(s[j]));
+        if (__all_sync(0xffffffffu, most * cap_k <= kTanhEnd)) {
+#pragma unroll
+          for (int j = 0; j < kCols; j += 2) tanh2(s[j], s[j + 1], cap_k);
+        } else {
+#pragma unroll
+          for (int j = 0; j < kCols; ++j)
+            s[j] = 1.0f - 2.0f * rcp_approx(exp2_approx(s[j] * (2.0f * kLog2e * cap_k)) + 1.0f);
+        }
       }
       if (kb + kCols > r_hi || kb < r_lo) {
         const int lo = r_lo - kb, hi = r_hi - kb;
@@ -799,11 +813,11 @@ __global__ void __launch_bounds__(TileShape<D, kFP8>::kThreads, 1)
   if (warp == 9) tmem_dealloc(tmem, 512);
 }
 
-template <int D, bool kFP8>
+template <int D, bool kFP8, bool kCap>
 cudaError_t launch_t(const AttnParams& p, const CUtensorMap& mk, const CUtensorMap& mv,
                      cudaStream_t stream) {
   using S = TileShape<D, kFP8>;
-  cudaError_t e = cudaFuncSetAttribute(tiles_kernel<D, kFP8>,
+  cudaError_t e = cudaFuncSetAttribute(tiles_kernel<D, kFP8, kCap>,
                                        cudaFuncAttributeMaxDynamicSharedMemorySize, S::kSmem);
   if (e != cudaSuccess) return e;
   const unsigned tiles = static_cast<unsigned>(p.B) * p.c.heads * p.row_tiles;
@@ -811,7 +825,14 @@ cudaError_t launch_t(const AttnParams& p, const CUtensorMap& mk, const CUtensorM
   cudaLaunchConfig_t cfg = make_cfg(dim3(p.whole + (tiles - p.whole) * p.splits),
                                     dim3(S::kThreads), stream, true, attr);
   cfg.dynamicSmemBytes = S::kSmem;
-  return cudaLaunchKernelEx(&cfg, tiles_kernel<D, kFP8>, mk, mv, p);
+  return cudaLaunchKernelEx(&cfg, tiles_kernel<D, kFP8, kCap>, mk, mv, p);
+}
+
+template <int D, bool kFP8>
+cudaError_t launch_c(const AttnParams& p, const CUtensorMap& mk, const CUtensorMap& mv,
+                     cudaStream_t stream) {
+  return p.softcap > 0.0f ? launch_t<D, kFP8, true>(p, mk, mv, stream)
+                          : launch_t<D, kFP8, false>(p, mk, mv, stream);
 }
 
 }  // namespace
@@ -821,10 +842,10 @@ cudaError_t launch_attention_tiles(const AttnParams& p, int head_dim, bool fp8,
   CUtensorMap mk, mv;
   if (!cache_maps(p, head_dim, fp8, &mk, &mv)) return cudaErrorInvalidValue;
   if (fp8)
-    return head_dim == 128 ? launch_t<128, true>(p, mk, mv, stream)
-                           : launch_t<64, true>(p, mk, mv, stream);
-  return head_dim == 128 ? launch_t<128, false>(p, mk, mv, stream)
-                         : launch_t<64, false>(p, mk, mv, stream);
+    return head_dim == 128 ? launch_c<128, true>(p, mk, mv, stream)
+                           : launch_c<64, true>(p, mk, mv, stream);
+  return head_dim == 128 ? launch_c<128, false>(p, mk, mv, stream)
+                         : launch_c<64, false>(p, mk, mv, stream);
 }
 
 }  // namespace moe
