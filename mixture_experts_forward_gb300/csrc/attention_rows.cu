@@ -162,8 +162,8 @@ __global__ void
     mbar_init(bar(bars.q_full), S::kSoftmax);
     mbar_init(bar(bars.s_full[0]), 1);
     mbar_init(bar(bars.s_full[1]), 1);
-    mbar_init(bar(bars.p_full[0]), S::kSoftmax);
-    mbar_init(bar(bars.p_full[1]), S::kSoftmax);
+    mbar_init(bar(bars.p_full[0]), S::kSoftmax / 32);
+    mbar_init(bar(bars.p_full[1]), S::kSoftmax / 32);
     mbar_init(bar(bars.o_step), 1);
     mbar_init(bar(bars.o_last), 1);
     mbar_init(bar(bars.drain), 1);
@@ -516,7 +516,8 @@ __global__ void
         fence_async_smem();
       }
       tc_fence_before();
-      mbar_arrive(bar(bars.p_full[i & 1]));
+      __syncwarp();
+      if (lane == 0) mbar_arrive(bar(bars.p_full[i & 1]));   // (32 arrivals take a hundred cycles)
     }
     if (ok && n > 0) ok = wait(bar(bars.o_last), 0);
     tc_fence_after();

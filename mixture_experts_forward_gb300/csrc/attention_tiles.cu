@@ -65,10 +65,11 @@ struct TileShape {
   static constexpr int oScale = oRaw + kRawSlots * kCodeBytes;         // [slot][ks f32 | vs * 2^-e f16x2]
   static constexpr int oRowf = oScale + (kFP8 ? kScaleSlots * 1024 : 0);
   static constexpr int kSmem = oRowf + (kFP8 ? 1024 : 0);
-  // setmaxnreg shares: softmax, the rest (BF16: 384 x 168 registers at launch, 2 x 128 x 208 +
-  // 128 x 80 = 63488 of 64512; FP8: 512 x 128, 2 x 128 x 192 + 2 x 128 x 64 = 65536)
-  static constexpr int kRegsSoftmax = kFP8 ? 192 : 208;
-  static constexpr int kRegsOther = kFP8 ? 64 : 80;
+  // setmaxnreg shares: softmax, the rest (BF16: 384 x 168 registers at launch, 2 x 128 x 200 +
+  // 128 x 96 = 63488 of 64512; FP8: 512 x 128, 2 x 128 x 184 + 2 x 128 x 72 = 65536).  With 80
+  // for BF16's rest the MMA warp spills: 681 instead of 666 us for 4096 rows at 16384 keys.
+  static constexpr int kRegsSoftmax = kFP8 ? 184 : 200;
+  static constexpr int kRegsOther = kFP8 ? 72 : 96;
 };
 
 struct Bars {
@@ -99,7 +100,7 @@ __global__ void __launch_bounds__(TileShape<D, kFP8>::kThreads, 1)
   auto bar = [&](const uint64_t& x) { return smem_u32(&x); };
   if (tid == 0) {
     for (int i = 0; i < S::kSlots; ++i) {
-      mbar_init(bar(bars.full[i]), kFP8 ? 128 : 1);
+      mbar_init(bar(bars.full[i]), kFP8 ? 4 : 1);
       mbar_init(bar(bars.empty[i]), 1);
     }
     for (int i = 0; i < S::kKSlots; ++i) {
@@ -108,12 +109,12 @@ __global__ void __launch_bounds__(TileShape<D, kFP8>::kThreads, 1)
     }
     for (int i = 0; i < S::kRawSlots; ++i) {
       mbar_init(bar(bars.raw_full[i]), 1);
-      mbar_init(bar(bars.raw_empty[i]), 128);
+      mbar_init(bar(bars.raw_empty[i]), 4);
     }
     mbar_init(bar(bars.q_full), 256);
     for (int w = 0; w < 2; ++w) {
       mbar_init(bar(bars.s_full[w]), 1);
-      mbar_init(bar(bars.p_full[w]), 128);
+      mbar_init(bar(bars.p_full[w]), 4);
       mbar_init(bar(bars.o_done[w]), 1);
     }
     for (int i = 0; i < S::kScaleSlots; ++i) {
@@ -395,12 +396,13 @@ __global__ void __launch_bounds__(TileShape<D, kFP8>::kThreads, 1)
       if (!ok) break;
       tc_fence_after();
       if (!idle) tile(i, k0 + i * kKeys, sslot);
+      // (one arrival per warp: 32 on one barrier take a hundred cycles)
       tc_fence_before();
-      if constexpr (kFP8) {
-        __syncwarp();
-        if (lane == 0) mbar_arrive(bar(bars.sc_empty[sslot]));
+      __syncwarp();
+      if (lane == 0) {
+        mbar_arrive(bar(bars.p_full[w]));
+        if (kFP8) mbar_arrive(bar(bars.sc_empty[sslot]));
       }
-      mbar_arrive(bar(bars.p_full[w]));
     }
     if constexpr (kFP8) {
       // the key tiles that this group does not see: their scales are done with
@@ -798,10 +800,12 @@ __global__ void __launch_bounds__(TileShape<D, kFP8>::kThreads, 1)
                        : "memory");
         }
         fence_async_smem();
-        mbar_arrive(bar(bars.full[0]) + 8 * slot);
-        mbar_arrive(bar(bars.raw_empty[0]) + 8 * rslot);
         __syncwarp();
-        if (lane == 0) mbar_arrive(bar(bars.sc_empty[0]) + 8 * sslot);
+        if (lane == 0) {
+          mbar_arrive(bar(bars.full[0]) + 8 * slot);
+          mbar_arrive(bar(bars.raw_empty[0]) + 8 * rslot);
+          mbar_arrive(bar(bars.sc_empty[0]) + 8 * sslot);
+        }
         if (++rslot == S::kRawSlots) { rslot = 0; rpar ^= 1; }
         if (++slot == S::kSlots) { slot = 0; par ^= 1; }
         if (++sslot == S::kScaleSlots) { sslot = 0; spar ^= 1; }
