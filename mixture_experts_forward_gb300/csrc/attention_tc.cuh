@@ -98,26 +98,6 @@ __device__ __forceinline__ void add2(float& d0, float& d1, float a0, float a1) {
       : "f"(a0), "f"(a1));
 }
 
-// (a0, a1) = tanh(k a0), tanh(k a1) for |k a| <= kTanhEnd: t + t s q(s), s = t^2, q the
-// polynomial of degree 5 that meets (tanh(t)/t - 1)/s at the Chebyshev points of
-// [0, kTanhEnd^2]; largest error 5.2e-8 in binary32.
-constexpr float kTanhEnd = 0.8f;
-__device__ __forceinline__ void tanh2(float& a0, float& a1, float k) {
-  constexpr float c[6] = {-3.333333135e-01f, 1.333306283e-01f, -5.391799286e-02f, 2.152135596e-02f, -7.734463084e-03f, 1.762877218e-03f};
-  float s0, s1, q0 = c[5], q1 = c[5];
-  mul2(a0, a1, a0, a1, k, k);
-  mul2(s0, s1, a0, a1, a0, a1);
-#pragma unroll
-  for (int i = 4; i >= 0; --i) {
-    float r0 = c[i], r1 = c[i];
-    fma2(r0, r1, q0, q1, s0, s1);
-    q0 = r0;
-    q1 = r1;
-  }
-  mul2(q0, q1, q0, q1, s0, s1);
-  fma2(a0, a1, q0, q1, a0, a1);
-}
-
 // D[tmem] (+)= A[smem] * B[smem]^T over 32 E4M3 elements, K-major tiles of codes.
 template <int D>
 __device__ __forceinline__ void umma_codes(uint32_t d_tmem, uint32_t a_lo, uint32_t b_lo,

@@ -267,7 +267,7 @@ __global__ void __launch_bounds__(TileShape<D, kFP8>::kThreads, 1)
       }
     }
     const float ninf = __int_as_float(0xff800000);
-    const float cap_k = kCap ? sc / cap : 0.0f;
+    const float cap_k = kCap ? 2.0f * kLog2e * sc / cap : 0.0f;
     const float f = (kCap ? cap : sc) * kLog2e;   // from s (or tanh) to log2 units
     constexpr float kFar = kFP8 ? 16384.0f : 1.0e18f;
     float ref = 0.0f, l = 0.0f;
@@ -295,27 +295,43 @@ __global__ void __launch_bounds__(TileShape<D, kFP8>::kThreads, 1)
         }
         e = bars.e[sslot];
       }
+      // the scores of keys that the row does not see become x
+      const bool edge = kb + kCols > r_hi || kb < r_lo;
+      auto hide = [&](float x) {
+        // a bit for each key that the row sees, 32 keys at a time
+#pragma unroll
+        for (int q = 0; q < kCols / 32; ++q) {
+          const int lo = min(max(r_lo - kb - 32 * q, 0), 32), hi = min(max(r_hi - kb - 32 * q, 0), 32);
+          const uint32_t below_hi = hi == 32 ? 0xffffffffu : (1u << hi) - 1u;
+          const uint32_t seen = lo == 32 ? 0u : below_hi & (0xffffffffu << lo);
+#pragma unroll
+          for (int j = 0; j < 32; ++j)
+            if ((seen >> j & 1u) == 0u) s[32 * q + j] = x;
+        }
+      };
       if constexpr (kCap) {
-        // s becomes tanh(score / cap).  Where every score of the warp's rows is below 0.8 cap,
-        // by a polynomial in packed arithmetic: the two special functions per score of the
-        // general form take 8 cycles of their unit, twice an exponential's.
-        float most = 0.0f;
+        // s becomes tanh(score / cap) = 1 - 2 / (e + 1), e = exp(2 score / cap), with one
+        // reciprocal for four scores (e is cut at 2^31, where tanh is 1, so four
+        // factors stay finite): 1.25 special functions and 6 other operations per score.
+        // (One reciprocal each: 8 cycles of their unit; a polynomial of degree 13: 9
+        // operations, and a bound on the scores first.)  What lies past the last key may be a NaN
+        // and must not reach its neighbours; one in a score that is seen stays one.
+        if (edge) hide(0.0f);
 #pragma unroll
-        for (int j = 0; j < kCols; ++j) most = fmaxf(most, fabsf(s[j]));
-        if (__all_sync(0xffffffffu, most * cap_k <= kTanhEnd)) {
+        for (int j = 0; j < kCols; j += 4) {
+          float d[4];
 #pragma unroll
-          for (int j = 0; j < kCols; j += 2) tanh2(s[j], s[j + 1], cap_k);
-        } else {
-#pragma unroll
-          for (int j = 0; j < kCols; ++j)
-            s[j] = 1.0f - 2.0f * rcp_approx(exp2_approx(s[j] * (2.0f * kLog2e * cap_k)) + 1.0f);
+          for (int q = 0; q < 4; ++q) d[q] = exp2_approx(min_nan(s[j + q] * cap_k, 31.0f)) + 1.0f;
+          const float ab = d[0] * d[1], cd = d[2] * d[3];
+          const float r = rcp_approx(ab * cd);
+          const float rab = -2.0f * r * cd, rcd = -2.0f * r * ab;
+          s[j] = fmaf(rab, d[1], 1.0f);
+          s[j + 1] = fmaf(rab, d[0], 1.0f);
+          s[j + 2] = fmaf(rcd, d[3], 1.0f);
+          s[j + 3] = fmaf(rcd, d[2], 1.0f);
         }
       }
-      if (kb + kCols > r_hi || kb < r_lo) {
-        const int lo = r_lo - kb, hi = r_hi - kb;
-#pragma unroll
-        for (int j = 0; j < kCols; ++j) s[j] = (j < lo || j >= hi) ? ninf : s[j];
-      }
+      if (edge) hide(ninf);
       auto row_max = [&]() {
         float x[4] = {s[0], s[1], s[2], s[3]};
 #pragma unroll

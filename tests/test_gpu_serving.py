@@ -264,6 +264,37 @@ def test_scores_far_from_zero(D, fp8, sign, q_len, window):
 
 
 @pytest.mark.parametrize("D,fp8", FORMS)
+@pytest.mark.parametrize("q_len", [2, 150])
+@pytest.mark.parametrize("softcap", [0.0, 20.0])
+def test_a_nan_reaches_its_rows_and_no_others(D, fp8, q_len, softcap):
+    """A NaN in one query row, and in a key that only the last rows see: those rows
+    are NaN, the rows before it are not (scores are masked before they meet a sum)."""
+    n = 300
+    k, v = rand_bf16(n, 1, D, seed=1), rand_bf16(n, 1, D, seed=2)
+    k[n - 1, 0, 5] = math.nan
+    q = rand_bf16(q_len, 2, D, seed=3)
+    q[0, 1, 7] = math.nan
+    c = R.Paged([k.nan_to_num(0.0)], [v], 16, fp8)
+    last = R.Paged([k], [v], 16, False) if not fp8 else None
+    if fp8:                                   # the NaN code in the last key
+        pos = n - 1
+        c.k[c.table[0, pos // 16], 0, pos % 16, 5] = R.NAN_CODE
+    else:
+        c = last
+    ws = attention_ws()
+    out, lse = L.paged_attention(q.cuda(), c.k, c.v, c.table, cu([q_len]), i32([n]), ws, max_q=q_len,
+                                 k_scales=c.ks, v_scales=c.vs, softcap=softcap, lse=True)
+    assert L.get_error(ws) == L.MOE_OK
+    bad = torch.isnan(out.float()).all(-1).cpu()
+    some = torch.isnan(out.float()).any(-1).cpu()
+    want = torch.zeros(q_len, 2, dtype=torch.bool)
+    want[0, 1] = True
+    want[q_len - 1] = True
+    assert torch.equal(some, want) and torch.equal(bad, want)
+    assert torch.equal(torch.isnan(lse).cpu(), want)
+
+
+@pytest.mark.parametrize("D,fp8", FORMS)
 def test_negative_scale(D, fp8):
     check_attention([3, 200], [300, 333], 4, 2, D, 32, fp8, scale=-0.11)
 
