@@ -314,9 +314,19 @@ __global__ void __launch_bounds__(TileShape<D, kFP8>::kThreads, 1)
         // reciprocal for four scores (e is cut at 2^31, where tanh is 1, so four
         // factors stay finite): 1.25 special functions and 6 other operations per score.
         // (One reciprocal each: 8 cycles of their unit; a polynomial of degree 13: 9
-        // operations, and a bound on the scores first.)  What lies past the last key may be a NaN
-        // and must not reach its neighbours; one in a score that is seen stays one.
-        if (edge) hide(0.0f);
+        // operations, and a bound on the scores first.)  A NaN in a
+        // score that the row does not see (past the last key anything may lie) must not reach
+        // its neighbours: a sum finds it, and the hidden scores become 0.
+        if (edge) {
+          float x[4] = {s[0], s[1], s[2], s[3]};
+#pragma unroll
+          for (int j = 4; j < kCols; j += 4) {
+            add2(x[0], x[1], s[j], s[j + 1]);
+            add2(x[2], x[3], s[j + 2], s[j + 3]);
+          }
+          const float all = (x[0] + x[1]) + (x[2] + x[3]);
+          if (all != all) hide(0.0f);
+        }
 #pragma unroll
         for (int j = 0; j < kCols; j += 4) {
           float d[4];
