@@ -24,6 +24,7 @@
 // each); then one warp loads and one issues the MMAs.  Scores are double-buffered in
 // tensor memory.  Up to 32 rows two CTAs share an SM.
 #include <cstring>
+#include <type_traits>
 
 #include "attention_tc.cuh"
 
@@ -50,17 +51,21 @@ struct RowsShape {
   static constexpr int kHalf = 111 * 1024, kWhole = 222 * 1024;
   static constexpr int kCtas = N <= 32 && (kHalf - oSlots) / kTileBytes >= 3 ? 2 : 1;
   static constexpr int kFit = ((kCtas == 2 ? kHalf : kWhole) - oSlots) / kTileBytes;
-  static constexpr int kSlots = kFit > 8 ? 8 : kFit;
+  static constexpr int kSlots = kFit > 12 ? 12 : kFit;
   static constexpr int kSmem = oSlots + kSlots * kTileBytes;
-  static constexpr int kTmem = N == 48 ? 256 : 4 * N;    // S twice, O (FP8: hi and lo)
+  // tensor memory: S twice, O (FP8: hi and lo)
+  static constexpr int oO = 2 * N;
+  static constexpr int kTmemUsed = oO + 2 * N;
+  static constexpr int kTmem = kTmemUsed <= 64 ? 64 : kTmemUsed <= 128 ? 128 : kTmemUsed <= 256 ? 256 : 512;
   static_assert(kSlots >= 3, "two tiles of keys and one of values");
+  static_assert(kCtas * kTmem <= 512, "tensor memory");
   static_assert(kSlots * kTileBytes >= kMaxParts * N * 4, "the joining weights fit the ring");
   static_assert(oQ % 1024 == 0, "swizzled tiles start on 1024 bytes");
 };
 
 template <int N, int kGroups>
 struct RowsBars {
-  uint64_t full[8], empty[8];
+  uint64_t full[12], empty[12];
   uint64_t q_full, s_full[2], p_full[2], o_step, o_last, drain;
   uint32_t tmem;
   int abort, flag;
@@ -322,7 +327,7 @@ __global__ void
     const bool idle = w * NH >= t.rows;
     const int group_bar = 2 + w;
     int E = 0;                                           // FP8: weights carry vs * 2^(4 - E)
-    const uint32_t o_tm = tmem + lanes + 2 * N + w * NH;
+    const uint32_t o_tm = tmem + lanes + S::oO + w * NH;
     // Per row over the tile's keys: each thread's x[r] to the maximum over the group.  (A NaN
     // is no maximum: fmaxf passes over it.)
     auto group_max = [&](float (&x)[NH]) {
@@ -347,21 +352,21 @@ __global__ void
 
     // (A wait that gave up ends the waiting, not the loop: a group's warps still meet at
     // their barriers, and what they compute is dropped.)
+#pragma unroll 1
     for (int i = 0; i < n; ++i) {
-      const int kb = k0 + i * kKeys, key = kb + key_lane;
       const float ks = ks_next, vs = vs_next;
       fetch(i + 1, page_next);
       page_next = page_of(i + 2);
       if (ok) ok = wait(bar(bars.s_full[i & 1]), (i >> 1) & 1);
       tc_fence_after();
-      constexpr int kWords = kFP8 ? NH / 4 : NH / 2;     // of this thread's weights, per term
-      uint32_t hi[kWords], lo[kWords];
       if (!idle) {
-        float s[NH], x[NH];
-        tmem_ld_cols<NH>(tmem + lanes + (i & 1) * N + w * NH, s);
-        // x = s * factor * ks + add, masked
+        const int kb = k0 + i * kKeys, key = kb + key_lane;
         const bool edge = kb < lo_max || kb + kKeys > hi_min;
-        auto scaled = [&](bool shifted) {
+        // x = the scores (in log2 units) + add, masked; they stay in tensor memory
+        float x[NH], sum[NH];
+        auto scores = [&](auto shifted) {
+          float s[NH];
+          tmem_ld_cols<NH>(tmem + lanes + (i & 1) * N + w * NH, s);
 #pragma unroll
           for (int r = 0; r < NH; r += 4) {
             float4 f = make_float4(sc, sc, sc, sc);
@@ -376,11 +381,12 @@ __global__ void
               for (int j = 0; j < 4; ++j)
                 x[r + j] = soft_capped(s[r + j] * g[j], cap_k, cap) * kLog2e +
                            (shifted ? nref[r + j] : 0.0f);
+            } else if constexpr (shifted) {
+              fma2_to(x[r], x[r + 1], s[r], s[r + 1], f.x, f.y, nref[r], nref[r + 1]);
+              fma2_to(x[r + 2], x[r + 3], s[r + 2], s[r + 3], f.z, f.w, nref[r + 2], nref[r + 3]);
             } else {
-#pragma unroll
-              for (int j = 0; j < 4; ++j) x[r + j] = shifted ? nref[r + j] : 0.0f;
-              fma2(x[r], x[r + 1], s[r], s[r + 1], f.x, f.y);
-              fma2(x[r + 2], x[r + 3], s[r + 2], s[r + 3], f.z, f.w);
+              mul2(x[r], x[r + 1], s[r], s[r + 1], f.x, f.y);
+              mul2(x[r + 2], x[r + 3], s[r + 2], s[r + 3], f.z, f.w);
             }
           }
           if (edge) {
@@ -389,30 +395,64 @@ __global__ void
               if (key < bars.lo[w * NH + r] || key >= bars.hi[w * NH + r]) x[r] = ninf;
           }
         };
+        // rows whose first keys are in this tile
+        uint32_t now = 0;
         if (pending != 0u) {
-          // rows whose first keys are in this tile take its maximum as their reference
-          uint32_t now = 0;
 #pragma unroll
           for (int r = 0; r < NH; ++r)
             if (bars.lo[w * NH + r] < kb + kKeys) now |= 1u << r;
           now &= pending;
-          if (now != 0u) {
-            scaled(false);
-            group_max(x);
-#pragma unroll
-            for (int r = 0; r < NH; ++r)
-              if (now >> r & 1u) nref[r] = x[r] > ninf ? -x[r] : 0.0f;
-            // (the first tile has the first keys of some row, or no row of the group sees any)
-            if (kFP8 && pending == seeing) E = group_exponent(vs);
-            pending &= ~now;
-          }
         }
-        // the weights x (FP8: with the value scale), their two terms, and whether one is
-        // beyond its type
-        auto weigh = [&]() -> bool {
-          scaled(true);
+        // One pass, unless rows start here or a weight is beyond its type: the group then takes
+        // the rows' maxima first.
+        auto prepare = [&](bool starts) {
+            scores(std::false_type());
+            group_max(x);
+            if (starts) {
 #pragma unroll
-          for (int r = 0; r < NH; ++r) x[r] = exp2_approx(x[r]);
+              for (int r = 0; r < NH; ++r)
+                if (now >> r & 1u) nref[r] = x[r] > ninf ? -x[r] : 0.0f;
+              // (the first tile has the first keys of some row, or no row of the group sees any)
+              if (kFP8 && pending == seeing) E = group_exponent(vs);
+              pending &= ~now;
+            } else {
+              const int E2 = kFP8 ? group_exponent(vs) : 0;
+              if (ok && i > 0) ok = wait(bar(bars.o_step), (i - 1) & 1);
+              tc_fence_after();
+              const float unit = kFP8 ? exp2_approx(static_cast<float>(E - E2)) : 1.0f;
+              const uint32_t started = seeing & ~pending;
+#pragma unroll
+              for (int r = 0; r < NH; ++r) {
+                const float want = fminf(nref[r], -x[r]);
+                const bool moves = started >> r & 1u;
+                x[r] = moves ? exp2_approx(want - nref[r]) : 1.0f;   // the row's sums shrink
+                if (moves) nref[r] = want;
+                l[r] *= x[r];
+              }
+              E = E2;
+              if (i > 0) {
+#pragma unroll
+                for (int term = 0; term < (kFP8 ? 2 : 1); ++term) {
+                  float o[NH];
+                  tmem_ld_cols<NH>(o_tm + term * N, o);
+                  uint32_t u[NH];
+#pragma unroll
+                  for (int r = 0; r < NH; ++r) u[r] = __float_as_uint(o[r] * x[r] * unit);
+                  tmem_st_cols<NH>(o_tm + term * N, u);
+                }
+                tmem_st_wait();
+              }
+            }
+        };
+        auto pass = [&]() -> bool {
+          // the weights' two terms, to [buffer][term][chunk of rows][key][16 bytes] (where a
+          // pass is done again nobody has read them), and their sums without the value scale
+          scores(std::true_type());
+#pragma unroll
+          for (int r = 0; r < NH; ++r) sum[r] = exp2_approx(x[r]);
+          constexpr int kWords = kFP8 ? NH / 4 : NH / 2;   // of this thread's weights, per term
+          uint32_t hi[kWords], lo[kWords];
+          bool far;
           if constexpr (kFP8) {
             const float vw = vs * exp2_approx(static_cast<float>(4 - E));
             __half2 most = __float2half2_rn(0.0f);
@@ -422,7 +462,7 @@ __global__ void
 #pragma unroll
               for (int k = 0; k < 2; ++k) {
                 float a, c;
-                mul2(a, c, x[4 * j + 2 * k], x[4 * j + 2 * k + 1], vw, vw);
+                mul2(a, c, sum[4 * j + 2 * k], sum[4 * j + 2 * k + 1], vw, vw);
                 const uint16_t hc = cvt_e4m3x2(a, c);
                 const uint32_t back = e4m3x2_to_f16x2(hc);
                 const __half2 full = __floats2half2_rn(a, c);
@@ -439,80 +479,52 @@ __global__ void
               hi[j] = hw;
               lo[j] = lw;
             }
-            return fmaxf(__low2float(most), __high2float(most)) > 448.0f;
+            far = fmaxf(__low2float(most), __high2float(most)) > 448.0f;
           } else {
             float most = 0.0f;
 #pragma unroll
             for (int j = 0; j < NH / 2; ++j) {
-              most = fmaxf(most, fmaxf(x[2 * j], x[2 * j + 1]));
-              __nv_bfloat162 hh = __floats2bfloat162_rn(x[2 * j], x[2 * j + 1]);
+              most = fmaxf(most, fmaxf(sum[2 * j], sum[2 * j + 1]));
+              __nv_bfloat162 hh = __floats2bfloat162_rn(sum[2 * j], sum[2 * j + 1]);
               const float2 back = __bfloat1622float2(hh);
-              __nv_bfloat162 ll = __floats2bfloat162_rn(x[2 * j] - back.x, x[2 * j + 1] - back.y);
+              __nv_bfloat162 ll =
+                  __floats2bfloat162_rn(sum[2 * j] - back.x, sum[2 * j + 1] - back.y);
               hi[j] = *reinterpret_cast<uint32_t*>(&hh);
               lo[j] = *reinterpret_cast<uint32_t*>(&ll);
             }
-            return most > 1.0e18f;
+            far = most > 1.0e18f;
           }
-        };
-        bool far = weigh();
-        if (named_bar_any(group_bar, 128, far)) {
-          scaled(false);
-          group_max(x);
-          const int E2 = kFP8 ? group_exponent(vs) : 0;
-          if (ok && i > 0) ok = wait(bar(bars.o_step), (i - 1) & 1);
-          tc_fence_after();
-          const float unit = kFP8 ? exp2_approx(static_cast<float>(E - E2)) : 1.0f;
-          const uint32_t started = seeing & ~pending;
+          // one buffer of weights: the last product has read those before (that of the tile
+          // before it is complete: it came before these scores)
+          if (S::kPBufs == 1 && ok && i > 0) ok = wait(bar(bars.o_step), (i - 1) & 1);
+          const uint32_t at = sbase + S::oP + (S::kPBufs == 2 ? (i & 1) * 2 * S::kPTerm : 0) +
+                              w * NH / S::kChunkRows * (kKeys * 16) + key_lane * 16 +
+                              (kWords < 4 ? w * kWords * 4 : 0);
 #pragma unroll
-          for (int r = 0; r < NH; ++r) {
-            const float want = fminf(nref[r], -x[r]);
-            const bool moves = started >> r & 1u;
-            x[r] = moves ? exp2_approx(want - nref[r]) : 1.0f;       // the row's sums shrink
-            if (moves) nref[r] = want;
-            l[r] *= x[r];
-          }
-          E = E2;
-          if (i > 0) {
-#pragma unroll
-            for (int term = 0; term < (kFP8 ? 2 : 1); ++term) {
-              float o[NH];
-              tmem_ld_cols<NH>(o_tm + term * N, o);
-              uint32_t u[NH];
-#pragma unroll
-              for (int r = 0; r < NH; ++r) u[r] = __float_as_uint(o[r] * x[r] * unit);
-              tmem_st_cols<NH>(o_tm + term * N, u);
-            }
-            tmem_st_wait();
-          }
-          weigh();
-        }
-#pragma unroll
-        for (int r = 0; r < NH; r += 2) add2(l[r], l[r + 1], x[r], x[r + 1]);
-      }
-      // one buffer of weights: the last product has read those before (that of the tile before it
-      // is complete: it came before these scores)
-      if (S::kPBufs == 1 && ok && i > 0) ok = wait(bar(bars.o_step), (i - 1) & 1);
-      if (!idle) {
-        // [buffer][term][chunk of rows][key][16 bytes]
-        const uint32_t at = sbase + S::oP + (S::kPBufs == 2 ? (i & 1) * 2 * S::kPTerm : 0) +
-                            w * NH / S::kChunkRows * (kKeys * 16) + key_lane * 16 +
-                            (kWords < 4 ? w * kWords * 4 : 0);
-#pragma unroll
-        for (int term = 0; term < 2; ++term) {
-          const uint32_t* v = term == 0 ? hi : lo;
-          if constexpr (kWords < 4) {
-            asm volatile("st.shared.v2.u32 [%0], {%1, %2};" ::"r"(at + term * S::kPTerm), "r"(v[0]),
-                         "r"(v[1])
-                         : "memory");
-          } else {
-#pragma unroll
-            for (int q = 0; q < kWords / 4; ++q)
-              asm volatile("st.shared.v4.u32 [%0], {%1, %2, %3, %4};" ::"r"(
-                               at + term * S::kPTerm + q * (kKeys * 16)),
-                           "r"(v[4 * q]), "r"(v[4 * q + 1]), "r"(v[4 * q + 2]), "r"(v[4 * q + 3])
+          for (int term = 0; term < 2; ++term) {
+            const uint32_t* v = term == 0 ? hi : lo;
+            if constexpr (kWords < 4) {
+              asm volatile("st.shared.v2.u32 [%0], {%1, %2};" ::"r"(at + term * S::kPTerm),
+                           "r"(v[0]), "r"(v[1])
                            : "memory");
+            } else {
+#pragma unroll
+              for (int q = 0; q < kWords / 4; ++q)
+                asm volatile("st.shared.v4.u32 [%0], {%1, %2, %3, %4};" ::"r"(
+                                 at + term * S::kPTerm + q * (kKeys * 16)),
+                             "r"(v[4 * q]), "r"(v[4 * q + 1]), "r"(v[4 * q + 2]), "r"(v[4 * q + 3])
+                             : "memory");
+            }
           }
+          return far;
+        };
+        if (now != 0u) prepare(true);
+        if (named_bar_any(group_bar, 128, pass())) {
+          prepare(false);
+          pass();
         }
+#pragma unroll
+        for (int r = 0; r < NH; r += 2) add2(l[r], l[r + 1], sum[r], sum[r + 1]);
         fence_async_smem();
       }
       tc_fence_before();
@@ -652,14 +664,14 @@ __global__ void
 #pragma unroll
             for (int x = 0; x < 2 * kSteps; ++x) {       // the weights' hi, then lo
               const int s = x % kSteps, term = x / kSteps;
-              umma_ss<kFP8>(tm + 2 * N + (kFP8 ? term * N : 0), a + s * kVStep, kTileHi,
+              umma_ss<kFP8>(tm + S::oO + (kFP8 ? term * N : 0), a + s * kVStep, kTileHi,
                             pb + term * (S::kPTerm >> 4) + s * kPStep, kPHi, idesc_o,
                             (kFP8 ? s > 0 : x > 0) ? 1u : (first ? 0u : 1u));
             }
           } else {
             for (int term = 0; term < 2; ++term)
               for (int s = s0; s < s1; ++s)
-                umma_ss<kFP8>(tm + 2 * N + (kFP8 ? term * N : 0), a + s * kVStep, kTileHi,
+                umma_ss<kFP8>(tm + S::oO + (kFP8 ? term * N : 0), a + s * kVStep, kTileHi,
                               pb + term * (S::kPTerm >> 4) + s * kPStep, kPHi, idesc_o,
                               (s > s0 || (!kFP8 && term > 0)) ? 1u : (first ? 0u : 1u));
           }
@@ -720,9 +732,8 @@ __global__ void
     constexpr int kRowBytes = kFP8 ? D : 2 * D;
     bool ok = p.drop_producer == 0;
     int f = 0;
-    for (; f < 2 * n && ok; ++f) {
-      const Item it = item_at(f, n, 2);
-      const int kb = k0 + it.i * kKeys;
+    auto load = [&](bool v, int i) -> bool {
+      const int kb = k0 + i * kKeys;
       const int key = kb + lane * box;
       const bool mine = lane < segs && key < k1;
       int page = mine ? __ldg(table + (key >> p.c.page_log2)) : 0;
@@ -731,8 +742,7 @@ __global__ void
         page = 0;                          // (a place that exists)
       }
       const int slot = f % S::kSlots;
-      ok = wait(bar(bars.empty[slot]), ((f / S::kSlots) & 1) ^ 1);
-      if (!ok) break;
+      if (!wait(bar(bars.empty[slot]), ((f / S::kSlots) & 1) ^ 1)) return false;
       const uint32_t full = bar(bars.full[slot]);
       if (lane == 0) {
         const int loaded = min(segs, (k1 - kb + box - 1) / box);
@@ -742,7 +752,7 @@ __global__ void
       if (mine) {
         const int row = ((page * p.c.heads + h) << p.c.page_log2) +
                         (key & ((1 << p.c.page_log2) - 1));
-        const CUtensorMap* map = it.v ? &map_v : &map_k;
+        const CUtensorMap* map = v ? &map_v : &map_k;
         const uint32_t dst = sbase + S::oSlots + slot * S::kTileBytes;
         if constexpr (kFP8) {
           tma_load_2d(dst + lane * box * D, map, full, 0, row, policy);
@@ -753,6 +763,15 @@ __global__ void
         }
       }
       __syncwarp();
+      ++f;
+      return true;
+    };
+    // in the order that the MMAs take them: keys of the first two tiles, then each tile's
+    // values and the keys of the tile after the next
+    for (int i = 0; i < 2 && i < n && ok; ++i) ok = load(false, i);
+    for (int i = 0; i < n && ok; ++i) {
+      ok = load(true, i);
+      if (ok && i + 2 < n) ok = load(false, i + 2);
     }
     if (!ok)                               // copies in flight land before the memory goes
       for (int g = max(0, f - S::kSlots); g < f; ++g)

@@ -91,6 +91,15 @@ __device__ __forceinline__ void fma2_bc(float& d0, float& d1, float a0, float a1
       : "=f"(d0), "=f"(d1)
       : "f"(a0), "f"(a1), "f"(b), "f"(c));
 }
+// (a0, a1) * (b0, b1) + (c0, c1)
+__device__ __forceinline__ void fma2_to(float& d0, float& d1, float a0, float a1, float b0,
+                                        float b1, float c0, float c1) {
+  asm("{\n\t.reg .b64 pa, pb, pc;\n\t"
+      "mov.b64 pa, {%2, %3};\n\tmov.b64 pb, {%4, %5};\n\tmov.b64 pc, {%6, %7};\n\t"
+      "fma.rn.f32x2 pa, pa, pb, pc;\n\tmov.b64 {%0, %1}, pa;\n\t}"
+      : "=f"(d0), "=f"(d1)
+      : "f"(a0), "f"(a1), "f"(b0), "f"(b1), "f"(c0), "f"(c1));
+}
 __device__ __forceinline__ void add2(float& d0, float& d1, float a0, float a1) {
   asm("{\n\t.reg .b64 pa, pd;\n\tmov.b64 pd, {%0, %1};\n\tmov.b64 pa, {%2, %3};\n\t"
       "add.rn.f32x2 pd, pd, pa;\n\tmov.b64 {%0, %1}, pd;\n\t}"
@@ -139,33 +148,6 @@ __device__ __forceinline__ bool elect_one() {
 }
 __device__ __forceinline__ void fence_async_smem() {
   asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
-}
-
-// The order in which key and value tiles are taken: K of the first `lead`
-// tiles, then V of tile i and K of tile i + lead in turn (lead 1: a score buffer per row
-// tile; lead 2: two for the one row tile).
-struct Item {
-  bool v;
-  int i;
-};
-__device__ __forceinline__ Item item_at(int f, int n, int lead) {
-  const int first = min(lead, n);
-  Item it;
-  if (f < first) {
-    it.v = false;
-    it.i = f;
-    return it;
-  }
-  f -= first;
-  const int pairs = n - first;
-  if (f < 2 * pairs) {
-    it.v = (f & 1) == 0;
-    it.i = it.v ? (f >> 1) : (f >> 1) + lead;
-  } else {
-    it.v = true;
-    it.i = f - pairs;
-  }
-  return it;
 }
 
 // The cache rows [rows, D] in boxes of up to 128 positions: bf16 in boxes of 64

@@ -708,9 +708,12 @@ __global__ void __launch_bounds__(TileShape<D, kFP8>::kThreads, 1)
         ++r.f;
         return true;
       };
-      for (int f = 0; f < 2 * n && ok; ++f) {
-        const Item it = item_at(f, n, 1);
-        ok = load(kFP8 && !it.v ? rk : rv, it.v, it.i);
+      // in the order that the MMAs take them
+      auto keys = [&](int i) { return load(kFP8 ? rk : rv, false, i); };
+      if (n > 0) ok = ok && keys(0);
+      for (int i = 0; i < n && ok; ++i) {
+        ok = load(rv, true, i);
+        if (ok && i + 1 < n) ok = keys(i + 1);
       }
       if (!ok) {                           // copies in flight land before the memory goes
         for (int g = max(0, rv.f - rv.slots); g < rv.f; ++g)
