@@ -88,15 +88,21 @@ __device__ __forceinline__ TileView tile_view(const AttnParams& p, int b, int h,
   return t;
 }
 
-// A tile's keys are cut into parts of p.chunk from `base` (t.lo rounded down
-// to `align`), the last part taking what is left.
-struct Parts {
-  int base, count;         // count <= p.splits; 0: the tile sees no key
+// A tile's keys, cut evenly into whole key tiles over at most `parts` CTAs: the range
+// of CTA `part`.  count 0: no key is seen (CTA 0 writes the empty rows).
+struct Share {
+  int k0, k1, n, count;          // keys [k0, k1), in n key tiles; CTAs that have some
 };
-__device__ __forceinline__ Parts tile_parts(const AttnParams& p, const TileView& t, int align) {
-  Parts s;
-  s.base = t.lo / align * align;
-  s.count = t.hi > t.lo ? min(p.splits, (t.hi - s.base + p.chunk - 1) / p.chunk) : 0;
+__device__ __forceinline__ Share share_of(const TileView& t, int parts, int part) {
+  constexpr int kTile = kTileKeys;
+  Share s;
+  const int base = t.lo / kTile * kTile;
+  const int all = t.hi > t.lo ? (t.hi - base + kTile - 1) / kTile : 0;
+  const int each = max(1, (all + parts - 1) / parts);
+  s.count = (all + each - 1) / each;
+  s.k0 = base + part * each * kTile;
+  s.k1 = all == 0 ? s.k0 : min(t.hi, s.k0 + each * kTile);
+  s.n = (s.k1 - s.k0 + kTile - 1) / kTile;
   return s;
 }
 
@@ -123,30 +129,30 @@ __host__ __device__ __forceinline__ int64_t partial_floats(int rows) {
   return static_cast<int64_t>(rows) * (D + 2);
 }
 
-// Called by `threads` threads of the CTA after its part has been written to
-// p.partial: the last CTA of the tile to arrive joins the parts, in their order, and writes
-// out and lse.  `tile` numbers the tiles that are split, part_rows the rows that a part has
-// room for; named barrier `bar` joins the threads; `weights` is shared memory for
-// count * part_rows floats.  First a thread per row turns the parts' maxima and sums into
+// Called by `threads` threads of the CTA after its part has been written: the last CTA of
+// the tile to arrive joins the parts, in their order, and writes out and lse.  `parts`: the
+// first of the tile's `count` parts, one after another, part_rows the rows that each has
+// room for; `counter` is the tile's own; named barrier `bar` joins the threads; `weights` is
+// shared memory for count * part_rows floats.  First a thread per row turns the parts' maxima and sums into
 // weights, then all threads stream the parts, kAhead 16-byte loads in flight each.
 template <int D>
-__device__ __forceinline__ void join_parts(const AttnParams& p, const TileView& t, int64_t tile,
-                                           int part_rows, int count, int tid, int threads,
-                                           int bar, float* weights, int* s_flag) {
+__device__ __forceinline__ void join_parts(const AttnParams& p, const TileView& t,
+                                           const float* parts, unsigned* counter, int part_rows,
+                                           int count, int tid, int threads, int bar,
+                                           float* weights, int* s_flag) {
   constexpr int kAhead = 8;
   __threadfence();
   named_bar_sync(bar, threads);
   if (tid == 0) {
-    const unsigned prev = atomicAdd(p.counters + tile, 1u);
+    const unsigned prev = atomicAdd(counter, 1u);
     const int last = prev == static_cast<unsigned>(count - 1);
-    if (last) p.counters[tile] = 0u;   // every part has arrived
+    if (last) *counter = 0u;   // every part has arrived
     *s_flag = last;
   }
   named_bar_sync(bar, threads);
   if (!*s_flag) return;
   __threadfence();
   const int64_t stride = partial_floats<D>(part_rows);
-  const float* parts = p.partial + tile * p.splits * stride;
   const float* ml = parts + static_cast<int64_t>(part_rows) * D;
   const float ninf = __int_as_float(0xff800000);
   for (int r = tid; r < t.rows; r += threads) {

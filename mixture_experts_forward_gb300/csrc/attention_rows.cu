@@ -145,6 +145,85 @@ __device__ __forceinline__ float transposed(float (&x)[NH], F op) {
   return x[0];
 }
 
+// What a CTA has to do: row tile rt of sequence b and cache head h, part `part` of its
+// `parts`, of which CTA number `first` has part 0.  b < 0: nothing.
+struct Job {
+  int b, h, rt, part, parts, first;
+};
+
+// One CTA per tile.
+__device__ __forceinline__ Job whole_job(const AttnParams& p) {
+  Job j;
+  const int bh = blockIdx.x / p.row_tiles;
+  j.rt = blockIdx.x - bh * p.row_tiles;
+  j.b = bh / p.c.heads;
+  j.h = bh - j.b * p.c.heads;
+  j.part = 0;
+  j.parts = 1;
+  j.first = blockIdx.x;
+  return j;
+}
+
+// Fewer tiles than the grid has CTAs (one for every place on the SMs): each sequence's
+// tiles are cut into as many parts of about `size` key tiles as its length asks for, size the
+// smallest, in steps of an eighth, for which the grid holds them all; ragged
+// sequences then give CTAs even work in one round.  Every warp finds this out for itself
+// from the lengths (at most as many as CTAs).
+__device__ __forceinline__ Job shared_job(const AttnParams& p) {
+  const int lane = threadIdx.x & 31, places = gridDim.x, unit = p.c.heads * p.row_tiles;
+  // (the first 32 lengths stay in a register)
+  auto load_tiles = [&](int b) {
+    const int len = b < p.B ? min(max(__ldg(p.kv_lens + b), 0), p.span) : 0;
+    return (len + kKeys - 1) / kKeys;
+  };
+  const int tiles0 = load_tiles(lane);
+  auto key_tiles = [&](int b0) { return b0 == 0 ? tiles0 : load_tiles(b0 + lane); };
+  auto sum32 = [&](int v) {
+    return static_cast<int>(__reduce_add_sync(0xffffffffu, static_cast<unsigned>(v)));
+  };
+  int all = 0;
+  for (int b0 = 0; b0 < p.B; b0 += 32) all += sum32(key_tiles(b0));
+  // (quotients in binary32: every CTA computes the same ones, and any would do)
+  float size = fmaxf(2.0f, ceilf(__fdividef(static_cast<float>(all) * unit, static_cast<float>(places))));
+  auto parts_of = [&](int b0) {
+    const int n = static_cast<int>(ceilf(__fdividef(static_cast<float>(key_tiles(b0)), size) - 1e-4f));
+    return b0 + lane < p.B ? max(1, n) : 0;
+  };
+  for (;;) {
+    int parts = 0;
+    for (int b0 = 0; b0 < p.B; b0 += 32) parts += sum32(parts_of(b0));
+    if (static_cast<int64_t>(parts) * unit <= places || size > all) break;
+    size = ceilf(size * 1.125f);
+  }
+  Job j;
+  j.b = -1;
+  int before = 0;                                  // CTAs of the sequences before
+  for (int b0 = 0; b0 < p.B && j.b < 0; b0 += 32) {
+    const int parts = parts_of(b0);
+    int inc = parts * unit;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const int up = __shfl_up_sync(0xffffffffu, inc, o);
+      if (lane >= o) inc += up;
+    }
+    const int c = blockIdx.x;
+    const unsigned here = __ballot_sync(0xffffffffu, before + inc > c);
+    if (here != 0u) {
+      const int l = __ffs(here) - 1;
+      const int start = before + __shfl_sync(0xffffffffu, inc - parts * unit, l);
+      j.parts = __shfl_sync(0xffffffffu, parts, l);
+      j.b = b0 + l;
+      const int tile = (c - start) / j.parts;
+      j.part = (c - start) - tile * j.parts;
+      j.h = tile / p.row_tiles;
+      j.rt = tile - j.h * p.row_tiles;
+      j.first = c - j.part;
+    }
+    before += __shfl_sync(0xffffffffu, inc, 31);
+  }
+  return j;
+}
+
 template <int D, bool kFP8, int N>
 __global__ void
     __launch_bounds__(RowsShape<D, kFP8, N>::kThreads, RowsShape<D, kFP8, N>::kCtas)
@@ -186,22 +265,22 @@ __global__ void
   pdl_wait();
   pdl_launch_dependents();
 
-  const int rt = static_cast<int>(blockIdx.x % p.row_tiles);
-  const int bh = static_cast<int>(blockIdx.x / p.row_tiles);
-  const int b = bh / p.c.heads, h = bh - b * p.c.heads;
-  const int part = blockIdx.y;
-  const TileView t = tile_view(p, b, h, rt, N, part == 0 && rt == 0 && tid == 0);
-  const Parts parts = tile_parts(p, t, kKeys);
-  if (t.rows == 0 || part >= max(1, parts.count)) {      // nothing to do here
+  const Job job = p.splits > 1 ? shared_job(p) : whole_job(p);
+  const int b = job.b, h = job.h;
+  TileView t;
+  Share share;
+  if (b >= 0) {
+    t = tile_view(p, b, h, job.rt, N, job.part == 0 && job.rt == 0 && tid == 0);
+    share = share_of(t, job.parts, job.part);
+  }
+  if (b < 0 || t.rows == 0 || job.part >= max(1, share.count)) {   // nothing to do here
     if (warp == kMmaWarp) {
       const uint32_t at = *reinterpret_cast<volatile uint32_t*>(&bars.tmem);
       tmem_dealloc(at, S::kTmem);
     }
     return;
   }
-  const int k0 = parts.base + part * p.chunk;
-  const int k1 = parts.count == 0 ? k0 : (part + 1 >= parts.count ? t.hi : k0 + p.chunk);
-  const int n = (k1 - k0 + kKeys - 1) / kKeys;    // key tiles
+  const int k0 = share.k0, k1 = share.k1, n = share.n;   // keys, key tiles
   if (tid < N) {                                  // the rows' places and keys
     int lo = 0, hi = 0;
     int64_t in = -1, out = 0;
@@ -535,9 +614,9 @@ __global__ void
     tc_fence_after();
 
     // ---- results: the sums over the keys, then a channel per lane
-    const bool split = parts.count > 1;
-    float* dst = p.partial + (static_cast<int64_t>(blockIdx.x) * p.splits + part) *
-                                 partial_floats<D>(p.part_rows);
+    const bool split = share.count > 1;
+    float* parts = p.partial + static_cast<int64_t>(job.first) * partial_floats<D>(p.part_rows);
+    float* dst = parts + job.part * partial_floats<D>(p.part_rows);
     if (!idle) {
       float o[NH];
 #pragma unroll
@@ -591,8 +670,8 @@ __global__ void
       }
     }
     if (split)
-      join_parts<D>(p, t, blockIdx.x, p.part_rows, parts.count, tid, S::kSoftmax, 1,
-                    reinterpret_cast<float*>(smem + S::oSlots), &bars.flag);
+      join_parts<D>(p, t, parts, p.counters + job.first, p.part_rows, share.count, tid,
+                    S::kSoftmax, 1, reinterpret_cast<float*>(smem + S::oSlots), &bars.flag);
   } else if (warp == kMmaWarp) {
     // =================================================================== MMA
     if (n > 0) {
@@ -791,8 +870,7 @@ cudaError_t launch_n(const AttnParams& p, const CUtensorMap& mk, const CUtensorM
   if (e != cudaSuccess) return e;
   cudaLaunchAttribute attr[1];
   cudaLaunchConfig_t cfg =
-      make_cfg(dim3(static_cast<unsigned>(p.B) * p.c.heads * p.row_tiles, p.splits),
-               dim3(S::kThreads), stream, true, attr);
+      make_cfg(dim3(p.whole), dim3(S::kThreads), stream, true, attr);
   cfg.dynamicSmemBytes = S::kSmem;
   return cudaLaunchKernelEx(&cfg, rows_kernel<D, kFP8, N>, mk, mv, p);
 }

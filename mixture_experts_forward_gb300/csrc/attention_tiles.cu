@@ -151,20 +151,15 @@ __global__ void __launch_bounds__(TileShape<D, kFP8>::kThreads, 1)
   const int bh = tile_no % tiles_bh;
   const int b = bh / p.c.heads, h = bh - b * p.c.heads;
   const TileView t = tile_view(p, b, h, rt, 2 * kRows, part == 0 && rt == 0 && tid == 0);
-  // its keys, cut evenly into whole key tiles
-  const int base = t.lo / kKeys * kKeys;
-  const int all = t.hi > t.lo ? (t.hi - base + kKeys - 1) / kKeys : 0;
-  const int each = max(1, (all + splits - 1) / splits), count = (all + each - 1) / each;
-  if (t.rows == 0 || part >= max(1, count)) {                    // nothing to do here
+  const Share share = share_of(t, splits, part);
+  if (t.rows == 0 || part >= max(1, share.count)) {                    // nothing to do here
     if (warp == 9) {
       const uint32_t at = *reinterpret_cast<volatile uint32_t*>(&bars.tmem);
       tmem_dealloc(at, 512);
     }
     return;
   }
-  const int k0 = base + part * each * kKeys;
-  const int k1 = all == 0 ? k0 : min(t.hi, k0 + each * kKeys);
-  const int n = (k1 - k0 + kKeys - 1) / kKeys;                   // key tiles
+  const int k0 = share.k0, k1 = share.k1, n = share.n;           // keys, key tiles
   // key tiles of each group: row tile 0 may end earlier, row tile 1 may not exist
   const int hi0 = min(k1, row_hi(p, t, (t.first_row + min(t.rows, kRows) - 1) / p.group));
   const int n0 = max(0, min(n, (hi0 - k0 + kKeys - 1) / kKeys));
@@ -448,11 +443,12 @@ __global__ void __launch_bounds__(TileShape<D, kFP8>::kThreads, 1)
       l = 0.0f;
     }
     if (!started) ref = ninf;
-    const bool split = count > 1;
+    const bool split = share.count > 1;
     const float inv = l == 0.0f ? 0.0f : 1.0f / l;
     const float g = (kFP8 ? exp2_approx(static_cast<float>(E)) : 1.0f) * (split ? 1.0f : inv);
-    float* dst = p.partial + (static_cast<int64_t>(tile_no - p.whole) * p.splits + part) *
-                                 partial_floats<D>(p.part_rows);
+    float* parts = p.partial + static_cast<int64_t>(tile_no - p.whole) * p.splits *
+                                   partial_floats<D>(p.part_rows);
+    float* dst = parts + part * partial_floats<D>(p.part_rows);
     __nv_bfloat16* orow = real && !split ? out_row(p, t, my) : nullptr;
     if (!idle) {
 #pragma unroll 1
@@ -493,8 +489,8 @@ __global__ void __launch_bounds__(TileShape<D, kFP8>::kThreads, 1)
       }
     }
     if (split)
-      join_parts<D>(p, t, tile_no - p.whole, p.part_rows, count, tid, 256, 1,
-                    reinterpret_cast<float*>(smem + S::oSlots), &bars.flag);
+      join_parts<D>(p, t, parts, p.counters + (tile_no - p.whole), p.part_rows, share.count, tid,
+                    256, 1, reinterpret_cast<float*>(smem + S::oSlots), &bars.flag);
   } else if (warp < 12) {
     regs_dec<S::kRegsOther>();
     if (warp == 9 && n > 0) {

@@ -49,7 +49,7 @@ bool ws_ok(const void* ws) {
 
 bool stride8(int64_t s) { return s % 8 == 0; }
 
-constexpr int kMaxTiles = 65536 / 4;   // counters of split tiles
+static_assert(MOE_ATTENTION_CTRL_BYTES - MOE_CTRL_BYTES >= 4 * kMaxParts, "a counter per CTA");
 
 }  // namespace
 
@@ -171,17 +171,15 @@ moe_status_t moe_paged_attention(const moe_attention_args* a, void* ws, size_t w
   const long long most = (span + 255) / 256;      // parts of at least 256 keys
   const cudaStream_t st = static_cast<cudaStream_t>(stream);
   if (few) {
-    // Parts of the same length (ragged sequences then give even work), as many as the SMs
-    // have places for CTAs.
-    long long splits = static_cast<long long>(attention_rows_places(tile_rows, D, fp8)) * sms / tiles;
-    if (splits > most) splits = most;
-    if (splits > room_parts / tiles) splits = room_parts / tiles;
-    if (splits > kMaxParts) splits = kMaxParts;
-    if (tiles > kMaxTiles || splits < 2) splits = 1;
-    // (the last part takes whatever lies past splits * chunk)
-    p.splits = static_cast<int>(splits);
-    p.chunk = splits > 1 ? static_cast<int>(((span + splits - 1) / splits + 127) / 128 * 128)
-                         : 0x40000000;
+    // Fewer tiles than places for CTAs on the SMs: a CTA for every place, which share the
+    // tiles' keys among them (in parts of at least 256; the kernel goes by kv_lens).
+    const long long places =
+        static_cast<long long>(attention_rows_places(tile_rows, D, fp8)) * sms;
+    const bool share = tiles < places && most > 1 && places <= room_parts && places <= kMaxParts;
+    p.splits = share ? static_cast<int>(places) : 1;
+    p.whole = static_cast<int>(share ? places : tiles);
+    p.span = static_cast<int>(a->window > 0 && a->window + rows / group + 128 < room
+                                  ? a->window + rows / group + 128 : room);
     return cuda_status(launch_attention_rows(p, tile_rows, D, fp8, st));
   }
   // One tile per SM at a time.  The tiles past the last full round, which are the early rows,

@@ -45,8 +45,9 @@ struct AttnParams {
   float scale, softcap;
   int window, causal;
   int row_tiles;                 // row tiles per (sequence, head)
-  int splits, chunk;             // parts of the keys, keys per part (few rows)
-  int whole;                     // many rows: tiles before the ones that are split
+  int splits;                    // parts of a tile's keys at most
+  int whole;                     // many rows: tiles before the ones that are split; few: CTAs
+  int span;                      // keys that a tile sees at most (few rows)
   int part_rows;                 // rows that a part's result has room for
   unsigned* counters;            // one per (sequence, head, row tile); zero between calls
   float* partial;                // per (tile, part): rows x (head_dim sums, maximum, sum)
@@ -61,8 +62,8 @@ cudaError_t launch_kv_write(const KvCacheView& c, int head_dim, bool fp8, const 
 cudaError_t launch_kv_read(const KvCacheView& c, int head_dim, bool fp8, const int32_t* table,
                            int table_stride, const int32_t* cu, const int32_t* starts, int B,
                            int rows, void* k_out, void* v_out, Ctrl* ctrl, cudaStream_t stream);
-// Parts of a tile at most.
-constexpr int kMaxParts = 192;
+// Parts of a tile (and CTAs that share tiles) at most.
+constexpr int kMaxParts = 320;
 // Up to 16, 32, 48 or 64 rows per tile (tile_rows), tcgen05 with keys and channels as the rows.
 int attention_rows_places(int tile_rows, int head_dim, bool fp8);   // CTAs per SM
 cudaError_t launch_attention_rows(const AttnParams& p, int tile_rows, int head_dim, bool fp8,
