@@ -1,9 +1,8 @@
 // Attention of few rows over the paged cache: single tokens (decode) and
-// short drafted runs, up to 64 rows (new tokens x query heads of one cache head)
-// per tile.  Bound by HBM: every cached byte is read once, by TMA, and meets few rows.
+// short drafted runs, up to 64 rows (new tokens x query heads of one cache head).  Bound by HBM: every cached byte is read once, by TMA, and meets few rows.
 //
 // The products are turned round, so that a key is a lane and a row a column:
-//   S^T[keys x rows] = K Q^T          (A = the key tile as it lies in the cache)
+//   S^T[keys x rows] = K Q^T               (A = the key tile as it lies in the cache)
 //   O^T[channels x rows] += V^T P^T   (A = the value tile, MN-major)
 // With 128 rows of the tensor core filled by keys and channels, 8 or 40 query rows
 // cost no padding to 128; a softmax thread owns a key, so a quantised cache's two
@@ -145,19 +144,17 @@ __device__ __forceinline__ float transposed(float (&x)[NH], F op) {
   return x[0];
 }
 
-// What a CTA has to do: row tile rt of sequence b and cache head h, part `part` of its
-// `parts`, of which CTA number `first` has part 0.  b < 0: nothing.
+// What a CTA has to do: sequence b and cache head h (all their rows are one tile), part
+// `part` of `parts`, of which CTA number `first` has part 0.  b < 0: nothing.
 struct Job {
-  int b, h, rt, part, parts, first;
+  int b, h, part, parts, first;
 };
 
 // One CTA per tile.
 __device__ __forceinline__ Job whole_job(const AttnParams& p) {
   Job j;
-  const int bh = blockIdx.x / p.row_tiles;
-  j.rt = blockIdx.x - bh * p.row_tiles;
-  j.b = bh / p.c.heads;
-  j.h = bh - j.b * p.c.heads;
+  j.b = blockIdx.x / p.c.heads;
+  j.h = blockIdx.x - j.b * p.c.heads;
   j.part = 0;
   j.parts = 1;
   j.first = blockIdx.x;
@@ -170,7 +167,7 @@ __device__ __forceinline__ Job whole_job(const AttnParams& p) {
 // sequences then give CTAs even work in one round.  Every warp finds this out for itself
 // from the lengths (at most as many as CTAs).
 __device__ __forceinline__ Job shared_job(const AttnParams& p) {
-  const int lane = threadIdx.x & 31, places = gridDim.x, unit = p.c.heads * p.row_tiles;
+  const int lane = threadIdx.x & 31, places = gridDim.x, unit = p.c.heads;
   // (the first 32 lengths stay in a register)
   auto load_tiles = [&](int b) {
     const int len = b < p.B ? min(max(__ldg(p.kv_lens + b), 0), p.span) : 0;
@@ -213,10 +210,8 @@ __device__ __forceinline__ Job shared_job(const AttnParams& p) {
       const int start = before + __shfl_sync(0xffffffffu, inc - parts * unit, l);
       j.parts = __shfl_sync(0xffffffffu, parts, l);
       j.b = b0 + l;
-      const int tile = (c - start) / j.parts;
-      j.part = (c - start) - tile * j.parts;
-      j.h = tile / p.row_tiles;
-      j.rt = tile - j.h * p.row_tiles;
+      j.h = (c - start) / j.parts;
+      j.part = (c - start) - j.h * j.parts;
       j.first = c - j.part;
     }
     before += __shfl_sync(0xffffffffu, inc, 31);
@@ -270,7 +265,7 @@ __global__ void
   TileView t;
   Share share;
   if (b >= 0) {
-    t = tile_view(p, b, h, job.rt, N, job.part == 0 && job.rt == 0 && tid == 0);
+    t = tile_view(p, b, h, 0, N, job.part == 0 && tid == 0);
     share = share_of(t, job.parts, job.part);
   }
   if (b < 0 || t.rows == 0 || job.part >= max(1, share.count)) {   // nothing to do here
@@ -807,7 +802,7 @@ __global__ void
     // =================================================================== TMA loads
     const int box = min(1 << p.c.page_log2, kKeys);
     const int segs = kKeys / box;
-    const uint64_t policy = p.row_tiles > 1 ? policy_evict_last() : policy_evict_first();
+    const uint64_t policy = policy_evict_first();         // (read once)
     constexpr int kRowBytes = kFP8 ? D : 2 * D;
     bool ok = p.drop_producer == 0;
     int f = 0;
