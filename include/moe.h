@@ -455,8 +455,9 @@ typedef struct {
   int q_heads;                /* a multiple of cache.heads; query head h reads cache
                                  head h / (q_heads / cache.heads) */
   int max_q;                  /* at least the largest number of new tokens of a sequence */
-  int max_kv;                 /* about the longest kv_lens: sizes the split of long caches
-                                 (a hint, results do not depend on it); 0 = the table's width */
+  int max_kv;                 /* about the longest kv_lens: whether and how far long caches are
+                                 split (a hint: any value gives a right result, the order of
+                                 the sums goes by it); 0 = the table's width */
   int table_stride;           /* entries in a row of block_table */
   const void* q;              /* bf16, 16-byte aligned; strides in elements, multiples of 8 */
   int64_t q_stride_t, q_stride_h;
@@ -478,7 +479,7 @@ typedef struct {
  * first MOE_ATTENTION_CTRL_BYTES, all zeroed before the first use; the calls
  * leave them zero), then room for the partial results of a split cache.  With
  * MOE_ATTENTION_WS_BYTES every call splits as far as it gains; a smaller one (at
- * least MOE_ATTENTION_CTRL_BYTES) splits less.  Not to be shared with other
+ * least MOE_ATTENTION_CTRL_BYTES) splits less or not at all.  Not to be shared with other
  * entry points or with a call on another stream that may run at the same time. */
 #define MOE_ATTENTION_CTRL_BYTES (MOE_CTRL_BYTES + 65536)
 #define MOE_ATTENTION_WS_BYTES (64 << 20)
@@ -488,10 +489,13 @@ typedef struct {
  *   s_j = cap(scale * q . k_j),  out = sum_j softmax(s)_j v_j over the positions
  *   j that the mask leaves,  lse = ln sum_j exp s_j.
  * A row whose mask leaves nothing gets out = 0 and lse = -inf.  Scores, softmax
- * statistics and sums are binary32; the weights are rounded once for the
- * second product and out once to bf16.  One sequence's new tokens may be
- * any number from 0 (chunks of a prompt, drafted runs, single tokens: the form
- * is chosen by their number).  What lies past kv_lens in a page is never used;
+ * statistics and sums are binary32, and out is rounded once to bf16.  For the
+ * second product, max_q * q_heads / heads > 64: the weights are rounded to bf16
+ * over a BF16 cache and to binary16 over an FP8 one, whose values are rounded
+ * to binary16 with their scale; up to 64: the weights are the sum of two bf16
+ * or two E4M3 terms and the values are taken as cached.  One sequence's new
+ * tokens may be any number from 0 (chunks of a prompt, drafted runs, single
+ * tokens).  What lies past kv_lens in a page is never used;
  * a NaN or infinity in a value row reaches every row of a tile that has a row
  * seeing it.  Lengths out of range record MOE_ERR_DEVICE_FAULT. */
 moe_status_t moe_paged_attention(const moe_attention_args* args, void* ws, size_t ws_bytes,

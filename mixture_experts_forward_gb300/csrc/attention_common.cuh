@@ -6,7 +6,6 @@
 // layout, from one query head per cache head to all of them, fills tiles alike.
 #pragma once
 
-#include "ieee_math.cuh"
 #include "serve_internal.cuh"
 
 namespace moe {

@@ -264,7 +264,9 @@ __global__ void __launch_bounds__(TileShape<D, kFP8>::kThreads, 1)
     const float ninf = __int_as_float(0xff800000);
     const float cap_k = kCap ? 2.0f * kLog2e * sc / cap : 0.0f;
     const float f = (kCap ? cap : sc) * kLog2e;   // from s (or tanh) to log2 units
-    constexpr float kFar = kFP8 ? 16384.0f : 1.0e18f;
+    // (binary16 weights: the first keys' largest is 2^3, so a weight is rounded to 2^-28 of it
+    // at worst, and what many small ones add up to beside it is kept)
+    constexpr float kFar = kFP8 ? 16384.0f : 1.0e18f, kAbove = kFP8 ? 3.0f : 0.0f;
     float ref = 0.0f, l = 0.0f;
     bool started = false;                            // the row has seen a key
     int E = 0;                                       // FP8: O is in units of 2^E
@@ -348,7 +350,7 @@ __global__ void __launch_bounds__(TileShape<D, kFP8>::kThreads, 1)
       if (__any_sync(0xffffffffu, first)) {
         const float top = row_max();
         if (first) {
-          ref = top > ninf ? top : 0.0f;
+          ref = top > ninf ? top - kAbove : 0.0f;
           E = e;
           started = true;
         }
@@ -384,7 +386,7 @@ __global__ void __launch_bounds__(TileShape<D, kFP8>::kThreads, 1)
       if (__any_sync(0xffffffffu, sum > kFar)) {
         // (every row of the warp moves to its largest score so far)
         const float top = row_max();
-        const float want = started ? fmaxf(ref, top) : ref;
+        const float want = started ? fmaxf(ref, top - kAbove) : ref;
         const float keep = exp2_approx(ref - want);
         const float g = kFP8 ? keep * exp2_approx(static_cast<float>(E - e)) : keep;
         l *= keep;

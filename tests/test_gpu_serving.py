@@ -264,6 +264,30 @@ def test_scores_far_from_zero(D, fp8, sign, q_len, window):
 
 
 @pytest.mark.parametrize("D,fp8", FORMS)
+@pytest.mark.parametrize("q_len", [1, 6, 13])
+@pytest.mark.parametrize("gap,at,size", [(12.3, 0, 1.0), (13.5, 0, 1.0), (13.5, 0, 2.0 ** -6),
+                                         (13.5, 5000, 1.0)])
+def test_many_small_weights_beside_a_large_one(D, fp8, q_len, gap, at, size):
+    """One key takes most of the weight, and 131071 others share the rest with equal weights
+    (so that roundings do not cancel): what they add up to must not be lost.  One CTA has
+    them all: the workspace has no room for a split."""
+    n = 131072
+    q = torch.ones(q_len, 8, D, dtype=torch.bfloat16, device="cuda")
+    k = torch.zeros(n, 1, D, dtype=torch.bfloat16)
+    k[at] = gap / math.sqrt(D)
+    v = (rand_bf16(1, 1, D, seed=2).abs() + 0.5).to(torch.bfloat16).expand(n, 1, D).clone()
+    v[at] = (rand_bf16(1, D, seed=3) * size).to(torch.bfloat16)
+    c = R.Paged([k], [v], 256, fp8)
+    ws = L.new_workspace(L.ATTENTION_CTRL_BYTES)
+    got, lse = L.paged_attention(q, c.k, c.v, c.table, cu([q_len]), i32([n]), ws, max_q=q_len,
+                                 k_scales=c.ks, v_scales=c.vs, causal=False, lse=True)
+    assert L.get_error(ws) == L.MOE_OK
+    want, want_l, tol, tol_l = R.attention(q, c, [q_len], [n], causal=False)
+    assert bool(((got.double() - want).abs() <= tol).all())
+    assert bool(((lse.double() - want_l).abs() <= tol_l).all())
+
+
+@pytest.mark.parametrize("D,fp8", FORMS)
 @pytest.mark.parametrize("q_len", [2, 150])
 @pytest.mark.parametrize("softcap", [0.0, 20.0])
 def test_a_nan_reaches_its_rows_and_no_others(D, fp8, q_len, softcap):
