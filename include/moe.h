@@ -491,8 +491,9 @@ typedef struct {
  * A row whose mask leaves nothing gets out = 0 and lse = -inf.  Scores, softmax
  * statistics and sums are binary32, and out is rounded once to bf16.  For the
  * second product, max_q * q_heads / heads > 64: the weights are rounded to bf16
- * over a BF16 cache and to binary16 over an FP8 one, whose values are rounded
- * to binary16 with their scale; up to 64: the weights are the sum of two bf16
+ * over a BF16 cache and to binary16 over an FP8 one (below 2^-28 of the row's
+ * largest they count as 0), whose values are rounded to binary16 with their
+ * scale; up to 64: the weights are the sum of two bf16
  * or two E4M3 terms and the values are taken as cached.  One sequence's new
  * tokens may be any number from 0 (chunks of a prompt, drafted runs, single
  * tokens).  What lies past kv_lens in a page is never used;

@@ -18,8 +18,9 @@
 // sum of two E4M3 terms (exact for elements within 2^-10 of the row's largest, to 2^-18 of
 // it below), and so is each weight, hi = E4M3(x), lo = E4M3(16 (x - hi)), with
 // sums of their own: 8 to 9 significant bits over 2^-13 .. 448, the first tile's
-// largest weight at 16 .. 32.  x carries the value scale (relative to 2^E, the first tile's
-// largest), so V is never rewritten.  BF16 caches split the weights in two bf16 terms.
+// largest at 16.  x carries the value scale (relative to 2^E, the first tile's largest), and
+// so do the references: a large weight on a small value keeps its bits, and V is never
+// rewritten.  BF16 caches split the weights in two bf16 terms.
 // Nothing but the output is then rounded to fewer bits than the cache has.
 //
 // Groups of four warps share the rows of every key tile (a thread per key, 8 or 16 rows
@@ -493,7 +494,16 @@ __global__ void
         // One pass, unless rows start here, or weights are beyond their type or (FP8) too
         // small for it: the group then takes the rows' maxima first.
         auto prepare = [&](bool starts) {
+            // (the first tile has the first keys of some row, or no row of the group sees any)
+            if (kFP8 && starts && pending == seeing) E = E_top = group_exponent(vs);
+            const int E2 = !kFP8 ? 0 : starts ? E : max(group_exponent(vs), E_top - static_cast<int>(kDown));
             scores(std::false_type());
+            if constexpr (kFP8) {
+              // what meets the E4M3 type is the weight times the value scale
+              const float lv = fmaxf(log2f(vs) - static_cast<float>(E2), -kDown);
+#pragma unroll
+              for (int r = 0; r < NH; ++r) x[r] += lv;
+            }
             group_max(x);
             if (starts) {
 #pragma unroll
@@ -502,11 +512,8 @@ __global__ void
                   nref[r] = x[r] > ninf ? -x[r] : 0.0f;
                   if (key_lane == r) bars.top[w * NH + r] = nref[r];
                 }
-              // (the first tile has the first keys of some row, or no row of the group sees any)
-              if (kFP8 && pending == seeing) E = E_top = group_exponent(vs);
               pending &= ~now;
             } else {
-              const int E2 = kFP8 ? max(group_exponent(vs), E_top - static_cast<int>(kDown)) : 0;
               const uint32_t started = seeing & ~pending;
               // to the tile's maximum, but at most kDown below the highest reference so far
 #pragma unroll

@@ -22,9 +22,9 @@
 // power of two per row: exact for elements within 2^-10 of the row's largest, to
 // 2^-18 of it below), so a score costs what a 16-bit one does and K is never
 // rewritten; its scale multiplies the score in binary32.  V's codes become
-// code * (vs * 2^-e) in binary16, 2^e the tile's largest value scale, which
-// keeps them in range with 2^-11 of relative rounding; 2^e goes into the
-// softmax.  (Splitting the weights in two E4M3 terms instead would spare V's
+// code * (vs * 2^-e) in binary16, with 2^(e + 5) the tile's largest value scale (a power
+// of two of it), so that the largest codes just fit and smaller values keep the 11 bits
+// down to 2^-19 of that scale; 2^e goes into the softmax.  (Splitting the weights in two E4M3 terms instead would spare V's
 // conversion, but takes four more conversions per pair of weights, and those run
 // at 32 lanes a cycle: 983 cycles per row tile against 230 for V's codes.)
 // The softmax takes a maximum only for a row's first keys: later weights are
@@ -269,7 +269,7 @@ __global__ void __launch_bounds__(TileShape<D, kFP8>::kThreads, 1)
     constexpr float kFar = kFP8 ? 16384.0f : 1.0e18f, kAbove = kFP8 ? 3.0f : 0.0f;
     float ref = 0.0f, l = 0.0f;
     bool started = false;                            // the row has seen a key
-    int E = 0;                                       // FP8: O is in units of 2^E
+    int E = 0, E_top = 0;                            // FP8: O is in units of 2^E
     const uint32_t s_tm = tmem + lanes + w * kKeys, o_tm = tmem + lanes + 256 + w * D;
 
     // One key tile: the scores of this thread's row, of the keys from kb on, to weights
@@ -352,6 +352,7 @@ __global__ void __launch_bounds__(TileShape<D, kFP8>::kThreads, 1)
         if (first) {
           ref = top > ninf ? top - kAbove : 0.0f;
           E = e;
+          E_top = e;
           started = true;
         }
       }
@@ -383,15 +384,19 @@ __global__ void __launch_bounds__(TileShape<D, kFP8>::kThreads, 1)
         return (sum0 + sum1) + (sum2 + sum3);
       };
       float sum = weigh();
-      if (__any_sync(0xffffffffu, sum > kFar)) {
+      // (FP8: also where the tile's values are far smaller than those that set E, which would
+      // leave few bits of the weights; E stays within 40 of the largest, so O stays finite)
+      const int to = kFP8 ? max(e, E_top - 40) : 0;
+      if (__any_sync(0xffffffffu, sum > kFar || (kFP8 && started && to < E - 3))) {
         // (every row of the warp moves to its largest score so far)
         const float top = row_max();
         const float want = started ? fmaxf(ref, top - kAbove) : ref;
         const float keep = exp2_approx(ref - want);
-        const float g = kFP8 ? keep * exp2_approx(static_cast<float>(E - e)) : keep;
+        const float g = kFP8 ? keep * exp2_approx(static_cast<float>(E - to)) : keep;
         l *= keep;
         ref = want;
-        E = e;
+        E = to;
+        E_top = max(E_top, E);
         if (i > 0) {
           // (these scores are complete, so every earlier product of this group is too)
 #pragma unroll 1
@@ -751,8 +756,8 @@ __global__ void __launch_bounds__(TileShape<D, kFP8>::kThreads, 1)
         // the tile's largest value scale (scales are not negative: their bits are ordered)
         const uint32_t top = __reduce_max_sync(
             0xffffffffu, __float_as_uint(fmaxf(fmaxf(vs[0], vs[1]), fmaxf(vs[2], vs[3]))));
-        const int ex = min(max(static_cast<int>((top >> 23) & 255u), 1), 253);
-        const float mul = __uint_as_float(static_cast<uint32_t>(254 - ex) << 23);   // 2^-e
+        const int ex = min(max(static_cast<int>((top >> 23) & 255u), 6), 253);
+        const float mul = __uint_as_float(static_cast<uint32_t>(259 - ex) << 23);   // 2^(5 - e)
         uint32_t g[4];
 #pragma unroll
         for (int j = 0; j < 4; ++j) {
@@ -762,7 +767,7 @@ __global__ void __launch_bounds__(TileShape<D, kFP8>::kThreads, 1)
         uint8_t* sc = smem + S::oScale + slot * 1024 + lane * 16;
         *reinterpret_cast<float4*>(sc) = make_float4(ks[0], ks[1], ks[2], ks[3]);
         *reinterpret_cast<uint4*>(sc + 512) = make_uint4(g[0], g[1], g[2], g[3]);
-        if (lane == 0) bars.e[slot] = ex - 127;
+        if (lane == 0) bars.e[slot] = ex - 127 - 5;
         __syncwarp();
         if (lane == 0) mbar_arrive(bar(bars.sc_full[slot]));
         fetch(i + 1, page_next);

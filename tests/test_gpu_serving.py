@@ -288,6 +288,55 @@ def test_many_small_weights_beside_a_large_one(D, fp8, q_len, gap, at, size):
 
 
 @pytest.mark.parametrize("D,fp8", FORMS)
+@pytest.mark.parametrize("q_len", [1, 9, 40])
+@pytest.mark.parametrize("at", [0, 200])
+@pytest.mark.parametrize("small", [10, 14, 18])
+def test_all_weight_on_a_small_value(D, fp8, q_len, at, small):
+    """The key that takes (1 - e^-18 of) the weight has a value 2^-small of its neighbours':
+    the output is that value, to the output's own rounding."""
+    if fp8 and q_len * 4 > 64 and small == 18:
+        pytest.skip("binary16 weights end at 2^-28 of the row's largest: the neighbours, with weights "
+                    "of 2^-34.6, count as nothing, which shows in channels where the value is 0")
+    n = 300
+    q = torch.ones(q_len, 4, D, dtype=torch.bfloat16, device="cuda")
+    k = torch.zeros(n, 1, D, dtype=torch.bfloat16)
+    k[at] = 24.0 / math.sqrt(D)
+    v = rand_bf16(n, 1, D, seed=1)
+    v[at] = (v[at].float() * 2.0 ** -small).to(torch.bfloat16)
+    c = R.Paged([k], [v], 64, fp8)
+    ws = attention_ws()
+    got, lse = L.paged_attention(q, c.k, c.v, c.table, cu([q_len]), i32([n]), ws, max_q=q_len,
+                                 k_scales=c.ks, v_scales=c.vs, causal=False, lse=True)
+    assert L.get_error(ws) == L.MOE_OK
+    want, want_l, tol, tol_l = R.attention(q, c, [q_len], [n], causal=False)
+    assert bool(((got.double() - want).abs() <= tol).all())
+    assert bool(((lse.double() - want_l).abs() <= tol_l).all())
+
+
+@pytest.mark.parametrize("D,fp8", FORMS)
+@pytest.mark.parametrize("q_len", [1, 9, 40])
+@pytest.mark.parametrize("span", [3, 6, 10])
+def test_value_rows_of_very_different_sizes(D, fp8, q_len, span):
+    """Value rows of sizes 2^-span to 2^span in any order under sharp scores: a row whose
+    weight lies on a small value, beside large ones of no weight, keeps its bits."""
+    n = 3000
+    for seed in range(2):
+        g = torch.Generator().manual_seed(seed)
+        k = torch.randn(n, 1, D, generator=g).to(torch.bfloat16)
+        size = torch.exp2((torch.rand(n, 1, 1, generator=g) * 2 - 1) * span)
+        v = (torch.randn(n, 1, D, generator=g) * size).to(torch.bfloat16)
+        q = (torch.randn(q_len, 4, D, generator=g) * 3).to(torch.bfloat16).cuda()
+        c = R.Paged([k], [v], 64, fp8, seed=seed)
+        for ws in (attention_ws(), L.new_workspace(L.ATTENTION_CTRL_BYTES)):
+            got, lse = L.paged_attention(q, c.k, c.v, c.table, cu([q_len]), i32([n]), ws,
+                                         max_q=q_len, k_scales=c.ks, v_scales=c.vs, lse=True)
+            assert L.get_error(ws) == L.MOE_OK
+            want, want_l, tol, tol_l = R.attention(q, c, [q_len], [n])
+            assert bool(((got.double() - want).abs() <= tol).all())
+            assert bool(((lse.double() - want_l).abs() <= tol_l).all())
+
+
+@pytest.mark.parametrize("D,fp8", FORMS)
 @pytest.mark.parametrize("q_len", [2, 150])
 @pytest.mark.parametrize("softcap", [0.0, 20.0])
 def test_a_nan_reaches_its_rows_and_no_others(D, fp8, q_len, softcap):
