@@ -331,7 +331,7 @@ __global__ void
     // (FP8) this thread's key: its page two tiles ahead, its scales one
     auto page_of = [&](int i) {
       const int key = k0 + i * kKeys + key_lane;
-      return kFP8 && key < k1 ? __ldg(table + (key >> p.c.page_log2)) : -1;
+      return kFP8 && key < k1 && key >= t.lo ? __ldg(table + (key >> p.c.page_log2)) : -1;
     };
     float ks_next = 0.0f, vs_next = 0.0f;
     auto fetch = [&](int i, int page) {
@@ -500,7 +500,7 @@ __global__ void
             scores(std::false_type());
             if constexpr (kFP8) {
               // what meets the E4M3 type is the weight times the value scale
-              const float lv = fmaxf(log2f(vs) - static_cast<float>(E2), -kDown);
+              const float lv = fminf(fmaxf(log2f(vs) - static_cast<float>(E2), -kDown), kDown);
 #pragma unroll
               for (int r = 0; r < NH; ++r) x[r] += lv;
             }
@@ -849,6 +849,7 @@ __global__ void
     // =================================================================== TMA loads
     const int box = min(1 << p.c.page_log2, kKeys);
     const int segs = kKeys / box;
+    const int first_key = max(t.lo, k0);                  // pages before a window are not read
     const uint64_t policy = policy_evict_first();         // (read once)
     constexpr int kRowBytes = kFP8 ? D : 2 * D;
     bool ok = p.drop_producer == 0;
@@ -856,7 +857,7 @@ __global__ void
     auto load = [&](bool v, int i) -> bool {
       const int kb = k0 + i * kKeys;
       const int key = kb + lane * box;
-      const bool mine = lane < segs && key < k1;
+      const bool mine = lane < segs && key < k1 && key + box > first_key;
       int page = mine ? __ldg(table + (key >> p.c.page_log2)) : 0;
       if (page < 0 || page >= p.c.num_pages) {
         set_error(p.ctrl, MOE_ERR_DEVICE_FAULT, 22);
@@ -866,7 +867,7 @@ __global__ void
       if (!wait(bar(bars.empty[slot]), ((f / S::kSlots) & 1) ^ 1)) return false;
       const uint32_t full = bar(bars.full[slot]);
       if (lane == 0) {
-        const int loaded = min(segs, (k1 - kb + box - 1) / box);
+        const int loaded = min(segs, (k1 - kb + box - 1) / box) - max(0, (first_key - kb) / box);
         mbar_arrive_expect_tx(full, loaded * box * kRowBytes);
       }
       __syncwarp();

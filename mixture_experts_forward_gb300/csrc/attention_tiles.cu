@@ -658,6 +658,7 @@ __global__ void __launch_bounds__(TileShape<D, kFP8>::kThreads, 1)
       // ================================================================= TMA loads
       const int box = min(1 << p.c.page_log2, kKeys);
       const int segs = kKeys / box;
+      const int first_key = max(t.lo, k0);           // pages before a window are not read
       const uint64_t policy = p.row_tiles > 1 ? policy_evict_last() : policy_evict_first();
       constexpr int kRowBytes = kFP8 ? D : 2 * D;
       bool ok = p.drop_producer == 0;
@@ -680,7 +681,7 @@ __global__ void __launch_bounds__(TileShape<D, kFP8>::kThreads, 1)
       auto load = [&](Ring& r, bool v, int i) {
         const int kb = k0 + i * kKeys;
         const int key = kb + lane * box;
-        const bool mine = lane < segs && key < k1;
+        const bool mine = lane < segs && key < k1 && key + box > first_key;
         int page = mine ? __ldg(table + (key >> p.c.page_log2)) : 0;
         if (page < 0 || page >= p.c.num_pages) {
           set_error(p.ctrl, MOE_ERR_DEVICE_FAULT, 22);
@@ -690,7 +691,7 @@ __global__ void __launch_bounds__(TileShape<D, kFP8>::kThreads, 1)
         if (!wait(r.empty + 8 * slot, ((r.f / r.slots) & 1) ^ 1)) return false;
         const uint32_t full = r.full + 8 * slot;
         if (lane == 0) {
-          const int loaded = min(segs, (k1 - kb + box - 1) / box);
+          const int loaded = min(segs, (k1 - kb + box - 1) / box) - max(0, (first_key - kb) / box);
           mbar_arrive_expect_tx(full, loaded * box * kRowBytes);
         }
         __syncwarp();
@@ -741,7 +742,7 @@ __global__ void __launch_bounds__(TileShape<D, kFP8>::kThreads, 1)
                             << p.c.page_log2) + (key & page_mask);
 #pragma unroll
         for (int j = 0; j < 4; ++j) {
-          const bool x = have && key + j < k1;
+          const bool x = have && key + j < k1 && key + j >= t.lo;
           ks[j] = x ? __ldg(p.c.k_scales + at + j) : 0.0f;
           vs[j] = x ? __ldg(p.c.v_scales + at + j) : 0.0f;
         }

@@ -337,6 +337,52 @@ def test_value_rows_of_very_different_sizes(D, fp8, q_len, span):
 
 
 @pytest.mark.parametrize("D,fp8", FORMS)
+@pytest.mark.parametrize("page", [16, 64, 256])
+@pytest.mark.parametrize("q_len", [1, 9, 40])
+@pytest.mark.parametrize("softcap", [0.0, 20.0])
+def test_pages_before_the_window_may_be_gone(D, fp8, page, q_len, softcap):
+    """Pages wholly before the first token's window have left the table, and the positions
+    of a page that are before it are NaN."""
+    n, window = 1100, 300
+    first = n - q_len - window + 1
+    keys, vals = rand_bf16(n, 2, D, seed=1), rand_bf16(n, 2, D, seed=2)
+    q = rand_bf16(q_len, 4, D, seed=3).cuda()
+    c = R.Paged([keys], [vals], page, fp8)
+    want, want_l, tol, tol_l = R.attention(q, c, [q_len], [n], window=window, softcap=softcap)
+    for pos in range(first):
+        pg = int(c.table[0, pos // page])
+        for x in (c.k, c.v):
+            x[pg, :, pos % page] = R.NAN_CODE if fp8 else math.nan
+        for x in (c.ks, c.vs) if fp8 else ():
+            x[pg, :, pos % page] = math.nan
+    c.table[0, :first // page] = -1
+    ws = attention_ws()
+    got, lse = L.paged_attention(q, c.k, c.v, c.table, cu([q_len]), i32([n]), ws, max_q=q_len,
+                                 k_scales=c.ks, v_scales=c.vs, window=window, softcap=softcap,
+                                 lse=True)
+    assert L.get_error(ws) == L.MOE_OK
+    assert bool(((got.double() - want).abs() <= tol).all())
+    assert bool(((lse.double() - want_l).abs() <= tol_l).all())
+
+
+@pytest.mark.parametrize("D,fp8", FORMS)
+@pytest.mark.parametrize("q_len", [1, 9, 40])
+def test_an_infinite_value_leaves_lse_alone(D, fp8, q_len):
+    n = 500
+    k, v = rand_bf16(n, 1, D, seed=1), rand_bf16(n, 1, D, seed=2)
+    v[200, 0, 3] = math.inf
+    q = rand_bf16(q_len, 4, D, seed=3).cuda()
+    c = R.Paged([k], [v], 16, fp8)
+    ws = attention_ws()
+    got, lse = L.paged_attention(q, c.k, c.v, c.table, cu([q_len]), i32([n]), ws, max_q=q_len,
+                                 k_scales=c.ks, v_scales=c.vs, lse=True)
+    assert L.get_error(ws) == L.MOE_OK
+    _, want_l, _, tol_l = R.attention(q, c, [q_len], [n])
+    assert not bool(torch.isfinite(got[..., 3].float()).any())
+    assert bool(((lse.double() - want_l).abs() <= tol_l).all())
+
+
+@pytest.mark.parametrize("D,fp8", FORMS)
 @pytest.mark.parametrize("q_len", [2, 150])
 @pytest.mark.parametrize("softcap", [0.0, 20.0])
 def test_a_nan_reaches_its_rows_and_no_others(D, fp8, q_len, softcap):
