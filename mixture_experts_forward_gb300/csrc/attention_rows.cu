@@ -847,8 +847,8 @@ __global__ void
     }
   } else {
     // =================================================================== TMA loads
-    const int box = min(1 << p.c.page_log2, kKeys);
-    const int segs = kKeys / box;
+    const int box_log2 = min(p.c.page_log2, 7), box = 1 << box_log2;   // (kKeys = 2^7)
+    const int segs = kKeys >> box_log2;
     const int first_key = max(t.lo, k0);                  // pages before a window are not read
     const uint64_t policy = policy_evict_first();         // (read once)
     constexpr int kRowBytes = kFP8 ? D : 2 * D;
@@ -867,7 +867,8 @@ __global__ void
       if (!wait(bar(bars.empty[slot]), ((f / S::kSlots) & 1) ^ 1)) return false;
       const uint32_t full = bar(bars.full[slot]);
       if (lane == 0) {
-        const int loaded = min(segs, (k1 - kb + box - 1) / box) - max(0, (first_key - kb) / box);
+        const int loaded = min(segs, (k1 - kb + box - 1) >> box_log2) -
+                           max(0, (first_key - kb) >> box_log2);
         mbar_arrive_expect_tx(full, loaded * box * kRowBytes);
       }
       __syncwarp();
