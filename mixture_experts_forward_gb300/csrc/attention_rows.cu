@@ -1,7 +1,7 @@
 // Attention of few rows over the paged cache: single tokens (decode) and
 // short drafted runs, up to 64 rows (new tokens x query heads of one cache
 // head).  Every cached byte is read once, by TMA, and meets few rows: decode is bound
-// by HBM (16 rows, 304 tiles of 8192 keys: 6.8 TB/s from BF16, 6.2 from E4M3), 33 to 64
+// by HBM (16 rows, 304 tiles of 8192 keys: 6.7 TB/s from BF16, 6.2 from E4M3), 33 to 64
 // rows over E4M3 codes by the softmax warps (conversions of the weights).
 //
 // The products are turned round, so that a key is a lane and a row a column:
@@ -854,18 +854,26 @@ __global__ void
     constexpr int kRowBytes = kFP8 ? D : 2 * D;
     bool ok = p.drop_producer == 0;
     int f = 0;
-    auto load = [&](bool v, int i) -> bool {
+    auto is_mine = [&](int i) {
+      const int key = k0 + i * kKeys + lane * box;
+      return lane < segs && key < k1 && key + box > first_key;
+    };
+    // this lane's page of key tile i; fetched some tiles ahead
+    auto page_at = [&](int i) {
+      return is_mine(i) ? __ldg(table + ((k0 + i * kKeys + lane * box) >> p.c.page_log2)) : 0;
+    };
+    int slot = 0;
+    uint32_t parity = 1;
+    auto load = [&](bool v, int i, int page) -> bool {
       const int kb = k0 + i * kKeys;
       const int key = kb + lane * box;
-      const bool mine = lane < segs && key < k1 && key + box > first_key;
-      int page = mine ? __ldg(table + (key >> p.c.page_log2)) : 0;
+      const bool mine = is_mine(i);
       if (page < 0 || page >= p.c.num_pages) {
         set_error(p.ctrl, MOE_ERR_DEVICE_FAULT, 22);
         page = 0;                          // (a place that exists)
       }
-      const int slot = f % S::kSlots;
-      if (!wait(bar(bars.empty[slot]), ((f / S::kSlots) & 1) ^ 1)) return false;
-      const uint32_t full = bar(bars.full[slot]);
+      if (!wait(bar(bars.empty[0]) + 8 * slot, parity)) return false;
+      const uint32_t full = bar(bars.full[0]) + 8 * slot;
       if (lane == 0) {
         const int loaded = min(segs, (k1 - kb + box - 1) >> box_log2) -
                            max(0, (first_key - kb) >> box_log2);
@@ -887,14 +895,23 @@ __global__ void
       }
       __syncwarp();
       ++f;
+      if (++slot == S::kSlots) {
+        slot = 0;
+        parity ^= 1;
+      }
       return true;
     };
     // in the order that the MMAs take them: keys of the first two tiles, then each tile's
     // values and the keys of the tile after the next
-    for (int i = 0; i < 2 && i < n && ok; ++i) ok = load(false, i);
+    int pages[3] = {page_at(0), page_at(1), page_at(2)};
+    for (int i = 0; i < 2 && i < n && ok; ++i) ok = load(false, i, pages[i]);
     for (int i = 0; i < n && ok; ++i) {
-      ok = load(true, i);
-      if (ok && i + 2 < n) ok = load(false, i + 2);
+      const int next = page_at(i + 3);
+      ok = load(true, i, pages[0]);
+      if (ok && i + 2 < n) ok = load(false, i + 2, pages[2]);
+      pages[0] = pages[1];
+      pages[1] = pages[2];
+      pages[2] = next;
     }
     if (!ok)                               // copies in flight land before the memory goes
       for (int g = max(0, f - S::kSlots); g < f; ++g)
