@@ -87,7 +87,10 @@ struct RowsBars {
   alignas(16) float part[kGroups][4][N / kGroups];   // per group and warp: maxima or sums
   alignas(16) float scale[N];     // of the row's sums at the end
   uint32_t vs[kGroups][4];        // per group and warp: largest value scale (bits)
-  uint32_t large[kGroups][4];     // per group and warp: rows that have a large weight (bits)
+  // per group and warp: rows that have a large weight (bits).  A buffer for even key tiles and
+  // one for odd: with scores and weights double-buffered, nothing but the barrier of the next
+  // tile keeps a warp from storing its word while another still reads the tile before's.
+  uint32_t large[2][kGroups][4];
 };
 
 // D[tmem] (+)= A[smem] * B[smem], any layouts (both descriptors' words given).
@@ -633,13 +636,14 @@ __global__ void
 #pragma unroll
           for (int r = 0; r < NH; ++r) large |= sum[r] >= least ? 1u << r : 0u;
           large = __reduce_or_sync(0xffffffffu, large);
-          if (lane == 0) bars.large[w][warp & 3] = large;
+          if (lane == 0) bars.large[i & 1][w][warp & 3] = large;
         }
         bool again = named_bar_any(group_bar, 128, far);
-        if constexpr (kFP8)
-          again = again || (seeing & ~pending &
-                            ~(bars.large[w][0] | bars.large[w][1] | bars.large[w][2] |
-                              bars.large[w][3])) != 0u;
+        if constexpr (kFP8) {
+          const uint32_t(&large)[4] = bars.large[i & 1][w];
+          again = again ||
+                  (seeing & ~pending & ~(large[0] | large[1] | large[2] | large[3])) != 0u;
+        }
         if (again) {
           prepare(false);
           pass();

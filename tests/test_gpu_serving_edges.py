@@ -1,0 +1,84 @@
+"""Attention over the paged cache where it can go wrong: rows of the dispatch's edges, calls in
+which the groups of the few-row form disagree about a second pass, windows and values at the ends
+of their types, batches of unlike sequences (against 64 bits)."""
+import math
+
+import pytest
+import torch
+
+import serving_reference as R
+from gpu_helpers import ensure_built
+from mixture_experts_forward_gb300 import _lib as L
+
+pytestmark = pytest.mark.gpu
+
+FORMS = [(64, False), (64, True), (128, False), (128, True)]
+
+
+@pytest.fixture(scope="module", autouse=True)
+def built():
+    ensure_built()
+
+
+@pytest.fixture(scope="module")
+def ws(built):
+    return L.new_workspace(L.ATTENTION_WS_BYTES)
+
+
+def i32(x):
+    return torch.tensor(x, dtype=torch.int32, device="cuda")
+
+
+def cu(lens):
+    at = [0]
+    for n in lens:
+        at.append(at[-1] + n)
+    return i32(at)
+
+
+def rand_bf16(*shape, seed=0, scale=1.0):
+    g = torch.Generator().manual_seed(seed)
+    return (torch.randn(*shape, generator=g) * scale).to(torch.bfloat16)
+
+
+def attend(q, c, q_lens, kv_lens, ws, **kw):
+    """(out, lse) of a call that records no fault and leaves its counters zero."""
+    got = L.paged_attention(q, c.k, c.v, c.table, cu(q_lens), i32(kv_lens), ws, max_q=max(q_lens),
+                            k_scales=c.ks, v_scales=c.vs, lse=True, **kw)
+    assert L.get_error(ws) == L.MOE_OK
+    assert not bool(ws[L.CTRL_BYTES:L.ATTENTION_CTRL_BYTES].any()), "counters left behind"
+    return got
+
+
+def within(got, want, tol):
+    """got is within tol of want, and as infinite as want."""
+    got = got.double()
+    inf = torch.isinf(want)
+    return torch.equal(got[inf], want[inf]) and bool(((got - want).abs() <= tol)[~inf].all())
+
+
+@pytest.mark.parametrize("D", [64, 128])
+@pytest.mark.parametrize("q_len,Hq", [(1, 16), (5, 8), (12, 4), (15, 4)])
+def test_groups_that_disagree_about_a_second_pass(D, q_len, Hq, ws):
+    """FP8, few rows: key tiles whose weights are small for some rows and large for others, in
+    an order that changes from tile to tile, so that some warps take a second pass in nearly every
+    tile and others in none.  Repeated calls give the same bits."""
+    n = 128 * 60 + 17
+    g = torch.Generator().manual_seed(D + q_len)
+    k = torch.randn(n, 1, D, generator=g) * 0.3
+    # channel x is strong in some key tiles, and query row x looks at channel x
+    level = torch.randn(60 + 1, D, generator=g) * 3
+    k += level.repeat_interleave(128, 0)[:n, None, :]
+    q = torch.randn(q_len, Hq, D, generator=g) * 0.05
+    for r in range(q_len * Hq):
+        q[r // Hq, r % Hq, r % D] += 12.0
+    c = R.Paged([k.to(torch.bfloat16)], [rand_bf16(n, 1, D, seed=3)], 64, True)
+    q = q.to(torch.bfloat16).cuda()
+    want, want_l, tol, tol_l = R.attention(q, c, [q_len], [n])
+    one = L.new_workspace(L.ATTENTION_CTRL_BYTES)             # no room for a split: one CTA
+    for w in (one, ws):
+        first = attend(q, c, [q_len], [n], w)
+        assert within(first[0], want, tol)
+        for _ in range(50):
+            again = attend(q, c, [q_len], [n], w)
+            assert torch.equal(again[0], first[0]) and torch.equal(again[1], first[1])
