@@ -15,9 +15,9 @@
 // a second pass and a rescale of O follow).
 //
 // E4M3 caches go to the tensor core as they are, in both products: the query is the
-// sum of two E4M3 terms (exact for elements within 2^-10 of the row's largest, to 2^-18 of
-// it below), and so is each weight, hi = E4M3(x), lo = E4M3(16 (x - hi)), with
-// sums of their own: 8 to 9 significant bits over 2^-13 .. 448, the first tile's
+// sum of an E4M3 and an E5M2 term (exact for elements within 2^-13 of the row's largest, to
+// 2^-21 of it below), and each weight of two E4M3 terms, hi = E4M3(x), lo = E4M3(16 (x - hi)),
+// with sums of their own: 8 to 9 significant bits over 2^-13 .. 448, the first tile's
 // largest at 16.  x carries the value scale (relative to 2^E, the first tile's largest), and
 // so do the references: a large weight on a small value keeps its bits, and V is never
 // rewritten.  BF16 caches split the weights in two bf16 terms.
@@ -763,8 +763,8 @@ __global__ void
             for (int s = 0; s < 2 * (D / 32); ++s) {     // the query's hi, then lo
               const uint32_t off = ((s % (D / 32)) * 32) >> 4;
               umma_ss<true>(tm + buf * N, a + off, kTileHi,
-                            q_lo + (s / (D / 32)) * (S::kQTerm >> 4) + off, kTileHi, idesc_s,
-                            s > 0);
+                            q_lo + (s / (D / 32)) * (S::kQTerm >> 4) + off, kTileHi,
+                            s < D / 32 ? idesc_s : idesc_s | kBIsE5M2, s > 0);
             }
           } else {
 #pragma unroll

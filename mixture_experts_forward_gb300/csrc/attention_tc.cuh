@@ -107,7 +107,9 @@ __device__ __forceinline__ void add2(float& d0, float& d1, float a0, float a1) {
       : "f"(a0), "f"(a1));
 }
 
-// D[tmem] (+)= A[smem] * B[smem]^T over 32 E4M3 elements, K-major tiles of codes.
+// D[tmem] (+)= A[smem] * B[smem]^T over 32 8-bit elements, K-major tiles of codes.
+// (kind::f8f6f4 takes a type for each operand: these bits make A or B, made as E4M3, an E5M2.)
+constexpr uint32_t kAIsE5M2 = 1u << 7, kBIsE5M2 = 1u << 10;
 template <int D>
 __device__ __forceinline__ void umma_codes(uint32_t d_tmem, uint32_t a_lo, uint32_t b_lo,
                                            uint32_t idesc, uint32_t accumulate) {
@@ -176,8 +178,17 @@ inline bool cache_maps(const AttnParams& p, int D, bool fp8, CUtensorMap* k, CUt
   return cache_map(k, p.c.k, D, fp8, rows, box) && cache_map(v, p.c.v, D, fp8, rows, box);
 }
 
-// Eight bf16 elements (four words), times a power of two, as the sums of two
-// E4M3 terms each.
+__device__ __forceinline__ uint16_t cvt_e5m2x2(float lo, float hi) {
+  uint16_t r;
+  asm("cvt.rn.satfinite.e5m2x2.f32 %0, %1, %2;" : "=h"(r) : "f"(hi), "f"(lo));
+  return r;
+}
+
+// Eight bf16 elements x (four words), times a power of two that brings the row's largest into
+// [2^7, 2^8), as the sums of an E4M3 and an E5M2 term: hi = E4M3(x), lo = E5M2(x - hi).  From
+// 2^-6 on hi leaves at most 8 units of x's last place, which an E5M2 holds exactly, and below
+// it at most 2^-10, rounded by at most 2^-14: exact for elements within 2^-13 of the row's
+// largest, to 2^-21 of it below.  (An E4M3 lo ends at 2^-9 and loses up to 2^-17.)
 __device__ __forceinline__ void two_terms(const uint32_t (&x)[4], float mul, uint32_t (&hi)[2],
                                           uint32_t (&lo)[2]) {
 #pragma unroll
@@ -189,7 +200,7 @@ __device__ __forceinline__ void two_terms(const uint32_t (&x)[4], float mul, uin
       const float x1 = __uint_as_float(x[2 * i + j] & 0xffff0000u) * mul;
       const uint16_t hc = cvt_e4m3x2(x0, x1);
       const float2 f = e4m3x2_to_f32(hc);
-      const uint16_t lc = cvt_e4m3x2(x0 - f.x, x1 - f.y);
+      const uint16_t lc = cvt_e5m2x2(x0 - f.x, x1 - f.y);
       hi[i] |= static_cast<uint32_t>(hc) << (16 * j);
       lo[i] |= static_cast<uint32_t>(lc) << (16 * j);
     }

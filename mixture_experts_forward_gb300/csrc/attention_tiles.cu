@@ -18,9 +18,9 @@
 //   warp 10          (FP8) the tiles' scales;
 //   warps 12-15      (FP8) turn V's codes into binary16 tiles.
 // E4M3 caches: K's codes go to the tensor core as they are (kind::f8f6f4), against
-// the query as the sum of two E4M3 terms (hi = E4M3(q), lo = E4M3(q - hi), after a
-// power of two per row: exact for elements within 2^-10 of the row's largest, to
-// 2^-18 of it below), so a score costs what a 16-bit one does and K is never
+// the query as the sum of two terms (hi = E4M3(q), lo = E5M2(q - hi), after a
+// power of two per row: exact for elements within 2^-13 of the row's largest, to
+// 2^-21 of it below), so a score costs what a 16-bit one does and K is never
 // rewritten; its scale multiplies the score in binary32.  V's codes become
 // code * (vs * 2^-e) in binary16, with 2^(e + 5) the tile's largest value scale (a power
 // of two of it), so that the largest codes just fit and smaller values keep the 11 bits
@@ -555,7 +555,7 @@ __global__ void __launch_bounds__(TileShape<D, kFP8>::kThreads, 1)
             for (int s = 0; s < 2 * (D / 32); ++s) {     // hi, then lo
               const uint32_t off = ((s % (D / 32)) * 32) >> 4;
               umma_codes<D>(tm + w * kKeys, q + (s / (D / 32)) * (S::kCodeBytes >> 4) + off,
-                            k + off, idesc_s, s > 0);
+                            k + off, s < D / 32 ? idesc_s : idesc_s | kAIsE5M2, s > 0);
             }
           } else {
 #pragma unroll

@@ -78,7 +78,26 @@ def test_groups_that_disagree_about_a_second_pass(D, q_len, Hq, ws):
     one = L.new_workspace(L.ATTENTION_CTRL_BYTES)             # no room for a split: one CTA
     for w in (one, ws):
         first = attend(q, c, [q_len], [n], w)
-        assert within(first[0], want, tol)
+        assert within(first[0], want, tol) and within(first[1], want_l, tol_l)
         for _ in range(50):
             again = attend(q, c, [q_len], [n], w)
             assert torch.equal(again[0], first[0]) and torch.equal(again[1], first[1])
+
+
+@pytest.mark.parametrize("D", [64, 128])
+@pytest.mark.parametrize("q_len", [1, 9, 70])
+@pytest.mark.parametrize("fp8", [True, False])
+def test_small_query_elements_beside_a_large_one(D, q_len, fp8, ws):
+    """The scores come from elements between 2^-10.3 and 2^-6.9 of their row's largest, which
+    meets keys of 0: the query's terms hold them exactly."""
+    n = 300
+    g = torch.Generator().manual_seed(q_len)
+    q = (torch.rand(q_len, 4, D, generator=g) * 0.09 + 0.01) * (torch.randint(0, 2, (q_len, 4, D), generator=g) * 2 - 1)
+    q[..., 5] = 12.0
+    k = 1.0 + 0.1 * torch.randn(n, 1, D, generator=g)
+    k[..., 5] = 0.0
+    c = R.Paged([k.to(torch.bfloat16)], [rand_bf16(n, 1, D, seed=3)], 64, fp8)
+    q = q.to(torch.bfloat16).cuda()
+    want, want_l, tol, tol_l = R.attention(q, c, [q_len], [n])
+    out, lse = attend(q, c, [q_len], [n], ws)
+    assert within(out, want, tol) and within(lse, want_l, tol_l)
