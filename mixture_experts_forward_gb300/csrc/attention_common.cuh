@@ -51,8 +51,11 @@ struct TileView {
 __device__ __forceinline__ int row_hi(const AttnParams& p, const TileView& t, int tok) {
   return p.causal ? min(t.kv_len, t.kv_len - t.q_len + tok + 1) : t.kv_len;
 }
+// (compared before the subtraction: a window may be any int, and a sequence may have more new
+// tokens than positions)
 __device__ __forceinline__ int row_lo(const AttnParams& p, const TileView& t, int tok) {
-  return p.window > 0 ? max(0, t.kv_len - t.q_len + tok + 1 - p.window) : 0;
+  const int end = t.kv_len - t.q_len + tok + 1;
+  return p.window > 0 && end > p.window ? end - p.window : 0;
 }
 
 __device__ __forceinline__ TileView tile_view(const AttnParams& p, int b, int h, int tile,

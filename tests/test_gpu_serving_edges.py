@@ -101,3 +101,19 @@ def test_small_query_elements_beside_a_large_one(D, q_len, fp8, ws):
     want, want_l, tol, tol_l = R.attention(q, c, [q_len], [n])
     out, lse = attend(q, c, [q_len], [n], ws)
     assert within(out, want, tol) and within(lse, want_l, tol_l)
+
+
+@pytest.mark.parametrize("D,fp8", FORMS)
+@pytest.mark.parametrize("q_len,Hq", [(12, 2), (15, 8), (150, 2), (300, 4)])
+@pytest.mark.parametrize("window", [2 ** 31 - 1, 2 ** 31 - 100])
+def test_a_window_as_wide_as_it_can_be(D, fp8, q_len, Hq, window, ws):
+    """Wider than any cache: the rows see what they see without one, where a sequence has more
+    new tokens than positions too."""
+    kv = [8, 100, 700]
+    lens = [q_len, q_len, min(q_len, 20)]
+    c = R.Paged([rand_bf16(n, 2, D, seed=n) for n in kv], [rand_bf16(n, 2, D, seed=n + 1) for n in kv],
+                32, fp8)
+    q = rand_bf16(sum(lens), Hq, D, seed=3).cuda()
+    out, lse = attend(q, c, lens, kv, ws, window=window)
+    want, want_l, tol, tol_l = R.attention(q, c, lens, kv)
+    assert within(out, want, tol) and within(lse, want_l, tol_l)
