@@ -170,8 +170,8 @@ moe_status_t moe_paged_attention(const moe_attention_args* a, void* ws, size_t w
       static_cast<long long>((ws_bytes - MOE_ATTENTION_CTRL_BYTES) / part_bytes);
   // The keys a tile may see, by the caller's hint
   long long span = a->max_kv > 0 && a->max_kv < room ? a->max_kv : room;
-  if (a->window > 0 && a->window + tile_rows / group + 128 < span)
-    span = a->window + tile_rows / group + 128;
+  const long long reach = static_cast<long long>(a->window) + tile_rows / group + 128;
+  if (a->window > 0 && reach < span) span = reach;
   const long long most = (span + 255) / 256;      // parts of at least 256 keys
   const cudaStream_t st = static_cast<cudaStream_t>(stream);
   if (few) {
@@ -182,8 +182,7 @@ moe_status_t moe_paged_attention(const moe_attention_args* a, void* ws, size_t w
     const bool share = tiles < places && most > 1 && places <= room_parts && places <= kMaxParts;
     p.splits = share ? static_cast<int>(places) : 1;
     p.whole = static_cast<int>(share ? places : tiles);
-    p.span = static_cast<int>(a->window > 0 && a->window + rows / group + 128 < room
-                                  ? a->window + rows / group + 128 : room);
+    p.span = static_cast<int>(a->window > 0 && reach < room ? reach : room);
     return cuda_status(launch_attention_rows(p, tile_rows, D, fp8, st));
   }
   // One tile per SM at a time.  The tiles past the last full round, which are the early rows,

@@ -117,3 +117,19 @@ def test_a_window_as_wide_as_it_can_be(D, fp8, q_len, Hq, window, ws):
     out, lse = attend(q, c, lens, kv, ws, window=window)
     want, want_l, tol, tol_l = R.attention(q, c, lens, kv)
     assert within(out, want, tol) and within(lse, want_l, tol_l)
+
+
+@pytest.mark.parametrize("D,fp8", FORMS)
+@pytest.mark.parametrize("q_lens,kv,Hq,page", [([1], [40000], 8, 64), ([30, 3], [9000, 40], 4, 16),
+                                               ([150, 20], [6000, 700], 4, 32), ([12, 12], [8, 100], 2, 32),
+                                               ([300, 20], [100, 700], 4, 32)])
+def test_a_window_wider_than_the_cache_is_none(D, fp8, q_lens, kv, Hq, page, ws):
+    """The same split as without a window, so the same bits: 2^31 - 1, and just as wide as the
+    table's positions."""
+    c = R.Paged([rand_bf16(n, 1, D, seed=n) for n in kv], [rand_bf16(n, 1, D, seed=n + 1) for n in kv],
+                page, fp8)
+    q = rand_bf16(sum(q_lens), Hq, D, seed=3).cuda()
+    plain, plain_lse = attend(q, c, q_lens, kv, ws)
+    for window in (2 ** 31 - 1, 2 ** 31 - 100, c.table.shape[1] * page):
+        out, lse = attend(q, c, q_lens, kv, ws, window=window)
+        assert torch.equal(out, plain) and torch.equal(lse, plain_lse)
