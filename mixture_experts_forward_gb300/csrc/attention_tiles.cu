@@ -467,7 +467,7 @@ __global__ void __launch_bounds__(TileShape<D, kFP8>::kThreads, 1)
           tmem_ld16(o_tm + d, o);
           tmem_ld_wait(o);
 #pragma unroll
-          for (int j = 0; j < 16; ++j) o[j] *= g;
+          for (int j = 0; j < 16; ++j) o[j] = l == 0.0f ? 0.0f : o[j] * g;   // (0 * NaN)
         }
         if (!real) continue;
         if (split) {

@@ -133,3 +133,26 @@ def test_a_window_wider_than_the_cache_is_none(D, fp8, q_lens, kv, Hq, page, ws)
     for window in (2 ** 31 - 1, 2 ** 31 - 100, c.table.shape[1] * page):
         out, lse = attend(q, c, q_lens, kv, ws, window=window)
         assert torch.equal(out, plain) and torch.equal(lse, plain_lse)
+
+
+@pytest.mark.parametrize("D,fp8", FORMS)
+@pytest.mark.parametrize("bad", [math.nan, math.inf])
+@pytest.mark.parametrize("q_len,Hq", [(15, 2), (15, 8), (40, 2), (120, 2), (300, 2)])
+def test_rows_that_see_nothing_beside_a_bad_value(D, fp8, bad, q_len, Hq, ws):
+    """More new tokens than positions, and a value row that is not finite: the rows that see no
+    key give 0 and -inf, whatever lies in a value."""
+    n = 9
+    k, v = rand_bf16(n, 1, D, seed=1), rand_bf16(n, 1, D, seed=2)
+    c = R.Paged([k], [v], 16, fp8)
+    pg, at = int(c.table[0, 0]), 4
+    if fp8:
+        c.v[pg, 0, at, 5] = R.NAN_CODE if math.isnan(bad) else 0x7e
+        c.vs[pg, 0, at] = bad
+    else:
+        c.v[pg, 0, at, 5] = bad
+    q = rand_bf16(q_len, Hq, D, seed=3).cuda()
+    for w in (ws, L.new_workspace(L.ATTENTION_CTRL_BYTES)):
+        out, lse = attend(q, c, [q_len], [n], w)
+        assert bool((out[:q_len - n] == 0).all()) and bool((lse[:q_len - n] == -math.inf).all())
+        assert bool(torch.isfinite(lse[q_len - n:]).all())
+        assert not bool(torch.isfinite(out[-1, :, 5]).any())
