@@ -401,7 +401,7 @@ __global__ void
     const float cap = p.softcap, cap_k = cap > 0.0f ? 2.0f * kLog2e / cap : 0.0f;
     const float sc = fabsf(p.scale) * (cap > 0.0f ? 1.0f : kLog2e);
     float nref[NH], l[NH];                               // minus the rows' references; sums
-    uint32_t pending = 0;                                // rows that have not seen their first key
+    uint32_t pending = 0;                                // rows that have not seen a score above -inf
     int lo_max = k0, hi_min = k1;
 #pragma unroll
     for (int r = 0; r < NH; ++r) {
@@ -497,7 +497,7 @@ __global__ void
         // One pass, unless rows start here, or weights are beyond their type or (FP8) too
         // small for it: the group then takes the rows' maxima first.
         auto prepare = [&](bool starts) {
-            // (the first tile has the first keys of some row, or no row of the group sees any)
+            // (until a row has started, every weight is 0)
             if (kFP8 && starts && pending == seeing) E = E_top = group_exponent(vs);
             const int E2 = !kFP8 ? 0 : starts ? E : max(group_exponent(vs), E_top - static_cast<int>(kDown));
             scores(std::false_type());
@@ -511,11 +511,11 @@ __global__ void
             if (starts) {
 #pragma unroll
               for (int r = 0; r < NH; ++r)
-                if (now >> r & 1u) {
-                  nref[r] = x[r] > ninf ? -x[r] : 0.0f;
+                if ((now >> r & 1u) && x[r] > ninf) {    // (all -inf: the next tile's keys)
+                  nref[r] = -x[r];
                   if (key_lane == r) bars.top[w * NH + r] = nref[r];
+                  pending &= ~(1u << r);
                 }
-              pending &= ~now;
             } else {
               const uint32_t started = seeing & ~pending;
               // to the tile's maximum, but at most kDown below the highest reference so far
@@ -690,7 +690,7 @@ __global__ void
         const float all = saw ? (bars.part[w][0][key_lane] + bars.part[w][1][key_lane]) +
                                     (bars.part[w][2][key_lane] + bars.part[w][3][key_lane])
                               : 0.0f;
-        const float rf = saw ? mine : ninf;
+        const float rf = all != 0.0f ? mine : ninf;
         bars.scale[row] = !saw ? 0.0f : split ? unit : all == 0.0f ? 0.0f : unit / all;
         if (row < t.rows) {
           if (split) {

@@ -345,12 +345,13 @@ __global__ void __launch_bounds__(TileShape<D, kFP8>::kThreads, 1)
         for (int j = 4; j < kCols; ++j) x[j & 3] = fmaxf(x[j & 3], s[j]);
         return fmaxf(fmaxf(x[0], x[1]), fmaxf(x[2], x[3])) * f;
       };
-      // a row's first keys set its reference
+      // a row's first keys set its reference (the first of which a score is not -inf: a key may
+      // be as low as its type goes)
       const bool first = !started && kb < r_hi && kb + kKeys > r_lo;
       if (__any_sync(0xffffffffu, first)) {
         const float top = row_max();
-        if (first) {
-          ref = top > ninf ? top - kAbove : 0.0f;
+        if (first && top > ninf) {
+          ref = top - kAbove;
           E = e;
           E_top = e;
           started = true;

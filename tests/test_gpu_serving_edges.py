@@ -156,3 +156,29 @@ def test_rows_that_see_nothing_beside_a_bad_value(D, fp8, bad, q_len, Hq, ws):
         assert bool((out[:q_len - n] == 0).all()) and bool((lse[:q_len - n] == -math.inf).all())
         assert bool(torch.isfinite(lse[q_len - n:]).all())
         assert not bool(torch.isfinite(out[-1, :, 5]).any())
+
+
+@pytest.mark.parametrize("D,fp8", FORMS)
+@pytest.mark.parametrize("q_len,Hq", [(1, 4), (6, 4), (13, 4), (40, 4), (300, 1)])
+@pytest.mark.parametrize("n,low", [(700, 100), (700, 300), (9000, 6000)])
+@pytest.mark.parametrize("value", [-3e38, -math.inf])
+def test_first_keys_as_low_as_their_type_goes(D, fp8, q_len, Hq, n, low, value, ws):
+    """The first `low` keys score -inf in binary32 (weight 0), and all others near -160: nothing
+    may lean on a reference of 0, neither in one CTA nor where parts are joined.  The result is
+    that of the other keys alone."""
+    if fp8 and math.isinf(value):
+        pytest.skip("a row with an infinity has an infinite scale and reads back as NaN")
+    base = rand_bf16(1, 1, D, seed=3).abs() + 0.5
+    base[..., 0] = 0
+    q = base.expand(q_len, Hq, D) + rand_bf16(q_len, Hq, D, seed=4, scale=0.02)
+    q[..., 0] = 12.0
+    k = -base.expand(n, 1, D) + rand_bf16(n, 1, D, seed=5, scale=0.05)
+    k[..., 0] = 0
+    k[:low, 0, 0] = value
+    k, v, q = k.to(torch.bfloat16), rand_bf16(n, 1, D, seed=6), q.to(torch.bfloat16).cuda()
+    scale = 160.0 / float((base.double() ** 2).sum())
+    c, rest = R.Paged([k], [v], 64, fp8), R.Paged([k[low:]], [v[low:]], 64, fp8)
+    want, want_l, tol, tol_l = R.attention(q, rest, [q_len], [n - low], scale=scale, causal=False)
+    for w in (ws, L.new_workspace(L.ATTENTION_CTRL_BYTES)):
+        out, lse = attend(q, c, [q_len], [n], w, scale=scale, causal=False)
+        assert within(out, want, tol) and within(lse, want_l, tol_l)
