@@ -491,7 +491,7 @@ typedef struct {
  * A row whose mask leaves nothing gets out = 0 and lse = -inf.  Scores, softmax
  * statistics and sums are binary32, and out is rounded once to bf16.  Over an FP8 cache the
  * query goes in as an E4M3 and an E5M2 term: elements below 2^-13 of their row's largest are
- * rounded, to 2^-21 of it.  For the
+ * rounded, to 2^-21 of it, and an infinite one makes its row NaN.  For the
  * second product, max_q * q_heads / heads > 64: the weights are rounded to bf16
  * over a BF16 cache and to binary16 over an FP8 one (below 2^-28 of the row's
  * largest they count as 0), whose values are rounded to binary16 with their

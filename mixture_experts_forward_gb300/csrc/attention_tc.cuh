@@ -188,7 +188,8 @@ __device__ __forceinline__ uint16_t cvt_e5m2x2(float lo, float hi) {
 // [2^7, 2^8), as the sums of an E4M3 and an E5M2 term: hi = E4M3(x), lo = E5M2(x - hi).  From
 // 2^-6 on hi leaves at most 8 units of x's last place, which an E5M2 holds exactly, and below
 // it at most 2^-10, rounded by at most 2^-14: exact for elements within 2^-13 of the row's
-// largest, to 2^-21 of it below.  (An E4M3 lo ends at 2^-9 and loses up to 2^-17.)
+// largest, to 2^-21 of it below.  (An E4M3 lo ends at 2^-9 and loses up to 2^-17.)  An
+// infinity, which neither type has, becomes a NaN: x * 0 + x.
 __device__ __forceinline__ void two_terms(const uint32_t (&x)[4], float mul, uint32_t (&hi)[2],
                                           uint32_t (&lo)[2]) {
 #pragma unroll
@@ -196,8 +197,10 @@ __device__ __forceinline__ void two_terms(const uint32_t (&x)[4], float mul, uin
     hi[i] = lo[i] = 0;
 #pragma unroll
     for (int j = 0; j < 2; ++j) {
-      const float x0 = __uint_as_float(x[2 * i + j] << 16) * mul;
-      const float x1 = __uint_as_float(x[2 * i + j] & 0xffff0000u) * mul;
+      float x0 = __uint_as_float(x[2 * i + j] << 16) * mul;
+      float x1 = __uint_as_float(x[2 * i + j] & 0xffff0000u) * mul;
+      x0 = fmaf(x0, 0.0f, x0);
+      x1 = fmaf(x1, 0.0f, x1);
       const uint16_t hc = cvt_e4m3x2(x0, x1);
       const float2 f = e4m3x2_to_f32(hc);
       const uint16_t lc = cvt_e5m2x2(x0 - f.x, x1 - f.y);

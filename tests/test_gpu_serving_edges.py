@@ -182,3 +182,28 @@ def test_first_keys_as_low_as_their_type_goes(D, fp8, q_len, Hq, n, low, value, 
     for w in (ws, L.new_workspace(L.ATTENTION_CTRL_BYTES)):
         out, lse = attend(q, c, [q_len], [n], w, scale=scale, causal=False)
         assert within(out, want, tol) and within(lse, want_l, tol_l)
+
+
+@pytest.mark.parametrize("D,fp8", FORMS)
+@pytest.mark.parametrize("q_len", [1, 9, 150])
+@pytest.mark.parametrize("bad", [math.inf, -math.inf])
+@pytest.mark.parametrize("softcap", [0.0, 20.0])
+def test_an_infinite_query_element(D, fp8, q_len, bad, softcap, ws):
+    """Its scores are infinities of both signs: without a cap the row is NaN.  (Capped, BF16
+    scores of +-c are numbers; over an FP8 cache the row is NaN either way.)  Other rows are not
+    touched, and a row that sees nothing stays 0."""
+    n, at = 300, q_len - 1
+    k, v = rand_bf16(n, 1, D, seed=1), rand_bf16(n, 1, D, seed=2)
+    q = rand_bf16(q_len, 2, D, seed=3)
+    c = R.Paged([k], [v], 16, fp8)
+    want, want_l, tol, tol_l = R.attention(q.cuda(), c, [q_len], [n], softcap=softcap)
+    q[at, 1, 7] = bad
+    out, lse = attend(q.cuda(), c, [q_len], [n], ws, softcap=softcap)
+    others = torch.ones(q_len, 2, dtype=torch.bool)
+    others[at, 1] = False
+    assert within(out[others], want[others], tol[others])
+    assert within(lse[others], want_l[others], tol_l[others])
+    if fp8 or not softcap:
+        assert bool(torch.isnan(out[at, 1]).all()) and bool(torch.isnan(lse[at, 1]))
+    out, lse = attend(q.cuda(), c, [q_len], [0], ws, softcap=softcap)
+    assert bool((out == 0).all()) and bool((lse == -math.inf).all())
