@@ -751,6 +751,7 @@ __global__ void __launch_bounds__(TileShape<D, kFP8>::kThreads, 1)
       };
       bool ok = p.drop_producer == 0;
       int page_next = page_of(1);
+      int ex_top = 0;                  // of the tiles so far
       fetch(0, page_of(0));
       for (int i = 0; i < n && ok; ++i) {
         const int slot = i % S::kScaleSlots;
@@ -759,7 +760,11 @@ __global__ void __launch_bounds__(TileShape<D, kFP8>::kThreads, 1)
         // the tile's largest value scale (scales are not negative: their bits are ordered)
         const uint32_t top = __reduce_max_sync(
             0xffffffffu, __float_as_uint(fmaxf(fmaxf(vs[0], vs[1]), fmaxf(vs[2], vs[3]))));
-        const int ex = min(max(static_cast<int>((top >> 23) & 255u), 6), 253);
+        // (at least 2^-80 of the largest so far, against which such values count as 0 anyway: a
+        // tile of zeros beside large ones must not take the weights, whose unit it is, out of
+        // binary32)
+        const int ex = max(min(max(static_cast<int>((top >> 23) & 255u), 6), 253), ex_top - 80);
+        ex_top = max(ex_top, ex);
         const float mul = __uint_as_float(static_cast<uint32_t>(259 - ex) << 23);   // 2^(5 - e)
         uint32_t g[4];
 #pragma unroll

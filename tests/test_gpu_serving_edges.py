@@ -207,3 +207,23 @@ def test_an_infinite_query_element(D, fp8, q_len, bad, softcap, ws):
         assert bool(torch.isnan(out[at, 1]).all()) and bool(torch.isnan(lse[at, 1]))
     out, lse = attend(q.cuda(), c, [q_len], [0], ws, softcap=softcap)
     assert bool((out == 0).all()) and bool((lse == -math.inf).all())
+
+
+@pytest.mark.parametrize("D,fp8", FORMS)
+@pytest.mark.parametrize("q_len", [1, 9, 40, 150])
+@pytest.mark.parametrize("small", [0.0, 1e-25])
+@pytest.mark.parametrize("tiles", [(0,), (2,), (1, 3), (4,)])
+def test_a_key_tile_of_zero_values_beside_large_ones(D, fp8, q_len, small, tiles, ws):
+    """Values near 1e20, but for whole key tiles of (nearly) zero ones: their weights count in
+    the sum all the same."""
+    n = 128 * 5
+    k, v = rand_bf16(n, 1, D, seed=1), rand_bf16(n, 1, D, seed=2).float() * 1e20
+    for t in tiles:
+        v[128 * t:128 * t + 128] *= small / 1e20
+    q = rand_bf16(q_len, 4, D, seed=3).cuda()
+    c = R.Paged([k], [v.to(torch.bfloat16)], 64, fp8)
+    for causal in (True, False):
+        want, want_l, tol, tol_l = R.attention(q, c, [q_len], [n], causal=causal)
+        for w in (ws, L.new_workspace(L.ATTENTION_CTRL_BYTES)):
+            out, lse = attend(q, c, [q_len], [n], w, causal=causal)
+            assert within(out, want, tol) and within(lse, want_l, tol_l)
