@@ -174,11 +174,25 @@ def new_workspace(nbytes: int, device="cuda") -> torch.Tensor:
     return torch.zeros((nbytes + 255) // 256 * 256, dtype=torch.uint8, device=device)
 
 
+def _new(shape, dtype, device, stream):
+    """An uninitialised result.  With a stream it comes from that stream's memory: a block of the
+    current stream's may have been freed while work queued there still reads it.  It is usually
+    read on the current stream later, so its release waits for that one too."""
+    if stream is None:
+        return torch.empty(shape, dtype=dtype, device=device)
+    with torch.cuda.stream(stream):
+        t = torch.empty(shape, dtype=dtype, device=device)
+    current = torch.cuda.current_stream(t.device)
+    if current.cuda_stream != stream.cuda_stream:
+        t.record_stream(current)
+    return t
+
+
 # ------------------------------------------------------------------ steps
 def route(logits: torch.Tensor, k: int, softcap: float = 0.0, renorm: int = 1, stream=None):
     M, E = logits.shape
-    ids = torch.empty(M, k, dtype=torch.int32, device=logits.device)
-    w = torch.empty(M, k, dtype=torch.float32, device=logits.device)
+    ids = _new((M, k), torch.int32, logits.device, stream)
+    w = _new((M, k), torch.float32, logits.device, stream)
     _check(lib().moe_route(_ptr(logits), M, E, k, float(softcap), int(renorm), _ptr(ids), _ptr(w),
                            _stream(stream)), "moe_route")
     return ids, w
@@ -187,12 +201,9 @@ def route(logits: torch.Tensor, k: int, softcap: float = 0.0, renorm: int = 1, s
 def layout(ids: torch.Tensor, E: int, block_m: int, ws: torch.Tensor, stream=None):
     M, k = ids.shape
     R = M * k
-    dev = ids.device
-    out = dict(counts=torch.empty(E, dtype=torch.int32, device=dev),
-               offsets=torch.empty(E + 1, dtype=torch.int32, device=dev),
-               sorted_route_ids=torch.empty(R, dtype=torch.int32, device=dev),
-               route_slot=torch.empty(R, dtype=torch.int32, device=dev),
-               tile_offsets=torch.empty(E + 1, dtype=torch.int32, device=dev))
+    out = {name: _new((n,), torch.int32, ids.device, stream) for name, n in (
+        ("counts", E), ("offsets", E + 1), ("sorted_route_ids", R), ("route_slot", R),
+        ("tile_offsets", E + 1))}
     _check(lib().moe_layout(_ptr(ids), M, E, k, block_m, _ptr(out["counts"]), _ptr(out["offsets"]),
                             _ptr(out["sorted_route_ids"]), _ptr(out["route_slot"]),
                             _ptr(out["tile_offsets"]), _ptr(ws), _stream(stream)), "moe_layout")
@@ -202,8 +213,8 @@ def layout(ids: torch.Tensor, E: int, block_m: int, ws: torch.Tensor, stream=Non
 def quant_gather(x: torch.Tensor, k: int, route_slot: torch.Tensor, zero_acc=None, stream=None):
     M, K = x.shape
     R = M * k
-    a_q = torch.empty(R, K, dtype=torch.uint8, device=x.device)
-    a_s = torch.empty(K // 128, R, dtype=torch.float32, device=x.device)
+    a_q = _new((R, K), torch.uint8, x.device, stream)
+    a_s = _new((K // 128, R), torch.float32, x.device, stream)
     zc = 0 if zero_acc is None else zero_acc.shape[1]
     _check(lib().moe_quant_gather(_ptr(x), M, K, k, _ptr(route_slot), _ptr(a_q), _ptr(a_s),
                                   _ptr(zero_acc), zc, _stream(stream)), "moe_quant_gather")
@@ -264,7 +275,7 @@ def scatter(rows: torch.Tensor, route_slot: torch.Tensor, weights: torch.Tensor,
     MOE_ERR_DEVICE_FAULT in ws's status word (get_error)."""
     M, k = weights.shape
     N = rows.shape[1]
-    out = torch.empty(M, N, dtype=torch.bfloat16, device=rows.device)
+    out = _new((M, N), torch.bfloat16, rows.device, stream)
     _check(lib().moe_scatter(_ptr(rows), _ptr(route_slot), _ptr(weights), M, N, k, _ptr(out),
                              _ptr(ws), _stream(stream)), "moe_scatter")
     return out
@@ -275,8 +286,8 @@ def swiglu_quant(gu: torch.Tensor, stream=None):
     (h_q u8 [R, I], h_scales f32 [I/128, R])."""
     R, I2 = gu.shape
     I = I2 // 2
-    h_q = torch.empty(R, I, dtype=torch.uint8, device=gu.device)
-    h_s = torch.empty(I // 128, R, dtype=torch.float32, device=gu.device)
+    h_q = _new((R, I), torch.uint8, gu.device, stream)
+    h_s = _new((I // 128, R), torch.float32, gu.device, stream)
     _check(lib().moe_swiglu_quant(_ptr(gu), R, I, _ptr(h_q), _ptr(h_s), _stream(stream)),
            "moe_swiglu_quant")
     return h_q, h_s
@@ -339,13 +350,6 @@ def _ints(t, n) -> bool:
     return t.dtype is _I32 and t.numel() == n and t.is_contiguous()
 
 
-def _keep(stream, *tensors):
-    """Results allocated on the current stream and written on another one."""
-    for t in tensors:
-        if t is not None:
-            t.record_stream(stream)
-
-
 def kv_write(k: torch.Tensor, v: torch.Tensor, slots: torch.Tensor, k_cache: torch.Tensor,
              v_cache: torch.Tensor, ws: torch.Tensor, k_scales=None, v_scales=None, stream=None):
     """moe_kv_write: k, v bf16 [T, heads, head_dim] (strided views allowed, the
@@ -378,15 +382,13 @@ def kv_read(k_cache: torch.Tensor, v_cache: torch.Tensor, block_table: torch.Ten
     if not (starts is None or _ints(starts, B)):
         _bad(what, "starts is int32 [B]")
     shape = (rows, c.heads, c.head_dim)
-    k = torch.empty(shape, dtype=_BF16, device=k_cache.device)
-    v = torch.empty(shape, dtype=_BF16, device=k_cache.device)
+    k = _new(shape, _BF16, k_cache.device, stream)
+    v = _new(shape, _BF16, k_cache.device, stream)
     code = lib().moe_kv_read(c, block_table.data_ptr(), entries, cu_rows.data_ptr(),
                              None if starts is None else starts.data_ptr(), B, rows, k.data_ptr(),
                              v.data_ptr(), ws.data_ptr(), _raw_stream(stream, k_cache))
     if code:
         _check(code, what)
-    if stream is not None:
-        _keep(stream, k, v)
     return k, v
 
 
@@ -407,12 +409,10 @@ def paged_attention(q: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.Tenso
         _bad(what, "q is bf16 [T, q_heads, head_dim] with contiguous rows")
     if not (_ints(block_table, B * entries) and _ints(cu_q, B + 1) and _ints(kv_lens, B)):
         _bad(what, "block_table is int32 [B, entries], cu_q int32 [B+1], kv_lens int32 [B]")
-    sums = torch.empty((T, Hq), dtype=_F32, device=q.device) if lse else None
+    sums = _new((T, Hq), _F32, q.device, stream) if lse else None
     if out is None:
-        out = torch.empty((T, Hq, D), dtype=_BF16, device=q.device)
+        out = _new((T, Hq, D), _BF16, q.device, stream)
         ot, oh = Hq * D, D
-        if stream is not None:
-            _keep(stream, out)
     else:
         ot, oh, od = out.stride()
         if not (out.dtype is _BF16 and out.shape == q.shape and od == 1):
@@ -424,8 +424,6 @@ def paged_attention(q: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.Tenso
     code = lib().moe_paged_attention(a, ws.data_ptr(), ws.numel(), _raw_stream(stream, q))
     if code:
         _check(code, what)
-    if stream is not None:
-        _keep(stream, sums)
     return out, sums
 
 
@@ -447,8 +445,8 @@ def verify_draft(p: torch.Tensor, q: torch.Tensor, draft: torch.Tensor, u_accept
         _bad(what, "draft is int32 [B, n], u_accept f32 [B, n], u_sample f32 [B]")
     if not (draft_lens is None or _ints(draft_lens, B)):
         _bad(what, "draft_lens is int32 [B]")
-    accepted = torch.empty(B, dtype=_I32, device=p.device)
-    tokens = torch.empty((B, n + 1), dtype=_I32, device=p.device)
+    accepted = _new((B,), _I32, p.device, stream)
+    tokens = _new((B, n + 1), _I32, p.device, stream)
     a = VerifyArgs(DTYPE_F32 if f32 else DTYPE_BF16, B, n, V, p.data_ptr(), pb, pi, q.data_ptr(),
                    qb, qi, draft.data_ptr(), None if draft_lens is None else draft_lens.data_ptr(),
                    u_accept.data_ptr(), u_sample.data_ptr(), accepted.data_ptr(),
@@ -456,8 +454,6 @@ def verify_draft(p: torch.Tensor, q: torch.Tensor, draft: torch.Tensor, u_accept
     code = lib().moe_verify_draft(a, ws.data_ptr(), _raw_stream(stream, p))
     if code:
         _check(code, what)
-    if stream is not None:
-        _keep(stream, accepted, tokens)
     return accepted, tokens
 
 
