@@ -498,7 +498,7 @@ typedef struct {
  * scale; up to 64: the weights are the sum of two bf16
  * or two E4M3 terms and the values are taken as cached.  One sequence's new
  * tokens may be any number from 0 (chunks of a prompt, drafted runs, single
- * tokens).  Pages that lie before every window of a sequence are not read.  What lies past kv_lens in a page is never used;
+ * tokens).  T, B or max_q = 0: nothing is launched, and out is left as it was.  Pages that lie before every window of a sequence are not read.  What lies past kv_lens in a page is never used;
  * a NaN or infinity in a value row reaches every row of a tile that has a row
  * seeing it.  Lengths out of range record MOE_ERR_DEVICE_FAULT. */
 moe_status_t moe_paged_attention(const moe_attention_args* args, void* ws, size_t ws_bytes,

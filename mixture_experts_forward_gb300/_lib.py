@@ -409,6 +409,8 @@ def paged_attention(q: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.Tenso
         _bad(what, "q is bf16 [T, q_heads, head_dim] with contiguous rows")
     if not (_ints(block_table, B * entries) and _ints(cu_q, B + 1) and _ints(kv_lens, B)):
         _bad(what, "block_table is int32 [B, entries], cu_q int32 [B+1], kv_lens int32 [B]")
+    if T > 0 and (B == 0 or max_q <= 0):
+        _bad(what, "rows of q, but no sequence or max_q = 0: nothing would write out")
     sums = _new((T, Hq), _F32, q.device, stream) if lse else None
     if out is None:
         out = _new((T, Hq, D), _BF16, q.device, stream)

@@ -227,3 +227,12 @@ def test_a_key_tile_of_zero_values_beside_large_ones(D, fp8, q_len, small, tiles
         for w in (ws, L.new_workspace(L.ATTENTION_CTRL_BYTES)):
             out, lse = attend(q, c, [q_len], [n], w, causal=causal)
             assert within(out, want, tol) and within(lse, want_l, tol_l)
+
+
+@pytest.mark.parametrize("B", [0, 2])
+def test_a_call_without_rows(B, ws):
+    c = R.Paged([rand_bf16(20, 1, 64)] * 2, [rand_bf16(20, 1, 64)] * 2, 16, True)
+    out, lse = L.paged_attention(torch.zeros(0, 4, 64, dtype=torch.bfloat16, device="cuda"), c.k, c.v,
+                                 c.table[:B], cu([0] * B), i32([20] * B), ws, max_q=0,
+                                 k_scales=c.ks, v_scales=c.vs, lse=True)
+    assert out.shape == (0, 4, 64) and lse.shape == (0, 4) and L.get_error(ws) == L.MOE_OK
