@@ -350,6 +350,19 @@ def _ints(t, n) -> bool:
     return t.dtype is _I32 and t.numel() == n and t.is_contiguous()
 
 
+def _placed(what: str, cache, ws, *tensors):
+    """Every tensor on the cache's GPU (a host address faults the kernel), and a workspace with
+    room for the control block."""
+    dev = cache.get_device()
+    if dev < 0 or ws.get_device() != dev:
+        _bad(what, "all tensors must be on one GPU")
+    for t in tensors:
+        if t is not None and t.get_device() != dev:
+            _bad(what, "all tensors must be on one GPU")
+    if ws.numel() * ws.element_size() < CTRL_BYTES:
+        raise MoeError(MOE_ERR_WORKSPACE, what)
+
+
 def kv_write(k: torch.Tensor, v: torch.Tensor, slots: torch.Tensor, k_cache: torch.Tensor,
              v_cache: torch.Tensor, ws: torch.Tensor, k_scales=None, v_scales=None, stream=None):
     """moe_kv_write: k, v bf16 [T, heads, head_dim] (strided views allowed, the
@@ -364,6 +377,7 @@ def kv_write(k: torch.Tensor, v: torch.Tensor, slots: torch.Tensor, k_cache: tor
         _bad(what, "k and v are bf16 [T, heads, head_dim] with contiguous rows")
     if not _ints(slots, T):
         _bad(what, "slots is int32 [T]")
+    _placed(what, k_cache, ws, v_cache, k_scales, v_scales, k, v, slots)
     code = lib().moe_kv_write(c, k.data_ptr(), v.data_ptr(), T, kt, kh, vt, vh, slots.data_ptr(),
                               ws.data_ptr(), _raw_stream(stream, k))
     if code:
@@ -381,6 +395,7 @@ def kv_read(k_cache: torch.Tensor, v_cache: torch.Tensor, block_table: torch.Ten
         _bad(what, "block_table is int32 [B, entries], cu_rows int32 [B+1]")
     if not (starts is None or _ints(starts, B)):
         _bad(what, "starts is int32 [B]")
+    _placed(what, k_cache, ws, v_cache, k_scales, v_scales, block_table, cu_rows, starts)
     shape = (rows, c.heads, c.head_dim)
     k = _new(shape, _BF16, k_cache.device, stream)
     v = _new(shape, _BF16, k_cache.device, stream)
@@ -411,14 +426,15 @@ def paged_attention(q: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.Tenso
         _bad(what, "block_table is int32 [B, entries], cu_q int32 [B+1], kv_lens int32 [B]")
     if T > 0 and (B == 0 or max_q <= 0):
         _bad(what, "rows of q, but no sequence or max_q = 0: nothing would write out")
+    if out is not None and not (out.dtype is _BF16 and out.shape == q.shape and out.stride(2) == 1):
+        _bad(what, "out is bf16, shaped like q, with contiguous rows")
+    _placed(what, k_cache, ws, v_cache, k_scales, v_scales, q, block_table, cu_q, kv_lens, out)
     sums = _new((T, Hq), _F32, q.device, stream) if lse else None
     if out is None:
         out = _new((T, Hq, D), _BF16, q.device, stream)
         ot, oh = Hq * D, D
     else:
-        ot, oh, od = out.stride()
-        if not (out.dtype is _BF16 and out.shape == q.shape and od == 1):
-            _bad(what, "out is bf16, shaped like q, with contiguous rows")
+        ot, oh, _ = out.stride()
     a = AttentionArgs(c, B, T, Hq, max_q, max_kv, entries, q.data_ptr(), qt, qh, out.data_ptr(),
                       ot, oh, sums.data_ptr() if lse else None, cu_q.data_ptr(),
                       kv_lens.data_ptr(), block_table.data_ptr(), scale, softcap, window,
@@ -447,6 +463,7 @@ def verify_draft(p: torch.Tensor, q: torch.Tensor, draft: torch.Tensor, u_accept
         _bad(what, "draft is int32 [B, n], u_accept f32 [B, n], u_sample f32 [B]")
     if not (draft_lens is None or _ints(draft_lens, B)):
         _bad(what, "draft_lens is int32 [B]")
+    _placed(what, p, ws, q, draft, draft_lens, u_accept, u_sample)
     accepted = _new((B,), _I32, p.device, stream)
     tokens = _new((B, n + 1), _I32, p.device, stream)
     a = VerifyArgs(DTYPE_F32 if f32 else DTYPE_BF16, B, n, V, p.data_ptr(), pb, pi, q.data_ptr(),

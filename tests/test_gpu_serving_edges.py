@@ -236,3 +236,22 @@ def test_a_call_without_rows(B, ws):
                                  c.table[:B], cu([0] * B), i32([20] * B), ws, max_q=0,
                                  k_scales=c.ks, v_scales=c.vs, lse=True)
     assert out.shape == (0, 4, 64) and lse.shape == (0, 4) and L.get_error(ws) == L.MOE_OK
+
+
+@pytest.mark.parametrize("name", ["write", "read", "attention", "verify"])
+def test_each_tensor_must_be_on_the_gpu(name):
+    """One tensor at a time left in host memory, and a workspace without room for its status."""
+    from test_serving_binding import all_calls
+    call, host = all_calls()[name]
+    on = {k: v.cuda() if isinstance(v, torch.Tensor) else v for k, v in host.items()}
+    if name == "verify":
+        on["q"] = on["p"][:, :3]
+    call(**on)
+    assert L.get_error(on["ws"]) in (L.MOE_OK, L.MOE_ERR_DEVICE_FAULT)   # (lengths of 0: no rows)
+    for key, v in host.items():
+        if isinstance(v, torch.Tensor):
+            with pytest.raises(L.MoeError, match="on one GPU"):
+                call(**dict(on, **{key: v}))
+    with pytest.raises(L.MoeError) as e:
+        call(**dict(on, ws=torch.zeros(128, dtype=torch.uint8, device="cuda")))
+    assert e.value.code == L.MOE_ERR_WORKSPACE
