@@ -466,7 +466,7 @@ typedef struct {
   float* lse;                 /* f32 [T, q_heads], or NULL */
   const int32_t* cu_q;        /* [B+1] first row of each sequence's new tokens; cu_q[B] = T */
   const int32_t* kv_lens;     /* [B] cached positions of each sequence, its new tokens included */
-  const int32_t* block_table; /* [B, table_stride] page ids */
+  const int32_t* block_table; /* [B, table_stride] page ids (NULL where table_stride = 0) */
   float scale;                /* of the scores; 0 = 1/sqrt(head_dim) */
   float softcap;              /* c > 0: scores become c * tanh(score / c); 0 = off */
   int window;                 /* w > 0: a token sees its last w positions, itself included

@@ -350,6 +350,20 @@ def _ints(t, n) -> bool:
     return t.dtype is _I32 and t.numel() == n and t.is_contiguous()
 
 
+def _table(what: str, t):
+    """(B, table_stride) of a block table: int32 [B, entries], or the columns of a wider one (its
+    rows are then as long as the wider table's, all within its storage)."""
+    B, entries = t.shape
+    if t.dtype is _I32:
+        if t.is_contiguous():
+            return B, entries
+        row, one = t.stride()
+        if (row >= entries and (one == 1 or entries == 1) and
+                (t.storage_offset() + B * row) * 4 <= t.untyped_storage().nbytes()):
+            return B, row
+    _bad(what, "block_table is int32 [B, entries] with contiguous rows")
+
+
 def _placed(what: str, cache, ws, *tensors):
     """Every tensor on the cache's GPU (a host address faults the kernel), and a workspace with
     room for the control block."""
@@ -372,6 +386,10 @@ def kv_write(k: torch.Tensor, v: torch.Tensor, slots: torch.Tensor, k_cache: tor
     T, H, D = k.shape
     kt, kh, kd = k.stride()
     vt, vh, vd = v.stride()
+    if T == 1:                       # (a dimension of one has any stride)
+        kt = vt = 0
+    if H == 1:
+        kh = vh = 0
     if not (H == c.heads and D == c.head_dim and v.shape == k.shape and k.dtype is _BF16 and
             v.dtype is _BF16 and kd == 1 and vd == 1):
         _bad(what, "k and v are bf16 [T, heads, head_dim] with contiguous rows")
@@ -390,9 +408,9 @@ def kv_read(k_cache: torch.Tensor, v_cache: torch.Tensor, block_table: torch.Ten
     """moe_kv_read: (k, v) bf16 [rows, heads, head_dim]; rows = cu_rows[-1]."""
     what = "moe_kv_read"
     c = _cache(what, k_cache, v_cache, k_scales, v_scales)
-    B, entries = block_table.shape
-    if not (_ints(block_table, B * entries) and _ints(cu_rows, B + 1)):
-        _bad(what, "block_table is int32 [B, entries], cu_rows int32 [B+1]")
+    B, entries = _table(what, block_table)
+    if not _ints(cu_rows, B + 1):
+        _bad(what, "cu_rows is int32 [B+1]")
     if not (starts is None or _ints(starts, B)):
         _bad(what, "starts is int32 [B]")
     _placed(what, k_cache, ws, v_cache, k_scales, v_scales, block_table, cu_rows, starts)
@@ -419,11 +437,11 @@ def paged_attention(q: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.Tenso
     c = _cache(what, k_cache, v_cache, k_scales, v_scales)
     T, Hq, D = q.shape
     qt, qh, qd = q.stride()
-    B, entries = block_table.shape
+    B, entries = _table(what, block_table)
     if not (q.dtype is _BF16 and D == c.head_dim and qd == 1):
         _bad(what, "q is bf16 [T, q_heads, head_dim] with contiguous rows")
-    if not (_ints(block_table, B * entries) and _ints(cu_q, B + 1) and _ints(kv_lens, B)):
-        _bad(what, "block_table is int32 [B, entries], cu_q int32 [B+1], kv_lens int32 [B]")
+    if not (_ints(cu_q, B + 1) and _ints(kv_lens, B)):
+        _bad(what, "cu_q is int32 [B+1], kv_lens int32 [B]")
     if T > 0 and (B == 0 or max_q <= 0):
         _bad(what, "rows of q, but no sequence or max_q = 0: nothing would write out")
     if out is not None and not (out.dtype is _BF16 and out.shape == q.shape and out.stride(2) == 1):
@@ -435,6 +453,10 @@ def paged_attention(q: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.Tenso
         ot, oh = Hq * D, D
     else:
         ot, oh, _ = out.stride()
+    if T == 1:
+        qt = ot = 0
+    if Hq == 1:
+        qh = oh = 0
     a = AttentionArgs(c, B, T, Hq, max_q, max_kv, entries, q.data_ptr(), qt, qh, out.data_ptr(),
                       ot, oh, sums.data_ptr() if lse else None, cu_q.data_ptr(),
                       kv_lens.data_ptr(), block_table.data_ptr(), scale, softcap, window,

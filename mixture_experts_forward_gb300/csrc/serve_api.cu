@@ -83,8 +83,8 @@ moe_status_t moe_kv_read(const moe_kv_cache* cache, const int32_t* block_table, 
   if (s != MOE_OK) return s;
   if (B < 0 || rows < 0 || table_stride < 0) return MOE_ERR_INVALID_ARG;
   if (rows == 0) return MOE_OK;
-  if (B == 0 || block_table == nullptr || cu_rows == nullptr || k_out == nullptr ||
-      v_out == nullptr)
+  if (B == 0 || (block_table == nullptr && table_stride > 0) || cu_rows == nullptr ||
+      k_out == nullptr || v_out == nullptr)
     return MOE_ERR_INVALID_ARG;
   if (!aligned16(k_out) || !aligned16(v_out)) return MOE_ERR_INVALID_ARG;
   if (c.heads > 0x7fffffff / (16 * 16)) return MOE_ERR_UNSUPPORTED;
@@ -112,7 +112,7 @@ moe_status_t moe_paged_attention(const moe_attention_args* a, void* ws, size_t w
     return MOE_ERR_INVALID_ARG;
   if (a->T == 0 || a->B == 0 || a->max_q == 0) return MOE_OK;
   if (a->q == nullptr || a->out == nullptr || a->cu_q == nullptr || a->kv_lens == nullptr ||
-      a->block_table == nullptr)
+      (a->block_table == nullptr && a->table_stride > 0))
     return MOE_ERR_INVALID_ARG;
   if (!aligned16(a->q) || !aligned16(a->out) || !aligned4(a->lse)) return MOE_ERR_INVALID_ARG;
   if (!stride8(a->q_stride_t) || !stride8(a->q_stride_h) || !stride8(a->out_stride_t) ||

@@ -255,3 +255,70 @@ def test_each_tensor_must_be_on_the_gpu(name):
     with pytest.raises(L.MoeError) as e:
         call(**dict(on, ws=torch.zeros(128, dtype=torch.uint8, device="cuda")))
     assert e.value.code == L.MOE_ERR_WORKSPACE
+
+
+@pytest.mark.parametrize("fp8", [True, False])
+def test_dimensions_of_one_have_any_stride(fp8, ws):
+    """One token, or one head: views whose stride there is no multiple of 8."""
+    D, n = 64, 40
+    k, v = rand_bf16(n, 1, D, seed=1), rand_bf16(n, 1, D, seed=2)
+    c = R.Paged([k], [v], 16, fp8)
+    q = rand_bf16(1, 4, D, seed=3).cuda()
+    want, want_l = attend(q, c, [1], [n], ws)
+
+    def odd(x, dim):                                    # the same values, a stride of 12 at dim
+        shape, stride = list(x.shape), list(x.stride())
+        stride[dim] = 12
+        return x.as_strided(shape, stride)
+    out, lse = attend(odd(q, 0), c, [1], [n], ws, out=odd(torch.empty_like(q), 0))
+    assert torch.equal(out, want) and torch.equal(lse, want_l)
+    one = q[:, :1].contiguous()
+    out, lse = attend(odd(one, 1), c, [1], [n], ws, out=odd(torch.empty_like(one), 1))
+    assert torch.equal(out, want[:, :1]) and torch.equal(lse, want_l[:, :1])
+    for T, dim in ((1, 0), (5, 1)):
+        new = rand_bf16(T, 1, D, seed=4).cuda()
+        slots = torch.arange(T, dtype=torch.int32, device="cuda")
+        pages = [L.new_kv_cache(L.DTYPE_FP8 if fp8 else L.DTYPE_BF16, 1, 16, 1, D) for _ in range(2)]
+        for x, (kc, vc, ks, vs) in zip((new, odd(new, dim)), pages):
+            L.kv_write(x, x, slots, kc, vc, ws, k_scales=ks, v_scales=vs)
+        assert all(torch.equal(a, b) for a, b in zip(*pages) if a is not None)
+
+
+@pytest.mark.parametrize("fp8", [True, False])
+@pytest.mark.parametrize("q_lens", [[1, 3], [1, 90]])
+def test_block_tables_that_are_columns_of_a_wider_one(fp8, q_lens, ws):
+    kv, D = [300, 211], 64
+    c = R.Paged([rand_bf16(n, 1, D, seed=n) for n in kv], [rand_bf16(n, 1, D, seed=n + 1) for n in kv],
+                16, fp8)
+    q = rand_bf16(sum(q_lens), 4, D, seed=3).cuda()
+    want = attend(q, c, q_lens, kv, ws)
+    rows = L.kv_read(c.k, c.v, c.table, cu(kv), sum(kv), ws, k_scales=c.ks, v_scales=c.vs)
+    w = c.table.shape[1]
+    wide = torch.full((3, w + 9), -1, dtype=torch.int32, device="cuda")
+    wide[:2, :w] = c.table
+    c.table = wide[:2, :w]
+    got = attend(q, c, q_lens, kv, ws)
+    assert torch.equal(got[0], want[0]) and torch.equal(got[1], want[1])
+    back = L.kv_read(c.k, c.v, c.table, cu(kv), sum(kv), ws, k_scales=c.ks, v_scales=c.vs)
+    assert torch.equal(back[0], rows[0]) and torch.equal(back[1], rows[1])
+    # rows that would run past the storage, that overlap, or that are not contiguous
+    for bad in (wide[1:, 1:w + 1], c.table[:1].expand(2, w), wide[:2, :2 * (w // 2):2]):
+        with pytest.raises(L.MoeError):
+            L.paged_attention(q, c.k, c.v, bad, cu(q_lens), i32(kv), ws, max_q=max(q_lens),
+                              k_scales=c.ks, v_scales=c.vs)
+
+
+@pytest.mark.parametrize("q_lens", [[1, 2], [90, 1]])
+@pytest.mark.parametrize("D,fp8", FORMS)
+def test_a_block_table_without_entries(D, fp8, q_lens, ws):
+    """Sequences with no cached position at all (states that are still empty)."""
+    c = R.Paged([rand_bf16(20, 1, D)], [rand_bf16(20, 1, D)], 16, fp8)
+    q = rand_bf16(sum(q_lens), 4, D, seed=3).cuda()
+    c.table = torch.empty(2, 0, dtype=torch.int32, device="cuda")
+    out, lse = attend(q, c, q_lens, [0, 0], ws, causal=False)
+    assert bool((out == 0).all()) and bool((lse == -math.inf).all())
+    L.paged_attention(q, c.k, c.v, c.table, cu(q_lens), i32([0, 1]), ws, max_q=max(q_lens),
+                      k_scales=c.ks, v_scales=c.vs)
+    assert L.get_error(ws) == L.MOE_ERR_DEVICE_FAULT
+    k, _ = L.kv_read(c.k, c.v, c.table, cu([0, 2]), 2, ws, k_scales=c.ks, v_scales=c.vs)
+    assert L.get_error(ws) == L.MOE_ERR_DEVICE_FAULT and bool((k == 0).all())
