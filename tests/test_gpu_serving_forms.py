@@ -88,3 +88,19 @@ def test_a_stalled_pipeline_of_the_64_row_form(D, fp8, q_len, G, workspaces):
             L.debug_set_pipeline_fault(False)
         again = attend(q, c, [q_len], [n], ws)
         assert torch.equal(good[0], again[0]) and torch.equal(good[1], again[1])
+
+
+@pytest.mark.parametrize("D,fp8", FORMS)
+@pytest.mark.parametrize("q_lens,kv_lens", [([700, 1], [700, 9000]), ([1, 1, 1, 600, 5], [5000, 77, 8000, 900, 4000]),
+                                            ([300, 1, 0, 130], [8192, 8192, 100, 130])])
+def test_chunks_and_single_tokens_in_one_call(D, fp8, q_lens, kv_lens, workspaces):
+    """Single tokens over long caches beside a chunk: all are taken in the chunk's form."""
+    for kw in (dict(), dict(window=1000), dict(max_kv=max(kv_lens))):
+        hint = kw.pop("max_kv", 0)
+        c = R.Paged([rand_bf16(n, 2, D, seed=n) for n in kv_lens],
+                    [rand_bf16(n, 2, D, seed=n + 1) for n in kv_lens], 64, fp8)
+        q = rand_bf16(sum(q_lens), 8, D, seed=7).cuda()
+        want, want_l, tol, tol_l = F.attention(q, c, q_lens, kv_lens, **kw)
+        for ws in workspaces:
+            out, lse = attend(q, c, q_lens, kv_lens, ws, max_kv=hint, **kw)
+            assert within(out, want, tol) and within(lse, want_l, tol_l)
