@@ -115,10 +115,8 @@ __device__ __forceinline__ void umma_ss(uint32_t d, uint32_t a_lo, uint32_t a_hi
 
 template <int kCols>
 __device__ __forceinline__ void tmem_ld_cols(uint32_t at, float* v) {
-  if constexpr (kCols == 32) {
-    tmem_ld32(at, v);
-    tmem_ld_wait32(v);
-  } else if constexpr (kCols == 16) {
+  static_assert(kCols == 8 || kCols == 16, "the rows of a group");
+  if constexpr (kCols == 16) {
     float(&x)[16] = *reinterpret_cast<float(*)[16]>(v);
     tmem_ld16(at, x);
     tmem_ld_wait(x);
@@ -130,9 +128,8 @@ __device__ __forceinline__ void tmem_ld_cols(uint32_t at, float* v) {
 }
 template <int kCols>
 __device__ __forceinline__ void tmem_st_cols(uint32_t at, const uint32_t* r) {
-  if constexpr (kCols >= 16) {
-#pragma unroll
-    for (int i = 0; i < kCols / 16; ++i) tmem_st16(at + 16 * i, r + 16 * i);
+  if constexpr (kCols == 16) {
+    tmem_st16(at, r);
   } else {
     asm volatile("tcgen05.st.sync.aligned.32x32b.x8.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8};" ::"r"(at),
                  "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]),

@@ -716,7 +716,7 @@ __global__ void __launch_bounds__(TileShape<D, kFP8>::kThreads, 1)
       };
       // in the order that the MMAs take them
       auto keys = [&](int i) { return load(kFP8 ? rk : rv, false, i); };
-      if (n > 0) ok = ok && keys(0);
+      ok = ok && keys(0);
       for (int i = 0; i < n && ok; ++i) {
         ok = load(rv, true, i);
         if (ok && i + 1 < n) ok = keys(i + 1);
