@@ -489,18 +489,23 @@ typedef struct {
  *   s_j = cap(scale * q . k_j),  out = sum_j softmax(s)_j v_j over the positions
  *   j that the mask leaves,  lse = ln sum_j exp s_j.
  * A row whose mask leaves nothing gets out = 0 and lse = -inf.  Scores, softmax
- * statistics and sums are binary32, and out is rounded once to bf16.  Over an FP8 cache the
- * query goes in as an E4M3 and an E5M2 term: elements below 2^-13 of their row's largest are
- * rounded, to 2^-21 of it, and an infinite one makes its row NaN.  For the
- * second product, max_q * q_heads / heads > 64: the weights are rounded to bf16
- * over a BF16 cache and to binary16 over an FP8 one (below 2^-28 of the row's
- * largest they count as 0), whose values are rounded to binary16 with their
- * scale; up to 64: the weights are the sum of two bf16
- * or two E4M3 terms and the values are taken as cached.  One sequence's new
- * tokens may be any number from 0 (chunks of a prompt, drafted runs, single
- * tokens).  T, B or max_q = 0: nothing is launched, and out is left as it was.  Pages that lie before every window of a sequence are not read.  What lies past kv_lens in a page is never used;
- * a NaN or infinity in a value row reaches every row of a tile that has a row
- * seeing it.  Lengths out of range record MOE_ERR_DEVICE_FAULT. */
+ * statistics and sums are binary32, and out is rounded once to bf16.  What is rounded besides:
+ *   scores   a soft cap's tanh has an absolute error of about 2^-22 (so a score 2^-22 * softcap,
+ *            which counts where softcap is far above the scores).  Over an FP8 cache the query
+ *            goes in as an E4M3 and an E5M2 term: elements below 2^-13 of their row's largest are
+ *            rounded, to 2^-21 of it, and an infinite one makes its row NaN.
+ *   few rows (max_q * q_heads / heads up to 64, or 48 over an FP8 cache): the weights are the sum
+ *            of two bf16 terms, or two E4M3 terms (8 to 9 bits; below 2^-14 of the largest weight
+ *            times value scale of the row in a tile of 128 keys they count as 0), and the values
+ *            are taken as cached.
+ *   more     over a BF16 cache the weights are rounded to bf16; over an FP8 one to binary16 (below
+ *            2^-28 of the row's largest they count as 0, below 2^-25 in key tiles whose values
+ *            are smaller), and its values to binary16 with their scale.
+ * One sequence's new tokens may be any number from 0 (chunks of a prompt, drafted runs, single
+ * tokens).  T, B or max_q = 0: nothing is launched, and out is left as it was.  Pages that lie
+ * before every window of a sequence are not read.  What lies past kv_lens in a page is never
+ * used; a NaN or infinity in a value row reaches every row of a tile that has a row seeing it, if
+ * it sees any key at all.  Lengths out of range record MOE_ERR_DEVICE_FAULT. */
 moe_status_t moe_paged_attention(const moe_attention_args* args, void* ws, size_t ws_bytes,
                                  void* stream);
 

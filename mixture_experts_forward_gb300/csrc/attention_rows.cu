@@ -1,8 +1,8 @@
 // Attention of few rows over the paged cache: single tokens (decode) and
 // short drafted runs, up to 64 rows (new tokens x query heads of one cache
-// head).  Every cached byte is read once, by TMA, and meets few rows: decode is bound
-// by HBM (16 rows, 304 tiles of 8192 keys: 6.7 TB/s from BF16, 6.2 from E4M3), 33 to 64
-// rows over E4M3 codes by the softmax warps (conversions of the weights).
+// head), 48 over E4M3 codes.  Every cached byte is read once, by TMA, and meets few rows: decode
+// is bound by HBM (16 rows, 304 tiles of 8192 keys: 6.5 TB/s from BF16, 6.1 from E4M3), 17 to 48
+// rows over E4M3 codes by the softmax warps (conversions of the weights; 3.3 to 4.2 TB/s).
 //
 // The products are turned round, so that a key is a lane and a row a column:
 //   S^T[keys x rows] = K Q^T               (A = the key tile as it lies in the cache)
@@ -25,7 +25,8 @@
 //
 // Groups of four warps share the rows of every key tile (a thread per key, 8 or 16 rows
 // each); then one warp loads and one issues the MMAs.  Scores are double-buffered in
-// tensor memory.  Up to 32 rows two CTAs share an SM.
+// tensor memory.  Up to 32 rows two CTAs share an SM (not BF16 heads of 128 above 16 rows, of
+// whose 32 KB tiles only two would fit beside a second CTA).
 #include <cstring>
 #include <type_traits>
 
@@ -44,7 +45,7 @@ struct RowsShape {
   static constexpr int kChunkRows = kFP8 ? 16 : 8;       // rows in 16 bytes of weights
   static constexpr int kPTerm = N / kChunkRows * kKeys * 16;
   // FP8 is bound by the softmax warps as well as by HBM: two buffers of weights spare them
-  // the wait for the product before (BF16: 98 % of the copy bandwidth with one)
+  // the wait for the product before (BF16: 95 % of the copy bandwidth with one)
   static constexpr int kPBufs = kFP8 ? 2 : 1;
   // offsets in shared memory: weights (hi, lo), query (FP8: hi, lo), the ring
   static constexpr int oP = 0;
@@ -71,7 +72,8 @@ struct RowsShape {
 // that tile's maximum (at most kDown below its highest one, in log2 units: sums stay
 // finite).  What a tile loses is then at most 128 * 2^-14 = 2^-7 of its largest weight.
 // (Drafted runs, 48 rows: 44 us without the check, 46 with it, 51 with kSmall = 4 in every
-// fourth tile.)
+// fourth tile.  The second pass costs where scores are sharp: queries four times as large, 93 us,
+// and decode of 64 sequences to 16384 positions 274 -> 356 us.)
 constexpr float kSmall = 1.0f, kDown = 40.0f;
 
 template <int N, int kGroups>
@@ -943,7 +945,8 @@ cudaError_t launch_d(const AttnParams& p, int tile_rows, const CUtensorMap& mk,
   if (tile_rows == 16) return launch_n<D, kFP8, 16>(p, mk, mv, stream);
   if (tile_rows == 32) return launch_n<D, kFP8, 32>(p, mk, mv, stream);
   if (tile_rows == 48) return launch_n<D, kFP8, 48>(p, mk, mv, stream);
-  return launch_n<D, kFP8, 64>(p, mk, mv, stream);
+  if constexpr (kFP8) return cudaErrorInvalidValue;      // (49 rows and more: 256-row tiles)
+  else return launch_n<D, kFP8, 64>(p, mk, mv, stream);
 }
 
 }  // namespace

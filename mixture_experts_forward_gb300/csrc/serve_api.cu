@@ -156,10 +156,12 @@ moe_status_t moe_paged_attention(const moe_attention_args* a, void* ws, size_t w
   p.drop_producer = loads_dropped() ? 1 : 0;
 
   // Few rows per cache head: one tile of them, keys as the tensor core's rows, bound by HBM.
-  // More: 256-row tiles.  (8192 keys, 38 sequences x 4 heads: 64 rows 94 / 119 us BF16 / FP8
-  // in the first form and 95 / 129 in the second, 96 rows as two tiles 164 / 202 and 96 / 130;
-  // 6 sequences: 64 rows 28 / 31 and 34 / 43, 128 rows 39 / 45 and 45 / 54.)
-  const bool few = rows <= 64;
+  // More: 256-row tiles.  (8192 keys x 4 heads x D 128, us in the first form / in the second.
+  // BF16, 64 rows: 38 sequences 109 / 109, 6 sequences 34 / 38.  FP8, whose small weights the
+  // first form checks: 48 rows 79 / 139 and 29 / 42; 64 rows, where its registers spill, 169 / 140
+  // and 46 / 46.  Scores four times as large, whose weights ask for a second pass in most tiles:
+  // 48 rows FP8 204 / 144 and 48 / 44.)
+  const bool few = rows <= (fp8 ? 48 : 64);
   const int tile_rows = !few ? kTileRows : rows <= 16 ? 16 : rows <= 32 ? 32 : rows <= 48 ? 48 : 64;
   p.row_tiles = static_cast<int>((rows + tile_rows - 1) / tile_rows);
   const long long tiles = static_cast<long long>(a->B) * p.c.heads * p.row_tiles;

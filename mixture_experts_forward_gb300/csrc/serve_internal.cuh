@@ -64,7 +64,8 @@ cudaError_t launch_kv_read(const KvCacheView& c, int head_dim, bool fp8, const i
                            int rows, void* k_out, void* v_out, Ctrl* ctrl, cudaStream_t stream);
 // Parts of a tile (and CTAs that share tiles) at most.
 constexpr int kMaxParts = 320;
-// Up to 16, 32, 48 or 64 rows per tile (tile_rows), tcgen05 with keys and channels as the rows.
+// Up to 16, 32, 48 or (BF16) 64 rows per tile (tile_rows), tcgen05 with keys and channels as the
+// rows.
 int attention_rows_places(int tile_rows, int head_dim, bool fp8);   // CTAs per SM
 cudaError_t launch_attention_rows(const AttnParams& p, int tile_rows, int head_dim, bool fp8,
                                   cudaStream_t stream);

@@ -21,7 +21,8 @@ error, an output is off by at most
              largest weight times value scale of the row in that tile of 128 keys is at least 1, on
              each code.  Many rows, FP8: 2^-25 of the row's largest weight, on each value.
 
-rows <= 64 (new tokens of the longest sequence x query heads per cache head) is the few-row form."""
+The few-row form takes up to 64 rows (new tokens of the longest sequence x query heads per cache
+head), 48 over an FP8 cache."""
 from __future__ import annotations
 
 import math
@@ -42,6 +43,10 @@ def _codes(cache, name, b, n):
     return x, sc[pg, :, pos % cache.page].double()
 
 
+def few_rows(rows, fp8):
+    return rows <= (48 if fp8 else 64)
+
+
 def rounding(few, fp8):
     if few:
         return 2.0 ** -11 + 2.0 ** -8 * (1 + 2.0 ** -7) if fp8 else 2.0 ** -16
@@ -52,7 +57,7 @@ def attention(q, cache, q_lens, kv_lens, *, scale=0.0, softcap=0.0, window=0, ca
     """(out, lse, tol_out, tol_lse) in float64."""
     T, Hq, D = q.shape
     G = Hq // cache.H
-    few = max(q_lens) * G <= 64
+    few = few_rows(max(q_lens) * G, cache.fp8)
     r = rounding(few, cache.fp8)
     scale = scale or 1.0 / math.sqrt(D)
     want, want_l, _, _ = R.attention(q, cache, q_lens, kv_lens, scale=scale, softcap=softcap,
@@ -124,4 +129,4 @@ def same_sign_case(q_len, G, D, fp8, device, n=2001):
     v = (1.0 + 0.75 * torch.rand(1, 1, D, generator=g)).to(torch.bfloat16)
     v[..., 0] = 1.75
     c = R.Paged([k], [v.expand(n, 1, D)], 64, fp8, device=device)
-    return q, c, -math.log(weight(q_len * G <= 64, fp8))
+    return q, c, -math.log(weight(few_rows(q_len * G, fp8), fp8))
