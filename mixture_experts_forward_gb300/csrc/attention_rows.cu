@@ -587,7 +587,9 @@ __global__ void
               hi[j] = hw;
               lo[j] = lw;
             }
-            far = fmaxf(__low2float(most), __high2float(most)) > 448.0f;
+            // (a value scale beyond binary32 in the present unit makes NaN of weights of 0, which
+            // the maximum passes over)
+            far = fmaxf(__low2float(most), __high2float(most)) > 448.0f || vw > 3.0e38f;
           } else {
             float most = 0.0f;
 #pragma unroll

@@ -322,3 +322,25 @@ def test_a_block_table_without_entries(D, fp8, q_lens, ws):
     assert L.get_error(ws) == L.MOE_ERR_DEVICE_FAULT
     k, _ = L.kv_read(c.k, c.v, c.table, cu([0, 2]), 2, ws, k_scales=c.ks, v_scales=c.vs)
     assert L.get_error(ws) == L.MOE_ERR_DEVICE_FAULT and bool((k == 0).all())
+
+
+@pytest.mark.parametrize("D,fp8", FORMS)
+@pytest.mark.parametrize("q_len", [1, 6, 12, 40])
+@pytest.mark.parametrize("zeros", [128, 256, 300])
+@pytest.mark.parametrize("size", [1.0, 4000.0, 1e30])
+def test_first_values_of_zero_and_later_ones_of_no_weight(D, fp8, q_len, zeros, size, ws):
+    """All weight is on the first keys, whose values are 0; the others score 200 lower.  The
+    output is 0 and lse that of the first keys, however large the other values are."""
+    n = 700
+    k = torch.zeros(n, 1, D)
+    k[:zeros, 0, 0] = 200.0 / math.sqrt(D)
+    v = rand_bf16(n, 1, D, seed=2).float() * size
+    v[:zeros] = 0
+    q = torch.zeros(q_len, 4, D, dtype=torch.bfloat16, device="cuda")
+    q[..., 0] = float(D)
+    c = R.Paged([k.to(torch.bfloat16)], [v.to(torch.bfloat16)], 64, fp8)
+    for causal in (True, False):
+        _, want_l, _, tol_l = R.attention(q, c, [q_len], [n], causal=causal)
+        for w in (ws, L.new_workspace(L.ATTENTION_CTRL_BYTES)):
+            out, lse = attend(q, c, [q_len], [n], w, causal=causal)
+            assert bool((out == 0).all()) and within(lse, want_l, tol_l)
