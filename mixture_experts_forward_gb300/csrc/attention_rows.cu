@@ -602,7 +602,7 @@ __global__ void
               hi[j] = *reinterpret_cast<uint32_t*>(&hh);
               lo[j] = *reinterpret_cast<uint32_t*>(&ll);
             }
-            far = most > 1.0e18f;
+            far = most > kFarWeight;
           }
           // one buffer of weights: the last product has read those before (that of the tile
           // before it is complete: it came before these scores)

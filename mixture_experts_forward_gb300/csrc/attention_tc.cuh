@@ -11,6 +11,11 @@
 namespace moe {
 
 constexpr int kKeys = 128;                     // keys per tile
+// A BF16 weight above this (2^40) moves its row's reference: sums of weights times values stay in
+// binary32 for values to 2^70 over 2^17 keys, and scores must rise by 28 to get there.  (2^24:
+// scores of a standard deviation of 12 move it in many tiles, 4096 tokens over 16384 positions 743
+// instead of 655 us; 2^60: values of 2^60 overflow.)
+constexpr float kFarWeight = 1099511627776.0f;
 constexpr uint32_t kHalfBytes = kKeys * 128;   // 64 bf16 channels of 128 rows
 
 // The 16-byte piece c of row r of a tile of codes (rows of D bytes, the

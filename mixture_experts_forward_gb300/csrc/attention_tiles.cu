@@ -267,7 +267,7 @@ __global__ void __launch_bounds__(TileShape<D, kFP8>::kThreads, 1)
     // (binary16 weights: the first keys' largest is 2^3, so a weight is rounded to 2^-28 of it
     // at worst, or to 2^-25 in a tile whose values' unit is up to 2^3 smaller, and what many small
     // ones add up to beside it is kept)
-    constexpr float kFar = kFP8 ? 16384.0f : 1.0e18f, kAbove = kFP8 ? 3.0f : 0.0f;
+    constexpr float kFar = kFP8 ? 16384.0f : kFarWeight, kAbove = kFP8 ? 3.0f : 0.0f;
     float ref = 0.0f, l = 0.0f;
     bool started = false;                            // the row has seen a key
     int E = 0, E_top = 0;                            // FP8: O is in units of 2^E

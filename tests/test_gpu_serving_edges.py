@@ -344,3 +344,25 @@ def test_first_values_of_zero_and_later_ones_of_no_weight(D, fp8, q_len, zeros, 
         for w in (ws, L.new_workspace(L.ATTENTION_CTRL_BYTES)):
             out, lse = attend(q, c, [q_len], [n], w, causal=causal)
             assert bool((out == 0).all()) and within(lse, want_l, tol_l)
+
+
+@pytest.mark.parametrize("D,fp8", FORMS)
+@pytest.mark.parametrize("q_len", [1, 6, 12, 40, 150])
+@pytest.mark.parametrize("rise", [10.0, 20.0, 38.0, 100.0])
+def test_large_values_under_rising_scores(D, fp8, q_len, rise, ws):
+    """Values near 1e23 whose keys score `rise` more after the first tile, and as much again after
+    the second: sums of weights times values stay finite."""
+    n = 128 * 5
+    k, v = rand_bf16(n, 1, D, seed=1).float() * 0.3, rand_bf16(n, 1, D, seed=2).float() * 1e23
+    k[..., 0] = 0
+    k[128:256, 0, 0] = 1.0
+    k[256:, 0, 0] = 2.0
+    q = rand_bf16(q_len, 4, D, seed=3)
+    q[..., 0] = rise * math.sqrt(D)
+    c = R.Paged([k.to(torch.bfloat16)], [v.to(torch.bfloat16)], 64, fp8)
+    q = q.cuda()
+    for causal in (True, False):
+        want, want_l, tol, tol_l = R.attention(q, c, [q_len], [n], causal=causal)
+        for w in (ws, L.new_workspace(L.ATTENTION_CTRL_BYTES)):
+            out, lse = attend(q, c, [q_len], [n], w, causal=causal)
+            assert within(out, want, tol) and within(lse, want_l, tol_l)
