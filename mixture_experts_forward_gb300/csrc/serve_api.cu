@@ -191,7 +191,8 @@ moe_status_t moe_paged_attention(const moe_attention_args* a, void* ws, size_t w
   // are cut into the number of parts that takes the least time by this estimate: about 1.5 us
   // for 128 keys, and 20 us more for a part (its 133 KB written and read again; 2 x 16
   // heads of 8192 rows and keys: 565 us whole, 623 us with the last 112 tiles in 4 parts;
-  // a 4096-row chunk at 16384 keys: 711 us whole, 688 us with its last 56 in 2).
+  // a 4096-row chunk at 16384 keys: 711 us whole, 688 us with its last 56 in 2; all with
+  // BF16 and D = 128.  FP8's tiles take longer and D = 64's parts are half as large: not fitted).
   // Early rows see fewer keys by the new tokens after them, but not those of single tokens or
   // drafted runs beside a long chunk (what the longest sequence leaves to each of the others is
   // then at most a row tile): they see all their keys.  (8192 tokens and one token over 8192

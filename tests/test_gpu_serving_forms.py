@@ -73,7 +73,8 @@ def test_roundings_that_agree(D, fp8, q_len, G, workspaces):
 @pytest.mark.parametrize("D,fp8", FORMS)
 @pytest.mark.parametrize("q_len,G", [(7, 7), (16, 4)])
 def test_a_stalled_pipeline_of_the_64_row_form(D, fp8, q_len, G, workspaces):
-    """No loads are issued: every wait runs out, the status says so, the next call is right."""
+    """No loads are issued: every wait runs out, the status says so, the next call is right.  (Over
+    an FP8 cache these rows go to the 256-row tiles.)"""
     n = 2000
     c = R.Paged([rand_bf16(n, 1, D, seed=1)], [rand_bf16(n, 1, D, seed=2)], 16, fp8)
     q = rand_bf16(q_len, G, D, seed=3).cuda()
