@@ -31,7 +31,7 @@ __device__ __forceinline__ float rcp_approx(float x) {
 }
 
 // c * tanh(x / c), by tanh(t) = 1 - 2 / (e^(2t) + 1): absolute error about
-// 2^-23 * c (k = 2 log2(e) / c; e^(2t) overflows to inf and underflows to 0 at
+// 2^-22 * c (k = 2 log2(e) / c; e^(2t) overflows to inf and underflows to 0 at
 // the right ends).
 __device__ __forceinline__ float soft_capped(float x, float k, float c) {
   const float e = exp2_approx(x * k);
