@@ -538,6 +538,168 @@ typedef struct {
  * MOE_ERR_DEVICE_FAULT.  ws: workspace of at least MOE_CTRL_BYTES. */
 moe_status_t moe_verify_draft(const moe_verify_args* args, void* ws, void* stream);
 
+/* ---------------------------------------------------------------------------
+ * Between the serving operators: the step's pages and slots, rotary positions,
+ * the expert layer for a few tokens, and the logits before the probabilities.
+ * The conventions above hold, `ws` and MOE_ERR_DEVICE_FAULT included.  A workspace
+ * is not to be shared with a call on another stream that may run at the same time. */
+
+/* The pages of a batch's sequences, all in device memory.  Row b of the block table
+ * holds sequence b's pages in its first held[b] entries; the pages that nobody holds are
+ * a stack of free_count[0] ids.  page_size 16 .. 256, a power of two; B at most 8192;
+ * B * table_stride, and the pages times page_size, below 2^31. */
+typedef struct {
+  int B, table_stride, page_size;
+  int free_capacity;          /* entries of free_pages */
+  int32_t* block_table;       /* [B, table_stride] */
+  int32_t* held;              /* [B] */
+  int32_t* free_pages;        /* [free_capacity] */
+  int32_t* free_count;        /* [1] */
+} moe_page_state;
+
+/* Plans one step: sequence b has lens[b] positions cached and brings new_lens[b] tokens, packed
+ * one sequence after another.  It needs max(0, ceil((lens + new) / page_size) - held) pages more
+ * and takes them from the top of the stack, the sequences in their order.  Those that need none
+ * are always served, the others as long as the pages last: the first for which they do not, and
+ * all after it that need some, are not served and take nothing.  Writes
+ *   slots      s32 [rows]  each token's slot for moe_kv_write; -1 for the tokens of a sequence
+ *                          that is not served and for the rows behind the last sequence,
+ *   positions  s32 [rows]  each token's position (0 behind the last sequence),
+ *   cu_q       s32 [B+1]   the first row of each sequence,
+ *   kv_lens    s32 [B]     lens + new, or 0 for a sequence that is not served (its attention
+ *                          is 0),
+ * and block_table, held, free_pages and free_count are brought up to date.
+ * MOE_ERR_DEVICE_FAULT, and the sequence is not served: a negative length, held outside
+ * 0 .. table_stride or less than the cached positions fill, more positions than the table has
+ * room for, rows past `rows` (cu_q stays within it).  Also recorded: a page id outside 0 ..
+ * num_pages - 1 (slot -1), a free_count outside 0 .. free_capacity (clamped). */
+moe_status_t moe_plan_step(const moe_page_state* pages, const int32_t* lens,
+                           const int32_t* new_lens, int rows, int num_pages, int32_t* slots,
+                           int32_t* positions, int32_t* cu_q, int32_t* kv_lens, void* ws,
+                           void* stream);
+
+/* Gives back the pages past the first keep[b] positions of each sequence (0: all of them; a
+ * negative number leaves the sequence as it is).  They go onto the stack with the last page of
+ * the last sequence first, so that the release of what a plan took restores the stack; their
+ * table entries become -1.  A held outside 0 .. table_stride, or a stack without room for all
+ * (then nothing is given back), records MOE_ERR_DEVICE_FAULT. */
+moe_status_t moe_release_pages(const moe_page_state* pages, const int32_t* keep, void* ws,
+                               void* stream);
+
+/* How the frequencies theta_i = base^(-2i/rotary_dim) are scaled for contexts longer than the
+ * trained `original`: kept where keep = 1, divided by `factor` where keep = 0, and
+ * theta * keep + theta / factor * (1 - keep) between. */
+typedef enum {
+  MOE_ROPE_NONE = 0,    /* keep = 1 */
+  MOE_ROPE_LINEAR = 1,  /* keep = 0 */
+  MOE_ROPE_TURNS = 2,   /* keep rises from 0 to 1 with the turns that pair i makes over `original`,
+                           between `low` and `high` turns */
+  MOE_ROPE_INDEX = 3    /* keep falls from 1 to 0 with i, between the (real-valued) indices that
+                           make `high` and `low` turns, rounded down and up and kept within
+                           0 .. rotary_dim - 1 (at least 0.001 apart) */
+} moe_rope_scaling_t;
+
+/* Fills the host array table[rotary_dim / 2] with the turns that each pair makes from one
+ * position to the next, theta_i / 2 pi, as a fraction of 2^64: the angle of position p is then
+ * p * table[i] mod 2^64, exact for every position.  rotary_dim a multiple of 2 up to 512; base > 1 and
+ * factor > 0; TURNS and INDEX: original > 0 and 0 < low < high.  Host only. */
+moe_status_t moe_rotary_table(int rotary_dim, double base, moe_rope_scaling_t scaling,
+                              double factor, double original, double low, double high,
+                              uint64_t* table);
+
+/* Arguments of moe_rotary.  Strides in elements, multiples of 8, so views of a packed projection
+ * can be passed; an output may be its input (same strides) and may not overlap it otherwise. */
+typedef struct {
+  int T;                      /* tokens */
+  int q_heads, kv_heads;      /* either may be 0 (without a cache) */
+  int head_dim;               /* multiple of 16 up to 256; with a cache, the cache's */
+  int rotary_dim;             /* the first elements of a head are rotated: multiple of 16 */
+  int interleaved;            /* 0: element i pairs with i + rotary_dim/2; 1: 2i with 2i + 1 */
+  float amplitude;            /* of the rotated part (1 = a rotation) */
+  const uint64_t* table;      /* [rotary_dim/2], device, 8-byte aligned (moe_rotary_table) */
+  const int32_t* positions;   /* [T], any number */
+  const void* q;              /* bf16 */
+  int64_t q_stride_t, q_stride_h;
+  void* q_out;                /* bf16 */
+  int64_t q_out_stride_t, q_out_stride_h;
+  const void* k;
+  int64_t k_stride_t, k_stride_h;
+  void* k_out;                /* without a cache */
+  int64_t k_out_stride_t, k_out_stride_h;
+  const void* v;              /* with a cache */
+  int64_t v_stride_t, v_stride_h;
+  const int32_t* slots;       /* [T], with a cache: as moe_kv_write's */
+  moe_kv_cache cache;         /* k == NULL: no cache; else heads = kv_heads */
+} moe_rotary_args;
+
+/* Rotary positions: pair i = (a, b) of each head of token t becomes
+ * amplitude * (a cos - b sin, a sin + b cos) at the angle of positions[t]; elements from
+ * rotary_dim on are copied.  In binary32 with one rounding at the end: q_out and k_out to
+ * bf16; with a cache, the rotated keys and the values go to slots[t] as moe_kv_write stores them
+ * (an FP8 cache quantises the binary32 keys).  Without a cache ws is not used (may be NULL).
+ * T = 0 is a no-op. */
+moe_status_t moe_rotary(const moe_rotary_args* args, void* ws, void* stream);
+
+/* The most tokens of one call of moe_forward_few. */
+#define MOE_FEW_TOKENS 16
+
+/* The whole gated expert layer for a few tokens (1 <= M <= MOE_FEW_TOKENS: single tokens, drafted
+ * runs) in two kernels: the arguments and the result of moe_forward's gated FFN (BF16, or
+ * FP8_E4M3 with gated = 1), each active expert's weights read once (above M * K = 65536 once for
+ * every 65536 / K tokens).  K a multiple of 64 (BF16) or 128 (FP8), N of 128, both at most 32768.
+ * Unlike moe_forward's FP8 form it quantises no activations: x enters as it is
+ * (binary16 times a power of two for each 128 elements: exact for those above 2^-31 of their
+ * block's largest, the others to 2^-39 of it), products are summed in binary32, silu(gate) * up
+ * keeps 11 bits (FP8) or 16 (BF16), and the output is rounded once.  block_m, sched, k_splits,
+ * use_graph, gather_rows and cta_pairs are ignored.  Routing is moe_route's, bit for bit.
+ * out: bf16 [M, K].  ws: moe_few_workspace_size() bytes. */
+moe_status_t moe_forward_few(const moe_forward_args* args, void* out, void* ws, size_t ws_bytes,
+                             void* stream);
+
+/* Workspace bytes needed by moe_forward_few (0 if the arguments are invalid). */
+size_t moe_few_workspace_size(const moe_forward_args* args);
+
+/* Arguments of moe_adjust_logits.  Sequence b has m rows of logits: the next token's, and with
+ * drafts the ones after each drafted token (m = n + 1).  Pointers may be NULL where noted. */
+typedef struct {
+  moe_dtype_t dtype;          /* of the logits: F32 or BF16 */
+  int B, m, V;                /* m at most 33; V at most 262144 */
+  const void* logits;         /* [B, m, V], rows contiguous */
+  int64_t logits_stride_b, logits_stride_i;
+  float* out;                 /* [B, m, V], rows contiguous; may be the logits (F32, same strides) */
+  int64_t out_stride_b, out_stride_i;
+  int probabilities;          /* 1: out = softmax of the adjusted logits over the temperature;
+                                 0: the adjusted logits (the temperature is not used) */
+  const int32_t* history;     /* [B, history_stride]: the prompt's tokens, then the outputs; -1 is
+                                 skipped.  NULL: none */
+  int history_stride;
+  const int32_t* history_lens;  /* [B] (NULL: history_stride each) */
+  const int32_t* prompt_lens;   /* [B] how many of them are the prompt's (NULL: none) */
+  const int32_t* draft;       /* [B, m - 1] drafted tokens: row i counts the first i of them as
+                                 outputs too; -1 is skipped.  NULL: none */
+  const float* repetition;    /* [B] > 0 (NULL: 1) */
+  const float* presence;      /* [B] (NULL: 0) */
+  const float* frequency;     /* [B] (NULL: 0) */
+  const float* temperature;   /* [B] >= 0 (NULL: 1); 0: all on the largest, the lowest id of equals */
+  int biases;                 /* entries of each row of bias_tokens, at most 1024 */
+  const int32_t* bias_tokens; /* [B, biases]; -1 is skipped; a token named twice gets both, added in
+                                 their order */
+  const float* bias_values;   /* [B, biases] */
+  const uint32_t* mask;       /* bit v % 32 of word v / 32 set: token v may be chosen.  NULL: all */
+  int64_t mask_stride_b, mask_stride_i;   /* in words; 0 shares a mask */
+} moe_logits_args;
+
+/* Penalties, biases and masks, then probabilities for moe_verify_draft.  For token v with logit l,
+ * c times among the outputs:
+ *   l > 0 ? l / repetition : l * repetition   if v is in the prompt or the outputs,
+ *   l -= frequency * c;  l -= presence if c > 0;  l += bias;  l = -inf if the mask forbids v.
+ * A NaN counts as -inf, and a logit of -inf stays there.  probabilities: p = exp((l - max) /
+ * temperature) / sum in binary32, tokens at -inf get 0, tokens at +inf share all of it; a row that
+ * is left with nothing gets 0 throughout.  Tokens outside [0, V), lengths outside the history, a
+ * repetition that is not > 0 and a temperature that is not >= 0 (taken as 1) record
+ * MOE_ERR_DEVICE_FAULT. */
+moe_status_t moe_adjust_logits(const moe_logits_args* args, void* ws, void* stream);
+
 #ifdef __cplusplus
 }
 #endif

@@ -18,6 +18,8 @@ MOE_ERR_CUDA, MOE_ERR_TIMEOUT, MOE_ERR_DEVICE_FAULT = 4, 5, 6
 DTYPE_FP8, DTYPE_BF16, DTYPE_F32 = 0, 1, 2
 EPI_SCATTER, EPI_STORE, EPI_SWIGLU, EPI_STORE_BF16 = 0, 1, 2, 3
 SCHED_QUEUE, SCHED_STATIC = 0, 1
+ROPE_SCALINGS = {"none": 0, "linear": 1, "turns": 2, "index": 3}   # moe_rope_scaling_t
+FEW_TOKENS = 16                             # MOE_FEW_TOKENS
 CTRL_BYTES = 256
 ATTENTION_CTRL_BYTES = CTRL_BYTES + 65536   # MOE_ATTENTION_CTRL_BYTES
 ATTENTION_WS_BYTES = 64 << 20               # MOE_ATTENTION_WS_BYTES
@@ -27,7 +29,9 @@ EXPORTS = ["moe_status_string", "moe_num_sms", "moe_route", "moe_layout", "moe_q
            "moe_forward_host", "moe_get_error", "moe_debug_set_pipeline_fault", "moe_forward_plan",
            "moe_last_cuda_error", "moe_grouped_gemm_noalloc", "moe_swiglu_quant",
            "moe_forward_workspace_map", "moe_gemm_cta_pairs", "moe_kv_write", "moe_kv_read",
-           "moe_paged_attention", "moe_verify_draft"]
+           "moe_paged_attention", "moe_verify_draft", "moe_plan_step", "moe_release_pages",
+           "moe_rotary_table", "moe_rotary", "moe_forward_few", "moe_few_workspace_size",
+           "moe_adjust_logits"]
 WS_NONE = (1 << 64) - 1   # MOE_WS_NONE
 
 
@@ -101,6 +105,44 @@ class VerifyArgs(ctypes.Structure):
                 ("accepted", ctypes.c_void_p), ("tokens", ctypes.c_void_p)]
 
 
+class PageState(ctypes.Structure):
+    _fields_ = [("B", ctypes.c_int), ("table_stride", ctypes.c_int), ("page_size", ctypes.c_int),
+                ("free_capacity", ctypes.c_int), ("block_table", ctypes.c_void_p),
+                ("held", ctypes.c_void_p), ("free_pages", ctypes.c_void_p),
+                ("free_count", ctypes.c_void_p)]
+
+
+class RotaryArgs(ctypes.Structure):
+    _fields_ = [("T", ctypes.c_int), ("q_heads", ctypes.c_int), ("kv_heads", ctypes.c_int),
+                ("head_dim", ctypes.c_int), ("rotary_dim", ctypes.c_int),
+                ("interleaved", ctypes.c_int), ("amplitude", ctypes.c_float),
+                ("table", ctypes.c_void_p), ("positions", ctypes.c_void_p),
+                ("q", ctypes.c_void_p), ("q_stride_t", ctypes.c_int64),
+                ("q_stride_h", ctypes.c_int64), ("q_out", ctypes.c_void_p),
+                ("q_out_stride_t", ctypes.c_int64), ("q_out_stride_h", ctypes.c_int64),
+                ("k", ctypes.c_void_p), ("k_stride_t", ctypes.c_int64),
+                ("k_stride_h", ctypes.c_int64), ("k_out", ctypes.c_void_p),
+                ("k_out_stride_t", ctypes.c_int64), ("k_out_stride_h", ctypes.c_int64),
+                ("v", ctypes.c_void_p), ("v_stride_t", ctypes.c_int64),
+                ("v_stride_h", ctypes.c_int64), ("slots", ctypes.c_void_p), ("cache", KvCache)]
+
+
+class LogitsArgs(ctypes.Structure):
+    _fields_ = [("dtype", ctypes.c_int), ("B", ctypes.c_int), ("m", ctypes.c_int),
+                ("V", ctypes.c_int), ("logits", ctypes.c_void_p),
+                ("logits_stride_b", ctypes.c_int64), ("logits_stride_i", ctypes.c_int64),
+                ("out", ctypes.c_void_p), ("out_stride_b", ctypes.c_int64),
+                ("out_stride_i", ctypes.c_int64), ("probabilities", ctypes.c_int),
+                ("history", ctypes.c_void_p), ("history_stride", ctypes.c_int),
+                ("history_lens", ctypes.c_void_p), ("prompt_lens", ctypes.c_void_p),
+                ("draft", ctypes.c_void_p), ("repetition", ctypes.c_void_p),
+                ("presence", ctypes.c_void_p), ("frequency", ctypes.c_void_p),
+                ("temperature", ctypes.c_void_p), ("biases", ctypes.c_int),
+                ("bias_tokens", ctypes.c_void_p), ("bias_values", ctypes.c_void_p),
+                ("mask", ctypes.c_void_p), ("mask_stride_b", ctypes.c_int64),
+                ("mask_stride_i", ctypes.c_int64)]
+
+
 _lib = None
 
 
@@ -140,9 +182,20 @@ def lib():
         L.moe_kv_read.argtypes = [ctypes.POINTER(KvCache), P, I, P, P, I, I, P, P, P, P]
         L.moe_paged_attention.argtypes = [ctypes.POINTER(AttentionArgs), P, ctypes.c_size_t, P]
         L.moe_verify_draft.argtypes = [ctypes.POINTER(VerifyArgs), P, P]
+        pages = ctypes.POINTER(PageState)
+        L.moe_plan_step.argtypes = [pages, P, P, I, I, P, P, P, P, P, P]
+        L.moe_release_pages.argtypes = [pages, P, P, P]
+        D = ctypes.c_double
+        L.moe_rotary_table.argtypes = [I, D, I, D, D, D, D, P]
+        L.moe_rotary.argtypes = [ctypes.POINTER(RotaryArgs), P, P]
+        L.moe_forward_few.argtypes = [ctypes.POINTER(ForwardArgs), P, P, ctypes.c_size_t, P]
+        L.moe_few_workspace_size.argtypes = [ctypes.POINTER(ForwardArgs)]
+        L.moe_few_workspace_size.restype = ctypes.c_size_t
+        L.moe_adjust_logits.argtypes = [ctypes.POINTER(LogitsArgs), P, P]
         for name in EXPORTS:
             if name not in ("moe_status_string", "moe_num_sms", "moe_workspace_size",
-                            "moe_last_cuda_error", "moe_gemm_cta_pairs"):
+                            "moe_last_cuda_error", "moe_gemm_cta_pairs",
+                            "moe_few_workspace_size"):
                 getattr(L, name).restype = I
         _lib = L
     return _lib
@@ -498,6 +551,228 @@ def verify_draft(p: torch.Tensor, q: torch.Tensor, draft: torch.Tensor, u_accept
     return accepted, tokens
 
 
+# ------------------------------------------------------------------ between the serving calls
+def _pages(what, block_table, held, free_pages, free_count, page_size) -> PageState:
+    B, stride = block_table.shape
+    if not (block_table.dtype is _I32 and block_table.is_contiguous()):
+        _bad(what, "block_table is int32 [B, entries], contiguous")
+    if not (_ints(held, B) and _ints(free_pages, free_pages.numel()) and _ints(free_count, 1)):
+        _bad(what, "held is int32 [B], free_pages int32, free_count int32 [1]")
+    return PageState(B, stride, page_size, free_pages.numel(), block_table.data_ptr(),
+                     held.data_ptr(), free_pages.data_ptr(), free_count.data_ptr())
+
+
+def plan_step(lens: torch.Tensor, new_lens: torch.Tensor, block_table: torch.Tensor,
+              held: torch.Tensor, free_pages: torch.Tensor, free_count: torch.Tensor, rows: int,
+              page_size: int, num_pages: int, ws: torch.Tensor, stream=None):
+    """moe_plan_step: (slots s32 [rows], positions s32 [rows], cu_q s32 [B+1], kv_lens s32 [B]);
+    block_table, held, free_pages and free_count are brought up to date."""
+    what = "moe_plan_step"
+    p = _pages(what, block_table, held, free_pages, free_count, page_size)
+    if not (_ints(lens, p.B) and _ints(new_lens, p.B)):
+        _bad(what, "lens and new_lens are int32 [B]")
+    _placed(what, block_table, ws, held, free_pages, free_count, lens, new_lens)
+    if rows < 0:
+        _bad(what, "rows is not negative")
+    # one block of memory for the four results, each at a multiple of 16 bytes
+    n, m = (rows + 3) // 4 * 4, (p.B + 4) // 4 * 4
+    block = _new((2 * n + 2 * m,), _I32, block_table.device, stream)
+    at = block.data_ptr()
+    code = lib().moe_plan_step(p, lens.data_ptr(), new_lens.data_ptr(), rows, num_pages, at,
+                               at + 4 * n, at + 8 * n, at + 8 * n + 4 * m, ws.data_ptr(),
+                               _raw_stream(stream, block_table))
+    if code:
+        _check(code, what)
+    return (block[:rows], block[n:n + rows], block[2 * n:2 * n + p.B + 1],
+            block[2 * n + m:2 * n + m + p.B])
+
+
+def release_pages(keep: torch.Tensor, block_table: torch.Tensor, held: torch.Tensor,
+                  free_pages: torch.Tensor, free_count: torch.Tensor, page_size: int,
+                  ws: torch.Tensor, stream=None):
+    """moe_release_pages: gives back the pages past keep s32 [B] positions (negative: none)."""
+    what = "moe_release_pages"
+    p = _pages(what, block_table, held, free_pages, free_count, page_size)
+    if not _ints(keep, p.B):
+        _bad(what, "keep is int32 [B]")
+    _placed(what, block_table, ws, held, free_pages, free_count, keep)
+    code = lib().moe_release_pages(p, keep.data_ptr(), ws.data_ptr(),
+                                   _raw_stream(stream, block_table))
+    if code:
+        _check(code, what)
+
+
+def rotary_table(rotary_dim: int, base: float = 10000.0, scaling: str = "none",
+                 factor: float = 1.0, original: float = 0.0, low: float = 1.0, high: float = 32.0,
+                 device="cuda") -> torch.Tensor:
+    """moe_rotary_table: int64 [rotary_dim/2], the turns of each pair from one position to the next
+    in units of 2^-64.  scaling: "none", "linear", "turns" or "index" (moe_rope_scaling_t)."""
+    what = "moe_rotary_table"
+    if scaling not in ROPE_SCALINGS:
+        _bad(what, f"scaling is one of {', '.join(ROPE_SCALINGS)}")
+    host = torch.empty(max(rotary_dim // 2, 1), dtype=torch.int64)
+    _check(lib().moe_rotary_table(rotary_dim, base, ROPE_SCALINGS[scaling], factor, original, low,
+                                  high, host.data_ptr()), what)
+    return host.to(device)
+
+
+def _heads(what, name, t, T=None):
+    """(T, heads, D, stride_t, stride_h) of bf16 [T, heads, D] with contiguous rows."""
+    n, H, D = t.shape
+    st, sh, sd = t.stride()
+    if not (t.dtype is _BF16 and (sd == 1 or D == 1) and (T is None or n == T)):
+        _bad(what, f"{name} is bf16 [T, heads, head_dim] with contiguous rows")
+    return n, H, D, (0 if n == 1 else st), (0 if H == 1 else sh)
+
+
+def _turns(what, table, positions, T):
+    if not (table.dtype is torch.int64 and table.dim() == 1 and table.is_contiguous()):
+        _bad(what, "table is the int64 [rotary_dim/2] of rotary_table")
+    if not _ints(positions, T):
+        _bad(what, "positions is int32 [T]")
+
+
+def _rotated(what, name, t, out, D, stream):
+    """(out, stride_t, stride_h): the result for t, new unless given."""
+    if out is None:
+        out = _new(t.shape, _BF16, t.device, stream)
+    elif out.shape != t.shape:
+        _bad(what, f"{name} is shaped like its input")
+    return out, *_heads(what, name, out)[3:]
+
+
+def rotary(q, k, positions: torch.Tensor, table: torch.Tensor, interleaved: bool = False,
+           amplitude: float = 1.0, q_out=None, k_out=None, stream=None):
+    """moe_rotary without a cache: (q_out, k_out) of q and k bf16 [T, heads, head_dim], either of
+    which may be None; an output may be its input."""
+    what = "moe_rotary"
+    first = q if q is not None else k
+    if first is None:
+        _bad(what, "q, k or both")
+    T, _, D = first.shape
+    _turns(what, table, positions, T)
+    a = RotaryArgs(T=T, head_dim=D, rotary_dim=2 * table.numel(), interleaved=1 if interleaved else 0,
+                   amplitude=amplitude, table=table.data_ptr(), positions=positions.data_ptr())
+    placed = [table, positions]
+    if q is not None:
+        _, a.q_heads, _, a.q_stride_t, a.q_stride_h = _heads(what, "q", q)
+        q_out, a.q_out_stride_t, a.q_out_stride_h = _rotated(what, "q_out", q, q_out, D, stream)
+        a.q, a.q_out = q.data_ptr(), q_out.data_ptr()
+        placed += [q, q_out]
+    if k is not None:
+        n, a.kv_heads, d, a.k_stride_t, a.k_stride_h = _heads(what, "k", k)
+        if n != T or d != D:
+            _bad(what, "q and k have the same tokens and head size")
+        k_out, a.k_out_stride_t, a.k_out_stride_h = _rotated(what, "k_out", k, k_out, D, stream)
+        a.k, a.k_out = k.data_ptr(), k_out.data_ptr()
+        placed += [k, k_out]
+    dev = first.get_device()
+    for t in placed:
+        if dev < 0 or t.get_device() != dev:
+            _bad(what, "all tensors must be on one GPU")
+    code = lib().moe_rotary(a, None, _raw_stream(stream, first))
+    if code:
+        _check(code, what)
+    return (None if q is None else q_out), (None if k is None else k_out)
+
+
+def rotary_write(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, positions: torch.Tensor,
+                 slots: torch.Tensor, table: torch.Tensor, k_cache: torch.Tensor,
+                 v_cache: torch.Tensor, ws: torch.Tensor, k_scales=None, v_scales=None,
+                 interleaved: bool = False, amplitude: float = 1.0, q_out=None, stream=None):
+    """moe_rotary into a paged cache: returns q rotated (bf16 [T, q_heads, head_dim]); k rotated
+    and v go to the slots s32 [T] of the cache, as kv_write stores them."""
+    what = "moe_rotary"
+    c = _cache(what, k_cache, v_cache, k_scales, v_scales)
+    T, Hq, D, qt, qh = _heads(what, "q", q)
+    _, H, d, kt, kh = _heads(what, "k", k, T)
+    _, _, _, vt, vh = _heads(what, "v", v, T)
+    if not (H == c.heads and D == d == c.head_dim and v.shape == k.shape):
+        _bad(what, "k and v are bf16 [T, heads, head_dim] of the cache, q has its head size")
+    _turns(what, table, positions, T)
+    if not _ints(slots, T):
+        _bad(what, "slots is int32 [T]")
+    q_out, ot, oh = _rotated(what, "q_out", q, q_out, D, stream)
+    _placed(what, k_cache, ws, v_cache, k_scales, v_scales, q, k, v, positions, slots, table, q_out)
+    a = RotaryArgs(T, Hq, H, D, 2 * table.numel(), 1 if interleaved else 0, amplitude,
+                   table.data_ptr(), positions.data_ptr(), q.data_ptr(), qt, qh, q_out.data_ptr(),
+                   ot, oh, k.data_ptr(), kt, kh, None, 0, 0, v.data_ptr(), vt, vh,
+                   slots.data_ptr(), c)
+    code = lib().moe_rotary(a, ws.data_ptr(), _raw_stream(stream, q))
+    if code:
+        _check(code, what)
+    return q_out
+
+
+def _per_sequence(what, B, **tensors):
+    for name, t in tensors.items():
+        if not (t is None or (t.dtype is _F32 and t.numel() == B and t.is_contiguous())):
+            _bad(what, f"{name} is f32 [B]")
+
+
+def adjust_logits(logits: torch.Tensor, ws: torch.Tensor, history=None, history_lens=None,
+                  prompt_lens=None, draft=None, repetition=None, presence=None, frequency=None,
+                  temperature=None, bias_tokens=None, bias_values=None, mask=None,
+                  probabilities: bool = True, out=None, stream=None) -> torch.Tensor:
+    """moe_adjust_logits: f32 [B, m, V] of logits [B, m, V] (f32 or bf16): the probabilities after
+    penalties, biases and mask, or (probabilities=False) the adjusted logits.  mask: int32
+    [B, m, words] or [B, words] (for all m rows), bit v % 32 of word v // 32 lets token v through."""
+    what = "moe_adjust_logits"
+    B, m, V = logits.shape
+    lb, li, lv = logits.stride()
+    f32 = logits.dtype is _F32
+    if not ((f32 or logits.dtype is _BF16) and (lv == 1 or V == 1)):
+        _bad(what, "logits is f32 or bf16 [B, m, V] with contiguous rows")
+    stride = 0
+    if history is not None:
+        stride = history.shape[-1]
+        if not _ints(history, B * stride):
+            _bad(what, "history is int32 [B, length]")
+    elif history_lens is not None or prompt_lens is not None:
+        _bad(what, "lengths without a history")
+    if not (history_lens is None or _ints(history_lens, B)) or not (prompt_lens is None or
+                                                                    _ints(prompt_lens, B)):
+        _bad(what, "history_lens and prompt_lens are int32 [B]")
+    if not (draft is None or _ints(draft, B * (m - 1))):
+        _bad(what, "draft is int32 [B, m - 1]")
+    _per_sequence(what, B, repetition=repetition, presence=presence, frequency=frequency,
+                  temperature=temperature)
+    biases = 0
+    if bias_tokens is not None or bias_values is not None:
+        if bias_tokens is None or bias_values is None:
+            _bad(what, "bias_tokens and bias_values come together")
+        biases = bias_tokens.shape[-1]
+        if not (_ints(bias_tokens, B * biases) and bias_values.dtype is _F32 and
+                bias_values.numel() == B * biases and bias_values.is_contiguous()):
+            _bad(what, "bias_tokens is int32 and bias_values f32 [B, biases]")
+    mb = mi = 0
+    if mask is not None:
+        words = (V + 31) // 32
+        s = mask.stride()
+        if not (mask.dtype is _I32 and mask.dim() in (2, 3) and mask.shape[0] == B and
+                mask.shape[-1] >= words and (s[-1] == 1 or mask.shape[-1] == 1) and
+                (mask.dim() == 2 or mask.shape[1] == m)):
+            _bad(what, "mask is int32 [B, m, words] or [B, words] with contiguous rows")
+        mb, mi = s[0], (s[1] if mask.dim() == 3 else 0)
+    _placed(what, logits, ws, history, history_lens, prompt_lens, draft, repetition, presence,
+            frequency, temperature, bias_tokens, bias_values, mask, out)
+    if out is None:
+        out = _new((B, m, V), _F32, logits.device, stream)
+    elif not (out.dtype is _F32 and out.shape == logits.shape and (out.stride(2) == 1 or V == 1)):
+        _bad(what, "out is f32, shaped like logits, with contiguous rows")
+    ob, oi, _ = out.stride()
+    p = lambda t: None if t is None else t.data_ptr()  # noqa: E731
+    a = LogitsArgs(DTYPE_F32 if f32 else DTYPE_BF16, B, m, V, logits.data_ptr(), lb, li,
+                   out.data_ptr(), ob, oi, 1 if probabilities else 0, p(history), stride,
+                   p(history_lens), p(prompt_lens), p(draft), p(repetition), p(presence),
+                   p(frequency), p(temperature), biases, p(bias_tokens), p(bias_values), p(mask), mb,
+                   mi)
+    code = lib().moe_adjust_logits(a, ws.data_ptr(), _raw_stream(stream, logits))
+    if code:
+        _check(code, what)
+    return out
+
+
 # ------------------------------------------------------------------ forward
 def forward_args(*, dtype, M, K, N, E, top_k, softcap=0.0, renorm=1, logits=None, x=None, w=None,
                  w_scales=None, w2=None, block_m=0, sched=SCHED_QUEUE, k_splits=0,
@@ -559,6 +834,27 @@ def ws_view(ws: torch.Tensor, offset: int, dtype: torch.dtype, shape) -> torch.T
 def forward(args: ForwardArgs, out: torch.Tensor, ws: torch.Tensor, stream=None):
     _check(lib().moe_forward(ctypes.byref(args), _ptr(out), _ptr(ws), ws.numel(), _stream(stream)),
            "moe_forward")
+    return out
+
+
+def few_workspace_size(args: ForwardArgs) -> int:
+    n = lib().moe_few_workspace_size(ctypes.byref(args))
+    if n == 0:
+        raise MoeError(MOE_ERR_INVALID_ARG, "moe_few_workspace_size")
+    return n
+
+
+def forward_few(args: ForwardArgs, out: torch.Tensor, ws: torch.Tensor, stream=None):
+    """moe_forward_few: the gated expert layer for at most FEW_TOKENS tokens (args as for forward);
+    ws: new_workspace(few_workspace_size(args))."""
+    what = "moe_forward_few"
+    if not (out.dtype is _BF16 and out.numel() == args.M * args.K and out.is_contiguous()):
+        _bad(what, "out is bf16 [M, K]")
+    _placed(what, out, ws)
+    code = lib().moe_forward_few(args, out.data_ptr(), ws.data_ptr(), ws.numel(),
+                                 _raw_stream(stream, out))
+    if code:
+        _check(code, what)
     return out
 
 

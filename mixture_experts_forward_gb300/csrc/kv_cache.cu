@@ -19,9 +19,6 @@ namespace {
 
 constexpr int kThreads = 256;
 
-// 1/s overflows binary32 below this maximum (s < 2^-126): such a row is zero.
-__device__ __forceinline__ float amax_floor() { return 448.0f * __uint_as_float(0x00800000u); }
-
 // Quantises 16 elements of a row shared by kTpr neighbouring lanes.
 template <int kTpr>
 __device__ __forceinline__ void quantise_piece(const uint4& raw0, const uint4& raw1, uint4& codes,

@@ -1,0 +1,325 @@
+// Penalties, biases and masks on logits, and their probabilities.
+//
+// A cluster of up to 8 CTAs takes one row, each CTA a contiguous part of the vocabulary that its
+// threads hold in registers (kPer values each, one load in flight per value), so the logits are
+// read once and the result is written once.  While the loads are under way the CTA counts the
+// history into shared memory, 32 bits a token of its part: bit 0 the prompt, bit 1 a bias, the
+// rest how often the token is among the outputs (integer atomics: the same in any order).  A token
+// whose word is zero is left as it is; biases of the same token are added by a warp that walks the
+// list in its order.  The softmax is over the CTA's own maximum and sum, which the CTAs exchange
+// once over distributed shared memory (max, sum, and the first token of the maximum for greedy
+// rows) and join in rank order, so repeated calls give the same bits.
+// Rows begin at any multiple of the element size (odd vocabularies): one element per lane and
+// load.  Bound by HBM for batches, by the launch and the chain of dependent steps for single rows.
+#include "serve_internal.cuh"
+
+namespace moe {
+namespace {
+
+constexpr int kLThreads = 512;
+constexpr int kLWarps = kLThreads / 32;
+constexpr int kLMaxCluster = 8;
+
+__device__ __forceinline__ float load_logit(const float* p) { return __ldg(p); }
+__device__ __forceinline__ float load_logit(const __nv_bfloat16* p) {
+  return __bfloat162float(__ldg(p));
+}
+
+__device__ __forceinline__ float neg_inf() { return __int_as_float(0xff800000); }
+
+template <typename T>
+struct LogitsParams {
+  const T* logits;
+  float* out;
+  int64_t l_sb, l_si, o_sb, o_si, m_sb, m_si;
+  const int32_t* history;
+  const int32_t* history_lens;
+  const int32_t* prompt_lens;
+  const int32_t* draft;
+  const float* repetition;
+  const float* presence;
+  const float* frequency;
+  const float* temperature;
+  const int32_t* bias_tokens;
+  const float* bias_values;
+  const uint32_t* mask;
+  Ctrl* ctrl;
+  int m, V, history_stride, biases, part, cluster;
+};
+
+// A CTA's share of a row: its maximum, where that is first, and the sum of exponentials.
+struct Share {
+  float max, sum;
+  int at, pad;
+};
+
+template <typename T, int kPer, bool kProbs>
+__global__ void __launch_bounds__(kLThreads, kPer <= 16 ? 3 : kPer <= 32 ? 2 : 1)
+    logits_kernel(const LogitsParams<T> p) {
+  extern __shared__ uint32_t s_count[];     // [part], then the biases' tokens and values
+  __shared__ Share s_share[kLMaxCluster];   // every CTA of the cluster writes its own here
+  __shared__ float s_max[kLWarps], s_sum[kLWarps];
+  __shared__ int s_at[kLWarps];
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  const int rank = blockIdx.x % p.cluster;
+  const int row = blockIdx.x / p.cluster;
+  const int b = row / p.m, i = row - b * p.m;
+  const int v0 = rank * p.part, n = min(p.part, p.V - v0);    // n may be <= 0
+  pdl_wait();
+  pdl_launch_dependents();
+  if (kProbs && p.cluster > 1)              // (before any CTA writes to another)
+    asm volatile("barrier.cluster.arrive.relaxed.aligned;" ::: "memory");
+
+  const T* src = p.logits + b * p.l_sb + i * p.l_si + v0;
+  float l[kPer];
+#pragma unroll
+  for (int j = 0; j < kPer; ++j) {
+    const int at = tid + j * kLThreads;
+    l[j] = at < n ? load_logit(src + at) : neg_inf();
+  }
+
+  // the counts
+  int32_t* s_bias_t = reinterpret_cast<int32_t*>(s_count + p.part);
+  float* s_bias_v = reinterpret_cast<float*>(s_bias_t + p.biases);
+  const bool counts = p.history != nullptr || p.draft != nullptr || p.biases > 0;
+  if (counts) {
+    for (int at = tid; at < p.part / 4; at += kLThreads)
+      reinterpret_cast<uint4*>(s_count)[at] = make_uint4(0u, 0u, 0u, 0u);
+    __syncthreads();
+    auto count = [&](int v, uint32_t what) {
+      if (v < 0 || v >= p.V) {
+        if (v != -1) set_error(p.ctrl, MOE_ERR_DEVICE_FAULT, 40);
+        return;
+      }
+      v -= v0;
+      if (v < 0 || v >= n) return;
+      if (what < 4) atomicOr(s_count + v, what); else atomicAdd(s_count + v, what);
+    };
+    if (p.history != nullptr) {
+      int len = p.history_stride, prompt = 0;
+      if (p.history_lens != nullptr) len = __ldg(p.history_lens + b);
+      if (p.prompt_lens != nullptr) prompt = __ldg(p.prompt_lens + b);
+      if (len < 0 || len > p.history_stride || prompt < 0 || prompt > len) {
+        if (tid == 0) set_error(p.ctrl, MOE_ERR_DEVICE_FAULT, 41);
+        len = min(max(len, 0), p.history_stride);
+        prompt = min(max(prompt, 0), len);
+      }
+      const int32_t* h = p.history + static_cast<int64_t>(b) * p.history_stride;
+      for (int at = tid; at < len; at += kLThreads) count(__ldg(h + at), at < prompt ? 1u : 4u);
+    }
+    if (p.draft != nullptr && tid < i) count(__ldg(p.draft + b * (p.m - 1) + tid), 4u);
+    for (int at = tid; at < p.biases; at += kLThreads) {
+      const int v = __ldg(p.bias_tokens + static_cast<int64_t>(b) * p.biases + at);
+      s_bias_t[at] = v;
+      s_bias_v[at] = __ldg(p.bias_values + static_cast<int64_t>(b) * p.biases + at);
+      count(v, 2u);
+    }
+    __syncthreads();
+  }
+  auto number = [&](const float* a, float none) { return a == nullptr ? none : __ldg(a + b); };
+  float rep = number(p.repetition, 1.0f), temp = number(p.temperature, 1.0f);
+  const float presence = number(p.presence, 0.0f), frequency = number(p.frequency, 0.0f);
+  if (!(rep > 0.0f) || !(temp >= 0.0f)) {
+    if (tid == 0) set_error(p.ctrl, MOE_ERR_DEVICE_FAULT, 42);
+    if (!(rep > 0.0f)) rep = 1.0f;
+    if (!(temp >= 0.0f)) temp = 1.0f;
+  }
+  const uint32_t* mask =
+      p.mask == nullptr ? nullptr : p.mask + b * p.m_sb + i * p.m_si + v0 / 32;
+
+  float top = neg_inf();
+#pragma unroll
+  for (int j = 0; j < kPer; ++j) {
+    const int at = tid + j * kLThreads;
+    const uint32_t c = counts && at < n ? s_count[at] : 0u;
+    if (c != 0) {
+      if ((c & ~2u) != 0) l[j] = l[j] > 0.0f ? __fdiv_rn(l[j], rep) : l[j] * rep;
+      if (c >= 4) l[j] = l[j] - frequency * static_cast<float>(c >> 2) - presence;
+    }
+    uint32_t biased = __ballot_sync(0xffffffffu, (c & 2u) != 0);
+    while (biased != 0) {
+      const int who = __ffs(biased) - 1;
+      biased &= biased - 1;
+      const int v = v0 + (at - lane + who);
+      for (int q = 0; q < p.biases; q += 32) {
+        const bool mine = q + lane < p.biases && s_bias_t[q + lane] == v;
+        uint32_t found = __ballot_sync(0xffffffffu, mine);
+        for (; found != 0; found &= found - 1)
+          if (lane == who && l[j] > neg_inf()) l[j] += s_bias_v[q + __ffs(found) - 1];
+      }
+    }
+    if (mask != nullptr && at < n && ((__ldg(mask + (at >> 5)) >> (at & 31)) & 1u) == 0)
+      l[j] = neg_inf();
+    if (!(l[j] >= neg_inf())) l[j] = neg_inf();               // NaN
+    top = fmaxf(top, l[j]);
+  }
+  float* out = p.out + b * p.o_sb + i * p.o_si + v0;
+  if constexpr (!kProbs) {
+#pragma unroll
+    for (int j = 0; j < kPer; ++j) {
+      const int at = tid + j * kLThreads;
+      if (at < n) out[at] = l[j];
+    }
+    return;
+  } else {
+    // the CTA's maximum, then (greedy) its first place or the sum
+    auto all_max = [&](float x) {
+#pragma unroll
+      for (int o = 16; o > 0; o >>= 1) x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, o));
+      return x;
+    };
+    top = all_max(top);
+    if (lane == 0) s_max[warp] = top;
+    __syncthreads();
+    top = s_max[0];
+#pragma unroll
+    for (int w = 1; w < kLWarps; ++w) top = fmaxf(top, s_max[w]);
+    const bool greedy = temp == 0.0f;
+    int first = 0x7fffffff;
+    float sum = 0.0f;
+    // exp((l - top) / temp) as a power of two; at the ends of the types: a token at the maximum is 1
+    // (also +inf), one at -inf is 0
+    const float rate = greedy ? 0.0f : fminf(__fdividef(1.4426950408889634f, temp), 3.0e38f);
+    if (greedy) {
+#pragma unroll
+      for (int j = kPer - 1; j >= 0; --j)
+        if (l[j] == top && top > neg_inf()) first = v0 + tid + j * kLThreads;
+      first = __reduce_min_sync(0xffffffffu, first);
+      if (lane == 0) s_at[warp] = first;
+    } else {
+#pragma unroll
+      for (int j = 0; j < kPer; ++j) {
+        const float d = (l[j] - top) * rate;
+        float e;
+        asm("ex2.approx.f32 %0, %1;" : "=f"(e) : "f"(d));
+        e = l[j] == top ? 1.0f : e;
+        e = l[j] == neg_inf() ? 0.0f : e;
+        l[j] = e;
+        sum += e;
+      }
+#pragma unroll
+      for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
+      if (lane == 0) s_sum[warp] = sum;
+    }
+    __syncthreads();
+    Share mine = {top, 0.0f, 0x7fffffff, 0};
+    if (greedy) {
+#pragma unroll
+      for (int w = 0; w < kLWarps; ++w) mine.at = min(mine.at, s_at[w]);
+    } else {
+#pragma unroll
+      for (int w = 0; w < kLWarps; ++w) mine.sum += s_sum[w];
+    }
+    if (p.cluster > 1) {
+      asm volatile("barrier.cluster.wait.aligned;" ::: "memory");
+      if (tid < p.cluster) {
+        uint32_t at;
+        asm volatile("mapa.shared::cluster.u32 %0, %1, %2;"
+                     : "=r"(at)
+                     : "r"(static_cast<uint32_t>(__cvta_generic_to_shared(s_share + rank))), "r"(tid));
+        asm volatile("st.shared::cluster.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(at),
+                     "r"(__float_as_uint(mine.max)), "r"(__float_as_uint(mine.sum)), "r"(mine.at),
+                     "r"(0)
+                     : "memory");
+      }
+      asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory");
+      asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory");
+    } else {
+      if (tid == 0) s_share[0] = mine;
+      __syncthreads();
+    }
+    float all = neg_inf(), total = 0.0f;
+    int choice = 0x7fffffff;
+    for (int c = 0; c < p.cluster; ++c) all = fmaxf(all, s_share[c].max);
+    auto factor = [&](float m) {
+      float f;
+      asm("ex2.approx.f32 %0, %1;" : "=f"(f) : "f"((m - all) * rate));
+      return m == all ? 1.0f : m == neg_inf() ? 0.0f : f;
+    };
+    for (int c = 0; c < p.cluster; ++c) {
+      const Share s = s_share[c];
+      if (s.max == all) choice = min(choice, s.at);
+      total += s.sum * factor(s.max);
+    }
+    const float scale = all == neg_inf() ? 0.0f : __fdiv_rn(factor(top), total);
+#pragma unroll
+    for (int j = 0; j < kPer; ++j) {
+      const int at = tid + j * kLThreads;
+      const float y = greedy ? (v0 + at == choice ? 1.0f : 0.0f) : l[j] * scale;
+      if (at < n) out[at] = y;
+    }
+  }
+}
+
+template <typename T, int kPer, bool kProbs>
+cudaError_t launch(LogitsParams<T> p, int rows, int cluster, cudaStream_t stream) {
+  p.part = kPer * kLThreads;
+  p.cluster = cluster;
+  const int bytes = p.part * 4 + p.biases * 8;
+  if (bytes > 48 * 1024) {
+    const cudaError_t e = cudaFuncSetAttribute(logits_kernel<T, kPer, kProbs>,
+                                               cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                               kPer * kLThreads * 4 + 1024 * 8);
+    if (e != cudaSuccess) return e;
+  }
+  cudaLaunchAttribute attr[2];
+  cudaLaunchConfig_t cfg = make_cfg(dim3(static_cast<unsigned>(rows) * cluster), dim3(kLThreads),
+                                    stream, true, attr);
+  attr[1].id = cudaLaunchAttributeClusterDimension;
+  attr[1].val.clusterDim.x = kProbs ? cluster : 1;
+  attr[1].val.clusterDim.y = 1;
+  attr[1].val.clusterDim.z = 1;
+  cfg.numAttrs = 2;
+  cfg.dynamicSmemBytes = bytes;
+  return cudaLaunchKernelEx(&cfg, logits_kernel<T, kPer, kProbs>, p);
+}
+
+template <typename T, bool kProbs>
+cudaError_t launch_rows(const LogitsParams<T>& p, int rows, cudaStream_t stream) {
+  // As many CTAs of 4096 tokens as the row has, up to 8; longer rows give each CTA more.
+  const int parts = (p.V + 4095) / 4096;
+  const int cluster = parts >= 5 ? 8 : parts >= 3 ? 4 : parts;
+  const int per = (p.V + cluster * kLThreads - 1) / (cluster * kLThreads);
+  if (per <= 8) return launch<T, 8, kProbs>(p, rows, cluster, stream);
+  if (per <= 16) return launch<T, 16, kProbs>(p, rows, cluster, stream);
+  if (per <= 32) return launch<T, 32, kProbs>(p, rows, cluster, stream);
+  return launch<T, 64, kProbs>(p, rows, cluster, stream);
+}
+
+template <typename T>
+cudaError_t launch_typed(const moe_logits_args& a, Ctrl* ctrl, cudaStream_t stream) {
+  LogitsParams<T> p = {};
+  p.logits = static_cast<const T*>(a.logits);
+  p.out = a.out;
+  p.l_sb = a.logits_stride_b, p.l_si = a.logits_stride_i;
+  p.o_sb = a.out_stride_b, p.o_si = a.out_stride_i;
+  p.m_sb = a.mask_stride_b, p.m_si = a.mask_stride_i;
+  p.history = a.history_stride > 0 ? a.history : nullptr;
+  p.history_lens = a.history_lens;
+  p.prompt_lens = a.prompt_lens;
+  p.draft = a.m > 1 ? a.draft : nullptr;
+  p.repetition = a.repetition;
+  p.presence = a.presence;
+  p.frequency = a.frequency;
+  p.temperature = a.temperature;
+  p.bias_tokens = a.bias_tokens;
+  p.bias_values = a.bias_values;
+  p.mask = a.mask;
+  p.ctrl = ctrl;
+  p.m = a.m;
+  p.V = a.V;
+  p.history_stride = a.history_stride;
+  p.biases = a.biases;
+  const int rows = a.B * a.m;
+  return a.probabilities ? launch_rows<T, true>(p, rows, stream)
+                         : launch_rows<T, false>(p, rows, stream);
+}
+
+}  // namespace
+
+cudaError_t launch_adjust_logits(const moe_logits_args& a, Ctrl* ctrl, cudaStream_t stream) {
+  return a.dtype == MOE_DTYPE_F32 ? launch_typed<float>(a, ctrl, stream)
+                                  : launch_typed<__nv_bfloat16>(a, ctrl, stream);
+}
+
+}  // namespace moe

@@ -18,6 +18,9 @@ __device__ __forceinline__ uint16_t cvt_e4m3x2(float lo, float hi) {
   return r;
 }
 
+// The cache's rows: 1/s overflows binary32 below this maximum (s < 2^-126), and such a row is zero.
+__device__ __forceinline__ float amax_floor() { return 448.0f * __uint_as_float(0x00800000u); }
+
 // Quantises elements [16c, 16c+16) of `row` (bf16).  The 8 threads of one
 // 128-element block must be lanes l, l^1, l^2, l^4 of the same warp, and every
 // lane of the warp must call this (invalid lanes pass valid = false).

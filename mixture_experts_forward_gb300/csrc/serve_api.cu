@@ -17,6 +17,18 @@ int log2_of(int x) {
   return n;
 }
 
+bool ws_ok(const void* ws) {
+  return ws != nullptr && (reinterpret_cast<uintptr_t>(ws) & 255u) == 0;
+}
+
+bool stride8(int64_t s) { return s % 8 == 0; }
+
+static_assert(MOE_ATTENTION_CTRL_BYTES - MOE_CTRL_BYTES >= 4 * kMaxParts, "a counter per CTA");
+
+}  // namespace
+
+namespace moe {
+
 moe_status_t check_cache(const moe_kv_cache* c, KvCacheView* view) {
   if (c == nullptr || c->k == nullptr || c->v == nullptr) return MOE_ERR_INVALID_ARG;
   if (c->dtype != MOE_DTYPE_FP8_E4M3 && c->dtype != MOE_DTYPE_BF16) return MOE_ERR_INVALID_ARG;
@@ -43,15 +55,7 @@ moe_status_t check_cache(const moe_kv_cache* c, KvCacheView* view) {
   return MOE_OK;
 }
 
-bool ws_ok(const void* ws) {
-  return ws != nullptr && (reinterpret_cast<uintptr_t>(ws) & 255u) == 0;
-}
-
-bool stride8(int64_t s) { return s % 8 == 0; }
-
-static_assert(MOE_ATTENTION_CTRL_BYTES - MOE_CTRL_BYTES >= 4 * kMaxParts, "a counter per CTA");
-
-}  // namespace
+}  // namespace moe
 
 extern "C" {
 

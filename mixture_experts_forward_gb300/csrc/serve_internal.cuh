@@ -74,6 +74,22 @@ constexpr int kTileRows = 256;
 constexpr int kTileKeys = 128;
 cudaError_t launch_attention_tiles(const AttnParams& p, int head_dim, bool fp8,
                                    cudaStream_t stream);
+// moe_kv_cache checked, and as the kernels take it (serve_api.cu).
+moe_status_t check_cache(const moe_kv_cache* c, KvCacheView* view);
+
+// Sequences of one plan at most: their prefix sums stay in shared memory.
+constexpr int kMaxPlanned = 8192;
+cudaError_t launch_plan_step(const moe_page_state& p, const int32_t* lens, const int32_t* news,
+                             int rows, int num_pages, int32_t* slots, int32_t* positions,
+                             int32_t* cu_q, int32_t* kv_lens, Ctrl* ctrl, int num_sms,
+                             cudaStream_t stream);
+cudaError_t launch_release_pages(const moe_page_state& p, const int32_t* keep, Ctrl* ctrl,
+                                 int num_sms, cudaStream_t stream);
+cudaError_t launch_rotary(const moe_rotary_args& a, const KvCacheView* cache, Ctrl* ctrl,
+                          int num_sms, cudaStream_t stream);
+cudaError_t launch_few_experts(const moe_forward_args& f, void* out, float* h, Ctrl* ctrl,
+                               int num_sms, cudaStream_t stream);
+cudaError_t launch_adjust_logits(const moe_logits_args& a, Ctrl* ctrl, cudaStream_t stream);
 cudaError_t launch_verify(const moe_verify_args& a, Ctrl* ctrl, int num_sms, cudaStream_t stream);
 
 }  // namespace moe
