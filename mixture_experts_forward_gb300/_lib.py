@@ -574,17 +574,16 @@ def plan_step(lens: torch.Tensor, new_lens: torch.Tensor, block_table: torch.Ten
     _placed(what, block_table, ws, held, free_pages, free_count, lens, new_lens)
     if rows < 0:
         _bad(what, "rows is not negative")
-    # one block of memory for the four results, each at a multiple of 16 bytes
-    n, m = (rows + 3) // 4 * 4, (p.B + 4) // 4 * 4
-    block = _new((2 * n + 2 * m,), _I32, block_table.device, stream)
-    at = block.data_ptr()
-    code = lib().moe_plan_step(p, lens.data_ptr(), new_lens.data_ptr(), rows, num_pages, at,
-                               at + 4 * n, at + 8 * n, at + 8 * n + 4 * m, ws.data_ptr(),
-                               _raw_stream(stream, block_table))
+    # one allocation for the four results
+    B = p.B
+    slots, positions, cu_q, kv_lens = _new((2 * rows + 2 * B + 1,), _I32, block_table.device,
+                                           stream).split_with_sizes((rows, rows, B + 1, B))
+    code = lib().moe_plan_step(p, lens.data_ptr(), new_lens.data_ptr(), rows, num_pages,
+                               slots.data_ptr(), positions.data_ptr(), cu_q.data_ptr(),
+                               kv_lens.data_ptr(), ws.data_ptr(), _raw_stream(stream, block_table))
     if code:
         _check(code, what)
-    return (block[:rows], block[n:n + rows], block[2 * n:2 * n + p.B + 1],
-            block[2 * n + m:2 * n + m + p.B])
+    return slots, positions, cu_q, kv_lens
 
 
 def release_pages(keep: torch.Tensor, block_table: torch.Tensor, held: torch.Tensor,

@@ -2,20 +2,24 @@
 //
 // With T <= 16 tokens nearly every weight is used for one or two of them, so the layer is one
 // pass over the active experts' weights and HBM bounds it; everything else has to hide behind
-// that stream.  A warp takes 16 weight rows at a time as the A operand of mma.sync m16n8k16 and
-// the tokens as its 8 columns (twice 8 above 8 tokens): the tensor core's legacy path is far
-// from its limit at this intensity (one MMA per 256 weights), and it takes the weights from
-// registers, so E4M3 codes become binary16 on the way (exact) and no activation has to be
-// quantised.  The order of k inside an MMA is free, so a lane loads 16 contiguous bytes of a row
-// and uses them as they lie.  Weights come by cp.async into a ring of the warp's own (2 KB a
-// step: 16 rows x 128 bytes, kDepth steps ahead); a lane reads back what it copied.
+// that stream.  A warp takes 16 weight rows at a time as the A operand of mma.sync and the tokens
+// as its 8 columns (twice 8 above 8 tokens), m16n8k16.  The tensor core's legacy path is far from
+// its limit at this intensity (an MMA per 256 weights), takes its operands from registers, so E4M3
+// codes become binary16 on the way (exact) and no activation has to be quantised, and leaves the
+// sums there: no tensor memory to read back for each 128-deep scale block.  (E4M3 operands in
+// m16n8k32 took 170 us instead of 96 for 16 tokens through 69 of 256 experts: that form is made of
+// conversions too, one for each MMA.)  The order of k inside
+// an MMA is free, so a lane loads 16 contiguous bytes of a row and uses them as they lie.  Weights
+// come by cp.async into a ring of the warp's own (4 KB a step: 16 rows x 256 bytes); a lane reads
+// back the rows' pieces that it copied itself.
 //
 // Up: a unit is 8 gate rows and the 8 up rows of the same h columns, in one MMA tile, so
 // silu(gate) * up is computed where the sums are; several warps share a unit's K where there
 // are few units.  Down: a cluster of 8 CTAs takes 128 output rows, each of its CTAs an equal
 // share of all active experts' K; the shares meet over distributed shared memory, in rank order
 // (no atomics: repeated calls give the same bits).  Every CTA routes by itself (the same device
-// function as moe_route), which costs a microsecond and saves a launch and its wait.
+// function as moe_route), which saves a launch and its wait; the down kernel does so, and fetches
+// its first weights, while the up kernel still runs.
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 
@@ -25,14 +29,12 @@
 namespace moe {
 namespace {
 
-constexpr int kUpThreads = 512, kUpWarps = kUpThreads / 32;
-constexpr int kDownThreads = 256, kDownWarps = kDownThreads / 32;
 constexpr int kMaxTok = MOE_FEW_TOKENS;
-constexpr int kStep = 2048;               // weight bytes of a step: 16 rows x 128
-constexpr int kSlot = kStep + 16;         // and the step's block scales
-constexpr int kCluster = 8;               // CTAs that share 128 output rows
+constexpr int kStepBytes = 256;           // of each row and step: two blocks of 128
+constexpr int kSlotBytes = 16 * kStepBytes;   // of the ring: a step's rows,
+constexpr int kSlot = kSlotBytes + 16;        // and its blocks' scales
+constexpr int kCluster = 8;               // CTAs that share 128 output rows, at most
 constexpr int kDownRows = 128;
-constexpr int kHRows = 96;                // staged rows of h (128 bytes of weights' k each)
 
 __device__ __forceinline__ void cp_async16(uint32_t dst, const void* src) {
   asm volatile("cp.async.cg.shared.global.L2::256B [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
@@ -46,21 +48,21 @@ __device__ __forceinline__ void cp_wait() {
   asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
 }
 
+// c += a x b; codes as binary16, or BF16.
 template <bool kFP8>
-__device__ __forceinline__ void mma16816(float (&c)[4], uint32_t a0, uint32_t a1, uint32_t a2,
-                                         uint32_t a3, uint32_t b0, uint32_t b1) {
+__device__ __forceinline__ void mma(float (&c)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
   if constexpr (kFP8)
     asm volatile(
         "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, "
         "{%0,%1,%2,%3};"
         : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
-        : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+        : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
   else
     asm volatile(
         "mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, "
         "{%8,%9}, {%0,%1,%2,%3};"
         : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
-        : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+        : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
 }
 
 // The power of two that takes a block's largest element into [2^14, 2^15) of binary16, and its
@@ -69,6 +71,12 @@ __device__ __forceinline__ void block_scale(float amax, float& up, float& down) 
   const int e = max(static_cast<int>(__float_as_uint(amax) >> 23), 27) - 127;   // <= 128
   up = __uint_as_float(static_cast<uint32_t>(14 - e + 127) << 23);
   down = __uint_as_float(static_cast<uint32_t>(e - 14 + 127) << 23);
+}
+
+// Four values, scaled, as binary16.
+__device__ __forceinline__ uint2 halves(const float (&v)[4], float up) {
+  const __half2 a = __floats2half2_rn(v[0] * up, v[1] * up), b = __floats2half2_rn(v[2] * up, v[3] * up);
+  return make_uint2(*reinterpret_cast<const uint32_t*>(&a), *reinterpret_cast<const uint32_t*>(&b));
 }
 
 struct FewParams {
@@ -84,6 +92,8 @@ struct FewParams {
   int T, H, I, E, k;
   float softcap;
   int renorm;
+  int h_rows;                  // rows of h that the down kernel stages at a time
+  int cluster;                 // CTAs that share 128 output rows (1, 2, 4 or 8)
 };
 
 __device__ __noinline__ void route_one(const float* row, int E, int k, float softcap, int renorm,
@@ -97,26 +107,34 @@ __device__ __noinline__ void route_one(const float* row, int E, int k, float sof
 struct Routing {
   int32_t* ids;                // [T * k]
   float* weights;              // [T * k]
-  uint32_t* tokens;            // [E] bit t: token t goes there
+  uint32_t* tokens;            // [E] bit t: token t goes there; bits 16 ..: place in `active`
   int32_t* active;             // [min(E, T * k)] the experts that any token goes to, ascending
+  uint8_t* choice;             // [active][kMaxTok] which of its k choices that is to the token
+  __host__ __device__ static int most(int T, int k, int E) { return E < T * k ? E : T * k; }
   __host__ __device__ static int bytes(int T, int k, int E) {
-    const int routes = T * k;
-    return (8 * routes + 4 * E + 4 * (E < routes ? E : routes) + 15) / 16 * 16;
+    return (8 * T * k + 4 * E + (4 + kMaxTok) * most(T, k, E) + 15) / 16 * 16;
   }
   __device__ Routing(uint8_t* p, int T, int k, int E)
       : ids(reinterpret_cast<int32_t*>(p)),
         weights(reinterpret_cast<float*>(ids + T * k)),
         tokens(reinterpret_cast<uint32_t*>(weights + T * k)),
-        active(reinterpret_cast<int32_t*>(tokens + E)) {}
+        active(reinterpret_cast<int32_t*>(tokens + E)),
+        choice(reinterpret_cast<uint8_t*>(active + most(T, k, E))) {}
+  __device__ uint32_t tokens_of(int a) const { return tokens[active[a]] & 0xffffu; }
 };
 
-// Fills r; returns how many experts are active.  All threads of the CTA.
-__device__ __forceinline__ int route_all(const FewParams& p, const Routing& r, int* s_n) {
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, warps = blockDim.x >> 5;
+// Routes this warp's tokens and clears the table; route_join() follows.
+__device__ __forceinline__ void route_tokens(const FewParams& p, const Routing& r) {
+  const int warp = threadIdx.x >> 5;
   for (int e = threadIdx.x; e < p.E; e += blockDim.x) r.tokens[e] = 0;
-  for (int t = warp; t < p.T; t += warps)
+  for (int t = warp; t < p.T; t += blockDim.x / 32)
     route_one(p.logits + static_cast<size_t>(t) * p.E, p.E, p.k, p.softcap, p.renorm,
               r.ids + t * p.k, r.weights + t * p.k);
+}
+
+// The active experts, by all threads; returns how many there are.
+__device__ __forceinline__ int route_join(const FewParams& p, const Routing& r, int* s_n) {
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   __syncthreads();
   for (int i = threadIdx.x; i < p.T * p.k; i += blockDim.x) {
     const int e = r.ids[i];
@@ -129,121 +147,126 @@ __device__ __forceinline__ int route_all(const FewParams& p, const Routing& r, i
   if (warp == 0) {
     int n = 0;
     for (int e0 = 0; e0 < p.E; e0 += 32) {
-      const bool on = e0 + lane < p.E && r.tokens[e0 + lane] != 0;
-      const uint32_t m = __ballot_sync(0xffffffffu, on);
-      if (on) r.active[n + __popc(m & ((1u << lane) - 1u))] = e0 + lane;
+      const int e = e0 + lane;
+      const uint32_t t = e < p.E ? r.tokens[e] : 0u;
+      const uint32_t m = __ballot_sync(0xffffffffu, t != 0);
+      if (t != 0) {
+        const int a = n + __popc(m & ((1u << lane) - 1u));
+        r.active[a] = e;
+        r.tokens[e] = t | (static_cast<uint32_t>(a) << 16);
+      }
       n += __popc(m);
     }
     if (lane == 0) *s_n = n;
   }
   __syncthreads();
+  for (int i = threadIdx.x; i < p.T * p.k; i += blockDim.x) {
+    const int e = r.ids[i], t = i / p.k;
+    if (e >= 0 && e < p.E) r.choice[(r.tokens[e] >> 16) * kMaxTok + t] = static_cast<uint8_t>(i - t * p.k);
+  }
+  __syncthreads();
   return *s_n;
 }
 
-// The 8 (FP8) or 4 (BF16) MMAs of one step for one group of 8 tokens.  w: the lane's 16 bytes of
-// rows g and g + 8 in the two halves of the 128 bytes; b: the lane's token's row at this step.
-// FP8: code q of the 16 is k = 16 t + q of its half, and b holds 128 binary16; BF16: 64.
+// One block of 128 bytes of 16 rows, as A operands: the lane's 16 bytes of rows g and g + 8 in
+// its two halves.
 template <bool kFP8>
-__device__ __forceinline__ void load_b(uint4 (&b)[4], const uint8_t* row, int t, bool there) {
-#pragma unroll
-  for (int c = 0; c < 2; ++c) {
-    if constexpr (kFP8) {
-      const uint4* q = reinterpret_cast<const uint4*>(row + c * 128 + t * 32);
-      b[2 * c] = there ? q[0] : make_uint4(0u, 0u, 0u, 0u);
-      b[2 * c + 1] = there ? q[1] : make_uint4(0u, 0u, 0u, 0u);
-    } else {
-      const uint4* q = reinterpret_cast<const uint4*>(row + c * 64 + t * 16);
-      b[c] = there ? q[0] : make_uint4(0u, 0u, 0u, 0u);
-    }
-  }
-}
-
-template <bool kFP8>
-struct Weights {
-  uint32_t a[kFP8 ? 8 : 4][4];
-  // the lane's pieces of a ring slot: row g, row g + 8 of half 0, then of half 1
-  __device__ __forceinline__ void load(const uint8_t* slot, int lane) {
-    const uint4* q = reinterpret_cast<const uint4*>(slot) + lane;
+struct Block {
+  static constexpr int kMmas = kFP8 ? 4 : 2;             // in each half
+  uint32_t a[2 * kMmas][4];
+  // the lane's piece of row g in the block's two halves (row g + 8 lies 8 rows further)
+  __device__ __forceinline__ void load(const uint8_t* first, const uint8_t* second) {
 #pragma unroll
     for (int c = 0; c < 2; ++c) {
-      const uint4 lo = q[64 * c], hi = q[64 * c + 32];
+      const uint8_t* q = c == 0 ? first : second;
+      const uint4 lo = *reinterpret_cast<const uint4*>(q);
+      const uint4 hi = *reinterpret_cast<const uint4*>(q + 8 * kStepBytes);
       const uint32_t l[4] = {lo.x, lo.y, lo.z, lo.w}, u[4] = {hi.x, hi.y, hi.z, hi.w};
-      if constexpr (kFP8) {
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          a[4 * c + i][0] = e4m3x2_to_f16x2(static_cast<uint16_t>(l[i]));
-          a[4 * c + i][1] = e4m3x2_to_f16x2(static_cast<uint16_t>(u[i]));
-          a[4 * c + i][2] = e4m3x2_to_f16x2(static_cast<uint16_t>(l[i] >> 16));
-          a[4 * c + i][3] = e4m3x2_to_f16x2(static_cast<uint16_t>(u[i] >> 16));
-        }
-      } else {
-#pragma unroll
-        for (int i = 0; i < 2; ++i) {
-          a[2 * c + i][0] = l[2 * i];
-          a[2 * c + i][1] = u[2 * i];
-          a[2 * c + i][2] = l[2 * i + 1];
-          a[2 * c + i][3] = u[2 * i + 1];
+      for (int i = 0; i < kMmas; ++i) {
+        uint32_t(&m)[4] = a[kMmas * c + i];
+        if constexpr (kFP8) {
+          m[0] = e4m3x2_to_f16x2(static_cast<uint16_t>(l[i]));
+          m[1] = e4m3x2_to_f16x2(static_cast<uint16_t>(u[i]));
+          m[2] = e4m3x2_to_f16x2(static_cast<uint16_t>(l[i] >> 16));
+          m[3] = e4m3x2_to_f16x2(static_cast<uint16_t>(u[i] >> 16));
+        } else {
+          m[0] = l[2 * i], m[1] = u[2 * i], m[2] = l[2 * i + 1], m[3] = u[2 * i + 1];
         }
       }
     }
   }
-  __device__ __forceinline__ void multiply(float (&c)[4], const uint4 (&b)[4]) const {
+  // times the activations: 128 binary16 or 64 bf16 of the lane's token's row, or zeros
+  __device__ __forceinline__ void multiply(float (&c)[4], const uint8_t* row, int t, bool there) const {
 #pragma unroll
-    for (int i = 0; i < (kFP8 ? 4 : 2); ++i) {
-      mma16816<kFP8>(c, a[2 * i][0], a[2 * i][1], a[2 * i][2], a[2 * i][3], b[i].x, b[i].y);
-      mma16816<kFP8>(c, a[2 * i + 1][0], a[2 * i + 1][1], a[2 * i + 1][2], a[2 * i + 1][3], b[i].z,
-                     b[i].w);
+    for (int i = 0; i < kMmas; ++i) {
+      uint4 b = make_uint4(0u, 0u, 0u, 0u);
+      const int at = kFP8 ? i / 2 * 128 + t * 32 + i % 2 * 16 : i * 64 + t * 16;
+      if (there) b = *reinterpret_cast<const uint4*>(row + at);
+      mma<kFP8>(c, a[2 * i], b.x, b.y);
+      mma<kFP8>(c, a[2 * i + 1], b.z, b.w);
     }
   }
 };
 
-// Copies one step's 16 rows (two row pointers of the lane, its 16 bytes of both halves).
-__device__ __forceinline__ void copy_step(uint32_t slot, const uint8_t* lo, const uint8_t* hi) {
-  const uint32_t d = slot + lane_id() * 16;
-  cp_async16(d, lo);
-  cp_async16(d + 512, hi);
-  cp_async16(d + 1024, lo + 64);
-  cp_async16(d + 1536, hi + 64);
+// Copies one step's 16 rows x 256 bytes (128 unless `both`), two rows an instruction: lane l brings
+// 16-byte piece l % 16 of row l / 16 of the pair.  src: the lane's piece of the first pair; the
+// second eight rows begin `gap` bytes after the first row.  In the slot the pieces of odd rows change places in
+// fours, so that the products' loads (four neighbouring pieces of two rows) meet no bank twice.
+__device__ __forceinline__ uint32_t piece_at(int row, int piece) {
+  return row * kStepBytes + ((piece ^ ((row & 1) << 2)) << 4);
+}
+__device__ __forceinline__ void copy_step(uint32_t slot, const uint8_t* src, int64_t row_bytes,
+                                          int64_t gap, bool both) {
+  const int lane = threadIdx.x & 31, piece = lane & 15;
+  if (!both && piece >= 8) return;
+  const uint32_t d = slot + piece_at(lane >> 4, piece);
+#pragma unroll
+  for (int j = 0; j < 8; ++j) {
+    cp_async16(d + 2 * j * kStepBytes, src);
+    src += j == 3 ? gap - 6 * row_bytes : 2 * row_bytes;
+  }
 }
 
 // ----------------------------------------------------------------------------
-// Up: h[route, i] = silu(gate_i) * up_i.
+// Up: h[route, i] = silu(gate_i) * up_i.  x lies in shared memory, FP8 as binary16 scaled by a
+// power of two for each 128 elements; tokens' rows are so far apart that a load's eight 16-byte
+// pieces (two tokens') fall into different banks.
 template <bool kFP8>
-__host__ __device__ constexpr int x_pitch(int H) {   // bytes; tokens 16 or 64 bytes apart in the banks
-  return 2 * H + (kFP8 ? 16 : 64);
-}
+__host__ __device__ constexpr int x_pitch(int H) { return 2 * H + (kFP8 ? 16 : 64); }
 
-template <bool kFP8, int kGroups, int kDepth>
+template <bool kFP8, int kGroups, int kWarps, int kDepth>
 int up_smem(const FewParams& p) {
   return Routing::bytes(p.T, p.k, p.E) + p.T * x_pitch<kFP8>(p.H) +
-         (kFP8 ? p.H / 128 * kMaxTok * 4 : 0) + kUpWarps * kGroups * 512 +
-         kUpWarps * kDepth * kSlot;
+         (kFP8 ? p.H / 128 * 8 * kGroups * 4 : 0) + 2 * kWarps * kGroups * 512 +
+         kWarps * kDepth * kSlot;
 }
 
-template <bool kFP8, int kGroups, int kDepth>
-__global__ void __launch_bounds__(kUpThreads, 1) few_up_kernel(const FewParams p) {
+template <bool kFP8, int kGroups, int kWarps, int kDepth>
+__global__ void __launch_bounds__(kWarps * 32, kWarps == 8 ? 2 : 1) few_up_kernel(const FewParams p) {
   extern __shared__ __align__(16) uint8_t smem[];
   __shared__ int s_n;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
   const Routing r(smem, p.T, p.k, p.E);
   const int pitch = x_pitch<kFP8>(p.H);
   uint8_t* s_x = smem + Routing::bytes(p.T, p.k, p.E);
-  float* s_xs = reinterpret_cast<float*>(s_x + p.T * pitch);            // FP8: [K/128][kMaxTok]
-  float4* s_red = reinterpret_cast<float4*>(s_xs + (kFP8 ? p.H / 128 * kMaxTok : 0));
-  uint8_t* s_ring = reinterpret_cast<uint8_t*>(s_red + kUpWarps * kGroups * 32) +
+  float* s_xs = reinterpret_cast<float*>(s_x + p.T * pitch);            // FP8: [K/128][tokens]
+  float4* s_red = reinterpret_cast<float4*>(s_xs + (kFP8 ? p.H / 128 * 8 * kGroups : 0));
+  uint8_t* s_ring = reinterpret_cast<uint8_t*>(s_red + 2 * kWarps * kGroups * 32) +
                     warp * kDepth * kSlot;
   const uint32_t ring = smem_u32(s_ring);
   pdl_wait();
   pdl_launch_dependents();
 
-  // x into shared memory (a warp per 128 elements of a token)
+  route_tokens(p, r);
+  // x into shared memory, a warp per 128 elements of a token (the warps that do not route first)
   const int blocks = (p.H + 127) / 128;
-  for (int b = warp; b < p.T * blocks; b += kUpWarps) {
+  for (int b = (warp + kWarps - p.T % kWarps) % kWarps; b < p.T * blocks; b += kWarps) {
     const int tok = b / blocks, blk = b - tok * blocks;
     const int at = blk * 128 + lane * 4;
     if (!kFP8 && at >= p.H) continue;
     const uint2 raw = __ldg(reinterpret_cast<const uint2*>(p.x + static_cast<size_t>(tok) * p.H + at));
-    uint2* dst = reinterpret_cast<uint2*>(s_x + tok * pitch + at * 2);
+    uint8_t* row = s_x + tok * pitch;
     if constexpr (kFP8) {
       const float v[4] = {__uint_as_float(raw.x << 16), __uint_as_float(raw.x & 0xffff0000u),
                           __uint_as_float(raw.y << 16), __uint_as_float(raw.y & 0xffff0000u)};
@@ -252,54 +275,60 @@ __global__ void __launch_bounds__(kUpThreads, 1) few_up_kernel(const FewParams p
       for (int o = 16; o > 0; o >>= 1) amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, o));
       float up, down;
       block_scale(amax, up, down);
-      const __half2 lo = __floats2half2_rn(v[0] * up, v[1] * up);
-      const __half2 hi = __floats2half2_rn(v[2] * up, v[3] * up);
-      *dst = make_uint2(*reinterpret_cast<const uint32_t*>(&lo), *reinterpret_cast<const uint32_t*>(&hi));
-      if (lane == 0) s_xs[blk * kMaxTok + tok] = down;
+      *reinterpret_cast<uint2*>(row + at * 2) = halves(v, up);
+      if (lane == 0) s_xs[blk * 8 * kGroups + tok] = down;
     } else {
-      *dst = raw;
+      *reinterpret_cast<uint2*>(row + at * 2) = raw;
     }
   }
   if (kFP8)      // columns of no token
-    for (int i = threadIdx.x; i < blocks * kMaxTok; i += kUpThreads)
-      if (i % kMaxTok >= p.T) s_xs[i] = 0.0f;
-  const int active = route_all(p, r, &s_n);
+    for (int i = threadIdx.x; i < blocks * 8 * kGroups; i += kWarps * 32)
+      if (i % (8 * kGroups) >= p.T) s_xs[i] = 0.0f;
+  const int active = route_join(p, r, &s_n);
 
-  // Warps that share a unit: as many as it takes to give every warp of the grid work.
   const int per_expert = p.I / 8;
   const int units = active * per_expert;
   const int row_bytes = p.H * (kFP8 ? 1 : 2);
-  const int nkb = row_bytes / 128;
+  const int nkb = row_bytes / 128, steps = (nkb + 1) / 2;
+  // Warps that share a unit: the number that takes the fewest steps of the slowest warp, a step
+  // more for every join.
   int share = 1;
-  while (share < 16 && units * share < static_cast<int>(gridDim.x) * kUpWarps && 2 * share <= nkb)
-    share *= 2;
+  for (int n = 1, best = 0x7fffffff; n <= kWarps && n <= steps; n *= 2) {
+    const int groups = gridDim.x * (kWarps / n);
+    const int cost = (units + groups - 1) / groups * ((steps + n - 1) / n + (n > 1));
+    if (cost < best) best = cost, share = n;
+  }
   const int sub = warp & (share - 1);
-  const int stride = gridDim.x * (kUpWarps / share);
-  const int first = blockIdx.x * (kUpWarps / share) + warp / share;
+  const int stride = gridDim.x * (kWarps / share);
+  const int first = blockIdx.x * (kWarps / share) + warp / share;
+  const int64_t to_up = static_cast<int64_t>(p.I) * row_bytes;     // from a gate row to its up row
 
-  // the copies run kDepth steps ahead of the products, over the units' boundaries
-  int lu = first, lkb = sub;
-  const uint8_t* lo = nullptr;
-  const float* ls = nullptr;
+  // the copies run kDepth - 1 steps ahead of the products, over the units' boundaries
+  int lu = first, ls = sub;
+  const uint8_t* src = nullptr;             // the lane's piece of the first rows
+  const float* scale = nullptr;             // lanes 0, 1: the gate rows' two; 2, 3: the up rows'
   auto aim = [&]() {
-    if (lu >= units) return;
     const int a = lu / per_expert, i0 = (lu - a * per_expert) * 8;
-    const int64_t e = r.active[a];
-    lo = p.w + (e * 2 * p.I + i0 + g) * row_bytes + t * 16;
-    if constexpr (kFP8) ls = p.w_scales + (e * 2 * p.I + i0) / 128 * nkb;
+    const int64_t row = static_cast<int64_t>(r.active[a]) * 2 * p.I + i0;
+    src = p.w + (row + (lane >> 4)) * row_bytes + (lane & 15) * 16 + sub * kStepBytes;
+    if constexpr (kFP8)
+      scale = p.w_scales + (row + (lane & 2 ? p.I : 0)) / 128 * nkb + 2 * sub + (lane & 1);
   };
-  aim();
+  if (lu < units) aim();
   auto copy = [&](int slot) {
     if (lu < units) {
-      const uint32_t d = ring + slot * kSlot;
-      const uint8_t* src = lo + lkb * 128;
-      copy_step(d, src, src + static_cast<int64_t>(p.I) * row_bytes);
-      if (kFP8 && lane < 2) cp_async4(d + kStep + lane * 4, ls + lane * (p.I / 128 * nkb) + lkb);
-      lkb += share;
-      if (lkb >= nkb) {
-        lkb = sub;
+      copy_step(ring + slot * kSlot, src, row_bytes, to_up, 2 * ls + 1 < nkb);
+      src += share * kStepBytes;
+      if constexpr (kFP8) {
+        if (lane < 4 && 2 * ls + (lane & 1) < nkb)
+          cp_async4(ring + slot * kSlot + kSlotBytes + lane * 4, scale);
+        scale += 2 * share;
+      }
+      ls += share;
+      if (ls >= steps) {
+        ls = sub;
         lu += stride;
-        aim();
+        if (lu < units) aim();
       }
     }
     cp_commit();
@@ -307,69 +336,72 @@ __global__ void __launch_bounds__(kUpThreads, 1) few_up_kernel(const FewParams p
 #pragma unroll
   for (int d = 0; d < kDepth - 1; ++d) copy(d);
 
-  int slot = 0;
+  // the columns' tokens (those of no token read token 0's row: their sums are not used)
+  const uint8_t* row[kGroups];
+#pragma unroll
+  for (int n = 0; n < kGroups; ++n) row[n] = s_x + (8 * n + g < p.T ? 8 * n + g : 0) * pitch;
+  const float* xs = s_xs + 2 * t;
+  const uint32_t half0 = piece_at(g, t), half1 = piece_at(g, 4 + t);
+  int slot = 0, parity = 0;
   for (int u = first; u < units; u += stride) {
     const int a = u / per_expert, i0 = (u - a * per_expert) * 8;
-    const int e = r.active[a];
-    const uint32_t tokens = r.tokens[e];
+    const uint32_t tokens = r.tokens_of(a);
     float acc[kGroups][4];
 #pragma unroll
     for (int n = 0; n < kGroups; ++n)
 #pragma unroll
       for (int i = 0; i < 4; ++i) acc[n][i] = 0.0f;
-    for (int kb = sub; kb < nkb; kb += share) {
-      __syncwarp();                         // the slot's scales have been read by all lanes
+    for (int s = sub; s < steps; s += share) {
+      __syncwarp();                         // the slot to be filled has been read by all lanes
       copy(slot == 0 ? kDepth - 1 : slot - 1);
       cp_wait<kDepth - 1>();
       __syncwarp();
-      const uint8_t* s = s_ring + slot * kSlot;
-      Weights<kFP8> w;
-      w.load(s, lane);
-      float gs = 1.0f, us = 1.0f;
-      if constexpr (kFP8) {
-        gs = *reinterpret_cast<const float*>(s + kStep);
-        us = *reinterpret_cast<const float*>(s + kStep + 4);
-      }
+      const uint8_t* q = s_ring + slot * kSlot;
+      const float* sc = reinterpret_cast<const float*>(q + kSlotBytes);
 #pragma unroll
-      for (int n = 0; n < kGroups; ++n) {
-        if (kGroups > 1 && ((tokens >> (8 * n)) & 255u) == 0) continue;
-        const int tok = 8 * n + g;
-        uint4 b[4];
-        load_b<kFP8>(b, s_x + (tok < p.T ? tok : 0) * pitch + kb * (kFP8 ? 256 : 128), t, true);
-        if constexpr (kFP8) {
-          float c[4] = {0.0f, 0.0f, 0.0f, 0.0f};
-          w.multiply(c, b);
-          const float2 xs = *reinterpret_cast<const float2*>(s_xs + kb * kMaxTok + 8 * n + 2 * t);
-          acc[n][0] = fmaf(c[0], gs * xs.x, acc[n][0]);
-          acc[n][1] = fmaf(c[1], gs * xs.y, acc[n][1]);
-          acc[n][2] = fmaf(c[2], us * xs.x, acc[n][2]);
-          acc[n][3] = fmaf(c[3], us * xs.y, acc[n][3]);
-        } else {
-          w.multiply(acc[n], b);
+      for (int b = 0; b < 2; ++b) {
+        const int kb = 2 * s + b;
+        if (b == 1 && kb >= nkb) break;
+        Block<kFP8> w;
+        w.load(q + half0 + b * 128, q + half1 + b * 128);
+#pragma unroll
+        for (int n = 0; n < kGroups; ++n) {
+          if (kGroups > 1 && ((tokens >> (8 * n)) & 255u) == 0) continue;
+          if constexpr (kFP8) {
+            float c[4] = {0.0f, 0.0f, 0.0f, 0.0f};
+            w.multiply(c, row[n] + kb * 256, t, true);
+            const float2 x2 = *reinterpret_cast<const float2*>(xs + kb * 8 * kGroups + 8 * n);
+            acc[n][0] = fmaf(c[0], sc[b] * x2.x, acc[n][0]);
+            acc[n][1] = fmaf(c[1], sc[b] * x2.y, acc[n][1]);
+            acc[n][2] = fmaf(c[2], sc[2 + b] * x2.x, acc[n][2]);
+            acc[n][3] = fmaf(c[3], sc[2 + b] * x2.y, acc[n][3]);
+          } else {
+            w.multiply(acc[n], row[n] + kb * 128, t, true);
+          }
         }
       }
       slot = slot == kDepth - 1 ? 0 : slot + 1;
     }
-    // the sharing warps' sums meet in the first of them
+    // the sharing warps' sums meet in the first of them; two buffers in turn, so one barrier a unit
     if (share > 1) {
-      const int bar = 1 + warp / share;
+      float4* red = s_red + parity * kWarps * kGroups * 32;
+      parity ^= 1;
       if (sub > 0)
 #pragma unroll
         for (int n = 0; n < kGroups; ++n)
-          s_red[(warp * kGroups + n) * 32 + lane] =
+          red[(warp * kGroups + n) * 32 + lane] =
               make_float4(acc[n][0], acc[n][1], acc[n][2], acc[n][3]);
-      asm volatile("bar.sync %0, %1;" ::"r"(bar), "r"(share * 32) : "memory");
+      asm volatile("bar.sync %0, %1;" ::"r"(1 + warp / share), "r"(share * 32) : "memory");
       if (sub == 0)
         for (int j = 1; j < share; ++j)
 #pragma unroll
           for (int n = 0; n < kGroups; ++n) {
-            const float4 v = s_red[((warp + j) * kGroups + n) * 32 + lane];
+            const float4 v = red[((warp + j) * kGroups + n) * 32 + lane];
             acc[n][0] += v.x;
             acc[n][1] += v.y;
             acc[n][2] += v.z;
             acc[n][3] += v.w;
           }
-      asm volatile("bar.sync %0, %1;" ::"r"(bar), "r"(share * 32) : "memory");
     }
     if (sub != 0) continue;
 #pragma unroll
@@ -378,74 +410,81 @@ __global__ void __launch_bounds__(kUpThreads, 1) few_up_kernel(const FewParams p
       for (int i = 0; i < 2; ++i) {
         const int tok = 8 * n + 2 * t + i;
         if (((tokens >> tok) & 1u) == 0) continue;
-        int j = 0;
-        while (j < p.k - 1 && r.ids[tok * p.k + j] != e) ++j;
+        const int route = tok * p.k + r.choice[a * kMaxTok + tok];
         const float gate = acc[n][i], up = acc[n][2 + i];
-        p.h[static_cast<size_t>(tok * p.k + j) * p.I + i0 + g] =
-            __fdiv_rn(gate, 1.0f + exp_ieee(-gate)) * up;
+        p.h[static_cast<size_t>(route) * p.I + i0 + g] = __fdiv_rn(gate, 1.0f + exp_ieee(-gate)) * up;
       }
   }
 }
 
 // ----------------------------------------------------------------------------
-// Down: out[t, n] = sum over t's experts of weight * (w2[e, n, :] . h).
+// Down: out[t, n] = sum over t's experts of weight * (w2[e, n, :] . h).  A staged row is one
+// block of one token's h, times its weight: FP8 as binary16 scaled by a power of two (11 bits),
+// BF16 in two terms (16 bits).
 template <bool kFP8>
-constexpr int h_pitch() {                   // bytes; neighbouring rows in other banks
-  return kFP8 ? 272 : 320;
+constexpr int h_pitch() {                   // bytes; as x_pitch
+  return kFP8 ? 256 + 16 : 2 * 128 + 64;
 }
 
-template <bool kFP8, int kDepth>
+template <bool kFP8, int kGroups, int kWarps, int kDepth>
 int down_smem(const FewParams& p) {
-  return Routing::bytes(p.T, p.k, p.E) + kHRows * (h_pitch<kFP8>() + 4 + 8) +
-         kDownRows * kMaxTok * 4 + kDownWarps * kDepth * kSlot;
+  return Routing::bytes(p.T, p.k, p.E) + p.h_rows * (h_pitch<kFP8>() + 4 + 4 + 8) +
+         kWarps / 8 * kDownRows * 8 * kGroups * 4 + kWarps * kDepth * kSlot;
 }
 
-template <bool kFP8, int kGroups, int kDepth>
-__global__ void __cluster_dims__(kCluster, 1, 1) __launch_bounds__(kDownThreads, 2)
+template <bool kFP8, int kGroups, int kWarps, int kDepth>
+__global__ void __launch_bounds__(kWarps * 32, kWarps == 8 ? 2 : 1)
     few_down_kernel(const FewParams p) {
   extern __shared__ __align__(16) uint8_t smem[];
   __shared__ int s_n;
+  constexpr int kCols = 8 * kGroups;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
   const Routing r(smem, p.T, p.k, p.E);
   uint8_t* s_h = smem + Routing::bytes(p.T, p.k, p.E);
-  float* s_hs = reinterpret_cast<float*>(s_h + kHRows * h_pitch<kFP8>());
-  int2* s_step = reinterpret_cast<int2*>(s_hs + kHRows);        // (active expert, first row)
-  float* s_part = reinterpret_cast<float*>(s_step + kHRows);    // [row][token]
-  uint8_t* s_ring = reinterpret_cast<uint8_t*>(s_part + kDownRows * kMaxTok) + warp * kDepth * kSlot;
+  float* s_hs = reinterpret_cast<float*>(s_h + p.h_rows * h_pitch<kFP8>());   // FP8: rows' scales
+  int* s_what = reinterpret_cast<int*>(s_hs + p.h_rows);        // what a row holds: route, block
+  int2* s_step = reinterpret_cast<int2*>(s_what + p.h_rows);    // a block: (active expert, first row)
+  float* s_part = reinterpret_cast<float*>(s_step + p.h_rows);  // [row][token]
+  uint8_t* s_ring = reinterpret_cast<uint8_t*>(s_part + kWarps / 8 * kDownRows * kCols) + warp * kDepth * kSlot;
   const uint32_t ring = smem_u32(s_ring);
-  const int rank = blockIdx.x % kCluster;
-  const int n0 = blockIdx.x / kCluster * kDownRows + warp * 16;
+  const int cluster = p.cluster, rank = blockIdx.x % cluster;
+  const int tile = warp & 7, part = warp >> 3;                  // 16 warps: two for each row tile
+  const int n0 = blockIdx.x / cluster * kDownRows + tile * 16;
   const bool idle = n0 >= p.H;                                  // (H is a multiple of 16)
-  const int active = route_all(p, r, &s_n);
+  route_tokens(p, r);
+  const int active = route_join(p, r, &s_n);
 
-  // this CTA's share of the steps (expert by expert, 128 bytes of k each)
+  // this CTA's share of the steps (two blocks each, expert by expert)
   const int row_bytes = p.I * (kFP8 ? 1 : 2);
-  const int nkb = row_bytes / 128;
-  const int64_t steps = static_cast<int64_t>(active) * nkb;
-  const int s0 = static_cast<int>(steps * rank / kCluster);
-  const int s1 = static_cast<int>(steps * (rank + 1) / kCluster);
+  const int nkb = row_bytes / 128, per = (nkb + 1) / 2;
+  const int64_t all = static_cast<int64_t>(active) * per;
+  const int s0 = static_cast<int>(all * rank / cluster);
+  const int s1 = static_cast<int>(all * (rank + 1) / cluster);
 
-  int ls = s0, la = s0 / nkb, lkb = s0 - la * nkb;
-  const uint8_t* lo = nullptr;
-  const float* lsc = nullptr;
+  constexpr int kParts = kWarps / 8;        // warps that take a row tile's steps in turn
+  int ls = s0 + part, la = ls / per, lp = ls - la * per;
+  const uint8_t* src = nullptr;             // the lane's piece of the first rows
+  const float* scale = nullptr;             // lanes 0, 1: the step's two
   auto aim = [&]() {
-    if (ls >= s1) return;
-    const int64_t e = r.active[la];
-    lo = p.w2 + (e * p.H + n0 + g) * row_bytes + t * 16;
-    if constexpr (kFP8) lsc = p.w2_scales + (e * (p.H / 128) + n0 / 128) * nkb;
+    const int64_t row = static_cast<int64_t>(r.active[la]) * p.H + n0;
+    src = p.w2 + (row + (lane >> 4)) * row_bytes + (lane & 15) * 16 + lp * kStepBytes;
+    if constexpr (kFP8) scale = p.w2_scales + row / 128 * nkb + 2 * lp + (lane & 1);
   };
-  if (!idle) aim();
+  if (!idle && ls < s1) aim();
   auto copy = [&](int slot) {
     if (ls < s1 && !idle) {
-      const uint32_t d = ring + slot * kSlot;
-      const uint8_t* src = lo + lkb * 128;
-      copy_step(d, src, src + 8 * static_cast<int64_t>(row_bytes));
-      if (kFP8 && lane == 0) cp_async4(d + kStep, lsc + lkb);
-      ++ls;
-      if (++lkb == nkb) {
-        lkb = 0;
-        ++la;
-        aim();
+      copy_step(ring + slot * kSlot, src, row_bytes, 8 * static_cast<int64_t>(row_bytes), 2 * lp + 1 < nkb);
+      src += kParts * kStepBytes;
+      if constexpr (kFP8) {
+        if (lane < 2 && 2 * lp + lane < nkb)
+          cp_async4(ring + slot * kSlot + kSlotBytes + lane * 4, scale);
+        scale += 2 * kParts;
+      }
+      ls += kParts;
+      lp += kParts;
+      if (lp >= per) {
+        while (lp >= per) lp -= per, ++la;
+        if (ls < s1) aim();
       }
     }
     cp_commit();
@@ -460,94 +499,116 @@ __global__ void __cluster_dims__(kCluster, 1, 1) __launch_bounds__(kDownThreads,
   for (int n = 0; n < kGroups; ++n)
 #pragma unroll
     for (int i = 0; i < 4; ++i) acc[n][i] = 0.0f;
+  const uint32_t half0 = piece_at(g, t), half1 = piece_at(g, 4 + t);
   int slot = 0;
   for (int s = s0; s < s1;) {
-    // the next steps whose rows of h (one per token and step) fit
-    int count = 0, rows = 0;
+    // the next steps whose rows of h (one per token and block) fit; s_step holds their blocks, two
+    // a step
+    int count = 0, rows = 0, used = 0;
     while (s + count < s1) {
-      const int a = (s + count) / nkb, kb = (s + count) - a * nkb;
-      const int n = __popc(r.tokens[r.active[a]]);
-      const int take = min(min(nkb - kb, s1 - s - count), (kHRows - rows) / n);
+      const int a = (s + count) / per, p0 = (s + count) - a * per;
+      const uint32_t tokens = r.tokens_of(a);
+      const int n = __popc(tokens);
+      // (a step counts two blocks here, also the last of an odd number)
+      const int take = min(min(per - p0, s1 - s - count), min(p.h_rows - rows, p.h_rows - used) / (2 * n));
       if (take == 0) break;
-      for (int i = threadIdx.x; i < take; i += kDownThreads) s_step[count + i] = make_int2(a, rows + i * n);
+      const int blocks = min(2 * take, nkb - 2 * p0);
+      for (int i = threadIdx.x; i < 2 * take; i += kWarps * 32) s_step[used + i] = make_int2(a, rows + i * n);
+      for (int i = threadIdx.x; i < blocks * n; i += kWarps * 32) {
+        const int tok = __fns(tokens, 0, i % n + 1);
+        s_what[rows + i] = (2 * p0 + i / n) << 16 | (tok * p.k + r.choice[a * kMaxTok + tok]);
+      }
       count += take;
-      rows += take * n;
+      used += 2 * take;
+      rows += blocks * n;
     }
     __syncthreads();
-    // h times its route's weight, in the MMA's type
-    for (int i = warp; i < count; i += kDownWarps) {
-      const int2 at = s_step[i];
-      const int e = r.active[at.x], kb = s + i - at.x * nkb;
-      uint32_t m = r.tokens[e];
-      for (int row = at.y; m != 0; ++row, m &= m - 1) {
-        const int tok = __ffs(m) - 1;
-        int j = 0;
-        while (j < p.k - 1 && r.ids[tok * p.k + j] != e) ++j;
-        const int route = tok * p.k + j;
-        const float weight = r.weights[route];
-        const float* src = p.h + static_cast<size_t>(route) * p.I;
-        uint8_t* dst = s_h + row * h_pitch<kFP8>();
+    // h times its route's weight, in the MMA's types; four rows' loads in flight
+    for (int i0 = warp; i0 < rows; i0 += 4 * kWarps) {
+      float v[4][4];
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        const int i = i0 + j * kWarps;
+        if (i >= rows) break;
+        const float* src = p.h + static_cast<size_t>(s_what[i] & 0xffff) * p.I;
+        const int kb = s_what[i] >> 16;
         if constexpr (kFP8) {
-          float4 v = __ldcg(reinterpret_cast<const float4*>(src + kb * 128) + lane);
-          v.x *= weight, v.y *= weight, v.z *= weight, v.w *= weight;
-          float amax = fmaxf(fmaxf(fabsf(v.x), fabsf(v.y)), fmaxf(fabsf(v.z), fabsf(v.w)));
+          const float4 f = __ldcg(reinterpret_cast<const float4*>(src + kb * 128) + lane);
+          v[j][0] = f.x, v[j][1] = f.y, v[j][2] = f.z, v[j][3] = f.w;
+        } else {
+          const float2 f = __ldcg(reinterpret_cast<const float2*>(src + kb * 64) + lane);
+          v[j][0] = f.x, v[j][1] = f.y;
+        }
+      }
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        const int i = i0 + j * kWarps;
+        if (i >= rows) break;
+        const float weight = r.weights[s_what[i] & 0xffff];
+        if constexpr (kFP8) {
+          float amax = 0.0f;
+#pragma unroll
+          for (int e = 0; e < 4; ++e) {
+            v[j][e] *= weight;
+            amax = fmaxf(amax, fabsf(v[j][e]));
+          }
 #pragma unroll
           for (int o = 16; o > 0; o >>= 1) amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, o));
           float up, down;
           block_scale(amax, up, down);
-          const __half2 a = __floats2half2_rn(v.x * up, v.y * up);
-          const __half2 b = __floats2half2_rn(v.z * up, v.w * up);
-          reinterpret_cast<uint2*>(dst)[lane] =
-              make_uint2(*reinterpret_cast<const uint32_t*>(&a), *reinterpret_cast<const uint32_t*>(&b));
-          if (lane == 0) s_hs[row] = down;
+          *reinterpret_cast<uint2*>(s_h + i * h_pitch<kFP8>() + lane * 8) = halves(v[j], up);
+          if (lane == 0) s_hs[i] = down;
         } else {
-          // two bf16 terms: 16 bits of h
-          float2 v = __ldcg(reinterpret_cast<const float2*>(src + kb * 64) + lane);
-          v.x *= weight, v.y *= weight;
-          const __nv_bfloat162 hi = __floats2bfloat162_rn(v.x, v.y);
+          const float x = v[j][0] * weight, y = v[j][1] * weight;
+          const __nv_bfloat162 hi = __floats2bfloat162_rn(x, y);
           const float2 back = __bfloat1622float2(hi);
-          const __nv_bfloat162 rest = __floats2bfloat162_rn(v.x - back.x, v.y - back.y);
-          reinterpret_cast<uint32_t*>(dst)[lane] = *reinterpret_cast<const uint32_t*>(&hi);
-          reinterpret_cast<uint32_t*>(dst + 128)[lane] = *reinterpret_cast<const uint32_t*>(&rest);
+          const __nv_bfloat162 rest = __floats2bfloat162_rn(x - back.x, y - back.y);
+          uint32_t* dst = reinterpret_cast<uint32_t*>(s_h + i * h_pitch<kFP8>()) + lane;
+          dst[0] = *reinterpret_cast<const uint32_t*>(&hi);
+          dst[32] = *reinterpret_cast<const uint32_t*>(&rest);
         }
       }
     }
     __syncthreads();
     if (!idle) {
-      for (int i = 0; i < count; ++i) {
+      // (a row tile's warps take every kParts-th step of the share, counted from its start)
+      for (int i = (part + kParts - (s - s0) % kParts) % kParts; i < count; i += kParts) {
+        const int a = s_step[2 * i].x;
+        const uint32_t tokens = r.tokens_of(a);
+        const bool both = 2 * (s + i - a * per) + 1 < nkb;
         __syncwarp();
         copy(slot == 0 ? kDepth - 1 : slot - 1);
         cp_wait<kDepth - 1>();
         __syncwarp();
-        const uint8_t* sl = s_ring + slot * kSlot;
-        Weights<kFP8> w;
-        w.load(sl, lane);
-        const int2 at = s_step[i];
-        const uint32_t tokens = r.tokens[r.active[at.x]];
+        const uint8_t* q = s_ring + slot * kSlot;
+        const float* sc = reinterpret_cast<const float*>(q + kSlotBytes);
 #pragma unroll
-        for (int n = 0; n < kGroups; ++n) {
-          if (kGroups > 1 && ((tokens >> (8 * n)) & 255u) == 0) continue;
-          auto row_of = [&](int tok) { return at.y + __popc(tokens & ((1u << tok) - 1u)); };
-          const int tok = 8 * n + g;
-          const bool there = (tokens >> tok) & 1u;
-          const uint8_t* row = s_h + (there ? row_of(tok) : at.y) * h_pitch<kFP8>();
-          uint4 b[4];
-          load_b<kFP8>(b, row, t, there);
-          if constexpr (kFP8) {
-            const float ws = *reinterpret_cast<const float*>(sl + kStep);
-            float c[4] = {0.0f, 0.0f, 0.0f, 0.0f};
-            w.multiply(c, b);
-            const int t0 = 8 * n + 2 * t;
-            const float h0 = ((tokens >> t0) & 1u) ? s_hs[row_of(t0)] * ws : 0.0f;
-            const float h1 = ((tokens >> (t0 + 1)) & 1u) ? s_hs[row_of(t0 + 1)] * ws : 0.0f;
-            acc[n][0] = fmaf(c[0], h0, acc[n][0]);
-            acc[n][1] = fmaf(c[1], h1, acc[n][1]);
-            acc[n][2] = fmaf(c[2], h0, acc[n][2]);
-            acc[n][3] = fmaf(c[3], h1, acc[n][3]);
-          } else {
-            w.multiply(acc[n], b);
-            load_b<kFP8>(b, row + 128, t, there);
-            w.multiply(acc[n], b);
+        for (int b = 0; b < 2; ++b) {
+          if (b == 1 && !both) break;
+          Block<kFP8> w;
+          w.load(q + half0 + b * 128, q + half1 + b * 128);
+          const int base = s_step[2 * i + b].y;
+#pragma unroll
+          for (int n = 0; n < kGroups; ++n) {
+            if (kGroups > 1 && ((tokens >> (8 * n)) & 255u) == 0) continue;
+            auto row_of = [&](int tok) { return base + __popc(tokens & ((1u << tok) - 1u)); };
+            const int tok = 8 * n + g;
+            const bool there = (tokens >> tok) & 1u;
+            const uint8_t* row = s_h + row_of(tok) * h_pitch<kFP8>();
+            if constexpr (kFP8) {
+              float c[4] = {0.0f, 0.0f, 0.0f, 0.0f};
+              w.multiply(c, row, t, there);
+              const int t0 = 8 * n + 2 * t;
+              const float h0 = ((tokens >> t0) & 1u) ? s_hs[row_of(t0)] * sc[b] : 0.0f;
+              const float h1 = ((tokens >> (t0 + 1)) & 1u) ? s_hs[row_of(t0 + 1)] * sc[b] : 0.0f;
+              acc[n][0] = fmaf(c[0], h0, acc[n][0]);
+              acc[n][1] = fmaf(c[1], h1, acc[n][1]);
+              acc[n][2] = fmaf(c[2], h0, acc[n][2]);
+              acc[n][3] = fmaf(c[3], h1, acc[n][3]);
+            } else {
+              w.multiply(acc[n], row, t, there);
+              w.multiply(acc[n], row + 128, t, there);
+            }
           }
         }
         slot = slot == kDepth - 1 ? 0 : slot + 1;
@@ -556,28 +617,36 @@ __global__ void __cluster_dims__(kCluster, 1, 1) __launch_bounds__(kDownThreads,
     s += count;
     __syncthreads();                        // before the next rows overwrite these
   }
-  // the shares meet: rank r adds rows 16 r .. 16 r + 15, in the ranks' order
+  // the shares meet, in the order of ranks and parts: rank r adds its part of the rows
 #pragma unroll
   for (int n = 0; n < kGroups; ++n)
 #pragma unroll
     for (int i = 0; i < 4; ++i)
-      s_part[(warp * 16 + g + 8 * (i >> 1)) * kMaxTok + 8 * n + 2 * t + (i & 1)] = acc[n][i];
+      s_part[(part * kDownRows + tile * 16 + g + 8 * (i >> 1)) * kCols + 8 * n + 2 * t + (i & 1)] = acc[n][i];
   asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory");
   asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory");
-  const int row = threadIdx.x & 15, tok = threadIdx.x >> 4;
-  const int n = blockIdx.x / kCluster * kDownRows + rank * 16 + row;
-  if (tok < p.T && n < p.H) {
-    const uint32_t mine = smem_u32(s_part + (rank * 16 + row) * kMaxTok + tok);
-    float part[kCluster];
+  const int rows = kDownRows / cluster;
+  for (int i = threadIdx.x; i < rows * p.T; i += kWarps * 32) {
+    const int tok = i / rows, row = rank * rows + i - tok * rows;
+    const int n = blockIdx.x / cluster * kDownRows + row;
+    if (n >= p.H) continue;
+    float v[kCluster * kParts];
 #pragma unroll
-    for (int c = 0; c < kCluster; ++c) {
-      uint32_t at;
-      asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(at) : "r"(mine), "r"(c));
-      asm volatile("ld.shared::cluster.f32 %0, [%1];" : "=f"(part[c]) : "r"(at));
-    }
-    float sum = part[0];
+    for (int c = 0; c < kCluster; ++c)
 #pragma unroll
-    for (int c = 1; c < kCluster; ++c) sum += part[c];
+      for (int q = 0; q < kParts; ++q) {
+        float& x = v[c * kParts + q];
+        x = 0.0f;
+        if (c >= cluster) continue;
+        uint32_t at;
+        asm volatile("mapa.shared::cluster.u32 %0, %1, %2;"
+                     : "=r"(at)
+                     : "r"(smem_u32(s_part + (q * kDownRows + row) * kCols + tok)), "r"(c));
+        asm volatile("ld.shared::cluster.f32 %0, [%1];" : "=f"(x) : "r"(at));
+      }
+    float sum = v[0];
+#pragma unroll
+    for (int c = 1; c < kCluster * kParts; ++c) sum += v[c];
     p.out[static_cast<size_t>(tok) * p.H + n] = __float2bfloat16_rn(sum);
   }
   asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory");
@@ -585,35 +654,57 @@ __global__ void __cluster_dims__(kCluster, 1, 1) __launch_bounds__(kDownThreads,
 }
 
 constexpr int kMaxSmem = 226 * 1024;       // 227 KB a CTA, less the static part
-constexpr int kDownDepth = 4;
 
-template <bool kFP8, int kGroups, int kDepth>
+template <bool kFP8, int kGroups, int kWarps, int kDepth>
 cudaError_t launch_up(const FewParams& p, int sms, cudaStream_t stream) {
-  const int bytes = up_smem<kFP8, kGroups, kDepth>(p);
-  cudaError_t e = cudaFuncSetAttribute(few_up_kernel<kFP8, kGroups, kDepth>,
-                                       cudaFuncAttributeMaxDynamicSharedMemorySize, kMaxSmem);
+  auto* kernel = few_up_kernel<kFP8, kGroups, kWarps, kDepth>;
+  cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kMaxSmem);
+  if (e == cudaSuccess) e = prefer_max_shared(kernel);
   if (e != cudaSuccess) return e;
   cudaLaunchAttribute attr[1];
-  cudaLaunchConfig_t cfg = make_cfg(dim3(sms), dim3(kUpThreads), stream, true, attr);
-  cfg.dynamicSmemBytes = bytes;
-  return cudaLaunchKernelEx(&cfg, few_up_kernel<kFP8, kGroups, kDepth>, p);
+  cudaLaunchConfig_t cfg = make_cfg(dim3(sms), dim3(kWarps * 32), stream, true, attr);
+  cfg.dynamicSmemBytes = up_smem<kFP8, kGroups, kWarps, kDepth>(p);
+  return cudaLaunchKernelEx(&cfg, kernel, p);
+}
+
+template <bool kFP8, int kGroups, int kWarps, int kDepth>
+cudaError_t launch_down(const FewParams& p, cudaStream_t stream) {
+  auto* kernel = few_down_kernel<kFP8, kGroups, kWarps, kDepth>;
+  cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kMaxSmem);
+  if (e == cudaSuccess) e = prefer_max_shared(kernel);
+  if (e != cudaSuccess) return e;
+  cudaLaunchAttribute attr[2];
+  cudaLaunchConfig_t cfg = make_cfg(dim3((p.H + kDownRows - 1) / kDownRows * p.cluster),
+                                    dim3(kWarps * 32), stream, true, attr);
+  attr[1].id = cudaLaunchAttributeClusterDimension;
+  attr[1].val.clusterDim.x = p.cluster;
+  attr[1].val.clusterDim.y = 1;
+  attr[1].val.clusterDim.z = 1;
+  cfg.numAttrs = 2;
+  cfg.dynamicSmemBytes = down_smem<kFP8, kGroups, kWarps, kDepth>(p);
+  return cudaLaunchKernelEx(&cfg, kernel, p);
 }
 
 template <bool kFP8, int kGroups>
-cudaError_t launch_few(const FewParams& p, int sms, cudaStream_t stream) {
-  // four steps ahead, or two where x takes the room (above 12 tokens of 4096, say)
-  cudaError_t e = up_smem<kFP8, kGroups, 4>(p) <= kMaxSmem
-                      ? launch_up<kFP8, kGroups, 4>(p, sms, stream)
-                      : launch_up<kFP8, kGroups, 2>(p, sms, stream);
+cudaError_t launch_few(FewParams p, int sms, cudaStream_t stream) {
+  // 8 warps an SM leave room for the down kernel's CTAs beside the up kernel's, which pays where the
+  // work is small; 16 stream faster.  x takes what room the rings leave.
+  const int64_t routed = static_cast<int64_t>(Routing::most(p.T, p.k, p.E)) * 2 * p.I * p.H * (kFP8 ? 1 : 2);
+  const bool small = routed <= (32ll << 20);
+  cudaError_t e;
+  if (!small && up_smem<kFP8, kGroups, 16, 2>(p) <= kMaxSmem)
+    e = launch_up<kFP8, kGroups, 16, 2>(p, sms, stream);
+  else if (up_smem<kFP8, kGroups, 8, 3>(p) <= kMaxSmem)
+    e = launch_up<kFP8, kGroups, 8, 3>(p, sms, stream);
+  else
+    e = launch_up<kFP8, kGroups, 8, 2>(p, sms, stream);
   if (e != cudaSuccess) return e;
-  e = cudaFuncSetAttribute(few_down_kernel<kFP8, kGroups, kDownDepth>,
-                           cudaFuncAttributeMaxDynamicSharedMemorySize, kMaxSmem);
-  if (e != cudaSuccess) return e;
-  cudaLaunchAttribute attr[1];
-  cudaLaunchConfig_t cfg = make_cfg(dim3((p.H + kDownRows - 1) / kDownRows * kCluster),
-                                    dim3(kDownThreads), stream, true, attr);
-  cfg.dynamicSmemBytes = down_smem<kFP8, kDownDepth>(p);
-  return cudaLaunchKernelEx(&cfg, few_down_kernel<kFP8, kGroups, kDownDepth>, p);
+  // CTAs for one round over the SMs (those that a cluster of this size can use)
+  const int chunks = (p.H + kDownRows - 1) / kDownRows;
+  p.cluster = kCluster;
+  while (p.cluster > 1 && chunks * p.cluster > sms) p.cluster /= 2;
+  return small ? launch_down<kFP8, kGroups, 8, 3>(p, stream)
+               : launch_down<kFP8, kGroups, 16, 2>(p, stream);
 }
 
 }  // namespace
@@ -644,6 +735,7 @@ cudaError_t launch_few_experts(const moe_forward_args& f, void* out, float* h, C
     p.k = f.top_k;
     p.softcap = f.softcap;
     p.renorm = f.renorm;
+    p.h_rows = p.T <= 4 ? 32 : 64;
     cudaError_t e;
     if (fp8)
       e = p.T <= 8 ? launch_few<true, 1>(p, num_sms, stream) : launch_few<true, 2>(p, num_sms, stream);

@@ -54,7 +54,7 @@ struct Share {
 };
 
 template <typename T, int kPer, bool kProbs>
-__global__ void __launch_bounds__(kLThreads, kPer <= 16 ? 3 : kPer <= 32 ? 2 : 1)
+__global__ void __launch_bounds__(kLThreads, kPer <= 8 ? 3 : kPer <= 32 ? 2 : 1)
     logits_kernel(const LogitsParams<T> p) {
   extern __shared__ uint32_t s_count[];     // [part], then the biases' tokens and values
   __shared__ Share s_share[kLMaxCluster];   // every CTA of the cluster writes its own here
@@ -76,6 +76,17 @@ __global__ void __launch_bounds__(kLThreads, kPer <= 16 ? 3 : kPer <= 32 ? 2 : 1
   for (int j = 0; j < kPer; ++j) {
     const int at = tid + j * kLThreads;
     l[j] = at < n ? load_logit(src + at) : neg_inf();
+  }
+
+  // word j of the mask for this warp's tokens of turn j, by lane j
+  constexpr int kWords = (kPer + 31) / 32;
+  uint32_t words[kWords];
+#pragma unroll
+  for (int w = 0; w < kWords; ++w) {
+    const int at = (warp + (32 * w + lane) * kLWarps) * 32;
+    words[w] = 0xffffffffu;
+    if (p.mask != nullptr && 32 * w + lane < kPer && at < n)
+      words[w] = __ldg(p.mask + b * p.m_sb + i * p.m_si + (v0 + at) / 32);
   }
 
   // the counts
@@ -105,7 +116,14 @@ __global__ void __launch_bounds__(kLThreads, kPer <= 16 ? 3 : kPer <= 32 ? 2 : 1
         prompt = min(max(prompt, 0), len);
       }
       const int32_t* h = p.history + static_cast<int64_t>(b) * p.history_stride;
-      for (int at = tid; at < len; at += kLThreads) count(__ldg(h + at), at < prompt ? 1u : 4u);
+      for (int at = tid; at < len; at += 4 * kLThreads) {
+        int v[4];
+#pragma unroll
+        for (int j = 0; j < 4; ++j)
+          v[j] = at + j * kLThreads < len ? __ldg(h + at + j * kLThreads) : -1;
+#pragma unroll
+        for (int j = 0; j < 4; ++j) count(v[j], at + j * kLThreads < prompt ? 1u : 4u);
+      }
     }
     if (p.draft != nullptr && tid < i) count(__ldg(p.draft + b * (p.m - 1) + tid), 4u);
     for (int at = tid; at < p.biases; at += kLThreads) {
@@ -124,35 +142,44 @@ __global__ void __launch_bounds__(kLThreads, kPer <= 16 ? 3 : kPer <= 32 ? 2 : 1
     if (!(rep > 0.0f)) rep = 1.0f;
     if (!(temp >= 0.0f)) temp = 1.0f;
   }
-  const uint32_t* mask =
-      p.mask == nullptr ? nullptr : p.mask + b * p.m_sb + i * p.m_si + v0 / 32;
 
-  float top = neg_inf();
+  uint32_t biased[kWords] = {};             // bit j: this thread's value j has a bias
 #pragma unroll
   for (int j = 0; j < kPer; ++j) {
     const int at = tid + j * kLThreads;
-    const uint32_t c = counts && at < n ? s_count[at] : 0u;
+    const uint32_t c = counts ? s_count[at] : 0u;
     if (c != 0) {
       if ((c & ~2u) != 0) l[j] = l[j] > 0.0f ? __fdiv_rn(l[j], rep) : l[j] * rep;
       if (c >= 4) l[j] = l[j] - frequency * static_cast<float>(c >> 2) - presence;
+      biased[j / 32] |= ((c >> 1) & 1u) << (j % 32);
     }
-    uint32_t biased = __ballot_sync(0xffffffffu, (c & 2u) != 0);
-    while (biased != 0) {
-      const int who = __ffs(biased) - 1;
-      biased &= biased - 1;
-      const int v = v0 + (at - lane + who);
-      for (int q = 0; q < p.biases; q += 32) {
-        const bool mine = q + lane < p.biases && s_bias_t[q + lane] == v;
-        uint32_t found = __ballot_sync(0xffffffffu, mine);
-        for (; found != 0; found &= found - 1)
-          if (lane == who && l[j] > neg_inf()) l[j] += s_bias_v[q + __ffs(found) - 1];
-      }
-    }
-    if (mask != nullptr && at < n && ((__ldg(mask + (at >> 5)) >> (at & 31)) & 1u) == 0)
-      l[j] = neg_inf();
-    if (!(l[j] >= neg_inf())) l[j] = neg_inf();               // NaN
-    top = fmaxf(top, l[j]);
+    const uint32_t word = __shfl_sync(0xffffffffu, words[j / 32], j % 32);
+    if (((word >> lane) & 1u) == 0 || !(l[j] >= neg_inf())) l[j] = neg_inf();   // (or NaN)
   }
+#pragma unroll
+  for (int w = 0; w < kWords; ++w) {
+    const uint32_t any = __reduce_or_sync(0xffffffffu, biased[w]);
+    if (any == 0) continue;
+#pragma unroll
+    for (int j = 32 * w; j < (kPer < 32 * w + 32 ? kPer : 32 * w + 32); ++j) {
+      if (((any >> (j % 32)) & 1u) == 0) continue;
+      uint32_t lanes = __ballot_sync(0xffffffffu, (biased[w] >> (j % 32)) & 1u);
+      for (; lanes != 0; lanes &= lanes - 1) {
+        const int who = __ffs(lanes) - 1;
+        const int v = v0 + warp * 32 + j * kLThreads + who;
+        for (int q = 0; q < p.biases; q += 32) {
+          const bool mine = q + lane < p.biases && s_bias_t[q + lane] == v;
+          uint32_t found = __ballot_sync(0xffffffffu, mine);
+          for (; found != 0; found &= found - 1)
+            if (lane == who && l[j] > neg_inf()) l[j] += s_bias_v[q + __ffs(found) - 1];
+        }
+      }
+      if (!(l[j] >= neg_inf())) l[j] = neg_inf();
+    }
+  }
+  float top = neg_inf();
+#pragma unroll
+  for (int j = 0; j < kPer; ++j) top = fmaxf(top, l[j]);
   float* out = p.out + b * p.o_sb + i * p.o_si + v0;
   if constexpr (!kProbs) {
 #pragma unroll
