@@ -33,8 +33,7 @@ constexpr int kMaxTok = MOE_FEW_TOKENS;
 constexpr int kStepBytes = 256;           // of each row and step: two blocks of 128
 constexpr int kSlotBytes = 16 * kStepBytes;   // of the ring: a step's rows,
 constexpr int kSlot = kSlotBytes + 16;        // and its blocks' scales
-constexpr int kCluster = 8;               // CTAs that share 128 output rows, at most
-constexpr int kDownRows = 128;
+constexpr int kCluster = 8;               // CTAs that share output rows, at most
 
 __device__ __forceinline__ void cp_async16(uint32_t dst, const void* src) {
   asm volatile("cp.async.cg.shared.global.L2::256B [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
@@ -73,8 +72,16 @@ __device__ __forceinline__ void block_scale(float amax, float& up, float& down) 
   down = __uint_as_float(static_cast<uint32_t>(e - 14 + 127) << 23);
 }
 
+// Four codes as binary16, two in each half.
+__device__ __forceinline__ void codes_to_halves(uint32_t codes, uint32_t& first, uint32_t& second) {
+  asm("{\n\t.reg .b16 lo, hi;\n\tmov.b32 {lo, hi}, %2;\n\t"
+      "cvt.rn.f16x2.e4m3x2 %0, lo;\n\tcvt.rn.f16x2.e4m3x2 %1, hi;\n\t}"
+      : "=r"(first), "=r"(second)
+      : "r"(codes));
+}
+
 // Four values, scaled, as binary16.
-__device__ __forceinline__ uint2 halves(const float (&v)[4], float up) {
+__device__ __forceinline__ uint2 halves(const float* v, float up) {
   const __half2 a = __floats2half2_rn(v[0] * up, v[1] * up), b = __floats2half2_rn(v[2] * up, v[3] * up);
   return make_uint2(*reinterpret_cast<const uint32_t*>(&a), *reinterpret_cast<const uint32_t*>(&b));
 }
@@ -93,79 +100,107 @@ struct FewParams {
   float softcap;
   int renorm;
   int h_rows;                  // rows of h that the down kernel stages at a time
-  int cluster;                 // CTAs that share 128 output rows (1, 2, 4 or 8)
+  int tiles;                   // 16-row tiles of output rows that a down CTA takes (4 or 8),
+  int cluster;                 // and how many CTAs share them (1, 2, 4 or 8)
 };
 
-__device__ __noinline__ void route_one(const float* row, int E, int k, float softcap, int renorm,
-                                       int32_t* ids, float* weights) {
-  if (E <= 64) route_token<2>(row, E, k, softcap, renorm, ids, weights);
-  else if (E <= 256) route_token<8>(row, E, k, softcap, renorm, ids, weights);
-  else route_token<32>(row, E, k, softcap, renorm, ids, weights);
+template <int NPL>
+__device__ __forceinline__ void select_one(const float* z, int E, int k, int renorm, int32_t* ids,
+                                           float* weights) {
+  float mine[NPL];
+#pragma unroll
+  for (int i = 0; i < NPL; ++i) {
+    const int e = (threadIdx.x & 31) + 32 * i;
+    mine[i] = e < E ? z[e] : 0.0f;
+  }
+  route_select<NPL>(mine, E, k, renorm, ids, weights);
+}
+
+__device__ __noinline__ void route_one(const float* z, int E, int k, int renorm, int32_t* ids,
+                                       float* weights) {
+  if (E <= 64) select_one<2>(z, E, k, renorm, ids, weights);
+  else if (E <= 256) select_one<8>(z, E, k, renorm, ids, weights);
+  else select_one<32>(z, E, k, renorm, ids, weights);
 }
 
 // What every CTA knows of the routing, in shared memory.
 struct Routing {
   int32_t* ids;                // [T * k]
   float* weights;              // [T * k]
-  uint32_t* tokens;            // [E] bit t: token t goes there; bits 16 ..: place in `active`
+  uint32_t* tokens;            // [E] bit t: token t goes there
   int32_t* active;             // [min(E, T * k)] the experts that any token goes to, ascending
+  int32_t* before;             // [active + 1] routes to the experts before each of them
+  uint32_t* on;                // [32] bit e % 32 of word e / 32: expert e is active
   uint8_t* choice;             // [active][kMaxTok] which of its k choices that is to the token
   __host__ __device__ static int most(int T, int k, int E) { return E < T * k ? E : T * k; }
   __host__ __device__ static int bytes(int T, int k, int E) {
-    return (8 * T * k + 4 * E + (4 + kMaxTok) * most(T, k, E) + 15) / 16 * 16;
+    return (8 * T * k + 4 * E + (8 + kMaxTok) * most(T, k, E) + 4 + 128 + 15) / 16 * 16;
   }
   __device__ Routing(uint8_t* p, int T, int k, int E)
       : ids(reinterpret_cast<int32_t*>(p)),
         weights(reinterpret_cast<float*>(ids + T * k)),
         tokens(reinterpret_cast<uint32_t*>(weights + T * k)),
         active(reinterpret_cast<int32_t*>(tokens + E)),
-        choice(reinterpret_cast<uint8_t*>(active + most(T, k, E))) {}
-  __device__ uint32_t tokens_of(int a) const { return tokens[active[a]] & 0xffffu; }
+        before(active + most(T, k, E)),
+        on(reinterpret_cast<uint32_t*>(before + most(T, k, E) + 1)),
+        choice(reinterpret_cast<uint8_t*>(on + 32)) {}
+  __device__ uint32_t tokens_of(int a) const { return tokens[active[a]]; }
 };
 
-// Routes this warp's tokens and clears the table; route_join() follows.
-__device__ __forceinline__ void route_tokens(const FewParams& p, const Routing& r) {
+// The tokens' routes: the capped logits by all threads (z: room for T * E numbers), then each
+// token by a warp; route_join() follows.
+__device__ __forceinline__ void route_tokens(const FewParams& p, const Routing& r, float* z) {
   const int warp = threadIdx.x >> 5;
+  for (int i = threadIdx.x; i < p.T * p.E; i += blockDim.x) z[i] = cap_logit(__ldg(p.logits + i), p.softcap);
   for (int e = threadIdx.x; e < p.E; e += blockDim.x) r.tokens[e] = 0;
+  if (threadIdx.x < 32) r.on[threadIdx.x] = 0;
+  __syncthreads();
   for (int t = warp; t < p.T; t += blockDim.x / 32)
-    route_one(p.logits + static_cast<size_t>(t) * p.E, p.E, p.k, p.softcap, p.renorm,
-              r.ids + t * p.k, r.weights + t * p.k);
+    route_one(z + t * p.E, p.E, p.k, p.renorm, r.ids + t * p.k, r.weights + t * p.k);
 }
 
 // The active experts, by all threads; returns how many there are.
-__device__ __forceinline__ int route_join(const FewParams& p, const Routing& r, int* s_n) {
+__device__ __forceinline__ int route_join(const FewParams& p, const Routing& r) {
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int routes = p.T * p.k;
   __syncthreads();
-  for (int i = threadIdx.x; i < p.T * p.k; i += blockDim.x) {
+  for (int i = threadIdx.x; i < routes; i += blockDim.x) {
     const int e = r.ids[i];
-    if (e >= 0 && e < p.E)
+    if (e >= 0 && e < p.E) {
       atomicOr(r.tokens + e, 1u << (i / p.k));
-    else
+      atomicOr(r.on + (e >> 5), 1u << (e & 31));
+    } else {
       set_error(p.ctrl, MOE_ERR_DEVICE_FAULT, 30);   // a NaN logit that no key stands for
+    }
+  }
+  __syncthreads();
+  int active = 0;
+  for (int w = 0; w < (p.E + 31) / 32; ++w) active += __popc(r.on[w]);
+  for (int i = threadIdx.x; i < routes; i += blockDim.x) {
+    const int e = r.ids[i], t = i / p.k;
+    if (e < 0 || e >= p.E) continue;
+    int a = __popc(r.on[e >> 5] & ((1u << (e & 31)) - 1u));
+    for (int w = 0; w < (e >> 5); ++w) a += __popc(r.on[w]);
+    r.active[a] = e;                        // (its tokens write the same)
+    r.choice[a * kMaxTok + t] = static_cast<uint8_t>(i - t * p.k);
   }
   __syncthreads();
   if (warp == 0) {
-    int n = 0;
-    for (int e0 = 0; e0 < p.E; e0 += 32) {
-      const int e = e0 + lane;
-      const uint32_t t = e < p.E ? r.tokens[e] : 0u;
-      const uint32_t m = __ballot_sync(0xffffffffu, t != 0);
-      if (t != 0) {
-        const int a = n + __popc(m & ((1u << lane) - 1u));
-        r.active[a] = e;
-        r.tokens[e] = t | (static_cast<uint32_t>(a) << 16);
+    int sum = 0;
+    for (int a0 = 0; a0 < active; a0 += 32) {
+      const int a = a0 + lane, n = a < active ? __popc(r.tokens[r.active[a]]) : 0;
+      int upto = n;
+#pragma unroll
+      for (int o = 1; o < 32; o <<= 1) {
+        const int u = __shfl_up_sync(0xffffffffu, upto, o);
+        if (lane >= o) upto += u;
       }
-      n += __popc(m);
+      if (a < active) r.before[a] = sum + upto - n;
+      sum += __shfl_sync(0xffffffffu, upto, 31);
     }
-    if (lane == 0) *s_n = n;
+    if (lane == 0) r.before[active] = sum;
   }
-  __syncthreads();
-  for (int i = threadIdx.x; i < p.T * p.k; i += blockDim.x) {
-    const int e = r.ids[i], t = i / p.k;
-    if (e >= 0 && e < p.E) r.choice[(r.tokens[e] >> 16) * kMaxTok + t] = static_cast<uint8_t>(i - t * p.k);
-  }
-  __syncthreads();
-  return *s_n;
+  return active;                            // (`before` is there after the next barrier)
 }
 
 // One block of 128 bytes of 16 rows, as A operands: the lane's 16 bytes of rows g and g + 8 in
@@ -186,10 +221,8 @@ struct Block {
       for (int i = 0; i < kMmas; ++i) {
         uint32_t(&m)[4] = a[kMmas * c + i];
         if constexpr (kFP8) {
-          m[0] = e4m3x2_to_f16x2(static_cast<uint16_t>(l[i]));
-          m[1] = e4m3x2_to_f16x2(static_cast<uint16_t>(u[i]));
-          m[2] = e4m3x2_to_f16x2(static_cast<uint16_t>(l[i] >> 16));
-          m[3] = e4m3x2_to_f16x2(static_cast<uint16_t>(u[i] >> 16));
+          codes_to_halves(l[i], m[0], m[2]);
+          codes_to_halves(u[i], m[1], m[3]);
         } else {
           m[0] = l[2 * i], m[1] = u[2 * i], m[2] = l[2 * i + 1], m[3] = u[2 * i + 1];
         }
@@ -235,56 +268,77 @@ __device__ __forceinline__ void copy_step(uint32_t slot, const uint8_t* src, int
 template <bool kFP8>
 __host__ __device__ constexpr int x_pitch(int H) { return 2 * H + (kFP8 ? 16 : 64); }
 
+// Buffers for the sums of warps that share a unit: two in turn need one barrier a unit, but not
+// where they would take the room of a ring (32 KB).
+__host__ __device__ constexpr int red_buffers(int groups, int warps) { return groups * warps < 32 ? 2 : 1; }
+
 template <bool kFP8, int kGroups, int kWarps, int kDepth>
 int up_smem(const FewParams& p) {
   return Routing::bytes(p.T, p.k, p.E) + p.T * x_pitch<kFP8>(p.H) +
-         (kFP8 ? p.H / 128 * 8 * kGroups * 4 : 0) + 2 * kWarps * kGroups * 512 +
+         (kFP8 ? p.H / 128 * 8 * kGroups * 4 : 0) + red_buffers(kGroups, kWarps) * kWarps * kGroups * 512 +
          kWarps * kDepth * kSlot;
 }
 
 template <bool kFP8, int kGroups, int kWarps, int kDepth>
 __global__ void __launch_bounds__(kWarps * 32, kWarps == 8 ? 2 : 1) few_up_kernel(const FewParams p) {
   extern __shared__ __align__(16) uint8_t smem[];
-  __shared__ int s_n;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
   const Routing r(smem, p.T, p.k, p.E);
   const int pitch = x_pitch<kFP8>(p.H);
   uint8_t* s_x = smem + Routing::bytes(p.T, p.k, p.E);
   float* s_xs = reinterpret_cast<float*>(s_x + p.T * pitch);            // FP8: [K/128][tokens]
   float4* s_red = reinterpret_cast<float4*>(s_xs + (kFP8 ? p.H / 128 * 8 * kGroups : 0));
-  uint8_t* s_ring = reinterpret_cast<uint8_t*>(s_red + 2 * kWarps * kGroups * 32) +
+  uint8_t* s_ring = reinterpret_cast<uint8_t*>(s_red + red_buffers(kGroups, kWarps) * kWarps * kGroups * 32) +
                     warp * kDepth * kSlot;
   const uint32_t ring = smem_u32(s_ring);
   pdl_wait();
   pdl_launch_dependents();
 
-  route_tokens(p, r);
-  // x into shared memory, a warp per 128 elements of a token (the warps that do not route first)
+  route_tokens(p, r, reinterpret_cast<float*>(s_x + p.T * pitch + (kFP8 ? p.H / 128 * 8 * kGroups * 4 : 0)));
+  // x into shared memory, 8 elements a lane and four loads in flight, by the warps that do not route
+  // where those are many
+  const int stagers = p.T < kWarps / 2 ? kWarps - p.T : kWarps;
   const int blocks = (p.H + 127) / 128;
-  for (int b = (warp + kWarps - p.T % kWarps) % kWarps; b < p.T * blocks; b += kWarps) {
-    const int tok = b / blocks, blk = b - tok * blocks;
-    const int at = blk * 128 + lane * 4;
-    if (!kFP8 && at >= p.H) continue;
-    const uint2 raw = __ldg(reinterpret_cast<const uint2*>(p.x + static_cast<size_t>(tok) * p.H + at));
-    uint8_t* row = s_x + tok * pitch;
-    if constexpr (kFP8) {
-      const float v[4] = {__uint_as_float(raw.x << 16), __uint_as_float(raw.x & 0xffff0000u),
-                          __uint_as_float(raw.y << 16), __uint_as_float(raw.y & 0xffff0000u)};
-      float amax = fmaxf(fmaxf(fabsf(v[0]), fabsf(v[1])), fmaxf(fabsf(v[2]), fabsf(v[3])));
+  if (warp >= kWarps - stagers) {
+    const int per_token = p.H / 8, pieces = p.T * per_token;   // (FP8: whole blocks of 16 pieces)
+    for (int i0 = (warp - (kWarps - stagers)) * 32 + lane; i0 < (pieces + 31) / 32 * 32; i0 += 4 * 32 * stagers) {
+      uint4 raw[4];
 #pragma unroll
-      for (int o = 16; o > 0; o >>= 1) amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, o));
-      float up, down;
-      block_scale(amax, up, down);
-      *reinterpret_cast<uint2*>(row + at * 2) = halves(v, up);
-      if (lane == 0) s_xs[blk * 8 * kGroups + tok] = down;
-    } else {
-      *reinterpret_cast<uint2*>(row + at * 2) = raw;
+      for (int j = 0; j < 4; ++j) {
+        const int i = i0 + j * 32 * stagers;
+        raw[j] = i < pieces ? __ldg(reinterpret_cast<const uint4*>(p.x) + i) : make_uint4(0u, 0u, 0u, 0u);
+      }
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        const int i = i0 + j * 32 * stagers;
+        const int tok = i / per_token, piece = i - tok * per_token;
+        if constexpr (kFP8) {
+          const uint32_t w[4] = {raw[j].x, raw[j].y, raw[j].z, raw[j].w};
+          float v[8], amax = 0.0f;
+#pragma unroll
+          for (int e = 0; e < 4; ++e) {
+            v[2 * e] = __uint_as_float(w[e] << 16);
+            v[2 * e + 1] = __uint_as_float(w[e] & 0xffff0000u);
+            amax = fmaxf(amax, fmaxf(fabsf(v[2 * e]), fabsf(v[2 * e + 1])));
+          }
+#pragma unroll
+          for (int o = 8; o > 0; o >>= 1) amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, o));
+          float up, down;
+          block_scale(amax, up, down);
+          if (i >= pieces) continue;
+          const uint2 a = halves(v, up), b = halves(v + 4, up);
+          *reinterpret_cast<uint4*>(s_x + tok * pitch + piece * 16) = make_uint4(a.x, a.y, b.x, b.y);
+          if (piece % 16 == 0) s_xs[piece / 16 * 8 * kGroups + tok] = down;
+        } else if (i < pieces) {
+          *reinterpret_cast<uint4*>(s_x + tok * pitch + piece * 16) = raw[j];
+        }
+      }
     }
   }
   if (kFP8)      // columns of no token
     for (int i = threadIdx.x; i < blocks * 8 * kGroups; i += kWarps * 32)
       if (i % (8 * kGroups) >= p.T) s_xs[i] = 0.0f;
-  const int active = route_join(p, r, &s_n);
+  const int active = route_join(p, r);
 
   const int per_expert = p.I / 8;
   const int units = active * per_expert;
@@ -295,7 +349,7 @@ __global__ void __launch_bounds__(kWarps * 32, kWarps == 8 ? 2 : 1) few_up_kerne
   int share = 1;
   for (int n = 1, best = 0x7fffffff; n <= kWarps && n <= steps; n *= 2) {
     const int groups = gridDim.x * (kWarps / n);
-    const int cost = (units + groups - 1) / groups * ((steps + n - 1) / n + (n > 1));
+    const int cost = __float2int_ru(__fdividef(units, groups)) * ((steps + n - 1) / n + (n > 1));
     if (cost < best) best = cost, share = n;
   }
   const int sub = warp & (share - 1);
@@ -303,20 +357,27 @@ __global__ void __launch_bounds__(kWarps * 32, kWarps == 8 ? 2 : 1) few_up_kerne
   const int first = blockIdx.x * (kWarps / share) + warp / share;
   const int64_t to_up = static_cast<int64_t>(p.I) * row_bytes;     // from a gate row to its up row
 
-  // the copies run kDepth - 1 steps ahead of the products, over the units' boundaries
-  int lu = first, ls = sub;
+  // the copies run kDepth steps ahead of the products, over the units' boundaries
+  // a unit is the active expert `a` and the `c`-th 8 of its columns
+  const int stride_a = stride / per_expert, stride_c = stride - stride_a * per_expert;
+  auto step_unit = [&](int& a, int& c) {
+    a += stride_a;
+    c += stride_c;
+    if (c >= per_expert) c -= per_expert, ++a;
+  };
+  int la = first / per_expert, lc = first - la * per_expert, ls = sub;
+  int ca = la, cc = lc;
   const uint8_t* src = nullptr;             // the lane's piece of the first rows
   const float* scale = nullptr;             // lanes 0, 1: the gate rows' two; 2, 3: the up rows'
   auto aim = [&]() {
-    const int a = lu / per_expert, i0 = (lu - a * per_expert) * 8;
-    const int64_t row = static_cast<int64_t>(r.active[a]) * 2 * p.I + i0;
+    const int64_t row = static_cast<int64_t>(r.active[la]) * 2 * p.I + lc * 8;
     src = p.w + (row + (lane >> 4)) * row_bytes + (lane & 15) * 16 + sub * kStepBytes;
     if constexpr (kFP8)
       scale = p.w_scales + (row + (lane & 2 ? p.I : 0)) / 128 * nkb + 2 * sub + (lane & 1);
   };
-  if (lu < units) aim();
+  if (la < active) aim();
   auto copy = [&](int slot) {
-    if (lu < units) {
+    if (la < active) {
       copy_step(ring + slot * kSlot, src, row_bytes, to_up, 2 * ls + 1 < nkb);
       src += share * kStepBytes;
       if constexpr (kFP8) {
@@ -327,14 +388,14 @@ __global__ void __launch_bounds__(kWarps * 32, kWarps == 8 ? 2 : 1) few_up_kerne
       ls += share;
       if (ls >= steps) {
         ls = sub;
-        lu += stride;
-        if (lu < units) aim();
+        step_unit(la, lc);
+        if (la < active) aim();
       }
     }
     cp_commit();
   };
 #pragma unroll
-  for (int d = 0; d < kDepth - 1; ++d) copy(d);
+  for (int d = 0; d < kDepth; ++d) copy(d);
 
   // the columns' tokens (those of no token read token 0's row: their sums are not used)
   const uint8_t* row[kGroups];
@@ -343,8 +404,9 @@ __global__ void __launch_bounds__(kWarps * 32, kWarps == 8 ? 2 : 1) few_up_kerne
   const float* xs = s_xs + 2 * t;
   const uint32_t half0 = piece_at(g, t), half1 = piece_at(g, 4 + t);
   int slot = 0, parity = 0;
-  for (int u = first; u < units; u += stride) {
-    const int a = u / per_expert, i0 = (u - a * per_expert) * 8;
+  while (ca < active) {
+    const int a = ca, i0 = cc * 8;
+    step_unit(ca, cc);
     const uint32_t tokens = r.tokens_of(a);
     float acc[kGroups][4];
 #pragma unroll
@@ -352,8 +414,6 @@ __global__ void __launch_bounds__(kWarps * 32, kWarps == 8 ? 2 : 1) few_up_kerne
 #pragma unroll
       for (int i = 0; i < 4; ++i) acc[n][i] = 0.0f;
     for (int s = sub; s < steps; s += share) {
-      __syncwarp();                         // the slot to be filled has been read by all lanes
-      copy(slot == 0 ? kDepth - 1 : slot - 1);
       cp_wait<kDepth - 1>();
       __syncwarp();
       const uint8_t* q = s_ring + slot * kSlot;
@@ -380,12 +440,15 @@ __global__ void __launch_bounds__(kWarps * 32, kWarps == 8 ? 2 : 1) few_up_kerne
           }
         }
       }
+      __syncwarp();                         // the slot has been read by all lanes
+      copy(slot);
       slot = slot == kDepth - 1 ? 0 : slot + 1;
     }
-    // the sharing warps' sums meet in the first of them; two buffers in turn, so one barrier a unit
+    // the sharing warps' sums meet in the first of them
     if (share > 1) {
+      constexpr bool kTwo = red_buffers(kGroups, kWarps) == 2;
       float4* red = s_red + parity * kWarps * kGroups * 32;
-      parity ^= 1;
+      if (kTwo) parity ^= 1;
       if (sub > 0)
 #pragma unroll
         for (int n = 0; n < kGroups; ++n)
@@ -402,6 +465,7 @@ __global__ void __launch_bounds__(kWarps * 32, kWarps == 8 ? 2 : 1) few_up_kerne
             acc[n][2] += v.z;
             acc[n][3] += v.w;
           }
+      if (!kTwo) asm volatile("bar.sync %0, %1;" ::"r"(1 + warp / share), "r"(share * 32) : "memory");
     }
     if (sub != 0) continue;
 #pragma unroll
@@ -428,31 +492,31 @@ constexpr int h_pitch() {                   // bytes; as x_pitch
 
 template <bool kFP8, int kGroups, int kWarps, int kDepth>
 int down_smem(const FewParams& p) {
-  return Routing::bytes(p.T, p.k, p.E) + p.h_rows * (h_pitch<kFP8>() + 4 + 4 + 8) +
-         kWarps / 8 * kDownRows * 8 * kGroups * 4 + kWarps * kDepth * kSlot;
+  return Routing::bytes(p.T, p.k, p.E) + p.h_rows * (h_pitch<kFP8>() + 4 + 4) +
+         kWarps * 16 * 8 * kGroups * 4 + kWarps * kDepth * kSlot;
 }
 
 template <bool kFP8, int kGroups, int kWarps, int kDepth>
 __global__ void __launch_bounds__(kWarps * 32, kWarps == 8 ? 2 : 1)
     few_down_kernel(const FewParams p) {
   extern __shared__ __align__(16) uint8_t smem[];
-  __shared__ int s_n;
-  constexpr int kCols = 8 * kGroups;
+  constexpr int kCols = 8 * kGroups, kMaxParts = kWarps / 4;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
   const Routing r(smem, p.T, p.k, p.E);
   uint8_t* s_h = smem + Routing::bytes(p.T, p.k, p.E);
   float* s_hs = reinterpret_cast<float*>(s_h + p.h_rows * h_pitch<kFP8>());   // FP8: rows' scales
   int* s_what = reinterpret_cast<int*>(s_hs + p.h_rows);        // what a row holds: route, block
-  int2* s_step = reinterpret_cast<int2*>(s_what + p.h_rows);    // a block: (active expert, first row)
-  float* s_part = reinterpret_cast<float*>(s_step + p.h_rows);  // [row][token]
-  uint8_t* s_ring = reinterpret_cast<uint8_t*>(s_part + kWarps / 8 * kDownRows * kCols) + warp * kDepth * kSlot;
+  float* s_part = reinterpret_cast<float*>(s_what + p.h_rows);  // [part][row][token]
+  uint8_t* s_ring = reinterpret_cast<uint8_t*>(s_part + kWarps * 16 * kCols) + warp * kDepth * kSlot;
   const uint32_t ring = smem_u32(s_ring);
   const int cluster = p.cluster, rank = blockIdx.x % cluster;
-  const int tile = warp & 7, part = warp >> 3;                  // 16 warps: two for each row tile
-  const int n0 = blockIdx.x / cluster * kDownRows + tile * 16;
+  const int tile = warp % p.tiles, part = warp / p.tiles;       // the parts of a tile's warps
+  const int parts = kWarps / p.tiles;                           // take its steps in turn
+  const int n_cta = blockIdx.x / cluster * p.tiles * 16, n0 = n_cta + tile * 16;
   const bool idle = n0 >= p.H;                                  // (H is a multiple of 16)
-  route_tokens(p, r);
-  const int active = route_join(p, r, &s_n);
+  route_tokens(p, r, reinterpret_cast<float*>(s_part));
+  const int active = route_join(p, r);
+  __syncthreads();
 
   // this CTA's share of the steps (two blocks each, expert by expert)
   const int row_bytes = p.I * (kFP8 ? 1 : 2);
@@ -461,8 +525,8 @@ __global__ void __launch_bounds__(kWarps * 32, kWarps == 8 ? 2 : 1)
   const int s0 = static_cast<int>(all * rank / cluster);
   const int s1 = static_cast<int>(all * (rank + 1) / cluster);
 
-  constexpr int kParts = kWarps / 8;        // warps that take a row tile's steps in turn
   int ls = s0 + part, la = ls / per, lp = ls - la * per;
+  const int la0 = la, lp0 = lp;
   const uint8_t* src = nullptr;             // the lane's piece of the first rows
   const float* scale = nullptr;             // lanes 0, 1: the step's two
   auto aim = [&]() {
@@ -474,14 +538,14 @@ __global__ void __launch_bounds__(kWarps * 32, kWarps == 8 ? 2 : 1)
   auto copy = [&](int slot) {
     if (ls < s1 && !idle) {
       copy_step(ring + slot * kSlot, src, row_bytes, 8 * static_cast<int64_t>(row_bytes), 2 * lp + 1 < nkb);
-      src += kParts * kStepBytes;
+      src += parts * kStepBytes;
       if constexpr (kFP8) {
         if (lane < 2 && 2 * lp + lane < nkb)
           cp_async4(ring + slot * kSlot + kSlotBytes + lane * 4, scale);
-        scale += 2 * kParts;
+        scale += 2 * parts;
       }
-      ls += kParts;
-      lp += kParts;
+      ls += parts;
+      lp += parts;
       if (lp >= per) {
         while (lp >= per) lp -= per, ++la;
         if (ls < s1) aim();
@@ -490,39 +554,53 @@ __global__ void __launch_bounds__(kWarps * 32, kWarps == 8 ? 2 : 1)
     cp_commit();
   };
 #pragma unroll
-  for (int d = 0; d < kDepth - 1; ++d) copy(d);
-  pdl_wait();                               // the weights above do not depend on the up kernel
-  pdl_launch_dependents();
-
+  for (int d = 0; d < kDepth; ++d) copy(d);
   float acc[kGroups][4];
 #pragma unroll
   for (int n = 0; n < kGroups; ++n)
 #pragma unroll
     for (int i = 0; i < 4; ++i) acc[n][i] = 0.0f;
   const uint32_t half0 = piece_at(g, t), half1 = piece_at(g, 4 + t);
+  // Row of block kb of expert a's first token, counted over all of them: those of a block are
+  // neighbours, then come the expert's next blocks.
+  auto row_at = [&](int a, int kb) { return r.before[a] * nkb + (r.before[a + 1] - r.before[a]) * kb; };
+  auto row_of_step = [&](int64_t s) {
+    const int a = static_cast<int>(s / per);
+    return a >= active ? r.before[active] * nkb : row_at(a, 2 * static_cast<int>(s - static_cast<int64_t>(a) * per));
+  };
+  bool waited = false;                      // for the up kernel: nothing so far depends on it
   int slot = 0;
+  int ca = la0, cp = lp0;                   // the warp's next step
   for (int s = s0; s < s1;) {
-    // the next steps whose rows of h (one per token and block) fit; s_step holds their blocks, two
-    // a step
-    int count = 0, rows = 0, used = 0;
-    while (s + count < s1) {
-      const int a = (s + count) / per, p0 = (s + count) - a * per;
-      const uint32_t tokens = r.tokens_of(a);
-      const int n = __popc(tokens);
-      // (a step counts two blocks here, also the last of an odd number)
-      const int take = min(min(per - p0, s1 - s - count), min(p.h_rows - rows, p.h_rows - used) / (2 * n));
-      if (take == 0) break;
-      const int blocks = min(2 * take, nkb - 2 * p0);
-      for (int i = threadIdx.x; i < 2 * take; i += kWarps * 32) s_step[used + i] = make_int2(a, rows + i * n);
-      for (int i = threadIdx.x; i < blocks * n; i += kWarps * 32) {
-        const int tok = __fns(tokens, 0, i % n + 1);
-        s_what[rows + i] = (2 * p0 + i / n) << 16 | (tok * p.k + r.choice[a * kMaxTok + tok]);
+    // the next steps whose rows of h fit
+    const int first = row_of_step(s);
+    int end = s1;
+    if (row_of_step(end) - first > p.h_rows) {
+      int lo = s + 1, hi = s1;              // (one step always fits) the first end that does not
+      while (hi - lo > 1) {
+        const int mid = (lo + hi) >> 1;
+        if (row_of_step(mid) - first > p.h_rows) hi = mid; else lo = mid;
       }
-      count += take;
-      used += 2 * take;
-      rows += blocks * n;
+      end = lo;
+    }
+    const int rows = row_of_step(end) - first;
+    for (int i = threadIdx.x; i < rows; i += kWarps * 32) {
+      const int at = first + i;
+      int lo = 0, hi = active;              // its expert
+      while (hi - lo > 1) {
+        const int mid = (lo + hi) >> 1;
+        if (r.before[mid] * nkb <= at) lo = mid; else hi = mid;
+      }
+      const int n = r.before[lo + 1] - r.before[lo];
+      const int in = at - r.before[lo] * nkb, kb = in / n;
+      uint32_t tokens = r.tokens_of(lo);
+      for (int q = in - kb * n; q > 0; --q) tokens &= tokens - 1;
+      const int tok = __ffs(tokens) - 1;
+      s_what[i] = kb << 16 | (tok * p.k + r.choice[lo * kMaxTok + tok]);
     }
     __syncthreads();
+    if (!waited) pdl_wait();
+    waited = true;
     // h times its route's weight, in the MMA's types; four rows' loads in flight
     for (int i0 = warp; i0 < rows; i0 += 4 * kWarps) {
       float v[4][4];
@@ -571,13 +649,12 @@ __global__ void __launch_bounds__(kWarps * 32, kWarps == 8 ? 2 : 1)
     }
     __syncthreads();
     if (!idle) {
-      // (a row tile's warps take every kParts-th step of the share, counted from its start)
-      for (int i = (part + kParts - (s - s0) % kParts) % kParts; i < count; i += kParts) {
-        const int a = s_step[2 * i].x;
+      for (; ca * per + cp < end;) {
+        const int a = ca, kb0 = 2 * cp;
         const uint32_t tokens = r.tokens_of(a);
-        const bool both = 2 * (s + i - a * per) + 1 < nkb;
-        __syncwarp();
-        copy(slot == 0 ? kDepth - 1 : slot - 1);
+        const bool both = kb0 + 1 < nkb;
+        cp += parts;
+        while (cp >= per) cp -= per, ++ca;
         cp_wait<kDepth - 1>();
         __syncwarp();
         const uint8_t* q = s_ring + slot * kSlot;
@@ -587,7 +664,7 @@ __global__ void __launch_bounds__(kWarps * 32, kWarps == 8 ? 2 : 1)
           if (b == 1 && !both) break;
           Block<kFP8> w;
           w.load(q + half0 + b * 128, q + half1 + b * 128);
-          const int base = s_step[2 * i + b].y;
+          const int base = row_at(a, kb0 + b) - first;
 #pragma unroll
           for (int n = 0; n < kGroups; ++n) {
             if (kGroups > 1 && ((tokens >> (8 * n)) & 255u) == 0) continue;
@@ -611,42 +688,46 @@ __global__ void __launch_bounds__(kWarps * 32, kWarps == 8 ? 2 : 1)
             }
           }
         }
+        __syncwarp();
+        copy(slot);
         slot = slot == kDepth - 1 ? 0 : slot + 1;
       }
     }
-    s += count;
+    s = end;
     __syncthreads();                        // before the next rows overwrite these
   }
+  if (!waited) pdl_wait();
+  pdl_launch_dependents();
   // the shares meet, in the order of ranks and parts: rank r adds its part of the rows
 #pragma unroll
   for (int n = 0; n < kGroups; ++n)
 #pragma unroll
     for (int i = 0; i < 4; ++i)
-      s_part[(part * kDownRows + tile * 16 + g + 8 * (i >> 1)) * kCols + 8 * n + 2 * t + (i & 1)] = acc[n][i];
+      s_part[((part * p.tiles + tile) * 16 + g + 8 * (i >> 1)) * kCols + 8 * n + 2 * t + (i & 1)] = acc[n][i];
   asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory");
   asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory");
-  const int rows = kDownRows / cluster;
+  const int rows = p.tiles * 16 / cluster;
   for (int i = threadIdx.x; i < rows * p.T; i += kWarps * 32) {
     const int tok = i / rows, row = rank * rows + i - tok * rows;
-    const int n = blockIdx.x / cluster * kDownRows + row;
+    const int n = n_cta + row;
     if (n >= p.H) continue;
-    float v[kCluster * kParts];
+    float v[kCluster * kMaxParts];
 #pragma unroll
     for (int c = 0; c < kCluster; ++c)
 #pragma unroll
-      for (int q = 0; q < kParts; ++q) {
-        float& x = v[c * kParts + q];
+      for (int q = 0; q < kMaxParts; ++q) {
+        float& x = v[c * kMaxParts + q];
         x = 0.0f;
-        if (c >= cluster) continue;
+        if (c >= cluster || q >= parts) continue;
         uint32_t at;
         asm volatile("mapa.shared::cluster.u32 %0, %1, %2;"
                      : "=r"(at)
-                     : "r"(smem_u32(s_part + (q * kDownRows + row) * kCols + tok)), "r"(c));
+                     : "r"(smem_u32(s_part + ((q * p.tiles * 16) + row) * kCols + tok)), "r"(c));
         asm volatile("ld.shared::cluster.f32 %0, [%1];" : "=f"(x) : "r"(at));
       }
     float sum = v[0];
 #pragma unroll
-    for (int c = 1; c < kCluster * kParts; ++c) sum += v[c];
+    for (int c = 1; c < kCluster * kMaxParts; ++c) sum += v[c];
     p.out[static_cast<size_t>(tok) * p.H + n] = __float2bfloat16_rn(sum);
   }
   asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory");
@@ -674,7 +755,7 @@ cudaError_t launch_down(const FewParams& p, cudaStream_t stream) {
   if (e == cudaSuccess) e = prefer_max_shared(kernel);
   if (e != cudaSuccess) return e;
   cudaLaunchAttribute attr[2];
-  cudaLaunchConfig_t cfg = make_cfg(dim3((p.H + kDownRows - 1) / kDownRows * p.cluster),
+  cudaLaunchConfig_t cfg = make_cfg(dim3((p.H + p.tiles * 16 - 1) / (p.tiles * 16) * p.cluster),
                                     dim3(kWarps * 32), stream, true, attr);
   attr[1].id = cudaLaunchAttributeClusterDimension;
   attr[1].val.clusterDim.x = p.cluster;
@@ -691,6 +772,14 @@ cudaError_t launch_few(FewParams p, int sms, cudaStream_t stream) {
   // work is small; 16 stream faster.  x takes what room the rings leave.
   const int64_t routed = static_cast<int64_t>(Routing::most(p.T, p.k, p.E)) * 2 * p.I * p.H * (kFP8 ? 1 : 2);
   const bool small = routed <= (32ll << 20);
+  // One round over the SMs with as many CTAs as it takes: clusters of 8 find room for 15 on 152
+  // SMs with a CTA each, those of 4 for 36.
+  p.tiles = (p.H + 63) / 64 <= sms ? 4 : 8;
+  const int chunks = (p.H + p.tiles * 16 - 1) / (p.tiles * 16);
+  p.cluster = chunks * 8 <= sms * 3 / 4 ? 8 : chunks * 4 <= sms * 15 / 16 ? 4 : chunks * 2 <= sms ? 2 : 1;
+  // rows of h at a time: all of a share's, if they are spread evenly, but no more than 48 KB
+  const int64_t even = static_cast<int64_t>(p.T) * p.k * p.I * (kFP8 ? 1 : 2) / 128 / p.cluster;
+  p.h_rows = even * 5 / 4 + 32 < 160 ? static_cast<int>(even * 5 / 4 + 32) / 4 * 4 : 160;
   cudaError_t e;
   if (!small && up_smem<kFP8, kGroups, 16, 2>(p) <= kMaxSmem)
     e = launch_up<kFP8, kGroups, 16, 2>(p, sms, stream);
@@ -699,18 +788,14 @@ cudaError_t launch_few(FewParams p, int sms, cudaStream_t stream) {
   else
     e = launch_up<kFP8, kGroups, 8, 2>(p, sms, stream);
   if (e != cudaSuccess) return e;
-  // CTAs for one round over the SMs (those that a cluster of this size can use)
-  const int chunks = (p.H + kDownRows - 1) / kDownRows;
-  p.cluster = kCluster;
-  while (p.cluster > 1 && chunks * p.cluster > sms) p.cluster /= 2;
   return small ? launch_down<kFP8, kGroups, 8, 3>(p, stream)
                : launch_down<kFP8, kGroups, 16, 2>(p, stream);
 }
 
 }  // namespace
 
-cudaError_t launch_few_experts(const moe_forward_args& f, void* out, float* h, Ctrl* ctrl,
-                               int num_sms, cudaStream_t stream) {
+cudaError_t launch_few_experts(const moe_forward_args& f, void* out, uint8_t* ws, int num_sms,
+                               cudaStream_t stream) {
   const bool fp8 = f.dtype == MOE_DTYPE_FP8_E4M3;
   // x of one launch fits shared memory beside the rings
   int most = 65536 / f.K;
@@ -725,9 +810,10 @@ cudaError_t launch_few_experts(const moe_forward_args& f, void* out, float* h, C
     p.w_scales = f.w_scales;
     p.w2 = static_cast<const uint8_t*>(f.w2);
     p.w2_scales = f.w2_scales;
-    p.h = h + static_cast<size_t>(t0) * f.top_k * f.N;
     p.out = static_cast<__nv_bfloat16*>(out) + static_cast<size_t>(t0) * f.K;
-    p.ctrl = ctrl;
+    p.ctrl = reinterpret_cast<Ctrl*>(ws);
+    // (every pass has the same place: its kernels wait for those of the pass before)
+    p.h = reinterpret_cast<float*>(ws + MOE_CTRL_BYTES);
     p.T = t1 - t0;
     p.H = f.K;
     p.I = f.N;
@@ -735,7 +821,6 @@ cudaError_t launch_few_experts(const moe_forward_args& f, void* out, float* h, C
     p.k = f.top_k;
     p.softcap = f.softcap;
     p.renorm = f.renorm;
-    p.h_rows = p.T <= 4 ? 32 : 64;
     cudaError_t e;
     if (fp8)
       e = p.T <= 8 ? launch_few<true, 1>(p, num_sms, stream) : launch_few<true, 2>(p, num_sms, stream);

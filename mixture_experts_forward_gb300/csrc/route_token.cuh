@@ -40,26 +40,22 @@ __device__ __forceinline__ uint32_t order_key(float z) {
   return (u & 0x80000000u) ? ~u : (u | 0x80000000u);
 }
 
-// Routes one token with one warp.  NPL = experts per lane (E <= 32 * NPL);
-// lane l owns experts l, l+32, ...
+// z = softcap * tanh(logit / softcap), or the logit itself (softcap 0).
+__device__ __forceinline__ float cap_logit(float l, float softcap) {
+  return softcap > 0.0f ? __fmul_rn(softcap, tanh_ieee(__fdiv_rn(l, softcap))) : l;
+}
+
+// Selects one token's experts from its capped logits with one warp.  NPL = experts per lane
+// (E <= 32 * NPL); lane l owns experts l, l+32, ... (z of those past E is not used).
 template <int NPL>
-__device__ __forceinline__ int route_token(const float* __restrict__ row, int E, int k,
-                                           float softcap, int renorm, int32_t* __restrict__ ids,
-                                           float* __restrict__ weights) {
+__device__ __forceinline__ int route_select(const float (&z)[NPL], int E, int k, int renorm,
+                                            int32_t* __restrict__ ids,
+                                            float* __restrict__ weights) {
   const int lane = threadIdx.x & 31;
-  float z[NPL];
   uint32_t key[NPL];
 #pragma unroll
-  for (int i = 0; i < NPL; ++i) {
-    const int e = lane + 32 * i;
-    z[i] = e < E ? __ldg(row + e) : 0.0f;
-  }
-#pragma unroll
-  for (int i = 0; i < NPL; ++i) {
-    const int e = lane + 32 * i;
-    if (softcap > 0.0f) z[i] = __fmul_rn(softcap, tanh_ieee(__fdiv_rn(z[i], softcap)));
-    key[i] = e < E ? order_key(z[i]) : 0u;  // key 0: below every real value
-  }
+  for (int i = 0; i < NPL; ++i)
+    key[i] = lane + 32 * i < E ? order_key(z[i]) : 0u;  // key 0: below every real value
 
   // this lane's best remaining expert (largest key; the first one wins ties,
   // which is the lowest id because ids grow with i)
@@ -126,6 +122,23 @@ __device__ __forceinline__ int route_token(const float* __restrict__ row, int E,
     weights[lane] = __fdiv_rn(my_e, s);
   }
   return my_id;  // lane j < k: the j-th selected expert
+}
+
+// Routes one token with one warp.
+template <int NPL>
+__device__ __forceinline__ int route_token(const float* __restrict__ row, int E, int k,
+                                           float softcap, int renorm, int32_t* __restrict__ ids,
+                                           float* __restrict__ weights) {
+  const int lane = threadIdx.x & 31;
+  float z[NPL];
+#pragma unroll
+  for (int i = 0; i < NPL; ++i) {
+    const int e = lane + 32 * i;
+    z[i] = e < E ? __ldg(row + e) : 0.0f;
+  }
+#pragma unroll
+  for (int i = 0; i < NPL; ++i) z[i] = cap_logit(z[i], softcap);
+  return route_select<NPL>(z, E, k, renorm, ids, weights);
 }
 
 }  // namespace moe

@@ -195,8 +195,7 @@ moe_status_t moe_forward_few(const moe_forward_args* args, void* out, void* ws, 
   if (!ws_ok(ws) || ws_bytes < few_bytes(args)) return MOE_ERR_WORKSPACE;
   const int sms = device_sms();
   if (sms <= 0) return MOE_ERR_CUDA;
-  float* h = reinterpret_cast<float*>(static_cast<uint8_t*>(ws) + MOE_CTRL_BYTES);
-  return cuda_status(launch_few_experts(*args, out, h, static_cast<Ctrl*>(ws), sms,
+  return cuda_status(launch_few_experts(*args, out, static_cast<uint8_t*>(ws), sms,
                                         static_cast<cudaStream_t>(stream)));
 }
 
