@@ -1,4 +1,5 @@
-// The whole gated expert layer for a few tokens (single tokens, drafted runs): two kernels.
+// The whole gated expert layer for a few tokens (single tokens, drafted runs): two kernels after
+// the router.
 //
 // With T <= 16 tokens nearly every weight is used for one or two of them, so the layer is one
 // pass over the active experts' weights and HBM bounds it; everything else has to hide behind
@@ -17,13 +18,14 @@
 // silu(gate) * up is computed where the sums are; several warps share a unit's K where there
 // are few units.  Down: a cluster of 8 CTAs takes 128 output rows, each of its CTAs an equal
 // share of all active experts' K; the shares meet over distributed shared memory, in rank order
-// (no atomics: repeated calls give the same bits).  Every CTA routes by itself (the same device
-// function as moe_route), which saves a launch and its wait; the down kernel does so, and fetches
-// its first weights, while the up kernel still runs.
+// (no atomics: repeated calls give the same bits).  The tokens are routed before by moe_route's
+// kernel, during which the up kernel stages x; while the up kernel runs, the down kernel fetches its first
+// weights as far as it finds room.  (Routing in every CTA of both kernels instead saved a launch but
+// took 8 us of each for 16 tokens and 256 experts.)
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 
-#include "route_token.cuh"
+#include "ieee_math.cuh"
 #include "serve_internal.cuh"
 
 namespace moe {
@@ -87,7 +89,8 @@ __device__ __forceinline__ uint2 halves(const float* v, float up) {
 }
 
 struct FewParams {
-  const float* logits;
+  const int32_t* ids;          // [T * k] the routes (moe_route)
+  const float* weights;        // [T * k]
   const __nv_bfloat16* x;
   const uint8_t* w;
   const float* w_scales;
@@ -97,31 +100,11 @@ struct FewParams {
   __nv_bfloat16* out;
   Ctrl* ctrl;
   int T, H, I, E, k;
-  float softcap;
-  int renorm;
+  int share;                   // warps that share a unit of the up kernel (a power of two)
   int h_rows;                  // rows of h that the down kernel stages at a time
   int tiles;                   // 16-row tiles of output rows that a down CTA takes (4 or 8),
   int cluster;                 // and how many CTAs share them (1, 2, 4 or 8)
 };
-
-template <int NPL>
-__device__ __forceinline__ void select_one(const float* z, int E, int k, int renorm, int32_t* ids,
-                                           float* weights) {
-  float mine[NPL];
-#pragma unroll
-  for (int i = 0; i < NPL; ++i) {
-    const int e = (threadIdx.x & 31) + 32 * i;
-    mine[i] = e < E ? z[e] : 0.0f;
-  }
-  route_select<NPL>(mine, E, k, renorm, ids, weights);
-}
-
-__device__ __noinline__ void route_one(const float* z, int E, int k, int renorm, int32_t* ids,
-                                       float* weights) {
-  if (E <= 64) select_one<2>(z, E, k, renorm, ids, weights);
-  else if (E <= 256) select_one<8>(z, E, k, renorm, ids, weights);
-  else select_one<32>(z, E, k, renorm, ids, weights);
-}
 
 // What every CTA knows of the routing, in shared memory.
 struct Routing {
@@ -147,27 +130,27 @@ struct Routing {
   __device__ uint32_t tokens_of(int a) const { return tokens[active[a]]; }
 };
 
-// The tokens' routes: the capped logits by all threads (z: room for T * E numbers), then each
-// token by a warp; route_join() follows.
-__device__ __forceinline__ void route_tokens(const FewParams& p, const Routing& r, float* z) {
-  const int warp = threadIdx.x >> 5;
-  for (int i = threadIdx.x; i < p.T * p.E; i += blockDim.x) z[i] = cap_logit(__ldg(p.logits + i), p.softcap);
+// Before the routes are there.
+__device__ __forceinline__ void route_clear(const FewParams& p, const Routing& r) {
   for (int e = threadIdx.x; e < p.E; e += blockDim.x) r.tokens[e] = 0;
   if (threadIdx.x < 32) r.on[threadIdx.x] = 0;
   __syncthreads();
-  for (int t = warp; t < p.T; t += blockDim.x / 32)
-    route_one(z + t * p.E, p.E, p.k, p.renorm, r.ids + t * p.k, r.weights + t * p.k);
 }
 
-// The active experts, by all threads; returns how many there are.
+// Reads the routes and finds the active experts, by all threads; returns how many there are.
+// kAll: their weights and `before` too (there after the next barrier).
+template <bool kAll>
 __device__ __forceinline__ int route_join(const FewParams& p, const Routing& r) {
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int routes = p.T * p.k;
-  __syncthreads();
+  const uint32_t inverse = 0xffffffffu / p.k + 1;            // i / k = umulhi(i, inverse), k > 1
+  auto token_of = [&](int i) { return p.k == 1 ? i : static_cast<int>(__umulhi(i, inverse)); };
   for (int i = threadIdx.x; i < routes; i += blockDim.x) {
-    const int e = r.ids[i];
+    const int e = __ldcg(p.ids + i);
+    if constexpr (kAll) r.weights[i] = __ldcg(p.weights + i);
+    r.ids[i] = e;
     if (e >= 0 && e < p.E) {
-      atomicOr(r.tokens + e, 1u << (i / p.k));
+      atomicOr(r.tokens + e, 1u << token_of(i));
       atomicOr(r.on + (e >> 5), 1u << (e & 31));
     } else {
       set_error(p.ctrl, MOE_ERR_DEVICE_FAULT, 30);   // a NaN logit that no key stands for
@@ -177,7 +160,7 @@ __device__ __forceinline__ int route_join(const FewParams& p, const Routing& r) 
   int active = 0;
   for (int w = 0; w < (p.E + 31) / 32; ++w) active += __popc(r.on[w]);
   for (int i = threadIdx.x; i < routes; i += blockDim.x) {
-    const int e = r.ids[i], t = i / p.k;
+    const int e = r.ids[i], t = token_of(i);
     if (e < 0 || e >= p.E) continue;
     int a = __popc(r.on[e >> 5] & ((1u << (e & 31)) - 1u));
     for (int w = 0; w < (e >> 5); ++w) a += __popc(r.on[w]);
@@ -185,7 +168,7 @@ __device__ __forceinline__ int route_join(const FewParams& p, const Routing& r) 
     r.choice[a * kMaxTok + t] = static_cast<uint8_t>(i - t * p.k);
   }
   __syncthreads();
-  if (warp == 0) {
+  if (kAll && warp == 0) {
     int sum = 0;
     for (int a0 = 0; a0 < active; a0 += 32) {
       const int a = a0 + lane, n = a < active ? __popc(r.tokens[r.active[a]]) : 0;
@@ -200,7 +183,7 @@ __device__ __forceinline__ int route_join(const FewParams& p, const Routing& r) 
     }
     if (lane == 0) r.before[active] = sum;
   }
-  return active;                            // (`before` is there after the next barrier)
+  return active;
 }
 
 // One block of 128 bytes of 16 rows, as A operands: the lane's 16 bytes of rows g and g + 8 in
@@ -283,6 +266,7 @@ template <bool kFP8, int kGroups, int kWarps, int kDepth>
 __global__ void __launch_bounds__(kWarps * 32, kWarps == 8 ? 2 : 1) few_up_kernel(const FewParams p) {
   extern __shared__ __align__(16) uint8_t smem[];
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
+  __shared__ int s_ticket[kWarps][8];
   const Routing r(smem, p.T, p.k, p.E);
   const int pitch = x_pitch<kFP8>(p.H);
   uint8_t* s_x = smem + Routing::bytes(p.T, p.k, p.E);
@@ -291,93 +275,89 @@ __global__ void __launch_bounds__(kWarps * 32, kWarps == 8 ? 2 : 1) few_up_kerne
   uint8_t* s_ring = reinterpret_cast<uint8_t*>(s_red + red_buffers(kGroups, kWarps) * kWarps * kGroups * 32) +
                     warp * kDepth * kSlot;
   const uint32_t ring = smem_u32(s_ring);
-  pdl_wait();
-  pdl_launch_dependents();
-
-  route_tokens(p, r, reinterpret_cast<float*>(s_x + p.T * pitch + (kFP8 ? p.H / 128 * 8 * kGroups * 4 : 0)));
-  // x into shared memory, 8 elements a lane and four loads in flight, by the warps that do not route
-  // where those are many
-  const int stagers = p.T < kWarps / 2 ? kWarps - p.T : kWarps;
+  // The warps that share units, and the units they take: after the first `ahead`, which are dealt
+  // out, tickets from a counter, each drawn `ahead` units before its own, so that no copy waits for
+  // one.
+  // SMs do not get equal shares of HBM: with equal shares of the units the first of them
+  // were done at half the time of the last (five tokens through 18 BF16 experts: 50 and 109 us).
+  const int share = p.share, sub = warp & (share - 1);
+  const int row_bytes = p.H * (kFP8 ? 1 : 2);
+  const int nkb = row_bytes / 128, steps = (nkb + 1) / 2;
+  // (unit j's steps copy up to the start of unit j + 1 + kDepth / steps; tickets drawn with unit
+  // j - 1 are known then, and fewer than 8 are at any time)
+  const int ahead = kDepth / (steps / share) + 2;
+  const int groups = gridDim.x * (kWarps / share);
+  volatile int* ticket = s_ticket[warp / share];
+  if (sub == 0 && lane < ahead) ticket[lane] = lane * groups + blockIdx.x * (kWarps / share) + warp / share;
+  // x into shared memory, 8 elements a lane: it was there before the routing kernel began, which
+  // is waited for afterwards
   const int blocks = (p.H + 127) / 128;
-  if (warp >= kWarps - stagers) {
+  {
     const int per_token = p.H / 8, pieces = p.T * per_token;   // (FP8: whole blocks of 16 pieces)
-    for (int i0 = (warp - (kWarps - stagers)) * 32 + lane; i0 < (pieces + 31) / 32 * 32; i0 += 4 * 32 * stagers) {
-      uint4 raw[4];
+    const uint32_t inverse = 0xffffffffu / per_token + 1;      // (i * per_token < 2^32)
+    const uint4* from = reinterpret_cast<const uint4*>(p.x);
+    const int first = threadIdx.x, step = kWarps * 32;
+    uint4 next = first < pieces ? __ldg(from + first) : make_uint4(0u, 0u, 0u, 0u);
+#pragma unroll 1
+    for (int i = first; i < (pieces + 31) / 32 * 32; i += step) {
+      const uint4 raw = next;
+      if (i + step < pieces) next = __ldg(from + i + step);
+      const int tok = __umulhi(i, inverse), piece = i - tok * per_token;
+      uint4* dst = reinterpret_cast<uint4*>(s_x + tok * pitch + piece * 16);
+      if constexpr (kFP8) {
+        const uint32_t w[4] = {raw.x, raw.y, raw.z, raw.w};
+        float v[8], amax = 0.0f;
 #pragma unroll
-      for (int j = 0; j < 4; ++j) {
-        const int i = i0 + j * 32 * stagers;
-        raw[j] = i < pieces ? __ldg(reinterpret_cast<const uint4*>(p.x) + i) : make_uint4(0u, 0u, 0u, 0u);
-      }
-#pragma unroll
-      for (int j = 0; j < 4; ++j) {
-        const int i = i0 + j * 32 * stagers;
-        const int tok = i / per_token, piece = i - tok * per_token;
-        if constexpr (kFP8) {
-          const uint32_t w[4] = {raw[j].x, raw[j].y, raw[j].z, raw[j].w};
-          float v[8], amax = 0.0f;
-#pragma unroll
-          for (int e = 0; e < 4; ++e) {
-            v[2 * e] = __uint_as_float(w[e] << 16);
-            v[2 * e + 1] = __uint_as_float(w[e] & 0xffff0000u);
-            amax = fmaxf(amax, fmaxf(fabsf(v[2 * e]), fabsf(v[2 * e + 1])));
-          }
-#pragma unroll
-          for (int o = 8; o > 0; o >>= 1) amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, o));
-          float up, down;
-          block_scale(amax, up, down);
-          if (i >= pieces) continue;
-          const uint2 a = halves(v, up), b = halves(v + 4, up);
-          *reinterpret_cast<uint4*>(s_x + tok * pitch + piece * 16) = make_uint4(a.x, a.y, b.x, b.y);
-          if (piece % 16 == 0) s_xs[piece / 16 * 8 * kGroups + tok] = down;
-        } else if (i < pieces) {
-          *reinterpret_cast<uint4*>(s_x + tok * pitch + piece * 16) = raw[j];
+        for (int e = 0; e < 4; ++e) {
+          v[2 * e] = __uint_as_float(w[e] << 16);
+          v[2 * e + 1] = __uint_as_float(w[e] & 0xffff0000u);
+          amax = fmaxf(amax, fmaxf(fabsf(v[2 * e]), fabsf(v[2 * e + 1])));
         }
+#pragma unroll
+        for (int o = 8; o > 0; o >>= 1) amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, o));
+        float up, down;
+        block_scale(amax, up, down);
+        const uint2 a = halves(v, up), b = halves(v + 4, up);
+        if (i < pieces) {
+          *dst = make_uint4(a.x, a.y, b.x, b.y);
+          if (piece % 16 == 0) s_xs[piece / 16 * 8 * kGroups + tok] = down;
+        }
+      } else if (i < pieces) {
+        *dst = raw;
       }
     }
   }
   if (kFP8)      // columns of no token
     for (int i = threadIdx.x; i < blocks * 8 * kGroups; i += kWarps * 32)
       if (i % (8 * kGroups) >= p.T) s_xs[i] = 0.0f;
-  const int active = route_join(p, r);
+  route_clear(p, r);
+  pdl_wait();
+  pdl_launch_dependents();
+  const int active = route_join<false>(p, r);
 
   const int per_expert = p.I / 8;
   const int units = active * per_expert;
-  const int row_bytes = p.H * (kFP8 ? 1 : 2);
-  const int nkb = row_bytes / 128, steps = (nkb + 1) / 2;
-  // Warps that share a unit: the number that takes the fewest steps of the slowest warp, a step
-  // more for every join.
-  int share = 1;
-  for (int n = 1, best = 0x7fffffff; n <= kWarps && n <= steps; n *= 2) {
-    const int groups = gridDim.x * (kWarps / n);
-    const int cost = __float2int_ru(__fdividef(units, groups)) * ((steps + n - 1) / n + (n > 1));
-    if (cost < best) best = cost, share = n;
-  }
-  const int sub = warp & (share - 1);
-  const int stride = gridDim.x * (kWarps / share);
-  const int first = blockIdx.x * (kWarps / share) + warp / share;
   const int64_t to_up = static_cast<int64_t>(p.I) * row_bytes;     // from a gate row to its up row
 
   // the copies run kDepth steps ahead of the products, over the units' boundaries
-  // a unit is the active expert `a` and the `c`-th 8 of its columns
-  const int stride_a = stride / per_expert, stride_c = stride - stride_a * per_expert;
-  auto step_unit = [&](int& a, int& c) {
-    a += stride_a;
-    c += stride_c;
-    if (c >= per_expert) c -= per_expert, ++a;
+  const uint32_t inverse = 0xffffffffu / per_expert + 1;      // (per_expert >= 16)
+  auto expert_of = [&](int u) {             // u / per_expert
+    const int a = __umulhi(u, inverse);     // (one too many where u * per_expert passes 2^32)
+    return a * per_expert > u ? a - 1 : a;
   };
-  int la = first / per_expert, lc = first - la * per_expert, ls = sub;
-  int ca = la, cc = lc;
+  int lj = 0, lu = ticket[0], ls = sub;     // the unit that is copied, and its next step
   const uint8_t* src = nullptr;             // the lane's piece of the first rows
   const float* scale = nullptr;             // lanes 0, 1: the gate rows' two; 2, 3: the up rows'
   auto aim = [&]() {
-    const int64_t row = static_cast<int64_t>(r.active[la]) * 2 * p.I + lc * 8;
+    const int a = expert_of(lu);
+    const int64_t row = static_cast<int64_t>(r.active[a]) * 2 * p.I + (lu - a * per_expert) * 8;
     src = p.w + (row + (lane >> 4)) * row_bytes + (lane & 15) * 16 + sub * kStepBytes;
     if constexpr (kFP8)
       scale = p.w_scales + (row + (lane & 2 ? p.I : 0)) / 128 * nkb + 2 * sub + (lane & 1);
   };
-  if (la < active) aim();
+  if (lu < units) aim();
   auto copy = [&](int slot) {
-    if (la < active) {
+    if (lu < units) {
       copy_step(ring + slot * kSlot, src, row_bytes, to_up, 2 * ls + 1 < nkb);
       src += share * kStepBytes;
       if constexpr (kFP8) {
@@ -388,8 +368,8 @@ __global__ void __launch_bounds__(kWarps * 32, kWarps == 8 ? 2 : 1) few_up_kerne
       ls += share;
       if (ls >= steps) {
         ls = sub;
-        step_unit(la, lc);
-        if (la < active) aim();
+        lu = ticket[++lj & 7];
+        if (lu < units) aim();
       }
     }
     cp_commit();
@@ -404,9 +384,10 @@ __global__ void __launch_bounds__(kWarps * 32, kWarps == 8 ? 2 : 1) few_up_kerne
   const float* xs = s_xs + 2 * t;
   const uint32_t half0 = piece_at(g, t), half1 = piece_at(g, 4 + t);
   int slot = 0, parity = 0;
-  while (ca < active) {
-    const int a = ca, i0 = cc * 8;
-    step_unit(ca, cc);
+  for (int j = 0, u = ticket[0]; u < units; u = ticket[++j & 7]) {
+    int drawn = 0;
+    if (sub == 0 && lane == 0) drawn = ahead * groups + atomicAdd(&p.ctrl->queue, 1u);
+    const int a = expert_of(u), i0 = (u - a * per_expert) * 8;
     const uint32_t tokens = r.tokens_of(a);
     float acc[kGroups][4];
 #pragma unroll
@@ -444,8 +425,11 @@ __global__ void __launch_bounds__(kWarps * 32, kWarps == 8 ? 2 : 1) few_up_kerne
       copy(slot);
       slot = slot == kDepth - 1 ? 0 : slot + 1;
     }
+    if (sub == 0 && lane == 0) ticket[(j + ahead) & 7] = drawn;
     // the sharing warps' sums meet in the first of them
-    if (share > 1) {
+    if (share == 1) {
+      __syncwarp();
+    } else {
       constexpr bool kTwo = red_buffers(kGroups, kWarps) == 2;
       float4* red = s_red + parity * kWarps * kGroups * 32;
       if (kTwo) parity ^= 1;
@@ -456,10 +440,10 @@ __global__ void __launch_bounds__(kWarps * 32, kWarps == 8 ? 2 : 1) few_up_kerne
               make_float4(acc[n][0], acc[n][1], acc[n][2], acc[n][3]);
       asm volatile("bar.sync %0, %1;" ::"r"(1 + warp / share), "r"(share * 32) : "memory");
       if (sub == 0)
-        for (int j = 1; j < share; ++j)
+        for (int w = 1; w < share; ++w)
 #pragma unroll
           for (int n = 0; n < kGroups; ++n) {
-            const float4 v = red[((warp + j) * kGroups + n) * 32 + lane];
+            const float4 v = red[((warp + w) * kGroups + n) * 32 + lane];
             acc[n][0] += v.x;
             acc[n][1] += v.y;
             acc[n][2] += v.z;
@@ -500,7 +484,7 @@ template <bool kFP8, int kGroups, int kWarps, int kDepth>
 __global__ void __launch_bounds__(kWarps * 32, kWarps == 8 ? 2 : 1)
     few_down_kernel(const FewParams p) {
   extern __shared__ __align__(16) uint8_t smem[];
-  constexpr int kCols = 8 * kGroups, kMaxParts = kWarps / 4;
+  constexpr int kCols = 8 * kGroups;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
   const Routing r(smem, p.T, p.k, p.E);
   uint8_t* s_h = smem + Routing::bytes(p.T, p.k, p.E);
@@ -514,16 +498,16 @@ __global__ void __launch_bounds__(kWarps * 32, kWarps == 8 ? 2 : 1)
   const int parts = kWarps / p.tiles;                           // take its steps in turn
   const int n_cta = blockIdx.x / cluster * p.tiles * 16, n0 = n_cta + tile * 16;
   const bool idle = n0 >= p.H;                                  // (H is a multiple of 16)
-  route_tokens(p, r, reinterpret_cast<float*>(s_part));
-  const int active = route_join(p, r);
+  // (the up kernel has begun, so the routing is done)
+  route_clear(p, r);
+  const int active = route_join<true>(p, r);
   __syncthreads();
 
   // this CTA's share of the steps (two blocks each, expert by expert)
   const int row_bytes = p.I * (kFP8 ? 1 : 2);
   const int nkb = row_bytes / 128, per = (nkb + 1) / 2;
-  const int64_t all = static_cast<int64_t>(active) * per;
-  const int s0 = static_cast<int>(all * rank / cluster);
-  const int s1 = static_cast<int>(all * (rank + 1) / cluster);
+  const int all = active * per;             // (at most 512 * 256)
+  const int s0 = all * rank / cluster, s1 = all * (rank + 1) / cluster;
 
   int ls = s0 + part, la = ls / per, lp = ls - la * per;
   const int la0 = la, lp0 = lp;
@@ -564,9 +548,9 @@ __global__ void __launch_bounds__(kWarps * 32, kWarps == 8 ? 2 : 1)
   // Row of block kb of expert a's first token, counted over all of them: those of a block are
   // neighbours, then come the expert's next blocks.
   auto row_at = [&](int a, int kb) { return r.before[a] * nkb + (r.before[a + 1] - r.before[a]) * kb; };
-  auto row_of_step = [&](int64_t s) {
-    const int a = static_cast<int>(s / per);
-    return a >= active ? r.before[active] * nkb : row_at(a, 2 * static_cast<int>(s - static_cast<int64_t>(a) * per));
+  auto row_of_step = [&](int s) {
+    const int a = s / per;
+    return a >= active ? r.before[active] * nkb : row_at(a, 2 * (s - a * per));
   };
   bool waited = false;                      // for the up kernel: nothing so far depends on it
   int slot = 0;
@@ -601,11 +585,12 @@ __global__ void __launch_bounds__(kWarps * 32, kWarps == 8 ? 2 : 1)
     __syncthreads();
     if (!waited) pdl_wait();
     waited = true;
-    // h times its route's weight, in the MMA's types; four rows' loads in flight
-    for (int i0 = warp; i0 < rows; i0 += 4 * kWarps) {
-      float v[4][4];
+    // h times its route's weight, in the MMA's types; eight rows' loads in flight
+    constexpr int kAtOnce = 8;
+    for (int i0 = warp; i0 < rows; i0 += kAtOnce * kWarps) {
+      float v[kAtOnce][4];
 #pragma unroll
-      for (int j = 0; j < 4; ++j) {
+      for (int j = 0; j < kAtOnce; ++j) {
         const int i = i0 + j * kWarps;
         if (i >= rows) break;
         const float* src = p.h + static_cast<size_t>(s_what[i] & 0xffff) * p.I;
@@ -619,7 +604,7 @@ __global__ void __launch_bounds__(kWarps * 32, kWarps == 8 ? 2 : 1)
         }
       }
 #pragma unroll
-      for (int j = 0; j < 4; ++j) {
+      for (int j = 0; j < kAtOnce; ++j) {
         const int i = i0 + j * kWarps;
         if (i >= rows) break;
         const float weight = r.weights[s_what[i] & 0xffff];
@@ -698,12 +683,29 @@ __global__ void __launch_bounds__(kWarps * 32, kWarps == 8 ? 2 : 1)
   }
   if (!waited) pdl_wait();
   pdl_launch_dependents();
-  // the shares meet, in the order of ranks and parts: rank r adds its part of the rows
+  if (blockIdx.x == 0 && threadIdx.x == 0) p.ctrl->queue = 0;   // for the next up kernel
+  // a tile's parts meet in the first of them, then the shares, in the ranks' order: rank r adds its
+  // part of the rows
+  auto part_at = [&](int q, int n, int i) -> float& {
+    return s_part[((q * p.tiles + tile) * 16 + g + 8 * (i >> 1)) * kCols + 8 * n + 2 * t + (i & 1)];
+  };
+  if (part > 0)
 #pragma unroll
-  for (int n = 0; n < kGroups; ++n)
+    for (int n = 0; n < kGroups; ++n)
 #pragma unroll
-    for (int i = 0; i < 4; ++i)
-      s_part[((part * p.tiles + tile) * 16 + g + 8 * (i >> 1)) * kCols + 8 * n + 2 * t + (i & 1)] = acc[n][i];
+      for (int i = 0; i < 4; ++i) part_at(part, n, i) = acc[n][i];
+  __syncthreads();
+  if (part == 0) {
+    for (int q = 1; q < parts; ++q)
+#pragma unroll
+      for (int n = 0; n < kGroups; ++n)
+#pragma unroll
+        for (int i = 0; i < 4; ++i) acc[n][i] += part_at(q, n, i);
+#pragma unroll
+    for (int n = 0; n < kGroups; ++n)
+#pragma unroll
+      for (int i = 0; i < 4; ++i) part_at(0, n, i) = acc[n][i];
+  }
   asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory");
   asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory");
   const int rows = p.tiles * 16 / cluster;
@@ -711,23 +713,19 @@ __global__ void __launch_bounds__(kWarps * 32, kWarps == 8 ? 2 : 1)
     const int tok = i / rows, row = rank * rows + i - tok * rows;
     const int n = n_cta + row;
     if (n >= p.H) continue;
-    float v[kCluster * kMaxParts];
+    const uint32_t mine = smem_u32(s_part + row * kCols + tok);
+    float v[kCluster];
 #pragma unroll
-    for (int c = 0; c < kCluster; ++c)
-#pragma unroll
-      for (int q = 0; q < kMaxParts; ++q) {
-        float& x = v[c * kMaxParts + q];
-        x = 0.0f;
-        if (c >= cluster || q >= parts) continue;
-        uint32_t at;
-        asm volatile("mapa.shared::cluster.u32 %0, %1, %2;"
-                     : "=r"(at)
-                     : "r"(smem_u32(s_part + ((q * p.tiles * 16) + row) * kCols + tok)), "r"(c));
-        asm volatile("ld.shared::cluster.f32 %0, [%1];" : "=f"(x) : "r"(at));
-      }
+    for (int c = 0; c < kCluster; ++c) {
+      v[c] = 0.0f;
+      if (c >= cluster) continue;
+      uint32_t at;
+      asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(at) : "r"(mine), "r"(c));
+      asm volatile("ld.shared::cluster.f32 %0, [%1];" : "=f"(v[c]) : "r"(at));
+    }
     float sum = v[0];
 #pragma unroll
-    for (int c = 1; c < kCluster * kMaxParts; ++c) sum += v[c];
+    for (int c = 1; c < kCluster; ++c) sum += v[c];
     p.out[static_cast<size_t>(tok) * p.H + n] = __float2bfloat16_rn(sum);
   }
   asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory");
@@ -766,6 +764,24 @@ cudaError_t launch_down(const FewParams& p, cudaStream_t stream) {
   return cudaLaunchKernelEx(&cfg, kernel, p);
 }
 
+// Warps that share a unit: the fewest steps of the longest warp if all routes go to experts of their
+// own, a step and a half more for a join (one token through 8 FP8 experts: 15, 16 and 18 us with 2,
+// 4 and 8; 16 tokens through 69: 66, 66, 69, 77 with 1 to 8; 5 through 18 BF16 experts: 116, 112 and 111
+// with 2, 4 and 8).
+int unit_share(const FewParams& p, bool fp8, int warps, int sms) {
+  const int steps = (p.H * (fp8 ? 1 : 2) / 128 + 1) / 2;
+  const int64_t units = static_cast<int64_t>(Routing::most(p.T, p.k, p.E)) * p.I / 8;
+  int share = 1;
+  double best = 1e30;
+  for (int n = 1; n <= warps && n <= steps; n *= 2) {
+    const int64_t groups = static_cast<int64_t>(sms) * (warps / n);
+    const double cost = static_cast<double>((units + groups - 1) / groups) *
+                        ((steps + n - 1) / n + (n > 1 ? 1.5 : 0.0));
+    if (cost < best) best = cost, share = n;
+  }
+  return share;
+}
+
 template <bool kFP8, int kGroups>
 cudaError_t launch_few(FewParams p, int sms, cudaStream_t stream) {
   // 8 warps an SM leave room for the down kernel's CTAs beside the up kernel's, which pays where the
@@ -777,11 +793,16 @@ cudaError_t launch_few(FewParams p, int sms, cudaStream_t stream) {
   p.tiles = (p.H + 63) / 64 <= sms ? 4 : 8;
   const int chunks = (p.H + p.tiles * 16 - 1) / (p.tiles * 16);
   p.cluster = chunks * 8 <= sms * 3 / 4 ? 8 : chunks * 4 <= sms * 15 / 16 ? 4 : chunks * 2 <= sms ? 2 : 1;
-  // rows of h at a time: all of a share's, if they are spread evenly, but no more than 48 KB
-  const int64_t even = static_cast<int64_t>(p.T) * p.k * p.I * (kFP8 ? 1 : 2) / 128 / p.cluster;
-  p.h_rows = even * 5 / 4 + 32 < 160 ? static_cast<int>(even * 5 / 4 + 32) / 4 * 4 : 160;
+  // rows of h at a time: all of a share's if they are spread evenly, as far as there is room
+  const int64_t even = static_cast<int64_t>(p.T) * p.k * p.I * (kFP8 ? 1 : 2) / 128 / p.cluster * 5 / 4 + 32;
+  p.h_rows = 0;
+  const int fixed = small ? down_smem<kFP8, kGroups, 8, 3>(p) : down_smem<kFP8, kGroups, 16, 2>(p);
+  const int64_t room = ((small ? kMaxSmem / 2 : kMaxSmem) - fixed) / (h_pitch<kFP8>() + 8);
+  p.h_rows = static_cast<int>(even < room ? even : room < 32 ? 32 : room) / 4 * 4;
   cudaError_t e;
-  if (!small && up_smem<kFP8, kGroups, 16, 2>(p) <= kMaxSmem)
+  const bool wide = !small && up_smem<kFP8, kGroups, 16, 2>(p) <= kMaxSmem;
+  p.share = unit_share(p, kFP8, wide ? 16 : 8, sms);
+  if (wide)
     e = launch_up<kFP8, kGroups, 16, 2>(p, sms, stream);
   else if (up_smem<kFP8, kGroups, 8, 3>(p) <= kMaxSmem)
     e = launch_up<kFP8, kGroups, 8, 3>(p, sms, stream);
@@ -801,10 +822,15 @@ cudaError_t launch_few_experts(const moe_forward_args& f, void* out, uint8_t* ws
   int most = 65536 / f.K;
   if (most > kMaxTok) most = kMaxTok;
   const int passes = (f.M + most - 1) / most;
+  int32_t* ids = reinterpret_cast<int32_t*>(ws + MOE_CTRL_BYTES);
+  float* weights = reinterpret_cast<float*>(ids + kMaxTok * 32);
+  cudaError_t e = launch_route(f.logits, f.M, f.E, f.top_k, f.softcap, f.renorm, ids, weights, stream, true);
+  if (e != cudaSuccess) return e;
   for (int i = 0; i < passes; ++i) {
     const int t0 = f.M * i / passes, t1 = f.M * (i + 1) / passes;
     FewParams p;
-    p.logits = f.logits + static_cast<size_t>(t0) * f.E;
+    p.ids = ids + t0 * f.top_k;
+    p.weights = weights + t0 * f.top_k;
     p.x = static_cast<const __nv_bfloat16*>(f.x) + static_cast<size_t>(t0) * f.K;
     p.w = static_cast<const uint8_t*>(f.w);
     p.w_scales = f.w_scales;
@@ -813,15 +839,12 @@ cudaError_t launch_few_experts(const moe_forward_args& f, void* out, uint8_t* ws
     p.out = static_cast<__nv_bfloat16*>(out) + static_cast<size_t>(t0) * f.K;
     p.ctrl = reinterpret_cast<Ctrl*>(ws);
     // (every pass has the same place: its kernels wait for those of the pass before)
-    p.h = reinterpret_cast<float*>(ws + MOE_CTRL_BYTES);
+    p.h = weights + kMaxTok * 32;
     p.T = t1 - t0;
     p.H = f.K;
     p.I = f.N;
     p.E = f.E;
     p.k = f.top_k;
-    p.softcap = f.softcap;
-    p.renorm = f.renorm;
-    cudaError_t e;
     if (fp8)
       e = p.T <= 8 ? launch_few<true, 1>(p, num_sms, stream) : launch_few<true, 2>(p, num_sms, stream);
     else

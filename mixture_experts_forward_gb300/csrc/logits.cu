@@ -45,6 +45,7 @@ struct LogitsParams {
   const uint32_t* mask;
   Ctrl* ctrl;
   int m, V, history_stride, biases, part, cluster;
+  int rows;                                 // rows of a sequence that a cluster takes
 };
 
 // A CTA's share of a row: its maximum, where that is first, and the sum of exponentials.
@@ -57,80 +58,88 @@ template <typename T, int kPer, bool kProbs>
 __global__ void __launch_bounds__(kLThreads, kPer <= 8 ? 3 : kPer <= 32 ? 2 : 1)
     logits_kernel(const LogitsParams<T> p) {
   extern __shared__ uint32_t s_count[];     // [part], then the biases' tokens and values
-  __shared__ Share s_share[kLMaxCluster];   // every CTA of the cluster writes its own here
+  __shared__ Share s_share[2][kLMaxCluster];   // every CTA of the cluster writes its own here
   __shared__ float s_max[kLWarps], s_sum[kLWarps];
   __shared__ int s_at[kLWarps];
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int rank = blockIdx.x % p.cluster;
-  const int row = blockIdx.x / p.cluster;
-  const int b = row / p.m, i = row - b * p.m;
+  const int group = blockIdx.x / p.cluster;           // p.rows rows of a sequence
+  const int groups = (p.m + p.rows - 1) / p.rows;     // of a sequence
+  const int b = group / groups, i0 = (group - b * groups) * p.rows, i1 = min(p.m, i0 + p.rows);
   const int v0 = rank * p.part, n = min(p.part, p.V - v0);    // n may be <= 0
+  constexpr int kWords = (kPer + 31) / 32;
   pdl_wait();
   pdl_launch_dependents();
   if (kProbs && p.cluster > 1)              // (before any CTA writes to another)
     asm volatile("barrier.cluster.arrive.relaxed.aligned;" ::: "memory");
 
-  const T* src = p.logits + b * p.l_sb + i * p.l_si + v0;
   float l[kPer];
+  uint32_t words[kWords];                   // word j of the mask for this warp's tokens of turn j, by lane j
+  auto load_row = [&](int i) {
+    const T* src = p.logits + b * p.l_sb + i * p.l_si + v0 + tid;
 #pragma unroll
-  for (int j = 0; j < kPer; ++j) {
-    const int at = tid + j * kLThreads;
-    l[j] = at < n ? load_logit(src + at) : neg_inf();
-  }
-
-  // word j of the mask for this warp's tokens of turn j, by lane j
-  constexpr int kWords = (kPer + 31) / 32;
-  uint32_t words[kWords];
+    for (int j = 0; j < kPer; ++j)
+      l[j] = tid + j * kLThreads < n ? load_logit(src + j * kLThreads) : neg_inf();
 #pragma unroll
-  for (int w = 0; w < kWords; ++w) {
-    const int at = (warp + (32 * w + lane) * kLWarps) * 32;
-    words[w] = 0xffffffffu;
-    if (p.mask != nullptr && 32 * w + lane < kPer && at < n)
-      words[w] = __ldg(p.mask + b * p.m_sb + i * p.m_si + (v0 + at) / 32);
-  }
+    for (int w = 0; w < kWords; ++w) {
+      const int at = (warp + (32 * w + lane) * kLWarps) * 32;
+      words[w] = 0xffffffffu;
+      if (p.mask != nullptr && 32 * w + lane < kPer && at < n)
+        words[w] = __ldg(p.mask + b * p.m_sb + i * p.m_si + (v0 + at) / 32);
+    }
+  };
+  load_row(i0);
 
   // the counts
   int32_t* s_bias_t = reinterpret_cast<int32_t*>(s_count + p.part);
   float* s_bias_v = reinterpret_cast<float*>(s_bias_t + p.biases);
   const bool counts = p.history != nullptr || p.draft != nullptr || p.biases > 0;
+  auto count = [&](int v, uint32_t what) {
+    if (v < 0 || v >= p.V) {
+      if (v != -1) set_error(p.ctrl, MOE_ERR_DEVICE_FAULT, 40);
+      return;
+    }
+    v -= v0;
+    if (v < 0 || v >= n) return;
+    if (what < 4) atomicOr(s_count + v, what); else atomicAdd(s_count + v, what);
+  };
   if (counts) {
-    for (int at = tid; at < p.part / 4; at += kLThreads)
-      reinterpret_cast<uint4*>(s_count)[at] = make_uint4(0u, 0u, 0u, 0u);
-    __syncthreads();
-    auto count = [&](int v, uint32_t what) {
-      if (v < 0 || v >= p.V) {
-        if (v != -1) set_error(p.ctrl, MOE_ERR_DEVICE_FAULT, 40);
-        return;
-      }
-      v -= v0;
-      if (v < 0 || v >= n) return;
-      if (what < 4) atomicOr(s_count + v, what); else atomicAdd(s_count + v, what);
-    };
+    int len = 0, prompt = 0;
     if (p.history != nullptr) {
-      int len = p.history_stride, prompt = 0;
-      if (p.history_lens != nullptr) len = __ldg(p.history_lens + b);
+      len = p.history_lens != nullptr ? __ldg(p.history_lens + b) : p.history_stride;
       if (p.prompt_lens != nullptr) prompt = __ldg(p.prompt_lens + b);
       if (len < 0 || len > p.history_stride || prompt < 0 || prompt > len) {
         if (tid == 0) set_error(p.ctrl, MOE_ERR_DEVICE_FAULT, 41);
         len = min(max(len, 0), p.history_stride);
         prompt = min(max(prompt, 0), len);
       }
-      const int32_t* h = p.history + static_cast<int64_t>(b) * p.history_stride;
-      for (int at = tid; at < len; at += 4 * kLThreads) {
-        int v[4];
-#pragma unroll
-        for (int j = 0; j < 4; ++j)
-          v[j] = at + j * kLThreads < len ? __ldg(h + at + j * kLThreads) : -1;
-#pragma unroll
-        for (int j = 0; j < 4; ++j) count(v[j], at + j * kLThreads < prompt ? 1u : 4u);
-      }
     }
-    if (p.draft != nullptr && tid < i) count(__ldg(p.draft + b * (p.m - 1) + tid), 4u);
+    for (int at = tid; at < p.part / 4; at += kLThreads)
+      reinterpret_cast<uint4*>(s_count)[at] = make_uint4(0u, 0u, 0u, 0u);
+    const int32_t* h = p.history + static_cast<int64_t>(b) * p.history_stride;
+    constexpr int kAtOnce = 4;
+    int v[kAtOnce];
+    auto load = [&](int at) {
+#pragma unroll
+      for (int j = 0; j < kAtOnce; ++j)
+        v[j] = at + j * kLThreads < len ? __ldg(h + at + j * kLThreads) : -1;
+    };
+    load(tid);
+    __syncthreads();
+    for (int at = tid; at < len; at += kAtOnce * kLThreads) {
+      int now[kAtOnce];
+#pragma unroll
+      for (int j = 0; j < kAtOnce; ++j) now[j] = v[j];
+      load(at + kAtOnce * kLThreads);
+#pragma unroll
+      for (int j = 0; j < kAtOnce; ++j) count(now[j], at + j * kLThreads < prompt ? 1u : 4u);
+    }
+    if (p.draft != nullptr && tid < i0) count(__ldg(p.draft + b * (p.m - 1) + tid), 4u);
     for (int at = tid; at < p.biases; at += kLThreads) {
-      const int v = __ldg(p.bias_tokens + static_cast<int64_t>(b) * p.biases + at);
-      s_bias_t[at] = v;
+      const int t = __ldg(p.bias_tokens + static_cast<int64_t>(b) * p.biases + at);
+      s_bias_t[at] = t;
       s_bias_v[at] = __ldg(p.bias_values + static_cast<int64_t>(b) * p.biases + at);
-      count(v, 2u);
+      count(t, 2u);
     }
     __syncthreads();
   }
@@ -142,146 +151,168 @@ __global__ void __launch_bounds__(kLThreads, kPer <= 8 ? 3 : kPer <= 32 ? 2 : 1)
     if (!(rep > 0.0f)) rep = 1.0f;
     if (!(temp >= 0.0f)) temp = 1.0f;
   }
+  const float inverse = __fdiv_rn(1.0f, rep);
 
-  uint32_t biased[kWords] = {};             // bit j: this thread's value j has a bias
-#pragma unroll
-  for (int j = 0; j < kPer; ++j) {
-    const int at = tid + j * kLThreads;
-    const uint32_t c = counts ? s_count[at] : 0u;
-    if (c != 0) {
-      if ((c & ~2u) != 0) l[j] = l[j] > 0.0f ? __fdiv_rn(l[j], rep) : l[j] * rep;
-      if (c >= 4) l[j] = l[j] - frequency * static_cast<float>(c >> 2) - presence;
-      biased[j / 32] |= ((c >> 1) & 1u) << (j % 32);
+  for (int i = i0; i < i1; ++i) {
+    if (i > i0) {
+      // the next row: one more draft, by the thread that the barrier below orders before the counts' readers
+      if (counts && p.draft != nullptr) {
+        if (!kProbs) __syncthreads();       // (with probabilities the exchange has ordered the readers before)
+        if (tid == 0) count(__ldg(p.draft + b * (p.m - 1) + i - 1), 4u);
+        __syncthreads();
+      }
+      load_row(i);
     }
-    const uint32_t word = __shfl_sync(0xffffffffu, words[j / 32], j % 32);
-    if (((word >> lane) & 1u) == 0 || !(l[j] >= neg_inf())) l[j] = neg_inf();   // (or NaN)
-  }
+    uint32_t biased[kWords] = {};           // bit j: this thread's value j has a bias
 #pragma unroll
-  for (int w = 0; w < kWords; ++w) {
-    const uint32_t any = __reduce_or_sync(0xffffffffu, biased[w]);
-    if (any == 0) continue;
+    for (int j = 0; j < kPer; ++j) {
+      const uint32_t c = counts ? s_count[tid + j * kLThreads] : 0u;
+      if (c != 0) {
+        if ((c & ~2u) != 0) l[j] *= l[j] > 0.0f ? inverse : rep;
+        if (c >= 4) l[j] = l[j] - frequency * static_cast<float>(c >> 2) - presence;
+        biased[j / 32] |= ((c >> 1) & 1u) << (j % 32);
+      }
+      const uint32_t word = __shfl_sync(0xffffffffu, words[j / 32], j % 32);
+      if (((word >> lane) & 1u) == 0 || !(l[j] >= neg_inf())) l[j] = neg_inf();   // (or NaN)
+    }
 #pragma unroll
-    for (int j = 32 * w; j < (kPer < 32 * w + 32 ? kPer : 32 * w + 32); ++j) {
-      if (((any >> (j % 32)) & 1u) == 0) continue;
-      uint32_t lanes = __ballot_sync(0xffffffffu, (biased[w] >> (j % 32)) & 1u);
-      for (; lanes != 0; lanes &= lanes - 1) {
-        const int who = __ffs(lanes) - 1;
-        const int v = v0 + warp * 32 + j * kLThreads + who;
-        for (int q = 0; q < p.biases; q += 32) {
-          const bool mine = q + lane < p.biases && s_bias_t[q + lane] == v;
-          uint32_t found = __ballot_sync(0xffffffffu, mine);
-          for (; found != 0; found &= found - 1)
-            if (lane == who && l[j] > neg_inf()) l[j] += s_bias_v[q + __ffs(found) - 1];
+    for (int w = 0; w < kWords; ++w) {
+      const uint32_t any = __reduce_or_sync(0xffffffffu, biased[w]);
+      if (any == 0) continue;
+#pragma unroll
+      for (int j = 32 * w; j < (kPer < 32 * w + 32 ? kPer : 32 * w + 32); ++j) {
+        if (((any >> (j % 32)) & 1u) == 0) continue;
+        uint32_t lanes = __ballot_sync(0xffffffffu, (biased[w] >> (j % 32)) & 1u);
+        float add = l[j];
+        for (; lanes != 0; lanes &= lanes - 1) {
+          const int who = __ffs(lanes) - 1;
+          const int v = v0 + warp * 32 + j * kLThreads + who;
+          for (int q = 0; q < p.biases; q += 32) {
+            const bool mine = q + lane < p.biases && s_bias_t[q + lane] == v;
+            uint32_t found = __ballot_sync(0xffffffffu, mine);
+            for (; found != 0; found &= found - 1)
+              if (lane == who && add > neg_inf()) add += s_bias_v[q + __ffs(found) - 1];
+          }
         }
+        l[j] = add >= neg_inf() ? add : neg_inf();
       }
-      if (!(l[j] >= neg_inf())) l[j] = neg_inf();
     }
-  }
-  float top = neg_inf();
+    float* out = p.out + b * p.o_sb + i * p.o_si + v0 + tid;
+    if constexpr (!kProbs) {
 #pragma unroll
-  for (int j = 0; j < kPer; ++j) top = fmaxf(top, l[j]);
-  float* out = p.out + b * p.o_sb + i * p.o_si + v0;
-  if constexpr (!kProbs) {
-#pragma unroll
-    for (int j = 0; j < kPer; ++j) {
-      const int at = tid + j * kLThreads;
-      if (at < n) out[at] = l[j];
-    }
-    return;
-  } else {
-    // the CTA's maximum, then (greedy) its first place or the sum
-    auto all_max = [&](float x) {
-#pragma unroll
-      for (int o = 16; o > 0; o >>= 1) x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, o));
-      return x;
-    };
-    top = all_max(top);
-    if (lane == 0) s_max[warp] = top;
-    __syncthreads();
-    top = s_max[0];
-#pragma unroll
-    for (int w = 1; w < kLWarps; ++w) top = fmaxf(top, s_max[w]);
-    const bool greedy = temp == 0.0f;
-    int first = 0x7fffffff;
-    float sum = 0.0f;
-    // exp((l - top) / temp) as a power of two; at the ends of the types: a token at the maximum is 1
-    // (also +inf), one at -inf is 0
-    const float rate = greedy ? 0.0f : fminf(__fdividef(1.4426950408889634f, temp), 3.0e38f);
-    if (greedy) {
-#pragma unroll
-      for (int j = kPer - 1; j >= 0; --j)
-        if (l[j] == top && top > neg_inf()) first = v0 + tid + j * kLThreads;
-      first = __reduce_min_sync(0xffffffffu, first);
-      if (lane == 0) s_at[warp] = first;
+      for (int j = 0; j < kPer; ++j)
+        if (tid + j * kLThreads < n) out[j * kLThreads] = l[j];
     } else {
+      // the CTA's maximum, then (greedy) its first place or the sum
+      float top = neg_inf();
 #pragma unroll
-      for (int j = 0; j < kPer; ++j) {
-        const float d = (l[j] - top) * rate;
-        float e;
-        asm("ex2.approx.f32 %0, %1;" : "=f"(e) : "f"(d));
-        e = l[j] == top ? 1.0f : e;
-        e = l[j] == neg_inf() ? 0.0f : e;
-        l[j] = e;
-        sum += e;
-      }
+      for (int j = 0; j < kPer; ++j) top = fmaxf(top, l[j]);
 #pragma unroll
-      for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
-      if (lane == 0) s_sum[warp] = sum;
-    }
-    __syncthreads();
-    Share mine = {top, 0.0f, 0x7fffffff, 0};
-    if (greedy) {
-#pragma unroll
-      for (int w = 0; w < kLWarps; ++w) mine.at = min(mine.at, s_at[w]);
-    } else {
-#pragma unroll
-      for (int w = 0; w < kLWarps; ++w) mine.sum += s_sum[w];
-    }
-    if (p.cluster > 1) {
-      asm volatile("barrier.cluster.wait.aligned;" ::: "memory");
-      if (tid < p.cluster) {
-        uint32_t at;
-        asm volatile("mapa.shared::cluster.u32 %0, %1, %2;"
-                     : "=r"(at)
-                     : "r"(static_cast<uint32_t>(__cvta_generic_to_shared(s_share + rank))), "r"(tid));
-        asm volatile("st.shared::cluster.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(at),
-                     "r"(__float_as_uint(mine.max)), "r"(__float_as_uint(mine.sum)), "r"(mine.at),
-                     "r"(0)
-                     : "memory");
-      }
-      asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory");
-      asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory");
-    } else {
-      if (tid == 0) s_share[0] = mine;
+      for (int o = 16; o > 0; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
+      if (lane == 0) s_max[warp] = top;
       __syncthreads();
-    }
-    float all = neg_inf(), total = 0.0f;
-    int choice = 0x7fffffff;
-    for (int c = 0; c < p.cluster; ++c) all = fmaxf(all, s_share[c].max);
-    auto factor = [&](float m) {
-      float f;
-      asm("ex2.approx.f32 %0, %1;" : "=f"(f) : "f"((m - all) * rate));
-      return m == all ? 1.0f : m == neg_inf() ? 0.0f : f;
-    };
-    for (int c = 0; c < p.cluster; ++c) {
-      const Share s = s_share[c];
-      if (s.max == all) choice = min(choice, s.at);
-      total += s.sum * factor(s.max);
-    }
-    const float scale = all == neg_inf() ? 0.0f : __fdiv_rn(factor(top), total);
+      top = s_max[0];
 #pragma unroll
-    for (int j = 0; j < kPer; ++j) {
-      const int at = tid + j * kLThreads;
-      const float y = greedy ? (v0 + at == choice ? 1.0f : 0.0f) : l[j] * scale;
-      if (at < n) out[at] = y;
+      for (int w = 1; w < kLWarps; ++w) top = fmaxf(top, s_max[w]);
+      const bool greedy = temp == 0.0f;
+      int first = 0x7fffffff;
+      float sum = 0.0f;
+      // exp((l - top) / temp) as a power of two; the rate stays between the ends of the type, so
+      // that a difference of 0 gives 1 and one of -inf gives 0
+      const float rate = fminf(fmaxf(__fdiv_rn(1.4426950408889634f, temp), 1.2e-38f), 3.0e38f);
+      if (greedy) {
+#pragma unroll
+        for (int j = kPer - 1; j >= 0; --j)
+          if (l[j] == top && top > neg_inf()) first = v0 + tid + j * kLThreads;
+        first = __reduce_min_sync(0xffffffffu, first);
+        if (lane == 0) s_at[warp] = first;
+      } else {
+        if (top == -neg_inf()) {
+#pragma unroll
+          for (int j = 0; j < kPer; ++j) {
+            l[j] = l[j] == top ? 1.0f : 0.0f;
+            sum += l[j];
+          }
+        } else {
+          const float base = top == neg_inf() ? 0.0f : top;
+#pragma unroll
+          for (int j = 0; j < kPer; ++j) {
+            asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(l[j]) : "f"((l[j] - base) * rate));
+            sum += l[j];
+          }
+        }
+#pragma unroll
+        for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
+        if (lane == 0) s_sum[warp] = sum;
+      }
+      __syncthreads();
+      // the CTAs' shares (two buffers in turn: no CTA is two rows ahead of another)
+      Share* share = s_share[(i - i0) & 1];
+      if (p.cluster > 1) {
+        if (i == i0) asm volatile("barrier.cluster.wait.aligned;" ::: "memory");
+        if (tid < p.cluster) {
+          Share mine = {top, 0.0f, 0x7fffffff, 0};
+#pragma unroll
+          for (int w = 0; w < kLWarps; ++w)
+            if (greedy) mine.at = min(mine.at, s_at[w]); else mine.sum += s_sum[w];
+          uint32_t at;
+          asm volatile("mapa.shared::cluster.u32 %0, %1, %2;"
+                       : "=r"(at)
+                       : "r"(static_cast<uint32_t>(__cvta_generic_to_shared(share + rank))), "r"(tid));
+          asm volatile("st.shared::cluster.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(at),
+                       "r"(__float_as_uint(mine.max)), "r"(__float_as_uint(mine.sum)), "r"(mine.at),
+                       "r"(0)
+                       : "memory");
+        }
+        asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory");
+        asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory");
+      } else {
+        if (tid == 0) {
+          Share mine = {top, 0.0f, 0x7fffffff, 0};
+          for (int w = 0; w < kLWarps; ++w)
+            if (greedy) mine.at = min(mine.at, s_at[w]); else mine.sum += s_sum[w];
+          share[0] = mine;
+        }
+        __syncthreads();
+      }
+      float all = neg_inf(), total = 0.0f;
+      int choice = 0x7fffffff;
+      for (int c = 0; c < p.cluster; ++c) all = fmaxf(all, share[c].max);
+      auto factor = [&](float m) {
+        float f;
+        asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(f) : "f"((m - all) * rate));
+        return m == all ? 1.0f : m == neg_inf() ? 0.0f : f;
+      };
+      for (int c = 0; c < p.cluster; ++c) {
+        const Share s = share[c];
+        if (s.max == all) choice = min(choice, s.at);
+        total += s.sum * factor(s.max);
+      }
+      if (greedy) {
+#pragma unroll
+        for (int j = 0; j < kPer; ++j) l[j] = v0 + tid + j * kLThreads == choice ? 1.0f : 0.0f;
+      }
+      const float scale = greedy ? 1.0f : all == neg_inf() ? 0.0f : __fdiv_rn(factor(top), total);
+#pragma unroll
+      for (int j = 0; j < kPer; ++j)
+        if (tid + j * kLThreads < n) out[j * kLThreads] = l[j] * scale;
     }
   }
 }
 
 template <typename T, int kPer, bool kProbs>
-cudaError_t launch(LogitsParams<T> p, int rows, int cluster, cudaStream_t stream) {
+cudaError_t launch(LogitsParams<T> p, int B, int cluster, int num_sms, cudaStream_t stream) {
   p.part = kPer * kLThreads;
   p.cluster = cluster;
+  // Rows of a sequence that share their counts: what takes the fewest rounds of the clusters that
+  // find room, counting costs about half a row.
+  const int room = num_sms * (kPer <= 8 ? 3 : kPer <= 32 ? 2 : 1) / cluster;
+  double best = 1e30;
+  for (int rows = 1; rows <= p.m; ++rows) {
+    const int64_t clusters = static_cast<int64_t>(B) * ((p.m + rows - 1) / rows);
+    const double cost = static_cast<double>((clusters + room - 1) / room) * (rows + 0.5);
+    if (cost < best) best = cost, p.rows = rows;
+  }
   const int bytes = p.part * 4 + p.biases * 8;
   if (bytes > 48 * 1024) {
     const cudaError_t e = cudaFuncSetAttribute(logits_kernel<T, kPer, kProbs>,
@@ -290,8 +321,8 @@ cudaError_t launch(LogitsParams<T> p, int rows, int cluster, cudaStream_t stream
     if (e != cudaSuccess) return e;
   }
   cudaLaunchAttribute attr[2];
-  cudaLaunchConfig_t cfg = make_cfg(dim3(static_cast<unsigned>(rows) * cluster), dim3(kLThreads),
-                                    stream, true, attr);
+  const unsigned groups = static_cast<unsigned>(B) * ((p.m + p.rows - 1) / p.rows);
+  cudaLaunchConfig_t cfg = make_cfg(dim3(groups * cluster), dim3(kLThreads), stream, true, attr);
   attr[1].id = cudaLaunchAttributeClusterDimension;
   attr[1].val.clusterDim.x = kProbs ? cluster : 1;
   attr[1].val.clusterDim.y = 1;
@@ -302,19 +333,19 @@ cudaError_t launch(LogitsParams<T> p, int rows, int cluster, cudaStream_t stream
 }
 
 template <typename T, bool kProbs>
-cudaError_t launch_rows(const LogitsParams<T>& p, int rows, cudaStream_t stream) {
+cudaError_t launch_rows(const LogitsParams<T>& p, int B, int num_sms, cudaStream_t stream) {
   // As many CTAs of 4096 tokens as the row has, up to 8; longer rows give each CTA more.
   const int parts = (p.V + 4095) / 4096;
   const int cluster = parts >= 5 ? 8 : parts >= 3 ? 4 : parts;
   const int per = (p.V + cluster * kLThreads - 1) / (cluster * kLThreads);
-  if (per <= 8) return launch<T, 8, kProbs>(p, rows, cluster, stream);
-  if (per <= 16) return launch<T, 16, kProbs>(p, rows, cluster, stream);
-  if (per <= 32) return launch<T, 32, kProbs>(p, rows, cluster, stream);
-  return launch<T, 64, kProbs>(p, rows, cluster, stream);
+  if (per <= 8) return launch<T, 8, kProbs>(p, B, cluster, num_sms, stream);
+  if (per <= 16) return launch<T, 16, kProbs>(p, B, cluster, num_sms, stream);
+  if (per <= 32) return launch<T, 32, kProbs>(p, B, cluster, num_sms, stream);
+  return launch<T, 64, kProbs>(p, B, cluster, num_sms, stream);
 }
 
 template <typename T>
-cudaError_t launch_typed(const moe_logits_args& a, Ctrl* ctrl, cudaStream_t stream) {
+cudaError_t launch_typed(const moe_logits_args& a, Ctrl* ctrl, int num_sms, cudaStream_t stream) {
   LogitsParams<T> p = {};
   p.logits = static_cast<const T*>(a.logits);
   p.out = a.out;
@@ -337,16 +368,16 @@ cudaError_t launch_typed(const moe_logits_args& a, Ctrl* ctrl, cudaStream_t stre
   p.V = a.V;
   p.history_stride = a.history_stride;
   p.biases = a.biases;
-  const int rows = a.B * a.m;
-  return a.probabilities ? launch_rows<T, true>(p, rows, stream)
-                         : launch_rows<T, false>(p, rows, stream);
+  return a.probabilities ? launch_rows<T, true>(p, a.B, num_sms, stream)
+                         : launch_rows<T, false>(p, a.B, num_sms, stream);
 }
 
 }  // namespace
 
-cudaError_t launch_adjust_logits(const moe_logits_args& a, Ctrl* ctrl, cudaStream_t stream) {
-  return a.dtype == MOE_DTYPE_F32 ? launch_typed<float>(a, ctrl, stream)
-                                  : launch_typed<__nv_bfloat16>(a, ctrl, stream);
+cudaError_t launch_adjust_logits(const moe_logits_args& a, Ctrl* ctrl, int num_sms,
+                                 cudaStream_t stream) {
+  return a.dtype == MOE_DTYPE_F32 ? launch_typed<float>(a, ctrl, num_sms, stream)
+                                  : launch_typed<__nv_bfloat16>(a, ctrl, num_sms, stream);
 }
 
 }  // namespace moe

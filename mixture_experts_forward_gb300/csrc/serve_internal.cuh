@@ -87,10 +87,12 @@ cudaError_t launch_release_pages(const moe_page_state& p, const int32_t* keep, C
                                  int num_sms, cudaStream_t stream);
 cudaError_t launch_rotary(const moe_rotary_args& a, const KvCacheView* cache, Ctrl* ctrl,
                           int num_sms, cudaStream_t stream);
-// ws: the control block, then h in binary32, [M * top_k, N]
+// ws: kFewWsBytes (the control block and the routes), then h in binary32, [M * top_k, N]
+constexpr size_t kFewWsBytes = MOE_CTRL_BYTES + MOE_FEW_TOKENS * 32 * 8;
 cudaError_t launch_few_experts(const moe_forward_args& f, void* out, uint8_t* ws, int num_sms,
                                cudaStream_t stream);
-cudaError_t launch_adjust_logits(const moe_logits_args& a, Ctrl* ctrl, cudaStream_t stream);
+cudaError_t launch_adjust_logits(const moe_logits_args& a, Ctrl* ctrl, int num_sms,
+                                 cudaStream_t stream);
 cudaError_t launch_verify(const moe_verify_args& a, Ctrl* ctrl, int num_sms, cudaStream_t stream);
 
 }  // namespace moe

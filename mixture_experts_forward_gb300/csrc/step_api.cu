@@ -49,7 +49,7 @@ moe_status_t check_few(const moe_forward_args* f) {
 }
 
 size_t few_bytes(const moe_forward_args* f) {
-  return MOE_CTRL_BYTES + static_cast<size_t>(f->M) * f->top_k * f->N * 4;
+  return kFewWsBytes + static_cast<size_t>(f->M) * f->top_k * f->N * 4;
 }
 
 }  // namespace
@@ -219,7 +219,9 @@ moe_status_t moe_adjust_logits(const moe_logits_args* a, void* ws, void* stream)
   for (const void* w : words)
     if (!aligned_to(w, 4)) return MOE_ERR_INVALID_ARG;
   if (!ws_ok(ws)) return MOE_ERR_WORKSPACE;
-  return cuda_status(launch_adjust_logits(*a, static_cast<Ctrl*>(ws),
+  const int sms = device_sms();
+  if (sms <= 0) return MOE_ERR_CUDA;
+  return cuda_status(launch_adjust_logits(*a, static_cast<Ctrl*>(ws), sms,
                                           static_cast<cudaStream_t>(stream)));
 }
 
