@@ -571,9 +571,9 @@ def plan_step(lens: torch.Tensor, new_lens: torch.Tensor, block_table: torch.Ten
     p = _pages(what, block_table, held, free_pages, free_count, page_size)
     if not (_ints(lens, p.B) and _ints(new_lens, p.B)):
         _bad(what, "lens and new_lens are int32 [B]")
-    _placed(what, block_table, ws, held, free_pages, free_count, lens, new_lens)
     if rows < 0:
         _bad(what, "rows is not negative")
+    _placed(what, block_table, ws, held, free_pages, free_count, lens, new_lens)
     # one allocation for the four results
     B = p.B
     slots, positions, cu_q, kv_lens = _new((2 * rows + 2 * B + 1,), _I32, block_table.device,
@@ -753,12 +753,13 @@ def adjust_logits(logits: torch.Tensor, ws: torch.Tensor, history=None, history_
                 (mask.dim() == 2 or mask.shape[1] == m)):
             _bad(what, "mask is int32 [B, m, words] or [B, words] with contiguous rows")
         mb, mi = s[0], (s[1] if mask.dim() == 3 else 0)
+    if out is not None and not (out.dtype is _F32 and out.shape == logits.shape and
+                                (out.stride(2) == 1 or V == 1)):
+        _bad(what, "out is f32, shaped like logits, with contiguous rows")
     _placed(what, logits, ws, history, history_lens, prompt_lens, draft, repetition, presence,
             frequency, temperature, bias_tokens, bias_values, mask, out)
     if out is None:
         out = _new((B, m, V), _F32, logits.device, stream)
-    elif not (out.dtype is _F32 and out.shape == logits.shape and (out.stride(2) == 1 or V == 1)):
-        _bad(what, "out is f32, shaped like logits, with contiguous rows")
     ob, oi, _ = out.stride()
     p = lambda t: None if t is None else t.data_ptr()  # noqa: E731
     a = LogitsArgs(DTYPE_F32 if f32 else DTYPE_BF16, B, m, V, logits.data_ptr(), lb, li,

@@ -1,16 +1,21 @@
 // Penalties, biases and masks on logits, and their probabilities.
 //
-// A cluster of up to 8 CTAs takes one row, each CTA a contiguous part of the vocabulary that its
+// A cluster of up to 8 CTAs takes one row at a time, each CTA a contiguous part of the vocabulary that its
 // threads hold in registers (kPer values each, one load in flight per value), so the logits are
-// read once and the result is written once.  While the loads are under way the CTA counts the
+// read once and the result is written once.  While the first loads are under way the CTA counts the
 // history into shared memory, 32 bits a token of its part: bit 0 the prompt, bit 1 a bias, the
-// rest how often the token is among the outputs (integer atomics: the same in any order).  A token
-// whose word is zero is left as it is; biases of the same token are added by a warp that walks the
+// rest how often the token is among the outputs (integer atomics: the same in any order); further rows
+// of the sequence add one draft each.  Biases of the same token are added by a warp that walks the
 // list in its order.  The softmax is over the CTA's own maximum and sum, which the CTAs exchange
 // once over distributed shared memory (max, sum, and the first token of the maximum for greedy
 // rows) and join in rank order, so repeated calls give the same bits.
 // Rows begin at any multiple of the element size (odd vocabularies): one element per lane and
-// load.  Bound by HBM for batches, by the launch and the chain of dependent steps for single rows.
+// load.  Bound, for batches, by a row's chain of steps (the pass over the values, the maximum, the exponentials, the
+// exchange: 13 us with two CTAs an SM, where HBM would take 6; 576 rows of 131071 280 us) and for
+// single rows by the launch and the same chain (8 us).  Slower or no faster over both F32 drafts and
+// BF16 batches: quads on 16-byte boundaries with the next row copied ahead (270 and 91 us against 280 and 68),
+// values kept in shared memory with one exchange a row (278 and 92), that with chunks of 128 tokens dealt to the
+// CTAs in turn (272 and 99).
 #include "serve_internal.cuh"
 
 namespace moe {
@@ -49,7 +54,7 @@ struct LogitsParams {
 };
 
 // A CTA's share of a row: its maximum, where that is first, and the sum of exponentials.
-struct Share {
+struct alignas(16) Share {                 // (stored as one vector)
   float max, sum;
   int at, pad;
 };
@@ -57,7 +62,7 @@ struct Share {
 template <typename T, int kPer, bool kProbs>
 __global__ void __launch_bounds__(kLThreads, kPer <= 8 ? 3 : kPer <= 32 ? 2 : 1)
     logits_kernel(const LogitsParams<T> p) {
-  extern __shared__ uint32_t s_count[];     // [part], then the biases' tokens and values
+  extern __shared__ __align__(16) uint32_t s_count[];   // [part], then the biases' tokens and values
   __shared__ Share s_share[2][kLMaxCluster];   // every CTA of the cluster writes its own here
   __shared__ float s_max[kLWarps], s_sum[kLWarps];
   __shared__ int s_at[kLWarps];

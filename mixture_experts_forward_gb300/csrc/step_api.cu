@@ -16,7 +16,7 @@ moe_status_t check_pages(const moe_page_state* p) {
   if (p == nullptr) return MOE_ERR_INVALID_ARG;
   if (p->B < 0 || p->table_stride < 0 || p->page_size <= 0 || p->free_capacity < 0)
     return MOE_ERR_INVALID_ARG;
-  if (p->held == nullptr || p->free_count == nullptr ||
+  if ((p->held == nullptr && p->B > 0) || p->free_count == nullptr ||
       (p->block_table == nullptr && p->table_stride > 0 && p->B > 0) ||
       (p->free_pages == nullptr && p->free_capacity > 0))
     return MOE_ERR_INVALID_ARG;
