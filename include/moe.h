@@ -644,7 +644,7 @@ moe_status_t moe_rotary(const moe_rotary_args* args, void* ws, void* stream);
 #define MOE_FEW_TOKENS 16
 
 /* The whole gated expert layer for a few tokens (1 <= M <= MOE_FEW_TOKENS: single tokens, drafted
- * runs) in two kernels: the arguments and the result of moe_forward's gated FFN (BF16, or
+ * runs) in two kernels after the router's: the arguments and the result of moe_forward's gated FFN (BF16, or
  * FP8_E4M3 with gated = 1), each active expert's weights read once (above M * K = 65536 once for
  * every 65536 / K tokens).  K a multiple of 64 (BF16) or 128 (FP8), N of 128, both at most 32768.
  * Unlike moe_forward's FP8 form it quantises no activations: x enters as it is
@@ -672,7 +672,7 @@ typedef struct {
                                  0: the adjusted logits (the temperature is not used) */
   const int32_t* history;     /* [B, history_stride]: the prompt's tokens, then the outputs; -1 is
                                  skipped.  NULL: none */
-  int history_stride;
+  int history_stride;         /* below 2^20 - 63 */
   const int32_t* history_lens;  /* [B] (NULL: history_stride each) */
   const int32_t* prompt_lens;   /* [B] how many of them are the prompt's (NULL: none) */
   const int32_t* draft;       /* [B, m - 1] drafted tokens: row i counts the first i of them as
@@ -682,8 +682,8 @@ typedef struct {
   const float* frequency;     /* [B] (NULL: 0) */
   const float* temperature;   /* [B] >= 0 (NULL: 1); 0: all on the largest, the lowest id of equals */
   int biases;                 /* entries of each row of bias_tokens, at most 1024 */
-  const int32_t* bias_tokens; /* [B, biases]; -1 is skipped; a token named twice gets both, added in
-                                 their order */
+  const int32_t* bias_tokens; /* [B, biases]; -1 is skipped; a token named more than once gets the
+                                 sum, added up in their order */
   const float* bias_values;   /* [B, biases] */
   const uint32_t* mask;       /* bit v % 32 of word v / 32 set: token v may be chosen.  NULL: all */
   int64_t mask_stride_b, mask_stride_i;   /* in words; 0 shares a mask */
@@ -691,7 +691,8 @@ typedef struct {
 
 /* Penalties, biases and masks, then probabilities for moe_verify_draft.  For token v with logit l,
  * c times among the outputs:
- *   l > 0 ? l / repetition : l * repetition   if v is in the prompt or the outputs,
+ *   l > 0 ? l / repetition : l * repetition   if v is in the prompt or the outputs (the division
+ *                                             is a product with the rounded reciprocal),
  *   l -= frequency * c;  l -= presence if c > 0;  l += bias;  l = -inf if the mask forbids v.
  * A NaN counts as -inf, and a logit of -inf stays there.  probabilities: p = exp((l - max) /
  * temperature) / sum in binary32, tokens at -inf get 0, tokens at +inf share all of it; a row that

@@ -3,10 +3,8 @@
 // A cluster of up to 8 CTAs takes one row at a time, each CTA a contiguous part of the vocabulary that its
 // threads hold in registers (kPer values each, one load in flight per value), so the logits are
 // read once and the result is written once.  While the first loads are under way the CTA counts the
-// history into shared memory, 32 bits a token of its part: bit 0 the prompt, bit 1 a bias, the
-// rest how often the token is among the outputs (integer atomics: the same in any order); further rows
-// of the sequence add one draft each.  Biases of the same token are added by a warp that walks the
-// list in its order.  The softmax is over the CTA's own maximum and sum, which the CTAs exchange
+// history into shared memory, a word for each token of its part (integer atomics: the same in any
+// order); further rows of the sequence add one draft each.  The softmax is over the CTA's own maximum and sum, which the CTAs exchange
 // once over distributed shared memory (max, sum, and the first token of the maximum for greedy
 // rows) and join in rank order, so repeated calls give the same bits.
 // Rows begin at any multiple of the element size (odd vocabularies): one element per lane and
@@ -24,6 +22,9 @@ namespace {
 constexpr int kLThreads = 512;
 constexpr int kLWarps = kLThreads / 32;
 constexpr int kLMaxCluster = 8;
+// A token's word: bit 0 the prompt, then 11 bits the first bias that names it (1 + its place), then how
+// often it is among the outputs.
+constexpr uint32_t kOnce = 1u << 12;
 
 __device__ __forceinline__ float load_logit(const float* p) { return __ldg(p); }
 __device__ __forceinline__ float load_logit(const __nv_bfloat16* p) {
@@ -66,6 +67,7 @@ __global__ void __launch_bounds__(kLThreads, kPer <= 8 ? 3 : kPer <= 32 ? 2 : 1)
   __shared__ Share s_share[2][kLMaxCluster];   // every CTA of the cluster writes its own here
   __shared__ float s_max[kLWarps], s_sum[kLWarps];
   __shared__ int s_at[kLWarps];
+  __shared__ int s_draft[32];
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int rank = blockIdx.x % p.cluster;
   const int group = blockIdx.x / p.cluster;           // p.rows rows of a sequence
@@ -98,6 +100,7 @@ __global__ void __launch_bounds__(kLThreads, kPer <= 8 ? 3 : kPer <= 32 ? 2 : 1)
   // the counts
   int32_t* s_bias_t = reinterpret_cast<int32_t*>(s_count + p.part);
   float* s_bias_v = reinterpret_cast<float*>(s_bias_t + p.biases);
+  float* s_bias_sum = s_bias_v + p.biases;
   const bool counts = p.history != nullptr || p.draft != nullptr || p.biases > 0;
   auto count = [&](int v, uint32_t what) {
     if (v < 0 || v >= p.V) {
@@ -106,7 +109,7 @@ __global__ void __launch_bounds__(kLThreads, kPer <= 8 ? 3 : kPer <= 32 ? 2 : 1)
     }
     v -= v0;
     if (v < 0 || v >= n) return;
-    if (what < 4) atomicOr(s_count + v, what); else atomicAdd(s_count + v, what);
+    if (what < kOnce) atomicOr(s_count + v, what); else atomicAdd(s_count + v, what);
   };
   if (counts) {
     int len = 0, prompt = 0;
@@ -130,6 +133,10 @@ __global__ void __launch_bounds__(kLThreads, kPer <= 8 ? 3 : kPer <= 32 ? 2 : 1)
         v[j] = at + j * kLThreads < len ? __ldg(h + at + j * kLThreads) : -1;
     };
     load(tid);
+    for (int at = tid; at < p.biases; at += kLThreads) {
+      s_bias_t[at] = __ldg(p.bias_tokens + static_cast<int64_t>(b) * p.biases + at);
+      s_bias_v[at] = __ldg(p.bias_values + static_cast<int64_t>(b) * p.biases + at);
+    }
     __syncthreads();
     for (int at = tid; at < len; at += kAtOnce * kLThreads) {
       int now[kAtOnce];
@@ -137,14 +144,29 @@ __global__ void __launch_bounds__(kLThreads, kPer <= 8 ? 3 : kPer <= 32 ? 2 : 1)
       for (int j = 0; j < kAtOnce; ++j) now[j] = v[j];
       load(at + kAtOnce * kLThreads);
 #pragma unroll
-      for (int j = 0; j < kAtOnce; ++j) count(now[j], at + j * kLThreads < prompt ? 1u : 4u);
+      for (int j = 0; j < kAtOnce; ++j) count(now[j], at + j * kLThreads < prompt ? 1u : kOnce);
     }
-    if (p.draft != nullptr && tid < i0) count(__ldg(p.draft + b * (p.m - 1) + tid), 4u);
-    for (int at = tid; at < p.biases; at += kLThreads) {
-      const int t = __ldg(p.bias_tokens + static_cast<int64_t>(b) * p.biases + at);
-      s_bias_t[at] = t;
-      s_bias_v[at] = __ldg(p.bias_values + static_cast<int64_t>(b) * p.biases + at);
-      count(t, 2u);
+    if (p.draft != nullptr && tid < p.m - 1) {
+      const int t = __ldg(p.draft + b * (p.m - 1) + tid);
+      s_draft[tid] = t;
+      if (tid < i0) count(t, kOnce);
+    }
+    // the first bias of a token gets all of them, added up in their order; a warp for each
+    for (int at = warp; at < p.biases; at += kLWarps) {
+      const int t = s_bias_t[at];
+      if ((t < -1 || t >= p.V) && lane == 0) set_error(p.ctrl, MOE_ERR_DEVICE_FAULT, 40);
+      if (t < v0 || t >= v0 + n || t < 0 || t >= p.V) continue;
+      int first = -1;
+      float sum = 0.0f;
+      for (int q = 0; q < p.biases; q += 32) {
+        uint32_t same = __ballot_sync(0xffffffffu, q + lane < p.biases && s_bias_t[min(q + lane, p.biases - 1)] == t);
+        if (first < 0 && same != 0) first = q + __ffs(same) - 1;
+        if (first >= 0 && first != at) break;
+        for (; same != 0; same &= same - 1) sum += s_bias_v[q + __ffs(same) - 1];
+      }
+      if (first != at || lane != 0) continue;
+      s_bias_sum[at] = sum;
+      count(t, static_cast<uint32_t>(at + 1) << 1);
     }
     __syncthreads();
   }
@@ -160,47 +182,30 @@ __global__ void __launch_bounds__(kLThreads, kPer <= 8 ? 3 : kPer <= 32 ? 2 : 1)
 
   for (int i = i0; i < i1; ++i) {
     if (i > i0) {
-      // the next row: one more draft, by the thread that the barrier below orders before the counts' readers
+      load_row(i);
+      // the next row: one more draft
       if (counts && p.draft != nullptr) {
         if (!kProbs) __syncthreads();       // (with probabilities the exchange has ordered the readers before)
-        if (tid == 0) count(__ldg(p.draft + b * (p.m - 1) + i - 1), 4u);
+        if (tid == 0) count(s_draft[i - 1], kOnce);
         __syncthreads();
       }
-      load_row(i);
     }
-    uint32_t biased[kWords] = {};           // bit j: this thread's value j has a bias
+    if (i + 1 < i1) {                       // the next row comes to L2 meanwhile, 128 bytes a thread
+      const char* next = reinterpret_cast<const char*>(p.logits + b * p.l_sb + (i + 1) * p.l_si + v0);
+      for (int at = tid * 128; at < n * static_cast<int>(sizeof(T)); at += kLThreads * 128)
+        asm volatile("prefetch.global.L2 [%0];" ::"l"(next + at));
+    }
 #pragma unroll
     for (int j = 0; j < kPer; ++j) {
       const uint32_t c = counts ? s_count[tid + j * kLThreads] : 0u;
       if (c != 0) {
-        if ((c & ~2u) != 0) l[j] *= l[j] > 0.0f ? inverse : rep;
-        if (c >= 4) l[j] = l[j] - frequency * static_cast<float>(c >> 2) - presence;
-        biased[j / 32] |= ((c >> 1) & 1u) << (j % 32);
+        const uint32_t bias = (c >> 1) & (kOnce / 2 - 1);
+        if ((c & 1u) != 0 || c >= kOnce) l[j] *= l[j] > 0.0f ? inverse : rep;
+        if (c >= kOnce) l[j] = l[j] - frequency * static_cast<float>(c / kOnce) - presence;
+        if (bias != 0 && l[j] > neg_inf()) l[j] += s_bias_sum[bias - 1];
       }
       const uint32_t word = __shfl_sync(0xffffffffu, words[j / 32], j % 32);
       if (((word >> lane) & 1u) == 0 || !(l[j] >= neg_inf())) l[j] = neg_inf();   // (or NaN)
-    }
-#pragma unroll
-    for (int w = 0; w < kWords; ++w) {
-      const uint32_t any = __reduce_or_sync(0xffffffffu, biased[w]);
-      if (any == 0) continue;
-#pragma unroll
-      for (int j = 32 * w; j < (kPer < 32 * w + 32 ? kPer : 32 * w + 32); ++j) {
-        if (((any >> (j % 32)) & 1u) == 0) continue;
-        uint32_t lanes = __ballot_sync(0xffffffffu, (biased[w] >> (j % 32)) & 1u);
-        float add = l[j];
-        for (; lanes != 0; lanes &= lanes - 1) {
-          const int who = __ffs(lanes) - 1;
-          const int v = v0 + warp * 32 + j * kLThreads + who;
-          for (int q = 0; q < p.biases; q += 32) {
-            const bool mine = q + lane < p.biases && s_bias_t[q + lane] == v;
-            uint32_t found = __ballot_sync(0xffffffffu, mine);
-            for (; found != 0; found &= found - 1)
-              if (lane == who && add > neg_inf()) add += s_bias_v[q + __ffs(found) - 1];
-          }
-        }
-        l[j] = add >= neg_inf() ? add : neg_inf();
-      }
     }
     float* out = p.out + b * p.o_sb + i * p.o_si + v0 + tid;
     if constexpr (!kProbs) {
@@ -318,11 +323,11 @@ cudaError_t launch(LogitsParams<T> p, int B, int cluster, int num_sms, cudaStrea
     const double cost = static_cast<double>((clusters + room - 1) / room) * (rows + 0.5);
     if (cost < best) best = cost, p.rows = rows;
   }
-  const int bytes = p.part * 4 + p.biases * 8;
+  const int bytes = p.part * 4 + p.biases * 12;
   if (bytes > 48 * 1024) {
     const cudaError_t e = cudaFuncSetAttribute(logits_kernel<T, kPer, kProbs>,
                                                cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                               kPer * kLThreads * 4 + 1024 * 8);
+                                               kPer * kLThreads * 4 + 1024 * 12);
     if (e != cudaSuccess) return e;
   }
   cudaLaunchAttribute attr[2];

@@ -206,6 +206,7 @@ moe_status_t moe_adjust_logits(const moe_logits_args* a, void* ws, void* stream)
     return MOE_ERR_INVALID_ARG;
   if (a->probabilities != 0 && a->probabilities != 1) return MOE_ERR_INVALID_ARG;
   if (a->m > 33 || a->V > 262144 || a->biases > 1024) return MOE_ERR_UNSUPPORTED;
+  if (a->history != nullptr && a->history_stride > (1 << 20) - 64) return MOE_ERR_UNSUPPORTED;
   // a CTA for each eighth of a row, counted in 32 bits
   if (static_cast<long long>(a->B) * a->m > 0x7fffffffll / 64) return MOE_ERR_UNSUPPORTED;
   if (a->B == 0) return MOE_OK;
