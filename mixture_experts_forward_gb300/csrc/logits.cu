@@ -25,6 +25,7 @@ constexpr int kLMaxCluster = 8;
 // A token's word: bit 0 the prompt, then 11 bits the first bias that names it (1 + its place), then how
 // often it is among the outputs.
 constexpr uint32_t kOnce = 1u << 12;
+constexpr int kListShare = 4;             // the list holds a quarter of a CTA's tokens
 
 __device__ __forceinline__ float load_logit(const float* p) { return __ldg(p); }
 __device__ __forceinline__ float load_logit(const __nv_bfloat16* p) {
@@ -63,11 +64,12 @@ struct alignas(16) Share {                 // (stored as one vector)
 template <typename T, int kPer, bool kProbs>
 __global__ void __launch_bounds__(kLThreads, kPer <= 8 ? 3 : kPer <= 32 ? 2 : 1)
     logits_kernel(const LogitsParams<T> p) {
-  extern __shared__ __align__(16) uint32_t s_count[];   // [part], then the biases' tokens and values
+  extern __shared__ __align__(16) uint32_t s_count[];   // [part]: a token's word, later its value's bits, inverted
   __shared__ Share s_share[2][kLMaxCluster];   // every CTA of the cluster writes its own here
   __shared__ float s_max[kLWarps], s_sum[kLWarps];
   __shared__ int s_at[kLWarps];
-  __shared__ int s_draft[32];
+  __shared__ int s_draft[32], s_named;
+  __shared__ float s_number[4];
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int rank = blockIdx.x % p.cluster;
   const int group = blockIdx.x / p.cluster;           // p.rows rows of a sequence
@@ -75,18 +77,60 @@ __global__ void __launch_bounds__(kLThreads, kPer <= 8 ? 3 : kPer <= 32 ? 2 : 1)
   const int b = group / groups, i0 = (group - b * groups) * p.rows, i1 = min(p.m, i0 + p.rows);
   const int v0 = rank * p.part, n = min(p.part, p.V - v0);    // n may be <= 0
   constexpr int kWords = (kPer + 31) / 32;
+  const bool counts = p.history != nullptr || p.draft != nullptr || p.biases > 0;
+  const bool list = p.rows > 1;
+  if (counts) {
+    for (int at = tid; at < p.part / 4; at += kLThreads)
+      reinterpret_cast<uint4*>(s_count)[at] = make_uint4(0u, 0u, 0u, 0u);
+    if (tid == 0) s_named = 0;
+  }
   pdl_wait();
   pdl_launch_dependents();
   if (kProbs && p.cluster > 1)              // (before any CTA writes to another)
     asm volatile("barrier.cluster.arrive.relaxed.aligned;" ::: "memory");
 
+  // the tokens named: a word each, and the list of them (where it has room)
+  const int room = p.part / kListShare;
+  uint32_t* s_word = s_count + p.part;
+  int32_t* s_bias_t = reinterpret_cast<int32_t*>(s_word + room);
+  float* s_bias_v = reinterpret_cast<float*>(s_bias_t + p.biases);
+  float* s_bias_sum = s_bias_v + p.biases;
+  uint16_t* s_token = reinterpret_cast<uint16_t*>(s_bias_sum + p.biases);
+
+  // What the counts and the row's adjustment need comes before the row, which keeps the load units busy for microseconds.
+  float number = 1.0f;                      // the sequence's numbers, one a thread
+  if (tid < 4) {
+    const float* from = tid == 0 ? p.repetition : tid == 1 ? p.presence : tid == 2 ? p.frequency : p.temperature;
+    number = from == nullptr ? (tid == 0 || tid == 3 ? 1.0f : 0.0f) : __ldg(from + b);
+  }
+  int len = 0, prompt = 0;
+  constexpr int kAtOnce = 8;
+  int ahead[kAtOnce];                       // the history's next tokens
+  const int32_t* history = p.history + static_cast<int64_t>(b) * p.history_stride + tid;
+  auto load_history = [&](int at) {
+#pragma unroll
+    for (int j = 0; j < kAtOnce; ++j)
+      ahead[j] = at + tid + j * kLThreads < len ? __ldg(history + at + j * kLThreads) : -1;
+  };
+  if (p.history != nullptr) {
+    len = p.history_lens != nullptr ? __ldg(p.history_lens + b) : p.history_stride;
+    if (p.prompt_lens != nullptr) prompt = __ldg(p.prompt_lens + b);
+    if (len < 0 || len > p.history_stride || prompt < 0 || prompt > len) {
+      if (tid == 0) set_error(p.ctrl, MOE_ERR_DEVICE_FAULT, 41);
+      len = min(max(len, 0), p.history_stride);
+      prompt = min(max(prompt, 0), len);
+    }
+    load_history(0);
+  }
+  for (int at = tid; at < p.biases; at += kLThreads) {
+    cp_async4(smem_u32(s_bias_t + at), p.bias_tokens + static_cast<int64_t>(b) * p.biases + at);
+    cp_async4(smem_u32(s_bias_v + at), p.bias_values + static_cast<int64_t>(b) * p.biases + at);
+  }
+  if (p.draft != nullptr && tid < p.m - 1) cp_async4(smem_u32(s_draft + tid), p.draft + b * (p.m - 1) + tid);
+
   float l[kPer];
   uint32_t words[kWords];                   // word j of the mask for this warp's tokens of turn j, by lane j
   auto load_row = [&](int i) {
-    const T* src = p.logits + b * p.l_sb + i * p.l_si + v0 + tid;
-#pragma unroll
-    for (int j = 0; j < kPer; ++j)
-      l[j] = tid + j * kLThreads < n ? load_logit(src + j * kLThreads) : neg_inf();
 #pragma unroll
     for (int w = 0; w < kWords; ++w) {
       const int at = (warp + (32 * w + lane) * kLWarps) * 32;
@@ -94,63 +138,60 @@ __global__ void __launch_bounds__(kLThreads, kPer <= 8 ? 3 : kPer <= 32 ? 2 : 1)
       if (p.mask != nullptr && 32 * w + lane < kPer && at < n)
         words[w] = __ldg(p.mask + b * p.m_sb + i * p.m_si + (v0 + at) / 32);
     }
+    const T* src = p.logits + b * p.l_sb + i * p.l_si + v0 + tid;
+#pragma unroll
+    for (int j = 0; j < kPer; ++j)
+      l[j] = tid + j * kLThreads < n ? load_logit(src + j * kLThreads) : neg_inf();
   };
   load_row(i0);
+  if (tid < 4) s_number[tid] = number;
 
-  // the counts
-  int32_t* s_bias_t = reinterpret_cast<int32_t*>(s_count + p.part);
-  float* s_bias_v = reinterpret_cast<float*>(s_bias_t + p.biases);
-  float* s_bias_sum = s_bias_v + p.biases;
-  const bool counts = p.history != nullptr || p.draft != nullptr || p.biases > 0;
-  auto count = [&](int v, uint32_t what) {
+  // The word as it was, of a token of this part (else ~0u): a token's first name enters it in the list.
+  auto count = [&](int v, uint32_t what) -> uint32_t {
     if (v < 0 || v >= p.V) {
       if (v != -1) set_error(p.ctrl, MOE_ERR_DEVICE_FAULT, 40);
-      return;
+      return ~0u;
     }
     v -= v0;
-    if (v < 0 || v >= n) return;
-    if (what < kOnce) atomicOr(s_count + v, what); else atomicAdd(s_count + v, what);
+    if (v < 0 || v >= n) return ~0u;
+    return what < kOnce ? atomicOr(s_count + v, what) : atomicAdd(s_count + v, what);
   };
+  auto enter = [&](int v, int at) {
+    if (at < room) s_token[at] = static_cast<uint16_t>(v - v0);
+  };
+  bool listed = false;
+  cp_async_wait_all();
+  __syncthreads();
   if (counts) {
-    int len = 0, prompt = 0;
-    if (p.history != nullptr) {
-      len = p.history_lens != nullptr ? __ldg(p.history_lens + b) : p.history_stride;
-      if (p.prompt_lens != nullptr) prompt = __ldg(p.prompt_lens + b);
-      if (len < 0 || len > p.history_stride || prompt < 0 || prompt > len) {
-        if (tid == 0) set_error(p.ctrl, MOE_ERR_DEVICE_FAULT, 41);
-        len = min(max(len, 0), p.history_stride);
-        prompt = min(max(prompt, 0), len);
-      }
-    }
-    for (int at = tid; at < p.part / 4; at += kLThreads)
-      reinterpret_cast<uint4*>(s_count)[at] = make_uint4(0u, 0u, 0u, 0u);
-    const int32_t* h = p.history + static_cast<int64_t>(b) * p.history_stride;
-    constexpr int kAtOnce = 4;
-    int v[kAtOnce];
-    auto load = [&](int at) {
-#pragma unroll
-      for (int j = 0; j < kAtOnce; ++j)
-        v[j] = at + j * kLThreads < len ? __ldg(h + at + j * kLThreads) : -1;
-    };
-    load(tid);
-    for (int at = tid; at < p.biases; at += kLThreads) {
-      s_bias_t[at] = __ldg(p.bias_tokens + static_cast<int64_t>(b) * p.biases + at);
-      s_bias_v[at] = __ldg(p.bias_values + static_cast<int64_t>(b) * p.biases + at);
-    }
-    __syncthreads();
-    for (int at = tid; at < len; at += kAtOnce * kLThreads) {
+    for (int turn = 0; turn < len; turn += kAtOnce * kLThreads) {
       int now[kAtOnce];
 #pragma unroll
-      for (int j = 0; j < kAtOnce; ++j) now[j] = v[j];
-      load(at + kAtOnce * kLThreads);
+      for (int j = 0; j < kAtOnce; ++j) now[j] = ahead[j];
+      load_history(turn + kAtOnce * kLThreads);
+      if (!list) {
 #pragma unroll
-      for (int j = 0; j < kAtOnce; ++j) count(now[j], at + j * kLThreads < prompt ? 1u : kOnce);
+        for (int j = 0; j < kAtOnce; ++j) count(now[j], turn + tid + j * kLThreads < prompt ? 1u : kOnce);
+        continue;
+      }
+      uint32_t entered = 0;
+#pragma unroll
+      for (int j = 0; j < kAtOnce; ++j)
+        if (count(now[j], turn + tid + j * kLThreads < prompt ? 1u : kOnce) == 0) entered |= 1u << j;
+      int at = __popc(entered);             // one draw for a warp's new tokens
+#pragma unroll
+      for (int o = 1; o < 32; o <<= 1) {
+        const int up = __shfl_up_sync(0xffffffffu, at, o);
+        if (lane >= o) at += up;
+      }
+      int base = 0;
+      if (lane == 31 && at > 0) base = atomicAdd(&s_named, at);
+      at += __shfl_sync(0xffffffffu, base, 31) - __popc(entered);
+#pragma unroll
+      for (int j = 0; j < kAtOnce; ++j)
+        if ((entered >> j & 1u) != 0) enter(now[j], at++);
     }
-    if (p.draft != nullptr && tid < p.m - 1) {
-      const int t = __ldg(p.draft + b * (p.m - 1) + tid);
-      s_draft[tid] = t;
-      if (tid < i0) count(t, kOnce);
-    }
+    if (p.draft != nullptr && tid < i0 && count(s_draft[tid], kOnce) == 0 && list)
+      enter(s_draft[tid], atomicAdd(&s_named, 1));
     // the first bias of a token gets all of them, added up in their order; a warp for each
     for (int at = warp; at < p.biases; at += kLWarps) {
       const int t = s_bias_t[at];
@@ -166,13 +207,23 @@ __global__ void __launch_bounds__(kLThreads, kPer <= 8 ? 3 : kPer <= 32 ? 2 : 1)
       }
       if (first != at || lane != 0) continue;
       s_bias_sum[at] = sum;
-      count(t, static_cast<uint32_t>(at + 1) << 1);
+      if (count(t, static_cast<uint32_t>(at + 1) << 1) == 0 && list) enter(t, atomicAdd(&s_named, 1));
     }
     __syncthreads();
+    if (list && p.draft != nullptr) {       // drafts of the rows to come get places, with nothing counted
+      if (tid >= i0 && tid < i1 - 1) {
+        const int t = s_draft[tid], v = t - v0;
+        if (t < -1 || t >= p.V) set_error(p.ctrl, MOE_ERR_DEVICE_FAULT, 40);
+        bool is_new = t >= 0 && t < p.V && v >= 0 && v < n && s_count[v] == 0;
+        for (int d = i0; d < tid; ++d) is_new = is_new && s_draft[d] != t;
+        if (is_new) enter(t, atomicAdd(&s_named, 1));
+      }
+      __syncthreads();
+    }
+    listed = list && s_named <= room;
   }
-  auto number = [&](const float* a, float none) { return a == nullptr ? none : __ldg(a + b); };
-  float rep = number(p.repetition, 1.0f), temp = number(p.temperature, 1.0f);
-  const float presence = number(p.presence, 0.0f), frequency = number(p.frequency, 0.0f);
+  float rep = s_number[0], temp = s_number[3];
+  const float presence = s_number[1], frequency = s_number[2];
   if (!(rep > 0.0f) || !(temp >= 0.0f)) {
     if (tid == 0) set_error(p.ctrl, MOE_ERR_DEVICE_FAULT, 42);
     if (!(rep > 0.0f)) rep = 1.0f;
@@ -180,32 +231,74 @@ __global__ void __launch_bounds__(kLThreads, kPer <= 8 ? 3 : kPer <= 32 ? 2 : 1)
   }
   const float inverse = __fdiv_rn(1.0f, rep);
 
+  auto adjusted = [&](float x, uint32_t c) {
+    const uint32_t bias = (c >> 1) & (kOnce / 2 - 1);
+    if ((c & 1u) != 0 || c >= kOnce) x *= x > 0.0f ? inverse : rep;
+    if (c >= kOnce) x = x - frequency * static_cast<float>(c / kOnce) - presence;
+    if (bias != 0 && x > neg_inf()) x += s_bias_sum[bias - 1];
+    return x;
+  };
+
   for (int i = i0; i < i1; ++i) {
     if (i > i0) {
       load_row(i);
-      // the next row: one more draft
-      if (counts && p.draft != nullptr) {
-        if (!kProbs) __syncthreads();       // (with probabilities the exchange has ordered the readers before)
-        if (tid == 0) count(s_draft[i - 1], kOnce);
-        __syncthreads();
+      if (!kProbs) __syncthreads();         // (with probabilities the exchange has ordered the readers before)
+    }
+    if (listed) {
+      // The listed tokens' values by themselves; each is put where the pass finds it, inverted, so
+      // that it is never 0 (that would be a NaN, which counts as -inf).
+      const T* row = p.logits + b * p.l_sb + i * p.l_si + v0;
+      const int draft = i > i0 && p.draft != nullptr ? s_draft[i - 1] - v0 : -1;   // one more is counted
+      for (int at = tid; at < s_named; at += 2 * kLThreads) {
+        const bool two = at + kLThreads < s_named;
+        const int v[2] = {s_token[at], two ? s_token[at + kLThreads] : -1};
+        const float x[2] = {load_logit(row + v[0]), two ? load_logit(row + v[1]) : 0.0f};
+#pragma unroll
+        for (int q = 0; q < 2; ++q) {
+          if (v[q] < 0) break;
+          uint32_t c = i == i0 ? s_count[v[q]] : s_word[at + q * kLThreads];
+          if (v[q] == draft) c += kOnce;
+          s_word[at + q * kLThreads] = c;
+          s_count[v[q]] = ~__float_as_uint(fmaxf(adjusted(x[q], c), neg_inf()));
+        }
       }
+      __syncthreads();
+    } else if (i > i0 && p.draft != nullptr) {
+      if (tid == 0) count(s_draft[i - 1], kOnce);
+      __syncthreads();
     }
     if (i + 1 < i1) {                       // the next row comes to L2 meanwhile, 128 bytes a thread
       const char* next = reinterpret_cast<const char*>(p.logits + b * p.l_sb + (i + 1) * p.l_si + v0);
       for (int at = tid * 128; at < n * static_cast<int>(sizeof(T)); at += kLThreads * 128)
         asm volatile("prefetch.global.L2 [%0];" ::"l"(next + at));
     }
+    // the mask's bits turned round: bit j for this lane's value of turn j
+#pragma unroll
+    for (int w = 0; w < kWords; ++w)
+#pragma unroll
+      for (int o = 16; o > 0; o >>= 1) {
+        const uint32_t low = 0xffffffffu / ((1u << o) + 1u);      // the bits whose place has no o
+        const uint32_t other = __shfl_xor_sync(0xffffffffu, words[w], o);
+        words[w] = (lane & o) == 0 ? (words[w] & low) | ((other & low) << o)
+                                   : (words[w] & ~low) | ((other & ~low) >> o);
+      }
+    if (listed) {
+#pragma unroll
+      for (int j = 0; j < kPer; ++j) {
+        const uint32_t c = s_count[tid + j * kLThreads];
+        if (c != 0) l[j] = __uint_as_float(~c);
+      }
+    } else if (counts) {
+#pragma unroll
+      for (int j = 0; j < kPer; ++j) {
+        const uint32_t c = s_count[tid + j * kLThreads];
+        if (c != 0) l[j] = adjusted(l[j], c);
+      }
+    }
 #pragma unroll
     for (int j = 0; j < kPer; ++j) {
-      const uint32_t c = counts ? s_count[tid + j * kLThreads] : 0u;
-      if (c != 0) {
-        const uint32_t bias = (c >> 1) & (kOnce / 2 - 1);
-        if ((c & 1u) != 0 || c >= kOnce) l[j] *= l[j] > 0.0f ? inverse : rep;
-        if (c >= kOnce) l[j] = l[j] - frequency * static_cast<float>(c / kOnce) - presence;
-        if (bias != 0 && l[j] > neg_inf()) l[j] += s_bias_sum[bias - 1];
-      }
-      const uint32_t word = __shfl_sync(0xffffffffu, words[j / 32], j % 32);
-      if (((word >> lane) & 1u) == 0 || !(l[j] >= neg_inf())) l[j] = neg_inf();   // (or NaN)
+      l[j] = fmaxf(l[j], neg_inf());        // (a NaN counts as -inf)
+      if ((words[j / 32] >> (j % 32) & 1u) == 0) l[j] = neg_inf();
     }
     float* out = p.out + b * p.o_sb + i * p.o_si + v0 + tid;
     if constexpr (!kProbs) {
@@ -316,18 +409,20 @@ cudaError_t launch(LogitsParams<T> p, int B, int cluster, int num_sms, cudaStrea
   p.cluster = cluster;
   // Rows of a sequence that share their counts: what takes the fewest rounds of the clusters that
   // find room, counting costs about half a row.
-  const int room = num_sms * (kPer <= 8 ? 3 : kPer <= 32 ? 2 : 1) / cluster;
+  const int room = (cluster == 8 ? num_sms / 10 : cluster == 4 ? num_sms * 9 / 38 : num_sms / cluster) *
+                   (kPer <= 8 ? 3 : kPer <= 32 ? 2 : 1);
   double best = 1e30;
   for (int rows = 1; rows <= p.m; ++rows) {
     const int64_t clusters = static_cast<int64_t>(B) * ((p.m + rows - 1) / rows);
     const double cost = static_cast<double>((clusters + room - 1) / room) * (rows + 0.5);
     if (cost < best) best = cost, p.rows = rows;
   }
-  const int bytes = p.part * 4 + p.biases * 12;
+  const int bytes = p.part * 4 + p.part / kListShare * 6 + p.biases * 12;
   if (bytes > 48 * 1024) {
     const cudaError_t e = cudaFuncSetAttribute(logits_kernel<T, kPer, kProbs>,
                                                cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                               kPer * kLThreads * 4 + 1024 * 12);
+                                               kPer * kLThreads * 4 + kPer * kLThreads / kListShare * 6 +
+                                                   1024 * 12);
     if (e != cudaSuccess) return e;
   }
   cudaLaunchAttribute attr[2];

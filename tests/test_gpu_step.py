@@ -435,6 +435,20 @@ def test_logits(B, m, V, hist, nb, dtype, probs):
     check_logits(x, kw, probabilities=probs)
 
 
+@pytest.mark.parametrize("probs", [True, False])
+@pytest.mark.parametrize("B,m,V,hist", [(200, 5, 4000, 100), (200, 5, 4000, 9000), (38, 2, 70001, 2000),
+                                        (38, 2, 131072, 60000)])
+def test_logits_of_sequences_whose_rows_share_their_counts(B, m, V, hist, probs):
+    """So many rows that some of a sequence's go together; of the long histories a CTA's tokens are
+    mostly named, too many for a list."""
+    x, kw = logits_case(B, m, V, hist, 7, seed=V + hist)
+    g = torch.Generator().manual_seed(hist)
+    kw["history"] = torch.randint(0, V, (B, hist), generator=g, dtype=torch.int32)
+    kw["draft"][::2, 1:] = kw["draft"][::2, :1]                       # the same draft again
+    kw["draft"][1::2] = kw["history"][1::2, : m - 1]                  # and one that is in the prompt
+    check_logits(x, kw, probabilities=probs)
+
+
 def test_logits_one_thing_at_a_time():
     x, kw = logits_case(2, 3, 5001, 300, 20, 4)
     plain = check_logits(x, {})
