@@ -4,16 +4,24 @@
 // threads hold in registers (kPer values each, one load in flight per value), so the logits are
 // read once and the result is written once.  While the first loads are under way the CTA counts the
 // history into shared memory, a word for each token of its part (integer atomics: the same in any
-// order); further rows of the sequence add one draft each.  The softmax is over the CTA's own maximum and sum, which the CTAs exchange
+// order); further rows of the sequence add one draft each.  Where a CTA takes several rows it also
+// lists the tokens named: their values are adjusted by themselves, spread over the threads, and the
+// pass over the row finds them in the words' place, in 3 instructions a value instead of a branch
+// that most warps take.  The softmax is over the CTA's own maximum and sum, which the CTAs exchange
 // once over distributed shared memory (max, sum, and the first token of the maximum for greedy
-// rows) and join in rank order, so repeated calls give the same bits.
+// rows) and join in rank order, so repeated calls give the same bits.  Without probabilities
+// nothing is exchanged and the CTAs stand alone.
 // Rows begin at any multiple of the element size (odd vocabularies): one element per lane and
-// load.  Bound, for batches, by a row's chain of steps (the pass over the values, the maximum, the exponentials, the
-// exchange: 13 us with two CTAs an SM, where HBM would take 6; 576 rows of 131071 280 us) and for
-// single rows by the launch and the same chain (8 us).  Slower or no faster over both F32 drafts and
-// BF16 batches: quads on 16-byte boundaries with the next row copied ahead (270 and 91 us against 280 and 68),
-// values kept in shared memory with one exchange a row (278 and 92), that with chunks of 128 tokens dealt to the
-// CTAs in turn (272 and 99).
+// load.  Bound, for many rows, by a row's chain of steps (the loads, the pass, the maximum, the
+// exponentials, the exchange, the stores: 9 us with two CTAs an SM, of which HBM explains 5):
+// 576 rows of 131071 in 212 us (2.8 TB/s; without penalties, biases and mask 150), 200 BF16 rows of
+// 100003 without probabilities in 74 us (2.0 TB/s), one row 8 us: launch and chain.  Clusters of 8 leave a fifth of the SMs
+// empty, those of 4 with 64 values a thread fewer, but one CTA an SM overlaps with no other (212 and
+// 94).  No faster: quads on 16-byte boundaries with the next row copied ahead, values kept in shared
+// memory with one exchange a row, chunks of tokens dealt to the CTAs in turn, a fixed set of clusters with
+// equal shares of all rows.
+#include <algorithm>
+
 #include "serve_internal.cuh"
 
 namespace moe {
@@ -406,11 +414,13 @@ __global__ void __launch_bounds__(kLThreads, kPer <= 8 ? 3 : kPer <= 32 ? 2 : 1)
 template <typename T, int kPer, bool kProbs>
 cudaError_t launch(LogitsParams<T> p, int B, int cluster, int num_sms, cudaStream_t stream) {
   p.part = kPer * kLThreads;
+  if (!kProbs) cluster = (p.V + p.part - 1) / p.part;   // (CTAs of their own: no more than have tokens)
   p.cluster = cluster;
   // Rows of a sequence that share their counts: what takes the fewest rounds of the clusters that
-  // find room, counting costs about half a row.
-  const int room = (cluster == 8 ? num_sms / 10 : cluster == 4 ? num_sms * 9 / 38 : num_sms / cluster) *
-                   (kPer <= 8 ? 3 : kPer <= 32 ? 2 : 1);
+  // find room (of 152 SMs clusters of 8 use 120, of 4 144); counting costs about half a row.  (1, 2
+  // and 6 rows of 96 sequences' 6 a cluster: 297, 243 and 215 us.)
+  const int sms = !kProbs || cluster <= 2 ? num_sms : cluster == 4 ? num_sms * 18 / 19 : num_sms * 15 / 19;
+  const int room = std::max(1, sms * (kPer <= 8 ? 3 : kPer <= 32 ? 2 : 1) / cluster);
   double best = 1e30;
   for (int rows = 1; rows <= p.m; ++rows) {
     const int64_t clusters = static_cast<int64_t>(B) * ((p.m + rows - 1) / rows);
