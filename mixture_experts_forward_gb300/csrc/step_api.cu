@@ -123,6 +123,7 @@ moe_status_t moe_rotary_table(int rotary_dim, double base, moe_rope_scaling_t sc
     if (scaling == MOE_ROPE_INDEX) keep = 1.0 - (i - from) / (to - from);
     keep = std::fmin(1.0, std::fmax(0.0, keep));
     double turns = (theta * keep + theta / factor * (1.0 - keep)) / two_pi;
+    if (!std::isfinite(turns)) return MOE_ERR_INVALID_ARG;   // (a factor near the end of the type)
     turns -= std::floor(turns);                      // (a factor below 1 / 2 pi)
     // below 1, so the product is below 2^64 (53 bits of it, the rest zero)
     table[i] = static_cast<uint64_t>(turns * 18446744073709551616.0);

@@ -262,3 +262,14 @@ def test_what_the_binding_refuses(name):
         with pytest.raises(L.MoeError) as e:
             call(**{**args, **kw})
         assert "on one GPU" not in str(e.value), kw
+
+
+def test_sizes_past_the_types_are_refused():
+    out = (ctypes.c_uint64 * 64)()
+    # theta / factor is no number
+    assert L.lib().moe_rotary_table(64, 1e4, 1, 5e-324, 0, 1, 32, out) == INV
+    # a token's count and its other marks share 32 bits
+    most = (1 << 20) - 64
+    assert L.lib().moe_adjust_logits(logits_args(history_stride=most + 1), P(FAKE), None) == UNS
+    assert L.lib().moe_adjust_logits(logits_args(history_stride=most + 1, history=None, B=0), P(FAKE), None) == OK
+    assert L.lib().moe_adjust_logits(logits_args(history_stride=most), None, None) == WS
