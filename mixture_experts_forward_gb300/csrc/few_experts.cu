@@ -19,14 +19,15 @@
 // are few units.  Down: a cluster of 8 CTAs takes 128 output rows, each of its CTAs an equal
 // share of all active experts' K; the shares meet over distributed shared memory, in rank order
 // (no atomics: repeated calls give the same bits).  The tokens are routed before by moe_route's
-// kernel, during which the up kernel stages x; while the up kernel runs, the down kernel fetches its first
-// weights as far as it finds room.  (Routing in every CTA of both kernels instead saved a launch but
+// kernel, during which the up kernel stages x; while the up kernel runs, the down kernel fetches
+// its first weights as far as it finds room.  (Routing in every CTA of both kernels instead saved a launch but
 // took 8 us of each for 16 tokens and 256 experts.)
 //
-// Measured (HBM's floor for the experts that the tokens reach in brackets): one token, 8 FP8 experts of 512 x
-// 2048 15 us (3.8: the chain of three launches); 16 tokens, 69 of them 55-57 us (33: 22 + 12 us of
-// stream at 5.9 TB/s, the rest the router and the kernels' beginnings and ends); one token, 2 BF16 experts of 1024 x 4096
-// 15-18 us (7.6); 5 tokens, 18 BF16 experts of 1408 x 4096 110-127 us (94).
+// Measured (HBM's floor for the experts that the tokens reach in brackets): one token, 8 FP8 experts
+// of 512 x 2048 15 us (3.8: the chain of three launches); 16 tokens, 69 of them 55-57 us (33: 22 +
+// 12 us of stream at 6.4 TB/s, the rest the router and the kernels' beginnings and ends); one token,
+// 2 BF16 experts of 1024 x 4096 15-18 us (7.6); 5 tokens, 18 BF16 experts of 1408 x 4096 110-127 us
+// (94).
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 

@@ -1,7 +1,7 @@
 // Penalties, biases and masks on logits, and their probabilities.
 //
-// A cluster of up to 8 CTAs takes one row at a time, each CTA a contiguous part of the vocabulary that its
-// threads hold in registers (kPer values each, one load in flight per value), so the logits are
+// A cluster of up to 8 CTAs takes one row at a time, each CTA a contiguous part of the vocabulary
+// that its threads hold in registers (kPer values each, one load in flight per value), so the logits are
 // read once and the result is written once.  While the first loads are under way the CTA counts the
 // history into shared memory, a word for each token of its part (integer atomics: the same in any
 // order); further rows of the sequence add one draft each.  Where a CTA takes several rows it also
@@ -15,11 +15,11 @@
 // load.  Bound, for many rows, by a row's chain of steps (the loads, the pass, the maximum, the
 // exponentials, the exchange, the stores: 9 us with two CTAs an SM, of which HBM explains 5):
 // 576 rows of 131071 in 212 us (2.8 TB/s; without penalties, biases and mask 150), 200 BF16 rows of
-// 100003 without probabilities in 74 us (2.0 TB/s), one row 8 us: launch and chain.  Clusters of 8 leave a fifth of the SMs
-// empty, those of 4 with 64 values a thread fewer, but one CTA an SM overlaps with no other (212 and
-// 94).  No faster: quads on 16-byte boundaries with the next row copied ahead, values kept in shared
-// memory with one exchange a row, chunks of tokens dealt to the CTAs in turn, a fixed set of clusters with
-// equal shares of all rows.
+// 100003 without probabilities in 73 us (1.7 TB/s), one row 8-10 us: launch and chain.  Clusters of
+// 8 leave a fifth of the SMs empty, those of 4 with 64 values a thread fewer, but one CTA an SM
+// overlaps with no other (212 and 94).  No faster: quads on 16-byte boundaries with the next row
+// copied ahead, values kept in shared memory with one exchange a row, chunks of tokens dealt to the
+// CTAs in turn, a fixed set of clusters with equal shares of all rows.
 #include <algorithm>
 
 #include "serve_internal.cuh"
@@ -105,7 +105,8 @@ __global__ void __launch_bounds__(kLThreads, kPer <= 8 ? 3 : kPer <= 32 ? 2 : 1)
   float* s_bias_sum = s_bias_v + p.biases;
   uint16_t* s_token = reinterpret_cast<uint16_t*>(s_bias_sum + p.biases);
 
-  // What the counts and the row's adjustment need comes before the row, which keeps the load units busy for microseconds.
+  // What the counts and the adjustment need comes before the row, which keeps the load units busy
+  // for microseconds.
   float number = 1.0f;                      // the sequence's numbers, one a thread
   if (tid < 4) {
     const float* from = tid == 0 ? p.repetition : tid == 1 ? p.presence : tid == 2 ? p.frequency : p.temperature;

@@ -7,10 +7,10 @@
 // of 8 (16-byte loads and stores) that hold whole pairs, so a piece needs no other thread's
 // elements: in the half layout runs i .. i+7 and i + rotary_dim/2 .., else 16 neighbours.  A row's
 // pieces lie in neighbouring lanes, which share its maximum by shuffles where the cache is FP8.
-// One pass, bound by HBM; below a few hundred tokens by the launch.  16384 tokens of 32 + 2 x 8 heads
-// of 128 from a packed projection into an FP8 cache 70 us (5.3 TB/s, 80 % of a copy's rate), 5003 of
-// 24 + 2 x 8 heads of 64 into a BF16 one 12 us in a graph, 32 tokens 4 us.  The next pieces loaded a turn ahead
-// gave 69 us for twice the code.
+// One pass, bound by HBM; below a few hundred tokens by the launch.  16384 tokens of 32 + 2 x 8
+// heads of 128 from a packed projection into an FP8 cache take 70 us (5.3 TB/s, 80 % of a copy's
+// rate), 5003 of 24 + 2 x 8 heads of 64 into a BF16 one 12 us in a graph, 32 tokens 4 us.  The next
+// pieces loaded a turn ahead gave 69 us for twice the code.
 #include "quant_common.cuh"
 #include "serve_internal.cuh"
 

@@ -7,9 +7,9 @@
 // prefix.  Nothing that a CTA reads is written before all have read it: the table entries written
 // lie past held[], and held[] and free_count[] are updated by the last CTA to finish (a counter in
 // the control block).  A few bytes per row: bound by the launch and the chain of dependent loads
-// (lengths, scan, table entry, slot).  Plan and release together take 9 us for 8 sequences and 12 us
-// for 1024 with 17,000 new tokens (in a graph; the plan alone 7, the release 5), where the bytes
-// would take 0.03; the Python calls take 30 and 38.
+// (lengths, scan, table entry, slot).  Plan and release together take 9 us for 8 sequences and
+// 12 us for 1024 with 18432 new tokens (in a graph; the plan alone 7, the release 5), where the
+// bytes would take 0.03; the Python calls take 30 and 38.
 #include "serve_internal.cuh"
 
 namespace moe {
