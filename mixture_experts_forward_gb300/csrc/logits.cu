@@ -63,7 +63,7 @@ struct LogitsParams {
   int rows;                                 // rows of a sequence that a cluster takes
 };
 
-// A CTA's share of a row: its maximum, where that is first, and the sum of exponentials.
+// A warp's or CTA's share of a row: its maximum, where that is first, and the sum of exponentials.
 struct alignas(16) Share {                 // (stored as one vector)
   float max, sum;
   int at, pad;
@@ -74,8 +74,7 @@ __global__ void __launch_bounds__(kLThreads, kPer <= 8 ? 3 : kPer <= 32 ? 2 : 1)
     logits_kernel(const LogitsParams<T> p) {
   extern __shared__ __align__(16) uint32_t s_count[];   // [part]: a token's word, later its value's bits, inverted
   __shared__ Share s_share[2][kLMaxCluster];   // every CTA of the cluster writes its own here
-  __shared__ float s_max[kLWarps], s_sum[kLWarps];
-  __shared__ int s_at[kLWarps];
+  __shared__ Share s_warp[kLWarps];
   __shared__ int s_draft[32], s_named;
   __shared__ float s_number[4];
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
@@ -315,17 +314,12 @@ __global__ void __launch_bounds__(kLThreads, kPer <= 8 ? 3 : kPer <= 32 ? 2 : 1)
       for (int j = 0; j < kPer; ++j)
         if (tid + j * kLThreads < n) out[j * kLThreads] = l[j];
     } else {
-      // the CTA's maximum, then (greedy) its first place or the sum
+      // the warp's maximum, then (greedy) its first place or the sum
       float top = neg_inf();
 #pragma unroll
       for (int j = 0; j < kPer; ++j) top = fmaxf(top, l[j]);
 #pragma unroll
       for (int o = 16; o > 0; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
-      if (lane == 0) s_max[warp] = top;
-      __syncthreads();
-      top = s_max[0];
-#pragma unroll
-      for (int w = 1; w < kLWarps; ++w) top = fmaxf(top, s_max[w]);
       const bool greedy = temp == 0.0f;
       int first = 0x7fffffff;
       float sum = 0.0f;
@@ -337,7 +331,6 @@ __global__ void __launch_bounds__(kLThreads, kPer <= 8 ? 3 : kPer <= 32 ? 2 : 1)
         for (int j = kPer - 1; j >= 0; --j)
           if (l[j] == top && top > neg_inf()) first = v0 + tid + j * kLThreads;
         first = __reduce_min_sync(0xffffffffu, first);
-        if (lane == 0) s_at[warp] = first;
       } else {
         if (top == -neg_inf()) {
 #pragma unroll
@@ -355,56 +348,56 @@ __global__ void __launch_bounds__(kLThreads, kPer <= 8 ? 3 : kPer <= 32 ? 2 : 1)
         }
 #pragma unroll
         for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
-        if (lane == 0) s_sum[warp] = sum;
       }
+      if (lane == 0) s_warp[warp] = {top, sum, first, 0};
       __syncthreads();
+      // a share's sum, taken to another maximum
+      auto taken_to = [&](const Share& s, float max) {
+        float f;
+        asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(f) : "f"((s.max - max) * rate));
+        return s.max == max ? s.sum : s.max == neg_inf() ? 0.0f : s.sum * f;
+      };
       // the CTAs' shares (two buffers in turn: no CTA is two rows ahead of another)
       Share* share = s_share[(i - i0) & 1];
-      if (p.cluster > 1) {
-        if (i == i0) asm volatile("barrier.cluster.wait.aligned;" ::: "memory");
-        if (tid < p.cluster) {
-          Share mine = {top, 0.0f, 0x7fffffff, 0};
+      if (p.cluster > 1 && i == i0) asm volatile("barrier.cluster.wait.aligned;" ::: "memory");
+      if (warp == 0) {
+        Share mine = s_warp[lane % kLWarps];
+        float max = mine.max;
 #pragma unroll
-          for (int w = 0; w < kLWarps; ++w)
-            if (greedy) mine.at = min(mine.at, s_at[w]); else mine.sum += s_sum[w];
-          uint32_t at;
+        for (int o = kLWarps / 2; o > 0; o >>= 1) max = fmaxf(max, __shfl_xor_sync(0xffffffffu, max, o));
+        float part = taken_to(mine, max);
+#pragma unroll
+        for (int o = kLWarps / 2; o > 0; o >>= 1) part += __shfl_xor_sync(0xffffffffu, part, o);
+        const int at = __reduce_min_sync(0xffffffffu, mine.max == max ? mine.at : 0x7fffffff);
+        if (lane < p.cluster) {
+          uint32_t to;
           asm volatile("mapa.shared::cluster.u32 %0, %1, %2;"
-                       : "=r"(at)
-                       : "r"(static_cast<uint32_t>(__cvta_generic_to_shared(share + rank))), "r"(tid));
-          asm volatile("st.shared::cluster.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(at),
-                       "r"(__float_as_uint(mine.max)), "r"(__float_as_uint(mine.sum)), "r"(mine.at),
-                       "r"(0)
+                       : "=r"(to)
+                       : "r"(static_cast<uint32_t>(__cvta_generic_to_shared(share + rank))), "r"(lane));
+          asm volatile("st.shared::cluster.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(to),
+                       "r"(__float_as_uint(max)), "r"(__float_as_uint(part)), "r"(at), "r"(0)
                        : "memory");
         }
+      }
+      if (p.cluster > 1) {
         asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory");
         asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory");
       } else {
-        if (tid == 0) {
-          Share mine = {top, 0.0f, 0x7fffffff, 0};
-          for (int w = 0; w < kLWarps; ++w)
-            if (greedy) mine.at = min(mine.at, s_at[w]); else mine.sum += s_sum[w];
-          share[0] = mine;
-        }
         __syncthreads();
       }
       float all = neg_inf(), total = 0.0f;
       int choice = 0x7fffffff;
       for (int c = 0; c < p.cluster; ++c) all = fmaxf(all, share[c].max);
-      auto factor = [&](float m) {
-        float f;
-        asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(f) : "f"((m - all) * rate));
-        return m == all ? 1.0f : m == neg_inf() ? 0.0f : f;
-      };
       for (int c = 0; c < p.cluster; ++c) {
         const Share s = share[c];
         if (s.max == all) choice = min(choice, s.at);
-        total += s.sum * factor(s.max);
+        total += taken_to(s, all);
       }
       if (greedy) {
 #pragma unroll
         for (int j = 0; j < kPer; ++j) l[j] = v0 + tid + j * kLThreads == choice ? 1.0f : 0.0f;
       }
-      const float scale = greedy ? 1.0f : all == neg_inf() ? 0.0f : __fdiv_rn(factor(top), total);
+      const float scale = greedy ? 1.0f : all == neg_inf() ? 0.0f : __fdiv_rn(taken_to({top, 1.0f, 0, 0}, all), total);
 #pragma unroll
       for (int j = 0; j < kPer; ++j)
         if (tid + j * kLThreads < n) out[j * kLThreads] = l[j] * scale;
