@@ -7,19 +7,20 @@
 // order); further rows of the sequence add one draft each.  Where a CTA takes several rows it also
 // lists the tokens named: their values are adjusted by themselves, spread over the threads, and the
 // pass over the row finds them in the words' place, in 3 instructions a value instead of a branch
-// that most warps take.  The softmax is over the CTA's own maximum and sum, which the CTAs exchange
-// once over distributed shared memory (max, sum, and the first token of the maximum for greedy
-// rows) and join in rank order, so repeated calls give the same bits.  Without probabilities
+// that most warps take.  The softmax is over each warp's own maximum; the CTA joins its warps' sums
+// and the CTAs exchange theirs once over distributed shared memory (max, sum, and the first token of
+// the maximum for greedy rows) and join them in rank order, so repeated calls give the same bits.  Without probabilities
 // nothing is exchanged and the CTAs stand alone.
 // Rows begin at any multiple of the element size (odd vocabularies): one element per lane and
 // load.  Bound, for many rows, by a row's chain of steps (the loads, the pass, the maximum, the
-// exponentials, the exchange, the stores: 9 us with two CTAs an SM, of which HBM explains 5):
-// 576 rows of 131071 in 212 us (2.8 TB/s; without penalties, biases and mask 150), 200 BF16 rows of
+// exponentials, the exchange, the stores: 8.5 us with two CTAs an SM, of which HBM explains 5):
+// 576 rows of 131071 in 202 us (3.0 TB/s; without penalties, biases and mask 135), 200 BF16 rows of
 // 100003 without probabilities in 73 us (1.7 TB/s), one row 8-10 us: launch and chain.  Clusters of
 // 8 leave a fifth of the SMs empty, those of 4 with 64 values a thread fewer, but one CTA an SM
-// overlaps with no other (212 and 94).  No faster: quads on 16-byte boundaries with the next row
-// copied ahead, values kept in shared memory with one exchange a row, chunks of tokens dealt to the
-// CTAs in turn, a fixed set of clusters with equal shares of all rows.
+// overlaps with no other (the rows above 195 us, without the counts 142).  No faster: quads on
+// 16-byte boundaries with the next row copied ahead, values kept in shared memory with one exchange
+// a row, chunks of tokens dealt to the CTAs in turn, a fixed set of clusters with equal shares of
+// all rows, the named tokens of the next row adjusted beside the exchange (208).
 #include <algorithm>
 
 #include "serve_internal.cuh"
@@ -411,8 +412,8 @@ cudaError_t launch(LogitsParams<T> p, int B, int cluster, int num_sms, cudaStrea
   if (!kProbs) cluster = (p.V + p.part - 1) / p.part;   // (CTAs of their own: no more than have tokens)
   p.cluster = cluster;
   // Rows of a sequence that share their counts: what takes the fewest rounds of the clusters that
-  // find room (of 152 SMs clusters of 8 use 120, of 4 144); counting costs about half a row.  (1, 2
-  // and 6 rows of 96 sequences' 6 a cluster: 297, 243 and 215 us.)
+  // find room (of 152 SMs clusters of 8 use 120, of 4 144); counting costs about half a row.  (2, 3
+  // and 6 rows of 96 sequences' 6 a cluster: 219, 204 and 204 us.)
   const int sms = !kProbs || cluster <= 2 ? num_sms : cluster == 4 ? num_sms * 18 / 19 : num_sms * 15 / 19;
   const int room = std::max(1, sms * (kPer <= 8 ? 3 : kPer <= 32 ? 2 : 1) / cluster);
   double best = 1e30;
