@@ -423,13 +423,12 @@ cudaError_t launch(LogitsParams<T> p, int B, int cluster, int num_sms, cudaStrea
     if (cost < best) best = cost, p.rows = rows;
   }
   const int bytes = p.part * 4 + p.part / kListShare * 6 + p.biases * 12;
-  if (bytes > 48 * 1024) {
-    const cudaError_t e = cudaFuncSetAttribute(logits_kernel<T, kPer, kProbs>,
-                                               cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                               kPer * kLThreads * 4 + kPer * kLThreads / kListShare * 6 +
-                                                   1024 * 12);
-    if (e != cudaSuccess) return e;
-  }
+  // (also below 48 KB: a kernel's limit by default is that less its static part)
+  const cudaError_t e = cudaFuncSetAttribute(logits_kernel<T, kPer, kProbs>,
+                                             cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                             kPer * kLThreads * 4 + kPer * kLThreads / kListShare * 6 +
+                                                 1024 * 12);
+  if (e != cudaSuccess) return e;
   cudaLaunchAttribute attr[2];
   const unsigned groups = static_cast<unsigned>(B) * ((p.m + p.rows - 1) / p.rows);
   cudaLaunchConfig_t cfg = make_cfg(dim3(groups * cluster), dim3(kLThreads), stream, true, attr);
