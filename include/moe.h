@@ -646,7 +646,7 @@ moe_status_t moe_rotary(const moe_rotary_args* args, void* ws, void* stream);
 /* The whole gated expert layer for a few tokens (1 <= M <= MOE_FEW_TOKENS: single tokens, drafted
  * runs) in two kernels after the router's: the arguments and the result of moe_forward's gated FFN (BF16, or
  * FP8_E4M3 with gated = 1), each active expert's weights read once (above M * K = 65536 once for
- * every 65536 / K tokens).  K a multiple of 64 (BF16) or 128 (FP8), N of 128, both at most 32768.
+ * every 65536 / K tokens; with E from 512 and top_k from 24 twice from about M * K = 63000).  K a multiple of 64 (BF16) or 128 (FP8), N of 128, both at most 32768.
  * Unlike moe_forward's FP8 form it quantises no activations: x enters as it is
  * (binary16 times a power of two for each 128 elements: exact for those above 2^-31 of their
  * block's largest, the others to 2^-39 of it), products are summed in binary32, silu(gate) * up

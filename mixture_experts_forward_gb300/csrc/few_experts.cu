@@ -819,15 +819,29 @@ cudaError_t launch_few(FewParams p, int sms, cudaStream_t stream) {
                : launch_down<kFP8, kGroups, 16, 2>(p, stream);
 }
 
+// Whether x of p.T tokens and the routes' tables leave room for the up kernel's smallest rings.
+template <bool kFP8>
+bool tokens_fit(const FewParams& p) {
+  return (p.T <= 8 ? up_smem<kFP8, 1, 8, 2>(p) : up_smem<kFP8, 2, 8, 2>(p)) <= kMaxSmem;
+}
+
 }  // namespace
 
 cudaError_t launch_few_experts(const moe_forward_args& f, void* out, uint8_t* ws, int num_sms,
                                cudaStream_t stream) {
   const bool fp8 = f.dtype == MOE_DTYPE_FP8_E4M3;
-  // x of one launch fits shared memory beside the rings
+  // x of one launch fits shared memory beside the rings, and beside the routes' tables: these take up
+  // to 20 KB, so with hundreds of experts and 24 or more choices M * K near 65536 needs a pass more
   int most = 65536 / f.K;
   if (most > kMaxTok) most = kMaxTok;
-  const int passes = (f.M + most - 1) / most;
+  int passes = (f.M + most - 1) / most;
+  for (FewParams p = {};; ++passes) {       // (one token always fits)
+    p.T = (f.M + passes - 1) / passes;
+    p.H = f.K;
+    p.E = f.E;
+    p.k = f.top_k;
+    if (p.T == 1 || (fp8 ? tokens_fit<true>(p) : tokens_fit<false>(p))) break;
+  }
   int32_t* ids = reinterpret_cast<int32_t*>(ws + MOE_CTRL_BYTES);
   float* weights = reinterpret_cast<float*>(ids + kMaxTok * 32);
   cudaError_t e = launch_route(f.logits, f.M, f.E, f.top_k, f.softcap, f.renorm, ids, weights, stream, true);

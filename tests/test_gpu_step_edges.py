@@ -1,14 +1,20 @@
 """The operators between the serving calls where their sizes and values end (64-bit forms of
 tests/step_reference.py)."""
+import math
 import os
 import subprocess
 import sys
 
 import pytest
+import torch
 
+import step_reference as R
 from gpu_helpers import ensure_built
+from mixture_experts_forward_gb300 import _lib as L
+from mixture_experts_forward_gb300 import inputs
 
 pytestmark = pytest.mark.gpu
+BF16 = torch.bfloat16
 HERE = os.path.dirname(os.path.abspath(__file__))
 
 
@@ -37,3 +43,52 @@ def test_biases_that_end_near_the_default_limit_of_shared_memory(V, nb):
     code = FRESH.format(here=HERE, root=os.path.dirname(HERE), V=V, nb=nb)
     r = subprocess.run([sys.executable, "-c", code], capture_output=True, text=True, timeout=300)
     assert r.returncode == 0 and "fine" in r.stdout, r.stderr[-2000:]
+
+
+# ------------------------------------------------------------------ few tokens
+class Alike:
+    """n experts' values of which the same few repeat."""
+
+    def __init__(self, values, n):
+        self.values, self.shape = values, (n, *values.shape[1:])
+
+    def __getitem__(self, e):
+        return self.values[e % len(self.values)]
+
+
+def many_experts(fp8, T, H, I, E, k, seed, distinct=4):
+    """(args, tensors, x, values) of a layer of E experts of which `distinct` differ."""
+    g = torch.Generator().manual_seed(seed)
+    up = torch.randn(distinct, 2 * I, H, generator=g) / H ** 0.5
+    down = torch.randn(distinct, H, I, generator=g) / I ** 0.5
+    x = torch.randn(T, H, generator=g).to(BF16)
+    if fp8:
+        (up, up_s), (down, dn_s) = inputs.quantize_weights_e4m3(up), inputs.quantize_weights_e4m3(down)
+        wide = lambda w, s: (w.view(torch.float8_e4m3fn).double() *  # noqa: E731
+                             s.double().repeat_interleave(128, 1).repeat_interleave(128, 2))
+        values = wide(up, up_s), wide(down, dn_s)
+    else:
+        up, down, up_s, dn_s = up.to(BF16), down.to(BF16), None, None
+        values = up.double(), down.double()
+    dev = dict(w=up, w_scales=up_s, w2=down, w2_scales=dn_s)
+    dev = {n: None if t is None else t.cuda().repeat(E // distinct, 1, 1) for n, t in dev.items()}
+    dev.update(logits=torch.randn(T, E, generator=g).cuda(), x=x.cuda())
+    args = L.forward_args(dtype=L.DTYPE_FP8 if fp8 else L.DTYPE_BF16, M=T, K=H, N=I, E=E, top_k=k, gated=1, **dev)
+    return args, dev, x, [Alike(v, E) for v in values]
+
+
+@pytest.mark.parametrize("fp8,T,H,E,k", [(True, 16, 4096, 1024, 32), (False, 16, 4096, 1024, 32),
+                                         (True, 16, 4096, 512, 28), (True, 13, 4992, 1024, 32),
+                                         (False, 15, 4352, 1024, 32), (True, 16, 3968, 1024, 32)])
+def test_many_routes_and_long_rows(fp8, T, H, E, k):
+    """The routes' tables and x of these do not fit shared memory together: two passes."""
+    args, dev, x, values = many_experts(fp8, T, H, 128, E, k, seed=T + k)
+    ws = L.new_workspace(L.few_workspace_size(args))
+    out = torch.full((T, H), math.nan, dtype=BF16, device="cuda")
+    L.forward_few(args, out, ws)
+    assert L.get_error(ws) == L.MOE_OK
+    ids, w = L.route(dev["logits"], k)
+    want, err = R.few(x, ids.cpu(), w.cpu(), *values, fp8)
+    tol = err + (want.abs() + err) * 2.0 ** -8 + 1e-38
+    diff = (out.cpu().double() - want).abs()
+    assert (diff <= tol).all(), (diff / tol).max()
