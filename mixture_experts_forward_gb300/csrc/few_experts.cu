@@ -663,19 +663,25 @@ __global__ void __launch_bounds__(kWarps * 32, kWarps == 8 ? 2 : 1)
             const int tok = 8 * n + g;
             const bool there = (tokens >> tok) & 1u;
             const uint8_t* row = s_h + row_of(tok) * h_pitch<kFP8>();
+            // A column whose token does not go to the expert keeps its sums: 0 times a weight that
+            // is not finite is a NaN.
+            const int t0 = 8 * n + 2 * t;
+            const bool in0 = (tokens >> t0) & 1u, in1 = (tokens >> (t0 + 1)) & 1u;
             if constexpr (kFP8) {
               float c[4] = {0.0f, 0.0f, 0.0f, 0.0f};
               w.multiply(c, row, t, there);
-              const int t0 = 8 * n + 2 * t;
-              const float h0 = ((tokens >> t0) & 1u) ? s_hs[row_of(t0)] * sc[b] : 0.0f;
-              const float h1 = ((tokens >> (t0 + 1)) & 1u) ? s_hs[row_of(t0 + 1)] * sc[b] : 0.0f;
-              acc[n][0] = fmaf(c[0], h0, acc[n][0]);
-              acc[n][1] = fmaf(c[1], h1, acc[n][1]);
-              acc[n][2] = fmaf(c[2], h0, acc[n][2]);
-              acc[n][3] = fmaf(c[3], h1, acc[n][3]);
+              const float h0 = in0 ? s_hs[row_of(t0)] * sc[b] : 0.0f;
+              const float h1 = in1 ? s_hs[row_of(t0 + 1)] * sc[b] : 0.0f;
+              acc[n][0] = in0 ? fmaf(c[0], h0, acc[n][0]) : acc[n][0];
+              acc[n][1] = in1 ? fmaf(c[1], h1, acc[n][1]) : acc[n][1];
+              acc[n][2] = in0 ? fmaf(c[2], h0, acc[n][2]) : acc[n][2];
+              acc[n][3] = in1 ? fmaf(c[3], h1, acc[n][3]) : acc[n][3];
             } else {
-              w.multiply(acc[n], row, t, there);
-              w.multiply(acc[n], row + 128, t, there);
+              float c[4] = {acc[n][0], acc[n][1], acc[n][2], acc[n][3]};
+              w.multiply(c, row, t, there);
+              w.multiply(c, row + 128, t, there);
+              if (in0) acc[n][0] = c[0], acc[n][2] = c[2];
+              if (in1) acc[n][1] = c[1], acc[n][3] = c[3];
             }
           }
         }

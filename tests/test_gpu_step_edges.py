@@ -92,3 +92,27 @@ def test_many_routes_and_long_rows(fp8, T, H, E, k):
     tol = err + (want.abs() + err) * 2.0 ** -8 + 1e-38
     diff = (out.cpu().double() - want).abs()
     assert (diff <= tol).all(), (diff / tol).max()
+
+
+@pytest.mark.parametrize("T", [6, 13])
+@pytest.mark.parametrize("bad", [math.nan, math.inf])
+@pytest.mark.parametrize("fp8", [True, False])
+def test_weights_that_are_not_finite_stay_with_their_expert(fp8, bad, T):
+    """Tokens that are not routed to the expert keep their bits (FP8's infinity is a scale's)."""
+    H, E = 256, 8
+    args, dev, x, _ = many_experts(fp8, T, H, 128, E, 2, seed=T, distinct=8)
+    dev["logits"][:, 3] = -50.0
+    mine = torch.arange(T, device="cuda") % 3 == 1
+    dev["logits"][mine, 3] = 50.0                    # tokens 1, 4, .. go to expert 3
+    ws = L.new_workspace(L.few_workspace_size(args))
+    clean = L.forward_few(args, torch.empty(T, H, dtype=BF16, device="cuda"), ws)
+    assert clean.isfinite().all()
+    if fp8 and math.isinf(bad):
+        dev["w_scales"][3], dev["w2_scales"][3] = bad, bad
+    else:
+        for w in ("w", "w2"):
+            dev[w][3, ::5, ::3] = 0x7f if fp8 else bad
+    out = L.forward_few(args, torch.empty_like(clean), ws)
+    assert L.get_error(ws) == L.MOE_OK
+    assert torch.equal(out[~mine], clean[~mine])
+    assert not out[mine].isfinite().all(1).any()
