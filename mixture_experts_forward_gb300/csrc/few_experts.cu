@@ -631,7 +631,9 @@ __global__ void __launch_bounds__(kWarps * 32, kWarps == 8 ? 2 : 1)
           const float x = v[j][0] * weight, y = v[j][1] * weight;
           const __nv_bfloat162 hi = __floats2bfloat162_rn(x, y);
           const float2 back = __bfloat1622float2(hi);
-          const __nv_bfloat162 rest = __floats2bfloat162_rn(x - back.x, y - back.y);
+          // (nothing beside an infinity: it would be a NaN)
+          const __nv_bfloat162 rest = __floats2bfloat162_rn(isinf(back.x) ? 0.0f : x - back.x,
+                                                            isinf(back.y) ? 0.0f : y - back.y);
           uint32_t* dst = reinterpret_cast<uint32_t*>(s_h + i * h_pitch<kFP8>()) + lane;
           dst[0] = *reinterpret_cast<const uint32_t*>(&hi);
           dst[32] = *reinterpret_cast<const uint32_t*>(&rest);

@@ -116,3 +116,25 @@ def test_weights_that_are_not_finite_stay_with_their_expert(fp8, bad, T):
     assert L.get_error(ws) == L.MOE_OK
     assert torch.equal(out[~mine], clean[~mine])
     assert not out[mine].isfinite().all(1).any()
+
+
+@pytest.mark.parametrize("fp8", [True, False])
+def test_an_infinite_h_is_an_infinite_output(fp8):
+    """h past binary32 over positive weights: the sum is +inf, not NaN."""
+    H = 128
+    one = torch.ones(2, 256, H)
+    if fp8:
+        up = torch.full((2, 256, H), 0x38, dtype=torch.uint8, device="cuda")          # 1.0
+        kw = dict(w=up, w2=up[:, :128].contiguous(), w_scales=torch.ones(2, 2, 1, device="cuda"),
+                  w2_scales=torch.ones(2, 1, 1, device="cuda"))
+    else:
+        kw = dict(w=one.to(BF16).cuda(), w2=one[:, :128].to(BF16).cuda())
+    x = torch.full((2, H), 2.0 ** 70, dtype=BF16, device="cuda")
+    x[1] = 1.0
+    args = L.forward_args(dtype=L.DTYPE_FP8 if fp8 else L.DTYPE_BF16, M=2, K=H, N=128, E=2, top_k=1, gated=1, x=x,
+                          logits=torch.zeros(2, 2, device="cuda"), **kw)
+    ws = L.new_workspace(L.few_workspace_size(args))
+    out = L.forward_few(args, torch.empty(2, H, dtype=BF16, device="cuda"), ws)
+    assert (out[0] == math.inf).all()
+    # silu(128) * 128 = 2^14, 128 of them
+    assert (out[1] == 2.0 ** 21).all()
