@@ -2,11 +2,12 @@
 //
 // A CTA takes a few tokens.  Its threads first compute the tokens' cosines and sines into shared
 // memory, once for all heads: the angle is position * table mod 2^64, in fractions of a turn, an
-// integer product that is exact however far the position is; its top 32 bits as binary32 carry a
-// relative error of 2^-24 into sincospif.  Then each thread takes pieces of 16 elements: two runs
-// of 8 (16-byte loads and stores) that hold whole pairs, so a piece needs no other thread's
-// elements: in the half layout runs i .. i+7 and i + rotary_dim/2 .., else 16 neighbours.  A row's
-// pieces lie in neighbouring lanes, which share its maximum by shuffles where the cache is FP8.
+// integer product that is exact however far the position is; as binary32 (all 64 bits rounded once)
+// it carries a relative error of 2^-24 into sincospif, also for slow pairs at small positions.
+// Then each thread takes pieces of 16 elements: two runs of 8 (16-byte loads and stores) that hold
+// whole pairs, so a piece needs no other thread's elements: in the half layout runs i .. i+7 and
+// i + rotary_dim/2 .., else 16 neighbours.  A row's pieces lie in neighbouring lanes, which share
+// its maximum by shuffles where the cache is FP8.
 // One pass, bound by HBM; below a few hundred tokens by the launch.  16384 tokens of 32 + 2 x 8
 // heads of 128 from a packed projection into an FP8 cache take 70 us (5.3 TB/s, 80 % of a copy's
 // rate), 5003 of 24 + 2 x 8 heads of 64 into a BF16 one 12 us in a graph, 32 tokens 4 us.  The next
@@ -81,8 +82,8 @@ __global__ void __launch_bounds__(kRotThreads) rotary_kernel(const RotaryParams 
     const int tok = i / half;
     const int64_t pos = __ldg(p.positions + t0 + tok);
     const uint64_t turn = static_cast<uint64_t>(pos) * __ldg(p.table + (i - tok * half));
-    // half turns in [-1, 1)
-    const float x = static_cast<float>(static_cast<int32_t>(turn >> 32)) * 0x1p-31f;
+    // half turns in [-1, 1]
+    const float x = static_cast<float>(static_cast<int64_t>(turn)) * 0x1p-63f;
     float s, c;
     sincospif(x, &s, &c);
     s_cos[i] = c * p.amplitude;

@@ -138,3 +138,32 @@ def test_an_infinite_h_is_an_infinite_output(fp8):
     assert (out[0] == math.inf).all()
     # silu(128) * 128 = 2^14, 128 of them
     assert (out[1] == 2.0 ** 21).all()
+
+
+# ------------------------------------------------------------------ rotary
+@pytest.mark.parametrize("interleaved", [False, True])
+@pytest.mark.parametrize("base,factor", [(10000.0, 1.0), (500000.0, 8.0), (1e6, 40.0), (1e7, 1000.0)])
+def test_slow_pairs_at_small_positions(base, factor, interleaved):
+    """One element of each pair is 0, so that the other's sine stands alone.  What may be off: bf16's
+    half step and, relative to the result, sincospi (2 units of 2^-24), the product and the
+    amplitude's (one each); the angle within its turn by 2^-24 of it, by 2^-64 turns a position (the
+    table's step) and by 2^-50 of the whole angle (two evaluations in 64 bits)."""
+    rot, T = 128, 40
+    pos = torch.cat([torch.arange(-7, 25), torch.tensor([100, 1000, 30011, 131071, -100, -1000, 1 << 20, 77])])
+    kw = dict(base=base, scaling="linear", factor=factor)
+    theta, table = R.frequencies(rot, **kw), L.rotary_table(rot, **kw)
+    angle = pos.double()[:, None] * torch.tensor(theta, dtype=torch.float64)
+    within = torch.remainder(angle + math.pi, 2 * math.pi) - math.pi
+    off = within.abs() * 2.0 ** -24 + pos.double().abs()[:, None] * 2 * math.pi * 2.0 ** -64 + angle.abs() * 2.0 ** -50
+    off = (off.repeat_interleave(2, 1) if interleaved else torch.cat([off, off], 1))[:, None]
+    for zero in (0, 1):
+        x = torch.ones(T, 1, rot)
+        if interleaved:
+            x[..., zero::2] = 0
+        else:
+            x[..., zero * rot // 2:(zero + 1) * rot // 2] = 0
+        got, _ = L.rotary(x.to(BF16).cuda(), None, pos.to(torch.int32).cuda(), table, interleaved=interleaved)
+        want, _ = R.rotated(x, pos, theta, interleaved)
+        tol = want.abs() * (2.0 ** -8 + 4 * 2.0 ** -24) + off * 1.01
+        bad = (got.double().cpu() - want).abs() > tol
+        assert not bad.any(), (bad.sum(), got.double().cpu()[bad][:4], want[bad][:4])
