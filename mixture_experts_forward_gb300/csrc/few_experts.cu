@@ -159,7 +159,7 @@ __device__ __forceinline__ int route_join(const FewParams& p, const Routing& r) 
       atomicOr(r.tokens + e, 1u << token_of(i));
       atomicOr(r.on + (e >> 5), 1u << (e & 31));
     } else {
-      set_error(p.ctrl, MOE_ERR_DEVICE_FAULT, 30);   // a NaN logit that no key stands for
+      set_error(p.ctrl, MOE_ERR_DEVICE_FAULT, kFaultFewRoute);   // a NaN logit that no key stands for
     }
   }
   __syncthreads();

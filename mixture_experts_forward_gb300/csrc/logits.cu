@@ -125,7 +125,7 @@ __global__ void __launch_bounds__(kLThreads, kPer <= 8 ? 3 : kPer <= 32 ? 2 : 1)
     len = p.history_lens != nullptr ? __ldg(p.history_lens + b) : p.history_stride;
     if (p.prompt_lens != nullptr) prompt = __ldg(p.prompt_lens + b);
     if (len < 0 || len > p.history_stride || prompt < 0 || prompt > len) {
-      if (tid == 0) set_error(p.ctrl, MOE_ERR_DEVICE_FAULT, 41);
+      if (tid == 0) set_error(p.ctrl, MOE_ERR_DEVICE_FAULT, kFaultHistory);
       len = min(max(len, 0), p.history_stride);
       prompt = min(max(prompt, 0), len);
     }
@@ -158,7 +158,7 @@ __global__ void __launch_bounds__(kLThreads, kPer <= 8 ? 3 : kPer <= 32 ? 2 : 1)
   // The word as it was, of a token of this part (else ~0u): a token's first name enters it in the list.
   auto count = [&](int v, uint32_t what) -> uint32_t {
     if (v < 0 || v >= p.V) {
-      if (v != -1) set_error(p.ctrl, MOE_ERR_DEVICE_FAULT, 40);
+      if (v != -1) set_error(p.ctrl, MOE_ERR_DEVICE_FAULT, kFaultToken);
       return ~0u;
     }
     v -= v0;
@@ -204,7 +204,7 @@ __global__ void __launch_bounds__(kLThreads, kPer <= 8 ? 3 : kPer <= 32 ? 2 : 1)
     // the first bias of a token gets all of them, added up in their order; a warp for each
     for (int at = warp; at < p.biases; at += kLWarps) {
       const int t = s_bias_t[at];
-      if ((t < -1 || t >= p.V) && lane == 0) set_error(p.ctrl, MOE_ERR_DEVICE_FAULT, 40);
+      if ((t < -1 || t >= p.V) && lane == 0) set_error(p.ctrl, MOE_ERR_DEVICE_FAULT, kFaultToken);
       if (t < v0 || t >= v0 + n || t < 0 || t >= p.V) continue;
       int first = -1;
       float sum = 0.0f;
@@ -222,7 +222,7 @@ __global__ void __launch_bounds__(kLThreads, kPer <= 8 ? 3 : kPer <= 32 ? 2 : 1)
     if (list && p.draft != nullptr) {       // drafts of the rows to come get places, with nothing counted
       if (tid >= i0 && tid < i1 - 1) {
         const int t = s_draft[tid], v = t - v0;
-        if (t < -1 || t >= p.V) set_error(p.ctrl, MOE_ERR_DEVICE_FAULT, 40);
+        if (t < -1 || t >= p.V) set_error(p.ctrl, MOE_ERR_DEVICE_FAULT, kFaultToken);
         bool is_new = t >= 0 && t < p.V && v >= 0 && v < n && s_count[v] == 0;
         for (int d = i0; d < tid; ++d) is_new = is_new && s_draft[d] != t;
         if (is_new) enter(t, atomicAdd(&s_named, 1));
@@ -234,7 +234,7 @@ __global__ void __launch_bounds__(kLThreads, kPer <= 8 ? 3 : kPer <= 32 ? 2 : 1)
   float rep = s_number[0], temp = s_number[3];
   const float presence = s_number[1], frequency = s_number[2];
   if (!(rep > 0.0f) || !(temp >= 0.0f)) {
-    if (tid == 0) set_error(p.ctrl, MOE_ERR_DEVICE_FAULT, 42);
+    if (tid == 0) set_error(p.ctrl, MOE_ERR_DEVICE_FAULT, kFaultNumber);
     if (!(rep > 0.0f)) rep = 1.0f;
     if (!(temp >= 0.0f)) temp = 1.0f;
   }

@@ -93,7 +93,7 @@ __global__ void __launch_bounds__(kRotThreads) rotary_kernel(const RotaryParams 
     if (threadIdx.x < n) {
       int slot = __ldg(p.slots + t0 + threadIdx.x);
       if (slot < -1 || (slot >> p.c.page_log2) >= p.c.num_pages) {
-        set_error(p.ctrl, MOE_ERR_DEVICE_FAULT, 31);
+        set_error(p.ctrl, MOE_ERR_DEVICE_FAULT, kFaultRotarySlot);
         slot = -1;
       }
       s_slot[threadIdx.x] = slot;

@@ -77,6 +77,22 @@ cudaError_t launch_attention_tiles(const AttnParams& p, int head_dim, bool fp8,
 // moe_kv_cache checked, and as the kernels take it (serve_api.cu).
 moe_status_t check_cache(const moe_kv_cache* c, KvCacheView* view);
 
+// Where a fault of these operators was first seen (Ctrl::err_info): they may share a control block
+// with the forward (1 .. 6), the cache (10, 11), attention (20 .. 24) and the verification (30, 31).
+enum FaultPlace {
+  kFaultToken = 40,            // logits: a token id,
+  kFaultHistory = 41,          //   a length of the history or the prompt,
+  kFaultNumber = 42,           //   a repetition or a temperature
+  kFaultPlanCount = 50,        // plan: free_count,
+  kFaultPlanSequence = 51,     //   a sequence's lengths, held or rows,
+  kFaultPlanPage = 52,         //   a page id
+  kFaultReleaseCount = 53,     // release: free_count,
+  kFaultReleaseHeld = 54,      //   held,
+  kFaultReleaseRoom = 55,      //   no room on the stack
+  kFaultRotarySlot = 60,
+  kFaultFewRoute = 70,         // few tokens: a route to no expert
+};
+
 // Sequences of one plan at most: their prefix sums stay in shared memory.
 constexpr int kMaxPlanned = 8192;
 cudaError_t launch_plan_step(const moe_page_state& p, const int32_t* lens, const int32_t* news,

@@ -79,7 +79,7 @@ __global__ void __launch_bounds__(kPlanThreads)
   const int page = 1 << page_log2;
   const int said = *p.free_count;
   const int count = min(max(said, 0), p.free_capacity);
-  if (said != count && tid == 0) set_error(ctrl, MOE_ERR_DEVICE_FAULT, 20);
+  if (said != count && tid == 0) set_error(ctrl, MOE_ERR_DEVICE_FAULT, kFaultPlanCount);
 
   long long row0 = 0;
   int page0 = 0;
@@ -114,7 +114,7 @@ __global__ void __launch_bounds__(kPlanThreads)
     }
     const uint32_t m = __ballot_sync(0xffffffffu, bad);
     if (lane == 0 && b < p.B) s_bad[b >> 5] = m;
-    if (bad && blockIdx.x == 0) set_error(ctrl, MOE_ERR_DEVICE_FAULT, 21);
+    if (bad && blockIdx.x == 0) set_error(ctrl, MOE_ERR_DEVICE_FAULT, kFaultPlanSequence);
     row0 += total;
     page0 += pages;
   }
@@ -147,7 +147,7 @@ __global__ void __launch_bounds__(kPlanThreads)
         if (id >= 0 && id < num_pages)
           slot = (id << page_log2) + (pos & (page - 1));
         else
-          set_error(ctrl, MOE_ERR_DEVICE_FAULT, 22);
+          set_error(ctrl, MOE_ERR_DEVICE_FAULT, kFaultPlanPage);
       }
     }
     slots[r] = slot;
@@ -192,7 +192,7 @@ __global__ void __launch_bounds__(kPlanThreads)
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int said = *p.free_count;
   const int count = min(max(said, 0), p.free_capacity);
-  if (said != count && tid == 0) set_error(ctrl, MOE_ERR_DEVICE_FAULT, 23);
+  if (said != count && tid == 0) set_error(ctrl, MOE_ERR_DEVICE_FAULT, kFaultReleaseCount);
   int before = 0;
   for (int b0 = 0; b0 < p.B; b0 += kPlanThreads) {
     const int b = b0 + tid;
@@ -200,7 +200,7 @@ __global__ void __launch_bounds__(kPlanThreads)
     if (b < p.B) {
       const int held = p.held[b], kept = __ldg(keep + b);
       if (held < 0 || held > p.table_stride)
-        set_error(ctrl, MOE_ERR_DEVICE_FAULT, 24);
+        set_error(ctrl, MOE_ERR_DEVICE_FAULT, kFaultReleaseHeld);
       else if (kept >= 0)
         give = max(0, held - (kept == 0 ? 0 : ((kept - 1) >> page_log2) + 1));
     }
@@ -213,7 +213,7 @@ __global__ void __launch_bounds__(kPlanThreads)
   if (tid == 0) s_give[0] = 0;
   __syncthreads();
   const bool fits = before <= p.free_capacity - count;
-  if (!fits && tid == 0) set_error(ctrl, MOE_ERR_DEVICE_FAULT, 25);
+  if (!fits && tid == 0) set_error(ctrl, MOE_ERR_DEVICE_FAULT, kFaultReleaseRoom);
   if (fits) {
     const int warps = gridDim.x * (kPlanThreads / 32);
     for (int b = blockIdx.x * (kPlanThreads / 32) + warp; b < p.B; b += warps) {

@@ -167,3 +167,38 @@ def test_slow_pairs_at_small_positions(base, factor, interleaved):
         tol = want.abs() * (2.0 ** -8 + 4 * 2.0 ** -24) + off * 1.01
         bad = (got.double().cpu() - want).abs() > tol
         assert not bad.any(), (bad.sum(), got.double().cpu()[bad][:4], want[bad][:4])
+
+
+# ------------------------------------------------------------------ faults
+def test_a_shared_control_block_says_which_operator_saw_the_fault():
+    """The control block's fourth word, after one bad call of each operator on a block of their own."""
+    i32 = lambda *v: torch.tensor(v, dtype=torch.int32, device="cuda")  # noqa: E731
+    cache = L.new_kv_cache(L.DTYPE_BF16, 2, 16, 1, 64)[:2]
+    x = torch.ones(1, 1, 64, dtype=BF16, device="cuda")
+    p = torch.full((1, 2, 8), 0.125, device="cuda")
+    u = torch.zeros(1, device="cuda")
+    state = lambda: dict(block_table=i32(0, 1).view(1, 2), held=i32(2), free_pages=i32(3, 4, 5),  # noqa: E731
+                         free_count=i32(3), page_size=16)
+    bad = dict(
+        write=lambda ws: L.kv_write(x, x, i32(32), *cache, ws),
+        read=lambda ws: L.kv_read(*cache, i32(9).view(1, 1), i32(0, 1), 1, ws),
+        attention=lambda ws: L.paged_attention(x, *cache, i32(0).view(1, 1), i32(0, 1), i32(17), ws, max_q=1),
+        verify=lambda ws: L.verify_draft(p, p[:, :1].contiguous(), i32(8).view(1, 1), u.view(1, 1), u, ws),
+        plan=lambda ws: L.plan_step(i32(-1), i32(1), **state(), rows=1, num_pages=6, ws=ws),
+        plan_page=lambda ws: L.plan_step(i32(20), i32(1), **state(), rows=1, num_pages=1, ws=ws),
+        plan_count=lambda ws: L.plan_step(i32(20), i32(1), **{**state(), "free_count": i32(4)}, rows=1, num_pages=6,
+                                          ws=ws),
+        release_held=lambda ws: L.release_pages(i32(0), **{**state(), "held": i32(3)}, ws=ws),
+        release_count=lambda ws: L.release_pages(i32(-1), **{**state(), "free_count": i32(-1)}, ws=ws),
+        release_room=lambda ws: L.release_pages(i32(0), **state(), ws=ws),
+        rotary=lambda ws: L.rotary_write(x, x, x, i32(0), i32(32), L.rotary_table(64), *cache, ws),
+        token=lambda ws: L.adjust_logits(p, ws, draft=i32(8).view(1, 1)),
+        lengths=lambda ws: L.adjust_logits(p, ws, history=i32(1, 2).view(1, 2), history_lens=i32(3)),
+        number=lambda ws: L.adjust_logits(p, ws, temperature=torch.full((1,), -1.0, device="cuda")))
+    places = {}
+    for name, call in bad.items():
+        ws = L.new_workspace(L.ATTENTION_WS_BYTES if name == "attention" else L.CTRL_BYTES)
+        call(ws)
+        places[name] = ws[12:16].view(torch.int32).item()
+        assert L.get_error(ws) == L.MOE_ERR_DEVICE_FAULT, name
+    assert len(set(places.values())) == len(bad), places
