@@ -67,6 +67,7 @@ class ForwardArgs(ctypes.Structure):
                 ("use_graph", ctypes.c_int), ("gather_rows", ctypes.c_int),
                 ("gated", ctypes.c_int), ("w2_scales", ctypes.c_void_p),
                 ("cta_pairs", ctypes.c_int)]
+    __slots__ = ("tensors",)   # what forward_args took the addresses from
 
 
 class WorkspaceMap(ctypes.Structure):
@@ -780,16 +781,15 @@ def forward_args(*, dtype, M, K, N, E, top_k, softcap=0.0, renorm=1, logits=None
     """Arguments of moe_forward.  gated=1 with dtype FP8: the FP8 gated FFN
     (w = w_up codes [E,2N,K] + w_scales, w2 = w_down codes [E,K,N] + w2_scales).
     cta_pairs=-1: the grouped GEMMs on single CTAs only."""
-    return ForwardArgs(dtype=dtype, M=M, K=K, N=N, E=E, top_k=top_k, softcap=float(softcap),
-                       renorm=int(renorm), logits=None if logits is None else logits.data_ptr(),
-                       x=None if x is None else x.data_ptr(),
-                       w=None if w is None else w.data_ptr(),
-                       w_scales=None if w_scales is None else w_scales.data_ptr(),
-                       w2=None if w2 is None else w2.data_ptr(), block_m=block_m, sched=sched,
-                       k_splits=k_splits, use_graph=use_graph, gather_rows=gather_rows,
-                       gated=gated,
-                       w2_scales=None if w2_scales is None else w2_scales.data_ptr(),
-                       cta_pairs=cta_pairs)
+    # (by place: half the time of names)
+    a = ForwardArgs(dtype, M, K, N, E, top_k, softcap, int(renorm),
+                    None if logits is None else logits.data_ptr(),
+                    None if x is None else x.data_ptr(), None if w is None else w.data_ptr(),
+                    None if w_scales is None else w_scales.data_ptr(),
+                    None if w2 is None else w2.data_ptr(), block_m, sched, k_splits, use_graph,
+                    gather_rows, gated, None if w2_scales is None else w2_scales.data_ptr(), cta_pairs)
+    a.tensors = (logits, x, w, w2, w_scales, w2_scales)   # behind the addresses, for forward_few
+    return a
 
 
 def workspace_size(args: ForwardArgs) -> int:
@@ -844,12 +844,46 @@ def few_workspace_size(args: ForwardArgs) -> int:
     return n
 
 
+def _few_tensors(what: str, a: ForwardArgs, tensors, dev: int):
+    """The tensors behind forward_args' addresses: their types, sizes and place."""
+    logits, x, w, w2, w_scales, w2_scales = tensors
+    M, K, N, E = a.M, a.K, a.N, a.E
+    if logits is None or x is None or w is None or w2 is None:
+        _bad(what, "logits, x, w and w2")
+    if not (logits.dtype is _F32 and logits.numel() >= M * E and logits.is_contiguous()):
+        _bad(what, "logits is f32 [M, E]")
+    if not (x.dtype is _BF16 and x.numel() >= M * K and x.is_contiguous()):
+        _bad(what, "x is bf16 [M, K]")
+    n = E * K * N
+    if not (w.numel() >= 2 * n and w2.numel() >= n and w.is_contiguous() and w2.is_contiguous()):
+        _bad(what, "w is [E, 2N, K] and w2 [E, K, N]")
+    if a.dtype == DTYPE_FP8:
+        if not (w.element_size() == 1 and w2.element_size() == 1):
+            _bad(what, "w and w2 are E4M3 codes")
+        n >>= 14                            # blocks of 128 x 128
+        if w_scales is None or w2_scales is None or not (
+                w_scales.dtype is _F32 and w2_scales.dtype is _F32 and w_scales.numel() >= 2 * n and
+                w2_scales.numel() >= n and w_scales.is_contiguous() and w2_scales.is_contiguous()):
+            _bad(what, "w_scales is f32 [E, 2N/128, K/128] and w2_scales [E, K/128, N/128]")
+        there = w_scales.get_device() == w2_scales.get_device() == dev
+    else:
+        if not (w.dtype is _BF16 and w2.dtype is _BF16):
+            _bad(what, "w and w2 are bf16")
+        there = True
+    if not (there and logits.get_device() == x.get_device() == w.get_device() == w2.get_device() == dev):
+        _bad(what, "all tensors must be on one GPU")
+
+
 def forward_few(args: ForwardArgs, out: torch.Tensor, ws: torch.Tensor, stream=None):
     """moe_forward_few: the gated expert layer for at most FEW_TOKENS tokens (args as for forward);
-    ws: new_workspace(few_workspace_size(args))."""
+    ws: new_workspace(few_workspace_size(args)).  The tensors that forward_args was given are checked
+    for type, size and place."""
     what = "moe_forward_few"
     if not (out.dtype is _BF16 and out.numel() == args.M * args.K and out.is_contiguous()):
         _bad(what, "out is bf16 [M, K]")
+    tensors = getattr(args, "tensors", None)
+    if tensors is not None:                 # (else filled in by address: the caller's own)
+        _few_tensors(what, args, tensors, out.get_device())
     _placed(what, out, ws)
     code = lib().moe_forward_few(args, out.data_ptr(), ws.data_ptr(), ws.numel(),
                                  _raw_stream(stream, out))

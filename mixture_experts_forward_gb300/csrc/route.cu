@@ -318,13 +318,6 @@ __global__ void __launch_bounds__(kLayoutThreads, NPL <= 4 ? 2 : 1)
 cudaError_t launch_route(const float* logits, int M, int E, int k, float softcap, int renorm,
                          int32_t* ids, float* weights, cudaStream_t stream, bool pdl) {
   const int warps = 8;
-  cudaError_t err = prefer_max_shared(route_kernel<1>);
-  if (err == cudaSuccess) err = prefer_max_shared(route_kernel<2>);
-  if (err == cudaSuccess) err = prefer_max_shared(route_kernel<4>);
-  if (err == cudaSuccess) err = prefer_max_shared(route_kernel<8>);
-  if (err == cudaSuccess) err = prefer_max_shared(route_kernel<16>);
-  if (err == cudaSuccess) err = prefer_max_shared(route_kernel<32>);
-  if (err != cudaSuccess) return err;
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3((M + warps - 1) / warps);
   cfg.blockDim = dim3(32 * warps);
@@ -334,13 +327,19 @@ cudaError_t launch_route(const float* logits, int M, int E, int k, float softcap
   attr[0].val.programmaticStreamSerializationAllowed = pdl ? 1 : 0;
   cfg.attrs = attr;
   cfg.numAttrs = 1;
+  // (the preference of the kernel that is launched alone: a driver call each)
+  auto launch = [&](auto* kernel) {
+    const cudaError_t err = prefer_max_shared(kernel);
+    if (err != cudaSuccess) return err;
+    return cudaLaunchKernelEx(&cfg, kernel, logits, M, E, k, softcap, renorm, ids, weights);
+  };
   const int npl = (E + 31) / 32;
-  if (npl <= 1) return cudaLaunchKernelEx(&cfg, route_kernel<1>, logits, M, E, k, softcap, renorm, ids, weights);
-  if (npl <= 2) return cudaLaunchKernelEx(&cfg, route_kernel<2>, logits, M, E, k, softcap, renorm, ids, weights);
-  if (npl <= 4) return cudaLaunchKernelEx(&cfg, route_kernel<4>, logits, M, E, k, softcap, renorm, ids, weights);
-  if (npl <= 8) return cudaLaunchKernelEx(&cfg, route_kernel<8>, logits, M, E, k, softcap, renorm, ids, weights);
-  if (npl <= 16) return cudaLaunchKernelEx(&cfg, route_kernel<16>, logits, M, E, k, softcap, renorm, ids, weights);
-  return cudaLaunchKernelEx(&cfg, route_kernel<32>, logits, M, E, k, softcap, renorm, ids, weights);
+  if (npl <= 1) return launch(route_kernel<1>);
+  if (npl <= 2) return launch(route_kernel<2>);
+  if (npl <= 4) return launch(route_kernel<4>);
+  if (npl <= 8) return launch(route_kernel<8>);
+  if (npl <= 16) return launch(route_kernel<16>);
+  return launch(route_kernel<32>);
 }
 
 

@@ -202,3 +202,16 @@ def test_a_shared_control_block_says_which_operator_saw_the_fault():
         places[name] = ws[12:16].view(torch.int32).item()
         assert L.get_error(ws) == L.MOE_ERR_DEVICE_FAULT, name
     assert len(set(places.values())) == len(bad), places
+
+
+# ------------------------------------------------------------------ the binding
+@pytest.mark.parametrize("name", ["logits", "x", "w", "w_scales", "w2", "w2_scales"])
+def test_one_host_tensor_among_the_experts_arguments(name):
+    """Refused, before its address is passed on."""
+    args, dev, _, _ = many_experts(True, 2, 256, 128, 4, 2, seed=1)
+    ws, out = L.new_workspace(L.few_workspace_size(args)), torch.zeros(2, 256, dtype=BF16, device="cuda")
+    dev[name] = dev[name].cpu()
+    args = L.forward_args(dtype=L.DTYPE_FP8, M=2, K=256, N=128, E=4, top_k=2, gated=1, **dev)
+    with pytest.raises(L.MoeError, match="on one GPU"):
+        L.forward_few(args, out, ws)
+    assert (out == 0).all()
