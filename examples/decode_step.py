@@ -1,14 +1,14 @@
-"""Decoding with drafted runs by the operators of one decoder layer's step, nothing in torch but the
-products outside the library's scope.
+"""Decoding with drafted runs by the operators of one decoder layer's step.  In torch stay the
+embedding, the plain products, the draft model and the record of what was said.
 
 One step for B sequences with n drafted tokens each:
   plan_step (pages, slots, positions) -> embed -> q, k, v -> rotary_write (rotated, quantised into
   the cache) -> paged_attention -> forward_few (the expert layer, FP8) -> adjust_logits (penalties,
   biases, mask, temperature) -> verify_draft -> release_pages (what refused drafts had taken).
-Sequences that end give their pages back, and a waiting one takes their place.  Weights are random; the
+A sequence that ends gives its pages back, and a waiting one takes its row.  Weights are random; the
 draft model is the target without its attention and experts.
 
-    python examples/decode_step.py [--steps N]
+    python examples/decode_step.py [--steps N] [--waiting TOKENS]
 """
 from __future__ import annotations
 
@@ -124,13 +124,31 @@ class Server:
         self.said = self.said + accepted + 1
         return accepted, out
 
+    def end(self, b):
+        """Sequence b ends: all of its pages go back."""
+        keep = self.len.clone()
+        keep[b] = 0
+        L.release_pages(keep, self.table, self.held, self.free, self.count, PAGE, self.ctrl)
+        self.len, self.said[b], self.prompt[b] = keep, 0, 0
+
+    def admit(self, b, text):
+        """A sequence takes row b, which is free: all of its prompt but the last token is cached."""
+        n = text.numel()
+        new = torch.zeros_like(self.len)
+        new[b] = n - 1
+        self.forward(text[:-1], new, n - 1)
+        self.len, self.said[b], self.prompt[b] = self.len + new, n, n
+        self.history[b, :n] = text
+
     def status(self):
         return [L.get_error(w) for w in (self.ctrl, self.ws, self.few_ws)]
 
 
-def main(steps: int = 8, batch: int = 4, n_draft: int = 3, prompt: int = 37, seed: int = 0):
+def main(steps: int = 8, batch: int = 4, n_draft: int = 3, prompt: int = 37, seed: int = 0, waiting: int = 0):
+    """Decodes `steps` steps of `batch` sequences, then the first ends.  waiting > 0: one with a prompt
+    of so many tokens (2 to `prompt`) takes its place, and `steps` steps more are decoded."""
     g = torch.Generator(device="cuda").manual_seed(seed)
-    most = prompt + (steps + 1) * (n_draft + 1)
+    most = prompt + ((2 if waiting else 1) * steps + 1) * (n_draft + 1)
     pages = batch * -(-most // PAGE)
     s = Server(batch, n_draft, pages, most, seed)
     # prompts of ragged lengths, as one packed chunk each
@@ -143,25 +161,40 @@ def main(steps: int = 8, batch: int = 4, n_draft: int = 3, prompt: int = 37, see
     s.said, s.prompt = lens.clone(), lens.clone()
     last = text.gather(1, (lens - 1).long()[:, None])[:, 0]
     out = [[] for _ in range(batch)]
-    for _ in range(steps):
-        accepted, tokens = s.step(last, g)
-        last = tokens.gather(1, accepted.long()[:, None])[:, 0]
-        for b, (a, row) in enumerate(zip(accepted.tolist(), tokens.tolist())):
-            out[b] += row[:a + 1]
+
+    def decode(last):
+        for _ in range(steps):
+            accepted, tokens = s.step(last, g)
+            last = tokens.gather(1, accepted.long()[:, None])[:, 0]
+            for b, (a, row) in enumerate(zip(accepted.tolist(), tokens.tolist())):
+                out[b] += row[:a + 1]
+        return last
+
+    last = decode(last)
     lengths, held, free = s.len.tolist(), s.held.tolist(), int(s.count)
-    # the first sequence ends: its pages go back
-    keep = s.len.clone()
-    keep[0] = 0
-    L.release_pages(keep, s.table, s.held, s.free, s.count, PAGE, s.ctrl)
-    return dict(tokens=out, lengths=lengths, held=held, free=free, pages=pages, after=(s.held.tolist(), int(s.count)),
-                status=s.status(), server=s)
+    s.end(0)
+    r = dict(tokens=out, lengths=lengths, held=held, free=free, pages=pages, after=(s.held.tolist(), int(s.count)),
+             server=s)
+    if waiting:
+        ended, out[0] = out[0], []
+        text = torch.randint(VOCAB, (waiting,), device="cuda", generator=g, dtype=torch.int32)
+        s.admit(0, text)
+        last[0] = text[-1]
+        decode(last)
+        r.update(ended=ended, lengths=s.len.tolist(), held=s.held.tolist(), free=int(s.count))
+    r["status"] = s.status()
+    return r
 
 
 if __name__ == "__main__":
     ap = argparse.ArgumentParser()
     ap.add_argument("--steps", type=int, default=8)
-    r = main(ap.parse_args().steps)
+    ap.add_argument("--waiting", type=int, default=25)
+    a = ap.parse_args()
+    r = main(a.steps, waiting=a.waiting)
     for b, t in enumerate(r["tokens"]):
         print(f"sequence {b}: {len(t)} tokens {t[:12]}{' ...' if len(t) > 12 else ''}")
+    if "ended" in r:
+        print(f"(the first row had {len(r['ended'])} tokens of a sequence that ended)")
     print(f"cached positions {r['lengths']}, pages held {r['held']}, free {r['free']} of {r['pages']}, "
           f"status {r['status']}")
