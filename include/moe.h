@@ -547,7 +547,8 @@ moe_status_t moe_verify_draft(const moe_verify_args* args, void* ws, void* strea
 /* The pages of a batch's sequences, all in device memory.  Row b of the block table
  * holds sequence b's pages in its first held[b] entries; the pages that nobody holds are
  * a stack of free_count[0] ids.  page_size 16 .. 256, a power of two; B at most 8192;
- * B * table_stride, and the pages times page_size, below 2^31. */
+ * B * table_stride, and the pages times page_size, below 2^31; table_stride * page_size below
+ * 2^31 - 511. */
 typedef struct {
   int B, table_stride, page_size;
   int free_capacity;          /* entries of free_pages */
@@ -651,7 +652,11 @@ moe_status_t moe_rotary(const moe_rotary_args* args, void* ws, void* stream);
  * (binary16 times a power of two for each 128 elements: exact for those above 2^-31 of their
  * block's largest, the others to 2^-39 of it), products are summed in binary32, silu(gate) * up
  * keeps 11 bits (FP8) or 16 (BF16), and the output is rounded once.  block_m, sched, k_splits,
- * use_graph, gather_rows and cta_pairs are ignored.  Routing is moe_route's, bit for bit.
+ * use_graph, gather_rows and cta_pairs are ignored.  Routing is moe_route's, bit for bit.  Weights that
+ * are not finite reach the tokens of their expert alone.
+ * Faster than moe_forward up to about 6 tokens (one token: half its time), on a par at 8 to 10, slower
+ * from 12 on (16 tokens: 59 us against 55 through 69 FP8 experts of 512 x 2048, 263 against 220 through 40
+ * BF16 experts of 1408 x 4096).
  * out: bf16 [M, K].  ws: moe_few_workspace_size() bytes. */
 moe_status_t moe_forward_few(const moe_forward_args* args, void* out, void* ws, size_t ws_bytes,
                              void* stream);
@@ -695,7 +700,8 @@ typedef struct {
  *                                             is a product with the rounded reciprocal),
  *   l -= frequency * c;  l -= presence if c > 0;  l += bias;  l = -inf if the mask forbids v.
  * A NaN counts as -inf, and a logit of -inf stays there.  probabilities: p = exp((l - max) /
- * temperature) / sum in binary32, tokens at -inf get 0, tokens at +inf share all of it; a row that
+ * temperature) / sum in binary32, of a relative error below (d + 40) * 2^-22 for d = (max - l) /
+ * temperature (below 2^-126 it may be 0), tokens at -inf get 0, tokens at +inf share all of it; a row that
  * is left with nothing gets 0 throughout.  Tokens outside [0, V), lengths outside the history, a
  * repetition that is not > 0 and a temperature that is not >= 0 (taken as 1) record
  * MOE_ERR_DEVICE_FAULT. */

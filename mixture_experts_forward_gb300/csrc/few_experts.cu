@@ -11,23 +11,28 @@
 // m16n8k32 took 170 us instead of 96 for 16 tokens through 69 of 256 experts: that form is made of
 // conversions too, one for each MMA.)  The order of k inside
 // an MMA is free, so a lane loads 16 contiguous bytes of a row and uses them as they lie.  Weights
-// come by cp.async into a ring of the warp's own (4 KB a step: 16 rows x 256 bytes); a lane reads
-// back the rows' pieces that it copied itself.
+// come by cp.async into a ring of the warp's own (4 KB a step: 16 rows x 256 bytes).  A lane copies
+// one piece of every second row and reads pieces of two rows, mostly other lanes' copies: each wait
+// for the ring is followed by a __syncwarp.
 //
 // Up: a unit is 8 gate rows and the 8 up rows of the same h columns, in one MMA tile, so
 // silu(gate) * up is computed where the sums are; several warps share a unit's K where there
-// are few units.  Down: a cluster of 8 CTAs takes 128 output rows, each of its CTAs an equal
-// share of all active experts' K; the shares meet over distributed shared memory, in rank order
+// are few units.  Down: a cluster of up to 8 CTAs takes 64 or 128 output rows (as many CTAs as fill the
+// SMs once: clusters of 4 for H = 2048, of 2 for 4096), each of its CTAs an equal share of all
+// active experts' K; the shares meet over distributed shared memory, in rank order
 // (no atomics: repeated calls give the same bits).  The tokens are routed before by moe_route's
 // kernel, during which the up kernel stages x; while the up kernel runs, the down kernel fetches
 // its first weights as far as it finds room.  (Routing in every CTA of both kernels instead saved a launch but
 // took 8 us of each for 16 tokens and 256 experts.)
 //
-// Measured (HBM's floor for the experts that the tokens reach in brackets): one token, 8 FP8 experts
-// of 512 x 2048 15 us (3.8: the chain of three launches); 16 tokens, 69 of them 55-57 us (33: 22 +
-// 12 us of stream at 6.4 TB/s, the rest the router and the kernels' beginnings and ends); one token,
-// 2 BF16 experts of 1024 x 4096 15-18 us (7.6); 5 tokens, 18 BF16 experts of 1408 x 4096 110-127 us
-// (94).
+// Measured (HBM's floor for the experts that the tokens reach in brackets), a pass among others: one
+// token, 8 FP8 experts of 512 x 2048 15 us (3.8: the chain of three launches); 16 tokens, 69 of them
+// 55-59 us (33: 22 + 12 us of stream at 6.4 TB/s, the rest the router and the kernels' beginnings and
+// ends); one token, 2 BF16 experts of 1024 x 4096 15-18 us (7.6); 5 tokens, 18 BF16 experts of
+// 1408 x 4096 110-127 us (94).  The 128-token path of moe_forward, in a graph each: FP8 experts of
+// 512 x 2048 31 us against 16 here for one token, 46 / 37 for 8, 49 / 51 for 12, 55 / 59 for 16; BF16
+// of 1408 x 4096 61 / 45, 149 / 152 (8 tokens), 196 / 218 (12), 220 / 263 (16); from 9 tokens on a
+// weight tile meets two groups of MMA columns.
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 

@@ -14,8 +14,10 @@
 // Rows begin at any multiple of the element size (odd vocabularies): one element per lane and
 // load.  Bound, for many rows, by a row's chain of steps (the loads, the pass, the maximum, the
 // exponentials, the exchange, the stores: 8.5 us with two CTAs an SM, of which HBM explains 5):
-// 576 rows of 131071 in 202 us (3.0 TB/s; without penalties, biases and mask 135), 200 BF16 rows of
-// 100003 without probabilities in 73 us (1.7 TB/s), one row 8-10 us: launch and chain.  Clusters of
+// 576 rows of 131071 in 202 us (3.0 TB/s; without penalties, biases and mask 135; from BF16 211), 200
+// BF16 rows of 100003 without probabilities in 73 us (1.7 TB/s; without the history 55, without
+// anything 37; 68 before rows of a sequence shared their counts, which these do not), one row 8-10 us:
+// launch and chain.  Clusters of
 // 8 leave a fifth of the SMs empty, those of 4 with 64 values a thread fewer, but one CTA an SM
 // overlaps with no other (the rows above 195 us, without the counts 142).  No faster: quads on
 // 16-byte boundaries with the next row copied ahead, values kept in shared memory with one exchange

@@ -215,3 +215,22 @@ def test_one_host_tensor_among_the_experts_arguments(name):
     with pytest.raises(L.MoeError, match="on one GPU"):
         L.forward_few(args, out, ws)
     assert (out == 0).all()
+
+
+# ------------------------------------------------------------------ the exponential
+@pytest.mark.parametrize("temperature", [1.0, 0.3, 7.0])
+@pytest.mark.parametrize("V", [4000, 50257, 262144])
+def test_probabilities_far_below_the_largest(V, temperature):
+    """Relative to themselves off by (d + 40) 2^-22, d = (max - l) / temperature: 2^-22 of d for the
+    difference, the rate's two roundings and the product, twice 2^-22 for the exponentials, the mean of d
+    under the distribution (at most ln V, 12.5) and 81 additions of 2^-24 for the sum."""
+    g = torch.Generator().manual_seed(V)
+    x = torch.randn(2, 1, V, generator=g) * 14 * temperature
+    x[1] = torch.rand(1, V, generator=g) * 60 * temperature
+    out = L.adjust_logits(x.cuda(), L.new_workspace(L.CTRL_BYTES),
+                          temperature=torch.full((2,), temperature, device="cuda")).cpu().double()
+    t = float(torch.tensor(temperature))
+    d = (x.double().amax(-1, keepdim=True) - x.double()) / t
+    want = torch.softmax(-d, -1)
+    seen = want > 2.0 ** -120
+    assert ((out - want).abs() <= want * (d + 40) * 2.0 ** -22)[seen].all()
