@@ -67,7 +67,7 @@ class ForwardArgs(ctypes.Structure):
                 ("use_graph", ctypes.c_int), ("gather_rows", ctypes.c_int),
                 ("gated", ctypes.c_int), ("w2_scales", ctypes.c_void_p),
                 ("cta_pairs", ctypes.c_int)]
-    __slots__ = ("tensors",)   # what forward_args took the addresses from
+    __slots__ = ("given",)   # the tensors that forward_args was given, and their addresses
 
 
 class WorkspaceMap(ctypes.Structure):
@@ -781,14 +781,16 @@ def forward_args(*, dtype, M, K, N, E, top_k, softcap=0.0, renorm=1, logits=None
     """Arguments of moe_forward.  gated=1 with dtype FP8: the FP8 gated FFN
     (w = w_up codes [E,2N,K] + w_scales, w2 = w_down codes [E,K,N] + w2_scales).
     cta_pairs=-1: the grouped GEMMs on single CTAs only."""
+    pl = None if logits is None else logits.data_ptr()
+    px = None if x is None else x.data_ptr()
+    pw = None if w is None else w.data_ptr()
+    ps = None if w_scales is None else w_scales.data_ptr()
+    pw2 = None if w2 is None else w2.data_ptr()
+    ps2 = None if w2_scales is None else w2_scales.data_ptr()
     # (by place: half the time of names)
-    a = ForwardArgs(dtype, M, K, N, E, top_k, softcap, int(renorm),
-                    None if logits is None else logits.data_ptr(),
-                    None if x is None else x.data_ptr(), None if w is None else w.data_ptr(),
-                    None if w_scales is None else w_scales.data_ptr(),
-                    None if w2 is None else w2.data_ptr(), block_m, sched, k_splits, use_graph,
-                    gather_rows, gated, None if w2_scales is None else w2_scales.data_ptr(), cta_pairs)
-    a.tensors = (logits, x, w, w2, w_scales, w2_scales)   # behind the addresses, for forward_few
+    a = ForwardArgs(dtype, M, K, N, E, top_k, softcap, int(renorm), pl, px, pw, ps, pw2, block_m, sched,
+                    k_splits, use_graph, gather_rows, gated, ps2, cta_pairs)
+    a.given = (logits, x, w, w2, w_scales, w2_scales), (pl, px, pw, ps, pw2, ps2)
     return a
 
 
@@ -877,12 +879,13 @@ def _few_tensors(what: str, a: ForwardArgs, tensors, dev: int):
 def forward_few(args: ForwardArgs, out: torch.Tensor, ws: torch.Tensor, stream=None):
     """moe_forward_few: the gated expert layer for at most FEW_TOKENS tokens (args as for forward);
     ws: new_workspace(few_workspace_size(args)).  The tensors that forward_args was given are checked
-    for type, size and place."""
+    for type, size and place (addresses written into args later are not)."""
     what = "moe_forward_few"
     if not (out.dtype is _BF16 and out.numel() == args.M * args.K and out.is_contiguous()):
         _bad(what, "out is bf16 [M, K]")
-    tensors = getattr(args, "tensors", None)
-    if tensors is not None:                 # (else filled in by address: the caller's own)
+    tensors, addresses = getattr(args, "given", (None, None))
+    # (other addresses are filled in by the caller, who answers for them)
+    if addresses == (args.logits, args.x, args.w, args.w_scales, args.w2, args.w2_scales):
         _few_tensors(what, args, tensors, out.get_device())
     _placed(what, out, ws)
     code = lib().moe_forward_few(args, out.data_ptr(), ws.data_ptr(), ws.numel(),

@@ -58,3 +58,22 @@ def test_tensors_in_host_memory(fp8):
     w = torch.zeros(E, 2 * N, K, dtype=torch.float8_e4m3fn)        # codes under their own type
     with pytest.raises(L.MoeError, match="on one GPU"):
         call(True, w=w, x=torch.zeros(M + 4, K, dtype=torch.bfloat16))
+
+
+def test_addresses_that_the_caller_fills_in():
+    """Not the tensors that forward_args was given (if any): those are not looked at."""
+    kw = dict(dtype=L.DTYPE_FP8, M=M, K=K, N=N, E=E, top_k=2, gated=1)
+    one = torch.zeros(1, K, dtype=torch.bfloat16)
+    other = L.forward_args(**{**kw, "M": 1}, **{**tensors(True), "x": one})
+    empty = L.forward_args(**kw)
+    t = tensors(True)
+    for a in (other, empty):
+        a.M = M
+        for name in t:
+            setattr(a, name, t[name].data_ptr())
+        with pytest.raises(L.MoeError, match="on one GPU"):        # of out and ws
+            L.forward_few(a, torch.zeros(M, K, dtype=torch.bfloat16), torch.zeros(1 << 16, dtype=torch.uint8))
+    small = L.forward_args(**{**kw, "M": 1}, **{**t, "x": one})
+    small.M = M                                                    # more tokens than x has
+    with pytest.raises(L.MoeError, match="x is bf16"):
+        L.forward_few(small, torch.zeros(M, K, dtype=torch.bfloat16), torch.zeros(1 << 16, dtype=torch.uint8))
